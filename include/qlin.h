@@ -287,6 +287,118 @@ qlin_status qlin_gather_qmm_noalloc(const void* x, qlin_dtype x_dtype, int64_t B
 size_t qlin_gather_qmm_noalloc_max_rows(void);
 size_t qlin_gather_qmm_noalloc_max_experts(void);
 
+/*
+ * qlin_moe_route -- choice of k experts for each token, with their weights:
+ * the router in front of qlin_gather_qmm / qlin_gather_mxfp4_matmul.
+ *   logits   [T, E] of dtype (QLIN_F32, QLIN_F16 or QLIN_BF16); all
+ *            arithmetic is fp32.
+ *   score    "softmax" (over the token's E logits) or "sigmoid" (each on its
+ *            own): s.
+ *   bias     fp32 [E] or NULL: a balance bias, added to s for the choice only.
+ *   groups   the experts form `groups` runs of E/groups; a group counts as its
+ *            largest s + bias (group_top 1) or the sum of its two largest
+ *            (group_top 2), and only experts of the groups_kept best groups can
+ *            be chosen. 1, 1, 1: no groups.
+ *   experts  out, int32 [T, k]: the k largest s + bias in descending order,
+ *            equal ones by ascending index (without a bias the logits
+ *            themselves are compared). An expert whose logit is not finite, or
+ *            whose s + bias is NaN, cannot be chosen; places left over get -1.
+ *   weights  out, fp32 [T, k]: scale * s of the expert (without its bias),
+ *            divided by the sum of the token's chosen s + 1e-20 if renormalize;
+ *            0 at places left over.
+ * 1 <= k <= min(64, experts of the kept groups), E <= 1024, groups <= 64.
+ * T == 0 is a no-op.
+ */
+qlin_status qlin_moe_route(const void* logits, qlin_dtype dtype, int64_t T, int64_t E, int64_t k,
+                           const float* bias, const char* score, int renormalize, double scale,
+                           int64_t groups, int64_t groups_kept, int group_top, float* weights,
+                           int32_t* experts, void* stream);
+
+/*
+ * qlin_moe_route_grad -- gradient of qlin_moe_route's weights with respect to
+ * its logits; the choice and the bias carry none.
+ *   logits, score, renormalize, scale: as given to qlin_moe_route.
+ *   experts       int32 [T, k], its output (distinct per token; entries
+ *                 outside [0, E) are places left over).
+ *   grad_weights  fp32 [T, k].
+ *   grad_logits   out, [T, E] of dtype: computed in fp32, rounded once. Zero
+ *                 for logits that are not finite.
+ */
+qlin_status qlin_moe_route_grad(const void* logits, qlin_dtype dtype, int64_t T, int64_t E,
+                                int64_t k, const int32_t* experts, const float* grad_weights,
+                                const char* score, int renormalize, double scale,
+                                void* grad_logits, void* stream);
+
+/*
+ * qlin_mxfp4_matmul -- y = x . W^T with both operands in mxfp4, on the 4-bit
+ * scaled MFMA (no operand is decoded; fp32 accumulation, one rounding).
+ *   x         x_dtype QLIN_F32, QLIN_F16 or QLIN_BF16: [M, K], quantized along
+ *             K by qlin_quantize's mxfp4 rule on the way; with activation
+ *             "swiglu" x is [M, 2K] and silu(x[:, :K]) * x[:, K:], taken in
+ *             fp32, is quantized. A block of 32 values that holds a NaN or an
+ *             infinity becomes NaN. x_scales must be NULL.
+ *             x_dtype QLIN_U8: mxfp4 words [M, K/8] as qlin_quantize writes
+ *             them, with x_scales [M, K/32]; no activation.
+ *   activation  NULL or "none", or "swiglu".
+ *   wq, scales  W [N, K] in mxfp4, packed along K: [N, K/8], [N, K/32].
+ *   workspace   device memory of at least qlin_mxfp4_matmul_workspace_bytes
+ *             bytes, 16-byte aligned, owned by the caller; overwritten (may be
+ *             NULL where that is 0).
+ *   y         out, [M, N] of y_dtype (QLIN_F32, QLIN_F16 or QLIN_BF16).
+ * K must be a multiple of 32 (at most 2^22); x words and wq 16-byte aligned.
+ * M == 0 is a no-op.
+ */
+size_t qlin_mxfp4_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N, qlin_dtype x_dtype);
+qlin_status qlin_mxfp4_matmul(const void* x, qlin_dtype x_dtype, const void* x_scales,
+                              const char* activation, int64_t M, int64_t K, const uint32_t* wq,
+                              const void* scales, int64_t N, void* workspace,
+                              size_t workspace_bytes, void* y, qlin_dtype y_dtype, void* stream);
+
+/*
+ * qlin_gather_mxfp4_matmul -- the product by experts:
+ *   y[r] = x[r / (R / B)] . W[experts[r]]^T      for r in [0, R)
+ * so that with x [T, K] and a router's experts [T, k] row (t, j) of y
+ * [T, k, N] is token t through its j-th expert. Each expert's weight is read
+ * in place, once per tile of its rows.
+ *   x         B rows, as for qlin_mxfp4_matmul; R must be a multiple of B.
+ *   wq, scales  [E, N, K/8], [E, N, K/32]; E <= 8000.
+ *   experts   int32 [R]; a row whose entry is outside [0, E) becomes zeros.
+ *   workspace  at least qlin_gather_mxfp4_matmul_workspace_bytes bytes.
+ * R == 0 is a no-op.
+ */
+size_t qlin_gather_mxfp4_matmul_workspace_bytes(int64_t B, int64_t R, int64_t K, int64_t E,
+                                                int64_t N, qlin_dtype x_dtype);
+qlin_status qlin_gather_mxfp4_matmul(const void* x, qlin_dtype x_dtype, const void* x_scales,
+                                     const char* activation, int64_t B, int64_t K,
+                                     const uint32_t* wq, const void* scales, int64_t E, int64_t N,
+                                     const int32_t* experts, int64_t R, void* workspace,
+                                     size_t workspace_bytes, void* y, qlin_dtype y_dtype,
+                                     void* stream);
+
+/*
+ * qlin_moe_combine -- y[t] = sum over j of weights[t, j] * h[t, j].
+ *   h        [T, k, D] of dtype (QLIN_F32, QLIN_F16 or QLIN_BF16).
+ *   weights  fp32 [T, k].
+ *   experts  int32 [T, k] or NULL; a place with a negative entry is left out
+ *            (its row of h is not read).
+ *   y        out, [T, D] of dtype; fp32 sums in the order of j, one rounding.
+ * T == 0 is a no-op.
+ */
+qlin_status qlin_moe_combine(const void* h, qlin_dtype dtype, int64_t T, int64_t k, int64_t D,
+                             const float* weights, const int32_t* experts, void* y, void* stream);
+
+/*
+ * qlin_moe_combine_grad -- the gradients of qlin_moe_combine for
+ * grad_y [T, D] of dtype:
+ *   grad_h        out, [T, k, D] of dtype: weights[t, j] * grad_y[t].
+ *   grad_weights  out, fp32 [T, k]: <grad_y[t], h[t, j]>.
+ * Both are zero at places left out. Results do not depend on scheduling.
+ */
+qlin_status qlin_moe_combine_grad(const void* grad_y, const void* h, qlin_dtype dtype, int64_t T,
+                                  int64_t k, int64_t D, const float* weights,
+                                  const int32_t* experts, void* grad_h, float* grad_weights,
+                                  void* stream);
+
 /* Message describing the calling thread's last failed call ("" if none). */
 const char* qlin_last_error(void);
 
@@ -294,7 +406,8 @@ const char* qlin_last_error(void);
  * Kernel path of the calling thread's last matmul-type call that reached a
  * launch (a static string: "decode", "in_out", "in_out_split",
  * "in_out_row_blocks", "prefill", "tiled", "generic", "gather_decode",
- * "gather_prefill", "qqmm_scaled_mfma"; "" before any). "generic" is the fp32 VALU fallback for
+ * "gather_prefill", "qqmm_scaled_mfma", "mxfp4_stream", "mxfp4_tiled",
+ * "mxfp4_gather_direct", "mxfp4_gather_stream", "mxfp4_gather_tiled"; "" before any). "generic" is the fp32 VALU fallback for
  * shapes the fast kernels do not take, typically an order of magnitude
  * slower; QLIN_WARN_FALLBACK=1 also prints a line to stderr when it runs.
  */

@@ -8,7 +8,9 @@ library is not built, every call raises.
 
 Raw ABI calls (same names as the C functions, minus the ``qlin_`` prefix):
 ``quantize``, ``dequantize``, ``quantized_matmul``, ``quantized_dense``,
-``qqmm``, ``gather_qmm`` operate on explicit tensors. ``QuantizedWeight`` bundles the packed weight with its
+``qqmm``, ``gather_qmm``, ``moe_route``, ``moe_route_grad``, ``mxfp4_matmul``,
+``gather_mxfp4_matmul``, ``moe_combine``, ``moe_combine_grad`` operate on
+explicit tensors. ``QuantizedWeight`` bundles the packed weight with its
 metadata, mirroring the field set of the "Emily.QuantizedWeight" page
 (value, scales, biases, group_size, bits, transpose, mode).
 """
@@ -16,12 +18,20 @@ from ._binding import (  # noqa: F401
     QlinError,
     QuantizedWeight,
     dequantize,
+    gather_mxfp4_matmul,
+    gather_mxfp4_matmul_workspace_bytes,
     gather_qmm,
     gather_qmm_noalloc,
     gather_qmm_workspace_bytes,
     last_path,
     library_path,
     load_library,
+    moe_combine,
+    moe_combine_grad,
+    moe_route,
+    moe_route_grad,
+    mxfp4_matmul,
+    mxfp4_matmul_workspace_bytes,
     quantize,
     qqmm,
     qqmm_workspace_bytes,

@@ -70,10 +70,23 @@ def load_library():
     lib.qlin_gather_qmm_noalloc.restype = i32
     lib.qlin_gather_qmm_noalloc_max_rows.restype = sz
     lib.qlin_gather_qmm_noalloc_max_experts.restype = sz
+    f64 = ctypes.c_double
+    lib.qlin_moe_route.argtypes = [vp, i32, i64, i64, i64, vp, cs, i32, f64, i64, i64, i32, vp, vp, vp]
+    lib.qlin_moe_route_grad.argtypes = [vp, i32, i64, i64, i64, vp, vp, cs, i32, f64, vp, vp]
+    lib.qlin_mxfp4_matmul.argtypes = [vp, i32, vp, cs, i64, i64, vp, vp, i64, vp, sz, vp, i32, vp]
+    lib.qlin_mxfp4_matmul_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    lib.qlin_mxfp4_matmul_workspace_bytes.restype = sz
+    lib.qlin_gather_mxfp4_matmul.argtypes = [vp, i32, vp, cs, i64, i64, vp, vp, i64, i64, vp, i64, vp,
+                                             sz, vp, i32, vp]
+    lib.qlin_gather_mxfp4_matmul_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, i32]
+    lib.qlin_gather_mxfp4_matmul_workspace_bytes.restype = sz
+    lib.qlin_moe_combine.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp]
+    lib.qlin_moe_combine_grad.argtypes = [vp, vp, i32, i64, i64, i64, vp, vp, vp, vp, vp]
     lib.qlin_last_error.restype = ctypes.c_char_p
     lib.qlin_last_path.restype = ctypes.c_char_p
     for f in ("qlin_quantize", "qlin_dequantize", "qlin_quantized_matmul", "qlin_quantized_dense",
-              "qlin_gather_qmm"):
+              "qlin_gather_qmm", "qlin_moe_route", "qlin_moe_route_grad", "qlin_mxfp4_matmul",
+              "qlin_gather_mxfp4_matmul", "qlin_moe_combine", "qlin_moe_combine_grad"):
         getattr(lib, f).restype = i32
     _lib = lib
     return lib
@@ -404,3 +417,212 @@ def gather_qmm_noalloc(x: torch.Tensor, qw: QuantizedWeight, rhs_indices: torch.
                                      _stream(dev))
     _check(rc)
     return y
+
+
+def _same(dev, **tensors):
+    """The named tensors (None skipped) are contiguous and on dev."""
+    for name, t in tensors.items():
+        if t is not None and _dev(t) != dev:
+            raise ValueError(f"{name} must be on {dev}")
+
+
+def _typed(dtype, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+
+
+def _float(**tensors):
+    for name, t in tensors.items():
+        if t.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+            raise ValueError(f"{name} must be float32, float16 or bfloat16")
+
+
+def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+              renormalize: bool = True, scale: float = 1.0, groups: int = 1, groups_kept: int = 1,
+              group_top: int = 1):
+    """qlin_moe_route: the k experts of each token and their weights.
+
+    logits [..., E]; bias float32 [E] (for the choice only). Returns
+    (weights float32 [..., k], experts int32 [..., k]), best first, equal
+    ones by ascending index; a place no expert can take holds -1 and 0.
+    """
+    lib = load_library()
+    dev = _dev(logits)
+    _float(logits=logits)
+    if logits.dim() < 1:
+        raise ValueError("logits has a last axis of experts")
+    E = logits.shape[-1]
+    if bias is not None:
+        _same(dev, bias=bias)
+        _typed(torch.float32, bias=bias)
+        if tuple(bias.shape) != (E,):
+            raise ValueError(f"bias must hold one value per expert ({E})")
+    T = logits.numel() // E if E else 0
+    shape = tuple(logits.shape[:-1]) + (max(int(k), 0),)
+    weights = torch.empty(shape, dtype=torch.float32, device=dev)
+    experts = torch.empty(shape, dtype=torch.int32, device=dev)
+    _check(lib.qlin_moe_route(_ptr(logits), _DTYPE[logits.dtype], T, E, k, _ptr(bias), score.encode(),
+                              int(bool(renormalize)), float(scale), groups, groups_kept, group_top,
+                              _ptr(weights), _ptr(experts), _stream(dev)))
+    return weights, experts
+
+
+def moe_route_grad(logits: torch.Tensor, experts: torch.Tensor, grad_weights: torch.Tensor,
+                   score: str = "softmax", renormalize: bool = True, scale: float = 1.0) -> torch.Tensor:
+    """qlin_moe_route_grad: gradient of moe_route's weights with respect to
+    logits, in logits' dtype; experts is moe_route's output for them."""
+    lib = load_library()
+    dev = _dev(logits)
+    _float(logits=logits)
+    _same(dev, experts=experts, grad_weights=grad_weights)
+    _typed(torch.int32, experts=experts)
+    _typed(torch.float32, grad_weights=grad_weights)
+    if experts.shape != grad_weights.shape or experts.shape[:-1] != logits.shape[:-1]:
+        raise ValueError("experts and grad_weights are [..., k] for logits [..., E]")
+    E, k = logits.shape[-1], experts.shape[-1]
+    T = logits.numel() // E if E else 0
+    out = torch.empty_like(logits)
+    _check(lib.qlin_moe_route_grad(_ptr(logits), _DTYPE[logits.dtype], T, E, k, _ptr(experts),
+                                   _ptr(grad_weights), score.encode(), int(bool(renormalize)), float(scale),
+                                   _ptr(out), _stream(dev)))
+    return out
+
+
+def _mxfp4_operands(x, qw, activation, dim):
+    """Device, x's pointers and dtype, its leading shape, K and N of an mxfp4 product."""
+    if qw.mode != "mxfp4" or not qw.transpose or qw.value.dim() != dim:
+        raise ValueError(f"the weight must be a {dim}-D mxfp4 weight in the [out, in] layout")
+    _dev(qw.value)
+    _dev(qw.scales)
+    K, N = qw.value.shape[-1] * 8, qw.value.shape[-2]
+    if isinstance(x, QuantizedWeight):
+        if x.mode != "mxfp4":
+            raise ValueError("a quantized x must be mxfp4")
+        t, scales, wide = x.value, x.scales, K // 8
+        code = _DTYPE[torch.uint8]
+        if tuple(scales.shape) != tuple(t.shape[:-1]) + (t.shape[-1] // 4,):
+            raise ValueError("x's scales do not fit its words")
+    else:
+        _float(x=x)
+        t, scales, wide = x, None, 2 * K if activation == "swiglu" else K
+        code = _DTYPE[x.dtype]
+    dev = _dev(t)
+    _same(dev, scales=scales, weight=qw.value, weight_scales=qw.scales)
+    if t.dim() < 1 or t.shape[-1] != wide:
+        raise ValueError(f"x's last dim {t.shape[-1] if t.dim() else None} does not match the weight's K={K}"
+                         + (" (twice K with swiglu)" if activation == "swiglu" else ""))
+    if tuple(qw.scales.shape) != tuple(qw.value.shape[:-1]) + (K // 32,):
+        raise ValueError("the weight's scales do not fit its words")
+    return dev, t, scales, code, tuple(t.shape[:-1]), K, N
+
+
+def _work(workspace, need, dev):
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    _same(dev, workspace=workspace)
+    return workspace
+
+
+def mxfp4_matmul_workspace_bytes(M: int, K: int, N: int, x_dtype: torch.dtype = torch.bfloat16) -> int:
+    """qlin_mxfp4_matmul_workspace_bytes; torch.uint8 stands for an x given as codes."""
+    return int(load_library().qlin_mxfp4_matmul_workspace_bytes(M, K, N, _DTYPE[x_dtype]))
+
+
+def mxfp4_matmul(x, qw: QuantizedWeight, activation: Optional[str] = None,
+                 out_dtype: Optional[torch.dtype] = None, workspace: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """qlin_mxfp4_matmul: x [..., K] times an mxfp4 weight [N, K], both as
+    4-bit codes on the scaled MFMA.
+
+    x is a float tensor, quantized to mxfp4 on the way (with activation
+    "swiglu": x [..., 2K], silu of its first half times its second), or an
+    mxfp4 QuantizedWeight that holds the activation's codes. y takes
+    out_dtype, by default x's (bfloat16 for codes).
+    """
+    lib = load_library()
+    dev, t, scales, code, lead, K, N = _mxfp4_operands(x, qw, activation, 2)
+    M = 1
+    for d in lead:
+        M *= d
+    dtype = out_dtype or (torch.bfloat16 if scales is not None else t.dtype)
+    y = _out(out, lead + (N,), dtype, dev)
+    need = int(lib.qlin_mxfp4_matmul_workspace_bytes(M, K, N, code))
+    ws = _work(workspace, need, dev)
+    _check(lib.qlin_mxfp4_matmul(_ptr(t), code, _ptr(scales), (activation or "none").encode(), M, K,
+                                 _ptr(qw.value), _ptr(qw.scales), N, _ptr(ws),
+                                 ws.numel() * ws.element_size(), _ptr(y), _DTYPE[dtype], _stream(dev)))
+    return y
+
+
+def gather_mxfp4_matmul_workspace_bytes(B: int, R: int, K: int, E: int, N: int,
+                                        x_dtype: torch.dtype = torch.bfloat16) -> int:
+    """qlin_gather_mxfp4_matmul_workspace_bytes; torch.uint8 stands for codes."""
+    return int(load_library().qlin_gather_mxfp4_matmul_workspace_bytes(B, R, K, E, N, _DTYPE[x_dtype]))
+
+
+def gather_mxfp4_matmul(x, qw: QuantizedWeight, experts: torch.Tensor, activation: Optional[str] = None,
+                        out_dtype: Optional[torch.dtype] = None, workspace: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """qlin_gather_mxfp4_matmul: y[r] = x[r // (R / B)] . W[experts[r]]^T.
+
+    x [B, K] (or [B, 2K] with "swiglu", or mxfp4 codes) as for mxfp4_matmul;
+    qw stacks experts [E, N, K]; experts int32 [B, ...], the experts of each
+    row of x. Returns y of shape experts.shape + (N,); a row whose expert is
+    outside [0, E) is zeros.
+    """
+    lib = load_library()
+    dev, t, scales, code, lead, K, N = _mxfp4_operands(x, qw, activation, 3)
+    _same(dev, experts=experts)
+    _typed(torch.int32, experts=experts)
+    if len(lead) != 1 or experts.dim() < 1 or experts.shape[0] != lead[0]:
+        raise ValueError("gather_mxfp4_matmul takes x [B, K] and experts [B, ...]")
+    B, R, E = lead[0], experts.numel(), qw.value.shape[0]
+    dtype = out_dtype or (torch.bfloat16 if scales is not None else t.dtype)
+    y = _out(out, tuple(experts.shape) + (N,), dtype, dev)
+    need = int(lib.qlin_gather_mxfp4_matmul_workspace_bytes(B, R, K, E, N, code))
+    ws = _work(workspace, need, dev)
+    _check(lib.qlin_gather_mxfp4_matmul(_ptr(t), code, _ptr(scales), (activation or "none").encode(), B, K,
+                                        _ptr(qw.value), _ptr(qw.scales), E, N, _ptr(experts), R, _ptr(ws),
+                                        ws.numel() * ws.element_size(), _ptr(y), _DTYPE[dtype],
+                                        _stream(dev)))
+    return y
+
+
+def _combine_operands(h, weights, experts):
+    dev = _dev(h)
+    _float(h=h)
+    _same(dev, weights=weights, experts=experts)
+    _typed(torch.float32, weights=weights)
+    _typed(torch.int32, experts=experts)
+    if h.dim() < 2 or weights.shape != h.shape[:-1] or (experts is not None and experts.shape != weights.shape):
+        raise ValueError("moe_combine takes h [..., k, D] with weights (and experts) [..., k]")
+    k, D = h.shape[-2], h.shape[-1]
+    return dev, (weights.numel() // k if k else 0), k, D
+
+
+def moe_combine(h: torch.Tensor, weights: torch.Tensor, experts: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """qlin_moe_combine: y[..., :] = sum over j of weights[..., j] * h[..., j, :],
+    places with a negative expert left out."""
+    lib = load_library()
+    dev, T, k, D = _combine_operands(h, weights, experts)
+    y = _out(out, tuple(h.shape[:-2]) + (D,), h.dtype, dev)
+    _check(lib.qlin_moe_combine(_ptr(h), _DTYPE[h.dtype], T, k, D, _ptr(weights), _ptr(experts), _ptr(y),
+                                _stream(dev)))
+    return y
+
+
+def moe_combine_grad(grad_y: torch.Tensor, h: torch.Tensor, weights: torch.Tensor,
+                     experts: Optional[torch.Tensor] = None):
+    """qlin_moe_combine_grad: (grad_h in h's dtype, grad_weights float32)."""
+    lib = load_library()
+    dev, T, k, D = _combine_operands(h, weights, experts)
+    _same(dev, grad_y=grad_y)
+    if grad_y.dtype != h.dtype or tuple(grad_y.shape) != tuple(h.shape[:-2]) + (D,):
+        raise ValueError(f"grad_y must be a {h.dtype} tensor of shape {tuple(h.shape[:-2]) + (D,)}")
+    grad_h = torch.empty_like(h)
+    grad_w = torch.empty_like(weights)
+    _check(lib.qlin_moe_combine_grad(_ptr(grad_y), _ptr(h), _DTYPE[h.dtype], T, k, D, _ptr(weights),
+                                     _ptr(experts), _ptr(grad_h), _ptr(grad_w), _stream(dev)))
+    return grad_h, grad_w

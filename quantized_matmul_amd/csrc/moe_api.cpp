@@ -1,0 +1,300 @@
+// moe_api.cpp -- the C ABI of the mixture-of-experts operators: argument
+// validation, workspace layout and launches. As everywhere in the library, a
+// rejected call launches nothing.
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "../../include/qlin.h"
+#include "api_common.h"
+#include "moe_common.h"
+#include "mx4_plan.h"
+
+using qlin::device_status;
+using qlin::fail;
+using qlin::is_float_dtype;
+using qlin::ok;
+
+namespace {
+
+constexpr int64_t kMaxIndex = (1LL << 31) - 1;
+
+qlin_status check_score(const char* score, double scale, int* sigmoid) {
+    if (!score) return fail(QLIN_ERR_INVALID_ARGUMENT, "score is NULL");
+    if (!strcmp(score, "softmax")) *sigmoid = 0;
+    else if (!strcmp(score, "sigmoid")) *sigmoid = 1;
+    else return fail(QLIN_ERR_INVALID_ARGUMENT, "unknown score \"%s\" (softmax, sigmoid)", score);
+    if (!std::isfinite((float)scale)) return fail(QLIN_ERR_INVALID_ARGUMENT, "scale must be finite in fp32");
+    return QLIN_OK;
+}
+
+qlin_status check_route(int dtype, int64_t T, int64_t E, int64_t k) {
+    if (!is_float_dtype(dtype)) return fail(QLIN_ERR_INVALID_ARGUMENT, "logits must be f32, f16 or bf16");
+    if (E < 1 || E > qlin::kRouteMaxExperts)
+        return fail(QLIN_ERR_INVALID_ARGUMENT, "E must be in [1, %d] (got %lld)", qlin::kRouteMaxExperts, (long long)E);
+    if (k < 1 || k > E || k > qlin::kRouteMaxChoice)
+        return fail(QLIN_ERR_INVALID_ARGUMENT, "k must be in [1, min(E, %d)] (got %lld)", qlin::kRouteMaxChoice,
+                    (long long)k);
+    if (T < 0) return fail(QLIN_ERR_INVALID_ARGUMENT, "T must be >= 0");
+    if (T > kMaxIndex) return fail(QLIN_ERR_UNSUPPORTED, "more than 2^31 - 1 tokens are not supported");
+    return QLIN_OK;
+}
+
+qlin_status check_aligned(const void* p, uintptr_t align, const char* what) {
+    if ((uintptr_t)p % align) return fail(QLIN_ERR_INVALID_ARGUMENT, "%s must be %d-byte aligned", what, (int)align);
+    return QLIN_OK;
+}
+
+uintptr_t elem(int dtype) { return dtype == QLIN_F32 ? 4 : 2; }
+
+size_t up(size_t n, size_t to) { return (n + to - 1) / to * to; }
+
+// Scale rows as the tiled kernel reads them.
+int64_t scale_stride(int64_t K) { return (int64_t)up((size_t)(K / 32), 16); }
+
+// Pieces of a product's workspace, each 256-byte aligned: x's codes and
+// scales (or, for given codes, their scales in 16-byte rows), W's scales in
+// 16-byte rows where K / 32 is not a multiple of 16, the row plan.
+struct Layout {
+    size_t xq, xs, ws, plan, bytes;
+};
+Layout layout(int64_t rows, int64_t R, int64_t K, int64_t E, int64_t N, int x_dtype, bool gather) {
+    Layout l{};
+    const bool tiled = qlin::mx4_tiled(gather ? R : rows, N, K, E, gather);
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t p = at;
+        at += up(n, 256);
+        return p;
+    };
+    l.xq = take(x_dtype == QLIN_U8 ? 0 : (size_t)rows * (size_t)(K / 2));
+    l.xs = take(x_dtype != QLIN_U8 || tiled ? (size_t)rows * (size_t)scale_stride(K) : 0);
+    l.ws = take(tiled && K % 512 ? (size_t)E * (size_t)N * (size_t)scale_stride(K) : 0);
+    l.plan = take(gather ? qlin::mx4_plan_bytes(R, E) : 0);
+    l.bytes = at;
+    return l;
+}
+
+bool product_sizes_ok(int64_t rows, int64_t K, int64_t N) {
+    return rows >= 0 && K >= 32 && K % 32 == 0 && K <= (1LL << 22) && N >= 1 && rows <= kMaxIndex && N <= kMaxIndex;
+}
+
+// Everything the dense and the gathered product share. rows: rows of x.
+qlin_status product(const void* x, int x_dtype, const void* x_scales, const char* activation, int64_t rows, int64_t K,
+                    const uint32_t* wq, const void* scales, int64_t E, int64_t N, const int32_t* experts, int64_t R,
+                    bool gather, void* workspace, size_t workspace_bytes, void* y, int y_dtype, hipStream_t st,
+                    const char* what) {
+    int swiglu = 0;
+    if (activation && !strcmp(activation, "swiglu")) swiglu = 1;
+    else if (activation && strcmp(activation, "none"))
+        return fail(QLIN_ERR_INVALID_ARGUMENT, "unknown activation \"%s\" (none, swiglu)", activation);
+    const bool codes = x_dtype == QLIN_U8;
+    if (!codes && !is_float_dtype(x_dtype))
+        return fail(QLIN_ERR_INVALID_ARGUMENT, "x must be f32, f16, bf16 or mxfp4 words");
+    if (!is_float_dtype(y_dtype)) return fail(QLIN_ERR_INVALID_ARGUMENT, "y must be f32, f16 or bf16");
+    if (codes && swiglu) return fail(QLIN_ERR_INVALID_ARGUMENT, "mxfp4 words take no activation");
+    if (rows < 0 || R < 0) return fail(QLIN_ERR_INVALID_ARGUMENT, "negative size");
+    if (N <= 0 || K <= 0 || E <= 0) return fail(QLIN_ERR_INVALID_ARGUMENT, "N, K and E must be positive");
+    if (K % 32) return fail(QLIN_ERR_INVALID_ARGUMENT, "K must be a multiple of 32 (got %lld)", (long long)K);
+    if (!product_sizes_ok(rows, K, N) || R > kMaxIndex)
+        return fail(QLIN_ERR_UNSUPPORTED, "rows and N above 2^31 - 1 or K above 2^22 are not supported");
+    if (gather) {
+        if (E > qlin::kMx4MaxExperts)
+            return fail(QLIN_ERR_UNSUPPORTED, "more than %lld experts are not supported",
+                        (long long)qlin::kMx4MaxExperts);
+        if (rows == 0 ? R != 0 : R % rows != 0)
+            return fail(QLIN_ERR_INVALID_ARGUMENT, "R (%lld) must be a multiple of the rows of x (%lld)", (long long)R,
+                        (long long)rows);
+    }
+    if (R == 0) return ok();
+    if (!x || !wq || !scales || !y || (gather && !experts)) return fail(QLIN_ERR_INVALID_ARGUMENT, "NULL tensor pointer");
+    if (codes && !x_scales) return fail(QLIN_ERR_INVALID_ARGUMENT, "mxfp4 words need x_scales");
+    if (!codes && x_scales) return fail(QLIN_ERR_INVALID_ARGUMENT, "x_scales go with mxfp4 words only");
+    qlin_status s;
+    if ((s = check_aligned(x, codes ? 16 : elem(x_dtype), "x"))) return s;
+    if ((s = check_aligned(wq, 16, "wq"))) return s;
+    if ((s = check_aligned(y, elem(y_dtype), "y"))) return s;
+    if ((s = check_aligned(experts, 4, "experts"))) return s;
+    const Layout l = layout(rows, R, K, E, N, x_dtype, gather);
+    if (l.bytes) {
+        if (!workspace || workspace_bytes < l.bytes)
+            return fail(QLIN_ERR_INVALID_ARGUMENT, "workspace of %zu bytes needed (got %zu)", l.bytes,
+                        workspace ? workspace_bytes : (size_t)0);
+        if ((s = check_aligned(workspace, 16, "workspace"))) return s;
+    }
+    char* const w = (char*)workspace;
+    const int64_t KS = K / 32, stride = scale_stride(K);
+    qlin::Mx4Args a{};
+    a.xq = (const uint8_t*)x;
+    a.xs = (const uint8_t*)x_scales;
+    a.wq = (const uint8_t*)wq;
+    a.ws = (const uint8_t*)scales;
+    a.y = y;
+    a.M = R;
+    a.N = N;
+    a.K = K;
+    a.xsstride = a.wsstride = KS;
+    a.ydt = y_dtype;
+    a.experts = experts;
+    a.B = rows;
+    a.E = E;
+    a.plan = w + l.plan;
+    hipError_t e;
+    if (!codes) {
+        a.xq = (const uint8_t*)(w + l.xq);
+        a.xs = (const uint8_t*)(w + l.xs);
+        a.xsstride = stride;
+        e = qlin::launch_mxfp4_activation(x, x_dtype, rows, K, swiglu, (uint32_t*)(w + l.xq), (uint8_t*)(w + l.xs),
+                                          stride, st);
+        if (e != hipSuccess) return device_status(e, what);
+    }
+    if (qlin::mx4_tiled(R, N, K, E, gather)) {
+        // the tiled kernel reads scale rows 16 bytes at a time
+        if (codes && (KS % 16 || (uintptr_t)x_scales % 16)) {
+            e = qlin::launch_mx4_pad_scales(a.xs, rows, KS, (uint8_t*)(w + l.xs), stride, st);
+            if (e != hipSuccess) return device_status(e, what);
+            a.xs = (const uint8_t*)(w + l.xs);
+            a.xsstride = stride;
+        }
+        if (KS % 16) {
+            e = qlin::launch_mx4_pad_scales(a.ws, E * N, KS, (uint8_t*)(w + l.ws), stride, st);
+            if (e != hipSuccess) return device_status(e, what);
+            a.ws = (const uint8_t*)(w + l.ws);
+            a.wsstride = stride;
+        }
+    }
+    const char* path = "";
+    e = qlin::launch_mx4_matmul(a, st, &path);
+    if (e == hipSuccess) qlin::record_path(path);
+    return device_status(e, what);
+}
+
+}  // namespace
+
+extern "C" {
+
+qlin_status qlin_moe_route(const void* logits, qlin_dtype dtype, int64_t T, int64_t E, int64_t k, const float* bias,
+                           const char* score, int renormalize, double scale, int64_t groups, int64_t groups_kept,
+                           int group_top, float* weights, int32_t* experts, void* stream) {
+    int sigmoid = 0;
+    qlin_status s = check_score(score, scale, &sigmoid);
+    if (s) return s;
+    if ((s = check_route(dtype, T, E, k))) return s;
+    if (groups < 1 || groups > qlin::kRouteMaxGroups || E % groups)
+        return fail(QLIN_ERR_INVALID_ARGUMENT, "groups must divide E and be in [1, %d] (got %lld)",
+                    qlin::kRouteMaxGroups, (long long)groups);
+    if (groups_kept < 1 || groups_kept > groups)
+        return fail(QLIN_ERR_INVALID_ARGUMENT, "groups_kept must be in [1, groups] (got %lld)", (long long)groups_kept);
+    if (group_top < 1 || group_top > 2 || group_top > E / groups)
+        return fail(QLIN_ERR_INVALID_ARGUMENT, "group_top must be 1 or 2 and at most a group's experts (got %d)",
+                    group_top);
+    if (k > groups_kept * (E / groups))
+        return fail(QLIN_ERR_INVALID_ARGUMENT, "k = %lld experts do not fit the %lld kept groups of %lld",
+                    (long long)k, (long long)groups_kept, (long long)(E / groups));
+    if (T == 0) return ok();
+    if (!logits || !weights || !experts) return fail(QLIN_ERR_INVALID_ARGUMENT, "NULL tensor pointer");
+    if ((s = check_aligned(logits, elem(dtype), "logits"))) return s;
+    if ((s = check_aligned(bias, 4, "bias"))) return s;
+    if ((s = check_aligned(weights, 4, "weights"))) return s;
+    if ((s = check_aligned(experts, 4, "experts"))) return s;
+    return device_status(qlin::launch_moe_route(logits, dtype, T, (int)E, (int)k, bias, sigmoid, renormalize ? 1 : 0,
+                                                (float)scale, (int)groups, (int)groups_kept, group_top, weights,
+                                                experts, (hipStream_t)stream),
+                         "moe_route");
+}
+
+qlin_status qlin_moe_route_grad(const void* logits, qlin_dtype dtype, int64_t T, int64_t E, int64_t k,
+                                const int32_t* experts, const float* grad_weights, const char* score, int renormalize,
+                                double scale, void* grad_logits, void* stream) {
+    int sigmoid = 0;
+    qlin_status s = check_score(score, scale, &sigmoid);
+    if (s) return s;
+    if ((s = check_route(dtype, T, E, k))) return s;
+    if (T == 0) return ok();
+    if (!logits || !experts || !grad_weights || !grad_logits)
+        return fail(QLIN_ERR_INVALID_ARGUMENT, "NULL tensor pointer");
+    if ((s = check_aligned(logits, elem(dtype), "logits"))) return s;
+    if ((s = check_aligned(grad_logits, elem(dtype), "grad_logits"))) return s;
+    if ((s = check_aligned(grad_weights, 4, "grad_weights"))) return s;
+    if ((s = check_aligned(experts, 4, "experts"))) return s;
+    return device_status(qlin::launch_moe_route_grad(logits, dtype, T, (int)E, (int)k, experts, grad_weights, sigmoid,
+                                                     renormalize ? 1 : 0, (float)scale, grad_logits,
+                                                     (hipStream_t)stream),
+                         "moe_route_grad");
+}
+
+size_t qlin_mxfp4_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N, qlin_dtype x_dtype) {
+    if (M == 0 || !product_sizes_ok(M, K, N)) return 0;
+    return layout(M, M, K, 1, N, x_dtype, false).bytes;
+}
+
+qlin_status qlin_mxfp4_matmul(const void* x, qlin_dtype x_dtype, const void* x_scales, const char* activation,
+                              int64_t M, int64_t K, const uint32_t* wq, const void* scales, int64_t N, void* workspace,
+                              size_t workspace_bytes, void* y, qlin_dtype y_dtype, void* stream) {
+    return product(x, x_dtype, x_scales, activation, M, K, wq, scales, 1, N, nullptr, M, false, workspace,
+                   workspace_bytes, y, y_dtype, (hipStream_t)stream, "mxfp4_matmul");
+}
+
+size_t qlin_gather_mxfp4_matmul_workspace_bytes(int64_t B, int64_t R, int64_t K, int64_t E, int64_t N,
+                                                qlin_dtype x_dtype) {
+    if (B < 1 || R < 1 || E < 1 || R > kMaxIndex || E > qlin::kMx4MaxExperts || !product_sizes_ok(B, K, N)) return 0;
+    return layout(B, R, K, E, N, x_dtype, true).bytes;
+}
+
+qlin_status qlin_gather_mxfp4_matmul(const void* x, qlin_dtype x_dtype, const void* x_scales, const char* activation,
+                                     int64_t B, int64_t K, const uint32_t* wq, const void* scales, int64_t E, int64_t N,
+                                     const int32_t* experts, int64_t R, void* workspace, size_t workspace_bytes,
+                                     void* y, qlin_dtype y_dtype, void* stream) {
+    return product(x, x_dtype, x_scales, activation, B, K, wq, scales, E, N, experts, R, true, workspace,
+                   workspace_bytes, y, y_dtype, (hipStream_t)stream, "gather_mxfp4_matmul");
+}
+
+namespace {
+
+qlin_status check_combine(int dtype, int64_t T, int64_t k, int64_t D) {
+    if (!is_float_dtype(dtype)) return fail(QLIN_ERR_INVALID_ARGUMENT, "h must be f32, f16 or bf16");
+    if (T < 0) return fail(QLIN_ERR_INVALID_ARGUMENT, "T must be >= 0");
+    if (k < 1 || D < 1) return fail(QLIN_ERR_INVALID_ARGUMENT, "k and D must be positive");
+    if (k > kMaxIndex || (T && k > kMaxIndex / T) || D > kMaxIndex)
+        return fail(QLIN_ERR_UNSUPPORTED, "more than 2^31 - 1 rows or columns are not supported");
+    return QLIN_OK;
+}
+
+}  // namespace
+
+qlin_status qlin_moe_combine(const void* h, qlin_dtype dtype, int64_t T, int64_t k, int64_t D, const float* weights,
+                             const int32_t* experts, void* y, void* stream) {
+    qlin_status s = check_combine(dtype, T, k, D);
+    if (s) return s;
+    if (T == 0) return ok();
+    if (!h || !weights || !y) return fail(QLIN_ERR_INVALID_ARGUMENT, "NULL tensor pointer");
+    if ((s = check_aligned(h, elem(dtype), "h"))) return s;
+    if ((s = check_aligned(y, elem(dtype), "y"))) return s;
+    if ((s = check_aligned(weights, 4, "weights"))) return s;
+    if ((s = check_aligned(experts, 4, "experts"))) return s;
+    return device_status(qlin::launch_moe_combine(h, dtype, T, (int)k, D, weights, experts, y, (hipStream_t)stream),
+                         "moe_combine");
+}
+
+qlin_status qlin_moe_combine_grad(const void* grad_y, const void* h, qlin_dtype dtype, int64_t T, int64_t k, int64_t D,
+                                  const float* weights, const int32_t* experts, void* grad_h, float* grad_weights,
+                                  void* stream) {
+    qlin_status s = check_combine(dtype, T, k, D);
+    if (s) return s;
+    if (T == 0) return ok();
+    if (!grad_y || !h || !weights || !grad_h || !grad_weights)
+        return fail(QLIN_ERR_INVALID_ARGUMENT, "NULL tensor pointer");
+    if ((s = check_aligned(h, elem(dtype), "h"))) return s;
+    if ((s = check_aligned(grad_y, elem(dtype), "grad_y"))) return s;
+    if ((s = check_aligned(grad_h, elem(dtype), "grad_h"))) return s;
+    if ((s = check_aligned(weights, 4, "weights"))) return s;
+    if ((s = check_aligned(grad_weights, 4, "grad_weights"))) return s;
+    if ((s = check_aligned(experts, 4, "experts"))) return s;
+    return device_status(qlin::launch_moe_combine_grad(grad_y, h, dtype, T, (int)k, D, weights, experts, grad_h,
+                                                       grad_weights, (hipStream_t)stream),
+                         "moe_combine_grad");
+}
+
+}  // extern "C"

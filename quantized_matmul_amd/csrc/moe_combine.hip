@@ -1,0 +1,166 @@
+// moe_combine.hip -- joins the experts' rows of each token, and its gradient.
+//
+//   y[t] = sum_j w[t, j] h[t, j]            h [T, k, D], w [T, k]
+//   dh[t, j] = w[t, j] dy[t]
+//   dw[t, j] = sum_d dy[t, d] h[t, j, d]
+//
+// Places whose expert is negative (dropped by the router) are left out: their
+// rows of h are not read, dh and dw get zeros. Sums are fp32 in a fixed order;
+// each output is rounded once.
+
+#include "qlin_common.h"
+#include "moe_common.h"
+
+namespace qlin {
+namespace {
+
+// VEC elements of dtype DT at element i (16-byte aligned unless VEC is 1).
+template <int DT, int VEC>
+__device__ __forceinline__ void load_v(const void* p, int64_t i, float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+        v[0] = load_f<DT>(p, i);
+    } else if constexpr (DT == QLIN_F32) {
+        const float4 q = *(const float4*)((const float*)p + i);
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
+        const uint4 q = *(const uint4*)((const uint16_t*)p + i);
+        const uint32_t d[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            v[2 * c] = DT == QLIN_BF16 ? bf16_bits_to_f32(d[c] & 0xFFFFu) : f16_bits_to_f32(d[c] & 0xFFFFu);
+            v[2 * c + 1] = DT == QLIN_BF16 ? bf16_bits_to_f32(d[c] >> 16) : f16_bits_to_f32(d[c] >> 16);
+        }
+    }
+}
+
+template <int DT, int VEC>
+__device__ __forceinline__ void store_v(void* p, int64_t i, const float (&v)[VEC]) {
+    if constexpr (VEC == 1) {
+        store_f<DT>(p, i, v[0]);
+    } else if constexpr (DT == QLIN_F32) {
+        *(float4*)((float*)p + i) = float4{v[0], v[1], v[2], v[3]};
+    } else {
+        uint32_t d[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t lo = DT == QLIN_BF16 ? f32_to_bf16_rne(v[2 * c]) : f32_to_f16_rne(v[2 * c]);
+            const uint32_t hi = DT == QLIN_BF16 ? f32_to_bf16_rne(v[2 * c + 1]) : f32_to_f16_rne(v[2 * c + 1]);
+            d[c] = lo | (hi << 16);
+        }
+        *(uint4*)((uint16_t*)p + i) = uint4{d[0], d[1], d[2], d[3]};
+    }
+}
+
+struct CombineArgs {
+    const void* h;
+    const float* w;
+    const int32_t* experts;   // [T, k] or null
+    int64_t T, D;
+    int k;
+    void* y;
+    const void* gy;
+    void* gh;
+    float* gw;
+};
+
+constexpr int COMBINE_THREADS = 256;
+
+// Each thread owns VEC consecutive outputs of one token.
+template <int DT, int VEC>
+__global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(CombineArgs a) {
+    const int64_t per = a.D / VEC;
+    const int64_t i = (int64_t)blockIdx.x * COMBINE_THREADS + threadIdx.x;
+    if (i >= a.T * per) return;
+    const int64_t t = i / per, d = (i - t * per) * VEC;
+    float acc[VEC];
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) acc[c] = 0.0f;
+    for (int j = 0; j < a.k; ++j) {
+        const int64_t r = t * a.k + j;
+        if (a.experts && a.experts[r] < 0) continue;
+        const float w = a.w[r];
+        float v[VEC];
+        load_v<DT, VEC>(a.h, r * a.D + d, v);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) acc[c] += w * v[c];
+    }
+    store_v<DT, VEC>(a.y, t * a.D + d, acc);
+}
+
+// One wave per row (t, j).
+template <int DT, int VEC>
+__global__ void __launch_bounds__(COMBINE_THREADS) combine_grad_kernel(CombineArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t r = (int64_t)blockIdx.x * (COMBINE_THREADS / 64) + (threadIdx.x >> 6);
+    if (r >= a.T * a.k) return;
+    const int64_t t = r / a.k;
+    const bool dead = a.experts && a.experts[r] < 0;
+    const float w = dead ? 0.0f : a.w[r];
+    float sum = 0.0f;
+    for (int64_t d = (int64_t)lane * VEC; d < a.D; d += 64 * VEC) {
+        float g[VEC], v[VEC], o[VEC];
+        if (dead) {
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) o[c] = 0.0f;
+        } else {
+            load_v<DT, VEC>(a.gy, t * a.D + d, g);
+            load_v<DT, VEC>(a.h, r * a.D + d, v);
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) {
+                sum += g[c] * v[c];
+                o[c] = w * g[c];
+            }
+        }
+        store_v<DT, VEC>(a.gh, r * a.D + d, o);
+    }
+    sum = wave_sum(sum);
+    if (lane == 0) a.gw[r] = sum;
+}
+
+bool wide(int dt, int64_t D, const void* a, const void* b, const void* c) {
+    const int64_t per = dt == QLIN_F32 ? 4 : 8;
+    return D % per == 0 && (((uintptr_t)a | (uintptr_t)b | (uintptr_t)c) & 15) == 0;
+}
+
+template <int DT, int WIDE>
+void run_combine(const CombineArgs& a, bool vec, hipStream_t st) {
+    const int64_t n = a.T * (vec ? a.D / WIDE : a.D);
+    const unsigned grid = (unsigned)((n + COMBINE_THREADS - 1) / COMBINE_THREADS);
+    if (vec) combine_kernel<DT, WIDE><<<grid, COMBINE_THREADS, 0, st>>>(a);
+    else combine_kernel<DT, 1><<<grid, COMBINE_THREADS, 0, st>>>(a);
+}
+
+template <int DT, int WIDE>
+void run_combine_grad(const CombineArgs& a, bool vec, hipStream_t st) {
+    const int64_t rows = a.T * a.k;
+    const unsigned grid = (unsigned)((rows + COMBINE_THREADS / 64 - 1) / (COMBINE_THREADS / 64));
+    if (vec) combine_grad_kernel<DT, WIDE><<<grid, COMBINE_THREADS, 0, st>>>(a);
+    else combine_grad_kernel<DT, 1><<<grid, COMBINE_THREADS, 0, st>>>(a);
+}
+
+}  // namespace
+
+hipError_t launch_moe_combine(const void* h, int dt, int64_t T, int k, int64_t D, const float* weights,
+                              const int32_t* experts, void* y, hipStream_t st) {
+    CombineArgs a{};
+    a.h = h; a.w = weights; a.experts = experts; a.T = T; a.D = D; a.k = k; a.y = y;
+    const bool vec = wide(dt, D, h, y, nullptr);
+    if (dt == QLIN_F32) run_combine<QLIN_F32, 4>(a, vec, st);
+    else if (dt == QLIN_BF16) run_combine<QLIN_BF16, 8>(a, vec, st);
+    else run_combine<QLIN_F16, 8>(a, vec, st);
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_combine_grad(const void* gy, const void* h, int dt, int64_t T, int k, int64_t D,
+                                   const float* weights, const int32_t* experts, void* gh, float* gw,
+                                   hipStream_t st) {
+    CombineArgs a{};
+    a.h = h; a.w = weights; a.experts = experts; a.T = T; a.D = D; a.k = k; a.gy = gy; a.gh = gh; a.gw = gw;
+    const bool vec = wide(dt, D, h, gy, gh);
+    if (dt == QLIN_F32) run_combine_grad<QLIN_F32, 4>(a, vec, st);
+    else if (dt == QLIN_BF16) run_combine_grad<QLIN_BF16, 8>(a, vec, st);
+    else run_combine_grad<QLIN_F16, 8>(a, vec, st);
+    return hipGetLastError();
+}
+
+}  // namespace qlin

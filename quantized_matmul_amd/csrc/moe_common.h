@@ -1,0 +1,94 @@
+// moe_common.h -- wave-wide helpers and launcher declarations of the
+// mixture-of-experts operators (routing, mxfp4 products, combine).
+#pragma once
+
+#include "qlin_common.h"
+
+namespace qlin {
+
+// One step of a wave reduction over DPP lanes: lanes without a source keep
+// `id`. row_shr 1, 2, 4, 8 reduce each row of 16 into its last lane; row_bcast
+// 15 and 31 carry rows into the next ones; lane 63 then holds the result.
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float id, float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(id), __float_as_int(v), CTRL, 0xf, 0xf, false));
+}
+
+// Value of v in a lane every lane names (wave-uniform result).
+__device__ __forceinline__ float lane_value(float v, int lane) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+// Largest v of the wave's 64 lanes, all active, none NaN.
+__device__ __forceinline__ float wave_max(float v) {
+    v = fmaxf(v, dpp_f<0x111>(v, v));
+    v = fmaxf(v, dpp_f<0x112>(v, v));
+    v = fmaxf(v, dpp_f<0x114>(v, v));
+    v = fmaxf(v, dpp_f<0x118>(v, v));
+    v = fmaxf(v, dpp_f<0x142>(v, v));
+    v = fmaxf(v, dpp_f<0x143>(v, v));
+    return lane_value(v, 63);
+}
+
+// Sum of v over the wave's 64 lanes, all active, in one fixed order.
+__device__ __forceinline__ float wave_sum(float v) {
+    v += dpp_f<0x111>(0.0f, v);
+    v += dpp_f<0x112>(0.0f, v);
+    v += dpp_f<0x114>(0.0f, v);
+    v += dpp_f<0x118>(0.0f, v);
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xa, 0xf, false));
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xc, 0xf, false));
+    return lane_value(v, 63);
+}
+
+// Largest expert count and choice of the router: 64 lanes of 16 experts, one
+// lane per place.
+constexpr int kRouteMaxExperts = 1024;
+constexpr int kRouteMaxChoice = 64;
+constexpr int kRouteMaxGroups = 64;
+
+hipError_t launch_moe_route(const void* logits, int dt, int64_t T, int E, int k, const float* bias,
+                            int sigmoid, int renorm, float scale, int groups, int kept, int group_top,
+                            float* weights, int32_t* experts, hipStream_t st);
+hipError_t launch_moe_route_grad(const void* logits, int dt, int64_t T, int E, int k, const int32_t* experts,
+                                 const float* grad_w, int sigmoid, int renorm, float scale, void* grad,
+                                 hipStream_t st);
+
+hipError_t launch_moe_combine(const void* h, int dt, int64_t T, int k, int64_t D, const float* weights,
+                              const int32_t* experts, void* y, hipStream_t st);
+hipError_t launch_moe_combine_grad(const void* gy, const void* h, int dt, int64_t T, int k, int64_t D,
+                                   const float* weights, const int32_t* experts, void* gh, float* gw,
+                                   hipStream_t st);
+
+// Quantizes x [M, K] (or silu(x[:, :K]) * x[:, K:] of x [M, 2K]) to mxfp4:
+// words [M, K/8], scale rows `sstride` bytes apart; bytes past K/32 get 127.
+hipError_t launch_mxfp4_activation(const void* x, int dt, int64_t M, int64_t K, int swiglu, uint32_t* xq,
+                                   uint8_t* xs, int64_t sstride, hipStream_t st);
+
+// Product of two mxfp4 operands; gather form with experts != null.
+struct Mx4Args {
+    const uint8_t* xq;        // codes [B, K/2 bytes]
+    const uint8_t* xs;        // scale rows, xsstride bytes apart
+    const uint8_t* wq;        // codes [E, N, K/2 bytes]
+    const uint8_t* ws;        // scale rows [E, N], wsstride bytes apart
+    void* y;                  // [M, N] (gather: [R, N])
+    int64_t M, N, K;          // gather: M = R
+    int64_t xsstride, wsstride;
+    int ydt;
+    // gather form
+    const int32_t* experts;   // [R] or null
+    int64_t B, E;             // row r reads x row r / (R / B)
+    void* plan;               // workspace of the row plan
+};
+// Bytes of the row plan for R rows over E experts (0 where none is made).
+size_t mx4_plan_bytes(int64_t R, int64_t E);
+// Whether the tiled kernel (and not the streaming one) takes the shape: it
+// reads scale rows in 16-byte units.
+bool mx4_tiled(int64_t M, int64_t N, int64_t K, int64_t E, bool gather);
+hipError_t launch_mx4_matmul(const Mx4Args& a, hipStream_t st, const char** path);
+// Copies scale rows of KS bytes to rows `stride` bytes apart, filled with 127.
+hipError_t launch_mx4_pad_scales(const uint8_t* s, int64_t rows, int64_t KS, uint8_t* out, int64_t stride,
+                                 hipStream_t st);
+
+}  // namespace qlin

@@ -16,9 +16,34 @@
 #include <string>
 
 #include "../../include/qlin.h"
+#include "api_common.h"
 #include "qlin_common.h"
 
 namespace qlin {
+
+thread_local std::string g_last_error;
+
+qlin_status fail(qlin_status st, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_last_error = buf;
+    return st;
+}
+
+qlin_status ok() {
+    g_last_error.clear();
+    return QLIN_OK;
+}
+
+qlin_status device_status(hipError_t e, const char* what) {
+    if (e == hipSuccess) return ok();
+    return fail(QLIN_ERR_DEVICE, "%s: %s", what, hipGetErrorString(e));
+}
+
+bool is_float_dtype(int d) { return d == QLIN_F32 || d == QLIN_F16 || d == QLIN_BF16; }
 
 DeviceShape device_shape() {
     // one entry per device id; a racing first call on one device at worst
@@ -52,7 +77,11 @@ hipError_t launch_qmm_nt_split(const QmmArgs& q, void* workspace, hipStream_t st
 
 namespace {
 
-thread_local std::string g_last_error;
+using qlin::device_status;
+using qlin::fail;
+using qlin::is_float_dtype;
+using qlin::ok;
+
 // kernel path of the calling thread's last successful matmul-type call
 thread_local const char* g_last_path = "";
 
@@ -68,32 +97,10 @@ void note_path(const char* p) {
     }
 }
 
-qlin_status fail(qlin_status st, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return st;
-}
-
 // qqmm in mxfp8 takes the scaled fp8 MFMA kernel from this many rows of x
 // (below it the weight stream bounds the time and the exact bf16 decode
 // kernels serve).
 constexpr int64_t kQqmmScaledMinRows = 32;
-
-qlin_status ok() {
-    g_last_error.clear();
-    return QLIN_OK;
-}
-
-qlin_status device_status(hipError_t e, const char* what) {
-    if (e == hipSuccess) return ok();
-    return fail(QLIN_ERR_DEVICE, "%s: %s", what, hipGetErrorString(e));
-}
-
-bool is_float_dtype(int d) { return d == QLIN_F32 || d == QLIN_F16 || d == QLIN_BF16; }
 
 // Parse the mode string and check (group_size, bits) against it and against
 // the quantized axis length.
@@ -256,9 +263,11 @@ qlin_status run_qmm(const qlin::QmmArgs& a, const uint32_t* perm, const uint32_t
 
 }  // namespace
 
+void qlin::record_path(const char* p) { note_path(p); }
+
 extern "C" {
 
-const char* qlin_last_error(void) { return g_last_error.c_str(); }
+const char* qlin_last_error(void) { return qlin::g_last_error.c_str(); }
 
 const char* qlin_last_path(void) { return g_last_path; }
 

@@ -1,0 +1,114 @@
+"""Argument checks of the mixture-of-experts entry points; no GPU: every
+rejection happens before the device is touched."""
+import ctypes
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+LIB = os.path.join(ROOT, "quantized_matmul_amd", "libqlin.so")
+
+pytestmark = pytest.mark.skipif(not os.path.exists(LIB), reason="libqlin.so not built")
+
+INVALID, UNSUPPORTED = 1, 2
+F32, F16, BF16, U8 = 0, 1, 2, 3
+P = ctypes.c_void_p(0x1000)   # never dereferenced: validation rejects first
+ODD = ctypes.c_void_p(0x1001)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from quantized_matmul_amd import _binding
+    return _binding.load_library()
+
+
+def err(lib):
+    return lib.qlin_last_error().decode()
+
+
+def test_header_functions_are_exported(lib):
+    text = open(os.path.join(ROOT, "include", "qlin.h")).read()
+    names = set(re.findall(r"\b(qlin_[a-z0-9_]+)\s*\(", text))
+    assert names >= {"qlin_moe_route", "qlin_moe_route_grad", "qlin_mxfp4_matmul", "qlin_gather_mxfp4_matmul",
+                     "qlin_mxfp4_matmul_workspace_bytes", "qlin_gather_mxfp4_matmul_workspace_bytes",
+                     "qlin_moe_combine", "qlin_moe_combine_grad"}
+    for n in names:
+        assert hasattr(lib, n), n
+
+
+def caller(f, base):
+    return lambda **kw: f(*dict(base, **kw).values())
+
+
+def test_route_rejects(lib):
+    call = caller(lib.qlin_moe_route, dict(x=P, dt=BF16, T=4, E=64, k=8, bias=None, score=b"softmax", renorm=1,
+                                           scale=1.0, groups=1, kept=1, top=1, w=P, e=P, st=None))
+    for bad in (dict(dt=U8), dict(E=0), dict(E=1025), dict(k=0), dict(k=65), dict(E=4, k=5), dict(T=-1),
+                dict(score=b"tanh"), dict(score=None), dict(scale=float("inf")), dict(scale=1e39),
+                dict(groups=5), dict(groups=0), dict(groups=8, kept=9), dict(groups=8, kept=0),
+                dict(groups=8, kept=2, top=3), dict(groups=64, kept=8, top=2), dict(groups=16, kept=1, k=8),
+                dict(x=None), dict(w=None), dict(e=None), dict(x=ODD), dict(dt=F32, x=ctypes.c_void_p(0x1002)),
+                dict(bias=ctypes.c_void_p(0x1002)), dict(w=ODD), dict(e=ODD)):
+        assert call(**bad) == INVALID, bad
+        assert err(lib)
+    assert call(T=1 << 31) == UNSUPPORTED
+    assert call(T=0, x=None, w=None, e=None) == 0
+    assert err(lib) == ""
+
+
+def test_route_grad_rejects(lib):
+    call = caller(lib.qlin_moe_route_grad, dict(x=P, dt=F32, T=4, E=64, k=8, e=P, g=P, score=b"sigmoid", renorm=1,
+                                                scale=1.0, out=P, st=None))
+    for bad in (dict(dt=U8), dict(E=2000), dict(k=0), dict(T=-1), dict(score=b""), dict(scale=float("nan")),
+                dict(x=None), dict(e=None), dict(g=None), dict(out=None), dict(x=ODD), dict(e=ODD), dict(g=ODD),
+                dict(out=ODD)):
+        assert call(**bad) == INVALID, bad
+    assert call(T=0, x=None, e=None, g=None, out=None) == 0
+
+
+def test_product_rejects(lib):
+    need = lib.qlin_mxfp4_matmul_workspace_bytes(4, 128, 64, BF16)
+    assert need > 0
+    call = caller(lib.qlin_mxfp4_matmul, dict(x=P, xdt=BF16, xs=None, act=b"none", M=4, K=128, wq=P, ws=P, N=64,
+                                              work=P, nb=need, y=P, ydt=BF16, st=None))
+    for bad in (dict(xdt=7), dict(ydt=U8), dict(act=b"gelu"), dict(M=-1), dict(K=0), dict(K=48), dict(N=0),
+                dict(x=None), dict(wq=None), dict(ws=None), dict(y=None), dict(xs=P), dict(xdt=U8),
+                dict(xdt=U8, xs=P, act=b"swiglu"), dict(xdt=U8, xs=P, x=ctypes.c_void_p(0x1008)), dict(x=ODD),
+                dict(wq=ctypes.c_void_p(0x1004)), dict(y=ODD), dict(work=None), dict(nb=need - 1),
+                dict(work=ctypes.c_void_p(0x1008))):
+        assert call(**bad) == INVALID, bad
+        assert err(lib)
+    assert call(K=1 << 23) == UNSUPPORTED
+    assert call(M=0, x=None, wq=None, ws=None, y=None, work=None, nb=0) == 0
+    # codes that need no copy of their scales need no workspace for few rows
+    assert lib.qlin_mxfp4_matmul_workspace_bytes(4, 128, 64, U8) == 0
+    assert lib.qlin_mxfp4_matmul_workspace_bytes(4, 100, 64, BF16) == 0
+
+
+def test_gather_rejects(lib):
+    size = lib.qlin_gather_mxfp4_matmul_workspace_bytes
+    need = size(4, 8, 128, 16, 64, BF16)
+    assert need > 0
+    call = caller(lib.qlin_gather_mxfp4_matmul, dict(x=P, xdt=BF16, xs=None, act=None, B=4, K=128, wq=P, ws=P, E=16,
+                                                     N=64, e=P, R=8, work=P, nb=need, y=P, ydt=F32, st=None))
+    for bad in (dict(R=9), dict(B=0), dict(B=-4), dict(R=-8), dict(E=0), dict(e=None), dict(K=33), dict(nb=need - 1),
+                dict(work=None), dict(e=ODD), dict(act=b"relu"), dict(ydt=U8)):
+        assert call(**bad) == INVALID, bad
+        assert err(lib)
+    assert call(E=8001) == UNSUPPORTED
+    assert call(B=0, R=0, x=None, e=None, work=None, nb=0) == 0
+
+
+def test_combine_rejects(lib):
+    call = caller(lib.qlin_moe_combine, dict(h=P, dt=F16, T=4, k=8, D=64, w=P, e=None, y=P, st=None))
+    for bad in (dict(dt=U8), dict(T=-1), dict(k=0), dict(D=0), dict(h=None), dict(w=None), dict(y=None), dict(h=ODD),
+                dict(w=ODD), dict(e=ODD), dict(y=ODD)):
+        assert call(**bad) == INVALID, bad
+    assert call(T=1 << 20, k=1 << 20) == UNSUPPORTED
+    assert call(T=0, h=None, w=None, y=None) == 0
+    call = caller(lib.qlin_moe_combine_grad, dict(gy=P, h=P, dt=BF16, T=4, k=8, D=64, w=P, e=None, gh=P, gw=P, st=None))
+    for bad in (dict(dt=U8), dict(T=-1), dict(k=0), dict(D=0), dict(gy=None), dict(h=None), dict(w=None), dict(gh=None),
+                dict(gw=None), dict(gy=ODD), dict(gw=ODD), dict(gh=ODD)):
+        assert call(**bad) == INVALID, bad
+    assert call(T=0, gy=None, h=None, w=None, gh=None, gw=None) == 0
