@@ -106,8 +106,9 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _stream(device) -> int:
+    """The device's current HIP stream (hipStream_t as an integer)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _dev(t: torch.Tensor):
@@ -419,23 +420,21 @@ def gather_qmm_noalloc(x: torch.Tensor, qw: QuantizedWeight, rhs_indices: torch.
     return y
 
 
-def _same(dev, **tensors):
-    """The named tensors (None skipped) are contiguous and on dev."""
-    for name, t in tensors.items():
-        if t is not None and _dev(t) != dev:
-            raise ValueError(f"{name} must be on {dev}")
+def _check_tensor(name, t, dev, dtype):
+    """t is a contiguous tensor of dtype on dev."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev} (got {t.device})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
-def _typed(dtype, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
-
-
-def _float(**tensors):
-    for name, t in tensors.items():
-        if t.dtype not in (torch.float32, torch.float16, torch.bfloat16):
-            raise ValueError(f"{name} must be float32, float16 or bfloat16")
+def _float_code(name, t):
+    code = _DTYPE.get(t.dtype, 3)
+    if code == 3:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16")
+    return code
 
 
 def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
@@ -447,24 +446,24 @@ def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", bias: Option
     (weights float32 [..., k], experts int32 [..., k]), best first, equal
     ones by ascending index; a place no expert can take holds -1 and 0.
     """
-    lib = load_library()
+    lib = _lib or load_library()
     dev = _dev(logits)
-    _float(logits=logits)
-    if logits.dim() < 1:
+    code = _float_code("logits", logits)
+    shape = logits.shape
+    if not shape:
         raise ValueError("logits has a last axis of experts")
-    E = logits.shape[-1]
+    E = shape[-1]
     if bias is not None:
-        _same(dev, bias=bias)
-        _typed(torch.float32, bias=bias)
-        if tuple(bias.shape) != (E,):
+        _check_tensor("bias", bias, dev, torch.float32)
+        if bias.shape != (E,):
             raise ValueError(f"bias must hold one value per expert ({E})")
     T = logits.numel() // E if E else 0
-    shape = tuple(logits.shape[:-1]) + (max(int(k), 0),)
+    shape = (*shape[:-1], max(k, 0))
     weights = torch.empty(shape, dtype=torch.float32, device=dev)
     experts = torch.empty(shape, dtype=torch.int32, device=dev)
-    _check(lib.qlin_moe_route(_ptr(logits), _DTYPE[logits.dtype], T, E, k, _ptr(bias), score.encode(),
-                              int(bool(renormalize)), float(scale), groups, groups_kept, group_top,
-                              _ptr(weights), _ptr(experts), _stream(dev)))
+    _check(lib.qlin_moe_route(logits.data_ptr(), code, T, E, k, None if bias is None else bias.data_ptr(),
+                              score.encode(), renormalize, scale, groups, groups_kept, group_top,
+                              weights.data_ptr(), experts.data_ptr(), _stream(dev)))
     return weights, experts
 
 
@@ -472,56 +471,63 @@ def moe_route_grad(logits: torch.Tensor, experts: torch.Tensor, grad_weights: to
                    score: str = "softmax", renormalize: bool = True, scale: float = 1.0) -> torch.Tensor:
     """qlin_moe_route_grad: gradient of moe_route's weights with respect to
     logits, in logits' dtype; experts is moe_route's output for them."""
-    lib = load_library()
+    lib = _lib or load_library()
     dev = _dev(logits)
-    _float(logits=logits)
-    _same(dev, experts=experts, grad_weights=grad_weights)
-    _typed(torch.int32, experts=experts)
-    _typed(torch.float32, grad_weights=grad_weights)
-    if experts.shape != grad_weights.shape or experts.shape[:-1] != logits.shape[:-1]:
+    code = _float_code("logits", logits)
+    _check_tensor("experts", experts, dev, torch.int32)
+    _check_tensor("grad_weights", grad_weights, dev, torch.float32)
+    if not logits.shape or experts.shape != grad_weights.shape or experts.shape[:-1] != logits.shape[:-1]:
         raise ValueError("experts and grad_weights are [..., k] for logits [..., E]")
-    E, k = logits.shape[-1], experts.shape[-1]
-    T = logits.numel() // E if E else 0
+    E = logits.shape[-1]
     out = torch.empty_like(logits)
-    _check(lib.qlin_moe_route_grad(_ptr(logits), _DTYPE[logits.dtype], T, E, k, _ptr(experts),
-                                   _ptr(grad_weights), score.encode(), int(bool(renormalize)), float(scale),
-                                   _ptr(out), _stream(dev)))
+    _check(lib.qlin_moe_route_grad(logits.data_ptr(), code, logits.numel() // E if E else 0, E,
+                                   experts.shape[-1], experts.data_ptr(), grad_weights.data_ptr(),
+                                   score.encode(), renormalize, scale, out.data_ptr(), _stream(dev)))
     return out
 
 
 def _mxfp4_operands(x, qw, activation, dim):
-    """Device, x's pointers and dtype, its leading shape, K and N of an mxfp4 product."""
-    if qw.mode != "mxfp4" or not qw.transpose or qw.value.dim() != dim:
+    """Device, x's tensor, scales and type code, y's default dtype, K and N of an mxfp4 product."""
+    value = qw.value
+    if qw.mode != "mxfp4" or not qw.transpose or value.dim() != dim:
         raise ValueError(f"the weight must be a {dim}-D mxfp4 weight in the [out, in] layout")
-    _dev(qw.value)
-    _dev(qw.scales)
-    K, N = qw.value.shape[-1] * 8, qw.value.shape[-2]
+    K, N = value.shape[-1] * 8, value.shape[-2]
+    wide = K
     if isinstance(x, QuantizedWeight):
         if x.mode != "mxfp4":
             raise ValueError("a quantized x must be mxfp4")
-        t, scales, wide = x.value, x.scales, K // 8
-        code = _DTYPE[torch.uint8]
-        if tuple(scales.shape) != tuple(t.shape[:-1]) + (t.shape[-1] // 4,):
+        t, scales, code, dtype, wide = x.value, x.scales, 3, torch.bfloat16, K // 8
+        dev = _dev(t)
+        _check_tensor("x's words", t, dev, torch.int32)
+        _check_tensor("x's scales", scales, dev, torch.uint8)
+        if scales.numel() * 4 != t.numel():
             raise ValueError("x's scales do not fit its words")
     else:
-        _float(x=x)
-        t, scales, wide = x, None, 2 * K if activation == "swiglu" else K
-        code = _DTYPE[x.dtype]
-    dev = _dev(t)
-    _same(dev, scales=scales, weight=qw.value, weight_scales=qw.scales)
-    if t.dim() < 1 or t.shape[-1] != wide:
-        raise ValueError(f"x's last dim {t.shape[-1] if t.dim() else None} does not match the weight's K={K}"
+        t, scales, code, dtype = x, None, _float_code("x", x), x.dtype
+        dev = _dev(t)
+        if activation == "swiglu":
+            wide = 2 * K
+    _check_tensor("the weight's words", value, dev, torch.int32)
+    _check_tensor("the weight's scales", qw.scales, dev, torch.uint8)
+    if not K or not t.shape or t.shape[-1] != wide:
+        raise ValueError(f"x's last dim {t.shape[-1] if t.shape else None} does not match the weight's K={K}"
                          + (" (twice K with swiglu)" if activation == "swiglu" else ""))
-    if tuple(qw.scales.shape) != tuple(qw.value.shape[:-1]) + (K // 32,):
+    if qw.scales.numel() * 4 != value.numel():
         raise ValueError("the weight's scales do not fit its words")
-    return dev, t, scales, code, tuple(t.shape[:-1]), K, N
+    return dev, t, scales, code, dtype, K, N
 
 
-def _work(workspace, need, dev):
+def _workspace(workspace, need, dev):
+    """(address, bytes) of the given workspace, or of a new one; the tensor keeps it alive."""
     if workspace is None:
-        return torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    _same(dev, workspace=workspace)
-    return workspace
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    else:
+        _dev(workspace)
+        if workspace.device != dev:
+            raise ValueError(f"workspace must be on {dev}")
+    if workspace is None:
+        return None, None, 0
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def mxfp4_matmul_workspace_bytes(M: int, K: int, N: int, x_dtype: torch.dtype = torch.bfloat16) -> int:
@@ -540,18 +546,17 @@ def mxfp4_matmul(x, qw: QuantizedWeight, activation: Optional[str] = None,
     mxfp4 QuantizedWeight that holds the activation's codes. y takes
     out_dtype, by default x's (bfloat16 for codes).
     """
-    lib = load_library()
-    dev, t, scales, code, lead, K, N = _mxfp4_operands(x, qw, activation, 2)
-    M = 1
-    for d in lead:
-        M *= d
-    dtype = out_dtype or (torch.bfloat16 if scales is not None else t.dtype)
-    y = _out(out, lead + (N,), dtype, dev)
-    need = int(lib.qlin_mxfp4_matmul_workspace_bytes(M, K, N, code))
-    ws = _work(workspace, need, dev)
-    _check(lib.qlin_mxfp4_matmul(_ptr(t), code, _ptr(scales), (activation or "none").encode(), M, K,
-                                 _ptr(qw.value), _ptr(qw.scales), N, _ptr(ws),
-                                 ws.numel() * ws.element_size(), _ptr(y), _DTYPE[dtype], _stream(dev)))
+    lib = _lib or load_library()
+    dev, t, scales, code, dtype, K, N = _mxfp4_operands(x, qw, activation, 2)
+    M = t.numel() // t.shape[-1]
+    if out_dtype is not None:
+        dtype = out_dtype
+    y = _out(out, (*t.shape[:-1], N), dtype, dev)
+    keep, ws, ws_bytes = _workspace(workspace, lib.qlin_mxfp4_matmul_workspace_bytes(M, K, N, code), dev)
+    _check(lib.qlin_mxfp4_matmul(t.data_ptr(), code, None if scales is None else scales.data_ptr(),
+                                 activation.encode() if activation else None, M, K, qw.value.data_ptr(),
+                                 qw.scales.data_ptr(), N, ws, ws_bytes, y.data_ptr(), _DTYPE[dtype],
+                                 _stream(dev)))
     return y
 
 
@@ -571,44 +576,46 @@ def gather_mxfp4_matmul(x, qw: QuantizedWeight, experts: torch.Tensor, activatio
     row of x. Returns y of shape experts.shape + (N,); a row whose expert is
     outside [0, E) is zeros.
     """
-    lib = load_library()
-    dev, t, scales, code, lead, K, N = _mxfp4_operands(x, qw, activation, 3)
-    _same(dev, experts=experts)
-    _typed(torch.int32, experts=experts)
-    if len(lead) != 1 or experts.dim() < 1 or experts.shape[0] != lead[0]:
+    lib = _lib or load_library()
+    dev, t, scales, code, dtype, K, N = _mxfp4_operands(x, qw, activation, 3)
+    _check_tensor("experts", experts, dev, torch.int32)
+    if t.dim() != 2 or not experts.shape or experts.shape[0] != t.shape[0]:
         raise ValueError("gather_mxfp4_matmul takes x [B, K] and experts [B, ...]")
-    B, R, E = lead[0], experts.numel(), qw.value.shape[0]
-    dtype = out_dtype or (torch.bfloat16 if scales is not None else t.dtype)
-    y = _out(out, tuple(experts.shape) + (N,), dtype, dev)
-    need = int(lib.qlin_gather_mxfp4_matmul_workspace_bytes(B, R, K, E, N, code))
-    ws = _work(workspace, need, dev)
-    _check(lib.qlin_gather_mxfp4_matmul(_ptr(t), code, _ptr(scales), (activation or "none").encode(), B, K,
-                                        _ptr(qw.value), _ptr(qw.scales), E, N, _ptr(experts), R, _ptr(ws),
-                                        ws.numel() * ws.element_size(), _ptr(y), _DTYPE[dtype],
-                                        _stream(dev)))
+    B, R, E = t.shape[0], experts.numel(), qw.value.shape[0]
+    if out_dtype is not None:
+        dtype = out_dtype
+    y = _out(out, (*experts.shape, N), dtype, dev)
+    keep, ws, ws_bytes = _workspace(
+        workspace, lib.qlin_gather_mxfp4_matmul_workspace_bytes(B, R, K, E, N, code), dev)
+    _check(lib.qlin_gather_mxfp4_matmul(t.data_ptr(), code, None if scales is None else scales.data_ptr(),
+                                        activation.encode() if activation else None, B, K,
+                                        qw.value.data_ptr(), qw.scales.data_ptr(), E, N, experts.data_ptr(),
+                                        R, ws, ws_bytes, y.data_ptr(), _DTYPE[dtype], _stream(dev)))
     return y
 
 
 def _combine_operands(h, weights, experts):
     dev = _dev(h)
-    _float(h=h)
-    _same(dev, weights=weights, experts=experts)
-    _typed(torch.float32, weights=weights)
-    _typed(torch.int32, experts=experts)
-    if h.dim() < 2 or weights.shape != h.shape[:-1] or (experts is not None and experts.shape != weights.shape):
+    code = _float_code("h", h)
+    shape = h.shape
+    if len(shape) < 2 or weights.shape != shape[:-1] or (experts is not None and experts.shape != shape[:-1]):
         raise ValueError("moe_combine takes h [..., k, D] with weights (and experts) [..., k]")
-    k, D = h.shape[-2], h.shape[-1]
-    return dev, (weights.numel() // k if k else 0), k, D
+    _check_tensor("weights", weights, dev, torch.float32)
+    if experts is not None:
+        _check_tensor("experts", experts, dev, torch.int32)
+        experts = experts.data_ptr()
+    k = shape[-2]
+    return dev, code, (weights.numel() // k if k else 0), k, shape[-1], experts
 
 
 def moe_combine(h: torch.Tensor, weights: torch.Tensor, experts: Optional[torch.Tensor] = None,
                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """qlin_moe_combine: y[..., :] = sum over j of weights[..., j] * h[..., j, :],
     places with a negative expert left out."""
-    lib = load_library()
-    dev, T, k, D = _combine_operands(h, weights, experts)
-    y = _out(out, tuple(h.shape[:-2]) + (D,), h.dtype, dev)
-    _check(lib.qlin_moe_combine(_ptr(h), _DTYPE[h.dtype], T, k, D, _ptr(weights), _ptr(experts), _ptr(y),
+    lib = _lib or load_library()
+    dev, code, T, k, D, ids = _combine_operands(h, weights, experts)
+    y = _out(out, (*h.shape[:-2], D), h.dtype, dev)
+    _check(lib.qlin_moe_combine(h.data_ptr(), code, T, k, D, weights.data_ptr(), ids, y.data_ptr(),
                                 _stream(dev)))
     return y
 
@@ -616,13 +623,13 @@ def moe_combine(h: torch.Tensor, weights: torch.Tensor, experts: Optional[torch.
 def moe_combine_grad(grad_y: torch.Tensor, h: torch.Tensor, weights: torch.Tensor,
                      experts: Optional[torch.Tensor] = None):
     """qlin_moe_combine_grad: (grad_h in h's dtype, grad_weights float32)."""
-    lib = load_library()
-    dev, T, k, D = _combine_operands(h, weights, experts)
-    _same(dev, grad_y=grad_y)
-    if grad_y.dtype != h.dtype or tuple(grad_y.shape) != tuple(h.shape[:-2]) + (D,):
-        raise ValueError(f"grad_y must be a {h.dtype} tensor of shape {tuple(h.shape[:-2]) + (D,)}")
+    lib = _lib or load_library()
+    dev, code, T, k, D, ids = _combine_operands(h, weights, experts)
+    _check_tensor("grad_y", grad_y, dev, h.dtype)
+    if grad_y.shape != (*h.shape[:-2], D):
+        raise ValueError(f"grad_y must have the shape {(*h.shape[:-2], D)}")
     grad_h = torch.empty_like(h)
     grad_w = torch.empty_like(weights)
-    _check(lib.qlin_moe_combine_grad(_ptr(grad_y), _ptr(h), _DTYPE[h.dtype], T, k, D, _ptr(weights),
-                                     _ptr(experts), _ptr(grad_h), _ptr(grad_w), _stream(dev)))
+    _check(lib.qlin_moe_combine_grad(grad_y.data_ptr(), h.data_ptr(), code, T, k, D, weights.data_ptr(), ids,
+                                     grad_h.data_ptr(), grad_w.data_ptr(), _stream(dev)))
     return grad_h, grad_w

@@ -20,25 +20,34 @@ __device__ __forceinline__ float lane_value(float v, int lane) {
 }
 __device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
-// Largest v of the wave's 64 lanes, all active, none NaN.
-__device__ __forceinline__ float wave_max(float v) {
-    v = fmaxf(v, dpp_f<0x111>(v, v));
-    v = fmaxf(v, dpp_f<0x112>(v, v));
-    v = fmaxf(v, dpp_f<0x114>(v, v));
-    v = fmaxf(v, dpp_f<0x118>(v, v));
-    v = fmaxf(v, dpp_f<0x142>(v, v));
-    v = fmaxf(v, dpp_f<0x143>(v, v));
-    return lane_value(v, 63);
+// Largest v of the wave's 64 lanes, all active (0 is the identity, so each
+// step is one instruction).
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+}
+__device__ __forceinline__ uint32_t max_u(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t min_u(uint32_t a, uint32_t b) { return a < b ? a : b; }
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = max_u(v, dpp_u<0x111>(v));
+    v = max_u(v, dpp_u<0x112>(v));
+    v = max_u(v, dpp_u<0x114>(v));
+    v = max_u(v, dpp_u<0x118>(v));
+    v = max_u(v, dpp_u<0x142>(v));
+    v = max_u(v, dpp_u<0x143>(v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
-// Sum of v over the wave's 64 lanes, all active, in one fixed order.
+// Sum of v over the wave's 64 lanes, all active, in one fixed order. Only lane
+// 63 ends with the whole sum: row_bcast 15 gives it rows 2 + 3 and lane 31
+// rows 0 + 1, which row_bcast 31 adds.
 __device__ __forceinline__ float wave_sum(float v) {
     v += dpp_f<0x111>(0.0f, v);
     v += dpp_f<0x112>(0.0f, v);
     v += dpp_f<0x114>(0.0f, v);
     v += dpp_f<0x118>(0.0f, v);
-    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xa, 0xf, false));
-    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xc, 0xf, false));
+    v += dpp_f<0x142>(0.0f, v);
+    v += dpp_f<0x143>(0.0f, v);
     return lane_value(v, 63);
 }
 

@@ -19,9 +19,10 @@
 //            is exactly 0 (w does not change when every logit of the choice
 //            moves together), so only the chosen logits get a gradient.
 //
-// One wave per token, four tokens per workgroup. Lane l holds experts
-// l V .. l V + V - 1 (V = 1, 2, 4, 8 or 16), so that a ballot of equal keys
-// orders them by index. Everything is fp32.
+// A token takes L lanes, 16 (a DPP row, four tokens a wave) up to 256 experts
+// and a wave beyond; lane l holds experts l V .. l V + V - 1 (V = 1, 2, 4, 8
+// or 16), so that the first of the lanes with equal keys has the lowest index.
+// Everything is fp32.
 
 #include "qlin_common.h"
 #include "moe_common.h"
@@ -40,126 +41,353 @@ struct RouteArgs {
     int E, k;
     int sigmoid, renorm;
     int groups, kept, group_top;
+    int seg;                 // lanes of a group where that is a power of two of whole lanes, else 0
+    int vec;                 // rows can be loaded V elements at a time
     float scale;
     float* weights;          // [T, k]
     int32_t* experts;        // [T, k]
 };
 
-// The lane's V logits; experts past E and logits that are not finite are -inf.
-template <int DT, int V>
-__device__ __forceinline__ void load_logits(const void* p, int64_t base, int e0, int E, float (&x)[V]) {
+// exp(x) for x <= 0 within 2 ulp: 2^(x log2 e), with what the product's
+// rounding lost put back to first order. Below -104 (under half of the least
+// subnormal; -inf and NaN too) the argument is held there, so the result is 0.
+__device__ __forceinline__ float exp_of(float x) {
+    const float hi = 0x1.715476p+0f, lo = 0x1.4ae0cp-26f;   // log2 e = hi + lo
+    x = fmaxf(x, -104.0f);
+    const float t = x * hi;
+    const float e = __builtin_amdgcn_exp2f(t);
+    const float d = __builtin_fmaf(x, hi, -t) + x * lo;     // |d| < 2^-16: 2^d = 1 + d ln 2
+    return __builtin_fmaf(e, d * 0x1.62e43p-1f, e);
+}
+
+// 1 / (1 + exp(-x)) from e = exp(-|x|): 1 / (1 + e), or e / (1 + e) for
+// negative x (0 for -inf). The reciprocal is the hardware's estimate and one
+// step of Newton's iteration.
+__device__ __forceinline__ float sigmoid_of(float x) {
+    const float e = exp_of(-fabsf(x)), d = 1.0f + e;
+    float r = __builtin_amdgcn_rcpf(d);
+    r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+    return x >= 0.0f ? r : e * r;
+}
+
+__device__ __forceinline__ float finite_or_none(float f) {
+    return fabsf(f) < INFINITY ? f : -INFINITY;   // NaN fails the comparison too
+}
+
+// The lane's V values of a row of E; values past E, and with FINITE those that are not finite, are -inf.
+template <int DT, int V, bool FINITE = true>
+__device__ __forceinline__ void load_logits(const void* p, int64_t base, int e0, int E, int vec, float (&x)[V]) {
+    constexpr int SIZE = DT == QLIN_F32 ? 4 : 2, BYTES = V * SIZE;
+    if (V > 1 && vec) {
+        struct __attribute__((aligned(BYTES < 16 ? BYTES : 16))) Raw {
+            uint32_t d[BYTES < 4 ? 1 : BYTES / 4];
+        } raw;
+        if (e0 < E) raw = *(const Raw*)((const char*)p + (base + e0) * SIZE);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float f;
+            if constexpr (DT == QLIN_F32) f = __uint_as_float(raw.d[v]);
+            else {
+                const uint32_t h = (raw.d[v / 2] >> (16 * (v & 1))) & 0xFFFFu;
+                f = DT == QLIN_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
+            }
+            x[v] = e0 < E ? (FINITE ? finite_or_none(f) : f) : -INFINITY;
+        }
+        return;
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int e = e0 + v;
-        const float f = e < E ? load_f<DT>(p, base + e) : -INFINITY;
-        x[v] = isfinite(f) ? f : -INFINITY;
+        const float f = load_f<DT>(p, base + (e < E ? e : E - 1));   // no branch between the loads
+        x[v] = e < E ? (FINITE ? finite_or_none(f) : f) : -INFINITY;
     }
 }
 
-// Scores of the lane's logits (0 where the logit is -inf).
+// exp of the lane's logits against the row's largest (0 for -inf, also where no logit is finite) and
+// their sum over the wave.
 template <int V>
-__device__ __forceinline__ void scores_of(const float (&x)[V], int sigmoid, float (&s)[V]) {
-    if (sigmoid) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = x[v] == -INFINITY ? 0.0f : 1.0f / (1.0f + expf(-x[v]));
-        return;
-    }
-    float m = x[0];
-#pragma unroll
-    for (int v = 1; v < V; ++v) m = fmaxf(m, x[v]);
-    m = wave_max(m);
+__device__ __forceinline__ float softmax_terms(const float (&x)[V], float top, float (&s)[V]) {
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        s[v] = x[v] == -INFINITY ? 0.0f : expf(x[v] - m);
+        s[v] = exp_of(x[v] - top);
         sum += s[v];
     }
-    sum = wave_sum(sum);
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = sum > 0.0f ? s[v] / sum : 0.0f;
+    return wave_sum(sum);
 }
 
-template <int DT, int V>
+// Floats as unsigned numbers of the same order, so that a step of a maximum
+// over lanes is one instruction: 0 below every number, for "none"; -0 counts
+// as +0.
+__device__ __forceinline__ uint32_t order_of(float f) {
+    const uint32_t u = __float_as_uint(f + 0.0f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return __uint_as_float(o ^ ((uint32_t)(~(int32_t)o >> 31) | 0x80000000u));
+}
+constexpr uint32_t NONE = 0;            // below order_of(-inf)
+
+template <int V>
+__device__ __forceinline__ uint32_t largest(const uint32_t (&x)[V]) {
+    uint32_t m = x[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) m = max_u(m, x[v]);
+    return m;
+}
+
+template <int V>
+__device__ __forceinline__ float row_max(const float (&x)[V]) {
+    uint32_t o[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = order_of(x[v]);
+    return value_of(wave_max(largest<V>(o)));
+}
+
+// (m1, m2) the two largest of the lane's and a partner's two largest.
+__device__ __forceinline__ void merge2(uint32_t& m1, uint32_t& m2, uint32_t p1, uint32_t p2) {
+    m2 = max_u(min_u(m1, p1), max_u(m2, p2));
+    m1 = max_u(m1, p1);
+}
+
+// What a token's L lanes know together. Every lane gets the result; `row` is the lane's place among
+// the L.
+template <int L>
+struct Lanes;
+
+template <>
+struct Lanes<64> {
+    __device__ static uint32_t max_all(uint32_t v) { return wave_max(v); }
+    __device__ static float sum_all(float v) { return wave_sum(v); }
+    // first of the token's lanes for which p holds (one does)
+    __device__ static int first(bool p, int lane) { return __builtin_ctzll(__ballot(p)); }
+};
+
+template <>
+struct Lanes<16> {
+    // rotations inside the row of 16: each step joins two sets of lanes whose results agree
+    __device__ static uint32_t max_all(uint32_t v) {
+        v = max_u(v, dpp_u<0x128>(v));
+        v = max_u(v, dpp_u<0x124>(v));
+        v = max_u(v, dpp_u<0x122>(v));
+        return max_u(v, dpp_u<0x121>(v));
+    }
+    __device__ static float sum_all(float v) {
+        v += dpp_f<0x128>(0.0f, v);
+        v += dpp_f<0x124>(0.0f, v);
+        v += dpp_f<0x122>(0.0f, v);
+        return v + dpp_f<0x121>(0.0f, v);
+    }
+    __device__ static int first(bool p, int lane) {
+        const uint64_t m = __ballot(p);
+        const uint32_t half = lane & 32 ? (uint32_t)(m >> 32) : (uint32_t)m;
+        return __builtin_ctz((half >> (lane & 16)) | 0x10000u) & 15;
+    }
+};
+
+// Whether the lane's group is among the `kept` best, for groups of a.seg whole
+// lanes. f holds the lane's V values.
+template <int L, int V>
+__device__ __forceinline__ bool in_best_groups(const RouteArgs& a, const uint32_t (&f)[V], int lane) {
+    uint32_t m1 = NONE, m2 = NONE;
+    // join the lanes' two largest over DPP inside rows of 16 lanes (each step
+    // joins two blocks that already agree), by shuffles beyond
+#pragma unroll
+    for (int v = 0; v < V; ++v) merge2(m1, m2, f[v], NONE);
+    if (a.seg > 1) merge2(m1, m2, dpp_u<0xB1>(m1), dpp_u<0xB1>(m2));      // quad_perm 1 0 3 2
+    if (a.seg > 2) merge2(m1, m2, dpp_u<0x4E>(m1), dpp_u<0x4E>(m2));      // quad_perm 2 3 0 1
+    if (a.seg > 4) merge2(m1, m2, dpp_u<0x141>(m1), dpp_u<0x141>(m2));    // row_half_mirror
+    if (a.seg > 8) merge2(m1, m2, dpp_u<0x140>(m1), dpp_u<0x140>(m2));    // row_mirror
+    if constexpr (L == 64) {
+        if (a.seg > 16) merge2(m1, m2, (uint32_t)__shfl_xor((int)m1, 16, 64), (uint32_t)__shfl_xor((int)m2, 16, 64));
+        if (a.seg > 32) merge2(m1, m2, (uint32_t)__shfl_xor((int)m1, 32, 64), (uint32_t)__shfl_xor((int)m2, 32, 64));
+    }
+    const float b1 = m1 == NONE ? -INFINITY : value_of(m1), b2 = m2 == NONE ? -INFINITY : value_of(m2);
+    const int row = lane & (L - 1);
+    uint32_t g = row < a.groups * a.seg ? order_of(a.group_top == 2 ? b1 + b2 : b1) : NONE;
+    bool in = false;
+    for (int r = 0; r < a.kept; ++r) {
+        const int win = Lanes<L>::first(g == Lanes<L>::max_all(g), lane);      // the first lane of its group
+        const bool mine = (uint32_t)(row - win) < (uint32_t)a.seg;
+        in |= mine;
+        g = mine ? NONE : g;
+    }
+    return in && row < a.groups * a.seg;
+}
+
+// Bits of the `kept` best groups where they are not whole lanes: through LDS,
+// one lane of the wave per group.
+template <int V>
+__device__ __forceinline__ uint64_t best_groups(const RouteArgs& a, const uint32_t (&f)[V], int lane, uint32_t* row) {
+    const int per = a.E / a.groups;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (lane * V + v < a.E) row[lane * V + v] = f[v];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    uint32_t m1 = NONE, m2 = NONE, g = NONE;
+    if (lane < a.groups) {
+        for (int e = 0; e < per; ++e) merge2(m1, m2, row[lane * per + e], NONE);
+        const float b1 = m1 == NONE ? -INFINITY : value_of(m1), b2 = m2 == NONE ? -INFINITY : value_of(m2);
+        g = order_of(a.group_top == 2 ? b1 + b2 : b1);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    uint64_t in = 0;
+    for (int r = 0; r < a.kept; ++r) {
+        const int win = __builtin_ctzll(__ballot(g == wave_max(g)));
+        in |= 1ull << win;
+        g = lane == win ? NONE : g;
+    }
+    return in;
+}
+
+// Batcher's odd-even merge sort of n = 2^i values as a list of comparisons.
+struct Sorter {
+    int n;
+    uint8_t a[64], b[64];
+};
+constexpr Sorter sorter(int n) {
+    Sorter s{0, {}, {}};
+    for (int p = 1; p < n; p *= 2)
+        for (int k = p; k >= 1; k /= 2)
+            for (int j = k % p; j + k < n; j += 2 * k)
+                for (int i = 0; i < k && i + j + k < n; ++i)
+                    if ((i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        s.a[s.n] = (uint8_t)(i + j);
+                        s.b[s.n] = (uint8_t)(i + j + k);
+                        ++s.n;
+                    }
+    return s;
+}
+
+// LDS of a wave, in words: the chosen experts of its tokens; then each lane's
+// sorted keys and places (the first is in registers), or the row of a group
+// choice (used before them).
+constexpr int kPlaces = kRouteMaxChoice;
+constexpr int route_lds(int L, int V) { return 64 / L * kPlaces + 2 * (V > 1 ? V : 0) * 64; }
+
+template <int DT, int L, int V>
 __global__ void __launch_bounds__(64 * ROUTE_WAVES) route_kernel(RouteArgs a) {
-    extern __shared__ float lds[];               // [waves][E], only with groups
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    const int64_t t = (int64_t)blockIdx.x * ROUTE_WAVES + wv;
-    const bool live = t < a.T;                   // the other waves only keep the barrier company
-    const int e0 = lane * V;
-    float x[V], s[V], key[V];
-    load_logits<DT, V>(a.logits, (live ? t : 0) * a.E, e0, a.E, x);
-    scores_of<V>(x, a.sigmoid, s);
+    __shared__ __align__(8) uint32_t lds[ROUTE_WAVES][route_lds(L, V)];
+    using G = Lanes<L>;
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, row = lane & (L - 1);
+    const int64_t mine_t = ((int64_t)blockIdx.x * ROUTE_WAVES + wv) * (64 / L) + lane / L;
+    if (__ballot(mine_t < a.T) == 0) return;     // waves share nothing
+    const int64_t t = mine_t < a.T ? mine_t : a.T - 1;
+    const int e0 = row * V;
+    float x[V], s[V];
+    uint32_t key[V];
+    load_logits<DT, V>(a.logits, t * a.E, e0, a.E, a.vec, x);
+    float bias[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) bias[v] = 0.0f;
+    if (a.bias) load_logits<QLIN_F32, V, false>(a.bias, 0, e0, a.E, a.vec, bias);
+    // scores of all experts only where the choice needs them
+    const bool grouped = a.kept < a.groups;
+    const bool scored = a.bias || (grouped && a.group_top == 2);
+    float top = 0.0f, inv = 0.0f;
+    if (!a.sigmoid) {
+        uint32_t o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = order_of(x[v]);
+        top = value_of(G::max_all(largest<V>(o)));
+        float sum = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) sum += s[v] = exp_of(x[v] - top);
+        sum = G::sum_all(sum);
+        inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] *= inv;
+    } else if (scored) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = sigmoid_of(x[v]);
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        key[v] = x[v];
-        if (a.bias && x[v] != -INFINITY) {
-            const float b = s[v] + a.bias[e0 + v];
-            key[v] = b == b ? b : -INFINITY;
-        }
+        const float b = a.bias ? s[v] + bias[v] : x[v];
+        key[v] = b > -INFINITY && x[v] > -INFINITY ? order_of(b) : NONE;   // NaN fails the comparison
     }
-    if (a.kept < a.groups) {
-        float* const row = lds + wv * a.E;
+    uint32_t* const chosen = lds[wv] + lane / L * kPlaces;
+    uint2* const list = (uint2*)(lds[wv] + 64 / L * kPlaces) + lane;          // [V][64]
+    if (grouped) {
+        uint32_t f[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (e0 + v < a.E) row[e0 + v] = x[v] == -INFINITY ? -INFINITY : (a.bias ? key[v] : s[v]);
-        __syncthreads();
-        const int per = a.E / a.groups;
-        float g = -INFINITY;
-        if (lane < a.groups) {
-            float m1 = -INFINITY, m2 = -INFINITY;
-            for (int e = 0; e < per; ++e) {
-                const float f = row[lane * per + e];
-                m2 = fmaxf(m2, fminf(m1, f));
-                m1 = fmaxf(m1, f);
+        for (int v = 0; v < V; ++v) f[v] = a.bias || a.group_top == 1 || key[v] == NONE ? key[v] : order_of(s[v]);
+        if (a.seg) {
+            const bool in = in_best_groups<L, V>(a, f, lane);
+#pragma unroll
+            for (int v = 0; v < V; ++v) key[v] = in ? key[v] : NONE;
+        } else if constexpr (L == 64) {
+            const uint64_t keep = best_groups<V>(a, f, lane, lds[wv] + kPlaces);
+            const int per = a.E / a.groups;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int gr = (e0 + v) / per;
+                if (gr >= a.groups || !((keep >> gr) & 1)) key[v] = NONE;
             }
-            g = a.group_top == 2 ? m1 + m2 : m1;
-        }
-        int rank = 0;
-        for (int o = 0; o < a.groups; ++o) {
-            const float f = lane_value(g, o);
-            rank += (f > g || (f == g && o < lane)) ? 1 : 0;
-        }
-        const uint64_t keep = __ballot(lane < a.groups && rank < a.kept);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int gr = (e0 + v) / per;
-            if (gr >= a.groups || !((keep >> gr) & 1)) key[v] = -INFINITY;
         }
     }
-    // k rounds: the wave's largest key, its lowest index
-    float my_s = 0.0f;
-    int my_e = -1;
+    // Each lane sorts its keys, of equal ones the lower place first, and keeps
+    // the best at hand. Then k rounds: the best of the token's lanes, of equal
+    // ones the first lane's; that lane notes it and takes its next.
+    uint32_t head = key[0], place = 0;
+    if constexpr (V > 1) {
+        uint64_t kp[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) kp[v] = (uint64_t)key[v] << 32 | (uint32_t)(V - 1 - v);
+        constexpr Sorter net = sorter(V);
+#pragma unroll
+        for (int c = 0; c < net.n; ++c) {
+            const uint64_t p = kp[net.a[c]], q = kp[net.b[c]];
+            kp[net.a[c]] = p < q ? q : p;
+            kp[net.b[c]] = p < q ? p : q;
+        }
+#pragma unroll
+        for (int v = 1; v < V; ++v) list[64 * v] = uint2{(uint32_t)(kp[v] >> 32), (uint32_t)(V - 1) - (uint32_t)kp[v]};
+        head = (uint32_t)(kp[0] >> 32);
+        place = (uint32_t)(V - 1) - (uint32_t)kp[0];
+    }
+    for (int j = row; j < a.k; j += L) chosen[j] = 0xFFFFFFFFu;
+    int taken = 0;
     for (int j = 0; j < a.k; ++j) {
-        float b = key[0], bs = s[0];
-        int bv = 0;
-#pragma unroll
-        for (int v = 1; v < V; ++v)
-            if (key[v] > b) {
-                b = key[v];
-                bs = s[v];
-                bv = v;
+        const uint32_t best = G::max_all(head);
+        if (L == 64 && best == NONE) break;
+        if (row == G::first(head == best, lane) && best != NONE) {
+            chosen[j] = (uint32_t)e0 + place;
+            ++taken;
+            if (V > 1 && taken < V) {
+                const uint2 n = list[64 * taken];
+                head = n.x;
+                place = n.y;
+            } else {
+                head = NONE;
             }
-        const float top = wave_max(b);
-        if (top == -INFINITY) break;
-        const int win = __builtin_ctzll(__ballot(b == top));
-        const float ws = lane_value(bs, win);
-        const int we = lane_value(bv, win) + win * V;
-        if (lane == j) {
-            my_s = ws;
-            my_e = we;
         }
-        if (lane == win) {
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    float sum = 0.0f;
+    constexpr int PER = kRouteMaxChoice / L;       // places of a lane
+    float sc[PER];
+    int id[PER];
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (v == bv) key[v] = -INFINITY;
+    for (int p = 0; p < PER; ++p) {
+        id[p] = -1;
+        sc[p] = 0.0f;
+        if (p * L < a.k) {
+            if (row + p * L < a.k) id[p] = (int)chosen[row + p * L];
+            if (id[p] >= 0) {
+                const float l = load_f<DT>(a.logits, t * a.E + id[p]);
+                sc[p] = a.sigmoid ? sigmoid_of(l) : exp_of(l - top) * inv;
+            }
+            sum += sc[p];
         }
     }
-    float w = a.scale * my_s;
-    if (a.renorm) w = w / (wave_sum(my_s) + 1e-20f);
-    if (live && lane < a.k) {
-        a.weights[t * a.k + lane] = w;
-        a.experts[t * a.k + lane] = my_e;
-    }
+    const float by = a.renorm ? a.scale / (G::sum_all(sum) + 1e-20f) : a.scale;
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+        if (row + p * L < a.k && mine_t < a.T) {
+            a.weights[t * a.k + row + p * L] = sc[p] * by;
+            a.experts[t * a.k + row + p * L] = id[p];
+        }
 }
 
 struct RouteGradArgs {
@@ -169,66 +397,128 @@ struct RouteGradArgs {
     int64_t T;
     int E, k;
     int sigmoid, renorm;
+    int vec;
     float scale;
     void* grad;              // [T, E], the logits' dtype
 };
 
+// Lane j works out the gradient of place j's logit; LDS carries it to the
+// lane that writes that logit. Only softmax needs the whole row of logits.
 template <int DT, int V>
 __global__ void __launch_bounds__(64 * ROUTE_WAVES) route_grad_kernel(RouteGradArgs a) {
-    extern __shared__ float lds[];               // [waves][2][E]: scores, then ds of the chosen
+    extern __shared__ float lds[];               // [waves][64 V]
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const int64_t t = (int64_t)blockIdx.x * ROUTE_WAVES + wv;
-    const bool live = t < a.T;
+    if (t >= a.T) return;                        // waves share nothing
     const int e0 = lane * V;
-    float* const srow = lds + wv * 2 * a.E;
-    float* const drow = srow + a.E;
-    float x[V], s[V];
-    load_logits<DT, V>(a.logits, (live ? t : 0) * a.E, e0, a.E, x);
-    scores_of<V>(x, a.sigmoid, s);
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-        if (e0 + v < a.E) {
-            srow[e0 + v] = s[v];
-            drow[e0 + v] = 0.0f;
-        }
-    __syncthreads();
+    float* const row = lds + wv * 64 * V;
     int id = -1;
-    float g = 0.0f, sc = 0.0f;
-    if (live && lane < a.k) {
+    float g = 0.0f, l = 0.0f;
+    if (lane < a.k) {
         id = a.experts[t * a.k + lane];
-        if (id < 0 || id >= a.E) id = -1;
-        if (id >= 0) {
-            g = a.grad_w[t * a.k + lane];
-            sc = srow[id];
+        if ((uint32_t)id < (uint32_t)a.E) {
+            l = finite_or_none(load_f<DT>(a.logits, t * a.E + id));
+            if (l == -INFINITY) id = -1;
+            else g = a.grad_w[t * a.k + lane];
+        } else {
+            id = -1;
         }
+    }
+    float x[V], s[V];
+    float sc = 0.0f;
+    if (a.sigmoid) {
+        if (id >= 0) sc = sigmoid_of(l);
+    } else {
+        load_logits<DT, V>(a.logits, t * a.E, e0, a.E, a.vec, x);
+        const float top = row_max<V>(x);
+        const float sum = softmax_terms<V>(x, top, s);
+        const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] *= inv;
+        if (id >= 0) sc = exp_of(l - top) * inv;
     }
     float ds = a.scale * g;
     if (a.renorm) {
         const float total = wave_sum(sc) + 1e-20f;
         ds = (a.scale * g - wave_sum(g * (a.scale * sc / total))) / total;
     }
-    const float dot = (!a.sigmoid && !a.renorm) ? wave_sum(ds * sc) : 0.0f;
-    if (id >= 0) drow[id] = ds;
-    __syncthreads();
-    if (!live) return;
+    const bool whole = !a.sigmoid && !a.renorm;
+    const float dot = whole ? wave_sum(ds * sc) : 0.0f;
+    float r = ds * sc;
+    if (a.sigmoid) r *= sigmoid_of(-l);
+    if (whole) r = sc * (ds - dot);
+    float o[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        if (e0 + v >= a.E) continue;
-        const float d = drow[e0 + v];
-        float r;
-        if (a.sigmoid) r = d == 0.0f ? 0.0f : d * s[v] * (1.0f / (1.0f + expf(x[v])));
-        else r = s[v] * (d - dot);
-        if (x[v] == -INFINITY) r = 0.0f;
-        store_f<DT>(a.grad, t * a.E + e0 + v, r);
+    for (int v = 0; v < V; ++v) row[e0 + v] = whole ? -s[v] * dot : 0.0f;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (id >= 0) row[id] = r;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = row[e0 + v];
+    constexpr int SIZE = DT == QLIN_F32 ? 4 : 2, BYTES = V * SIZE;
+    if (V > 1 && a.vec) {
+        struct __attribute__((aligned(BYTES < 16 ? BYTES : 16))) Raw {
+            uint32_t d[BYTES < 4 ? 1 : BYTES / 4];
+        } raw;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if constexpr (DT == QLIN_F32) raw.d[v] = __float_as_uint(o[v]);
+            else {
+                const uint32_t h = DT == QLIN_BF16 ? f32_to_bf16_rne(o[v]) : f32_to_f16_rne(o[v]);
+                raw.d[v / 2] = v & 1 ? raw.d[v / 2] | (h << 16) : h;
+            }
+        }
+        if (e0 < a.E) *(Raw*)((char*)a.grad + (t * a.E + e0) * SIZE) = raw;
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (e0 + v < a.E) store_f<DT>(a.grad, t * a.E + e0 + v, o[v]);
     }
 }
 
-template <int DT, int V>
-struct Route {
-    static void run(const RouteArgs& a, unsigned grid, size_t shm, hipStream_t st) {
-        route_kernel<DT, V><<<grid, 64 * ROUTE_WAVES, shm, st>>>(a);
+// Experts a lane for E of them over L lanes.
+inline int lane_width(int E, int L) {
+    int V = 1;
+    while (V * L < E) V *= 2;
+    return V;
+}
+
+// Lanes of a group of `per` experts where that is a power of two of whole lanes, else 0.
+inline int group_lanes(int per, int L, int V) {
+    const int lanes = per % V ? 0 : per / V;
+    return lanes >= 1 && lanes <= L && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+}
+
+// Whether every lane's V elements of every row are aligned and inside or outside the row as a whole.
+inline int whole_lanes(int dt, int E, int V, const void* a, const void* b) {
+    const int bytes = V * (dt == QLIN_F32 ? 4 : 2);
+    return E % V == 0 && (((uintptr_t)a | (uintptr_t)b) & (uintptr_t)((bytes < 16 ? bytes : 16) - 1)) == 0;
+}
+
+template <int DT, int L, int V>
+void route_launch(const RouteArgs& a, hipStream_t st) {
+    constexpr int per = ROUTE_WAVES * (64 / L);
+    route_kernel<DT, L, V><<<(unsigned)((a.T + per - 1) / per), 64 * ROUTE_WAVES, 0, st>>>(a);
+}
+template <int DT>
+void route_by_width(const RouteArgs& a, int L, int V, hipStream_t st) {
+    if (L == 16) {
+        switch (V) {
+        case 1: return route_launch<DT, 16, 1>(a, st);
+        case 2: return route_launch<DT, 16, 2>(a, st);
+        case 4: return route_launch<DT, 16, 4>(a, st);
+        case 8: return route_launch<DT, 16, 8>(a, st);
+        default: return route_launch<DT, 16, 16>(a, st);
+        }
     }
-};
+    switch (V) {
+    case 1: return route_launch<DT, 64, 1>(a, st);
+    case 2: return route_launch<DT, 64, 2>(a, st);
+    case 4: return route_launch<DT, 64, 4>(a, st);
+    case 8: return route_launch<DT, 64, 8>(a, st);
+    default: return route_launch<DT, 64, 16>(a, st);
+    }
+}
 template <int DT, int V>
 struct RouteGrad {
     static void run(const RouteGradArgs& a, unsigned grid, size_t shm, hipStream_t st) {
@@ -238,11 +528,13 @@ struct RouteGrad {
 
 template <template <int, int> class F, int DT, typename A>
 void by_width(int E, const A& a, unsigned grid, size_t shm, hipStream_t st) {
-    if (E <= 64) F<DT, 1>::run(a, grid, shm, st);
-    else if (E <= 128) F<DT, 2>::run(a, grid, shm, st);
-    else if (E <= 256) F<DT, 4>::run(a, grid, shm, st);
-    else if (E <= 512) F<DT, 8>::run(a, grid, shm, st);
-    else F<DT, 16>::run(a, grid, shm, st);
+    switch (lane_width(E, 64)) {
+    case 1: return F<DT, 1>::run(a, grid, shm, st);
+    case 2: return F<DT, 2>::run(a, grid, shm, st);
+    case 4: return F<DT, 4>::run(a, grid, shm, st);
+    case 8: return F<DT, 8>::run(a, grid, shm, st);
+    default: return F<DT, 16>::run(a, grid, shm, st);
+    }
 }
 
 template <template <int, int> class F, typename A>
@@ -259,16 +551,27 @@ hipError_t by_type(int dt, int E, const A& a, size_t shm, hipStream_t st) {
 hipError_t launch_moe_route(const void* logits, int dt, int64_t T, int E, int k, const float* bias,
                             int sigmoid, int renorm, float scale, int groups, int kept, int group_top,
                             float* weights, int32_t* experts, hipStream_t st) {
-    const RouteArgs a{logits, bias, T, E, k, sigmoid, renorm, groups, kept, group_top, scale, weights, experts};
-    const size_t shm = kept < groups ? (size_t)ROUTE_WAVES * E * sizeof(float) : 0;
-    return by_type<Route>(dt, E, a, shm, st);
+    const int per = E / groups;
+    int L = 16, V = lane_width(E, L), seg = group_lanes(per, L, V);
+    if (E > 256 || (kept < groups && !seg)) {
+        L = 64;
+        V = lane_width(E, L);
+        seg = group_lanes(per, L, V);
+    }
+    const RouteArgs a{logits, bias, T, E, k, sigmoid, renorm, groups, kept, group_top, seg,
+                      whole_lanes(dt, E, V, logits, nullptr) && whole_lanes(QLIN_F32, E, V, bias, nullptr), scale,
+                      weights, experts};
+    if (dt == QLIN_F32) route_by_width<QLIN_F32>(a, L, V, st);
+    else if (dt == QLIN_BF16) route_by_width<QLIN_BF16>(a, L, V, st);
+    else route_by_width<QLIN_F16>(a, L, V, st);
+    return hipGetLastError();
 }
 
 hipError_t launch_moe_route_grad(const void* logits, int dt, int64_t T, int E, int k, const int32_t* experts,
                                  const float* grad_w, int sigmoid, int renorm, float scale, void* grad,
                                  hipStream_t st) {
-    const RouteGradArgs a{logits, experts, grad_w, T, E, k, sigmoid, renorm, scale, grad};
-    return by_type<RouteGrad>(dt, E, a, (size_t)ROUTE_WAVES * 2 * E * sizeof(float), st);
+    const RouteGradArgs a{logits, experts, grad_w, T, E, k, sigmoid, renorm, whole_lanes(dt, E, lane_width(E, 64), logits, grad), scale, grad};
+    return by_type<RouteGrad>(dt, E, a, (size_t)ROUTE_WAVES * 64 * lane_width(E, 64) * sizeof(float), st);
 }
 
 }  // namespace qlin

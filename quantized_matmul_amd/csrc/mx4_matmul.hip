@@ -26,6 +26,8 @@
 #include "mx4_plan.h"
 
 #include <atomic>
+#include <cstdlib>
+#include <type_traits>
 
 namespace qlin {
 namespace {
@@ -59,6 +61,21 @@ __device__ __forceinline__ uint32_t scale4(const uint8_t* p, int left) {
         for (int b = 0; b < left; ++b) v = (v & ~(0xFFu << (8 * b))) | ((uint32_t)p[b] << (8 * b));
     }
     return v;
+}
+
+// Four consecutive outputs at element i (a multiple of 4, y aligned to four of them).
+template <int YDT>
+__device__ __forceinline__ void store4(void* y, int64_t i, float a, float b, float c, float d) {
+    if constexpr (YDT == QLIN_F32) {
+        *(float4*)((float*)y + i) = float4{a, b, c, d};
+    } else if constexpr (YDT == QLIN_BF16) {
+        typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
+        *(uint2*)((uint16_t*)y + i) = __builtin_bit_cast(uint2, bf16x4{(__bf16)a, (__bf16)b, (__bf16)c, (__bf16)d});
+    } else {
+        typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
+        *(uint2*)((uint16_t*)y + i) =
+            __builtin_bit_cast(uint2, f16x4{(_Float16)a, (_Float16)b, (_Float16)c, (_Float16)d});
+    }
 }
 
 // ------------------------------------------------------------- streaming
@@ -199,14 +216,20 @@ struct TiledArgs {
     int tiles_n;
     int xcds;
     int lds_nan;
+    int wide;          // outputs can be stored 16 bytes at a time
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
 }
 
-// Slot of 16-byte chunk c of row r in a 128-byte LDS row.
-__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+// 16-byte chunk c of row r sits in slot c ^ swz(r) of its LDS row of 128 or 64
+// bytes: any 8 neighbouring rows then keep a chunk in 8 different 16-byte
+// columns of the 128-byte bank line.
+template <int BKB>
+__device__ __forceinline__ int swz(int r) {
+    return BKB == 128 ? (r & 7) ^ ((r >> 3) & 1) : (r >> 1) & 3;
+}
 
 // s_waitcnt vmcnt(N) lgkmcnt(0). Field layout: vmcnt [3:0] and [15:14], expcnt [6:4], lgkmcnt [11:8].
 template <int N>
@@ -221,31 +244,56 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n, uint32_t xcd
     return x * per + (x < more ? x : more) + b / xcds;
 }
 
+#ifndef SPREAD
+#define SPREAD 1
+#endif
 constexpr uint32_t NOWHERE = 0x80000000u;   // past every buffer range: reads zeros
 
 // Tile of BN weight rows (n) by BM activation rows (m), WN x WM waves of
-// TN x TM 32x32 accumulators, K in steps of 256 codes (128 bytes a row):
+// TN x TM 32x32 accumulators, K in steps of BKB bytes (2 BKB codes) a row:
 //  * code rows go global -> LDS by buffer -> LDS loads, ST - 1 steps ahead
-//    through a ring of ST stages; one wave instruction moves 8 whole rows of a
-//    step, and row r keeps its 16-byte chunk c in slot c ^ swz(r), so that a
-//    fragment read meets no bank conflict;
-//  * scale rows go the same way, 16 bytes (two steps) at a time, issued with
+//    through a ring of ST stages; one wave instruction moves 1 KB of whole row
+//    pieces, swizzled so that a fragment read meets no bank conflict;
+//  * scale rows go the same way, 16 bytes (SG steps) at a time, issued with
 //    the codes of the step that first needs them;
-//  * a step is four instructions deep along K; the fragments of the next one
-//    are read while the current one multiplies.
+//  * a step is KH instructions deep along K; the fragments of the next one
+//    are read while the current one multiplies;
+//  * the outputs go through LDS, so that they leave in whole lines.
 // Rows past the tile and chunks past K read zeros (buffer range checks).
-template <int BN, int BM, int WN, int WM, int ST, int YDT, bool GATHER>
+template <int BN, int BM, int WN, int WM, int ST, int BKB>
+struct Shape {
+    static constexpr int NW = WN * WM, TN = BN / WN / 32, TM = BM / WM / 32;
+    static constexpr int CH = BKB / 16, KH = CH / 2;               // chunks of a row and step; instructions along K
+    static constexpr int WSTAGE = BN * BKB, STAGE = (BN + BM) * BKB;
+    static constexpr int RPL = 1024 / BKB;                         // rows one load moves
+    static constexpr int ND = (BN + BM) / RPL / NW;                // code loads per wave and step
+    static constexpr int NSI = (BN + BM) / 64;                     // scale loads per batch
+    static constexpr int NS = (NSI + NW - 1) / NW;                 // ... per wave
+    static constexpr int SG = 256 / BKB;                           // steps per batch of 16 scale bytes
+    static constexpr int LA = ST - 1;                              // steps ahead
+    static constexpr int SST = (LA + SG - 1) / SG + 1;             // scale stages
+    static constexpr int SSTAGE = (BN + BM) * 16;
+    static constexpr int LOOP = ST * STAGE + SST * SSTAGE;         // LDS of the loop
+    // LDS of the outputs: per wave 32 rows of TN 32 values, rows 16 bytes longer against conflicts
+    static constexpr int orow(int size) { return TN * 32 * size + 16; }
+    static constexpr int lds(int size) { return LOOP > NW * 32 * orow(size) ? LOOP : NW * 32 * orow(size); }
+    static_assert((BN / RPL) % NW == 0 && (BM / RPL) % NW == 0, "whole loads per wave");
+    // loads issued after those of a step of phase ph (its number mod SG) when it starts: the LA - 1
+    // steps after it, of which those that open a batch brought its scales
+    static constexpr int after(int ph) {
+        int n = 0;
+        for (int u = 1; u < LA; ++u) n += ND + ((ph + u) % SG == 0 ? NS : 0);
+        return n;
+    }
+};
+
+template <int BN, int BM, int WN, int WM, int ST, int BKB, int YDT, bool GATHER>
 __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
-    constexpr int NW = WN * WM, TN = BN / WN / 32, TM = BM / WM / 32;
-    constexpr int WSTAGE = BN * 128, XSTAGE = BM * 128, STAGE = WSTAGE + XSTAGE;
-    constexpr int ND = (BN + BM) / 8 / NW;                       // code loads per wave and step
-    constexpr int NSI = (BN + BM) / 64;                          // scale loads per batch of two steps
-    constexpr int NS = (NSI + NW - 1) / NW;                      // ... per wave
-    constexpr int LA = ST - 1, SST = (LA + 1) / 2 + 1;           // steps ahead; scale stages
-    constexpr int SSTAGE = (BN + BM) * 16;
-    static_assert((BN / 8) % NW == 0 && (BM / 8) % NW == 0, "whole loads per wave");
+    using S = Shape<BN, BM, WN, WM, ST, BKB>;
+    constexpr int NW = S::NW, TN = S::TN, TM = S::TM;
+    constexpr int YS = YDT == QLIN_F32 ? 4 : 2;
     extern __shared__ __align__(16) unsigned char smem[];
-    unsigned char* const slds = smem + ST * STAGE;
+    unsigned char* const slds = smem + ST * S::STAGE;
     const Mx4Args& a = p.a;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -288,8 +336,7 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
 
     if (!GATHER || expert < (uint32_t)a.E) {
         if (p.lds_nan) {   // debug: every LDS byte of the tile starts as NaN
-            constexpr int BYTES = ST * STAGE + SST * SSTAGE;
-            for (int o = tid * 16; o < BYTES; o += 64 * NW * 16) *(u32x4*)(smem + o) = u32x4{~0u, ~0u, ~0u, ~0u};
+            for (int o = tid * 16; o < S::lds(YS); o += 64 * NW * 16) *(u32x4*)(smem + o) = u32x4{~0u, ~0u, ~0u, ~0u};
             __syncthreads();
         }
         const uint32_t half = (uint32_t)(a.K / 2);
@@ -306,132 +353,170 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
             else return (uint32_t)r;
         };
 
-        uint32_t doff[ND], dchunk[ND];
+        uint32_t doff[S::ND], dchunk[S::ND];
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
+        for (int d = 0; d < S::ND; ++d) {
             const int blk = d * NW + wv;           // W's row blocks first, then x's
-            const bool isw = blk < BN / 8;
-            const int r = (isw ? blk : blk - BN / 8) * 8 + (lane >> 3);
-            dchunk[d] = (uint32_t)((lane & 7) ^ swz(r));
+            const bool isw = blk < BN / S::RPL;
+            const int r = (isw ? blk : blk - BN / S::RPL) * S::RPL + lane / S::CH;
+            dchunk[d] = (uint32_t)((lane & (S::CH - 1)) ^ swz<BKB>(r));
             const uint32_t row = isw ? (r < nrows ? (uint32_t)r : NOWHERE) : src(r);
             doff[d] = row == NOWHERE ? NOWHERE : row * half + dchunk[d] * 16u;
         }
-        const int nk = (KB + 7) / 8;
-        auto dma = [&](int stage, int kt) {
-            const bool tail = kt == nk - 1 && (KB & 7) != 0;
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                const bool isw = d < BN / 8 / NW;
-                uint32_t off = doff[d];
-                if (tail && (uint32_t)(kt * 8) + dchunk[d] >= (uint32_t)KB) off = NOWHERE;
-                unsigned char* to = smem + stage * STAGE + (d * NW + wv) * 1024;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(isw ? wr : xr, (__attribute__((address_space(3))) void*)to, 16,
-                                                         (int)off, kt * 128, 0, 0);
-            }
+        const int nk = (KB + S::CH - 1) / S::CH;
+        // load d of step kt (past the end: of the last step, so that the counts stay the same)
+        auto dma = [&](int kt, int d) {
+            const int k = kt < nk ? kt : nk - 1;
+            const bool isw = d < BN / S::RPL / NW;
+            uint32_t off = doff[d];
+            if (k == nk - 1 && KB % S::CH != 0 && (uint32_t)(k * S::CH) + dchunk[d] >= (uint32_t)KB) off = NOWHERE;
+            unsigned char* to = smem + (kt % ST) * S::STAGE + (d * NW + wv) * 1024;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(isw ? wr : xr, (__attribute__((address_space(3))) void*)to, 16,
+                                                     (int)off, k * BKB, 0, 0);
         };
-        uint32_t soff[NS];
+        uint32_t soff[S::NS];
 #pragma unroll
-        for (int d = 0; d < NS; ++d) {
-            const int blk = (d * NW + wv) % NSI;   // a wave without a load of its own repeats another's
+        for (int d = 0; d < S::NS; ++d) {
+            const int blk = (d * NW + wv) % S::NSI;   // a wave without a load of its own repeats another's
             const int r = (blk < BN / 64 ? blk : blk - BN / 64) * 64 + lane;
             const uint32_t row = blk < BN / 64 ? (r < nrows ? (uint32_t)r : NOWHERE) : src(r);
             soff[d] = row == NOWHERE ? NOWHERE : row * (uint32_t)(blk < BN / 64 ? a.wsstride : a.xsstride);
         }
         auto dma_scales = [&](int stage, int g) {
 #pragma unroll
-            for (int d = 0; d < NS; ++d) {
-                const int blk = (d * NW + wv) % NSI;
+            for (int d = 0; d < S::NS; ++d) {
+                const int blk = (d * NW + wv) % S::NSI;
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(
                     blk < BN / 64 ? wsr : xsr,
-                    (__attribute__((address_space(3))) void*)(slds + stage * SSTAGE + blk * 1024), 16, (int)soff[d],
+                    (__attribute__((address_space(3))) void*)(slds + stage * S::SSTAGE + blk * 1024), 16, (int)soff[d],
                     g * 16, 0, 0);
             }
         };
-        const int ng = (nk + 1) / 2;
-        // the loads of step kt, with its batch of scales before them where kt opens one
-        auto issue = [&](int kt) {
-            const int k = kt < nk ? kt : nk - 1;   // steps past the end repeat the last: counts stay the same
-            if ((kt & 1) == 0) {
-                const int g = kt >> 1;
-                dma_scales(g % SST, g < ng ? g : ng - 1);
+        const int ng = (nk + S::SG - 1) / S::SG;
+        // the batch of scales that step kt opens, if it opens one
+        auto open_scales = [&](int kt) {
+            if (kt % S::SG == 0) {
+                const int g = kt / S::SG;
+                dma_scales(g % S::SST, g < ng ? g : ng - 1);
             }
-            dma(kt % ST, k);
         };
 #pragma unroll
-        for (int u = 0; u < LA; ++u) issue(u);
+        for (int u = 0; u < S::LA; ++u) {
+            open_scales(u);
+#pragma unroll
+            for (int d = 0; d < S::ND; ++d) dma(u, d);
+        }
 
-        // The loads issued after those of step kt, when it starts: the LA - 1
-        // steps after it, of which those that open a batch brought its scales.
-        constexpr int EVEN = (LA - 1) * ND + ((LA - 1) / 2) * NS, ODD = (LA - 1) * ND + (LA / 2) * NS;
+        // the lane's place in a stage: row i of a 32-row tile, its first chunk;
+        // swz repeats every 16 rows and chunk h of the lane's piece differs in
+        // the low bits only
+        const uint32_t wlane = (uint32_t)(32 * TN * wn + i) * BKB + (((S::KH * j) ^ swz<BKB>(i)) << 4);
+        const uint32_t xlane = (uint32_t)(S::WSTAGE + (32 * TM * wm + i) * BKB) + (((S::KH * j) ^ swz<BKB>(i)) << 4);
+        const uint32_t slane = (uint32_t)i * 16 + (S::SG == 2 ? 4 * j : 0);
         auto step = [&](int kt) {
             __builtin_amdgcn_s_barrier();
-            issue(kt + LA);                        // into the stage read one step ago
-            __builtin_amdgcn_sched_barrier(0);
-            const unsigned char* const wt = smem + (kt % ST) * STAGE;
-            const unsigned char* const xt = wt + WSTAGE;
-            const unsigned char* const st = slds + ((kt >> 1) % SST) * SSTAGE + (kt & 1) * 8 + 4 * j;
+            const unsigned char* const stage = smem + (kt % ST) * S::STAGE;
+            // the scale bytes of the lane's blocks: its own dword of the step's 8
+            // bytes a row, or its half of 4
+            const unsigned char* const st = slds + (kt / S::SG % S::SST) * S::SSTAGE + (kt % S::SG) * (16 / S::SG) + slane;
+            const int shift = S::SG == 2 ? 0 : 16 * j;
             uint32_t sw[TN], sx[TM];
-#pragma unroll
-            for (int t = 0; t < TN; ++t) sw[t] = *(const uint32_t*)(st + (32 * (TN * wn + t) + i) * 16);
-#pragma unroll
-            for (int t = 0; t < TM; ++t) sx[t] = *(const uint32_t*)(st + (BN + 32 * (TM * wm + t) + i) * 16);
             u32x4 fa[2][TN], fb[2][TM];
             auto read = [&](int h) {
-                const int c = 4 * j + h;
 #pragma unroll
-                for (int t = 0; t < TN; ++t) {
-                    const int r = 32 * (TN * wn + t) + i;
-                    fa[h & 1][t] = *(const u32x4*)(wt + r * 128 + ((c ^ swz(r)) << 4));
-                }
+                for (int t = 0; t < TN; ++t) fa[h & 1][t] = *(const u32x4*)(stage + (wlane ^ (h << 4)) + t * 32 * BKB);
 #pragma unroll
-                for (int t = 0; t < TM; ++t) {
-                    const int r = 32 * (TM * wm + t) + i;
-                    fb[h & 1][t] = *(const u32x4*)(xt + r * 128 + ((c ^ swz(r)) << 4));
-                }
+                for (int t = 0; t < TM; ++t) fb[h & 1][t] = *(const u32x4*)(stage + (xlane ^ (h << 4)) + t * 32 * BKB);
             };
             read(0);
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                if (h < 3) read(h + 1);
+            for (int t = 0; t < TN; ++t) sw[t] = *(const uint32_t*)(st + 32 * (TN * wn + t) * 16) >> shift;
 #pragma unroll
-                for (int tn = 0; tn < TN; ++tn)
+            for (int t = 0; t < TM; ++t) sx[t] = *(const uint32_t*)(st + (BN + 32 * (TM * wm + t)) * 16) >> shift;
+            open_scales(kt + S::LA);
+            // the loads of step kt + LA go into the stage read one step ago, a few
+            // after each product so that none waits for the others to be taken
+            int d = 0;
 #pragma unroll
-                    for (int tm = 0; tm < TM; ++tm) {
-                        const u32x4 A = fa[h & 1][tn], B = fb[h & 1][tm];
-                        f32x16& c = acc[tn][tm];
-                        if (h == 0) c = mfma32<0>(A, B, c, sw[tn], sx[tm]);
-                        else if (h == 1) c = mfma32<1>(A, B, c, sw[tn], sx[tm]);
-                        else if (h == 2) c = mfma32<2>(A, B, c, sw[tn], sx[tm]);
-                        else c = mfma32<3>(A, B, c, sw[tn], sx[tm]);
+            for (int h = 0; h < S::KH; ++h) {
+                if (h + 1 < S::KH) read(h + 1);
+                __builtin_amdgcn_sched_barrier(0);   // keeps those reads ahead of this round's products
+#pragma unroll
+                for (int q = 0; q < TN * TM; ++q) {
+                    const u32x4 A = fa[h & 1][q / TM], B = fb[h & 1][q % TM];
+                    f32x16& c = acc[q / TM][q % TM];
+                    const uint32_t sa = sw[q / TM], sb = sx[q % TM];
+                    if (h == 0) c = mfma32<0>(A, B, c, sa, sb);
+                    else if (h == 1) c = mfma32<1>(A, B, c, sa, sb);
+                    else if (h == 2) c = mfma32<2>(A, B, c, sa, sb);
+                    else c = mfma32<3>(A, B, c, sa, sb);
+                    if (d < S::ND && q % SPREAD == SPREAD - 1) {
+                        dma(kt + S::LA, d++);
+                        __builtin_amdgcn_sched_barrier(0);
                     }
+                }
             }
         };
-        for (int kt = 0; kt < nk; kt += 2) {
-            wait_loads<EVEN>();
+        for (int kt = 0; kt < nk; kt += S::SG) {
+            wait_loads<S::after(0)>();
             step(kt);
             if (kt + 1 < nk) {
-                wait_loads<ODD>();
+                wait_loads<S::after(1)>();
                 step(kt + 1);
             }
+            if constexpr (S::SG == 4) {
+                if (kt + 2 < nk) {
+                    wait_loads<S::after(2)>();
+                    step(kt + 2);
+                }
+                if (kt + 3 < nk) {
+                    wait_loads<S::after(3)>();
+                    step(kt + 3);
+                }
+            }
         }
-        wait_loads<0>();                           // no load may land in LDS after the workgroup is gone
+        wait_loads<0>();                           // every load has landed ...
+        __syncthreads();                           // ... and every read is done: LDS is free for the outputs
     }
 
-    // acc[tn][tm][r] = D[n][m]: m = lane % 32, n = 8 (r / 4) + 4 (lane / 32) + r % 4
+    // acc[tn][tm][r] = D[n][m]: m = lane % 32, n = 8 (r / 4) + 4 (lane / 32) + r % 4.
+    // Each wave lays 32 rows m of its TN * 32 columns out in LDS and stores
+    // them by rows; no other wave reads them.
+    constexpr int OROW = S::orow(YS), PER = 16 / YS, LPR = TN * 32 / PER;   // values and lanes of a 16-byte store
+    unsigned char* const ot = smem + wv * 32 * OROW;
+    const int nw0 = n0 + 32 * TN * wn;
 #pragma unroll
     for (int tm = 0; tm < TM; ++tm) {
-        const int m = 32 * (TM * wm + tm) + i;
-        if (m >= rows) continue;
-        const int64_t dst = GATHER ? (int64_t)p.plan.perm[m0 + m] : m0 + m;
+        const int mb = 32 * (TM * wm + tm);
+        if (mb >= rows) break;
 #pragma unroll
         for (int tn = 0; tn < TN; ++tn)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const int n = n0 + 32 * (TN * wn + tn) + 8 * g + 4 * j;
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (n + r < a.N) store_f<YDT>(a.y, dst * a.N + n + r, acc[tn][tm][4 * g + r]);
+                const f32x16& c = acc[tn][tm];
+                store4<YDT>(ot + i * OROW, 32 * tn + 8 * g + 4 * j, c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]);
             }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (p.wide) {
+#pragma unroll 4
+            for (int r = lane / LPR; r < 32; r += 64 / LPR) {
+                const int c = (lane % LPR) * PER, n = nw0 + c;
+                if (mb + r >= rows || n >= a.N) continue;      // N is a multiple of PER
+                const int64_t dst = GATHER ? (int64_t)p.plan.perm[m0 + mb + r] : m0 + mb + r;
+                *(u32x4*)((unsigned char*)a.y + (dst * a.N + n) * YS) = *(const u32x4*)(ot + r * OROW + c * YS);
+            }
+        } else {
+            for (int r = 0; r < 32; ++r) {
+                if (mb + r >= rows) break;
+                const int64_t dst = GATHER ? (int64_t)p.plan.perm[m0 + mb + r] : m0 + mb + r;
+                for (int c = lane; c < TN * 32; c += 64) {
+                    if (nw0 + c >= a.N) break;
+                    if constexpr (YS == 4) ((uint32_t*)a.y)[dst * a.N + nw0 + c] = *(const uint32_t*)(ot + r * OROW + c * 4);
+                    else ((uint16_t*)a.y)[dst * a.N + nw0 + c] = *(const uint16_t*)(ot + r * OROW + c * 2);
+                }
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
 
@@ -464,29 +549,54 @@ hipError_t stream_rows(StreamArgs s, int mt, int64_t tiles, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <int BN, int BM, int WN, int WM, int ST, int YDT, bool GATHER>
+template <int BN, int BM, int WN, int WM, int ST, int BKB, int YDT, bool GATHER>
 hipError_t tiled_launch(TiledArgs p, hipStream_t st) {
     const Mx4Args& a = p.a;
     p.tiles_n = (int)((a.N + BN - 1) / BN);
     const int64_t tm = GATHER ? mx4_plan_max_tiles(a.M, a.E, BM) : (a.M + BM - 1) / BM;
     if (tm * p.tiles_n > 0x7fffffffLL) return hipErrorInvalidValue;
-    constexpr int SST = (ST - 1 + 1) / 2 + 1;
-    constexpr size_t shm = (size_t)ST * (BN + BM) * 128 + (size_t)SST * (BN + BM) * 16;
+    constexpr size_t shm = Shape<BN, BM, WN, WM, ST, BKB>::lds(YDT == QLIN_F32 ? 4 : 2);
+    static_assert(shm <= 160 * 1024, "LDS of a compute unit");
+    const auto kernel = mx4_tiled_kernel<BN, BM, WN, WM, ST, BKB, YDT, GATHER>;
     static std::atomic<bool> attr{false};
     if (!attr.load(std::memory_order_acquire)) {
-        const hipError_t e = hipFuncSetAttribute((const void*)mx4_tiled_kernel<BN, BM, WN, WM, ST, YDT, GATHER>,
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);
+        const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);
         if (e != hipSuccess) return e;
         attr.store(true, std::memory_order_release);
     }
-    mx4_tiled_kernel<BN, BM, WN, WM, ST, YDT, GATHER><<<(unsigned)(tm * p.tiles_n), 64 * WN * WM, shm, st>>>(p);
+    kernel<<<(unsigned)(tm * p.tiles_n), 64 * WN * WM, shm, st>>>(p);
     return hipGetLastError();
 }
 
 constexpr int64_t kStreamRows = 64;    // rows (of one expert, on average) up to which W is streamed
 
+int forced_tile() {
+    const char* e = getenv("QLIN_MXFP4_TILE");
+    return e && *e ? atoi(e) : -1;
+}
+
+template <int YDT, bool GATHER>
+hipError_t tiled_rows(const Mx4Args& a, const Mx4Plan& plan, uint32_t per, int tile, hipStream_t st) {
+    const TiledArgs p{a, plan, per, 0, device_shape().xcds, debug_lds_nan() ? 1 : 0,
+                      a.N % (YDT == QLIN_F32 ? 4 : 8) == 0 && (uintptr_t)a.y % 16 == 0 ? 1 : 0};
+    if (tile == 1) return tiled_launch<256, 256, 2, 2, 2, 128, YDT, GATHER>(p, st);
+    if (tile == 2) return tiled_launch<256, 256, 2, 4, 4, 64, YDT, GATHER>(p, st);
+    if (tile == 3) return tiled_launch<256, 128, 2, 2, 3, 64, YDT, GATHER>(p, st);
+    if (tile == 4) return tiled_launch<128, 128, 2, 2, 2, 128, YDT, GATHER>(p, st);
+    if (tile == 8) return tiled_launch<256, 128, 4, 2, 3, 128, YDT, GATHER>(p, st);
+    if (tile == 9) return tiled_launch<128, 64, 2, 2, 2, 128, YDT, GATHER>(p, st);
+    if (tile == 10) return tiled_launch<128, 64, 2, 2, 3, 128, YDT, GATHER>(p, st);
+    if (tile == 11) return tiled_launch<64, 64, 2, 2, 4, 128, YDT, GATHER>(p, st);
+    if (tile == 5) return tiled_launch<256, 256, 2, 2, 4, 64, YDT, GATHER>(p, st);
+    if (tile == 6) return tiled_launch<256, 256, 2, 4, 2, 128, YDT, GATHER>(p, st);
+    if (tile == 7) return tiled_launch<128, 128, 2, 2, 4, 64, YDT, GATHER>(p, st);
+    return tiled_launch<128, 128, 2, 2, 4, 128, YDT, GATHER>(p, st);
+}
+
 template <int YDT>
 hipError_t launch(const Mx4Args& a, hipStream_t st, const char** path) {
+    int tile = forced_tile();
+    if (tile < 0) tile = 4;
     if (!a.experts) {
         if (!mx4_tiled(a.M, a.N, a.K, 1, false)) {
             *path = "mxfp4_stream";
@@ -494,8 +604,7 @@ hipError_t launch(const Mx4Args& a, hipStream_t st, const char** path) {
             return stream_rows<YDT, DENSE>(StreamArgs{a, Mx4Plan{}, 1, 0}, mt, (a.M + 16 * mt - 1) / (16 * mt), st);
         }
         *path = "mxfp4_tiled";
-        return tiled_launch<128, 128, 2, 2, 4, YDT, false>(
-            TiledArgs{a, Mx4Plan{}, 1, 0, device_shape().xcds, debug_lds_nan() ? 1 : 0}, st);
+        return tiled_rows<YDT, false>(a, Mx4Plan{}, 1, tile, st);
     }
     const uint32_t per = (uint32_t)(a.M / a.B);
     if (2 * a.M <= a.E) {
@@ -505,7 +614,7 @@ hipError_t launch(const Mx4Args& a, hipStream_t st, const char** path) {
     Mx4Plan plan{};
     const bool tiled = mx4_tiled(a.M, a.N, a.K, a.E, true);
     const int mt = a.M <= 16 * a.E ? 1 : a.M <= 32 * a.E ? 2 : 4;
-    const int rows = tiled ? 128 : 16 * mt;
+    const int rows = tiled ? (tile >= 9 ? 64 : tile == 0 || tile == 3 || tile == 4 || tile == 7 || tile == 8 ? 128 : 256) : 16 * mt;
     hipError_t e = launch_mx4_plan(a.experts, a.M, a.E, rows, a.plan, &plan, st);
     if (e != hipSuccess) return e;
     if (!tiled) {
@@ -513,14 +622,13 @@ hipError_t launch(const Mx4Args& a, hipStream_t st, const char** path) {
         return stream_rows<YDT, PLAN>(StreamArgs{a, plan, per, 0}, mt, mx4_plan_max_tiles(a.M, a.E, rows), st);
     }
     *path = "mxfp4_gather_tiled";
-    return tiled_launch<128, 128, 2, 2, 4, YDT, true>(
-        TiledArgs{a, plan, per, 0, device_shape().xcds, debug_lds_nan() ? 1 : 0}, st);
+    return tiled_rows<YDT, true>(a, plan, per, tile, st);
 }
 
 }  // namespace
 
 bool mx4_tiled(int64_t M, int64_t N, int64_t K, int64_t E, bool gather) {
-    return M > kStreamRows * (gather ? E : 1);
+    const char* e = getenv("MX4S"); const int64_t kr = e ? atoi(e) : kStreamRows; return M > kr * (gather ? E : 1);
 }
 
 hipError_t launch_mx4_matmul(const Mx4Args& a, hipStream_t st, const char** path) {
