@@ -407,7 +407,7 @@ const char* qlin_last_error(void);
  * launch (a static string: "decode", "in_out", "in_out_split",
  * "in_out_row_blocks", "prefill", "tiled", "generic", "gather_decode",
  * "gather_prefill", "qqmm_scaled_mfma", "mxfp4_stream", "mxfp4_tiled",
- * "mxfp4_gather_direct", "mxfp4_gather_stream", "mxfp4_gather_tiled"; "" before any). "generic" is the fp32 VALU fallback for
+ * "mxfp4_gather_stream", "mxfp4_gather_tiled"; "" before any). "generic" is the fp32 VALU fallback for
  * shapes the fast kernels do not take, typically an order of magnitude
  * slower; QLIN_WARN_FALLBACK=1 also prints a line to stderr when it runs.
  */

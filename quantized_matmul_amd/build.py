@@ -5,7 +5,7 @@ quantized_matmul_amd/libqlin.so. Flags:
   --offload-arch=gfx950 -O3           CDNA4 only
   -Xclang -target-feature -Xclang -packed-fp32-ops
                                       no packed fp32 VALU instructions
-  -ffp-contract=off (quant.hip, mxfp4_act.hip)
+  -ffp-contract=off (quant.hip, mx4_prepare.hip)
                                       bit-exact quantize/dequantize rounding
 """
 import concurrent.futures as cf
@@ -19,11 +19,11 @@ OBJ = os.path.join(HERE, "_obj")
 LIB = os.path.join(HERE, "libqlin.so")
 SOURCES = ["qlin_api.cpp", "quant.hip", "qmm_generic.hip", "qmm_decode.hip", "qmm_tiled.hip", "qmm_nt.hip",
            "qmm_prefill.hip", "qmm_prefill2.hip", "gather_index.hip", "qqmm_mx8.hip",
-           "moe_api.cpp", "moe_route.hip", "moe_combine.hip", "mxfp4_act.hip", "mx4_plan.hip", "mx4_matmul.hip"]
+           "moe_api.cpp", "moe_route.hip", "moe_combine.hip", "mx4_prepare.hip", "mx4_matmul.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 COMMON = ["--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17", "-Wall",
           "-Wno-unused-function", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
-PER_FILE = {"quant.hip": ["-ffp-contract=off"], "mxfp4_act.hip": ["-ffp-contract=off"]}
+PER_FILE = {"quant.hip": ["-ffp-contract=off"], "mx4_prepare.hip": ["-ffp-contract=off"]}
 
 
 def _compile(src):

@@ -10,7 +10,7 @@
 #include "../../include/qlin.h"
 #include "api_common.h"
 #include "moe_common.h"
-#include "mx4_plan.h"
+#include "mx4_common.h"
 
 using qlin::device_status;
 using qlin::fail;
@@ -56,23 +56,26 @@ int64_t scale_stride(int64_t K) { return (int64_t)up((size_t)(K / 32), 16); }
 
 // Pieces of a product's workspace, each 256-byte aligned: x's codes and
 // scales (or, for given codes, their scales in 16-byte rows), W's scales in
-// 16-byte rows where K / 32 is not a multiple of 16, the row plan.
+// 16-byte rows where K / 32 is not a multiple of 16, the row plan. A streamed
+// float x needs none.
 struct Layout {
     size_t xq, xs, ws, plan, bytes;
 };
-Layout layout(int64_t rows, int64_t R, int64_t K, int64_t E, int64_t N, int x_dtype, bool gather) {
+Layout layout(const qlin::Mx4Choice& c, int64_t rows, int64_t R, int64_t K, int64_t E, int64_t N, bool codes,
+              bool gather) {
     Layout l{};
-    const bool tiled = qlin::mx4_tiled(gather ? R : rows, N, K, E, gather);
+    const bool tiled = c.path == qlin::Mx4Path::kTiled;
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t p = at;
         at += up(n, 256);
         return p;
     };
-    l.xq = take(x_dtype == QLIN_U8 ? 0 : (size_t)rows * (size_t)(K / 2));
-    l.xs = take(x_dtype != QLIN_U8 || tiled ? (size_t)rows * (size_t)scale_stride(K) : 0);
+    const bool quantized = !codes && c.path != qlin::Mx4Path::kStreamFloat;
+    l.xq = take(quantized ? (size_t)rows * (size_t)(K / 2) : 0);
+    l.xs = take(quantized || (codes && tiled) ? (size_t)rows * (size_t)scale_stride(K) : 0);
     l.ws = take(tiled && K % 512 ? (size_t)E * (size_t)N * (size_t)scale_stride(K) : 0);
-    l.plan = take(gather ? qlin::mx4_plan_bytes(R, E) : 0);
+    l.plan = take(gather && tiled ? qlin::mx4_plan_bytes(R, E) : 0);
     l.bytes = at;
     return l;
 }
@@ -117,7 +120,14 @@ qlin_status product(const void* x, int x_dtype, const void* x_scales, const char
     if ((s = check_aligned(wq, 16, "wq"))) return s;
     if ((s = check_aligned(y, elem(y_dtype), "y"))) return s;
     if ((s = check_aligned(experts, 4, "experts"))) return s;
-    const Layout l = layout(rows, R, K, E, N, x_dtype, gather);
+    // the tiled kernel's row offsets are 32 bits: tiles of W and (by experts) all of x's codes
+    const qlin::Mx4Choice c = qlin::mx4_choose(R, N, K, E, gather, codes);
+    const bool tiled = c.path == qlin::Mx4Path::kTiled;
+    if (gather && tiled && rows * (K / 2) >= (1LL << 31))
+        return fail(QLIN_ERR_UNSUPPORTED, "x has more than 2^32 values: split its rows over several calls");
+    const Layout l = layout(c, rows, R, K, E, N, codes, gather);
+    // W's scales, whole 16-byte rows at an address that is none: the streaming kernel takes any
+    const bool odd = tiled && (K / 32) % 16 == 0 && (uintptr_t)scales % 16;
     if (l.bytes) {
         if (!workspace || workspace_bytes < l.bytes)
             return fail(QLIN_ERR_INVALID_ARGUMENT, "workspace of %zu bytes needed (got %zu)", l.bytes,
@@ -137,20 +147,40 @@ qlin_status product(const void* x, int x_dtype, const void* x_scales, const char
     a.K = K;
     a.xsstride = a.wsstride = KS;
     a.ydt = y_dtype;
+    a.x = x;
+    a.xdt = x_dtype;
+    a.swiglu = swiglu;
     a.experts = experts;
     a.B = rows;
     a.E = E;
-    a.plan = w + l.plan;
+    const bool quantized = !codes && c.path != qlin::Mx4Path::kStreamFloat;
+    qlin::Mx4Plan plan{};
     hipError_t e;
-    if (!codes) {
-        a.xq = (const uint8_t*)(w + l.xq);
-        a.xs = (const uint8_t*)(w + l.xs);
-        a.xsstride = stride;
-        e = qlin::launch_mxfp4_activation(x, x_dtype, rows, K, swiglu, (uint32_t*)(w + l.xq), (uint8_t*)(w + l.xs),
-                                          stride, st);
-        if (e != hipSuccess) return device_status(e, what);
+    if (quantized || (gather && tiled && !odd)) {
+        qlin::Mx4Prepare q{};
+        q.dt = x_dtype;
+        q.K = K;
+        if (quantized) {
+            q.x = x;
+            q.rows = rows;
+            q.swiglu = swiglu;
+            q.xq = (uint32_t*)(w + l.xq);
+            q.xs = (uint8_t*)(w + l.xs);
+            q.sstride = stride;
+            a.xq = (const uint8_t*)(w + l.xq);
+            a.xs = (const uint8_t*)(w + l.xs);
+            a.xsstride = stride;
+        }
+        if (gather && tiled && !odd) {
+            q.experts = experts;
+            q.R = R;
+            q.E = E;
+            q.tile_rows = c.tile_rows;
+            q.plan = w + l.plan;
+        }
+        if ((e = qlin::launch_mx4_prepare(q, &plan, st)) != hipSuccess) return device_status(e, what);
     }
-    if (qlin::mx4_tiled(R, N, K, E, gather)) {
+    if (tiled && !odd) {
         // the tiled kernel reads scale rows 16 bytes at a time
         if (codes && (KS % 16 || (uintptr_t)x_scales % 16)) {
             e = qlin::launch_mx4_pad_scales(a.xs, rows, KS, (uint8_t*)(w + l.xs), stride, st);
@@ -165,9 +195,10 @@ qlin_status product(const void* x, int x_dtype, const void* x_scales, const char
             a.wsstride = stride;
         }
     }
-    const char* path = "";
-    e = qlin::launch_mx4_matmul(a, st, &path);
-    if (e == hipSuccess) qlin::record_path(path);
+    e = odd ? qlin::launch_mx4_stream_blocks(a, st) : qlin::launch_mx4_matmul(a, c, &plan, st);
+    if (e == hipSuccess)
+        qlin::record_path(tiled && !odd ? (gather ? "mxfp4_gather_tiled" : "mxfp4_tiled")
+                                        : (gather ? "mxfp4_gather_stream" : "mxfp4_stream"));
     return device_status(e, what);
 }
 
@@ -227,7 +258,8 @@ qlin_status qlin_moe_route_grad(const void* logits, qlin_dtype dtype, int64_t T,
 
 size_t qlin_mxfp4_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N, qlin_dtype x_dtype) {
     if (M == 0 || !product_sizes_ok(M, K, N)) return 0;
-    return layout(M, M, K, 1, N, x_dtype, false).bytes;
+    const bool codes = x_dtype == QLIN_U8;
+    return layout(qlin::mx4_choose(M, N, K, 1, false, codes), M, M, K, 1, N, codes, false).bytes;
 }
 
 qlin_status qlin_mxfp4_matmul(const void* x, qlin_dtype x_dtype, const void* x_scales, const char* activation,
@@ -240,7 +272,8 @@ qlin_status qlin_mxfp4_matmul(const void* x, qlin_dtype x_dtype, const void* x_s
 size_t qlin_gather_mxfp4_matmul_workspace_bytes(int64_t B, int64_t R, int64_t K, int64_t E, int64_t N,
                                                 qlin_dtype x_dtype) {
     if (B < 1 || R < 1 || E < 1 || R > kMaxIndex || E > qlin::kMx4MaxExperts || !product_sizes_ok(B, K, N)) return 0;
-    return layout(B, R, K, E, N, x_dtype, true).bytes;
+    const bool codes = x_dtype == QLIN_U8;
+    return layout(qlin::mx4_choose(R, N, K, E, true, codes), B, R, K, E, N, codes, true).bytes;
 }
 
 qlin_status qlin_gather_mxfp4_matmul(const void* x, qlin_dtype x_dtype, const void* x_scales, const char* activation,

@@ -70,11 +70,6 @@ hipError_t launch_moe_combine_grad(const void* gy, const void* h, int dt, int64_
                                    const float* weights, const int32_t* experts, void* gh, float* gw,
                                    hipStream_t st);
 
-// Quantizes x [M, K] (or silu(x[:, :K]) * x[:, K:] of x [M, 2K]) to mxfp4:
-// words [M, K/8], scale rows `sstride` bytes apart; bytes past K/32 get 127.
-hipError_t launch_mxfp4_activation(const void* x, int dt, int64_t M, int64_t K, int swiglu, uint32_t* xq,
-                                   uint8_t* xs, int64_t sstride, hipStream_t st);
-
 // Product of two mxfp4 operands; gather form with experts != null.
 struct Mx4Args {
     const uint8_t* xq;        // codes [B, K/2 bytes]
@@ -85,17 +80,49 @@ struct Mx4Args {
     int64_t M, N, K;          // gather: M = R
     int64_t xsstride, wsstride;
     int ydt;
+    // a float x, quantized inside the kernel (streaming kernel, few rows)
+    const void* x;
+    int xdt, swiglu;
     // gather form
     const int32_t* experts;   // [R] or null
     int64_t B, E;             // row r reads x row r / (R / B)
-    void* plan;               // workspace of the row plan
 };
-// Bytes of the row plan for R rows over E experts (0 where none is made).
+
+// How a product runs.
+enum class Mx4Path {
+    kStreamFloat,             // streaming kernel, x quantized inside it
+    kStream,                  // streaming kernel on x's codes
+    kTiled                    // tiled kernel on x's codes; reads scale rows in 16-byte units
+};
+struct Mx4Choice {
+    Mx4Path path;
+    int tile;                 // kTiled: index of the tile's shape
+    int tile_rows;            // its rows
+};
+Mx4Choice mx4_choose(int64_t M, int64_t N, int64_t K, int64_t E, bool gather, bool codes);
+hipError_t launch_mx4_matmul(const Mx4Args& a, const Mx4Choice& c, const struct Mx4Plan* plan, hipStream_t st);
+
+// The streaming kernel on x's codes for any number of rows: blocks of 16 (by experts: one row each).
+hipError_t launch_mx4_stream_blocks(const Mx4Args& a, hipStream_t st);
+
+// x's codes and scale rows `sstride` bytes apart (bytes past K / 32 get 127) from a
+// float x [rows, K] (swiglu: [rows, 2K]), unless x is null, and the row plan for
+// R experts, unless experts is null.
+struct Mx4Prepare {
+    const void* x;
+    int dt;
+    int64_t rows, K;
+    int swiglu;
+    uint32_t* xq;
+    uint8_t* xs;
+    int64_t sstride;
+    const int32_t* experts;
+    int64_t R, E;
+    int tile_rows;
+    void* plan;               // mx4_plan_bytes(R, E)
+};
 size_t mx4_plan_bytes(int64_t R, int64_t E);
-// Whether the tiled kernel (and not the streaming one) takes the shape: it
-// reads scale rows in 16-byte units.
-bool mx4_tiled(int64_t M, int64_t N, int64_t K, int64_t E, bool gather);
-hipError_t launch_mx4_matmul(const Mx4Args& a, hipStream_t st, const char** path);
+hipError_t launch_mx4_prepare(const Mx4Prepare& q, struct Mx4Plan* plan, hipStream_t st);
 // Copies scale rows of KS bytes to rows `stride` bytes apart, filled with 127.
 hipError_t launch_mx4_pad_scales(const uint8_t* s, int64_t rows, int64_t KS, uint8_t* out, int64_t stride,
                                  hipStream_t st);

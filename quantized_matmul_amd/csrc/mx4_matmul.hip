@@ -18,12 +18,14 @@
 // dword, and op_sel alone steps through them.
 //
 // Two kernels:
-//  * streaming (few rows): bound by reading W once. 16 NT weight rows per
-//    workgroup, K split over its waves, both operands straight from memory
-//    into the instruction's registers, partial sums joined through LDS.
+//  * streaming (up to 16 rows): bound by reading W once. 16 weight rows per
+//    workgroup, K split over its waves, W straight from memory into the
+//    instruction's registers, partial sums joined through LDS. Up to 4 rows of
+//    a float x are quantized by each wave for its own part of K, which costs
+//    less than the launch it saves.
 //  * tiled (many rows): bound by the matrix cores and LDS. See mx4_tiled_kernel.
 
-#include "mx4_plan.h"
+#include "mx4_common.h"
 
 #include <atomic>
 #include <cstdlib>
@@ -80,130 +82,116 @@ __device__ __forceinline__ void store4(void* y, int64_t i, float a, float b, flo
 
 // ------------------------------------------------------------- streaming
 
-enum Rows : int { DENSE = 0, DIRECT = 1, PLAN = 2 };
+constexpr int STREAM_ROWS = 16;        // rows of x the kernel takes
+constexpr int STREAM_FLOAT_ROWS = 4;   // ... of a float x
+constexpr int STREAM_WAVES = 16;
 
 struct StreamArgs {
     Mx4Args a;
-    Mx4Plan plan;
-    uint32_t per_entry;    // index rows per row of x
-    int tile_n;            // blocks along N
+    uint32_t per_entry;    // index rows per row of x (DIRECT)
+    int tiles_n;
+    int vec;               // a float x is 16-byte aligned
 };
 
-// Where the tile's local row m comes from and goes to; false past the tile.
-struct RowMap {
-    int64_t src, dst;
-    bool ok;
+// A run is 512 values along K, 16 blocks: lane piece q of an operand's row holds
+// blocks 4q .. 4q + 3, 64 bytes of codes and a dword of scales.
+struct Piece {
+    u32x4 c[4];
+    uint32_t s;
 };
 
-template <int NT, int MT, int YDT, int ROWS>
-__global__ void __launch_bounds__(512) mx4_stream_kernel(StreamArgs s) {
-    extern __shared__ float red[];                 // [waves][16 MT][16 NT]
+// Lane piece of run `run` of a row whose piece of run 0 starts at c and s; `left` blocks of it exist.
+__device__ __forceinline__ Piece load_piece(const uint8_t* c, const uint8_t* s, int run, int left) {
+    Piece p;
+    p.s = scale4(s + run * 16, left);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+        p.c[b] = b < left ? *(const u32x4*)(c + (int64_t)run * 256 + 16 * b) : u32x4{0, 0, 0, 0};
+    return p;
+}
+
+// DIRECT: one index row a workgroup, with its expert's W; else up to 16 rows of
+// x. XDT QLIN_U8: x's codes; else a float x of up to 4 rows, quantized here.
+template <int YDT, int XDT, bool DIRECT>
+__global__ void __launch_bounds__(64 * STREAM_WAVES) mx4_stream_kernel(StreamArgs s) {
+    constexpr bool FLOAT = XDT != QLIN_U8;
+    constexpr int XR = DIRECT ? 1 : STREAM_FLOAT_ROWS;
+    extern __shared__ __align__(16) uint32_t lds[];     // partial sums [waves][16][16]; codes of a float x
     const Mx4Args& a = s.a;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
     const int i = lane & 15, q = lane >> 4;
-    const uint32_t tile = blockIdx.x / (uint32_t)s.tile_n;
-    const int64_t n0 = (int64_t)(blockIdx.x - tile * (uint32_t)s.tile_n) * (16 * NT);
-    int64_t first = 0, rows = 0;                   // places of the tile's rows
-    uint32_t expert = 0;
-    bool zero = false;
-    if constexpr (ROWS == DENSE) {
-        first = (int64_t)tile * (16 * MT);
-        rows = a.M - first;
-    } else if constexpr (ROWS == DIRECT) {
-        first = tile;
-        rows = 1;
-        expert = (uint32_t)a.experts[tile];
-        zero = expert >= (uint32_t)a.E;
-    } else {
-        if (tile >= s.plan.first_tile[a.E + 1]) return;
-        expert = s.plan.tile_group[tile];
-        zero = expert == (uint32_t)a.E;
-        first = (int64_t)s.plan.offsets[expert] + (int64_t)(tile - s.plan.first_tile[expert]) * (16 * MT);
-        rows = (int64_t)s.plan.offsets[expert + 1] - first;
-    }
-    auto map = [&](int m) {
-        RowMap r{0, 0, m < rows};
-        if (!r.ok) return r;
-        if constexpr (ROWS == PLAN) {
-            const uint32_t row = s.plan.perm[first + m];
-            r.dst = row;
-            r.src = row / s.per_entry;
-        } else {
-            r.dst = first + m;
-            r.src = ROWS == DIRECT ? (int64_t)((uint32_t)first / s.per_entry) : first + m;
-        }
-        return r;
-    };
+    const uint32_t tile = DIRECT ? blockIdx.x / (uint32_t)s.tiles_n : 0;
+    const int64_t n0 = (int64_t)(blockIdx.x - tile * (uint32_t)s.tiles_n) * 16;
+    const int rows = DIRECT ? 1 : (int)a.M;
+    const int64_t src = DIRECT ? (int64_t)(tile / s.per_entry) : 0;     // first row of x
+    const uint32_t expert = DIRECT ? (uint32_t)a.experts[tile] : 0;
 
-    f32x4 acc[NT][MT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int u = 0; u < MT; ++u) acc[t][u] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    if (!zero) {
-        const int KB = (int)(a.K / 32);            // blocks per row
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    if (!DIRECT || expert < (uint32_t)a.E) {            // else the row is zeros
+        const int KB = (int)(a.K / 32);                 // blocks of a row
         const int64_t half = a.K / 2;
-        const uint8_t *wp[NT], *wsp[NT], *xp[MT], *xsp[MT];
-        bool xok[MT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            int64_t n = n0 + 16 * t + i;
-            n = n < a.N ? n : a.N - 1;             // rows past N are computed and not stored
-            wp[t] = a.wq + ((int64_t)expert * a.N + n) * half + 64 * q;
-            wsp[t] = a.ws + ((int64_t)expert * a.N + n) * a.wsstride + 4 * q;
-        }
-#pragma unroll
-        for (int u = 0; u < MT; ++u) {
-            const RowMap r = map(16 * u + i);
-            xok[u] = r.ok;
-            xp[u] = a.xq + r.src * half + 64 * q;
-            xsp[u] = a.xs + r.src * a.xsstride + 4 * q;
-        }
-        const int runs = (KB + 15) / 16;           // runs of 16 blocks: 4 per lane piece
+        const int64_t n = (int64_t)expert * a.N + (n0 + i < a.N ? n0 + i : a.N - 1);   // rows past N are not stored
+        const uint8_t* const wp = a.wq + n * half + 64 * q;
+        const uint8_t* const wsp = a.ws + n * a.wsstride + 4 * q;
+        const int64_t xrow = src + (i < rows ? i : 0);
+        const int runs = (KB + 15) / 16;
+        Piece w = load_piece(wp, wsp, wave, KB - wave * 16 - 4 * q);
         for (int run = wave; run < runs; run += waves) {
-            const int left = KB - run * 16 - 4 * q;          // blocks of this lane piece
-            u32x4 w[NT][4], x[MT][4];
-            uint32_t sw[NT], sx[MT];
+            const int left = KB - run * 16 - 4 * q;
+            Piece next = w;
+            if (run + waves < runs) next = load_piece(wp, wsp, run + waves, left - 16 * waves);
+            Piece x;
+            if constexpr (FLOAT) {
+                // lane l rounds values 8 l .. 8 l + 7 of the run, a row at a time; the wave's own LDS
+                // turns words into pieces
+                uint32_t* const words = lds + waves * 256 + wave * XR * 68;      // [XR][64] words, [XR][4] scales
+                uint8_t* const bytes = (uint8_t*)(words + XR * 64);
+                const int64_t k = (int64_t)run * 512 + 8 * lane;
+                const bool live = k < a.K;                                       // whole blocks of 4 lanes
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                sw[t] = scale4(wsp[t] + run * 16, left);
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    w[t][c] = c < left ? *(const u32x4*)(wp[t] + (int64_t)run * 256 + 16 * c) : u32x4{0, 0, 0, 0};
-            }
-#pragma unroll
-            for (int u = 0; u < MT; ++u) {
-                const int l = xok[u] ? left : 0;
-                sx[u] = scale4(xsp[u] + run * 16, l);
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    x[u][c] = c < l ? *(const u32x4*)(xp[u] + (int64_t)run * 256 + 16 * c) : u32x4{0, 0, 0, 0};
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int u = 0; u < MT; ++u) {
-                    acc[t][u] = mfma16<0>(w[t][0], x[u][0], acc[t][u], sw[t], sx[u]);
-                    acc[t][u] = mfma16<1>(w[t][1], x[u][1], acc[t][u], sw[t], sx[u]);
-                    acc[t][u] = mfma16<2>(w[t][2], x[u][2], acc[t][u], sw[t], sx[u]);
-                    acc[t][u] = mfma16<3>(w[t][3], x[u][3], acc[t][u], sw[t], sx[u]);
+                for (int r = 0; r < XR; ++r) {
+                    if (r >= rows) break;
+                    const int64_t at = (src + r) * a.K * (a.swiglu ? 2 : 1) + (live ? k : 0);
+                    float v[8];
+                    load8<XDT>(a.x, at, s.vec, v);
+                    if (a.swiglu) {
+                        float up[8];
+                        load8<XDT>(a.x, at + a.K, s.vec, up);
+                        swiglu8(v, up);
+                    }
+                    uint32_t byte;
+                    const uint32_t word = mxfp4_word(v, &byte);
+                    words[r * 64 + lane] = live ? word : 0u;
+                    if ((lane & 3) == 0) bytes[r * 16 + (lane >> 2)] = live ? (uint8_t)byte : (uint8_t)127;
                 }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                const int r = i < rows ? i : 0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const u32x4 v = *(const u32x4*)(words + r * 64 + 16 * q + 4 * b);
+                    x.c[b] = i < rows ? v : u32x4{0, 0, 0, 0};
+                }
+                x.s = i < rows ? *(const uint32_t*)(bytes + r * 16 + 4 * q) : ONES;
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            } else {
+                x = load_piece(a.xq + xrow * half + 64 * q, a.xs + xrow * a.xsstride + 4 * q, run, i < rows ? left : 0);
+            }
+            acc = mfma16<0>(w.c[0], x.c[0], acc, w.s, x.s);
+            acc = mfma16<1>(w.c[1], x.c[1], acc, w.s, x.s);
+            acc = mfma16<2>(w.c[2], x.c[2], acc, w.s, x.s);
+            acc = mfma16<3>(w.c[3], x.c[3], acc, w.s, x.s);
+            w = next;
         }
     }
     // D[n][m]: n = 4 q + r, m = i
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int u = 0; u < MT; ++u)
-            *(f32x4*)(red + ((wave * MT + u) * 16 + i) * (16 * NT) + 16 * t + 4 * q) = acc[t][u];
+    float* const red = (float*)lds;
+    *(f32x4*)(red + (wave * 16 + i) * 16 + 4 * q) = acc;
     __syncthreads();
-    for (int o = tid; o < 256 * NT * MT; o += blockDim.x) {
-        const int m = o / (16 * NT), n = o - m * (16 * NT);
+    for (int o = tid; o < 16 * rows; o += blockDim.x) {
         float v = 0.0f;
-        for (int w = 0; w < waves; ++w) v += red[w * (256 * NT * MT) + o];
-        const RowMap r = map(m);
-        if (r.ok && n0 + n < a.N) store_f<YDT>(a.y, r.dst * a.N + n0 + n, v);
+        for (int w = 0; w < waves; ++w) v += red[w * 256 + o];
+        const int m = o >> 4, n = o & 15;
+        if (n0 + n < a.N) store_f<YDT>(a.y, ((DIRECT ? (int64_t)tile : m)) * a.N + n0 + n, v);
     }
 }
 
@@ -520,33 +508,25 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
     }
 }
 
-__global__ void __launch_bounds__(256) pad_scales_kernel(const uint8_t* __restrict__ s, int64_t n, uint32_t KS,
-                                                         uint8_t* __restrict__ out, uint32_t stride) {
-    const int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (o >= n) return;
-    const int64_t row = o / stride;
-    const uint32_t c = (uint32_t)(o - row * stride);
-    out[o] = c < KS ? s[row * KS + c] : (uint8_t)127;
-}
-
 // ---------------------------------------------------------------- dispatch
 
-template <int NT, int MT, int YDT, int ROWS>
-void stream_launch(const StreamArgs& s, int64_t tiles, hipStream_t st) {
-    const int64_t runs = (s.a.K + 511) / 512;
-    const int waves = runs >= 8 ? 8 : runs >= 4 ? 4 : runs >= 2 ? 2 : 1;
-    const size_t shm = (size_t)waves * 256 * NT * MT * sizeof(float);
-    mx4_stream_kernel<NT, MT, YDT, ROWS><<<(unsigned)(tiles * s.tile_n), 64 * waves, shm, st>>>(s);
+template <int YDT, int XDT, bool DIRECT>
+hipError_t stream_launch(const Mx4Args& a, hipStream_t st) {
+    const int64_t runs = (a.K + 511) / 512;
+    const int waves = (int)(runs < STREAM_WAVES ? runs : STREAM_WAVES);
+    StreamArgs s{a, DIRECT ? (uint32_t)(a.M / a.B) : 1, (int)((a.N + 15) / 16), ((uintptr_t)a.x & 15) == 0};
+    const int64_t blocks = (DIRECT ? a.M : 1) * s.tiles_n;
+    if (blocks > 0x7fffffffLL || (!DIRECT && a.M > (XDT == QLIN_U8 ? STREAM_ROWS : STREAM_FLOAT_ROWS)))
+        return hipErrorInvalidValue;
+    const size_t floats = XDT == QLIN_U8 ? 0 : (DIRECT ? 1 : STREAM_FLOAT_ROWS) * 68;
+    mx4_stream_kernel<YDT, XDT, DIRECT>
+        <<<(unsigned)blocks, 64 * waves, (size_t)waves * (256 + floats) * sizeof(uint32_t), st>>>(s);
+    return hipGetLastError();
 }
 
-template <int YDT, int ROWS>
-hipError_t stream_rows(StreamArgs s, int mt, int64_t tiles, hipStream_t st) {
-    s.tile_n = (int)((s.a.N + 15) / 16);
-    if (tiles * s.tile_n > 0x7fffffffLL) return hipErrorInvalidValue;
-    if (mt == 1) stream_launch<1, 1, YDT, ROWS>(s, tiles, st);
-    else if (mt == 2) stream_launch<1, 2, YDT, ROWS>(s, tiles, st);
-    else stream_launch<1, 4, YDT, ROWS>(s, tiles, st);
-    return hipGetLastError();
+template <int YDT, int XDT>
+hipError_t stream_rows(const Mx4Args& a, hipStream_t st) {
+    return a.experts ? stream_launch<YDT, XDT, true>(a, st) : stream_launch<YDT, XDT, false>(a, st);
 }
 
 template <int BN, int BM, int WN, int WM, int ST, int BKB, int YDT, bool GATHER>
@@ -568,81 +548,87 @@ hipError_t tiled_launch(TiledArgs p, hipStream_t st) {
     return hipGetLastError();
 }
 
-constexpr int64_t kStreamRows = 64;    // rows (of one expert, on average) up to which W is streamed
-
-int forced_tile() {
-    const char* e = getenv("QLIN_MXFP4_TILE");
-    return e && *e ? atoi(e) : -1;
-}
+// Shapes of the tiled kernel's workgroup: weight rows x activation rows, waves, stages.
+//  0: 256 x 256, 8 waves of 128 x 64: the least LDS and L2 traffic a product; one workgroup a CU.
+//  1: 128 x 128, 4 waves of 64 x 64; two workgroups a CU, so one's outputs leave under the other's products.
+//  2: 128 x 64 and 3: 64 x 64, for few rows: more workgroups and more loads in flight for each byte of W.
+constexpr int kTiles = 4;
+constexpr int kTileN[kTiles] = {256, 128, 128, 64}, kTileM[kTiles] = {256, 128, 64, 64};
 
 template <int YDT, bool GATHER>
-hipError_t tiled_rows(const Mx4Args& a, const Mx4Plan& plan, uint32_t per, int tile, hipStream_t st) {
-    const TiledArgs p{a, plan, per, 0, device_shape().xcds, debug_lds_nan() ? 1 : 0,
+hipError_t tiled_rows(const Mx4Args& a, const Mx4Plan& plan, int tile, hipStream_t st) {
+    const TiledArgs p{a, plan, GATHER ? (uint32_t)(a.M / a.B) : 1, 0, device_shape().xcds, debug_lds_nan() ? 1 : 0,
                       a.N % (YDT == QLIN_F32 ? 4 : 8) == 0 && (uintptr_t)a.y % 16 == 0 ? 1 : 0};
-    if (tile == 1) return tiled_launch<256, 256, 2, 2, 2, 128, YDT, GATHER>(p, st);
-    if (tile == 2) return tiled_launch<256, 256, 2, 4, 4, 64, YDT, GATHER>(p, st);
-    if (tile == 3) return tiled_launch<256, 128, 2, 2, 3, 64, YDT, GATHER>(p, st);
-    if (tile == 4) return tiled_launch<128, 128, 2, 2, 2, 128, YDT, GATHER>(p, st);
-    if (tile == 8) return tiled_launch<256, 128, 4, 2, 3, 128, YDT, GATHER>(p, st);
-    if (tile == 9) return tiled_launch<128, 64, 2, 2, 2, 128, YDT, GATHER>(p, st);
-    if (tile == 10) return tiled_launch<128, 64, 2, 2, 3, 128, YDT, GATHER>(p, st);
-    if (tile == 11) return tiled_launch<64, 64, 2, 2, 4, 128, YDT, GATHER>(p, st);
-    if (tile == 5) return tiled_launch<256, 256, 2, 2, 4, 64, YDT, GATHER>(p, st);
-    if (tile == 6) return tiled_launch<256, 256, 2, 4, 2, 128, YDT, GATHER>(p, st);
-    if (tile == 7) return tiled_launch<128, 128, 2, 2, 4, 64, YDT, GATHER>(p, st);
-    return tiled_launch<128, 128, 2, 2, 4, 128, YDT, GATHER>(p, st);
+    switch (tile) {
+    case 0: return tiled_launch<256, 256, 2, 4, 2, 128, YDT, GATHER>(p, st);
+    case 1: return tiled_launch<128, 128, 2, 2, 2, 128, YDT, GATHER>(p, st);
+    case 2: return tiled_launch<128, 64, 2, 2, 3, 128, YDT, GATHER>(p, st);
+    default: return tiled_launch<64, 64, 2, 2, 4, 128, YDT, GATHER>(p, st);
+    }
 }
 
 template <int YDT>
-hipError_t launch(const Mx4Args& a, hipStream_t st, const char** path) {
-    int tile = forced_tile();
-    if (tile < 0) tile = 4;
-    if (!a.experts) {
-        if (!mx4_tiled(a.M, a.N, a.K, 1, false)) {
-            *path = "mxfp4_stream";
-            const int mt = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
-            return stream_rows<YDT, DENSE>(StreamArgs{a, Mx4Plan{}, 1, 0}, mt, (a.M + 16 * mt - 1) / (16 * mt), st);
-        }
-        *path = "mxfp4_tiled";
-        return tiled_rows<YDT, false>(a, Mx4Plan{}, 1, tile, st);
+hipError_t launch(const Mx4Args& a, const Mx4Choice& c, const Mx4Plan* plan, hipStream_t st) {
+    if (c.path == Mx4Path::kStreamFloat) {
+        if (a.xdt == QLIN_F32) return stream_rows<YDT, QLIN_F32>(a, st);
+        if (a.xdt == QLIN_F16) return stream_rows<YDT, QLIN_F16>(a, st);
+        return stream_rows<YDT, QLIN_BF16>(a, st);
     }
-    const uint32_t per = (uint32_t)(a.M / a.B);
-    if (2 * a.M <= a.E) {
-        *path = "mxfp4_gather_direct";
-        return stream_rows<YDT, DIRECT>(StreamArgs{a, Mx4Plan{}, per, 0}, 1, a.M, st);
-    }
-    Mx4Plan plan{};
-    const bool tiled = mx4_tiled(a.M, a.N, a.K, a.E, true);
-    const int mt = a.M <= 16 * a.E ? 1 : a.M <= 32 * a.E ? 2 : 4;
-    const int rows = tiled ? (tile >= 9 ? 64 : tile == 0 || tile == 3 || tile == 4 || tile == 7 || tile == 8 ? 128 : 256) : 16 * mt;
-    hipError_t e = launch_mx4_plan(a.experts, a.M, a.E, rows, a.plan, &plan, st);
-    if (e != hipSuccess) return e;
-    if (!tiled) {
-        *path = "mxfp4_gather_stream";
-        return stream_rows<YDT, PLAN>(StreamArgs{a, plan, per, 0}, mt, mx4_plan_max_tiles(a.M, a.E, rows), st);
-    }
-    *path = "mxfp4_gather_tiled";
-    return tiled_rows<YDT, true>(a, plan, per, tile, st);
+    if (c.path == Mx4Path::kStream) return stream_rows<YDT, QLIN_U8>(a, st);
+    return a.experts ? tiled_rows<YDT, true>(a, *plan, c.tile, st) : tiled_rows<YDT, false>(a, Mx4Plan{}, c.tile, st);
+}
+
+// QLIN_MXFP4_TILE=0..3 forces a tile of the tiled kernel (tests run every one on the same inputs).
+int forced_tile() {
+    const char* e = getenv("QLIN_MXFP4_TILE");
+    return e && e[0] >= '0' && e[0] < '0' + kTiles && !e[1] ? e[0] - '0' : -1;
 }
 
 }  // namespace
 
-bool mx4_tiled(int64_t M, int64_t N, int64_t K, int64_t E, bool gather) {
-    const char* e = getenv("MX4S"); const int64_t kr = e ? atoi(e) : kStreamRows; return M > kr * (gather ? E : 1);
+// Dense: up to 16 rows stream. Beyond, the largest tile that still gives every
+// CU one: N = K = 8192, us for 512 / 256 / 128 rows: 128 x 128 30.5 / 28.4 /
+// 25.7, 128 x 64 33 / 17.8 / 16.0, 64 x 64 48 / 21.7 / 12.9.
+// By experts: while index rows are few against the experts, hardly two share
+// one, and each streams its expert's W without a plan. Beyond, the tile goes by
+// the rows an expert has on average, 64 experts [1536, 2048], us for 16 / 64 /
+// 128 / 1024 rows: 256 x 256 42 / 53 / 59 / 189, 128 x 128 33 / 43 / 61 / 223,
+// 128 x 64 31 / 46 / 62 / 271; then by the CUs as above.
+Mx4Choice mx4_choose(int64_t M, int64_t N, int64_t K, int64_t E, bool gather, bool codes) {
+    if (gather ? 2 * M <= E : M <= STREAM_ROWS)
+        return {codes || (!gather && M > STREAM_FLOAT_ROWS) ? Mx4Path::kStream : Mx4Path::kStreamFloat, -1, 0};
+    int tile = forced_tile();
+    if (tile < 0) {
+        const int cus = device_shape().cus;
+        tile = !gather || M >= 128 * E ? 0 : M >= 32 * E ? 1 : 2;
+        auto count = [&](int t) {
+            const int64_t m = gather ? M / kTileM[t] + (E < M ? E : M) / 2 + 1 : (M + kTileM[t] - 1) / kTileM[t];
+            return m * ((N + kTileN[t] - 1) / kTileN[t]);
+        };
+        while (tile < kTiles - 1 && count(tile) < cus) ++tile;
+    }
+    return {Mx4Path::kTiled, tile, kTileM[tile]};
 }
 
-hipError_t launch_mx4_matmul(const Mx4Args& a, hipStream_t st, const char** path) {
-    if (a.ydt == QLIN_BF16) return launch<QLIN_BF16>(a, st, path);
-    if (a.ydt == QLIN_F16) return launch<QLIN_F16>(a, st, path);
-    return launch<QLIN_F32>(a, st, path);
+hipError_t launch_mx4_matmul(const Mx4Args& a, const Mx4Choice& c, const Mx4Plan* plan, hipStream_t st) {
+    if (a.ydt == QLIN_BF16) return launch<QLIN_BF16>(a, c, plan, st);
+    if (a.ydt == QLIN_F16) return launch<QLIN_F16>(a, c, plan, st);
+    return launch<QLIN_F32>(a, c, plan, st);
 }
 
-hipError_t launch_mx4_pad_scales(const uint8_t* s, int64_t rows, int64_t KS, uint8_t* out, int64_t stride,
-                                 hipStream_t st) {
-    const int64_t n = rows * stride, grid = (n + 255) / 256;
-    if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
-    pad_scales_kernel<<<(unsigned)grid, 256, 0, st>>>(s, n, (uint32_t)KS, out, (uint32_t)stride);
-    return hipGetLastError();
+hipError_t launch_mx4_stream_blocks(const Mx4Args& a, hipStream_t st) {
+    const Mx4Choice c{Mx4Path::kStream, -1, 0};
+    if (a.experts) return launch_mx4_matmul(a, c, nullptr, st);
+    for (int64_t m0 = 0; m0 < a.M; m0 += STREAM_ROWS) {
+        Mx4Args b = a;
+        b.M = a.M - m0 < STREAM_ROWS ? a.M - m0 : STREAM_ROWS;
+        b.xq = a.xq + m0 * (a.K / 2);
+        b.xs = a.xs + m0 * a.xsstride;
+        b.y = (char*)a.y + m0 * a.N * (a.ydt == QLIN_F32 ? 4 : 2);
+        const hipError_t e = launch_mx4_matmul(b, c, nullptr, st);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace qlin

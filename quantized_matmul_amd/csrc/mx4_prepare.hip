@@ -1,0 +1,251 @@
+// mx4_prepare.hip -- what an mxfp4 product needs before its tiles can run: the
+// activation's codes and scales, and, by experts, the row plan. Both come from
+// one launch where the rows fit one chunk, so that the plan's round trips hide
+// behind the activation.
+//
+// Activation: one thread per packed word (8 values), 4 lanes per block; bound
+// by HBM.
+// Plan: workgroups of their own at the front of the launch, bound by latency
+// (a few barriers and memory round trips). More than one chunk of rows takes a
+// second launch: first counts per chunk, then each chunk scans all counts for
+// its own places. The order of rows inside a group is free: each output row
+// depends on its own inputs only.
+
+#include "mx4_common.h"
+
+namespace qlin {
+namespace {
+
+constexpr int THREADS = 512;
+constexpr int PLAN_PER = 8;                          // index rows of a thread
+constexpr int PLAN_CHUNK = THREADS * PLAN_PER;       // ... and of a workgroup
+
+struct PrepareArgs {
+    // activation
+    const void* x;
+    int64_t words;          // packed words in all; 0: codes are given
+    uint32_t row_words;     // packed words of a row
+    int swiglu, vec;
+    uint32_t* xq;
+    uint8_t* xs;
+    int64_t sstride;
+    // plan
+    const int32_t* experts; // null: dense
+    int R, E, chunks, tile_rows;
+    Mx4Plan plan;
+};
+
+__device__ __forceinline__ uint32_t group_of(int32_t e, uint32_t E) { return (uint32_t)e < E ? (uint32_t)e : E; }
+
+// Rows of each group in chunk `chunk`, to counts.
+__device__ __forceinline__ void plan_count(const PrepareArgs& a, int chunk, uint32_t* cnt) {
+    for (int e = threadIdx.x; e <= a.E; e += THREADS) cnt[e] = 0;
+    __syncthreads();
+    const int r0 = chunk * PLAN_CHUNK + threadIdx.x;
+#pragma unroll
+    for (int c = 0; c < PLAN_PER; ++c)
+        if (r0 + c * THREADS < a.R) atomicAdd(&cnt[group_of(a.experts[r0 + c * THREADS], a.E)], 1u);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= a.E; e += THREADS) a.plan.counts[(size_t)chunk * (a.E + 1) + e] = cnt[e];
+}
+
+// Places of the rows of chunk `chunk`; chunk 0 writes the tables too. A single
+// chunk counts its rows itself.
+__device__ __forceinline__ void plan_place(const PrepareArgs& a, int chunk, uint32_t* sh) {
+    const int E = a.E, tid = threadIdx.x;
+    uint32_t* const tot = sh;                        // [E + 1] rows of the group
+    uint32_t* const cur = sh + E + 1;                // [E + 1] next place of this chunk's rows
+    __shared__ uint32_t wsum[THREADS / 64][2], carry[2];
+    const int r0 = chunk * PLAN_CHUNK + tid;
+    if (tid < 2) carry[tid] = 0;
+    uint32_t g[PLAN_PER];
+#pragma unroll
+    for (int c = 0; c < PLAN_PER; ++c) {
+        const int r = r0 + c * THREADS;
+        g[c] = group_of(a.experts[r < a.R ? r : a.R - 1], E);
+    }
+    if (a.chunks == 1) {
+        for (int e = tid; e <= E; e += THREADS) tot[e] = cur[e] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < PLAN_PER; ++c)
+            if (r0 + c * THREADS < a.R) atomicAdd(&tot[g[c]], 1u);
+    } else {
+        for (int e = tid; e <= E; e += THREADS) {
+            uint32_t all = 0, before = 0;
+#pragma unroll 4
+            for (int q = 0; q < a.chunks; ++q) {
+                const uint32_t n = a.plan.counts[(size_t)q * (E + 1) + e];
+                before += q < chunk ? n : 0u;
+                all += n;
+            }
+            tot[e] = all;
+            cur[e] = before;
+        }
+    }
+    __syncthreads();
+    // exclusive scans over the groups: places, and row tiles
+    for (int base = 0; base <= E; base += THREADS) {
+        const int e = base + tid;
+        const uint32_t n = e <= E ? tot[e] : 0u;
+        const uint32_t nt = (n + a.tile_rows - 1) / a.tile_rows;
+        uint32_t vn = n, vt = nt;
+        for (int off = 1; off < 64; off <<= 1) {
+            const uint32_t un = __shfl_up(vn, off, 64), ut = __shfl_up(vt, off, 64);
+            if ((tid & 63) >= off) {
+                vn += un;
+                vt += ut;
+            }
+        }
+        if ((tid & 63) == 63) {
+            wsum[tid >> 6][0] = vn;
+            wsum[tid >> 6][1] = vt;
+        }
+        __syncthreads();
+        uint32_t pn = carry[0], pt = carry[1];
+        for (int w = 0; w < (tid >> 6); ++w) {
+            pn += wsum[w][0];
+            pt += wsum[w][1];
+        }
+        const uint32_t first = pn + vn - n, ftile = pt + vt - nt;
+        if (e <= E) {
+            cur[e] += first;
+            if (chunk == 0) {
+                a.plan.offsets[e] = first;
+                a.plan.first_tile[e] = ftile;
+                for (uint32_t u = 0; u < nt; ++u) a.plan.tile_group[ftile + u] = (uint32_t)e;
+                if (e == E) {
+                    a.plan.offsets[E + 1] = first + n;
+                    a.plan.first_tile[E + 1] = ftile + nt;
+                }
+            }
+        }
+        __syncthreads();
+        if (tid == THREADS - 1) {
+            carry[0] = pn + vn;
+            carry[1] = pt + vt;
+        }
+        __syncthreads();
+    }
+    uint32_t at[PLAN_PER];
+#pragma unroll
+    for (int c = 0; c < PLAN_PER; ++c) at[c] = r0 + c * THREADS < a.R ? atomicAdd(&cur[g[c]], 1u) : 0u;
+#pragma unroll
+    for (int c = 0; c < PLAN_PER; ++c)
+        if (r0 + c * THREADS < a.R) a.plan.perm[at[c]] = (uint32_t)(r0 + c * THREADS);
+}
+
+template <int DT>
+__device__ __forceinline__ void activation(const PrepareArgs& a, int64_t wid) {
+    const bool live = wid < a.words;                 // whole blocks of 4 lanes are live or not
+    const int64_t w0 = live ? wid : 0;
+    const int64_t row = w0 / a.row_words;
+    const uint32_t col = (uint32_t)(w0 - row * a.row_words);
+    float v[8];
+    if (a.swiglu) {
+        float up[8];
+        load8<DT>(a.x, (row * 2 * a.row_words + col) * 8, a.vec, v);
+        load8<DT>(a.x, (row * 2 * a.row_words + a.row_words + col) * 8, a.vec, up);
+        swiglu8(v, up);
+    } else {
+        load8<DT>(a.x, w0 * 8, a.vec, v);
+    }
+    uint32_t byte;
+    const uint32_t word = mxfp4_word(v, &byte);
+    if (!live) return;
+    a.xq[wid] = word;
+    if ((threadIdx.x & 3) == 0) {
+        uint8_t* const s = a.xs + row * a.sstride;
+        const uint32_t blk = col >> 2;
+        s[blk] = (uint8_t)byte;
+        if (col + 4 == a.row_words)
+            for (int64_t p = blk + 1; p < a.sstride; ++p) s[p] = 127;
+    }
+}
+
+// Workgroups [0, chunks) make the plan (or, with several chunks, its counts), the others the activation.
+template <int DT>
+__global__ void __launch_bounds__(THREADS) mx4_prepare_kernel(PrepareArgs a) {
+    extern __shared__ uint32_t sh[];
+    int b = blockIdx.x;
+    if (a.experts) {
+        if (b < a.chunks) {
+            if (a.chunks == 1) plan_place(a, 0, sh);
+            else plan_count(a, b, sh);
+            return;
+        }
+        b -= a.chunks;
+    }
+    activation<DT>(a, (int64_t)b * THREADS + threadIdx.x);
+}
+
+__global__ void __launch_bounds__(THREADS) mx4_place_kernel(PrepareArgs a) {
+    extern __shared__ uint32_t sh[];
+    plan_place(a, blockIdx.x, sh);
+}
+
+__global__ void __launch_bounds__(256) pad_scales_kernel(const uint8_t* __restrict__ s, int64_t n, uint32_t KS,
+                                                         uint8_t* __restrict__ out, uint32_t stride) {
+    const int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (o >= n) return;
+    const int64_t row = o / stride;
+    const uint32_t c = (uint32_t)(o - row * stride);
+    out[o] = c < KS ? s[row * KS + c] : (uint8_t)127;
+}
+
+}  // namespace
+
+size_t mx4_plan_bytes(int64_t R, int64_t E) {
+    const int64_t chunks = (R + PLAN_CHUNK - 1) / PLAN_CHUNK;
+    return (size_t)(2 * (E + 2) + (R / kPlanMinTile + E + 1) + R + chunks * (E + 1)) * sizeof(uint32_t);
+}
+
+hipError_t launch_mx4_prepare(const Mx4Prepare& q, Mx4Plan* plan, hipStream_t st) {
+    PrepareArgs a{};
+    a.x = q.x;
+    a.words = q.x ? q.rows * (q.K / 8) : 0;
+    a.row_words = (uint32_t)(q.K / 8);
+    a.swiglu = q.swiglu;
+    a.vec = ((uintptr_t)q.x & 15) == 0;              // rows are whole multiples of 64 bytes
+    a.xq = q.xq;
+    a.xs = q.xs;
+    a.sstride = q.sstride;
+    int64_t blocks = (a.words + THREADS - 1) / THREADS;
+    size_t shm = 0;
+    if (q.experts) {
+        const int64_t R = q.R, E = q.E;
+        if (R < 1 || R >= (1LL << 31) || E < 1 || E > kMx4MaxExperts || q.tile_rows < kPlanMinTile)
+            return hipErrorInvalidValue;
+        a.experts = q.experts;
+        a.R = (int)R;
+        a.E = (int)E;
+        a.chunks = (int)((R + PLAN_CHUNK - 1) / PLAN_CHUNK);
+        a.tile_rows = q.tile_rows;
+        uint32_t* w = (uint32_t*)q.plan;
+        a.plan.offsets = w;
+        a.plan.first_tile = w + (E + 2);
+        a.plan.tile_group = w + 2 * (E + 2);
+        a.plan.perm = a.plan.tile_group + (R / kPlanMinTile + E + 1);
+        a.plan.counts = a.plan.perm + R;
+        *plan = a.plan;
+        blocks += a.chunks;
+        shm = (size_t)2 * (E + 1) * sizeof(uint32_t);
+    }
+    if (blocks == 0) return hipSuccess;
+    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+    if (q.dt == QLIN_F32) mx4_prepare_kernel<QLIN_F32><<<(unsigned)blocks, THREADS, shm, st>>>(a);
+    else if (q.dt == QLIN_F16) mx4_prepare_kernel<QLIN_F16><<<(unsigned)blocks, THREADS, shm, st>>>(a);
+    else mx4_prepare_kernel<QLIN_BF16><<<(unsigned)blocks, THREADS, shm, st>>>(a);
+    if (a.chunks > 1) mx4_place_kernel<<<(unsigned)a.chunks, THREADS, shm, st>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_mx4_pad_scales(const uint8_t* s, int64_t rows, int64_t KS, uint8_t* out, int64_t stride,
+                                 hipStream_t st) {
+    const int64_t n = rows * stride, grid = (n + 255) / 256;
+    if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
+    pad_scales_kernel<<<(unsigned)grid, 256, 0, st>>>(s, n, (uint32_t)KS, out, (uint32_t)stride);
+    return hipGetLastError();
+}
+
+}  // namespace qlin

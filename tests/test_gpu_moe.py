@@ -174,7 +174,7 @@ def test_dense_product(M, N, K, dtype):
     print(f"mxfp4_matmul M{M} N{N} K{K} {dtype}", flush=True)
     qw, x = weight((N, K), 400 + N), rand((M, K), dtype, 500 + M)
     y = qm.mxfp4_matmul(x, qw)
-    assert y.dtype == x.dtype and qm.last_path() == ("mxfp4_tiled" if M > 64 else "mxfp4_stream")
+    assert y.dtype == x.dtype and qm.last_path() == ("mxfp4_tiled" if M > 16 else "mxfp4_stream")
     close(y, ref.mxfp4_round(f64(x)) @ values(qw).T, K)
     # the same codes given as such: the same bits
     if dtype != "f16":
@@ -256,14 +256,14 @@ def choices(B, k, E, seed, dropped=0.0, one=None):
 
 GATHER = [
     # B, k, E, N, K, dropped, one expert, path
-    (1, 8, 64, 48, 96, 0.0, None, "mxfp4_gather_direct"),
-    (2, 4, 16, 33, 544, 0.3, None, "mxfp4_gather_direct"),
-    (1, 1, 1, 20, 32, 0.0, None, "mxfp4_gather_stream"),
-    (5, 3, 4, 130, 160, 0.1, None, "mxfp4_gather_stream"),
-    (40, 2, 4, 64, 512, 0.0, None, "mxfp4_gather_stream"),
-    (60, 2, 3, 65, 480, 0.2, None, "mxfp4_gather_stream"),
-    (50, 4, 8, 70, 256, 0.0, 5, "mxfp4_gather_stream"),
-    (30, 2, 8, 70, 256, 0.0, -1, "mxfp4_gather_stream"),
+    (1, 8, 64, 48, 96, 0.0, None, "mxfp4_gather_stream"),
+    (2, 4, 16, 33, 544, 0.3, None, "mxfp4_gather_stream"),
+    (1, 1, 1, 20, 32, 0.0, None, "mxfp4_gather_tiled"),
+    (5, 3, 4, 130, 160, 0.1, None, "mxfp4_gather_tiled"),
+    (40, 2, 4, 64, 512, 0.0, None, "mxfp4_gather_tiled"),
+    (60, 2, 3, 65, 480, 0.2, None, "mxfp4_gather_tiled"),
+    (50, 4, 8, 70, 256, 0.0, 5, "mxfp4_gather_tiled"),
+    (30, 2, 8, 70, 256, 0.0, -1, "mxfp4_gather_tiled"),
     (200, 2, 5, 140, 96, 0.1, None, "mxfp4_gather_tiled"),
     (300, 4, 6, 129, 1056, 0.05, None, "mxfp4_gather_tiled"),
     (300, 1, 3, 300, 512, 0.0, 2, "mxfp4_gather_tiled"),
@@ -333,7 +333,7 @@ def test_products_refuse():
     with pytest.raises(qm.QlinError):
         qm.mxfp4_matmul(x, qw, activation="tanh")
     with pytest.raises(qm.QlinError):
-        qm.mxfp4_matmul(x, qw, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+        qm.mxfp4_matmul(x.repeat(10, 1), qw, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     qe = weight((2, 32, 64), 631)
     for bad in (ids.long(), ids[:3], ids[:, :1].expand(4, 2)):
         with pytest.raises(ValueError):
@@ -341,6 +341,23 @@ def test_products_refuse():
     assert qm.mxfp4_matmul(x[:0], qw).shape == (0, 32)
     assert qm.gather_mxfp4_matmul(x[:0], qe, ids[:0]).shape == (0, 2, 32)
     assert qm.gather_mxfp4_matmul(x, qe, ids[:, :0]).shape == (4, 0, 32)
+
+
+@pytest.mark.parametrize("tile", ["0", "1", "2", "3"])
+@pytest.mark.parametrize("M,N,K", [(17, 70, 96), (130, 300, 544), (300, 513, 1056)])
+def test_every_tile(M, N, K, tile, monkeypatch):
+    """Each shape of the tiled kernel's workgroup, dense and by experts, in every output type."""
+    monkeypatch.setenv("QLIN_MXFP4_TILE", tile)
+    qw, x = weight((3, N, K), 650 + N), rand((M, K), "bf16", 750 + M)
+    ids = choices(M, 2, 3, 850, 0.1)
+    t, w, x64 = torch.from_numpy(ids).to(DEV), values(qw), ref.mxfp4_round(f64(x))
+    first = qm.QuantizedWeight(qw.value[0], qw.scales[0], None, 32, 4, True, "mxfp4")
+    for dt in (torch.float32, torch.bfloat16, torch.float16):
+        print(f"tile {tile} M{M} N{N} K{K} {dt}", flush=True)
+        close(qm.mxfp4_matmul(x, first, out_dtype=dt), x64 @ w[0].T, K)
+        assert qm.last_path() == "mxfp4_tiled"
+        close(qm.gather_mxfp4_matmul(x, qw, t, out_dtype=dt), ref.gather_product(x64, w, ids), K)
+        assert qm.last_path() == "mxfp4_gather_tiled"
 
 
 @pytest.mark.parametrize("M", [70, 300])
