@@ -17,65 +17,117 @@ __device__ __forceinline__ uint32_t e2m1_code(float v) {
     return c | ((__float_as_uint(v) >> 28) & 8u);
 }
 
-// Eight elements of dtype DT at element i; 16-byte loads where `vec` (the tensor
-// is 16-byte aligned and i a multiple of 8).
+// Eight consecutive elements of dtype DT as they lie in memory.
 template <int DT>
-__device__ __forceinline__ void load8(const void* p, int64_t i, bool vec, float (&v)[8]) {
-    if (!vec) {
+struct Eight {
+    uint32_t d[DT == QLIN_F32 ? 8 : 4];
+    __device__ __forceinline__ float at(int c) const {
+        if constexpr (DT == QLIN_F32) return __uint_as_float(d[c]);
+        const uint32_t h = (d[c / 2] >> (16 * (c & 1))) & 0xFFFFu;
+        return DT == QLIN_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
+    }
+};
+
+// 16-byte loads where `vec` (the tensor is 16-byte aligned and i a multiple of 8).
+template <int DT>
+__device__ __forceinline__ Eight<DT> load8(const void* p, int64_t i, bool vec) {
+    Eight<DT> r;
+    constexpr int N = DT == QLIN_F32 ? 8 : 4;
+    if (vec) {
+        const uint4* q = (const uint4*)((const char*)p + i * (DT == QLIN_F32 ? 4 : 2));
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = load_f<DT>(p, i + c);
+        for (int h = 0; h < N / 4; ++h) {
+            const uint4 t = q[h];
+            r.d[4 * h] = t.x; r.d[4 * h + 1] = t.y; r.d[4 * h + 2] = t.z; r.d[4 * h + 3] = t.w;
+        }
     } else if constexpr (DT == QLIN_F32) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float4 q = *(const float4*)((const float*)p + i + 4 * h);
-            v[4 * h] = q.x; v[4 * h + 1] = q.y; v[4 * h + 2] = q.z; v[4 * h + 3] = q.w;
-        }
+        for (int c = 0; c < 8; ++c) r.d[c] = ((const uint32_t*)p)[i + c];
     } else {
-        const uint4 q = *(const uint4*)((const uint16_t*)p + i);
-        const uint32_t d[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            v[2 * c] = DT == QLIN_BF16 ? bf16_bits_to_f32(d[c] & 0xFFFFu) : f16_bits_to_f32(d[c] & 0xFFFFu);
-            v[2 * c + 1] = DT == QLIN_BF16 ? bf16_bits_to_f32(d[c] >> 16) : f16_bits_to_f32(d[c] >> 16);
-        }
+        for (int c = 0; c < 4; ++c)
+            r.d[c] = ((const uint16_t*)p)[i + 2 * c] | (uint32_t)((const uint16_t*)p)[i + 2 * c + 1] << 16;
     }
+    return r;
 }
 
-// v = silu(v) * up in fp32, with one IEEE division; no contraction, so that
-// every kernel rounds alike.
-__device__ __forceinline__ void swiglu8(float (&v)[8], const float (&up)[8]) {
-#pragma clang fp contract(off)
+// silu(gate) * up in fp32 with the hardware's 2^x and 1 / x (1 ulp each): the
+// result is rounded to four bits next, so their ulps decide a code only where
+// it lies within about 2^-20 of a tie.
+template <int DT>
+__device__ __forceinline__ Eight<QLIN_F32> swiglu8(const Eight<DT>& gate, const Eight<DT>& up) {
+    Eight<QLIN_F32> r;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] = v[c] / (1.0f + expf(-v[c])) * up[c];
+    for (int c = 0; c < 8; ++c) {
+        const float g = gate.at(c);
+        const float s = g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -0x1.715476p+0f));
+        r.d[c] = __float_as_uint(s * up.at(c));
+    }
+    return r;
+}
+
+// Bits of the largest magnitude of the eight as an fp32 number (infinity or
+// above where one is not finite): integer maxima, since magnitudes order as
+// their bits do.
+template <int DT>
+__device__ __forceinline__ uint32_t amax_bits(const Eight<DT>& v) {
+    if constexpr (DT == QLIN_F32) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) m = max_u(m, v.d[c] & 0x7FFFFFFFu);
+        return m;
+    } else {
+        typedef __attribute__((ext_vector_type(2))) unsigned short u16x2;
+        u16x2 m = __builtin_bit_cast(u16x2, v.d[0] & 0x7FFF7FFFu);
+#pragma unroll
+        for (int c = 1; c < 4; ++c)
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v.d[c] & 0x7FFF7FFFu));
+        const uint32_t h = m[0] > m[1] ? m[0] : m[1];
+        if constexpr (DT == QLIN_BF16) return h << 16;
+        return h >= 0x7C00u ? 0x7F800000u : __float_as_uint(f16_bits_to_f32(h));
+    }
 }
 
 // The packed word of eight values; the four lanes of an aligned quad hold a
 // block of 32 (all active) and get its scale byte. qlin_quantize's mxfp4 rule:
 // shared exponent e = floor(log2 amax) - 2 in [-127, 127], byte e + 127 (0 for
-// an all-zero block), codes the nearest E2M1 of v / 2^e. A block with a NaN or
-// an infinity gets byte 255, the format's NaN.
-__device__ __forceinline__ uint32_t mxfp4_word(const float (&v)[8], uint32_t* byte) {
-    float amax = 0.0f;
-    bool bad = false;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        amax = fmaxf(amax, fabsf(v[c]));
-        bad |= !(fabsf(v[c]) < INFINITY);
-    }
-    uint32_t m = bad ? 0x7F800000u : __float_as_uint(amax);      // ordered like the numbers
+// an all-zero block), codes the nearest E2M1 of v / 2^e, ties to even,
+// saturated: what the hardware's conversion gives for every scale of 2^-126 and
+// above (checked on the device over ties, their neighbours and random values).
+// A block with a NaN or an infinity gets byte 255, the format's NaN.
+template <int DT>
+__device__ __forceinline__ uint32_t mxfp4_word(const Eight<DT>& v, uint32_t* byte) {
+    uint32_t m = amax_bits<DT>(v);
     m = max_u(m, dpp_u<0xB1>(m));                                // quad_perm 1 0 3 2
     m = max_u(m, dpp_u<0x4E>(m));                                // quad_perm 2 3 0 1
-    if (m >= 0x7F800000u) {
-        *byte = 255u;
-        return 0u;
-    }
-    int e = m == 0u ? -127 : (m >> 23 ? (int)(m >> 23) - 127 : (31 - __builtin_clz(m)) - 149) - 2;
-    e = e < -127 ? -127 : e;
-    *byte = (uint32_t)(e + 127);
+    const uint32_t ex = m >> 23;                                 // 0 for an fp32 subnormal: its block is scaled by 2^-127
+    *byte = ex >= 255u ? 255u : ex < 2u ? 0u : ex - 2u;
     uint32_t word = 0;
+    if (ex < 3u) {                                               // scale 2^-127
 #pragma unroll
-    for (int c = 0; c < 8; ++c) word |= e2m1_code(__builtin_ldexpf(v[c], -e)) << (4 * c);
-    return word;
+        for (int c = 0; c < 8; ++c) word |= e2m1_code(__builtin_ldexpf(v.at(c), 127)) << (4 * c);
+        return word;
+    }
+    const float scale = __uint_as_float(*byte << 23);
+    if constexpr (DT == QLIN_F32) {
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, v.at(0), v.at(1), scale, 0);
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, v.at(2), v.at(3), scale, 1);
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, v.at(4), v.at(5), scale, 2);
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, v.at(6), v.at(7), scale, 3);
+    } else if constexpr (DT == QLIN_BF16) {
+        typedef __attribute__((ext_vector_type(2))) __bf16 b2;
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(word, __builtin_bit_cast(b2, v.d[0]), scale, 0);
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(word, __builtin_bit_cast(b2, v.d[1]), scale, 1);
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(word, __builtin_bit_cast(b2, v.d[2]), scale, 2);
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(word, __builtin_bit_cast(b2, v.d[3]), scale, 3);
+    } else {
+        typedef __attribute__((ext_vector_type(2))) _Float16 h2;
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(word, __builtin_bit_cast(h2, v.d[0]), scale, 0);
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(word, __builtin_bit_cast(h2, v.d[1]), scale, 1);
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(word, __builtin_bit_cast(h2, v.d[2]), scale, 2);
+        word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(word, __builtin_bit_cast(h2, v.d[3]), scale, 3);
+    }
+    return ex >= 255u ? 0u : word;
 }
 
 // ------------------------------------------------------------------ row plan

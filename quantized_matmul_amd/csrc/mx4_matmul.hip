@@ -152,15 +152,12 @@ __global__ void __launch_bounds__(64 * STREAM_WAVES) mx4_stream_kernel(StreamArg
                 for (int r = 0; r < XR; ++r) {
                     if (r >= rows) break;
                     const int64_t at = (src + r) * a.K * (a.swiglu ? 2 : 1) + (live ? k : 0);
-                    float v[8];
-                    load8<XDT>(a.x, at, s.vec, v);
-                    if (a.swiglu) {
-                        float up[8];
-                        load8<XDT>(a.x, at + a.K, s.vec, up);
-                        swiglu8(v, up);
-                    }
-                    uint32_t byte;
-                    const uint32_t word = mxfp4_word(v, &byte);
+                    uint32_t byte, word;
+                    if (a.swiglu)
+                        word = mxfp4_word<QLIN_F32>(
+                            swiglu8<XDT>(load8<XDT>(a.x, at, s.vec), load8<XDT>(a.x, at + a.K, s.vec)), &byte);
+                    else
+                        word = mxfp4_word<XDT>(load8<XDT>(a.x, at, s.vec), &byte);
                     words[r * 64 + lane] = live ? word : 0u;
                     if ((lane & 3) == 0) bytes[r * 16 + (lane >> 2)] = live ? (uint8_t)byte : (uint8_t)127;
                 }

@@ -25,6 +25,7 @@ struct PrepareArgs {
     const void* x;
     int64_t words;          // packed words in all; 0: codes are given
     uint32_t row_words;     // packed words of a row
+    uint32_t div_mul, div_shift;   // word / row_words, see row_of; div_mul 0: 64-bit division
     int swiglu, vec;
     uint32_t* xq;
     uint8_t* xs;
@@ -135,32 +136,42 @@ __device__ __forceinline__ void plan_place(const PrepareArgs& a, int chunk, uint
         if (r0 + c * THREADS < a.R) a.plan.perm[at[c]] = (uint32_t)(r0 + c * THREADS);
 }
 
+// n / row_words for n < 2^32: the high word of a product and two shifts (Granlund and Montgomery's division by an
+// invariant, the multiplier from the host); a 64-bit division beyond.
+__device__ __forceinline__ int64_t row_of(const PrepareArgs& a, int64_t n) {
+    if (!a.div_mul) return n / a.row_words;
+    const uint32_t u = (uint32_t)n, h = __umulhi(u, a.div_mul);
+    return (h + ((u - h) >> 1)) >> a.div_shift;
+}
+
 template <int DT>
 __device__ __forceinline__ void activation(const PrepareArgs& a, int64_t wid) {
     const bool live = wid < a.words;                 // whole blocks of 4 lanes are live or not
     const int64_t w0 = live ? wid : 0;
-    const int64_t row = w0 / a.row_words;
+    const int64_t row = row_of(a, w0);
     const uint32_t col = (uint32_t)(w0 - row * a.row_words);
-    float v[8];
+    uint32_t byte, word;
     if (a.swiglu) {
-        float up[8];
-        load8<DT>(a.x, (row * 2 * a.row_words + col) * 8, a.vec, v);
-        load8<DT>(a.x, (row * 2 * a.row_words + a.row_words + col) * 8, a.vec, up);
-        swiglu8(v, up);
+        const int64_t at = (row * a.row_words + w0) * 8;
+        const Eight<DT> gate = load8<DT>(a.x, at, a.vec), up = load8<DT>(a.x, at + (int64_t)a.row_words * 8, a.vec);
+        word = mxfp4_word<QLIN_F32>(swiglu8<DT>(gate, up), &byte);
     } else {
-        load8<DT>(a.x, w0 * 8, a.vec, v);
+        word = mxfp4_word<DT>(load8<DT>(a.x, w0 * 8, a.vec), &byte);
     }
-    uint32_t byte;
-    const uint32_t word = mxfp4_word(v, &byte);
-    if (!live) return;
-    a.xq[wid] = word;
-    if ((threadIdx.x & 3) == 0) {
-        uint8_t* const s = a.xs + row * a.sstride;
-        const uint32_t blk = col >> 2;
+    uint8_t* const s = a.xs + row * a.sstride;
+    const uint32_t blk = col >> 2;
+    if (live) a.xq[wid] = word;
+    if (a.row_words % 16 == 0) {
+        // 16 lanes hold four blocks of one row: their bytes leave as a dword
+        uint32_t four = byte << (8 * (blk & 3));
+        four |= dpp_u<0x124>(four);                  // row_ror 4 and 8
+        four |= dpp_u<0x128>(four);
+        if (live && (threadIdx.x & 15) == 0) *(uint32_t*)(s + blk) = four;
+    } else if (live && (threadIdx.x & 3) == 0) {
         s[blk] = (uint8_t)byte;
-        if (col + 4 == a.row_words)
-            for (int64_t p = blk + 1; p < a.sstride; ++p) s[p] = 127;
     }
+    if (live && col + 4 == a.row_words)              // the row's last block
+        for (int64_t p = blk + 1; p < a.sstride; ++p) s[p] = 127;
 }
 
 // Workgroups [0, chunks) make the plan (or, with several chunks, its counts), the others the activation.
@@ -205,6 +216,12 @@ hipError_t launch_mx4_prepare(const Mx4Prepare& q, Mx4Plan* plan, hipStream_t st
     a.x = q.x;
     a.words = q.x ? q.rows * (q.K / 8) : 0;
     a.row_words = (uint32_t)(q.K / 8);
+    if (a.words < (1LL << 32) && a.row_words > 1) {
+        uint32_t l = 0;                              // ceil(log2 row_words)
+        while ((1ull << l) < a.row_words) ++l;
+        a.div_mul = (uint32_t)((((1ull << l) - a.row_words) << 32) / a.row_words + 1);
+        a.div_shift = l - 1;
+    }
     a.swiglu = q.swiglu;
     a.vec = ((uintptr_t)q.x & 15) == 0;              // rows are whole multiples of 64 bytes
     a.xq = q.xq;

@@ -235,6 +235,27 @@ def test_dense_product_marks_blocks_that_are_not_finite(M, bad):
     assert torch.equal(y[keep], clean[keep])
 
 
+@pytest.mark.parametrize("M", [2, 12, 40])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_activation_rounding_is_exact(M, dtype):
+    """Against the identity the product gives the rounded activation itself:
+    E2M1 ties and their neighbours at many scales, tiny blocks, signed zeros."""
+    K = 160
+    rng = np.random.default_rng(77)
+    ties = np.array([0, .25, .5, .75, 1, 1.25, 1.5, 1.75, 2, 2.5, 3, 3.5, 4, 5, 6, 7])
+    top = {"bf16": 60, "f16": 8, "f32": 60}[dtype]
+    v = rng.choice(ties, (M, K // 32, 32)) * (1 + rng.integers(-1, 2, (M, K // 32, 32)) * UNIT[dtype] * 2)
+    v *= rng.choice([-1.0, 1.0], v.shape) * np.exp2(rng.integers(-top, top, (M, K // 32, 1)))
+    v[0, 0] = 0.0
+    v[1, 1] = -0.0
+    v[1, 2] *= {"bf16": 1e-30, "f16": 1e-3, "f32": 1e-36}[dtype]        # down to the type's subnormals
+    x = torch.from_numpy(v.reshape(M, K)).to(DTYPES[dtype]).to(DEV)
+    eye = qm.quantize(torch.eye(K, device=DEV), 32, 4, "mxfp4")
+    assert np.array_equal(values(eye), np.eye(K))
+    y = qm.mxfp4_matmul(x, eye, out_dtype=torch.float32)
+    np.testing.assert_array_equal(f64(y), ref.mxfp4_round(f64(x)))
+
+
 @pytest.mark.parametrize("scale", [1e-30, 1e30, 0.0])
 def test_dense_product_extreme_values(scale):
     qw = weight((32, 64), 440)
