@@ -135,12 +135,36 @@ __device__ __forceinline__ uint32_t mxfp4_word(const Eight<DT>& v, uint32_t* byt
 // Experts of one call: two counters each in the 64 KB of LDS every kernel may ask for.
 constexpr int64_t kMx4MaxExperts = 8000;
 
+// n / d for n < 2^32 by a multiplication and shifts (Granlund and Montgomery's
+// division by an invariant); the host makes it.
+struct FastDiv {
+    uint32_t mul, shift;   // mul 0: d is 1
+    static FastDiv by(uint32_t d) {
+        if (d <= 1) return {0, 0};
+        uint32_t l = 0;    // ceil(log2 d)
+        while ((1ull << l) < d) ++l;
+        return {(uint32_t)((((1ull << l) - d) << 32) / d + 1), l - 1};
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+        if (!mul) return n;
+        const uint32_t h = __umulhi(n, mul);
+        return (h + ((n - h) >> 1)) >> shift;
+    }
+};
+
+// A row tile: everything a workgroup needs to know of it in one 32-byte load.
+struct Mx4Tile {
+    uint32_t group;         // expert; E: rows without one, whose outputs are zeros
+    uint32_t first, count;  // first row tile of the group, row tiles of the group
+    uint32_t place, rows;   // first place of the group in perm, rows of the group
+    uint32_t unused[3];
+};
+
 // Index rows grouped by expert and cut into row tiles. Rows whose expert is
 // outside [0, E) form one more group, E, whose tiles write zeros.
 struct Mx4Plan {
-    uint32_t* offsets;      // [E + 2] first place of each group in perm
-    uint32_t* first_tile;   // [E + 2] first row tile of each group; the last entry is the number of tiles
-    uint32_t* tile_group;   // group of each row tile
+    Mx4Tile* tiles;
+    uint32_t* total;        // [1] row tiles
     uint32_t* perm;         // [R] index rows by group
     uint32_t* counts;       // [chunks][E + 1] rows of each group in each chunk of rows
 };

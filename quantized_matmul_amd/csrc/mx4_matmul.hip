@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(64 * STREAM_WAVES) mx4_stream_kernel(StreamArg
 struct TiledArgs {
     Mx4Args a;
     Mx4Plan plan;
-    uint32_t per_entry;
+    FastDiv per_entry;     // index row / index rows per row of x
     int tiles_n;
     int xcds;
     int lds_nan;
@@ -229,10 +229,54 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n, uint32_t xcd
     return x * per + (x < more ? x : more) + b / xcds;
 }
 
-#ifndef SPREAD
-#define SPREAD 1
-#endif
 constexpr uint32_t NOWHERE = 0x80000000u;   // past every buffer range: reads zeros
+
+// Where a workgroup's tile lies. `b` numbers the tiles: by experts an expert's row
+// tiles run fastest, dense ones in bands of 8 row tiles, n outer and m inner in a
+// band, so that neighbours share W or x in their XCD's L2.
+struct TilePlace {
+    int64_t m0;            // first place (dense: row) of the tile
+    int rows, n0, nrows;
+    uint32_t expert;       // E: zeros
+};
+
+template <int BN, int BM, bool GATHER>
+__device__ __forceinline__ TilePlace tile_place(const TiledArgs& p, uint32_t b) {
+    const Mx4Args& a = p.a;
+    const uint32_t tn = (uint32_t)p.tiles_n;
+    TilePlace t;
+    int64_t rows;
+    if constexpr (GATHER) {
+        // one scalar load: the plan does not change while the kernel runs
+        typedef __attribute__((ext_vector_type(8))) uint32_t u32x8;
+        const Mx4Tile g = __builtin_bit_cast(
+            Mx4Tile, *(const __attribute__((address_space(4))) u32x8*)(p.plan.tiles + b / tn));
+        const uint32_t in = b - g.first * tn;
+        t.expert = g.group;
+        t.n0 = (int)(in / g.count) * BN;
+        const uint32_t m = in % g.count * BM;
+        t.m0 = (int64_t)g.place + m;
+        rows = (int64_t)g.rows - m;
+    } else {
+        const uint32_t tm = (uint32_t)((a.M + BM - 1) / BM);
+        const uint32_t band = b / (8 * tn), in = b - band * 8 * tn, h = tm - band * 8 < 8 ? tm - band * 8 : 8;
+        t.expert = 0;
+        t.n0 = (int)(in / h) * BN;
+        t.m0 = (int64_t)(band * 8 + in % h) * BM;
+        rows = a.M - t.m0;
+    }
+    t.rows = (int)(rows < BM ? rows : BM);
+    t.nrows = (int)(a.N - t.n0 < BN ? a.N - t.n0 : BN);
+    return t;
+}
+
+// Tiles in all.
+template <int BM, bool GATHER>
+__device__ __forceinline__ uint32_t tiles_total(const TiledArgs& p) {
+    const uint32_t tm =
+        GATHER ? *(const __attribute__((address_space(4))) uint32_t*)p.plan.total : (uint32_t)((p.a.M + BM - 1) / BM);
+    return tm * (uint32_t)p.tiles_n;
+}
 
 // Tile of BN weight rows (n) by BM activation rows (m), WN x WM waves of
 // TN x TM 32x32 accumulators, K in steps of BKB bytes (2 BKB codes) a row:
@@ -262,6 +306,9 @@ struct Shape {
     // LDS of the outputs: per wave 32 rows of TN 32 values, rows 16 bytes longer against conflicts
     static constexpr int orow(int size) { return TN * 32 * size + 16; }
     static constexpr int lds(int size) { return LOOP > NW * 32 * orow(size) ? LOOP : NW * 32 * orow(size); }
+    // products between two code loads of a step; all of them go out in it
+    static constexpr int EVERY = 2 * ND <= KH * TN * TM && TN * TM % 2 == 0 ? 2 : 1;
+    static_assert(ND * EVERY <= KH * TN * TM, "a step issues all its loads");
     static_assert((BN / RPL) % NW == 0 && (BM / RPL) % NW == 0, "whole loads per wave");
     // loads issued after those of a step of phase ph (its number mod SG) when it starts: the LA - 1
     // steps after it, of which those that open a batch brought its scales
@@ -285,31 +332,12 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
     const int wn = wv / WM, wm = wv % WM;
     const int i = lane & 31, j = lane >> 5;
 
-    int64_t m0, rows;
-    int n0;
-    uint32_t expert = 0;
-    if constexpr (GATHER) {
-        const uint32_t total = p.plan.first_tile[a.E + 1] * (uint32_t)p.tiles_n;
-        if (blockIdx.x >= total) return;
-        const uint32_t b = xcd_run(blockIdx.x, total, p.xcds);
-        expert = p.plan.tile_group[b / (uint32_t)p.tiles_n];
-        const uint32_t f = p.plan.first_tile[expert], cnt = p.plan.first_tile[expert + 1] - f;
-        const uint32_t in = b - f * (uint32_t)p.tiles_n;         // within the expert: m fastest
-        n0 = (int)(in / cnt) * BN;
-        m0 = (int64_t)p.plan.offsets[expert] + (int64_t)(in % cnt) * BM;
-        rows = (int64_t)p.plan.offsets[expert + 1] - m0;
-    } else {
-        const uint32_t b = xcd_run(blockIdx.x, gridDim.x, p.xcds);
-        const uint32_t tm = (uint32_t)((a.M + BM - 1) / BM);
-        // bands of 8 row tiles, n outer and m inner within a band
-        const uint32_t band = b / (8 * (uint32_t)p.tiles_n), in = b - band * 8 * (uint32_t)p.tiles_n;
-        const uint32_t h = tm - band * 8 < 8 ? tm - band * 8 : 8;
-        n0 = (int)(in / h) * BN;
-        m0 = (int64_t)(band * 8 + in % h) * BM;
-        rows = a.M - m0;
-    }
-    if (rows > BM) rows = BM;
-    const int nrows = (int)(a.N - n0 < BN ? a.N - n0 : BN);
+    const uint32_t total = tiles_total<BM, GATHER>(p);
+    if (blockIdx.x >= total) return;
+    const TilePlace t = tile_place<BN, BM, GATHER>(p, xcd_run(blockIdx.x, total, p.xcds));
+    const int64_t m0 = t.m0;
+    const int rows = t.rows, n0 = t.n0, nrows = t.nrows;
+    const uint32_t expert = t.expert;
 
     f32x16 acc[TN][TM];
 #pragma unroll
@@ -334,7 +362,7 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
         const __amdgpu_buffer_rsrc_t xsr = rsrc(a.xs + xrow * a.xsstride, (uint32_t)(xrows * a.xsstride));
         auto src = [&](int r) -> uint32_t {        // x row of local row r, NOWHERE past the tile
             if (r >= rows) return NOWHERE;
-            if constexpr (GATHER) return p.plan.perm[m0 + r] / p.per_entry;
+            if constexpr (GATHER) return p.per_entry(p.plan.perm[m0 + r]);
             else return (uint32_t)r;
         };
 
@@ -435,10 +463,7 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
                     else if (h == 1) c = mfma32<1>(A, B, c, sa, sb);
                     else if (h == 2) c = mfma32<2>(A, B, c, sa, sb);
                     else c = mfma32<3>(A, B, c, sa, sb);
-                    if (d < S::ND && q % SPREAD == SPREAD - 1) {
-                        dma(kt + S::LA, d++);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
+                    if (d < S::ND && q % S::EVERY == S::EVERY - 1) dma(kt + S::LA, d++);
                 }
             }
         };
@@ -546,7 +571,7 @@ hipError_t tiled_launch(TiledArgs p, hipStream_t st) {
 }
 
 // Shapes of the tiled kernel's workgroup: weight rows x activation rows, waves, stages.
-//  0: 256 x 256, 8 waves of 128 x 64: the least LDS and L2 traffic a product; one workgroup a CU.
+//  0: 256 x 256, 8 waves of 64 x 128: the least LDS and L2 traffic a product; one workgroup a CU.
 //  1: 128 x 128, 4 waves of 64 x 64; two workgroups a CU, so one's outputs leave under the other's products.
 //  2: 128 x 64 and 3: 64 x 64, for few rows: more workgroups and more loads in flight for each byte of W.
 constexpr int kTiles = 4;
@@ -554,10 +579,10 @@ constexpr int kTileN[kTiles] = {256, 128, 128, 64}, kTileM[kTiles] = {256, 128, 
 
 template <int YDT, bool GATHER>
 hipError_t tiled_rows(const Mx4Args& a, const Mx4Plan& plan, int tile, hipStream_t st) {
-    const TiledArgs p{a, plan, GATHER ? (uint32_t)(a.M / a.B) : 1, 0, device_shape().xcds, debug_lds_nan() ? 1 : 0,
+    const TiledArgs p{a, plan, FastDiv::by(GATHER ? (uint32_t)(a.M / a.B) : 1), 0, device_shape().xcds, debug_lds_nan() ? 1 : 0,
                       a.N % (YDT == QLIN_F32 ? 4 : 8) == 0 && (uintptr_t)a.y % 16 == 0 ? 1 : 0};
     switch (tile) {
-    case 0: return tiled_launch<256, 256, 2, 4, 2, 128, YDT, GATHER>(p, st);
+    case 0: return tiled_launch<256, 256, 4, 2, 2, 128, YDT, GATHER>(p, st);
     case 1: return tiled_launch<128, 128, 2, 2, 2, 128, YDT, GATHER>(p, st);
     case 2: return tiled_launch<128, 64, 2, 2, 3, 128, YDT, GATHER>(p, st);
     default: return tiled_launch<64, 64, 2, 2, 4, 128, YDT, GATHER>(p, st);

@@ -25,7 +25,8 @@ struct PrepareArgs {
     const void* x;
     int64_t words;          // packed words in all; 0: codes are given
     uint32_t row_words;     // packed words of a row
-    uint32_t div_mul, div_shift;   // word / row_words, see row_of; div_mul 0: 64-bit division
+    FastDiv by_row;         // word / row_words
+    int wide;               // 2^32 words or more: 64-bit division
     int swiglu, vec;
     uint32_t* xq;
     uint8_t* xs;
@@ -112,13 +113,9 @@ __device__ __forceinline__ void plan_place(const PrepareArgs& a, int chunk, uint
         if (e <= E) {
             cur[e] += first;
             if (chunk == 0) {
-                a.plan.offsets[e] = first;
-                a.plan.first_tile[e] = ftile;
-                for (uint32_t u = 0; u < nt; ++u) a.plan.tile_group[ftile + u] = (uint32_t)e;
-                if (e == E) {
-                    a.plan.offsets[E + 1] = first + n;
-                    a.plan.first_tile[E + 1] = ftile + nt;
-                }
+                for (uint32_t u = 0; u < nt; ++u)
+                    a.plan.tiles[ftile + u] = Mx4Tile{(uint32_t)e, ftile, nt, first, n, {0, 0, 0}};
+                if (e == E) *a.plan.total = ftile + nt;
             }
         }
         __syncthreads();
@@ -136,19 +133,11 @@ __device__ __forceinline__ void plan_place(const PrepareArgs& a, int chunk, uint
         if (r0 + c * THREADS < a.R) a.plan.perm[at[c]] = (uint32_t)(r0 + c * THREADS);
 }
 
-// n / row_words for n < 2^32: the high word of a product and two shifts (Granlund and Montgomery's division by an
-// invariant, the multiplier from the host); a 64-bit division beyond.
-__device__ __forceinline__ int64_t row_of(const PrepareArgs& a, int64_t n) {
-    if (!a.div_mul) return n / a.row_words;
-    const uint32_t u = (uint32_t)n, h = __umulhi(u, a.div_mul);
-    return (h + ((u - h) >> 1)) >> a.div_shift;
-}
-
 template <int DT>
 __device__ __forceinline__ void activation(const PrepareArgs& a, int64_t wid) {
     const bool live = wid < a.words;                 // whole blocks of 4 lanes are live or not
     const int64_t w0 = live ? wid : 0;
-    const int64_t row = row_of(a, w0);
+    const int64_t row = a.wide ? w0 / a.row_words : (int64_t)a.by_row((uint32_t)w0);
     const uint32_t col = (uint32_t)(w0 - row * a.row_words);
     uint32_t byte, word;
     if (a.swiglu) {
@@ -208,7 +197,7 @@ __global__ void __launch_bounds__(256) pad_scales_kernel(const uint8_t* __restri
 
 size_t mx4_plan_bytes(int64_t R, int64_t E) {
     const int64_t chunks = (R + PLAN_CHUNK - 1) / PLAN_CHUNK;
-    return (size_t)(2 * (E + 2) + (R / kPlanMinTile + E + 1) + R + chunks * (E + 1)) * sizeof(uint32_t);
+    return (size_t)(R / kPlanMinTile + E + 1) * sizeof(Mx4Tile) + (size_t)(1 + R + chunks * (E + 1)) * sizeof(uint32_t);
 }
 
 hipError_t launch_mx4_prepare(const Mx4Prepare& q, Mx4Plan* plan, hipStream_t st) {
@@ -216,12 +205,8 @@ hipError_t launch_mx4_prepare(const Mx4Prepare& q, Mx4Plan* plan, hipStream_t st
     a.x = q.x;
     a.words = q.x ? q.rows * (q.K / 8) : 0;
     a.row_words = (uint32_t)(q.K / 8);
-    if (a.words < (1LL << 32) && a.row_words > 1) {
-        uint32_t l = 0;                              // ceil(log2 row_words)
-        while ((1ull << l) < a.row_words) ++l;
-        a.div_mul = (uint32_t)((((1ull << l) - a.row_words) << 32) / a.row_words + 1);
-        a.div_shift = l - 1;
-    }
+    a.by_row = FastDiv::by(a.row_words);
+    a.wide = a.words >= (1LL << 32);
     a.swiglu = q.swiglu;
     a.vec = ((uintptr_t)q.x & 15) == 0;              // rows are whole multiples of 64 bytes
     a.xq = q.xq;
@@ -238,11 +223,9 @@ hipError_t launch_mx4_prepare(const Mx4Prepare& q, Mx4Plan* plan, hipStream_t st
         a.E = (int)E;
         a.chunks = (int)((R + PLAN_CHUNK - 1) / PLAN_CHUNK);
         a.tile_rows = q.tile_rows;
-        uint32_t* w = (uint32_t*)q.plan;
-        a.plan.offsets = w;
-        a.plan.first_tile = w + (E + 2);
-        a.plan.tile_group = w + 2 * (E + 2);
-        a.plan.perm = a.plan.tile_group + (R / kPlanMinTile + E + 1);
+        a.plan.tiles = (Mx4Tile*)q.plan;
+        a.plan.total = (uint32_t*)(a.plan.tiles + (R / kPlanMinTile + E + 1));
+        a.plan.perm = a.plan.total + 1;
         a.plan.counts = a.plan.perm + R;
         *plan = a.plan;
         blocks += a.chunks;
