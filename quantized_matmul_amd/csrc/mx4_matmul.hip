@@ -100,7 +100,15 @@ struct Piece {
     uint32_t s;
 };
 
-// Lane piece of run `run` of a row whose piece of run 0 starts at c and s; `left` blocks of it exist.
+// Lane piece of whole run `run` of a row whose piece of run 0 starts at c and s.
+__device__ __forceinline__ Piece load_piece(const uint8_t* c, const uint8_t* s, int run) {
+    Piece p;
+    __builtin_memcpy(&p.s, s + run * 16, 4);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) p.c[b] = *(const u32x4*)(c + (int64_t)run * 256 + 16 * b);
+    return p;
+}
+// The same of a run of which the piece has `left` blocks; the others are zeros.
 __device__ __forceinline__ Piece load_piece(const uint8_t* c, const uint8_t* s, int run, int left) {
     Piece p;
     p.s = scale4(s + run * 16, left);
@@ -118,7 +126,8 @@ __global__ void __launch_bounds__(64 * STREAM_WAVES) mx4_stream_kernel(StreamArg
     constexpr int XR = DIRECT ? 1 : STREAM_FLOAT_ROWS;
     extern __shared__ __align__(16) uint32_t lds[];     // partial sums [waves][16][16]; codes of a float x
     const Mx4Args& a = s.a;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, waves = blockDim.x >> 6;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i = lane & 15, q = lane >> 4;
     const uint32_t tile = DIRECT ? blockIdx.x / (uint32_t)s.tiles_n : 0;
     const int64_t n0 = (int64_t)(blockIdx.x - tile * (uint32_t)s.tiles_n) * 16;
@@ -133,15 +142,15 @@ __global__ void __launch_bounds__(64 * STREAM_WAVES) mx4_stream_kernel(StreamArg
         const int64_t n = (int64_t)expert * a.N + (n0 + i < a.N ? n0 + i : a.N - 1);   // rows past N are not stored
         const uint8_t* const wp = a.wq + n * half + 64 * q;
         const uint8_t* const wsp = a.ws + n * a.wsstride + 4 * q;
-        const int64_t xrow = src + (i < rows ? i : 0);
-        const int runs = (KB + 15) / 16;
-        Piece w = load_piece(wp, wsp, wave, KB - wave * 16 - 4 * q);
-        for (int run = wave; run < runs; run += waves) {
-            const int left = KB - run * 16 - 4 * q;
-            Piece next = w;
-            if (run + waves < runs) next = load_piece(wp, wsp, run + waves, left - 16 * waves);
-            Piece x;
-            if constexpr (FLOAT) {
+        const int64_t xrow = src + (i < rows ? i : 0);  // columns past the rows repeat the first and are not stored
+        const int whole = KB / 16;                      // whole runs; one more of KB % 16 blocks
+        const uint8_t* const xp = a.xq + xrow * half + 64 * q;
+        const uint8_t* const xsp = a.xs + xrow * a.xsstride + 4 * q;
+        // x's piece of a run: from its codes, or rounded here
+        auto x_piece = [&](int run) {
+            if constexpr (!FLOAT) {
+                return load_piece(xp, xsp, run);
+            } else {
                 // lane l rounds values 8 l .. 8 l + 7 of the run, a row at a time; the wave's own LDS
                 // turns words into pieces
                 uint32_t* const words = lds + waves * 256 + wave * XR * 68;      // [XR][64] words, [XR][4] scales
@@ -163,21 +172,40 @@ __global__ void __launch_bounds__(64 * STREAM_WAVES) mx4_stream_kernel(StreamArg
                 }
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
                 const int r = i < rows ? i : 0;
+                Piece x;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const u32x4 v = *(const u32x4*)(words + r * 64 + 16 * q + 4 * b);
-                    x.c[b] = i < rows ? v : u32x4{0, 0, 0, 0};
-                }
-                x.s = i < rows ? *(const uint32_t*)(bytes + r * 16 + 4 * q) : ONES;
+                for (int b = 0; b < 4; ++b) x.c[b] = *(const u32x4*)(words + r * 64 + 16 * q + 4 * b);
+                x.s = *(const uint32_t*)(bytes + r * 16 + 4 * q);
                 __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            } else {
-                x = load_piece(a.xq + xrow * half + 64 * q, a.xs + xrow * a.xsstride + 4 * q, run, i < rows ? left : 0);
+                return x;
             }
+        };
+        auto multiply = [&](const Piece& w, const Piece& x) {
             acc = mfma16<0>(w.c[0], x.c[0], acc, w.s, x.s);
             acc = mfma16<1>(w.c[1], x.c[1], acc, w.s, x.s);
             acc = mfma16<2>(w.c[2], x.c[2], acc, w.s, x.s);
             acc = mfma16<3>(w.c[3], x.c[3], acc, w.s, x.s);
-            w = next;
+        };
+        // two runs at a time, both pieces of W on their way before x is looked at (an odd last one loads twice)
+        for (int run = wave; run < whole; run += 2 * waves) {
+            const bool two = run + waves < whole;
+            const Piece w0 = load_piece(wp, wsp, run), w1 = load_piece(wp, wsp, two ? run + waves : run);
+            if constexpr (FLOAT) {
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(w0, x_piece(run));
+                if (two) multiply(w1, x_piece(run + waves));
+            } else {
+                const Piece x0 = x_piece(run), x1 = x_piece(two ? run + waves : run);
+                __builtin_amdgcn_sched_barrier(0);
+                multiply(w0, x0);
+                if (two) multiply(w1, x1);
+            }
+        }
+        if (KB % 16 && whole % waves == wave) {
+            const int left = KB - whole * 16 - 4 * q;
+            const Piece w = load_piece(wp, wsp, whole, left);
+            if constexpr (FLOAT) multiply(w, x_piece(whole));
+            else multiply(w, load_piece(xp, xsp, whole, left));
         }
     }
     // D[n][m]: n = 4 q + r, m = i
@@ -534,7 +562,9 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
 
 template <int YDT, int XDT, bool DIRECT>
 hipError_t stream_launch(const Mx4Args& a, hipStream_t st) {
-    const int64_t runs = (a.K + 511) / 512;
+    // a wave takes one run, or two where that lets all of W's loads be in flight at once (four waves a SIMD)
+    int64_t runs = (a.K + 511) / 512;
+    if ((DIRECT ? a.M : 1) * ((a.N + 15) / 16) * runs > 16 * (int64_t)device_shape().cus) runs = (runs + 1) / 2;
     const int waves = (int)(runs < STREAM_WAVES ? runs : STREAM_WAVES);
     StreamArgs s{a, DIRECT ? (uint32_t)(a.M / a.B) : 1, (int)((a.N + 15) / 16), ((uintptr_t)a.x & 15) == 0};
     const int64_t blocks = (DIRECT ? a.M : 1) * s.tiles_n;
