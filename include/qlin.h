@@ -379,8 +379,8 @@ qlin_status qlin_gather_mxfp4_matmul(const void* x, qlin_dtype x_dtype, const vo
  * qlin_moe_combine -- y[t] = sum over j of weights[t, j] * h[t, j].
  *   h        [T, k, D] of dtype (QLIN_F32, QLIN_F16 or QLIN_BF16).
  *   weights  fp32 [T, k].
- *   experts  int32 [T, k] or NULL; a place with a negative entry is left out
- *            (its row of h is not read).
+ *   experts  int32 [T, k] or NULL; a place with a negative entry is left out,
+ *            whatever its row of h holds.
  *   y        out, [T, D] of dtype; fp32 sums in the order of j, one rounding.
  * T == 0 is a no-op.
  */

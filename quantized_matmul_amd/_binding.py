@@ -459,8 +459,8 @@ def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", bias: Option
             raise ValueError(f"bias must hold one value per expert ({E})")
     T = logits.numel() // E if E else 0
     shape = (*shape[:-1], max(k, 0))
-    weights = torch.empty(shape, dtype=torch.float32, device=dev)
-    experts = torch.empty(shape, dtype=torch.int32, device=dev)
+    weights = torch.empty(*shape, dtype=torch.float32, device=dev)
+    experts = torch.empty(*shape, dtype=torch.int32, device=dev)
     _check(lib.qlin_moe_route(logits.data_ptr(), code, T, E, k, None if bias is None else bias.data_ptr(),
                               score.encode(), renormalize, scale, groups, groups_kept, group_top,
                               weights.data_ptr(), experts.data_ptr(), _stream(dev)))
@@ -551,7 +551,7 @@ def mxfp4_matmul(x, qw: QuantizedWeight, activation: Optional[str] = None,
     M = t.numel() // t.shape[-1]
     if out_dtype is not None:
         dtype = out_dtype
-    y = _out(out, (*t.shape[:-1], N), dtype, dev)
+    y = torch.empty(*t.shape[:-1], N, dtype=dtype, device=dev) if out is None else _out(out, (*t.shape[:-1], N), dtype, dev)
     keep, ws, ws_bytes = _workspace(workspace, lib.qlin_mxfp4_matmul_workspace_bytes(M, K, N, code), dev)
     _check(lib.qlin_mxfp4_matmul(t.data_ptr(), code, None if scales is None else scales.data_ptr(),
                                  activation.encode() if activation else None, M, K, qw.value.data_ptr(),
@@ -584,7 +584,7 @@ def gather_mxfp4_matmul(x, qw: QuantizedWeight, experts: torch.Tensor, activatio
     B, R, E = t.shape[0], experts.numel(), qw.value.shape[0]
     if out_dtype is not None:
         dtype = out_dtype
-    y = _out(out, (*experts.shape, N), dtype, dev)
+    y = torch.empty(*experts.shape, N, dtype=dtype, device=dev) if out is None else _out(out, (*experts.shape, N), dtype, dev)
     keep, ws, ws_bytes = _workspace(
         workspace, lib.qlin_gather_mxfp4_matmul_workspace_bytes(B, R, K, E, N, code), dev)
     _check(lib.qlin_gather_mxfp4_matmul(t.data_ptr(), code, None if scales is None else scales.data_ptr(),
@@ -614,7 +614,7 @@ def moe_combine(h: torch.Tensor, weights: torch.Tensor, experts: Optional[torch.
     places with a negative expert left out."""
     lib = _lib or load_library()
     dev, code, T, k, D, ids = _combine_operands(h, weights, experts)
-    y = _out(out, (*h.shape[:-2], D), h.dtype, dev)
+    y = torch.empty(*h.shape[:-2], D, dtype=h.dtype, device=dev) if out is None else _out(out, (*h.shape[:-2], D), h.dtype, dev)
     _check(lib.qlin_moe_combine(h.data_ptr(), code, T, k, D, weights.data_ptr(), ids, y.data_ptr(),
                                 _stream(dev)))
     return y

@@ -4,12 +4,14 @@
 //   dh[t, j] = w[t, j] dy[t]
 //   dw[t, j] = sum_d dy[t, d] h[t, j, d]
 //
-// Places whose expert is negative (dropped by the router) are left out: their
-// rows of h are not read, dh and dw get zeros. Sums are fp32 in a fixed order;
-// each output is rounded once.
+// Places whose expert is negative (dropped by the router) are left out: what
+// their rows of h hold does not matter, dh and dw get zeros. Sums are fp32 in a
+// fixed order; each output is rounded once. Both kernels are bound by HBM, and
+// by one round trip where there are few tokens: so all rows of a token are on
+// their way before any is used.
 
 #include "qlin_common.h"
-#include "moe_common.h"
+#include "mx4_common.h"
 
 namespace qlin {
 namespace {
@@ -61,28 +63,44 @@ struct CombineArgs {
     const void* gy;
     void* gh;
     float* gw;
+    FastDiv by_row;          // thread / threads of a token
+    int wide;                // 2^32 threads or more: 64-bit division
 };
 
 constexpr int COMBINE_THREADS = 256;
 
-// Each thread owns VEC consecutive outputs of one token.
-template <int DT, int VEC>
+// Each thread owns VEC consecutive outputs of one token and has KC rows of h in
+// flight; places past k read the token's first row again and count nothing, so
+// that no branch stands between the loads.
+template <int DT, int VEC, int KC>
 __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(CombineArgs a) {
     const int64_t per = a.D / VEC;
     const int64_t i = (int64_t)blockIdx.x * COMBINE_THREADS + threadIdx.x;
     if (i >= a.T * per) return;
-    const int64_t t = i / per, d = (i - t * per) * VEC;
+    const int64_t t = a.wide ? i / per : (int64_t)a.by_row((uint32_t)i), d = (i - t * per) * VEC;
+    const float* const w = a.w + t * a.k;
+    const int32_t* const e = (a.experts ? a.experts : (const int32_t*)a.w) + t * a.k;
+    const int64_t h = t * a.k * a.D + d;
     float acc[VEC];
 #pragma unroll
     for (int c = 0; c < VEC; ++c) acc[c] = 0.0f;
-    for (int j = 0; j < a.k; ++j) {
-        const int64_t r = t * a.k + j;
-        if (a.experts && a.experts[r] < 0) continue;
-        const float w = a.w[r];
-        float v[VEC];
-        load_v<DT, VEC>(a.h, r * a.D + d, v);
+    for (int j0 = 0; j0 < a.k; j0 += KC) {
+        float v[KC][VEC], wj[KC];
+        int32_t ej[KC];
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) acc[c] += w * v[c];
+        for (int q = 0; q < KC; ++q) {
+            const int j = j0 + q < a.k ? j0 + q : 0;
+            load_v<DT, VEC>(a.h, h + (int64_t)j * a.D, v[q]);
+            wj[q] = w[j];
+            ej[q] = e[j];
+        }
+#pragma unroll
+        for (int q = 0; q < KC; ++q) {
+            const bool live = j0 + q < a.k && (!a.experts || ej[q] >= 0);
+            const float f = live ? wj[q] : 0.0f;
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) acc[c] += f * (live ? v[q][c] : 0.0f);
+        }
     }
     store_v<DT, VEC>(a.y, t * a.D + d, acc);
 }
@@ -93,7 +111,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_grad_kernel(CombineAr
     const int lane = threadIdx.x & 63;
     const int64_t r = (int64_t)blockIdx.x * (COMBINE_THREADS / 64) + (threadIdx.x >> 6);
     if (r >= a.T * a.k) return;
-    const int64_t t = r / a.k;
+    const int64_t t = a.wide ? r / a.k : (int64_t)a.by_row((uint32_t)r);
     const bool dead = a.experts && a.experts[r] < 0;
     const float w = dead ? 0.0f : a.w[r];
     float sum = 0.0f;
@@ -123,16 +141,23 @@ bool wide(int dt, int64_t D, const void* a, const void* b, const void* c) {
 }
 
 template <int DT, int WIDE>
-void run_combine(const CombineArgs& a, bool vec, hipStream_t st) {
-    const int64_t n = a.T * (vec ? a.D / WIDE : a.D);
+void run_combine(CombineArgs a, bool vec, hipStream_t st) {
+    const int64_t per = vec ? a.D / WIDE : a.D, n = a.T * per;
+    a.by_row = FastDiv::by((uint32_t)per);
+    a.wide = n >= (1LL << 32);
     const unsigned grid = (unsigned)((n + COMBINE_THREADS - 1) / COMBINE_THREADS);
-    if (vec) combine_kernel<DT, WIDE><<<grid, COMBINE_THREADS, 0, st>>>(a);
-    else combine_kernel<DT, 1><<<grid, COMBINE_THREADS, 0, st>>>(a);
+    if (!vec) combine_kernel<DT, 1, 8><<<grid, COMBINE_THREADS, 0, st>>>(a);
+    else if (a.k <= 2) combine_kernel<DT, WIDE, 2><<<grid, COMBINE_THREADS, 0, st>>>(a);
+    else if (a.k <= 4) combine_kernel<DT, WIDE, 4><<<grid, COMBINE_THREADS, 0, st>>>(a);
+    else if (a.k <= 6) combine_kernel<DT, WIDE, 6><<<grid, COMBINE_THREADS, 0, st>>>(a);
+    else combine_kernel<DT, WIDE, 8><<<grid, COMBINE_THREADS, 0, st>>>(a);
 }
 
 template <int DT, int WIDE>
-void run_combine_grad(const CombineArgs& a, bool vec, hipStream_t st) {
+void run_combine_grad(CombineArgs a, bool vec, hipStream_t st) {
     const int64_t rows = a.T * a.k;
+    a.by_row = FastDiv::by((uint32_t)a.k);
+    a.wide = rows >= (1LL << 32);
     const unsigned grid = (unsigned)((rows + COMBINE_THREADS / 64 - 1) / (COMBINE_THREADS / 64));
     if (vec) combine_grad_kernel<DT, WIDE><<<grid, COMBINE_THREADS, 0, st>>>(a);
     else combine_grad_kernel<DT, 1><<<grid, COMBINE_THREADS, 0, st>>>(a);
