@@ -156,45 +156,46 @@ qlin_status product(const void* x, int x_dtype, const void* x_scales, const char
     const bool quantized = !codes && c.path != qlin::Mx4Path::kStreamFloat;
     qlin::Mx4Plan plan{};
     hipError_t e;
-    if (quantized || (gather && tiled && !odd)) {
-        qlin::Mx4Prepare q{};
-        q.dt = x_dtype;
-        q.K = K;
-        if (quantized) {
-            q.x = x;
-            q.rows = rows;
-            q.swiglu = swiglu;
-            q.xq = (uint32_t*)(w + l.xq);
-            q.xs = (uint8_t*)(w + l.xs);
-            q.sstride = stride;
-            a.xq = (const uint8_t*)(w + l.xq);
-            a.xs = (const uint8_t*)(w + l.xs);
-            a.xsstride = stride;
-        }
-        if (gather && tiled && !odd) {
-            q.experts = experts;
-            q.R = R;
-            q.E = E;
-            q.tile_rows = c.tile_rows;
-            q.plan = w + l.plan;
-        }
-        if ((e = qlin::launch_mx4_prepare(q, &plan, st)) != hipSuccess) return device_status(e, what);
+    qlin::Mx4Prepare q{};
+    q.dt = x_dtype;
+    q.K = K;
+    bool prepare = false;
+    if (quantized) {
+        prepare = true;
+        q.x = x;
+        q.rows = rows;
+        q.swiglu = swiglu;
+        q.xq = (uint32_t*)(w + l.xq);
+        q.xs = (uint8_t*)(w + l.xs);
+        q.sstride = stride;
+        a.xq = (const uint8_t*)(w + l.xq);
+        a.xs = (const uint8_t*)(w + l.xs);
+        a.xsstride = stride;
+    }
+    if (gather && tiled && !odd) {
+        prepare = true;
+        q.experts = experts;
+        q.R = R;
+        q.E = E;
+        q.tile_rows = c.tile_rows;
+        q.plan = w + l.plan;
     }
     if (tiled && !odd) {
         // the tiled kernel reads scale rows 16 bytes at a time
-        if (codes && (KS % 16 || (uintptr_t)x_scales % 16)) {
-            e = qlin::launch_mx4_pad_scales(a.xs, rows, KS, (uint8_t*)(w + l.xs), stride, st);
-            if (e != hipSuccess) return device_status(e, what);
-            a.xs = (const uint8_t*)(w + l.xs);
-            a.xsstride = stride;
-        }
         if (KS % 16) {
-            e = qlin::launch_mx4_pad_scales(a.ws, E * N, KS, (uint8_t*)(w + l.ws), stride, st);
-            if (e != hipSuccess) return device_status(e, what);
+            prepare = true;
+            q.pad[0] = {a.ws, E * N, KS, (uint8_t*)(w + l.ws)};
             a.ws = (const uint8_t*)(w + l.ws);
             a.wsstride = stride;
         }
+        if (codes && (KS % 16 || (uintptr_t)x_scales % 16)) {
+            prepare = true;
+            q.pad[1] = {a.xs, rows, KS, (uint8_t*)(w + l.xs)};
+            a.xs = (const uint8_t*)(w + l.xs);
+            a.xsstride = stride;
+        }
     }
+    if (prepare && (e = qlin::launch_mx4_prepare(q, &plan, st)) != hipSuccess) return device_status(e, what);
     e = odd ? qlin::launch_mx4_stream_blocks(a, st) : qlin::launch_mx4_matmul(a, c, &plan, st);
     if (e == hipSuccess)
         qlin::record_path(tiled && !odd ? (gather ? "mxfp4_gather_tiled" : "mxfp4_tiled")

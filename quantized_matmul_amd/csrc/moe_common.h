@@ -105,9 +105,16 @@ hipError_t launch_mx4_matmul(const Mx4Args& a, const Mx4Choice& c, const struct 
 // The streaming kernel on x's codes for any number of rows: blocks of 16 (by experts: one row each).
 hipError_t launch_mx4_stream_blocks(const Mx4Args& a, hipStream_t st);
 
+// Scale rows of KS bytes to copy to rows of whole 16-byte units, filled with 127.
+struct Mx4Scales {
+    const uint8_t* from;
+    int64_t rows, KS;
+    uint8_t* to;              // null: none
+};
+
 // x's codes and scale rows `sstride` bytes apart (bytes past K / 32 get 127) from a
-// float x [rows, K] (swiglu: [rows, 2K]), unless x is null, and the row plan for
-// R experts, unless experts is null.
+// float x [rows, K] (swiglu: [rows, 2K]), unless x is null; the row plan for
+// R experts, unless experts is null; scale rows to lay out.
 struct Mx4Prepare {
     const void* x;
     int dt;
@@ -120,11 +127,9 @@ struct Mx4Prepare {
     int64_t R, E;
     int tile_rows;
     void* plan;               // mx4_plan_bytes(R, E)
+    Mx4Scales pad[2];
 };
 size_t mx4_plan_bytes(int64_t R, int64_t E);
 hipError_t launch_mx4_prepare(const Mx4Prepare& q, struct Mx4Plan* plan, hipStream_t st);
-// Copies scale rows of KS bytes to rows `stride` bytes apart, filled with 127.
-hipError_t launch_mx4_pad_scales(const uint8_t* s, int64_t rows, int64_t KS, uint8_t* out, int64_t stride,
-                                 hipStream_t st);
 
 }  // namespace qlin

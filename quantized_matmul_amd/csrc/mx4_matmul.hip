@@ -229,7 +229,6 @@ struct TiledArgs {
     int tiles_n;
     int xcds;
     int lds_nan;
-    int wide;          // outputs can be stored 16 bytes at a time
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
@@ -535,22 +534,19 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
                 store4<YDT>(ot + i * OROW, 32 * tn + 8 * g + 4 * j, c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]);
             }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (p.wide) {
 #pragma unroll 4
-            for (int r = lane / LPR; r < 32; r += 64 / LPR) {
-                const int c = (lane % LPR) * PER, n = nw0 + c;
-                if (mb + r >= rows || n >= a.N) continue;      // N is a multiple of PER
-                const int64_t dst = GATHER ? (int64_t)p.plan.perm[m0 + mb + r] : m0 + mb + r;
-                *(u32x4*)((unsigned char*)a.y + (dst * a.N + n) * YS) = *(const u32x4*)(ot + r * OROW + c * YS);
-            }
-        } else {
-            for (int r = 0; r < 32; ++r) {
-                if (mb + r >= rows) break;
-                const int64_t dst = GATHER ? (int64_t)p.plan.perm[m0 + mb + r] : m0 + mb + r;
-                for (int c = lane; c < TN * 32; c += 64) {
-                    if (nw0 + c >= a.N) break;
-                    if constexpr (YS == 4) ((uint32_t*)a.y)[dst * a.N + nw0 + c] = *(const uint32_t*)(ot + r * OROW + c * 4);
-                    else ((uint16_t*)a.y)[dst * a.N + nw0 + c] = *(const uint16_t*)(ot + r * OROW + c * 2);
+        for (int r = lane / LPR; r < 32; r += 64 / LPR) {
+            const int c = (lane % LPR) * PER, n = nw0 + c;
+            if (mb + r >= rows || n >= a.N) continue;
+            const int64_t dst = GATHER ? (int64_t)p.plan.perm[m0 + mb + r] : m0 + mb + r;
+            unsigned char* const to = (unsigned char*)a.y + (dst * a.N + n) * YS;
+            if (n + PER <= a.N) {
+                const u32x4 v = *(const u32x4*)(ot + r * OROW + c * YS);
+                __builtin_memcpy(to, &v, 16);                  // a row of an odd N starts at any element
+            } else {
+                for (int q = 0; n + q < a.N; ++q) {
+                    if constexpr (YS == 4) ((uint32_t*)to)[q] = *(const uint32_t*)(ot + r * OROW + (c + q) * 4);
+                    else ((uint16_t*)to)[q] = *(const uint16_t*)(ot + r * OROW + (c + q) * 2);
                 }
             }
         }
@@ -609,8 +605,7 @@ constexpr int kTileN[kTiles] = {256, 128, 128, 64}, kTileM[kTiles] = {256, 128, 
 
 template <int YDT, bool GATHER>
 hipError_t tiled_rows(const Mx4Args& a, const Mx4Plan& plan, int tile, hipStream_t st) {
-    const TiledArgs p{a, plan, FastDiv::by(GATHER ? (uint32_t)(a.M / a.B) : 1), 0, device_shape().xcds, debug_lds_nan() ? 1 : 0,
-                      a.N % (YDT == QLIN_F32 ? 4 : 8) == 0 && (uintptr_t)a.y % 16 == 0 ? 1 : 0};
+    const TiledArgs p{a, plan, FastDiv::by(GATHER ? (uint32_t)(a.M / a.B) : 1), 0, device_shape().xcds, debug_lds_nan() ? 1 : 0};
     switch (tile) {
     case 0: return tiled_launch<256, 256, 4, 2, 2, 128, YDT, GATHER>(p, st);
     case 1: return tiled_launch<128, 128, 2, 2, 2, 128, YDT, GATHER>(p, st);

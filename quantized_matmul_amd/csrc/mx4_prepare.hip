@@ -1,10 +1,12 @@
 // mx4_prepare.hip -- what an mxfp4 product needs before its tiles can run: the
-// activation's codes and scales, and, by experts, the row plan. Both come from
-// one launch where the rows fit one chunk, so that the plan's round trips hide
-// behind the activation.
+// activation's codes and scales, by experts the row plan, and scale rows in
+// whole 16-byte units where K / 32 is no multiple of 16. All of it comes from
+// one launch where the index rows fit one chunk, so that the plan's round trips
+// hide behind the rest.
 //
 // Activation: one thread per packed word (8 values), 4 lanes per block; bound
 // by HBM.
+// Scale rows: one thread per 16-byte unit.
 // Plan: workgroups of their own at the front of the launch, bound by latency
 // (a few barriers and memory round trips). More than one chunk of rows takes a
 // second launch: first counts per chunk, then each chunk scans all counts for
@@ -31,6 +33,11 @@ struct PrepareArgs {
     uint32_t* xq;
     uint8_t* xs;
     int64_t sstride;
+    int act_blocks;
+    // scale rows to lay out: W's (0) and given codes' (1)
+    Mx4Scales pad[2];
+    FastDiv by_unit;        // 16-byte unit / units of a row
+    int pad_blocks[2];
     // plan
     const int32_t* experts; // null: dense
     int R, E, chunks, tile_rows;
@@ -163,7 +170,26 @@ __device__ __forceinline__ void activation(const PrepareArgs& a, int64_t wid) {
         for (int64_t p = blk + 1; p < a.sstride; ++p) s[p] = 127;
 }
 
-// Workgroups [0, chunks) make the plan (or, with several chunks, its counts), the others the activation.
+// One 16-byte unit of a scale row; bytes past the row are 127.
+__device__ __forceinline__ void pad_unit(const Mx4Scales& p, const FastDiv& by_unit, int64_t u) {
+    const int64_t units = (p.KS + 15) / 16;
+    if (u >= p.rows * units) return;
+    const int64_t row = p.rows * units < (1LL << 32) ? (int64_t)by_unit((uint32_t)u) : u / units;
+    const int64_t c = (u - row * units) * 16;
+    const uint8_t* const from = p.from + row * p.KS + c;
+    uint32_t d[4] = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
+    if (c + 16 <= p.KS) {
+        __builtin_memcpy(d, from, 16);                // rows start at any byte
+    } else {
+        const int left = (int)(p.KS - c);
+#pragma unroll
+        for (int b = 0; b < 16; ++b)
+            if (b < left) d[b / 4] = (d[b / 4] & ~(0xFFu << (8 * (b & 3)))) | (uint32_t)from[b] << (8 * (b & 3));
+    }
+    *(uint4*)(p.to + u * 16) = uint4{d[0], d[1], d[2], d[3]};
+}
+
+// Workgroups in order: the plan (with several chunks, its counts), the activation, scale rows.
 template <int DT>
 __global__ void __launch_bounds__(THREADS) mx4_prepare_kernel(PrepareArgs a) {
     extern __shared__ uint32_t sh[];
@@ -176,21 +202,16 @@ __global__ void __launch_bounds__(THREADS) mx4_prepare_kernel(PrepareArgs a) {
         }
         b -= a.chunks;
     }
-    activation<DT>(a, (int64_t)b * THREADS + threadIdx.x);
+    if (b < a.act_blocks) return activation<DT>(a, (int64_t)b * THREADS + threadIdx.x);
+    b -= a.act_blocks;
+    const int which = b < a.pad_blocks[0] ? 0 : 1;
+    if (which) b -= a.pad_blocks[0];
+    pad_unit(which ? a.pad[1] : a.pad[0], a.by_unit, (int64_t)b * THREADS + threadIdx.x);
 }
 
 __global__ void __launch_bounds__(THREADS) mx4_place_kernel(PrepareArgs a) {
     extern __shared__ uint32_t sh[];
     plan_place(a, blockIdx.x, sh);
-}
-
-__global__ void __launch_bounds__(256) pad_scales_kernel(const uint8_t* __restrict__ s, int64_t n, uint32_t KS,
-                                                         uint8_t* __restrict__ out, uint32_t stride) {
-    const int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (o >= n) return;
-    const int64_t row = o / stride;
-    const uint32_t c = (uint32_t)(o - row * stride);
-    out[o] = c < KS ? s[row * KS + c] : (uint8_t)127;
 }
 
 }  // namespace
@@ -213,6 +234,17 @@ hipError_t launch_mx4_prepare(const Mx4Prepare& q, Mx4Plan* plan, hipStream_t st
     a.xs = q.xs;
     a.sstride = q.sstride;
     int64_t blocks = (a.words + THREADS - 1) / THREADS;
+    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
+    a.act_blocks = (int)blocks;
+    const int64_t units = (q.K / 32 + 15) / 16;
+    a.by_unit = FastDiv::by((uint32_t)units);
+    for (int w = 0; w < 2; ++w) {
+        a.pad[w] = q.pad[w];
+        const int64_t n = q.pad[w].to ? (q.pad[w].rows * units + THREADS - 1) / THREADS : 0;
+        if (n > 0x7fffffffLL) return hipErrorInvalidValue;
+        a.pad_blocks[w] = (int)n;
+        blocks += n;
+    }
     size_t shm = 0;
     if (q.experts) {
         const int64_t R = q.R, E = q.E;
@@ -237,14 +269,6 @@ hipError_t launch_mx4_prepare(const Mx4Prepare& q, Mx4Plan* plan, hipStream_t st
     else if (q.dt == QLIN_F16) mx4_prepare_kernel<QLIN_F16><<<(unsigned)blocks, THREADS, shm, st>>>(a);
     else mx4_prepare_kernel<QLIN_BF16><<<(unsigned)blocks, THREADS, shm, st>>>(a);
     if (a.chunks > 1) mx4_place_kernel<<<(unsigned)a.chunks, THREADS, shm, st>>>(a);
-    return hipGetLastError();
-}
-
-hipError_t launch_mx4_pad_scales(const uint8_t* s, int64_t rows, int64_t KS, uint8_t* out, int64_t stride,
-                                 hipStream_t st) {
-    const int64_t n = rows * stride, grid = (n + 255) / 256;
-    if (grid > 0x7fffffffLL) return hipErrorInvalidValue;
-    pad_scales_kernel<<<(unsigned)grid, 256, 0, st>>>(s, n, (uint32_t)KS, out, (uint32_t)stride);
     return hipGetLastError();
 }
 
