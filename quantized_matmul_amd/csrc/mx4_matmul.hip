@@ -596,12 +596,23 @@ hipError_t tiled_launch(TiledArgs p, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Shapes of the tiled kernel's workgroup: weight rows x activation rows, waves, stages.
-//  0: 256 x 256, 8 waves of 64 x 128: the least LDS and L2 traffic a product; one workgroup a CU.
-//  1: 128 x 128, 4 waves of 64 x 64; two workgroups a CU, so one's outputs leave under the other's products.
-//  2: 128 x 64 and 3: 64 x 64, for few rows: more workgroups and more loads in flight for each byte of W.
+// Shapes of the tiled kernel's workgroup: weight rows x activation rows, how
+// many of it fit a CU, and what a round of them takes, in us: `start` for a
+// tile's first loads and its outputs, `step` for each step of 256 codes with
+// every place of the CU taken, `alone` with one workgroup a CU. Measured at N =
+// K = 8192 and N = 12288, K = 4096 with 128 to 8192 rows.
+//  0: 8 waves of 64 x 128: the least LDS and L2 traffic a product.
+//  1: 4 waves of 64 x 64: one workgroup's outputs leave under the other's products.
+//  2, 3: for few rows: more workgroups and more loads in flight for each byte of W.
 constexpr int kTiles = 4;
-constexpr int kTileN[kTiles] = {256, 128, 128, 64}, kTileM[kTiles] = {256, 128, 64, 64};
+struct TileShape {
+    int n, m, per_cu;
+    float start, step, alone;
+};
+constexpr TileShape kTile[kTiles] = {{256, 256, 1, 9.5f, 1.72f, 1.72f},
+                                     {128, 128, 2, 3.4f, 1.28f, 0.90f},
+                                     {128, 64, 2, 3.0f, 0.78f, 0.38f},
+                                     {64, 64, 2, 2.5f, 0.56f, 0.20f}};
 
 template <int YDT, bool GATHER>
 hipError_t tiled_rows(const Mx4Args& a, const Mx4Plan& plan, int tile, hipStream_t st) {
@@ -633,28 +644,36 @@ int forced_tile() {
 
 }  // namespace
 
-// Dense: up to 16 rows stream. Beyond, the largest tile that still gives every
-// CU one: N = K = 8192, us for 512 / 256 / 128 rows: 128 x 128 30.5 / 28.4 /
-// 25.7, 128 x 64 33 / 17.8 / 16.0, 64 x 64 48 / 21.7 / 12.9.
-// By experts: while index rows are few against the experts, hardly two share
-// one, and each streams its expert's W without a plan. Beyond, the tile goes by
-// the rows an expert has on average, 64 experts [1536, 2048], us for 16 / 64 /
-// 128 / 1024 rows: 256 x 256 42 / 53 / 59 / 189, 128 x 128 33 / 43 / 61 / 223,
-// 128 x 64 31 / 46 / 62 / 271; then by the CUs as above.
+// Dense: up to 16 rows stream. By experts: while index rows are few against the
+// experts, hardly two share one, and each streams its expert's W without a plan.
+// Beyond, the tile whose rounds over the CUs take least. An expert's last row
+// tile is half empty on average, so R rows make R / m + E / 2 tiles, or one an
+// expert if that is more. Against the best of the four tiles, over sizes drawn
+// from the operators' range, the choice is within 10% for nearly all.
 Mx4Choice mx4_choose(int64_t M, int64_t N, int64_t K, int64_t E, bool gather, bool codes) {
     if (gather ? 2 * M <= E : M <= STREAM_ROWS)
         return {codes || (!gather && M > STREAM_FLOAT_ROWS) ? Mx4Path::kStream : Mx4Path::kStreamFloat, -1, 0};
     int tile = forced_tile();
     if (tile < 0) {
-        const int cus = device_shape().cus;
-        tile = !gather || M >= 128 * E ? 0 : M >= 32 * E ? 1 : 2;
-        auto count = [&](int t) {
-            const int64_t m = gather ? M / kTileM[t] + (E < M ? E : M) / 2 + 1 : (M + kTileM[t] - 1) / kTileM[t];
-            return m * ((N + kTileN[t] - 1) / kTileN[t]);
-        };
-        while (tile < kTiles - 1 && count(tile) < cus) ++tile;
+        const int64_t cus = device_shape().cus, steps = (K + 255) / 256;
+        double best = 0;
+        for (int t = 0; t < kTiles; ++t) {
+            const TileShape& s = kTile[t];
+            int64_t m = (M + s.m - 1) / s.m;
+            if (gather) {
+                const int64_t hit = E < M ? E : M;
+                m = M / s.m + hit / 2 > hit ? M / s.m + hit / 2 : hit;
+            }
+            const int64_t tiles = m * ((N + s.n - 1) / s.n), places = cus * s.per_cu, rest = tiles % places;
+            double us = (double)(tiles / places) * (s.start + s.step * steps);
+            if (rest) us += s.start + (rest > cus ? s.step : s.alone) * steps;
+            if (t == 0 || us < best) {
+                best = us;
+                tile = t;
+            }
+        }
     }
-    return {Mx4Path::kTiled, tile, kTileM[tile]};
+    return {Mx4Path::kTiled, tile, kTile[tile].m};
 }
 
 hipError_t launch_mx4_matmul(const Mx4Args& a, const Mx4Choice& c, const Mx4Plan* plan, hipStream_t st) {
