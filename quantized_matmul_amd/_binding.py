@@ -422,6 +422,8 @@ def gather_qmm_noalloc(x: torch.Tensor, qw: QuantizedWeight, rhs_indices: torch.
 
 def _check_tensor(name, t, dev, dtype):
     """t is a contiguous tensor of dtype on dev."""
+    if t.dtype is dtype and t.is_contiguous() and t.device == dev:
+        return
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
     if t.device != dev:
@@ -488,11 +490,11 @@ def moe_route_grad(logits: torch.Tensor, experts: torch.Tensor, grad_weights: to
 
 def _mxfp4_operands(x, qw, activation, dim):
     """Device, x's tensor, scales and type code, y's default dtype, K and N of an mxfp4 product."""
-    value = qw.value
-    if qw.mode != "mxfp4" or not qw.transpose or value.dim() != dim:
+    value, wscales = qw.value, qw.scales
+    shape = value.shape
+    if qw.mode != "mxfp4" or not qw.transpose or len(shape) != dim:
         raise ValueError(f"the weight must be a {dim}-D mxfp4 weight in the [out, in] layout")
-    K, N = value.shape[-1] * 8, value.shape[-2]
-    wide = K
+    K, N = shape[-1] * 8, shape[-2]
     if isinstance(x, QuantizedWeight):
         if x.mode != "mxfp4":
             raise ValueError("a quantized x must be mxfp4")
@@ -505,28 +507,26 @@ def _mxfp4_operands(x, qw, activation, dim):
     else:
         t, scales, code, dtype = x, None, _float_code("x", x), x.dtype
         dev = _dev(t)
-        if activation == "swiglu":
-            wide = 2 * K
+        wide = 2 * K if activation == "swiglu" else K
     _check_tensor("the weight's words", value, dev, torch.int32)
-    _check_tensor("the weight's scales", qw.scales, dev, torch.uint8)
+    _check_tensor("the weight's scales", wscales, dev, torch.uint8)
     if not K or not t.shape or t.shape[-1] != wide:
         raise ValueError(f"x's last dim {t.shape[-1] if t.shape else None} does not match the weight's K={K}"
                          + (" (twice K with swiglu)" if activation == "swiglu" else ""))
-    if qw.scales.numel() * 4 != value.numel():
+    if wscales.numel() * 4 != value.numel():
         raise ValueError("the weight's scales do not fit its words")
     return dev, t, scales, code, dtype, K, N
 
 
 def _workspace(workspace, need, dev):
-    """(address, bytes) of the given workspace, or of a new one; the tensor keeps it alive."""
+    """(tensor, address, bytes) of the given workspace, or of a new one; the tensor keeps it alive."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    else:
-        _dev(workspace)
-        if workspace.device != dev:
-            raise ValueError(f"workspace must be on {dev}")
-    if workspace is None:
-        return None, None, 0
+        if not need:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        return workspace, workspace.data_ptr(), need
+    if _dev(workspace) != dev:
+        raise ValueError(f"workspace must be on {dev}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
