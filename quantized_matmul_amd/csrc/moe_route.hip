@@ -259,6 +259,18 @@ constexpr Sorter sorter(int n) {
     return s;
 }
 
+// Larger and smaller of two finite numbers, one instruction each.
+__device__ __forceinline__ double max_f64(double a, double b) {
+    double r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+__device__ __forceinline__ double min_f64(double a, double b) {
+    double r;
+    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+
 // LDS of a wave, in words: the chosen experts of its tokens; then each lane's
 // sorted keys and places (the first is in registers), or the row of a group
 // choice (used before them).
@@ -331,20 +343,27 @@ __global__ void __launch_bounds__(64 * ROUTE_WAVES) route_kernel(RouteArgs a) {
     // ones the first lane's; that lane notes it and takes its next.
     uint32_t head = key[0], place = 0;
     if constexpr (V > 1) {
-        uint64_t kp[V];
+        // key and place as one positive fp64 number of the same order (bits 2^60 + 256 key + V - 1 - place, all
+        // of one exponent), so that a comparison of the network is a maximum and a minimum
+        double kp[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) kp[v] = (uint64_t)key[v] << 32 | (uint32_t)(V - 1 - v);
+        for (int v = 0; v < V; ++v)
+            kp[v] = __hiloint2double((int)(0x10000000u | key[v] >> 24), (int)(key[v] << 8 | (uint32_t)(V - 1 - v)));
         constexpr Sorter net = sorter(V);
 #pragma unroll
         for (int c = 0; c < net.n; ++c) {
-            const uint64_t p = kp[net.a[c]], q = kp[net.b[c]];
-            kp[net.a[c]] = p < q ? q : p;
-            kp[net.b[c]] = p < q ? p : q;
+            const double p = kp[net.a[c]], q = kp[net.b[c]];
+            kp[net.a[c]] = max_f64(p, q);
+            kp[net.b[c]] = min_f64(p, q);
         }
+        auto entry = [&](int v) {
+            const uint32_t hi = (uint32_t)__double2hiint(kp[v]), lo = (uint32_t)__double2loint(kp[v]);
+            return uint2{hi << 24 | lo >> 8, (uint32_t)(V - 1) - (lo & 255u)};
+        };
 #pragma unroll
-        for (int v = 1; v < V; ++v) list[64 * v] = uint2{(uint32_t)(kp[v] >> 32), (uint32_t)(V - 1) - (uint32_t)kp[v]};
-        head = (uint32_t)(kp[0] >> 32);
-        place = (uint32_t)(V - 1) - (uint32_t)kp[0];
+        for (int v = 1; v < V; ++v) list[64 * v] = entry(v);
+        head = entry(0).x;
+        place = entry(0).y;
     }
     for (int j = row; j < a.k; j += L) chosen[j] = 0xFFFFFFFFu;
     int taken = 0;
