@@ -346,7 +346,8 @@ qlin_status qlin_moe_route_grad(const void* logits, qlin_dtype dtype, int64_t T,
  *             NULL where that is 0).
  *   y         out, [M, N] of y_dtype (QLIN_F32, QLIN_F16 or QLIN_BF16).
  * K must be a multiple of 32 (at most 2^22); x words and wq 16-byte aligned.
- * M == 0 is a no-op.
+ * M == 0 is a no-op. Products of more output tiles than one launch holds
+ * (none below 2^26 columns and 2^35 outputs) are QLIN_ERR_UNSUPPORTED.
  */
 size_t qlin_mxfp4_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N, qlin_dtype x_dtype);
 qlin_status qlin_mxfp4_matmul(const void* x, qlin_dtype x_dtype, const void* x_scales,

@@ -125,9 +125,11 @@ qlin_status product(const void* x, int x_dtype, const void* x_scales, const char
     const bool tiled = c.path == qlin::Mx4Path::kTiled;
     if (gather && tiled && rows * (K / 2) >= (1LL << 31))
         return fail(QLIN_ERR_UNSUPPORTED, "x has more than 2^32 values: split its rows over several calls");
-    const Layout l = layout(c, rows, R, K, E, N, codes, gather);
     // W's scales, whole 16-byte rows at an address that is none: the streaming kernel takes any
     const bool odd = tiled && (K / 32) % 16 == 0 && (uintptr_t)scales % 16;
+    if (!qlin::mx4_fits(R, N, K, E, gather, odd ? qlin::Mx4Choice{qlin::Mx4Path::kStream, -1, 0} : c))
+        return fail(QLIN_ERR_UNSUPPORTED, "more output tiles than one launch holds: split the rows over several calls");
+    const Layout l = layout(c, rows, R, K, E, N, codes, gather);
     if (l.bytes) {
         if (!workspace || workspace_bytes < l.bytes)
             return fail(QLIN_ERR_INVALID_ARGUMENT, "workspace of %zu bytes needed (got %zu)", l.bytes,

@@ -63,8 +63,9 @@ struct CombineArgs {
     const void* gy;
     void* gh;
     float* gw;
-    FastDiv by_row;          // thread / threads of a token
-    int wide;                // 2^32 threads or more: 64-bit division
+    int64_t first;           // first token (gradient: row) of the launch; the launch ends before `end`
+    int64_t end;
+    FastDiv by_row;          // thread / threads of a token (gradient: row / k)
 };
 
 constexpr int COMBINE_THREADS = 256;
@@ -75,9 +76,9 @@ constexpr int COMBINE_THREADS = 256;
 template <int DT, int VEC, int KC>
 __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(CombineArgs a) {
     const int64_t per = a.D / VEC;
-    const int64_t i = (int64_t)blockIdx.x * COMBINE_THREADS + threadIdx.x;
-    if (i >= a.T * per) return;
-    const int64_t t = a.wide ? i / per : (int64_t)a.by_row((uint32_t)i), d = (i - t * per) * VEC;
+    const uint32_t i = blockIdx.x * COMBINE_THREADS + threadIdx.x, own = a.by_row(i);
+    const int64_t t = a.first + own, d = (i - own * per) * VEC;
+    if (t >= a.end) return;
     const float* const w = a.w + t * a.k;
     const int32_t* const e = (a.experts ? a.experts : (const int32_t*)a.w) + t * a.k;
     const int64_t h = t * a.k * a.D + d;
@@ -109,9 +110,9 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(CombineArgs a)
 template <int DT, int VEC>
 __global__ void __launch_bounds__(COMBINE_THREADS) combine_grad_kernel(CombineArgs a) {
     const int lane = threadIdx.x & 63;
-    const int64_t r = (int64_t)blockIdx.x * (COMBINE_THREADS / 64) + (threadIdx.x >> 6);
-    if (r >= a.T * a.k) return;
-    const int64_t t = a.wide ? r / a.k : (int64_t)a.by_row((uint32_t)r);
+    const int64_t r = a.first + (int64_t)blockIdx.x * (COMBINE_THREADS / 64) + (threadIdx.x >> 6);
+    if (r >= a.end) return;
+    const int64_t t = a.by_row((uint32_t)r);      // rows are below 2^31
     const bool dead = a.experts && a.experts[r] < 0;
     const float w = dead ? 0.0f : a.w[r];
     float sum = 0.0f;
@@ -142,25 +143,29 @@ bool wide(int dt, int64_t D, const void* a, const void* b, const void* c) {
 
 template <int DT, int WIDE>
 void run_combine(CombineArgs a, bool vec, hipStream_t st) {
-    const int64_t per = vec ? a.D / WIDE : a.D, n = a.T * per;
+    const int64_t per = vec ? a.D / WIDE : a.D, most = kLaunchItems / per;   // threads of a token; tokens of a launch
     a.by_row = FastDiv::by((uint32_t)per);
-    a.wide = n >= (1LL << 32);
-    const unsigned grid = (unsigned)((n + COMBINE_THREADS - 1) / COMBINE_THREADS);
-    if (!vec) combine_kernel<DT, 1, 8><<<grid, COMBINE_THREADS, 0, st>>>(a);
-    else if (a.k <= 2) combine_kernel<DT, WIDE, 2><<<grid, COMBINE_THREADS, 0, st>>>(a);
-    else if (a.k <= 4) combine_kernel<DT, WIDE, 4><<<grid, COMBINE_THREADS, 0, st>>>(a);
-    else if (a.k <= 6) combine_kernel<DT, WIDE, 6><<<grid, COMBINE_THREADS, 0, st>>>(a);
-    else combine_kernel<DT, WIDE, 8><<<grid, COMBINE_THREADS, 0, st>>>(a);
+    for (a.first = 0; a.first < a.T; a.first = a.end) {
+        a.end = a.T - a.first < most ? a.T : a.first + most;
+        const unsigned grid = (unsigned)(((a.end - a.first) * per + COMBINE_THREADS - 1) / COMBINE_THREADS);
+        if (!vec) combine_kernel<DT, 1, 8><<<grid, COMBINE_THREADS, 0, st>>>(a);
+        else if (a.k <= 2) combine_kernel<DT, WIDE, 2><<<grid, COMBINE_THREADS, 0, st>>>(a);
+        else if (a.k <= 4) combine_kernel<DT, WIDE, 4><<<grid, COMBINE_THREADS, 0, st>>>(a);
+        else if (a.k <= 6) combine_kernel<DT, WIDE, 6><<<grid, COMBINE_THREADS, 0, st>>>(a);
+        else combine_kernel<DT, WIDE, 8><<<grid, COMBINE_THREADS, 0, st>>>(a);
+    }
 }
 
 template <int DT, int WIDE>
 void run_combine_grad(CombineArgs a, bool vec, hipStream_t st) {
-    const int64_t rows = a.T * a.k;
+    const int64_t rows = a.T * a.k, most = kLaunchItems / 64;
     a.by_row = FastDiv::by((uint32_t)a.k);
-    a.wide = rows >= (1LL << 32);
-    const unsigned grid = (unsigned)((rows + COMBINE_THREADS / 64 - 1) / (COMBINE_THREADS / 64));
-    if (vec) combine_grad_kernel<DT, WIDE><<<grid, COMBINE_THREADS, 0, st>>>(a);
-    else combine_grad_kernel<DT, 1><<<grid, COMBINE_THREADS, 0, st>>>(a);
+    for (a.first = 0; a.first < rows; a.first = a.end) {
+        a.end = rows - a.first < most ? rows : a.first + most;
+        const unsigned grid = (unsigned)((a.end - a.first + COMBINE_THREADS / 64 - 1) / (COMBINE_THREADS / 64));
+        if (vec) combine_grad_kernel<DT, WIDE><<<grid, COMBINE_THREADS, 0, st>>>(a);
+        else combine_grad_kernel<DT, 1><<<grid, COMBINE_THREADS, 0, st>>>(a);
+    }
 }
 
 }  // namespace

@@ -57,6 +57,10 @@ constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxChoice = 64;
 constexpr int kRouteMaxGroups = 64;
 
+// Work-items of one launch at most: a launch of 2^32 or more loses those beyond
+// a multiple of it without an error, so larger work takes several launches.
+constexpr int64_t kLaunchItems = 1LL << 31;
+
 hipError_t launch_moe_route(const void* logits, int dt, int64_t T, int E, int k, const float* bias,
                             int sigmoid, int renorm, float scale, int groups, int kept, int group_top,
                             float* weights, int32_t* experts, hipStream_t st);
@@ -99,6 +103,7 @@ struct Mx4Choice {
     int tile;                 // kTiled: index of the tile's shape
     int tile_rows;            // its rows
 };
+bool mx4_fits(int64_t M, int64_t N, int64_t K, int64_t E, bool gather, const Mx4Choice& c);   // one launch holds it
 Mx4Choice mx4_choose(int64_t M, int64_t N, int64_t K, int64_t E, bool gather, bool codes);
 hipError_t launch_mx4_matmul(const Mx4Args& a, const Mx4Choice& c, const struct Mx4Plan* plan, hipStream_t st);
 

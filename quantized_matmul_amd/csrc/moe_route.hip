@@ -33,6 +33,7 @@ namespace qlin {
 namespace {
 
 constexpr int ROUTE_WAVES = 4;
+constexpr int64_t ROUTE_TOKENS = kLaunchItems / 64;   // tokens of a launch, a wave each at most
 
 struct RouteArgs {
     const void* logits;
@@ -517,7 +518,14 @@ inline int whole_lanes(int dt, int E, int V, const void* a, const void* b) {
 template <int DT, int L, int V>
 void route_launch(const RouteArgs& a, hipStream_t st) {
     constexpr int per = ROUTE_WAVES * (64 / L);
-    route_kernel<DT, L, V><<<(unsigned)((a.T + per - 1) / per), 64 * ROUTE_WAVES, 0, st>>>(a);
+    RouteArgs part = a;
+    for (int64_t t = 0; t < a.T; t += ROUTE_TOKENS) {
+        part.T = a.T - t < ROUTE_TOKENS ? a.T - t : ROUTE_TOKENS;
+        part.logits = (const char*)a.logits + t * a.E * (DT == QLIN_F32 ? 4 : 2);
+        part.weights = a.weights + t * a.k;
+        part.experts = a.experts + t * a.k;
+        route_kernel<DT, L, V><<<(unsigned)((part.T + per - 1) / per), 64 * ROUTE_WAVES, 0, st>>>(part);
+    }
 }
 template <int DT>
 void route_by_width(const RouteArgs& a, int L, int V, hipStream_t st) {
@@ -539,30 +547,27 @@ void route_by_width(const RouteArgs& a, int L, int V, hipStream_t st) {
     }
 }
 template <int DT, int V>
-struct RouteGrad {
-    static void run(const RouteGradArgs& a, unsigned grid, size_t shm, hipStream_t st) {
-        route_grad_kernel<DT, V><<<grid, 64 * ROUTE_WAVES, shm, st>>>(a);
-    }
-};
-
-template <template <int, int> class F, int DT, typename A>
-void by_width(int E, const A& a, unsigned grid, size_t shm, hipStream_t st) {
-    switch (lane_width(E, 64)) {
-    case 1: return F<DT, 1>::run(a, grid, shm, st);
-    case 2: return F<DT, 2>::run(a, grid, shm, st);
-    case 4: return F<DT, 4>::run(a, grid, shm, st);
-    case 8: return F<DT, 8>::run(a, grid, shm, st);
-    default: return F<DT, 16>::run(a, grid, shm, st);
+void route_grad_launch(const RouteGradArgs& a, hipStream_t st) {
+    RouteGradArgs part = a;
+    for (int64_t t = 0; t < a.T; t += ROUTE_TOKENS) {
+        part.T = a.T - t < ROUTE_TOKENS ? a.T - t : ROUTE_TOKENS;
+        part.logits = (const char*)a.logits + t * a.E * (DT == QLIN_F32 ? 4 : 2);
+        part.grad = (char*)a.grad + t * a.E * (DT == QLIN_F32 ? 4 : 2);
+        part.experts = a.experts + t * a.k;
+        part.grad_w = a.grad_w + t * a.k;
+        route_grad_kernel<DT, V><<<(unsigned)((part.T + ROUTE_WAVES - 1) / ROUTE_WAVES), 64 * ROUTE_WAVES,
+                                   ROUTE_WAVES * 64 * V * sizeof(float), st>>>(part);
     }
 }
-
-template <template <int, int> class F, typename A>
-hipError_t by_type(int dt, int E, const A& a, size_t shm, hipStream_t st) {
-    const unsigned grid = (unsigned)((a.T + ROUTE_WAVES - 1) / ROUTE_WAVES);
-    if (dt == QLIN_F32) by_width<F, QLIN_F32>(E, a, grid, shm, st);
-    else if (dt == QLIN_BF16) by_width<F, QLIN_BF16>(E, a, grid, shm, st);
-    else by_width<F, QLIN_F16>(E, a, grid, shm, st);
-    return hipGetLastError();
+template <int DT>
+void route_grad_by_width(const RouteGradArgs& a, int V, hipStream_t st) {
+    switch (V) {
+    case 1: return route_grad_launch<DT, 1>(a, st);
+    case 2: return route_grad_launch<DT, 2>(a, st);
+    case 4: return route_grad_launch<DT, 4>(a, st);
+    case 8: return route_grad_launch<DT, 8>(a, st);
+    default: return route_grad_launch<DT, 16>(a, st);
+    }
 }
 
 }  // namespace
@@ -589,8 +594,12 @@ hipError_t launch_moe_route(const void* logits, int dt, int64_t T, int E, int k,
 hipError_t launch_moe_route_grad(const void* logits, int dt, int64_t T, int E, int k, const int32_t* experts,
                                  const float* grad_w, int sigmoid, int renorm, float scale, void* grad,
                                  hipStream_t st) {
-    const RouteGradArgs a{logits, experts, grad_w, T, E, k, sigmoid, renorm, whole_lanes(dt, E, lane_width(E, 64), logits, grad), scale, grad};
-    return by_type<RouteGrad>(dt, E, a, (size_t)ROUTE_WAVES * 64 * lane_width(E, 64) * sizeof(float), st);
+    const int V = lane_width(E, 64);
+    const RouteGradArgs a{logits, experts, grad_w, T, E, k, sigmoid, renorm, whole_lanes(dt, E, V, logits, grad), scale, grad};
+    if (dt == QLIN_F32) route_grad_by_width<QLIN_F32>(a, V, st);
+    else if (dt == QLIN_BF16) route_grad_by_width<QLIN_BF16>(a, V, st);
+    else route_grad_by_width<QLIN_F16>(a, V, st);
+    return hipGetLastError();
 }
 
 }  // namespace qlin

@@ -235,13 +235,14 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t b
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
 }
 
-// 16-byte chunk c of row r sits in slot c ^ swz(r) of its LDS row of 128 or 64
-// bytes: any 8 neighbouring rows then keep a chunk in 8 different 16-byte
-// columns of the 128-byte bank line.
-template <int BKB>
-__device__ __forceinline__ int swz(int r) {
-    return BKB == 128 ? (r & 7) ^ ((r >> 3) & 1) : (r >> 1) & 3;
-}
+constexpr int BKB = 128;                    // bytes of a row a step takes: 256 codes, 8 blocks
+constexpr int CH = BKB / 16, KH = CH / 2;   // chunks (blocks) of a row and step; instructions along K
+constexpr int SG = 2;                       // steps whose scales one 16-byte load of a row brings
+
+// 16-byte chunk c of row r sits in slot c ^ swz(r) of its LDS row of 128 bytes:
+// any 8 neighbouring rows then keep a chunk in 8 different 16-byte columns of
+// the 128-byte bank line.
+__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 
 // s_waitcnt vmcnt(N) lgkmcnt(0). Field layout: vmcnt [3:0] and [15:14], expcnt [6:4], lgkmcnt [11:8].
 template <int N>
@@ -306,7 +307,7 @@ __device__ __forceinline__ uint32_t tiles_total(const TiledArgs& p) {
 }
 
 // Tile of BN weight rows (n) by BM activation rows (m), WN x WM waves of
-// TN x TM 32x32 accumulators, K in steps of BKB bytes (2 BKB codes) a row:
+// TN x TM 32x32 accumulators, K in steps of BKB bytes a row:
 //  * code rows go global -> LDS by buffer -> LDS loads, ST - 1 steps ahead
 //    through a ring of ST stages; one wave instruction moves 1 KB of whole row
 //    pieces, swizzled so that a fragment read meets no bank conflict;
@@ -316,16 +317,14 @@ __device__ __forceinline__ uint32_t tiles_total(const TiledArgs& p) {
 //    are read while the current one multiplies;
 //  * the outputs go through LDS, so that they leave in whole lines.
 // Rows past the tile and chunks past K read zeros (buffer range checks).
-template <int BN, int BM, int WN, int WM, int ST, int BKB>
+template <int BN, int BM, int WN, int WM, int ST>
 struct Shape {
     static constexpr int NW = WN * WM, TN = BN / WN / 32, TM = BM / WM / 32;
-    static constexpr int CH = BKB / 16, KH = CH / 2;               // chunks of a row and step; instructions along K
     static constexpr int WSTAGE = BN * BKB, STAGE = (BN + BM) * BKB;
     static constexpr int RPL = 1024 / BKB;                         // rows one load moves
     static constexpr int ND = (BN + BM) / RPL / NW;                // code loads per wave and step
     static constexpr int NSI = (BN + BM) / 64;                     // scale loads per batch
     static constexpr int NS = (NSI + NW - 1) / NW;                 // ... per wave
-    static constexpr int SG = 256 / BKB;                           // steps per batch of 16 scale bytes
     static constexpr int LA = ST - 1;                              // steps ahead
     static constexpr int SST = (LA + SG - 1) / SG + 1;             // scale stages
     static constexpr int SSTAGE = (BN + BM) * 16;
@@ -346,9 +345,9 @@ struct Shape {
     }
 };
 
-template <int BN, int BM, int WN, int WM, int ST, int BKB, int YDT, bool GATHER>
+template <int BN, int BM, int WN, int WM, int ST, int YDT, bool GATHER>
 __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
-    using S = Shape<BN, BM, WN, WM, ST, BKB>;
+    using S = Shape<BN, BM, WN, WM, ST>;
     constexpr int NW = S::NW, TN = S::TN, TM = S::TM;
     constexpr int YS = YDT == QLIN_F32 ? 4 : 2;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -398,18 +397,18 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
         for (int d = 0; d < S::ND; ++d) {
             const int blk = d * NW + wv;           // W's row blocks first, then x's
             const bool isw = blk < BN / S::RPL;
-            const int r = (isw ? blk : blk - BN / S::RPL) * S::RPL + lane / S::CH;
-            dchunk[d] = (uint32_t)((lane & (S::CH - 1)) ^ swz<BKB>(r));
+            const int r = (isw ? blk : blk - BN / S::RPL) * S::RPL + lane / CH;
+            dchunk[d] = (uint32_t)((lane & (CH - 1)) ^ swz(r));
             const uint32_t row = isw ? (r < nrows ? (uint32_t)r : NOWHERE) : src(r);
             doff[d] = row == NOWHERE ? NOWHERE : row * half + dchunk[d] * 16u;
         }
-        const int nk = (KB + S::CH - 1) / S::CH;
+        const int nk = (KB + CH - 1) / CH;
         // load d of step kt (past the end: of the last step, so that the counts stay the same)
         auto dma = [&](int kt, int d) {
             const int k = kt < nk ? kt : nk - 1;
             const bool isw = d < BN / S::RPL / NW;
             uint32_t off = doff[d];
-            if (k == nk - 1 && KB % S::CH != 0 && (uint32_t)(k * S::CH) + dchunk[d] >= (uint32_t)KB) off = NOWHERE;
+            if (k == nk - 1 && KB % CH != 0 && (uint32_t)(k * CH) + dchunk[d] >= (uint32_t)KB) off = NOWHERE;
             unsigned char* to = smem + (kt % ST) * S::STAGE + (d * NW + wv) * 1024;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(isw ? wr : xr, (__attribute__((address_space(3))) void*)to, 16,
                                                      (int)off, k * BKB, 0, 0);
@@ -432,11 +431,11 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
                     g * 16, 0, 0);
             }
         };
-        const int ng = (nk + S::SG - 1) / S::SG;
+        const int ng = (nk + SG - 1) / SG;
         // the batch of scales that step kt opens, if it opens one
         auto open_scales = [&](int kt) {
-            if (kt % S::SG == 0) {
-                const int g = kt / S::SG;
+            if (kt % SG == 0) {
+                const int g = kt / SG;
                 dma_scales(g % S::SST, g < ng ? g : ng - 1);
             }
         };
@@ -450,16 +449,14 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
         // the lane's place in a stage: row i of a 32-row tile, its first chunk;
         // swz repeats every 16 rows and chunk h of the lane's piece differs in
         // the low bits only
-        const uint32_t wlane = (uint32_t)(32 * TN * wn + i) * BKB + (((S::KH * j) ^ swz<BKB>(i)) << 4);
-        const uint32_t xlane = (uint32_t)(S::WSTAGE + (32 * TM * wm + i) * BKB) + (((S::KH * j) ^ swz<BKB>(i)) << 4);
-        const uint32_t slane = (uint32_t)i * 16 + (S::SG == 2 ? 4 * j : 0);
+        const uint32_t wlane = (uint32_t)(32 * TN * wn + i) * BKB + (((KH * j) ^ swz(i)) << 4);
+        const uint32_t xlane = (uint32_t)(S::WSTAGE + (32 * TM * wm + i) * BKB) + (((KH * j) ^ swz(i)) << 4);
+        const uint32_t slane = (uint32_t)i * 16 + 4 * j;
         auto step = [&](int kt) {
             __builtin_amdgcn_s_barrier();
             const unsigned char* const stage = smem + (kt % ST) * S::STAGE;
-            // the scale bytes of the lane's blocks: its own dword of the step's 8
-            // bytes a row, or its half of 4
-            const unsigned char* const st = slds + (kt / S::SG % S::SST) * S::SSTAGE + (kt % S::SG) * (16 / S::SG) + slane;
-            const int shift = S::SG == 2 ? 0 : 16 * j;
+            // the scale bytes of the lane's blocks: a dword of the step's 8 bytes a row
+            const unsigned char* const st = slds + (kt / SG % S::SST) * S::SSTAGE + (kt % SG) * (16 / SG) + slane;
             uint32_t sw[TN], sx[TM];
             u32x4 fa[2][TN], fb[2][TM];
             auto read = [&](int h) {
@@ -470,16 +467,16 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
             };
             read(0);
 #pragma unroll
-            for (int t = 0; t < TN; ++t) sw[t] = *(const uint32_t*)(st + 32 * (TN * wn + t) * 16) >> shift;
+            for (int t = 0; t < TN; ++t) sw[t] = *(const uint32_t*)(st + 32 * (TN * wn + t) * 16);
 #pragma unroll
-            for (int t = 0; t < TM; ++t) sx[t] = *(const uint32_t*)(st + (BN + 32 * (TM * wm + t)) * 16) >> shift;
+            for (int t = 0; t < TM; ++t) sx[t] = *(const uint32_t*)(st + (BN + 32 * (TM * wm + t)) * 16);
             open_scales(kt + S::LA);
             // the loads of step kt + LA go into the stage read one step ago, a few
             // after each product so that none waits for the others to be taken
             int d = 0;
 #pragma unroll
-            for (int h = 0; h < S::KH; ++h) {
-                if (h + 1 < S::KH) read(h + 1);
+            for (int h = 0; h < KH; ++h) {
+                if (h + 1 < KH) read(h + 1);
                 __builtin_amdgcn_sched_barrier(0);   // keeps those reads ahead of this round's products
 #pragma unroll
                 for (int q = 0; q < TN * TM; ++q) {
@@ -494,22 +491,12 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
                 }
             }
         };
-        for (int kt = 0; kt < nk; kt += S::SG) {
+        for (int kt = 0; kt < nk; kt += SG) {
             wait_loads<S::after(0)>();
             step(kt);
             if (kt + 1 < nk) {
                 wait_loads<S::after(1)>();
                 step(kt + 1);
-            }
-            if constexpr (S::SG == 4) {
-                if (kt + 2 < nk) {
-                    wait_loads<S::after(2)>();
-                    step(kt + 2);
-                }
-                if (kt + 3 < nk) {
-                    wait_loads<S::after(3)>();
-                    step(kt + 3);
-                }
             }
         }
         wait_loads<0>();                           // every load has landed ...
@@ -556,16 +543,20 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
 
 // ---------------------------------------------------------------- dispatch
 
+// Waves of a workgroup: a wave takes one run, or two where that lets all of W's loads be in flight at once (four waves
+// a SIMD).
+int stream_waves(int64_t tiles_m, int64_t N, int64_t K) {
+    int64_t runs = (K + 511) / 512;
+    if (tiles_m * ((N + 15) / 16) * runs > 16 * (int64_t)device_shape().cus) runs = (runs + 1) / 2;
+    return (int)(runs < STREAM_WAVES ? runs : STREAM_WAVES);
+}
+
 template <int YDT, int XDT, bool DIRECT>
 hipError_t stream_launch(const Mx4Args& a, hipStream_t st) {
-    // a wave takes one run, or two where that lets all of W's loads be in flight at once (four waves a SIMD)
-    int64_t runs = (a.K + 511) / 512;
-    if ((DIRECT ? a.M : 1) * ((a.N + 15) / 16) * runs > 16 * (int64_t)device_shape().cus) runs = (runs + 1) / 2;
-    const int waves = (int)(runs < STREAM_WAVES ? runs : STREAM_WAVES);
+    const int waves = stream_waves(DIRECT ? a.M : 1, a.N, a.K);
     StreamArgs s{a, DIRECT ? (uint32_t)(a.M / a.B) : 1, (int)((a.N + 15) / 16), ((uintptr_t)a.x & 15) == 0};
     const int64_t blocks = (DIRECT ? a.M : 1) * s.tiles_n;
-    if (blocks > 0x7fffffffLL || (!DIRECT && a.M > (XDT == QLIN_U8 ? STREAM_ROWS : STREAM_FLOAT_ROWS)))
-        return hipErrorInvalidValue;
+    if (!DIRECT && a.M > (XDT == QLIN_U8 ? STREAM_ROWS : STREAM_FLOAT_ROWS)) return hipErrorInvalidValue;
     const size_t floats = XDT == QLIN_U8 ? 0 : (DIRECT ? 1 : STREAM_FLOAT_ROWS) * 68;
     mx4_stream_kernel<YDT, XDT, DIRECT>
         <<<(unsigned)blocks, 64 * waves, (size_t)waves * (256 + floats) * sizeof(uint32_t), st>>>(s);
@@ -577,15 +568,14 @@ hipError_t stream_rows(const Mx4Args& a, hipStream_t st) {
     return a.experts ? stream_launch<YDT, XDT, true>(a, st) : stream_launch<YDT, XDT, false>(a, st);
 }
 
-template <int BN, int BM, int WN, int WM, int ST, int BKB, int YDT, bool GATHER>
+template <int BN, int BM, int WN, int WM, int ST, int YDT, bool GATHER>
 hipError_t tiled_launch(TiledArgs p, hipStream_t st) {
     const Mx4Args& a = p.a;
     p.tiles_n = (int)((a.N + BN - 1) / BN);
     const int64_t tm = GATHER ? mx4_plan_max_tiles(a.M, a.E, BM) : (a.M + BM - 1) / BM;
-    if (tm * p.tiles_n > 0x7fffffffLL) return hipErrorInvalidValue;
-    constexpr size_t shm = Shape<BN, BM, WN, WM, ST, BKB>::lds(YDT == QLIN_F32 ? 4 : 2);
+    constexpr size_t shm = Shape<BN, BM, WN, WM, ST>::lds(YDT == QLIN_F32 ? 4 : 2);
     static_assert(shm <= 160 * 1024, "LDS of a compute unit");
-    const auto kernel = mx4_tiled_kernel<BN, BM, WN, WM, ST, BKB, YDT, GATHER>;
+    const auto kernel = mx4_tiled_kernel<BN, BM, WN, WM, ST, YDT, GATHER>;
     static std::atomic<bool> attr{false};
     if (!attr.load(std::memory_order_acquire)) {
         const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)shm);
@@ -606,22 +596,22 @@ hipError_t tiled_launch(TiledArgs p, hipStream_t st) {
 //  2, 3: for few rows: more workgroups and more loads in flight for each byte of W.
 constexpr int kTiles = 4;
 struct TileShape {
-    int n, m, per_cu;
+    int n, m, threads, per_cu;
     float start, step, alone;
 };
-constexpr TileShape kTile[kTiles] = {{256, 256, 1, 9.5f, 1.72f, 1.72f},
-                                     {128, 128, 2, 3.4f, 1.28f, 0.90f},
-                                     {128, 64, 2, 3.0f, 0.78f, 0.38f},
-                                     {64, 64, 2, 2.5f, 0.56f, 0.20f}};
+constexpr TileShape kTile[kTiles] = {{256, 256, 512, 1, 9.5f, 1.72f, 1.72f},
+                                     {128, 128, 256, 2, 3.4f, 1.28f, 0.90f},
+                                     {128, 64, 256, 2, 3.0f, 0.78f, 0.38f},
+                                     {64, 64, 256, 2, 2.5f, 0.56f, 0.20f}};
 
 template <int YDT, bool GATHER>
 hipError_t tiled_rows(const Mx4Args& a, const Mx4Plan& plan, int tile, hipStream_t st) {
     const TiledArgs p{a, plan, FastDiv::by(GATHER ? (uint32_t)(a.M / a.B) : 1), 0, device_shape().xcds, debug_lds_nan() ? 1 : 0};
     switch (tile) {
-    case 0: return tiled_launch<256, 256, 4, 2, 2, 128, YDT, GATHER>(p, st);
-    case 1: return tiled_launch<128, 128, 2, 2, 2, 128, YDT, GATHER>(p, st);
-    case 2: return tiled_launch<128, 64, 2, 2, 3, 128, YDT, GATHER>(p, st);
-    default: return tiled_launch<64, 64, 2, 2, 4, 128, YDT, GATHER>(p, st);
+    case 0: return tiled_launch<256, 256, 4, 2, 2, YDT, GATHER>(p, st);
+    case 1: return tiled_launch<128, 128, 2, 2, 2, YDT, GATHER>(p, st);
+    case 2: return tiled_launch<128, 64, 2, 2, 3, YDT, GATHER>(p, st);
+    default: return tiled_launch<64, 64, 2, 2, 4, YDT, GATHER>(p, st);
     }
 }
 
@@ -674,6 +664,16 @@ Mx4Choice mx4_choose(int64_t M, int64_t N, int64_t K, int64_t E, bool gather, bo
         }
     }
     return {Mx4Path::kTiled, tile, kTile[tile].m};
+}
+
+bool mx4_fits(int64_t M, int64_t N, int64_t K, int64_t E, bool gather, const Mx4Choice& c) {
+    if (c.path != Mx4Path::kTiled) {
+        const int64_t tiles_m = gather ? M : 1;
+        return tiles_m * ((N + 15) / 16) <= 2 * kLaunchItems / (64 * stream_waves(tiles_m, N, K)) - 1;
+    }
+    const TileShape& s = kTile[c.tile];
+    const int64_t m = gather ? mx4_plan_max_tiles(M, E, s.m) : (M + s.m - 1) / s.m;
+    return m * ((N + s.n - 1) / s.n) <= 2 * kLaunchItems / s.threads - 1;
 }
 
 hipError_t launch_mx4_matmul(const Mx4Args& a, const Mx4Choice& c, const Mx4Plan* plan, hipStream_t st) {

@@ -28,7 +28,6 @@ struct PrepareArgs {
     int64_t words;          // packed words in all; 0: codes are given
     uint32_t row_words;     // packed words of a row
     FastDiv by_row;         // word / row_words
-    int wide;               // 2^32 words or more: 64-bit division
     int swiglu, vec;
     uint32_t* xq;
     uint8_t* xs;
@@ -144,7 +143,7 @@ template <int DT>
 __device__ __forceinline__ void activation(const PrepareArgs& a, int64_t wid) {
     const bool live = wid < a.words;                 // whole blocks of 4 lanes are live or not
     const int64_t w0 = live ? wid : 0;
-    const int64_t row = a.wide ? w0 / a.row_words : (int64_t)a.by_row((uint32_t)w0);
+    const int64_t row = a.by_row((uint32_t)w0);
     const uint32_t col = (uint32_t)(w0 - row * a.row_words);
     uint32_t byte, word;
     if (a.swiglu) {
@@ -174,7 +173,7 @@ __device__ __forceinline__ void activation(const PrepareArgs& a, int64_t wid) {
 __device__ __forceinline__ void pad_unit(const Mx4Scales& p, const FastDiv& by_unit, int64_t u) {
     const int64_t units = (p.KS + 15) / 16;
     if (u >= p.rows * units) return;
-    const int64_t row = p.rows * units < (1LL << 32) ? (int64_t)by_unit((uint32_t)u) : u / units;
+    const int64_t row = by_unit((uint32_t)u);
     const int64_t c = (u - row * units) * 16;
     const uint8_t* const from = p.from + row * p.KS + c;
     uint32_t d[4] = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
@@ -223,28 +222,13 @@ size_t mx4_plan_bytes(int64_t R, int64_t E) {
 
 hipError_t launch_mx4_prepare(const Mx4Prepare& q, Mx4Plan* plan, hipStream_t st) {
     PrepareArgs a{};
-    a.x = q.x;
-    a.words = q.x ? q.rows * (q.K / 8) : 0;
     a.row_words = (uint32_t)(q.K / 8);
     a.by_row = FastDiv::by(a.row_words);
-    a.wide = a.words >= (1LL << 32);
     a.swiglu = q.swiglu;
     a.vec = ((uintptr_t)q.x & 15) == 0;              // rows are whole multiples of 64 bytes
-    a.xq = q.xq;
-    a.xs = q.xs;
     a.sstride = q.sstride;
-    int64_t blocks = (a.words + THREADS - 1) / THREADS;
-    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-    a.act_blocks = (int)blocks;
     const int64_t units = (q.K / 32 + 15) / 16;
     a.by_unit = FastDiv::by((uint32_t)units);
-    for (int w = 0; w < 2; ++w) {
-        a.pad[w] = q.pad[w];
-        const int64_t n = q.pad[w].to ? (q.pad[w].rows * units + THREADS - 1) / THREADS : 0;
-        if (n > 0x7fffffffLL) return hipErrorInvalidValue;
-        a.pad_blocks[w] = (int)n;
-        blocks += n;
-    }
     size_t shm = 0;
     if (q.experts) {
         const int64_t R = q.R, E = q.E;
@@ -260,15 +244,44 @@ hipError_t launch_mx4_prepare(const Mx4Prepare& q, Mx4Plan* plan, hipStream_t st
         a.plan.perm = a.plan.total + 1;
         a.plan.counts = a.plan.perm + R;
         *plan = a.plan;
-        blocks += a.chunks;
         shm = (size_t)2 * (E + 1) * sizeof(uint32_t);
     }
-    if (blocks == 0) return hipSuccess;
-    if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
-    if (q.dt == QLIN_F32) mx4_prepare_kernel<QLIN_F32><<<(unsigned)blocks, THREADS, shm, st>>>(a);
-    else if (q.dt == QLIN_F16) mx4_prepare_kernel<QLIN_F16><<<(unsigned)blocks, THREADS, shm, st>>>(a);
-    else mx4_prepare_kernel<QLIN_BF16><<<(unsigned)blocks, THREADS, shm, st>>>(a);
-    if (a.chunks > 1) mx4_place_kernel<<<(unsigned)a.chunks, THREADS, shm, st>>>(a);
+    // the first launch takes the plan and up to a part of everything else; few calls have more
+    const int64_t part = kLaunchItems / 4;           // items: words, 16-byte units
+    const int64_t row_bytes = q.K * (q.swiglu ? 2 : 1) * (q.dt == QLIN_F32 ? 4 : 2);
+    int64_t done = 0, padded[2] = {0, 0};            // rows
+    for (bool more = true; more;) {
+        more = false;
+        int64_t blocks = a.chunks;
+        // up to `part` items of the rows left: rows of this launch
+        auto take = [&](int64_t& at, int64_t rows, int64_t items, int* grid) {
+            const int64_t most = part / items, n = rows - at < most ? rows - at : most;
+            *grid = (int)((n * items + THREADS - 1) / THREADS);
+            blocks += *grid;
+            at += n;
+            more |= at < rows;
+            return n;
+        };
+        a.x = (const char*)q.x + done * row_bytes;
+        a.xq = q.xq + done * a.row_words;
+        a.xs = q.xs + done * q.sstride;
+        a.words = q.x ? take(done, q.rows, a.row_words, &a.act_blocks) * a.row_words : 0;
+        for (int w = 0; w < 2; ++w) {
+            if (!q.pad[w].to) continue;
+            a.pad[w] = q.pad[w];
+            a.pad[w].from += padded[w] * q.pad[w].KS;
+            a.pad[w].to += padded[w] * units * 16;
+            a.pad[w].rows = take(padded[w], q.pad[w].rows, units, &a.pad_blocks[w]);
+        }
+        if (blocks) {
+            if (q.dt == QLIN_F32) mx4_prepare_kernel<QLIN_F32><<<(unsigned)blocks, THREADS, shm, st>>>(a);
+            else if (q.dt == QLIN_F16) mx4_prepare_kernel<QLIN_F16><<<(unsigned)blocks, THREADS, shm, st>>>(a);
+            else mx4_prepare_kernel<QLIN_BF16><<<(unsigned)blocks, THREADS, shm, st>>>(a);
+        }
+        if (a.chunks > 1) mx4_place_kernel<<<(unsigned)a.chunks, THREADS, shm, st>>>(a);
+        a.experts = nullptr;                         // the plan is on its way
+        a.chunks = 0;
+    }
     return hipGetLastError();
 }
 

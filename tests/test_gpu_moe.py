@@ -472,3 +472,63 @@ def test_layer_on_another_stream_and_in_a_graph(B):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, y), rep
+
+
+# ------------------------------------------------- more than one launch holds
+
+def enough(gigabytes):
+    free = torch.cuda.mem_get_info()[0]
+    if free < gigabytes * 10 ** 9:
+        pytest.skip(f"needs {gigabytes} GB of device memory")
+
+
+def test_route_of_more_tokens_than_a_launch_holds():
+    enough(12)
+    T, E = 2 ** 28 + 5, 3                                    # 16 lanes a token
+    x = torch.empty((T, E), dtype=torch.bfloat16, device=DEV).normal_()
+    w, ids = qm.moe_route(x, 1)
+    for t in range(0, T, 2 ** 26):
+        pw, pids = qm.moe_route(x[t:t + 2 ** 26], 1)
+        assert torch.equal(w[t:t + 2 ** 26], pw) and torch.equal(ids[t:t + 2 ** 26], pids), t
+    T = 2 ** 26 + 5                                          # a wave a token
+    x, ids = x[:T], ids[:T]
+    g = torch.empty((T, 1), device=DEV).normal_()
+    gx = qm.moe_route_grad(x, ids, g, renormalize=False)
+    for t in range(0, T, 2 ** 24):
+        s = slice(t, t + 2 ** 24)
+        assert torch.equal(gx[s], qm.moe_route_grad(x[s], ids[s], g[s], renormalize=False)), t
+
+
+def test_combine_of_more_values_than_a_launch_holds():
+    enough(40)
+    T, D = 3, 2 ** 31 - 1                                    # a thread a value
+    h = torch.empty((T, 1, D), dtype=torch.bfloat16, device=DEV).normal_()
+    w = torch.tensor([[0.5], [1.25], [-3.0]], device=DEV)
+    y = qm.moe_combine(h, w)
+    for t in range(T):
+        for d in range(0, D, 2 ** 28):
+            s = slice(d, d + 2 ** 28)
+            assert torch.equal(y[t, s], (w[t] * h[t, 0, s].float()).bfloat16()), (t, d)
+    del h, y
+    T, D = 2 ** 26 + 3, 8                                    # a wave a row
+    h = torch.empty((T, 1, D), dtype=torch.bfloat16, device=DEV).normal_()
+    gy = torch.empty((T, D), dtype=torch.bfloat16, device=DEV).normal_()
+    w = torch.empty((T, 1), device=DEV).normal_()
+    gh, gw = qm.moe_combine_grad(gy, h, w)
+    for t in range(0, T, 2 ** 24):
+        s = slice(t, t + 2 ** 24)
+        assert torch.equal(gh[s, 0], (w[s] * gy[s].float()).bfloat16()), t
+        terms = gy[s].double() * h[s, 0].double()
+        assert ((gw[s, 0] - terms.sum(1)).abs() <= 8 * 2.0 ** -24 * terms.abs().sum(1)).all(), t
+
+
+def test_product_of_more_words_than_a_launch_holds():
+    enough(100)
+    M, N, K = 2 ** 22 + 1, 16, 8192                          # a thread a word of x; small integers: sums are exact
+    x = torch.empty((M, K), dtype=torch.bfloat16, device=DEV)
+    for m in range(0, M, 2 ** 18):
+        x[m:m + 2 ** 18].random_(-6, 7)
+    qw = qm.quantize(torch.empty((N, K), dtype=torch.bfloat16, device=DEV).random_(-6, 7), mode="mxfp4")
+    y = qm.mxfp4_matmul(x, qw, out_dtype=torch.float32)
+    for m in range(0, M, 2 ** 20):
+        assert torch.equal(y[m:m + 2 ** 20], qm.mxfp4_matmul(x[m:m + 2 ** 20], qw, out_dtype=torch.float32)), m

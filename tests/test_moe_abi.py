@@ -80,6 +80,9 @@ def test_product_rejects(lib):
         assert call(**bad) == INVALID, bad
         assert err(lib)
     assert call(K=1 << 23) == UNSUPPORTED
+    # more work-items than one launch takes, by the streaming and by the tiled kernel
+    assert call(M=1, K=32, N=(1 << 31) - 1, work=None, nb=0) == UNSUPPORTED and "launch" in err(lib)
+    assert call(M=(1 << 31) - 1, K=32, N=1 << 20, nb=1 << 60) == UNSUPPORTED and "launch" in err(lib)
     assert call(M=0, x=None, wq=None, ws=None, y=None, work=None, nb=0) == 0
     # a few rows need none: they are quantized inside the product, or given as codes
     assert lib.qlin_mxfp4_matmul_workspace_bytes(4, 128, 64, BF16) == 0
