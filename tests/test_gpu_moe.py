@@ -364,7 +364,7 @@ def test_products_refuse():
     assert qm.gather_mxfp4_matmul(x, qe, ids[:, :0]).shape == (4, 0, 32)
 
 
-@pytest.mark.parametrize("tile", ["0", "1", "2", "3"])
+@pytest.mark.parametrize("tile", ["0", "1", "2", "3", "4"])
 @pytest.mark.parametrize("M,N,K", [(17, 70, 96), (130, 300, 544), (300, 513, 1056)])
 def test_every_tile(M, N, K, tile, monkeypatch):
     """Each shape of the tiled kernel's workgroup, dense and by experts, in every output type."""
@@ -381,9 +381,11 @@ def test_every_tile(M, N, K, tile, monkeypatch):
         assert qm.last_path() == "mxfp4_gather_tiled"
 
 
+@pytest.mark.parametrize("tile", ["0", "1", "2", "3", "4"])
 @pytest.mark.parametrize("M", [70, 300])
-def test_tiled_product_reads_no_stale_lds(M, monkeypatch):
+def test_tiled_product_reads_no_stale_lds(M, tile, monkeypatch):
     """With the whole LDS filled with NaN before each tile the output is the same."""
+    monkeypatch.setenv("QLIN_MXFP4_TILE", tile)
     qw, x = weight((200, 1056), 640), rand((M, 1056), "bf16", 740)
     y = qm.mxfp4_matmul(x, qw)
     qe, ids = weight((2, 200, 1056), 641), torch.from_numpy(choices(M, 1, 2, 841)).to(DEV)
