@@ -297,8 +297,9 @@ size_t qlin_gather_qmm_noalloc_max_experts(void);
  *   bias     fp32 [E] or NULL: a balance bias, added to s for the choice only.
  *   groups   the experts form `groups` runs of E/groups; a group counts as its
  *            largest s + bias (group_top 1) or the sum of its two largest
- *            (group_top 2), and only experts of the groups_kept best groups can
- *            be chosen. 1, 1, 1: no groups.
+ *            (group_top 2; last where it has fewer to choose from), and only
+ *            experts of the groups_kept best groups can be chosen. 1, 1, 1: no
+ *            groups.
  *   experts  out, int32 [T, k]: the k largest s + bias in descending order,
  *            equal ones by ascending index (without a bias the logits
  *            themselves are compared). An expert whose logit is not finite, or

@@ -186,6 +186,12 @@ struct Lanes<16> {
     }
 };
 
+// A group's key from its two largest: -inf where it has fewer experts to choose from than count.
+__device__ __forceinline__ uint32_t group_key(const RouteArgs& a, uint32_t m1, uint32_t m2) {
+    if (a.group_top == 1) return m1 == NONE ? order_of(-INFINITY) : m1;
+    return order_of(m2 == NONE ? -INFINITY : value_of(m1) + value_of(m2));
+}
+
 // Whether the lane's group is among the `kept` best, for groups of a.seg whole
 // lanes. f holds the lane's V values.
 template <int L, int V>
@@ -203,9 +209,8 @@ __device__ __forceinline__ bool in_best_groups(const RouteArgs& a, const uint32_
         if (a.seg > 16) merge2(m1, m2, (uint32_t)__shfl_xor((int)m1, 16, 64), (uint32_t)__shfl_xor((int)m2, 16, 64));
         if (a.seg > 32) merge2(m1, m2, (uint32_t)__shfl_xor((int)m1, 32, 64), (uint32_t)__shfl_xor((int)m2, 32, 64));
     }
-    const float b1 = m1 == NONE ? -INFINITY : value_of(m1), b2 = m2 == NONE ? -INFINITY : value_of(m2);
     const int row = lane & (L - 1);
-    uint32_t g = row < a.groups * a.seg ? order_of(a.group_top == 2 ? b1 + b2 : b1) : NONE;
+    uint32_t g = row < a.groups * a.seg ? group_key(a, m1, m2) : NONE;
     bool in = false;
     for (int r = 0; r < a.kept; ++r) {
         const int win = Lanes<L>::first(g == Lanes<L>::max_all(g), lane);      // the first lane of its group
@@ -228,8 +233,7 @@ __device__ __forceinline__ uint64_t best_groups(const RouteArgs& a, const uint32
     uint32_t m1 = NONE, m2 = NONE, g = NONE;
     if (lane < a.groups) {
         for (int e = 0; e < per; ++e) merge2(m1, m2, row[lane * per + e], NONE);
-        const float b1 = m1 == NONE ? -INFINITY : value_of(m1), b2 = m2 == NONE ? -INFINITY : value_of(m2);
-        g = order_of(a.group_top == 2 ? b1 + b2 : b1);
+        g = group_key(a, m1, m2);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     uint64_t in = 0;

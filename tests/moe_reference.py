@@ -32,7 +32,7 @@ def route(x, k, score="softmax", bias=None, renormalize=True, scale=1.0, groups=
             g = []
             for i in range(groups):
                 v = sorted([value[e] if free[e] else -np.inf for e in range(i * per, (i + 1) * per)], reverse=True)
-                g.append(sum(v[:group_top]))
+                g.append(sum(v[:group_top]) if v[group_top - 1] > -np.inf else -np.inf)
             best = sorted(range(groups), key=lambda i: (-g[i], i))[:groups_kept]
             free &= np.isin(np.arange(E) // per, best)
         order = sorted([e for e in range(E) if free[e]], key=lambda e: (-key[e], e))[:k]

@@ -130,6 +130,21 @@ def test_route_groups_without_experts():
     np.testing.assert_allclose(f64(w), rw, rtol=4e-6)
 
 
+@pytest.mark.parametrize("E,groups", [(16, 4), (24, 8)])    # groups of whole lanes, and of others
+def test_route_groups_with_infinite_biases(E, groups):
+    per = E // groups
+    x = rand((3, E), "f32", 11)
+    x[1, 1:per] = -float("inf")         # the expert with the infinite bias is alone in its group
+    b = torch.zeros(E, device=DEV)
+    b[0] = float("inf")
+    b[per] = -float("inf")
+    for top in (1, 2):
+        w, ids = qm.moe_route(x, 3, bias=b, groups=groups, groups_kept=2, group_top=top, score="sigmoid")
+        rw, rids = ref.route(f64(x), 3, "sigmoid", bias=f64(b), groups=groups, groups_kept=2, group_top=top)
+        np.testing.assert_array_equal(ids.cpu().numpy(), rids)
+        np.testing.assert_allclose(f64(w), rw, rtol=4e-6)
+
+
 def test_route_empty_and_shapes():
     w, ids = qm.moe_route(torch.empty((0, 8), device=DEV), 2)
     assert w.shape == (0, 2) and ids.dtype == torch.int32
