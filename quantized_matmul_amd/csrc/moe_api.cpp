@@ -156,6 +156,13 @@ qlin_status product(const void* x, int x_dtype, const void* x_scales, const char
     a.B = rows;
     a.E = E;
     const bool quantized = !codes && c.path != qlin::Mx4Path::kStreamFloat;
+    // what the call touches: x, its codes, the experts met, y
+    const double touched = (double)rows * K * (codes ? 0.5 : (double)elem(x_dtype) * (swiglu ? 2 : 1) + 0.5) +
+                           (double)(E < R ? E : R) * N * K * 0.5 + (double)R * N * elem(y_dtype);
+    const bool large = touched >= (double)qlin::kStreamBytes;
+    // 16-byte stores off their alignment split lines, which the caches join (8192 rows, N 13001, K 4096: 298 us through
+    // them, 305 past them)
+    a.stream = large && N * elem(y_dtype) % 16 == 0 && (uintptr_t)y % 16 == 0;
     qlin::Mx4Plan plan{};
     hipError_t e;
     qlin::Mx4Prepare q{};
@@ -167,6 +174,7 @@ qlin_status product(const void* x, int x_dtype, const void* x_scales, const char
         q.x = x;
         q.rows = rows;
         q.swiglu = swiglu;
+        q.stream = large;
         q.xq = (uint32_t*)(w + l.xq);
         q.xs = (uint8_t*)(w + l.xs);
         q.sstride = stride;

@@ -35,21 +35,29 @@ __device__ __forceinline__ void load_v(const void* p, int64_t i, float (&v)[VEC]
     }
 }
 
-template <int DT, int VEC>
+// The same to memory; STREAM: past the caches.
+template <int DT, int VEC, bool STREAM>
 __device__ __forceinline__ void store_v(void* p, int64_t i, const float (&v)[VEC]) {
     if constexpr (VEC == 1) {
         store_f<DT>(p, i, v[0]);
     } else if constexpr (DT == QLIN_F32) {
-        *(float4*)((float*)p + i) = float4{v[0], v[1], v[2], v[3]};
+        typedef __attribute__((ext_vector_type(4))) float f32x4;
+        const f32x4 d = {v[0], v[1], v[2], v[3]};
+        f32x4* const to = (f32x4*)((float*)p + i);
+        if constexpr (STREAM) __builtin_nontemporal_store(d, to);
+        else *to = d;
     } else {
-        uint32_t d[4];
+        typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+        u32x4 d;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const uint32_t lo = DT == QLIN_BF16 ? f32_to_bf16_rne(v[2 * c]) : f32_to_f16_rne(v[2 * c]);
             const uint32_t hi = DT == QLIN_BF16 ? f32_to_bf16_rne(v[2 * c + 1]) : f32_to_f16_rne(v[2 * c + 1]);
             d[c] = lo | (hi << 16);
         }
-        *(uint4*)((uint16_t*)p + i) = uint4{d[0], d[1], d[2], d[3]};
+        u32x4* const to = (u32x4*)((uint16_t*)p + i);
+        if constexpr (STREAM) __builtin_nontemporal_store(d, to);
+        else *to = d;
     }
 }
 
@@ -73,7 +81,7 @@ constexpr int COMBINE_THREADS = 256;
 // Each thread owns VEC consecutive outputs of one token and has KC rows of h in
 // flight; places past k read the token's first row again and count nothing, so
 // that no branch stands between the loads.
-template <int DT, int VEC, int KC>
+template <int DT, int VEC, int KC, bool STREAM>
 __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(CombineArgs a) {
     const int64_t per = a.D / VEC;
     const uint32_t i = blockIdx.x * COMBINE_THREADS + threadIdx.x, own = a.by_row(i);
@@ -103,11 +111,11 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(CombineArgs a)
             for (int c = 0; c < VEC; ++c) acc[c] += f * (live ? v[q][c] : 0.0f);
         }
     }
-    store_v<DT, VEC>(a.y, t * a.D + d, acc);
+    store_v<DT, VEC, STREAM>(a.y, t * a.D + d, acc);
 }
 
 // One wave per row (t, j).
-template <int DT, int VEC>
+template <int DT, int VEC, bool STREAM>
 __global__ void __launch_bounds__(COMBINE_THREADS) combine_grad_kernel(CombineArgs a) {
     const int lane = threadIdx.x & 63;
     const int64_t r = a.first + (int64_t)blockIdx.x * (COMBINE_THREADS / 64) + (threadIdx.x >> 6);
@@ -130,7 +138,7 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_grad_kernel(CombineAr
                 o[c] = w * g[c];
             }
         }
-        store_v<DT, VEC>(a.gh, r * a.D + d, o);
+        store_v<DT, VEC, STREAM>(a.gh, r * a.D + d, o);
     }
     sum = wave_sum(sum);
     if (lane == 0) a.gw[r] = sum;
@@ -141,31 +149,43 @@ bool wide(int dt, int64_t D, const void* a, const void* b, const void* c) {
     return D % per == 0 && (((uintptr_t)a | (uintptr_t)b | (uintptr_t)c) & 15) == 0;
 }
 
-template <int DT, int WIDE>
+template <int DT, int WIDE, bool STREAM>
 void run_combine(CombineArgs a, bool vec, hipStream_t st) {
     const int64_t per = vec ? a.D / WIDE : a.D, most = kLaunchItems / per;   // threads of a token; tokens of a launch
     a.by_row = FastDiv::by((uint32_t)per);
     for (a.first = 0; a.first < a.T; a.first = a.end) {
         a.end = a.T - a.first < most ? a.T : a.first + most;
         const unsigned grid = (unsigned)(((a.end - a.first) * per + COMBINE_THREADS - 1) / COMBINE_THREADS);
-        if (!vec) combine_kernel<DT, 1, 8><<<grid, COMBINE_THREADS, 0, st>>>(a);
-        else if (a.k <= 2) combine_kernel<DT, WIDE, 2><<<grid, COMBINE_THREADS, 0, st>>>(a);
-        else if (a.k <= 4) combine_kernel<DT, WIDE, 4><<<grid, COMBINE_THREADS, 0, st>>>(a);
-        else if (a.k <= 6) combine_kernel<DT, WIDE, 6><<<grid, COMBINE_THREADS, 0, st>>>(a);
-        else combine_kernel<DT, WIDE, 8><<<grid, COMBINE_THREADS, 0, st>>>(a);
+        if (!vec) combine_kernel<DT, 1, 8, false><<<grid, COMBINE_THREADS, 0, st>>>(a);
+        else if (a.k <= 2) combine_kernel<DT, WIDE, 2, STREAM><<<grid, COMBINE_THREADS, 0, st>>>(a);
+        else if (a.k <= 4) combine_kernel<DT, WIDE, 4, STREAM><<<grid, COMBINE_THREADS, 0, st>>>(a);
+        else if (a.k <= 6) combine_kernel<DT, WIDE, 6, STREAM><<<grid, COMBINE_THREADS, 0, st>>>(a);
+        else combine_kernel<DT, WIDE, 8, STREAM><<<grid, COMBINE_THREADS, 0, st>>>(a);
     }
 }
 
-template <int DT, int WIDE>
+template <int DT, int WIDE, bool STREAM>
 void run_combine_grad(CombineArgs a, bool vec, hipStream_t st) {
     const int64_t rows = a.T * a.k, most = kLaunchItems / 64;
     a.by_row = FastDiv::by((uint32_t)a.k);
     for (a.first = 0; a.first < rows; a.first = a.end) {
         a.end = rows - a.first < most ? rows : a.first + most;
         const unsigned grid = (unsigned)((a.end - a.first + COMBINE_THREADS / 64 - 1) / (COMBINE_THREADS / 64));
-        if (vec) combine_grad_kernel<DT, WIDE><<<grid, COMBINE_THREADS, 0, st>>>(a);
-        else combine_grad_kernel<DT, 1><<<grid, COMBINE_THREADS, 0, st>>>(a);
+        if (vec) combine_grad_kernel<DT, WIDE, STREAM><<<grid, COMBINE_THREADS, 0, st>>>(a);
+        else combine_grad_kernel<DT, 1, false><<<grid, COMBINE_THREADS, 0, st>>>(a);
     }
+}
+
+template <int DT, int WIDE, bool STREAM>
+void run(const CombineArgs& a, bool vec, hipStream_t st, bool grad) {
+    if (grad) run_combine_grad<DT, WIDE, STREAM>(a, vec, st);
+    else run_combine<DT, WIDE, STREAM>(a, vec, st);
+}
+template <bool STREAM>
+void by_type(int dt, const CombineArgs& a, bool vec, hipStream_t st, bool grad) {
+    if (dt == QLIN_F32) run<QLIN_F32, 4, STREAM>(a, vec, st, grad);
+    else if (dt == QLIN_BF16) run<QLIN_BF16, 8, STREAM>(a, vec, st, grad);
+    else run<QLIN_F16, 8, STREAM>(a, vec, st, grad);
 }
 
 }  // namespace
@@ -175,9 +195,8 @@ hipError_t launch_moe_combine(const void* h, int dt, int64_t T, int k, int64_t D
     CombineArgs a{};
     a.h = h; a.w = weights; a.experts = experts; a.T = T; a.D = D; a.k = k; a.y = y;
     const bool vec = wide(dt, D, h, y, nullptr);
-    if (dt == QLIN_F32) run_combine<QLIN_F32, 4>(a, vec, st);
-    else if (dt == QLIN_BF16) run_combine<QLIN_BF16, 8>(a, vec, st);
-    else run_combine<QLIN_F16, 8>(a, vec, st);
+    if (T * (k + 1) * D * (dt == QLIN_F32 ? 4 : 2) >= kStreamBytes) by_type<true>(dt, a, vec, st, false);
+    else by_type<false>(dt, a, vec, st, false);
     return hipGetLastError();
 }
 
@@ -187,9 +206,8 @@ hipError_t launch_moe_combine_grad(const void* gy, const void* h, int dt, int64_
     CombineArgs a{};
     a.h = h; a.w = weights; a.experts = experts; a.T = T; a.D = D; a.k = k; a.gy = gy; a.gh = gh; a.gw = gw;
     const bool vec = wide(dt, D, h, gy, gh);
-    if (dt == QLIN_F32) run_combine_grad<QLIN_F32, 4>(a, vec, st);
-    else if (dt == QLIN_BF16) run_combine_grad<QLIN_BF16, 8>(a, vec, st);
-    else run_combine_grad<QLIN_F16, 8>(a, vec, st);
+    if (T * (2 * k + 1) * D * (dt == QLIN_F32 ? 4 : 2) >= kStreamBytes) by_type<true>(dt, a, vec, st, true);
+    else by_type<false>(dt, a, vec, st, true);
     return hipGetLastError();
 }
 

@@ -57,6 +57,15 @@ constexpr int kRouteMaxExperts = 1024;
 constexpr int kRouteMaxChoice = 64;
 constexpr int kRouteMaxGroups = 64;
 
+// An operator that touches this much and more reads and writes what it touches
+// once past the caches (non-temporal loads and stores): three quarters of the
+// 256 MB in front of the memory, which then keep what is read again. Outputs of
+// smaller calls are better left there. Measured (us, through the caches and
+// past them): 8192 bf16 rows, N 12288, K 4096 250 and 231; 65536 rows of 8 of 64
+// experts, N 1536, K 2048 184 and 162; 4096 fp32 rows, N 8192, K 2048, 147 MB
+// in all: 56 and 63.
+constexpr int64_t kStreamBytes = 192LL << 20;
+
 // Work-items of one launch at most: a launch of 2^32 or more loses those beyond
 // a multiple of it without an error, so larger work takes several launches.
 constexpr int64_t kLaunchItems = 1LL << 31;
@@ -84,6 +93,7 @@ struct Mx4Args {
     int64_t M, N, K;          // gather: M = R
     int64_t xsstride, wsstride;
     int ydt;
+    int stream;               // y goes past the caches
     // a float x, quantized inside the kernel (streaming kernel, few rows)
     const void* x;
     int xdt, swiglu;
@@ -125,6 +135,7 @@ struct Mx4Prepare {
     int dt;
     int64_t rows, K;
     int swiglu;
+    int stream;               // x goes past the caches
     uint32_t* xq;
     uint8_t* xs;
     int64_t sstride;

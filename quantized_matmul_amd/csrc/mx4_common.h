@@ -28,17 +28,20 @@ struct Eight {
     }
 };
 
-// 16-byte loads where `vec` (the tensor is 16-byte aligned and i a multiple of 8).
-template <int DT>
+// 16-byte loads where `vec` (the tensor is 16-byte aligned and i a multiple of 8); STREAM: past the caches.
+template <int DT, bool STREAM = false>
 __device__ __forceinline__ Eight<DT> load8(const void* p, int64_t i, bool vec) {
     Eight<DT> r;
     constexpr int N = DT == QLIN_F32 ? 8 : 4;
     if (vec) {
-        const uint4* q = (const uint4*)((const char*)p + i * (DT == QLIN_F32 ? 4 : 2));
+        typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+        const u32x4* q = (const u32x4*)((const char*)p + i * (DT == QLIN_F32 ? 4 : 2));
 #pragma unroll
         for (int h = 0; h < N / 4; ++h) {
-            const uint4 t = q[h];
-            r.d[4 * h] = t.x; r.d[4 * h + 1] = t.y; r.d[4 * h + 2] = t.z; r.d[4 * h + 3] = t.w;
+            u32x4 t;
+            if constexpr (STREAM) t = __builtin_nontemporal_load(q + h);
+            else t = q[h];
+            r.d[4 * h] = t[0]; r.d[4 * h + 1] = t[1]; r.d[4 * h + 2] = t[2]; r.d[4 * h + 3] = t[3];
         }
     } else if constexpr (DT == QLIN_F32) {
 #pragma unroll

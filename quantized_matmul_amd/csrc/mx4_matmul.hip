@@ -506,6 +506,8 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
     // acc[tn][tm][r] = D[n][m]: m = lane % 32, n = 8 (r / 4) + 4 (lane / 32) + r % 4.
     // Each wave lays 32 rows m of its TN * 32 columns out in LDS and stores
     // them by rows; no other wave reads them.
+    // In large calls y goes past the caches, which otherwise lose x and W to it
+    // just when the next tiles start.
     constexpr int OROW = S::orow(YS), PER = 16 / YS, LPR = TN * 32 / PER;   // values and lanes of a 16-byte store
     unsigned char* const ot = smem + wv * 32 * OROW;
     const int nw0 = n0 + 32 * TN * wn;
@@ -521,22 +523,28 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
                 store4<YDT>(ot + i * OROW, 32 * tn + 8 * g + 4 * j, c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]);
             }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        auto rows_out = [&](auto stream) {     // a loop each: in one, the two kinds of store would be merged
 #pragma unroll 4
-        for (int r = lane / LPR; r < 32; r += 64 / LPR) {
-            const int c = (lane % LPR) * PER, n = nw0 + c;
-            if (mb + r >= rows || n >= a.N) continue;
-            const int64_t dst = GATHER ? (int64_t)p.plan.perm[m0 + mb + r] : m0 + mb + r;
-            unsigned char* const to = (unsigned char*)a.y + (dst * a.N + n) * YS;
-            if (n + PER <= a.N) {
-                const u32x4 v = *(const u32x4*)(ot + r * OROW + c * YS);
-                __builtin_memcpy(to, &v, 16);                  // a row of an odd N starts at any element
-            } else {
-                for (int q = 0; n + q < a.N; ++q) {
-                    if constexpr (YS == 4) ((uint32_t*)to)[q] = *(const uint32_t*)(ot + r * OROW + (c + q) * 4);
-                    else ((uint16_t*)to)[q] = *(const uint16_t*)(ot + r * OROW + (c + q) * 2);
+            for (int r = lane / LPR; r < 32; r += 64 / LPR) {
+                const int c = (lane % LPR) * PER, n = nw0 + c;
+                if (mb + r >= rows || n >= a.N) continue;
+                const int64_t dst = GATHER ? (int64_t)p.plan.perm[m0 + mb + r] : m0 + mb + r;
+                unsigned char* const to = (unsigned char*)a.y + (dst * a.N + n) * YS;
+                if (n + PER <= a.N) {
+                    const u32x4 v = *(const u32x4*)(ot + r * OROW + c * YS);
+                    typedef u32x4 __attribute__((aligned(2))) any_u32x4;   // a row of an odd N starts at any element
+                    if constexpr (decltype(stream)::value) __builtin_nontemporal_store(v, (any_u32x4*)to);
+                    else *(any_u32x4*)to = v;
+                } else {
+                    for (int q = 0; n + q < a.N; ++q) {
+                        if constexpr (YS == 4) ((uint32_t*)to)[q] = *(const uint32_t*)(ot + r * OROW + (c + q) * 4);
+                        else ((uint16_t*)to)[q] = *(const uint16_t*)(ot + r * OROW + (c + q) * 2);
+                    }
                 }
             }
-        }
+        };
+        if (a.stream) rows_out(std::true_type());
+        else rows_out(std::false_type());
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 }
@@ -609,7 +617,8 @@ constexpr TileShape kTile[kTiles] = {{256, 256, 512, 1, 9.5f, 1.72f, 1.72f},
 
 template <int YDT, bool GATHER>
 hipError_t tiled_rows(const Mx4Args& a, const Mx4Plan& plan, int tile, hipStream_t st) {
-    const TiledArgs p{a, plan, FastDiv::by(GATHER ? (uint32_t)(a.M / a.B) : 1), 0, device_shape().xcds, debug_lds_nan() ? 1 : 0};
+    const TiledArgs p{a, plan, FastDiv::by(GATHER ? (uint32_t)(a.M / a.B) : 1), 0, device_shape().xcds,
+                      debug_lds_nan() ? 1 : 0};
     switch (tile) {
     case 0: return tiled_launch<256, 256, 4, 2, 2, YDT, GATHER>(p, st);
     case 1: return tiled_launch<128, 128, 2, 2, 2, YDT, GATHER>(p, st);

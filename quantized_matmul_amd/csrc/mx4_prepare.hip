@@ -139,7 +139,7 @@ __device__ __forceinline__ void plan_place(const PrepareArgs& a, int chunk, uint
         if (r0 + c * THREADS < a.R) a.plan.perm[at[c]] = (uint32_t)(r0 + c * THREADS);
 }
 
-template <int DT>
+template <int DT, bool STREAM>
 __device__ __forceinline__ void activation(const PrepareArgs& a, int64_t wid) {
     const bool live = wid < a.words;                 // whole blocks of 4 lanes are live or not
     const int64_t w0 = live ? wid : 0;
@@ -148,10 +148,11 @@ __device__ __forceinline__ void activation(const PrepareArgs& a, int64_t wid) {
     uint32_t byte, word;
     if (a.swiglu) {
         const int64_t at = (row * a.row_words + w0) * 8;
-        const Eight<DT> gate = load8<DT>(a.x, at, a.vec), up = load8<DT>(a.x, at + (int64_t)a.row_words * 8, a.vec);
+        const Eight<DT> gate = load8<DT, STREAM>(a.x, at, a.vec),
+                         up = load8<DT, STREAM>(a.x, at + (int64_t)a.row_words * 8, a.vec);
         word = mxfp4_word<QLIN_F32>(swiglu8<DT>(gate, up), &byte);
     } else {
-        word = mxfp4_word<DT>(load8<DT>(a.x, w0 * 8, a.vec), &byte);
+        word = mxfp4_word<DT>(load8<DT, STREAM>(a.x, w0 * 8, a.vec), &byte);
     }
     uint8_t* const s = a.xs + row * a.sstride;
     const uint32_t blk = col >> 2;
@@ -189,7 +190,7 @@ __device__ __forceinline__ void pad_unit(const Mx4Scales& p, const FastDiv& by_u
 }
 
 // Workgroups in order: the plan (with several chunks, its counts), the activation, scale rows.
-template <int DT>
+template <int DT, bool STREAM>
 __global__ void __launch_bounds__(THREADS) mx4_prepare_kernel(PrepareArgs a) {
     extern __shared__ uint32_t sh[];
     int b = blockIdx.x;
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(THREADS) mx4_prepare_kernel(PrepareArgs a) {
         }
         b -= a.chunks;
     }
-    if (b < a.act_blocks) return activation<DT>(a, (int64_t)b * THREADS + threadIdx.x);
+    if (b < a.act_blocks) return activation<DT, STREAM>(a, (int64_t)b * THREADS + threadIdx.x);
     b -= a.act_blocks;
     const int which = b < a.pad_blocks[0] ? 0 : 1;
     if (which) b -= a.pad_blocks[0];
@@ -274,9 +275,10 @@ hipError_t launch_mx4_prepare(const Mx4Prepare& q, Mx4Plan* plan, hipStream_t st
             a.pad[w].rows = take(padded[w], q.pad[w].rows, units, &a.pad_blocks[w]);
         }
         if (blocks) {
-            if (q.dt == QLIN_F32) mx4_prepare_kernel<QLIN_F32><<<(unsigned)blocks, THREADS, shm, st>>>(a);
-            else if (q.dt == QLIN_F16) mx4_prepare_kernel<QLIN_F16><<<(unsigned)blocks, THREADS, shm, st>>>(a);
-            else mx4_prepare_kernel<QLIN_BF16><<<(unsigned)blocks, THREADS, shm, st>>>(a);
+            auto kernel = q.stream ? mx4_prepare_kernel<QLIN_BF16, true> : mx4_prepare_kernel<QLIN_BF16, false>;
+            if (q.dt == QLIN_F32) kernel = q.stream ? mx4_prepare_kernel<QLIN_F32, true> : mx4_prepare_kernel<QLIN_F32, false>;
+            if (q.dt == QLIN_F16) kernel = q.stream ? mx4_prepare_kernel<QLIN_F16, true> : mx4_prepare_kernel<QLIN_F16, false>;
+            kernel<<<(unsigned)blocks, THREADS, shm, st>>>(a);
         }
         if (a.chunks > 1) mx4_place_kernel<<<(unsigned)a.chunks, THREADS, shm, st>>>(a);
         a.experts = nullptr;                         // the plan is on its way

@@ -549,3 +549,30 @@ def test_product_of_more_words_than_a_launch_holds():
     y = qm.mxfp4_matmul(x, qw, out_dtype=torch.float32)
     for m in range(0, M, 2 ** 20):
         assert torch.equal(y[m:m + 2 ** 20], qm.mxfp4_matmul(x[m:m + 2 ** 20], qw, out_dtype=torch.float32)), m
+
+
+def test_large_calls_that_pass_the_caches():
+    """Calls of over 192 MB store (and read x) with other instructions: the same bits as in parts."""
+    qw = weight((6200, 96), 980)
+    x = torch.empty((8192, 96), dtype=torch.bfloat16, device=DEV).normal_()
+    y = qm.mxfp4_matmul(x, qw, out_dtype=torch.float32)
+    qe = weight((4, 6200, 96), 981)
+    ids = torch.randint(-1, 4, (8192, 1), dtype=torch.int32, device=DEV)
+    ye = qm.gather_mxfp4_matmul(x, qe, ids, out_dtype=torch.float32)
+    for m in range(0, 8192, 1024):
+        s = slice(m, m + 1024)
+        assert torch.equal(y[s], qm.mxfp4_matmul(x[s], qw, out_dtype=torch.float32)), m
+        assert torch.equal(ye[s], qm.gather_mxfp4_matmul(x[s], qe, ids[s], out_dtype=torch.float32)), m
+    qw = weight((40, 4096), 982)
+    x = torch.empty((16000, 8192), dtype=torch.float16, device=DEV).normal_()
+    y = qm.mxfp4_matmul(x, qw, activation="swiglu")
+    for m in range(0, 16000, 1000):
+        assert torch.equal(y[m:m + 1000], qm.mxfp4_matmul(x[m:m + 1000], qw, activation="swiglu")), m
+    h, w = torch.empty((6000, 3, 4096), dtype=torch.bfloat16, device=DEV).normal_(), torch.rand((6000, 3), device=DEV)
+    gy = torch.empty((6000, 4096), dtype=torch.bfloat16, device=DEV).normal_()
+    y, (gh, gw) = qm.moe_combine(h, w), qm.moe_combine_grad(gy, h, w)
+    for t in range(0, 6000, 1000):
+        s = slice(t, t + 1000)
+        assert torch.equal(y[s], qm.moe_combine(h[s], w[s])), t
+        pgh, pgw = qm.moe_combine_grad(gy[s], h[s], w[s])
+        assert torch.equal(gh[s], pgh) and torch.equal(gw[s], pgw), t
