@@ -120,10 +120,11 @@ __device__ __forceinline__ float softmax_terms(const float (&x)[V], float top, f
 // Floats as unsigned numbers of the same order, so that a step of a maximum
 // over lanes is one instruction: 0 below every number, for "none"; -0 counts
 // as +0.
-__device__ __forceinline__ uint32_t order_of(float f) {
-    const uint32_t u = __float_as_uint(f + 0.0f);
+__device__ __forceinline__ uint32_t order_of_sum(float f) {   // f is not -0
+    const uint32_t u = __float_as_uint(f);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ uint32_t order_of(float f) { return order_of_sum(f + 0.0f); }
 __device__ __forceinline__ float value_of(uint32_t o) {
     return __uint_as_float(o ^ ((uint32_t)(~(int32_t)o >> 31) | 0x80000000u));
 }
@@ -143,6 +144,12 @@ __device__ __forceinline__ float row_max(const float (&x)[V]) {
 #pragma unroll
     for (int v = 0; v < V; ++v) o[v] = order_of(x[v]);
     return value_of(wave_max(largest<V>(o)));
+}
+
+// (m1, m2) the two largest of themselves and x.
+__device__ __forceinline__ void insert2(uint32_t& m1, uint32_t& m2, uint32_t x) {
+    m2 = max_u(min_u(m1, m2), min_u(max_u(m1, m2), x));    // the median: one instruction
+    m1 = max_u(m1, x);
 }
 
 // (m1, m2) the two largest of the lane's and a partner's two largest.
@@ -200,7 +207,7 @@ __device__ __forceinline__ bool in_best_groups(const RouteArgs& a, const uint32_
     // join the lanes' two largest over DPP inside rows of 16 lanes (each step
     // joins two blocks that already agree), by shuffles beyond
 #pragma unroll
-    for (int v = 0; v < V; ++v) merge2(m1, m2, f[v], NONE);
+    for (int v = 0; v < V; ++v) insert2(m1, m2, f[v]);
     if (a.seg > 1) merge2(m1, m2, dpp_u<0xB1>(m1), dpp_u<0xB1>(m2));      // quad_perm 1 0 3 2
     if (a.seg > 2) merge2(m1, m2, dpp_u<0x4E>(m1), dpp_u<0x4E>(m2));      // quad_perm 2 3 0 1
     if (a.seg > 4) merge2(m1, m2, dpp_u<0x141>(m1), dpp_u<0x141>(m2));    // row_half_mirror
@@ -232,7 +239,7 @@ __device__ __forceinline__ uint64_t best_groups(const RouteArgs& a, const uint32
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     uint32_t m1 = NONE, m2 = NONE, g = NONE;
     if (lane < a.groups) {
-        for (int e = 0; e < per; ++e) merge2(m1, m2, row[lane * per + e], NONE);
+        for (int e = 0; e < per; ++e) insert2(m1, m2, row[lane * per + e]);
         g = group_key(a, m1, m2);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -318,17 +325,27 @@ __global__ void __launch_bounds__(64 * ROUTE_WAVES) route_kernel(RouteArgs a) {
 #pragma unroll
         for (int v = 0; v < V; ++v) s[v] = sigmoid_of(x[v]);
     }
+    // NaN fails the comparison
+    if (a.bias) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const float b = a.bias ? s[v] + bias[v] : x[v];
-        key[v] = b > -INFINITY && x[v] > -INFINITY ? order_of(b) : NONE;   // NaN fails the comparison
+        for (int v = 0; v < V; ++v) {
+            const float b = __builtin_fmaf(x[v], 0.0f, s[v] + bias[v]);    // NaN where the logit is -inf
+            key[v] = b > -INFINITY ? order_of_sum(b) : NONE;
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = x[v] > -INFINITY ? order_of(x[v]) : NONE;
     }
     uint32_t* const chosen = lds[wv] + lane / L * kPlaces;
     uint2* const list = (uint2*)(lds[wv] + 64 / L * kPlaces) + lane;          // [V][64]
     if (grouped) {
         uint32_t f[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) f[v] = a.bias || a.group_top == 1 || key[v] == NONE ? key[v] : order_of(s[v]);
+        for (int v = 0; v < V; ++v) f[v] = key[v];
+        if (!a.bias && a.group_top == 2) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) f[v] = key[v] == NONE ? NONE : order_of_sum(s[v]);
+        }
         if (a.seg) {
             const bool in = in_best_groups<L, V>(a, f, lane);
 #pragma unroll
@@ -353,7 +370,8 @@ __global__ void __launch_bounds__(64 * ROUTE_WAVES) route_kernel(RouteArgs a) {
         double kp[V];
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            kp[v] = __hiloint2double((int)(0x10000000u | key[v] >> 24), (int)(key[v] << 8 | (uint32_t)(V - 1 - v)));
+            kp[v] = __hiloint2double((int)__builtin_amdgcn_alignbit(0x00100000u, key[v], 24),
+                                     (int)(key[v] << 8 | (uint32_t)(V - 1 - v)));
         constexpr Sorter net = sorter(V);
 #pragma unroll
         for (int c = 0; c < net.n; ++c) {
