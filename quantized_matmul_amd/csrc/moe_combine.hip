@@ -8,7 +8,9 @@
 // their rows of h hold does not matter, dh and dw get zeros. Sums are fp32 in a
 // fixed order; each output is rounded once. Both kernels are bound by HBM, and
 // by one round trip where there are few tokens: so all rows of a token are on
-// their way before any is used.
+// their way before any is used. 8192 tokens of 8 rows of 4096 bf16 values: 108
+// us (5.6 TB/s), the gradient 191 us (6.0 TB/s); 515 tokens of 6 rows of 2568:
+// 5.5 us; one token 2.6 us.
 
 #include "qlin_common.h"
 #include "mx4_common.h"

@@ -22,7 +22,11 @@
 // A token takes L lanes, 16 (a DPP row, four tokens a wave) up to 256 experts
 // and a wave beyond; lane l holds experts l V .. l V + V - 1 (V = 1, 2, 4, 8
 // or 16), so that the first of the lanes with equal keys has the lowest index.
-// Everything is fp32.
+// A lane sorts its keys once, then each of k rounds takes the largest head of
+// the lanes: at 16384 tokens of 256 experts in groups 28 us with a wave a token
+// and k passes over all values, 11.2 so. Everything is fp32.
+// Bound by instructions there (1000 for four tokens; its bytes would take 3.7
+// us), by the launch for few tokens (one token 2.7 us; 8191 of 60 experts 3.8).
 
 #include "qlin_common.h"
 #include "moe_common.h"
@@ -446,6 +450,7 @@ struct RouteGradArgs {
 
 // Lane j works out the gradient of place j's logit; LDS carries it to the
 // lane that writes that logit. Only softmax needs the whole row of logits.
+// Latency-bound: 8191 tokens of 60 experts, 4 chosen, 4.0 us.
 template <int DT, int V>
 __global__ void __launch_bounds__(64 * ROUTE_WAVES) route_grad_kernel(RouteGradArgs a) {
     extern __shared__ float lds[];               // [waves][64 V]

@@ -22,8 +22,15 @@
 //    workgroup, K split over its waves, W straight from memory into the
 //    instruction's registers, partial sums joined through LDS. Up to 4 rows of
 //    a float x are quantized by each wave for its own part of K, which costs
-//    less than the launch it saves.
-//  * tiled (many rows): bound by the matrix cores and LDS. See mx4_tiled_kernel.
+//    less than the launch it saves. One row, N 14336, K 4096: 8.4 us (3.7 TB/s
+//    with the launch); one token by 8 experts, N 1536, K 2048: 7.0 us; 16 rows
+//    of codes, N = K = 8192: 11.8 us.
+//  * tiled (many rows): bound by power, which holds the clock (matrix cores alone
+//    5.9 PFLOP/s; a step of 256 codes takes a 256 x 256 tile 2.1 us with random
+//    codes, 1.35 with zeros), and at small K by the start and outputs of a tile.
+//    8192 rows, N 12288, K 4096: 219 us (3.8 PFLOP/s); N = K = 8192: 284 us (3.9);
+//    65536 rows by 64 experts, N 4096, K 2048: 415 us (2.7); 512 tokens by 8 of
+//    64 experts, N 1536, K 2048: 34 us, 3.2 TB/s of W.
 
 #include "mx4_common.h"
 

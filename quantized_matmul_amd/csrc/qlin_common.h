@@ -20,7 +20,7 @@ struct DeviceShape {
 DeviceShape device_shape();
 
 // QLIN_DEBUG_LDS_NAN=1: the LDS-tiled kernels (many-row, pipelined 4-bit,
-// scaled fp8) fill their whole LDS with NaN bytes before each tile, so a
+// scaled fp8, mxfp4) fill their whole LDS with NaN bytes before each tile, so a
 // read of LDS that no load or store of the tile wrote -- a missing wait or
 // barrier, a wrong index -- turns the output into NaN. Read at each launch.
 bool debug_lds_nan();
