@@ -127,7 +127,8 @@ qlin_status product(const void* x, int x_dtype, const void* x_scales, const char
         return fail(QLIN_ERR_UNSUPPORTED, "x has more than 2^32 values: split its rows over several calls");
     // W's scales, whole 16-byte rows at an address that is none: the streaming kernel takes any
     const bool odd = tiled && (K / 32) % 16 == 0 && (uintptr_t)scales % 16;
-    if (!qlin::mx4_fits(R, N, K, E, gather, odd ? qlin::Mx4Choice{qlin::Mx4Path::kStream, -1, 0} : c))
+    const qlin::Mx4Choice run = odd ? qlin::Mx4Choice{qlin::Mx4Path::kStream, -1, 0} : c;
+    if (!qlin::mx4_fits(R, N, K, E, gather, run))
         return fail(QLIN_ERR_UNSUPPORTED, "more output tiles than one launch holds: split the rows over several calls");
     const Layout l = layout(c, rows, R, K, E, N, codes, gather);
     if (l.bytes) {
@@ -206,7 +207,7 @@ qlin_status product(const void* x, int x_dtype, const void* x_scales, const char
         }
     }
     if (prepare && (e = qlin::launch_mx4_prepare(q, &plan, st)) != hipSuccess) return device_status(e, what);
-    e = odd ? qlin::launch_mx4_stream_blocks(a, st) : qlin::launch_mx4_matmul(a, c, &plan, st);
+    e = qlin::launch_mx4_matmul(a, run, &plan, st);
     if (e == hipSuccess)
         qlin::record_path(tiled && !odd ? (gather ? "mxfp4_gather_tiled" : "mxfp4_tiled")
                                         : (gather ? "mxfp4_gather_stream" : "mxfp4_stream"));

@@ -117,9 +117,6 @@ bool mx4_fits(int64_t M, int64_t N, int64_t K, int64_t E, bool gather, const Mx4
 Mx4Choice mx4_choose(int64_t M, int64_t N, int64_t K, int64_t E, bool gather, bool codes);
 hipError_t launch_mx4_matmul(const Mx4Args& a, const Mx4Choice& c, const struct Mx4Plan* plan, hipStream_t st);
 
-// The streaming kernel on x's codes for any number of rows: blocks of 16 (by experts: one row each).
-hipError_t launch_mx4_stream_blocks(const Mx4Args& a, hipStream_t st);
-
 // Scale rows of KS bytes to copy to rows of whole 16-byte units, filled with 127.
 struct Mx4Scales {
     const uint8_t* from;

@@ -18,11 +18,12 @@
 // dword, and op_sel alone steps through them.
 //
 // Two kernels:
-//  * streaming (up to 16 rows): bound by reading W once. 16 weight rows per
-//    workgroup, K split over its waves, W straight from memory into the
-//    instruction's registers, partial sums joined through LDS. Up to 4 rows of
-//    a float x are quantized by each wave for its own part of K, which costs
-//    less than the launch it saves. One row, N 14336, K 4096: 8.4 us (3.7 TB/s
+//  * streaming (few rows): bound by reading W. 16 weight rows per workgroup, K
+//    split over its waves, W straight from memory into the instruction's
+//    registers, partial sums joined through LDS. Blocks of 16 rows of codes, 4 of
+//    a float x, which each wave quantizes for its own part of K, or by experts
+//    one index row: each block reads W for itself, which costs less than the
+//    launch it saves while W is small. One row, N 14336, K 4096: 8.4 us (3.7 TB/s
 //    with the launch); one token by 8 experts, N 1536, K 2048: 7.0 us; 16 rows
 //    of codes, N = K = 8192: 11.8 us.
 //  * tiled (many rows): bound by power, which holds the clock (matrix cores alone
@@ -89,14 +90,15 @@ __device__ __forceinline__ void store4(void* y, int64_t i, float a, float b, flo
 
 // ------------------------------------------------------------- streaming
 
-constexpr int STREAM_ROWS = 16;        // rows of x the kernel takes
+constexpr int STREAM_ROWS = 16;        // rows of x of a workgroup
 constexpr int STREAM_FLOAT_ROWS = 4;   // ... of a float x
 constexpr int STREAM_WAVES = 16;
 
 struct StreamArgs {
     Mx4Args a;
     uint32_t per_entry;    // index rows per row of x (DIRECT)
-    int tiles_n;
+    int tiles_n;           // workgroups of a block of rows
+    FastDiv by_tiles;      // workgroup / tiles_n
     int vec;               // a float x is 16-byte aligned
 };
 
@@ -125,21 +127,25 @@ __device__ __forceinline__ Piece load_piece(const uint8_t* c, const uint8_t* s, 
     return p;
 }
 
-// DIRECT: one index row a workgroup, with its expert's W; else up to 16 rows of
-// x. XDT QLIN_U8: x's codes; else a float x of up to 4 rows, quantized here.
+// Rows of a workgroup: by experts (DIRECT) one index row, with its expert's W.
+template <int XDT, bool DIRECT>
+constexpr int stream_block() { return DIRECT ? 1 : XDT == QLIN_U8 ? STREAM_ROWS : STREAM_FLOAT_ROWS; }
+
+// XDT QLIN_U8: x's codes; else a float x, quantized here.
 template <int YDT, int XDT, bool DIRECT>
 __global__ void __launch_bounds__(64 * STREAM_WAVES) mx4_stream_kernel(StreamArgs s) {
     constexpr bool FLOAT = XDT != QLIN_U8;
-    constexpr int XR = DIRECT ? 1 : STREAM_FLOAT_ROWS;
+    constexpr int XR = stream_block<XDT, DIRECT>();
     extern __shared__ __align__(16) uint32_t lds[];     // partial sums [waves][16][16]; codes of a float x
     const Mx4Args& a = s.a;
     const int tid = threadIdx.x, lane = tid & 63, waves = blockDim.x >> 6;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i = lane & 15, q = lane >> 4;
-    const uint32_t tile = DIRECT ? blockIdx.x / (uint32_t)s.tiles_n : 0;
+    const uint32_t tile = s.by_tiles(blockIdx.x);                       // block of rows
     const int64_t n0 = (int64_t)(blockIdx.x - tile * (uint32_t)s.tiles_n) * 16;
-    const int rows = DIRECT ? 1 : (int)a.M;
-    const int64_t src = DIRECT ? (int64_t)(tile / s.per_entry) : 0;     // first row of x
+    const int64_t m0 = (int64_t)tile * XR;                              // first row of y
+    const int rows = (int)(a.M - m0 < XR ? a.M - m0 : XR);
+    const int64_t src = DIRECT ? (int64_t)(tile / s.per_entry) : m0;    // ... and of x
     const uint32_t expert = DIRECT ? (uint32_t)a.experts[tile] : 0;
 
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(64 * STREAM_WAVES) mx4_stream_kernel(StreamArg
         float v = 0.0f;
         for (int w = 0; w < waves; ++w) v += red[w * 256 + o];
         const int m = o >> 4, n = o & 15;
-        if (n0 + n < a.N) store_f<YDT>(a.y, ((DIRECT ? (int64_t)tile : m)) * a.N + n0 + n, v);
+        if (n0 + n < a.N) store_f<YDT>(a.y, (m0 + m) * a.N + n0 + n, v);
     }
 }
 
@@ -560,23 +566,27 @@ __global__ void __launch_bounds__(64 * WN * WM) mx4_tiled_kernel(TiledArgs p) {
 
 // ---------------------------------------------------------------- dispatch
 
+// Reads of W by a float x's blocks of rows.
+int64_t stream_reads(int64_t M, bool gather) { return gather ? M : (M + STREAM_FLOAT_ROWS - 1) / STREAM_FLOAT_ROWS; }
+
 // Waves of a workgroup: a wave takes one run, or two where that lets all of W's loads be in flight at once (four waves
-// a SIMD).
-int stream_waves(int64_t tiles_m, int64_t N, int64_t K) {
+// a SIMD). Codes take as many as a float x, so that both give the same bits.
+int stream_waves(int64_t reads, int64_t N, int64_t K) {
     int64_t runs = (K + 511) / 512;
-    if (tiles_m * ((N + 15) / 16) * runs > 16 * (int64_t)device_shape().cus) runs = (runs + 1) / 2;
+    if (reads * ((N + 15) / 16) * runs > 16 * (int64_t)device_shape().cus) runs = (runs + 1) / 2;
     return (int)(runs < STREAM_WAVES ? runs : STREAM_WAVES);
 }
 
 template <int YDT, int XDT, bool DIRECT>
 hipError_t stream_launch(const Mx4Args& a, hipStream_t st) {
-    const int waves = stream_waves(DIRECT ? a.M : 1, a.N, a.K);
-    StreamArgs s{a, DIRECT ? (uint32_t)(a.M / a.B) : 1, (int)((a.N + 15) / 16), ((uintptr_t)a.x & 15) == 0};
-    const int64_t blocks = (DIRECT ? a.M : 1) * s.tiles_n;
-    if (!DIRECT && a.M > (XDT == QLIN_U8 ? STREAM_ROWS : STREAM_FLOAT_ROWS)) return hipErrorInvalidValue;
-    const size_t floats = XDT == QLIN_U8 ? 0 : (DIRECT ? 1 : STREAM_FLOAT_ROWS) * 68;
+    constexpr int ROWS = stream_block<XDT, DIRECT>();
+    const int64_t tiles_m = (a.M + ROWS - 1) / ROWS;
+    const int waves = stream_waves(stream_reads(a.M, DIRECT), a.N, a.K);
+    const int tiles_n = (int)((a.N + 15) / 16);
+    StreamArgs s{a, DIRECT ? (uint32_t)(a.M / a.B) : 1, tiles_n, FastDiv::by((uint32_t)tiles_n), ((uintptr_t)a.x & 15) == 0};
+    const size_t floats = XDT == QLIN_U8 ? 0 : ROWS * 68;
     mx4_stream_kernel<YDT, XDT, DIRECT>
-        <<<(unsigned)blocks, 64 * waves, (size_t)waves * (256 + floats) * sizeof(uint32_t), st>>>(s);
+        <<<(unsigned)(tiles_m * s.tiles_n), 64 * waves, (size_t)waves * (256 + floats) * sizeof(uint32_t), st>>>(s);
     return hipGetLastError();
 }
 
@@ -648,7 +658,7 @@ hipError_t launch(const Mx4Args& a, const Mx4Choice& c, const Mx4Plan* plan, hip
     return a.experts ? tiled_rows<YDT, true>(a, *plan, c.tile, st) : tiled_rows<YDT, false>(a, Mx4Plan{}, c.tile, st);
 }
 
-// QLIN_MXFP4_TILE=0..4 forces a tile of the tiled kernel (tests run every one on the same inputs).
+// QLIN_MXFP4_TILE=0..4 forces the tiled kernel and its tile (tests run every one on the same inputs).
 int forced_tile() {
     const char* e = getenv("QLIN_MXFP4_TILE");
     return e && e[0] >= '0' && e[0] < '0' + kTiles && !e[1] ? e[0] - '0' : -1;
@@ -656,16 +666,24 @@ int forced_tile() {
 
 }  // namespace
 
-// Dense: up to 16 rows stream. By experts: while index rows are few against the
-// experts, hardly two share one, and each streams its expert's W without a plan.
+// Few rows stream, each (dense: each 4) with a read of W of its own and x
+// rounded on the way, where that costs less than the launch and the plan that it
+// saves: up to 12 MB of such reads dense and 24 MB by experts (measured around
+// them, us streamed and not: 13 rows, N 653, K 3712 6.5 and 8.8; 36 rows, N
+// 5578, K 800, 20 MB 13.7 and 9.0; 51 by 10 experts, N 462, K 1952 7.3 and 9.6;
+// 210 by 32, N 393, K 768, 32 MB 11.4 and 9.5), and by experts also while index
+// rows are no more than experts, hardly two of which share one. Dense, up to 16
+// rows stream from codes.
 // Beyond, the tile whose rounds over the CUs take least. An expert's last row
 // tile is half empty on average, so R rows make R / m + E / 2 tiles, or one an
 // expert if that is more. Over 223 drawn sizes the choice costs 1.3% more than
 // the best of the five tiles on average and 18% at most.
 Mx4Choice mx4_choose(int64_t M, int64_t N, int64_t K, int64_t E, bool gather, bool codes) {
-    if (gather ? 2 * M <= E : M <= STREAM_ROWS)
-        return {codes || (!gather && M > STREAM_FLOAT_ROWS) ? Mx4Path::kStream : Mx4Path::kStreamFloat, -1, 0};
     int tile = forced_tile();
+    const int64_t reads = stream_reads(M, gather);
+    const bool again = reads == 1 || (double)reads * N * K * 0.5 <= (gather ? 24e6 : 12e6);
+    if (tile < 0 && (gather ? M <= E || again : M <= STREAM_ROWS || again))
+        return {codes || (!gather && !again) ? Mx4Path::kStream : Mx4Path::kStreamFloat, -1, 0};
     if (tile < 0) {
         const int64_t cus = device_shape().cus, steps = (K + 255) / 256;
         double best = 0;
@@ -690,8 +708,9 @@ Mx4Choice mx4_choose(int64_t M, int64_t N, int64_t K, int64_t E, bool gather, bo
 
 bool mx4_fits(int64_t M, int64_t N, int64_t K, int64_t E, bool gather, const Mx4Choice& c) {
     if (c.path != Mx4Path::kTiled) {
-        const int64_t tiles_m = gather ? M : 1;
-        return tiles_m * ((N + 15) / 16) <= 2 * kLaunchItems / (64 * stream_waves(tiles_m, N, K)) - 1;
+        const int rows = gather ? 1 : c.path == Mx4Path::kStream ? STREAM_ROWS : STREAM_FLOAT_ROWS;
+        return (M + rows - 1) / rows * ((N + 15) / 16) <=
+               2 * kLaunchItems / (64 * stream_waves(stream_reads(M, gather), N, K)) - 1;
     }
     const TileShape& s = kTile[c.tile];
     const int64_t m = gather ? mx4_plan_max_tiles(M, E, s.m) : (M + s.m - 1) / s.m;
@@ -702,21 +721,6 @@ hipError_t launch_mx4_matmul(const Mx4Args& a, const Mx4Choice& c, const Mx4Plan
     if (a.ydt == QLIN_BF16) return launch<QLIN_BF16>(a, c, plan, st);
     if (a.ydt == QLIN_F16) return launch<QLIN_F16>(a, c, plan, st);
     return launch<QLIN_F32>(a, c, plan, st);
-}
-
-hipError_t launch_mx4_stream_blocks(const Mx4Args& a, hipStream_t st) {
-    const Mx4Choice c{Mx4Path::kStream, -1, 0};
-    if (a.experts) return launch_mx4_matmul(a, c, nullptr, st);
-    for (int64_t m0 = 0; m0 < a.M; m0 += STREAM_ROWS) {
-        Mx4Args b = a;
-        b.M = a.M - m0 < STREAM_ROWS ? a.M - m0 : STREAM_ROWS;
-        b.xq = a.xq + m0 * (a.K / 2);
-        b.xs = a.xs + m0 * a.xsstride;
-        b.y = (char*)a.y + m0 * a.N * (a.ydt == QLIN_F32 ? 4 : 2);
-        const hipError_t e = launch_mx4_matmul(b, c, nullptr, st);
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
 }
 
 }  // namespace qlin

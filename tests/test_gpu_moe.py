@@ -178,6 +178,21 @@ def close(y, r, K):
     assert e <= tolerance(y.dtype, K), e
 
 
+@pytest.fixture(params=["chosen", "tiled"])
+def form(request, monkeypatch):
+    """Products by the kernel that their sizes choose, and by the tiled one."""
+    if request.param == "tiled":
+        monkeypatch.setenv("QLIN_MXFP4_TILE", "1")
+    return request.param
+
+
+def streams(R, N, K, E=None):
+    """Whether a product chooses the streaming kernel; E: by experts."""
+    if E is None:
+        return R <= 16 or -(-R // 4) * N * K <= 24e6
+    return R <= E or R * N * K <= 48e6
+
+
 DENSE = [(1, 16, 32), (1, 1, 64), (2, 17, 96), (3, 130, 160), (15, 48, 512), (16, 33, 544), (17, 64, 480),
          (31, 257, 1024), (33, 100, 2080), (64, 128, 256), (65, 128, 256), (65, 31, 32), (100, 130, 96),
          (129, 257, 544), (300, 300, 1056), (257, 129, 1536), (512, 256, 4096)]
@@ -185,11 +200,11 @@ DENSE = [(1, 16, 32), (1, 1, 64), (2, 17, 96), (3, 130, 160), (15, 48, 512), (16
 
 @pytest.mark.parametrize("M,N,K", DENSE)
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-def test_dense_product(M, N, K, dtype):
-    print(f"mxfp4_matmul M{M} N{N} K{K} {dtype}", flush=True)
+def test_dense_product(M, N, K, dtype, form):
+    print(f"mxfp4_matmul M{M} N{N} K{K} {dtype} {form}", flush=True)
     qw, x = weight((N, K), 400 + N), rand((M, K), dtype, 500 + M)
     y = qm.mxfp4_matmul(x, qw)
-    assert y.dtype == x.dtype and qm.last_path() == ("mxfp4_tiled" if M > 16 else "mxfp4_stream")
+    assert y.dtype == x.dtype and qm.last_path() == ("mxfp4_stream" if form == "chosen" and streams(M, N, K) else "mxfp4_tiled")
     close(y, ref.mxfp4_round(f64(x)) @ values(qw).T, K)
     # the same codes given as such: the same bits
     if dtype != "f16":
@@ -200,14 +215,14 @@ def test_dense_product(M, N, K, dtype):
 
 @pytest.mark.parametrize("M,N,K", [(1, 64, 96), (40, 130, 544), (200, 257, 320)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-def test_dense_product_swiglu(M, N, K, dtype):
+def test_dense_product_swiglu(M, N, K, dtype, form):
     qw, x = weight((N, K), 410 + N), rand((M, 2 * K), dtype, 510 + M)
     y = qm.mxfp4_matmul(x, qw, activation="swiglu")
     close(y, ref.mxfp4_round(ref.swiglu(f64(x))) @ values(qw).T, K)
 
 
 @pytest.mark.parametrize("M", [3, 80])
-def test_dense_product_types_and_unaligned_views(M):
+def test_dense_product_types_and_unaligned_views(M, form):
     N, K = 70, 288
     qw = weight((N, K), 420)
     flat = rand((M * K + 1,), "bf16", 520)
@@ -222,7 +237,7 @@ def test_dense_product_types_and_unaligned_views(M):
 
 
 @pytest.mark.parametrize("M", [5, 150])
-def test_dense_product_long_scale_rows_at_odd_addresses(M):
+def test_dense_product_long_scale_rows_at_odd_addresses(M, form):
     """K a multiple of 512 with scales that are not 16-byte aligned."""
     N, K = 130, 1024
     qw, x = weight((N, K), 421), rand((M, K), "bf16", 521)
@@ -240,7 +255,7 @@ def test_dense_product_long_scale_rows_at_odd_addresses(M):
 
 @pytest.mark.parametrize("M", [4, 90])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_dense_product_marks_blocks_that_are_not_finite(M, bad):
+def test_dense_product_marks_blocks_that_are_not_finite(M, bad, form):
     qw, x = weight((40, 128), 430), rand((M, 128), "bf16", 530)
     clean = qm.mxfp4_matmul(x, qw)
     x[1, 77] = bad
@@ -252,7 +267,7 @@ def test_dense_product_marks_blocks_that_are_not_finite(M, bad):
 
 @pytest.mark.parametrize("M", [2, 12, 40])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-def test_activation_rounding_is_exact(M, dtype):
+def test_activation_rounding_is_exact(M, dtype, form):
     """Against the identity the product gives the rounded activation itself:
     E2M1 ties and their neighbours at many scales, tiny blocks, signed zeros."""
     K = 160
@@ -272,7 +287,7 @@ def test_activation_rounding_is_exact(M, dtype):
 
 
 @pytest.mark.parametrize("scale", [1e-30, 1e30, 0.0])
-def test_dense_product_extreme_values(scale):
+def test_dense_product_extreme_values(scale, form):
     qw = weight((32, 64), 440)
     x = rand((3, 64), "f32", 540) * scale
     x[0, 32:] = 0.0
@@ -291,31 +306,33 @@ def choices(B, k, E, seed, dropped=0.0, one=None):
 
 
 GATHER = [
-    # B, k, E, N, K, dropped, one expert, path
-    (1, 8, 64, 48, 96, 0.0, None, "mxfp4_gather_stream"),
-    (2, 4, 16, 33, 544, 0.3, None, "mxfp4_gather_stream"),
-    (1, 1, 1, 20, 32, 0.0, None, "mxfp4_gather_tiled"),
-    (5, 3, 4, 130, 160, 0.1, None, "mxfp4_gather_tiled"),
-    (40, 2, 4, 64, 512, 0.0, None, "mxfp4_gather_tiled"),
-    (60, 2, 3, 65, 480, 0.2, None, "mxfp4_gather_tiled"),
-    (50, 4, 8, 70, 256, 0.0, 5, "mxfp4_gather_tiled"),
-    (30, 2, 8, 70, 256, 0.0, -1, "mxfp4_gather_tiled"),
-    (200, 2, 5, 140, 96, 0.1, None, "mxfp4_gather_tiled"),
-    (300, 4, 6, 129, 1056, 0.05, None, "mxfp4_gather_tiled"),
-    (300, 1, 3, 300, 512, 0.0, 2, "mxfp4_gather_tiled"),
-    (150, 2, 3, 40, 64, 0.0, -1, "mxfp4_gather_tiled"),
-    (2600, 2, 7, 64, 128, 0.02, None, "mxfp4_gather_tiled"),
+    # B, k, E, N, K, dropped, one expert
+    (1, 8, 64, 48, 96, 0.0, None),
+    (2, 4, 16, 33, 544, 0.3, None),
+    (1, 1, 1, 20, 32, 0.0, None),
+    (5, 3, 4, 130, 160, 0.1, None),
+    (40, 2, 4, 64, 512, 0.0, None),
+    (60, 2, 3, 65, 480, 0.2, None),
+    (50, 4, 8, 70, 256, 0.0, 5),
+    (30, 2, 8, 70, 256, 0.0, -1),
+    (200, 2, 5, 140, 96, 0.1, None),
+    (300, 4, 6, 129, 1056, 0.05, None),
+    (300, 1, 3, 300, 512, 0.0, 2),
+    (150, 2, 3, 40, 64, 0.0, -1),
+    (2600, 2, 7, 64, 128, 0.02, None),
+    (100, 2, 3, 1040, 1056, 0.1, None),
 ]
 
 
-@pytest.mark.parametrize("B,k,E,N,K,dropped,one,path", GATHER)
-def test_gather_product(B, k, E, N, K, dropped, one, path):
-    print(f"gather_mxfp4_matmul B{B} k{k} E{E} N{N} K{K} {path}", flush=True)
+@pytest.mark.parametrize("B,k,E,N,K,dropped,one", GATHER)
+def test_gather_product(B, k, E, N, K, dropped, one, form):
+    print(f"gather_mxfp4_matmul B{B} k{k} E{E} N{N} K{K} {form}", flush=True)
     qw, x = weight((E, N, K), 600 + N), rand((B, K), "bf16", 700 + B)
     ids = choices(B, k, E, 800 + B, dropped, one)
     t = torch.from_numpy(ids).to(DEV)
     y = qm.gather_mxfp4_matmul(x, qw, t, out_dtype=torch.float32)
-    assert qm.last_path() == path and y.shape == (B, k, N)
+    stream = form == "chosen" and streams(B * k, N, K, E)
+    assert qm.last_path() == ("mxfp4_gather_stream" if stream else "mxfp4_gather_tiled") and y.shape == (B, k, N)
     r = ref.gather_product(ref.mxfp4_round(f64(x)), values(qw), ids)
     close(y, r, K)
     assert (y[t < 0] == 0).all()
@@ -324,7 +341,7 @@ def test_gather_product(B, k, E, N, K, dropped, one, path):
 
 
 @pytest.mark.parametrize("B,E", [(3, 32), (90, 8), (700, 4)])
-def test_gather_product_swiglu_and_types(B, E):
+def test_gather_product_swiglu_and_types(B, E, form):
     N, K = 72, 224
     qw, x = weight((E, N, K), 610), rand((B, 2 * K), "f16", 710)
     ids = choices(B, 1, E, 810, 0.1)
@@ -336,7 +353,7 @@ def test_gather_product_swiglu_and_types(B, E):
     assert y1.shape == (B, N) and torch.equal(y1, y[:, 0])
 
 
-def test_gather_product_experts_out_of_range():
+def test_gather_product_experts_out_of_range(form):
     qw, x = weight((4, 32, 64), 620), rand((100, 64), "bf16", 720)
     ids = choices(100, 2, 4, 820)
     ids[::3, 1] = 4
@@ -348,7 +365,7 @@ def test_gather_product_experts_out_of_range():
     close(y, ref.gather_product(ref.mxfp4_round(f64(x)), values(qw), ids), 64)
 
 
-def test_gather_product_many_experts():
+def test_gather_product_many_experts(form):
     E = 3000
     qw, x = weight((E, 16, 32), 621), rand((2000, 32), "bf16", 721)
     ids = choices(2000, 3, E, 821, 0.01)
@@ -356,7 +373,7 @@ def test_gather_product_many_experts():
     close(y, ref.gather_product(ref.mxfp4_round(f64(x)), values(qw), ids), 32)
 
 
-def test_products_refuse():
+def test_products_refuse(monkeypatch):
     qw, x = weight((32, 64), 630), rand((4, 64), "bf16", 730)
     ids = torch.zeros((4, 2), dtype=torch.int32, device=DEV)
     q8 = qm.quantize(rand((32, 64), "bf16", 1), 32, 8, "mxfp8")
@@ -368,6 +385,7 @@ def test_products_refuse():
             f()
     with pytest.raises(qm.QlinError):
         qm.mxfp4_matmul(x, qw, activation="tanh")
+    monkeypatch.setenv("QLIN_MXFP4_TILE", "1")
     with pytest.raises(qm.QlinError):
         qm.mxfp4_matmul(x.repeat(10, 1), qw, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     qe = weight((2, 32, 64), 631)

@@ -68,9 +68,9 @@ def test_route_grad_rejects(lib):
 
 
 def test_product_rejects(lib):
-    need = lib.qlin_mxfp4_matmul_workspace_bytes(40, 128, 64, BF16)
+    need = lib.qlin_mxfp4_matmul_workspace_bytes(40, 1024, 4096, BF16)
     assert need > 0
-    call = caller(lib.qlin_mxfp4_matmul, dict(x=P, xdt=BF16, xs=None, act=b"none", M=40, K=128, wq=P, ws=P, N=64,
+    call = caller(lib.qlin_mxfp4_matmul, dict(x=P, xdt=BF16, xs=None, act=b"none", M=40, K=1024, wq=P, ws=P, N=4096,
                                               work=P, nb=need, y=P, ydt=BF16, st=None))
     for bad in (dict(xdt=7), dict(ydt=U8), dict(act=b"gelu"), dict(M=-1), dict(K=0), dict(K=48), dict(N=0),
                 dict(x=None), dict(wq=None), dict(ws=None), dict(y=None), dict(xs=P), dict(xdt=U8),
@@ -93,10 +93,11 @@ def test_product_rejects(lib):
 def test_gather_rejects(lib):
     size = lib.qlin_gather_mxfp4_matmul_workspace_bytes
     assert size(4, 8, 128, 16, 64, BF16) == 0    # hardly two rows share an expert: no plan
-    need = size(4, 16, 128, 16, 64, BF16)
+    assert size(4, 32, 128, 16, 64, BF16) == 0   # or W is so small that each reads it for itself
+    need = size(4, 32, 1024, 16, 2048, BF16)
     assert need > 0
-    call = caller(lib.qlin_gather_mxfp4_matmul, dict(x=P, xdt=BF16, xs=None, act=None, B=4, K=128, wq=P, ws=P, E=16,
-                                                     N=64, e=P, R=16, work=P, nb=need, y=P, ydt=F32, st=None))
+    call = caller(lib.qlin_gather_mxfp4_matmul, dict(x=P, xdt=BF16, xs=None, act=None, B=4, K=1024, wq=P, ws=P, E=16,
+                                                     N=2048, e=P, R=32, work=P, nb=need, y=P, ydt=F32, st=None))
     for bad in (dict(R=17), dict(B=0), dict(B=-4), dict(R=-8), dict(E=0), dict(e=None), dict(K=33), dict(nb=need - 1),
                 dict(work=None), dict(e=ODD), dict(act=b"relu"), dict(ydt=U8)):
         assert call(**bad) == INVALID, bad
