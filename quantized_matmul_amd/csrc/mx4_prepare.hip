@@ -20,8 +20,11 @@ namespace qlin {
 namespace {
 
 constexpr int THREADS = 512;
-constexpr int PLAN_PER = 8;                          // index rows of a thread
-constexpr int PLAN_CHUNK = THREADS * PLAN_PER;       // ... and of a workgroup
+constexpr int PLAN_PER = 8;                          // index rows of a thread ...
+constexpr int PLAN_CHUNK = THREADS * PLAN_PER;       // ... and of a workgroup, a chunk
+// A plan of up to two chunks of rows is one of twice the size: longer than a chunk's, but in the first launch (4872
+// rows 17.6 -> 14.7 us for the product; chunks of that size throughout 39.0 -> 42.5 at 16000 rows).
+constexpr int PLAN_ONE = 2;
 
 struct PrepareArgs {
     // activation
@@ -59,17 +62,18 @@ __device__ __forceinline__ void plan_count(const PrepareArgs& a, int chunk, uint
 }
 
 // Places of the rows of chunk `chunk`; chunk 0 writes the tables too. A single
-// chunk counts its rows itself.
+// chunk counts its rows itself. PER: rows of a thread.
+template <int PER>
 __device__ __forceinline__ void plan_place(const PrepareArgs& a, int chunk, uint32_t* sh) {
     const int E = a.E, tid = threadIdx.x;
     uint32_t* const tot = sh;                        // [E + 1] rows of the group
     uint32_t* const cur = sh + E + 1;                // [E + 1] next place of this chunk's rows
     __shared__ uint32_t wsum[THREADS / 64][2], carry[2];
-    const int r0 = chunk * PLAN_CHUNK + tid;
+    const int r0 = chunk * THREADS * PER + tid;
     if (tid < 2) carry[tid] = 0;
-    uint32_t g[PLAN_PER];
+    uint32_t g[PER];
 #pragma unroll
-    for (int c = 0; c < PLAN_PER; ++c) {
+    for (int c = 0; c < PER; ++c) {
         const int r = r0 + c * THREADS;
         g[c] = group_of(a.experts[r < a.R ? r : a.R - 1], E);
     }
@@ -77,7 +81,7 @@ __device__ __forceinline__ void plan_place(const PrepareArgs& a, int chunk, uint
         for (int e = tid; e <= E; e += THREADS) tot[e] = cur[e] = 0;
         __syncthreads();
 #pragma unroll
-        for (int c = 0; c < PLAN_PER; ++c)
+        for (int c = 0; c < PER; ++c)
             if (r0 + c * THREADS < a.R) atomicAdd(&tot[g[c]], 1u);
     } else {
         for (int e = tid; e <= E; e += THREADS) {
@@ -132,11 +136,11 @@ __device__ __forceinline__ void plan_place(const PrepareArgs& a, int chunk, uint
         }
         __syncthreads();
     }
-    uint32_t at[PLAN_PER];
+    uint32_t at[PER];
 #pragma unroll
-    for (int c = 0; c < PLAN_PER; ++c) at[c] = r0 + c * THREADS < a.R ? atomicAdd(&cur[g[c]], 1u) : 0u;
+    for (int c = 0; c < PER; ++c) at[c] = r0 + c * THREADS < a.R ? atomicAdd(&cur[g[c]], 1u) : 0u;
 #pragma unroll
-    for (int c = 0; c < PLAN_PER; ++c)
+    for (int c = 0; c < PER; ++c)
         if (r0 + c * THREADS < a.R) a.plan.perm[at[c]] = (uint32_t)(r0 + c * THREADS);
 }
 
@@ -191,13 +195,13 @@ __device__ __forceinline__ void pad_unit(const Mx4Scales& p, const FastDiv& by_u
 }
 
 // Workgroups in order: the plan (with several chunks, its counts), the activation, scale rows.
-template <int DT, bool STREAM>
+template <int DT, bool STREAM, int PER>
 __global__ void __launch_bounds__(THREADS) mx4_prepare_kernel(PrepareArgs a) {
     extern __shared__ uint32_t sh[];
     int b = blockIdx.x;
     if (a.experts) {
         if (b < a.chunks) {
-            if (a.chunks == 1) plan_place(a, 0, sh);
+            if (a.chunks == 1) plan_place<PER>(a, 0, sh);
             else plan_count(a, b, sh);
             return;
         }
@@ -212,7 +216,13 @@ __global__ void __launch_bounds__(THREADS) mx4_prepare_kernel(PrepareArgs a) {
 
 __global__ void __launch_bounds__(THREADS) mx4_place_kernel(PrepareArgs a) {
     extern __shared__ uint32_t sh[];
-    plan_place(a, blockIdx.x, sh);
+    plan_place<PLAN_PER>(a, blockIdx.x, sh);
+}
+
+template <int DT>
+auto prepare_kernel(bool stream, bool wide) {
+    if (wide) return stream ? mx4_prepare_kernel<DT, true, PLAN_ONE * PLAN_PER> : mx4_prepare_kernel<DT, false, PLAN_ONE * PLAN_PER>;
+    return stream ? mx4_prepare_kernel<DT, true, PLAN_PER> : mx4_prepare_kernel<DT, false, PLAN_PER>;
 }
 
 }  // namespace
@@ -232,6 +242,7 @@ hipError_t launch_mx4_prepare(const Mx4Prepare& q, Mx4Plan* plan, hipStream_t st
     const int64_t units = (q.K / 32 + 15) / 16;
     a.by_unit = FastDiv::by((uint32_t)units);
     size_t shm = 0;
+    bool wide = false;                               // one chunk of PLAN_ONE
     if (q.experts) {
         const int64_t R = q.R, E = q.E;
         if (R < 1 || R >= (1LL << 31) || E < 1 || E > kMx4MaxExperts || q.tile_rows < kPlanMinTile)
@@ -239,7 +250,8 @@ hipError_t launch_mx4_prepare(const Mx4Prepare& q, Mx4Plan* plan, hipStream_t st
         a.experts = q.experts;
         a.R = (int)R;
         a.E = (int)E;
-        a.chunks = (int)((R + PLAN_CHUNK - 1) / PLAN_CHUNK);
+        wide = R > PLAN_CHUNK && R <= PLAN_ONE * PLAN_CHUNK;
+        a.chunks = wide ? 1 : (int)((R + PLAN_CHUNK - 1) / PLAN_CHUNK);
         a.tile_rows = q.tile_rows;
         a.plan.tiles = (Mx4Tile*)q.plan;
         a.plan.total = (uint32_t*)(a.plan.tiles + (R / kPlanMinTile + E + 1));
@@ -276,9 +288,9 @@ hipError_t launch_mx4_prepare(const Mx4Prepare& q, Mx4Plan* plan, hipStream_t st
             a.pad[w].rows = take(padded[w], q.pad[w].rows, units, &a.pad_blocks[w]);
         }
         if (blocks) {
-            auto kernel = q.stream ? mx4_prepare_kernel<QLIN_BF16, true> : mx4_prepare_kernel<QLIN_BF16, false>;
-            if (q.dt == QLIN_F32) kernel = q.stream ? mx4_prepare_kernel<QLIN_F32, true> : mx4_prepare_kernel<QLIN_F32, false>;
-            if (q.dt == QLIN_F16) kernel = q.stream ? mx4_prepare_kernel<QLIN_F16, true> : mx4_prepare_kernel<QLIN_F16, false>;
+            const auto kernel = q.dt == QLIN_F32 ? prepare_kernel<QLIN_F32>(q.stream, wide)
+                              : q.dt == QLIN_F16 ? prepare_kernel<QLIN_F16>(q.stream, wide)
+                                                 : prepare_kernel<QLIN_BF16>(q.stream, wide);
             kernel<<<(unsigned)blocks, THREADS, shm, st>>>(a);
         }
         if (a.chunks > 1) mx4_place_kernel<<<(unsigned)a.chunks, THREADS, shm, st>>>(a);

@@ -321,6 +321,8 @@ GATHER = [
     (150, 2, 3, 40, 64, 0.0, -1),
     (2600, 2, 7, 64, 128, 0.02, None),
     (100, 2, 3, 1040, 1056, 0.1, None),
+    (1700, 4, 9, 40, 64, 0.02, None),
+    (3000, 3, 300, 33, 96, 0.0, None),
 ]
 
 
