@@ -18,7 +18,6 @@ __device__ __forceinline__ float dpp_f(float id, float v) {
 __device__ __forceinline__ float lane_value(float v, int lane) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
-__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
 
 // Largest v of the wave's 64 lanes, all active (0 is the identity, so each
 // step is one instruction).

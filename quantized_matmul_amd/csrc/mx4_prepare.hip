@@ -11,8 +11,8 @@
 // Plan: workgroups of their own at the front of the launch, bound by latency
 // (a few barriers and memory round trips). More than one chunk of rows takes a
 // second launch (65536 rows: 6.8 us): first counts per chunk, then each chunk
-// scans all counts for its own places. The order of rows inside a group is free: each output row
-// depends on its own inputs only.
+// scans all counts for its own places. The order of rows inside a group is
+// free: each output row depends on its own inputs only.
 
 #include "mx4_common.h"
 
