@@ -13,7 +13,8 @@
 // places that stay empty get expert -1 and weight 0.
 //
 // Gradient for g = dL/dw, S = the renormalizing sum:
-//   ds_i = c g_i, or (c g_i - sum_j g_j w_j) / S;
+//   ds_i = c g_i, or (c g_i - sum_j g_j w_j) / S, taken as
+//          c (sum_j (g_i - g_j) s_j + 1e-20 g_i) / S^2;
 //   sigmoid  dx_i = ds_i s_i (1 - s_i), with 1 - s_i = 1 / (1 + exp(x_i));
 //   softmax  dx_j = s_j (ds_j - sum_i ds_i s_i); with renormalization the sum
 //            is exactly 0 (w does not change when every logit of the choice
@@ -486,8 +487,11 @@ __global__ void __launch_bounds__(64 * ROUTE_WAVES) route_grad_kernel(RouteGradA
     }
     float ds = a.scale * g;
     if (a.renorm) {
-        const float total = wave_sum(sc) + 1e-20f;
-        ds = (a.scale * g - wave_sum(g * (a.scale * sc / total))) / total;
+        // differences from one place's g: what all of them share cancels exactly
+        const uint64_t places = __ballot(id >= 0);
+        const float g0 = lane_value(g, places ? __builtin_ctzll(places) : 0), dg = id >= 0 ? g - g0 : 0.0f;
+        const float sum = wave_sum(sc), total = sum + 1e-20f;
+        ds = (dg * sum - wave_sum(dg * sc) + 1e-20f * g) / total / total * a.scale;
     }
     const bool whole = !a.sigmoid && !a.renorm;
     const float dot = whole ? wave_sum(ds * sc) : 0.0f;

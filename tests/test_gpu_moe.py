@@ -96,6 +96,18 @@ def test_route_gradient_against_differences():
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_gradient_where_it_vanishes(score):
+    """Renormalized weights do not move with a single choice, nor under equal gradients: what is left is the
+    1e-20 of the denominator, below 1e-14 here, where fp32 differences of weights would leave 1e-8."""
+    x = rand((50, 20), "f32", 12, 2.0)
+    for k, g in ((1, rand((50, 1), "f32", 13)), (5, torch.full((50, 5), 0.7, device=DEV))):
+        _, ids = qm.moe_route(x, k, score=score, scale=2.5)
+        assert qm.moe_route_grad(x, ids, g, score=score, scale=2.5).abs().max() <= 1e-14
+    ids[:, 0], ids[::2, 3] = -1, -1                             # places left over, the first among them
+    assert qm.moe_route_grad(x, ids, g, score=score, scale=2.5).abs().max() <= 1e-14
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_ties_masks_and_empty_rows(score):
     inf = float("inf")
     low = torch.finfo(torch.float32).min
