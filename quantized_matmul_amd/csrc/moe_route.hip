@@ -491,7 +491,8 @@ __global__ void __launch_bounds__(64 * ROUTE_WAVES) route_grad_kernel(RouteGradA
         const uint64_t places = __ballot(id >= 0);
         const float g0 = lane_value(g, places ? __builtin_ctzll(places) : 0), dg = id >= 0 ? g - g0 : 0.0f;
         const float sum = wave_sum(sc), total = sum + 1e-20f;
-        ds = (dg * sum - wave_sum(dg * sc) + 1e-20f * g) / total / total * a.scale;
+        const float extra = total - sum;   // 1e-20, or 0 where that is lost in the sum
+        ds = (dg * sum - wave_sum(dg * sc) + extra * g) / total / total * a.scale;
     }
     const bool whole = !a.sigmoid && !a.renorm;
     const float dot = whole ? wave_sum(ds * sc) : 0.0f;

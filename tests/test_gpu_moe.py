@@ -105,6 +105,13 @@ def test_route_gradient_where_it_vanishes(score):
         assert qm.moe_route_grad(x, ids, g, score=score, scale=2.5).abs().max() <= 1e-14
     ids[:, 0], ids[::2, 3] = -1, -1                             # places left over, the first among them
     assert qm.moe_route_grad(x, ids, g, score=score, scale=2.5).abs().max() <= 1e-14
+    if score == "sigmoid":                                      # scores of the denominator's size: it counts
+        x = -46.0 + rand((50, 20), "f32", 14)
+        _, ids = qm.moe_route(x, 4, score=score)
+        g = rand((50, 4), "f32", 15)
+        r = ref.route_grad(f64(x), ids.cpu().numpy(), f64(g), score, True, 1.0)
+        np.testing.assert_allclose(f64(qm.moe_route_grad(x, ids, g, score=score)), r, rtol=1e-4,
+                                   atol=1e-5 * np.abs(r).max())
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
