@@ -363,7 +363,7 @@ qlin_status qlin_mxfp4_matmul(const void* x, qlin_dtype x_dtype, const void* x_s
  * [T, k, N] is token t through its j-th expert. Each expert's weight is read
  * in place, once per tile of its rows.
  *   x         B rows, as for qlin_mxfp4_matmul; R must be a multiple of B.
- *   wq, scales  [E, N, K/8], [E, N, K/32]; E <= 8000.
+ *   wq, scales  [E, N, K/8], [E, N, K/32]; E <= 8000, R <= 2^31 - 2^14.
  *   experts   int32 [R]; a row whose entry is outside [0, E) becomes zeros.
  *   workspace  at least qlin_gather_mxfp4_matmul_workspace_bytes bytes.
  * R == 0 is a no-op.

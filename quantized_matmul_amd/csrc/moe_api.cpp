@@ -101,9 +101,10 @@ qlin_status product(const void* x, int x_dtype, const void* x_scales, const char
     if (rows < 0 || R < 0) return fail(QLIN_ERR_INVALID_ARGUMENT, "negative size");
     if (N <= 0 || K <= 0 || E <= 0) return fail(QLIN_ERR_INVALID_ARGUMENT, "N, K and E must be positive");
     if (K % 32) return fail(QLIN_ERR_INVALID_ARGUMENT, "K must be a multiple of 32 (got %lld)", (long long)K);
-    if (!product_sizes_ok(rows, K, N) || R > kMaxIndex)
+    if (!product_sizes_ok(rows, K, N))
         return fail(QLIN_ERR_UNSUPPORTED, "rows and N above 2^31 - 1 or K above 2^22 are not supported");
     if (gather) {
+        if (R > qlin::kMx4MaxRows) return fail(QLIN_ERR_UNSUPPORTED, "more than 2^31 - 2^14 index rows are not supported");
         if (E > qlin::kMx4MaxExperts)
             return fail(QLIN_ERR_UNSUPPORTED, "more than %lld experts are not supported",
                         (long long)qlin::kMx4MaxExperts);
@@ -283,7 +284,7 @@ qlin_status qlin_mxfp4_matmul(const void* x, qlin_dtype x_dtype, const void* x_s
 
 size_t qlin_gather_mxfp4_matmul_workspace_bytes(int64_t B, int64_t R, int64_t K, int64_t E, int64_t N,
                                                 qlin_dtype x_dtype) {
-    if (B < 1 || R < 1 || E < 1 || R > kMaxIndex || E > qlin::kMx4MaxExperts || !product_sizes_ok(B, K, N)) return 0;
+    if (B < 1 || R < 1 || E < 1 || R > qlin::kMx4MaxRows || E > qlin::kMx4MaxExperts || !product_sizes_ok(B, K, N)) return 0;
     const bool codes = x_dtype == QLIN_U8;
     return layout(qlin::mx4_choose(R, N, K, E, true, codes), B, R, K, E, N, codes, true).bytes;
 }

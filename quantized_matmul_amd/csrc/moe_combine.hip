@@ -95,19 +95,20 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_kernel(CombineArgs a)
     float acc[VEC];
 #pragma unroll
     for (int c = 0; c < VEC; ++c) acc[c] = 0.0f;
-    for (int j0 = 0; j0 < a.k; j0 += KC) {
+    const uint32_t k = (uint32_t)a.k;
+    for (uint32_t j0 = 0; j0 < k; j0 += KC) {
         float v[KC][VEC], wj[KC];
         int32_t ej[KC];
 #pragma unroll
         for (int q = 0; q < KC; ++q) {
-            const int j = j0 + q < a.k ? j0 + q : 0;
+            const uint32_t j = j0 + q < k ? j0 + q : 0;
             load_v<DT, VEC>(a.h, h + (int64_t)j * a.D, v[q]);
             wj[q] = w[j];
             ej[q] = e[j];
         }
 #pragma unroll
         for (int q = 0; q < KC; ++q) {
-            const bool live = j0 + q < a.k && (!a.experts || ej[q] >= 0);
+            const bool live = j0 + q < k && (!a.experts || ej[q] >= 0);
             const float f = live ? wj[q] : 0.0f;
 #pragma unroll
             for (int c = 0; c < VEC; ++c) acc[c] += f * (live ? v[q][c] : 0.0f);

@@ -137,6 +137,8 @@ __device__ __forceinline__ uint32_t mxfp4_word(const Eight<DT>& v, uint32_t* byt
 
 // Experts of one call: two counters each in the 64 KB of LDS every kernel may ask for.
 constexpr int64_t kMx4MaxExperts = 8000;
+// Index rows of one call: their numbers, rounded up to a chunk of the plan, are 32-bit integers.
+constexpr int64_t kMx4MaxRows = (1LL << 31) - (1LL << 14);
 
 // n / d for n < 2^32 by a multiplication and shifts (Granlund and Montgomery's
 // division by an invariant); the host makes it.
@@ -169,7 +171,7 @@ struct Mx4Plan {
     Mx4Tile* tiles;
     uint32_t* total;        // [1] row tiles
     uint32_t* perm;         // [R] index rows by group
-    uint32_t* counts;       // [chunks][E + 1] rows of each group in each chunk of rows
+    uint32_t* counts;       // [chunks][E + 1] rows of each group in each chunk of rows; one more row for the scan
 };
 
 constexpr int kPlanMinTile = 64;   // least rows of a row tile

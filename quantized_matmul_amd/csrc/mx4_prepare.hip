@@ -25,6 +25,8 @@ constexpr int PLAN_CHUNK = THREADS * PLAN_PER;       // ... and of a workgroup, 
 // A plan of up to two chunks of rows is one of twice the size: longer than a chunk's, but in the first launch (4872
 // rows 17.6 -> 14.7 us for the product; chunks of that size throughout 39.0 -> 42.5 at 16000 rows).
 constexpr int PLAN_ONE = 2;
+// Above this many chunks a launch between the two scans the counts, which every chunk otherwise does for itself.
+constexpr int PLAN_SCAN = 64;
 
 struct PrepareArgs {
     // activation
@@ -44,6 +46,7 @@ struct PrepareArgs {
     // plan
     const int32_t* experts; // null: dense
     int R, E, chunks, tile_rows;
+    int scanned;            // counts hold the sums of the chunks before, and of all in a last row
     Mx4Plan plan;
 };
 
@@ -85,6 +88,11 @@ __device__ __forceinline__ void plan_place(const PrepareArgs& a, int chunk, uint
             if (r0 + c * THREADS < a.R) atomicAdd(&tot[g[c]], 1u);
     } else {
         for (int e = tid; e <= E; e += THREADS) {
+            if (a.scanned) {
+                tot[e] = a.plan.counts[(size_t)a.chunks * (E + 1) + e];
+                cur[e] = a.plan.counts[(size_t)chunk * (E + 1) + e];
+                continue;
+            }
             uint32_t all = 0, before = 0;
 #pragma unroll 4
             for (int q = 0; q < a.chunks; ++q) {
@@ -225,11 +233,26 @@ auto prepare_kernel(bool stream, bool wide) {
     return stream ? mx4_prepare_kernel<DT, true, PLAN_PER> : mx4_prepare_kernel<DT, false, PLAN_PER>;
 }
 
+// A thread for each group sums its counts over the chunks.
+__global__ void __launch_bounds__(THREADS) mx4_scan_kernel(PrepareArgs a) {
+    const int e = blockIdx.x * THREADS + threadIdx.x;
+    if (e > a.E) return;
+    uint32_t sum = 0;
+#pragma unroll 8
+    for (int q = 0; q < a.chunks; ++q) {
+        uint32_t* const at = a.plan.counts + (size_t)q * (a.E + 1) + e;
+        const uint32_t n = *at;
+        *at = sum;
+        sum += n;
+    }
+    a.plan.counts[(size_t)a.chunks * (a.E + 1) + e] = sum;
+}
+
 }  // namespace
 
 size_t mx4_plan_bytes(int64_t R, int64_t E) {
     const int64_t chunks = (R + PLAN_CHUNK - 1) / PLAN_CHUNK;
-    return (size_t)(R / kPlanMinTile + E + 1) * sizeof(Mx4Tile) + (size_t)(1 + R + chunks * (E + 1)) * sizeof(uint32_t);
+    return (size_t)(R / kPlanMinTile + E + 1) * sizeof(Mx4Tile) + (size_t)(1 + R + (chunks + 1) * (E + 1)) * sizeof(uint32_t);
 }
 
 hipError_t launch_mx4_prepare(const Mx4Prepare& q, Mx4Plan* plan, hipStream_t st) {
@@ -245,7 +268,7 @@ hipError_t launch_mx4_prepare(const Mx4Prepare& q, Mx4Plan* plan, hipStream_t st
     bool wide = false;                               // one chunk of PLAN_ONE
     if (q.experts) {
         const int64_t R = q.R, E = q.E;
-        if (R < 1 || R >= (1LL << 31) || E < 1 || E > kMx4MaxExperts || q.tile_rows < kPlanMinTile)
+        if (R < 1 || R > kMx4MaxRows || E < 1 || E > kMx4MaxExperts || q.tile_rows < kPlanMinTile)
             return hipErrorInvalidValue;
         a.experts = q.experts;
         a.R = (int)R;
@@ -292,6 +315,10 @@ hipError_t launch_mx4_prepare(const Mx4Prepare& q, Mx4Plan* plan, hipStream_t st
                               : q.dt == QLIN_F16 ? prepare_kernel<QLIN_F16>(q.stream, wide)
                                                  : prepare_kernel<QLIN_BF16>(q.stream, wide);
             kernel<<<(unsigned)blocks, THREADS, shm, st>>>(a);
+        }
+        if (a.chunks > PLAN_SCAN) {
+            mx4_scan_kernel<<<(unsigned)((a.E + THREADS) / THREADS), THREADS, 0, st>>>(a);
+            a.scanned = 1;
         }
         if (a.chunks > 1) mx4_place_kernel<<<(unsigned)a.chunks, THREADS, shm, st>>>(a);
         a.experts = nullptr;                         // the plan is on its way

@@ -386,6 +386,16 @@ def test_gather_product_experts_out_of_range(form):
     close(y, ref.gather_product(ref.mxfp4_round(f64(x)), values(qw), ids), 64)
 
 
+def test_gather_product_many_rows():
+    """More chunks of rows than each scans for itself: the same bits as in parts."""
+    qw, x = weight((5, 20, 64), 622), rand((160000, 64), "bf16", 722)
+    ids = torch.randint(-1, 6, (160000, 2), dtype=torch.int32, device=DEV)
+    y = qm.gather_mxfp4_matmul(x, qw, ids)
+    assert qm.last_path() == "mxfp4_gather_tiled"
+    for m in range(0, 160000, 80000):
+        assert torch.equal(y[m:m + 80000], qm.gather_mxfp4_matmul(x[m:m + 80000], qw, ids[m:m + 80000])), m
+
+
 def test_gather_product_many_experts(form):
     E = 3000
     qw, x = weight((E, 16, 32), 621), rand((2000, 32), "bf16", 721)

@@ -103,6 +103,8 @@ def test_gather_rejects(lib):
         assert call(**bad) == INVALID, bad
         assert err(lib)
     assert call(E=8001) == UNSUPPORTED
+    assert call(B=1 << 30, R=1 << 31) == UNSUPPORTED
+    assert call(B=(1 << 31) - 1, R=(1 << 31) - 1) == UNSUPPORTED
     assert call(B=0, R=0, x=None, e=None, work=None, nb=0) == 0
 
 
