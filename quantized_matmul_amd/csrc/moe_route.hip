@@ -289,14 +289,16 @@ __device__ __forceinline__ double min_f64(double a, double b) {
 }
 
 // LDS of a wave, in words: the chosen experts of its tokens; then each lane's
-// sorted keys and places (the first is in registers), or the row of a group
-// choice (used before them).
+// sorted keys and places (the first is in registers; none for one key), or the
+// row of a group choice (used before them, by whole waves only).
 constexpr int kPlaces = kRouteMaxChoice;
-constexpr int route_lds(int L, int V) { return 64 / L * kPlaces + 2 * (V > 1 ? V : 0) * 64; }
+constexpr int route_lds(int L, int V) { return 64 / L * kPlaces + (V > 1 ? 2 * V * 64 : L == 64 ? 64 : 0); }
 
 template <int DT, int L, int V>
 __global__ void __launch_bounds__(64 * ROUTE_WAVES) route_kernel(RouteArgs a) {
     __shared__ __align__(8) uint32_t lds[ROUTE_WAVES][route_lds(L, V)];
+    static_assert(L != 64 || route_lds(L, V) >= kPlaces + 64 * V, "the row of a group choice lies in the wave's own LDS");
+    static_assert(V == 1 || route_lds(L, V) >= 64 / L * kPlaces + 2 * 64 * V, "so do the lanes' lists");
     using G = Lanes<L>;
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, row = lane & (L - 1);
     const int64_t mine_t = ((int64_t)blockIdx.x * ROUTE_WAVES + wv) * (64 / L) + lane / L;
