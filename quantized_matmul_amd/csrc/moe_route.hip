@@ -17,8 +17,8 @@
 //          c (sum_j (g_i - g_j) s_j + 1e-20 g_i) / S^2;
 //   sigmoid  dx_i = ds_i s_i (1 - s_i), with 1 - s_i = 1 / (1 + exp(x_i));
 //   softmax  dx_j = s_j (ds_j - sum_i ds_i s_i); with renormalization the sum
-//            is exactly 0 (w does not change when every logit of the choice
-//            moves together), so only the chosen logits get a gradient.
+//            is c 1e-20 (sum_i g_i s_i) / S^2: nothing in fp32, and no gradient
+//            outside the choice, unless the chosen scores sum to about 1e-20.
 //
 // A token takes L lanes, 16 (a DPP row, four tokens a wave) up to 256 experts
 // and a wave beyond; lane l holds experts l V .. l V + V - 1 (V = 1, 2, 4, 8
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(64 * ROUTE_WAVES) route_grad_kernel(RouteGradA
         for (int v = 0; v < V; ++v) s[v] *= inv;
         if (id >= 0) sc = exp_of(l - top) * inv;
     }
-    float ds = a.scale * g;
+    float ds = a.scale * g, dot = 0.0f;
     if (a.renorm) {
         // differences from one place's g: what all of them share cancels exactly
         const uint64_t places = __ballot(id >= 0);
@@ -495,15 +495,14 @@ __global__ void __launch_bounds__(64 * ROUTE_WAVES) route_grad_kernel(RouteGradA
         const float sum = wave_sum(sc), total = sum + 1e-20f;
         const float extra = total - sum;   // 1e-20, or 0 where that is lost in the sum
         ds = (dg * sum - wave_sum(dg * sc) + extra * g) / total / total * a.scale;
+        if (!a.sigmoid) dot = extra / total * (wave_sum(g * sc) / total) * a.scale;   // no factor is near 1e-40
+    } else if (!a.sigmoid) {
+        dot = wave_sum(ds * sc);
     }
-    const bool whole = !a.sigmoid && !a.renorm;
-    const float dot = whole ? wave_sum(ds * sc) : 0.0f;
-    float r = ds * sc;
-    if (a.sigmoid) r *= sigmoid_of(-l);
-    if (whole) r = sc * (ds - dot);
+    const float r = a.sigmoid ? ds * sc * sigmoid_of(-l) : sc * (ds - dot);
     float o[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) row[e0 + v] = whole ? -s[v] * dot : 0.0f;
+    for (int v = 0; v < V; ++v) row[e0 + v] = a.sigmoid ? 0.0f : 0.0f - s[v] * dot;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     if (id >= 0) row[id] = r;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
