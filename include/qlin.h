@@ -341,7 +341,9 @@ qlin_status qlin_moe_route_grad(const void* logits, qlin_dtype dtype, int64_t T,
  *             x_dtype QLIN_U8: mxfp4 words [M, K/8] as qlin_quantize writes
  *             them, with x_scales [M, K/32]; no activation.
  *   activation  NULL or "none", or "swiglu".
- *   wq, scales  W [N, K] in mxfp4, packed along K: [N, K/8], [N, K/32].
+ *   wq, scales  W [N, K] in mxfp4, packed along K: [N, K/8], [N, K/32]; scales
+ *             at any address (products of many rows copy W's and x's into the
+ *             workspace first where K/32 or the address is no multiple of 16).
  *   workspace   device memory of at least qlin_mxfp4_matmul_workspace_bytes
  *             bytes, 16-byte aligned, owned by the caller; overwritten (may be
  *             NULL where that is 0).

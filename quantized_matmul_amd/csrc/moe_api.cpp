@@ -56,8 +56,8 @@ int64_t scale_stride(int64_t K) { return (int64_t)up((size_t)(K / 32), 16); }
 
 // Pieces of a product's workspace, each 256-byte aligned: x's codes and
 // scales (or, for given codes, their scales in 16-byte rows), W's scales in
-// 16-byte rows where K / 32 is not a multiple of 16, the row plan. A streamed
-// float x needs none.
+// 16-byte rows (used where they do not lie so already; the sizes do not tell
+// their address), the row plan. A streamed float x needs none.
 struct Layout {
     size_t xq, xs, ws, plan, bytes;
 };
@@ -74,7 +74,7 @@ Layout layout(const qlin::Mx4Choice& c, int64_t rows, int64_t R, int64_t K, int6
     const bool quantized = !codes && c.path != qlin::Mx4Path::kStreamFloat;
     l.xq = take(quantized ? (size_t)rows * (size_t)(K / 2) : 0);
     l.xs = take(quantized || (codes && tiled) ? (size_t)rows * (size_t)scale_stride(K) : 0);
-    l.ws = take(tiled && K % 512 ? (size_t)E * (size_t)N * (size_t)scale_stride(K) : 0);
+    l.ws = take(tiled ? (size_t)E * (size_t)N * (size_t)scale_stride(K) : 0);
     l.plan = take(gather && tiled ? qlin::mx4_plan_bytes(R, E) : 0);
     l.bytes = at;
     return l;
@@ -126,10 +126,7 @@ qlin_status product(const void* x, int x_dtype, const void* x_scales, const char
     const bool tiled = c.path == qlin::Mx4Path::kTiled;
     if (gather && tiled && rows * (K / 2) >= (1LL << 31))
         return fail(QLIN_ERR_UNSUPPORTED, "x has more than 2^32 values: split its rows over several calls");
-    // W's scales, whole 16-byte rows at an address that is none: the streaming kernel takes any
-    const bool odd = tiled && (K / 32) % 16 == 0 && (uintptr_t)scales % 16;
-    const qlin::Mx4Choice run = odd ? qlin::Mx4Choice{qlin::Mx4Path::kStream, -1, 0} : c;
-    if (!qlin::mx4_fits(R, N, K, E, gather, run))
+    if (!qlin::mx4_fits(R, N, K, E, gather, c))
         return fail(QLIN_ERR_UNSUPPORTED, "more output tiles than one launch holds: split the rows over several calls");
     const Layout l = layout(c, rows, R, K, E, N, codes, gather);
     if (l.bytes) {
@@ -184,7 +181,7 @@ qlin_status product(const void* x, int x_dtype, const void* x_scales, const char
         a.xs = (const uint8_t*)(w + l.xs);
         a.xsstride = stride;
     }
-    if (gather && tiled && !odd) {
+    if (gather && tiled) {
         prepare = true;
         q.experts = experts;
         q.R = R;
@@ -192,9 +189,9 @@ qlin_status product(const void* x, int x_dtype, const void* x_scales, const char
         q.tile_rows = c.tile_rows;
         q.plan = w + l.plan;
     }
-    if (tiled && !odd) {
+    if (tiled) {
         // the tiled kernel reads scale rows 16 bytes at a time
-        if (KS % 16) {
+        if (KS % 16 || (uintptr_t)scales % 16) {
             prepare = true;
             q.pad[0] = {a.ws, E * N, KS, (uint8_t*)(w + l.ws)};
             a.ws = (const uint8_t*)(w + l.ws);
@@ -208,10 +205,10 @@ qlin_status product(const void* x, int x_dtype, const void* x_scales, const char
         }
     }
     if (prepare && (e = qlin::launch_mx4_prepare(q, &plan, st)) != hipSuccess) return device_status(e, what);
-    e = qlin::launch_mx4_matmul(a, run, &plan, st);
+    e = qlin::launch_mx4_matmul(a, c, &plan, st);
     if (e == hipSuccess)
-        qlin::record_path(tiled && !odd ? (gather ? "mxfp4_gather_tiled" : "mxfp4_tiled")
-                                        : (gather ? "mxfp4_gather_stream" : "mxfp4_stream"));
+        qlin::record_path(tiled ? (gather ? "mxfp4_gather_tiled" : "mxfp4_tiled")
+                                : (gather ? "mxfp4_gather_stream" : "mxfp4_stream"));
     return device_status(e, what);
 }
 

@@ -1,8 +1,8 @@
 // mx4_prepare.hip -- what an mxfp4 product needs before its tiles can run: the
 // activation's codes and scales, by experts the row plan, and scale rows in
-// whole 16-byte units where K / 32 is no multiple of 16. All of it comes from
-// one launch where the index rows fit one chunk, so that the plan's round trips
-// hide behind the rest.
+// whole 16-byte units where K / 32 is no multiple of 16 or their address none.
+// All of it comes from one launch where the index rows fit one chunk, so that
+// the plan's round trips hide behind the rest.
 //
 // Activation: one thread per packed word (8 values), 4 lanes per block; bound
 // by HBM (65536 rows of 2 x 2048 bf16 values with swiglu: 103 us, 5.9 TB/s;

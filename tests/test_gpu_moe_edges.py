@@ -71,3 +71,35 @@ def test_route_gradient_of_scores_of_the_denominators_size(score, dtype):
         np.testing.assert_array_less(np.abs((slope * g64).sum(1) - r[:, e]), 1e-8 * largest[:, 0] + 1e-12)
     got = f64(qm.moe_route_grad(x.to(DEV), ids, g.to(DEV), score=score, scale=scale))
     assert (np.abs(got - r) <= 1e-5 * largest + UNIT[dtype] * np.abs(r) + 1e-30).all(), np.abs(got - r).max()
+
+
+def at_odd_address(scales, by):
+    pad = torch.empty(scales.numel() + by, dtype=torch.uint8, device=DEV)
+    pad[by:] = scales.reshape(-1)
+    return pad[by:].view(scales.shape)
+
+
+@pytest.mark.parametrize("by", [1, 4, 8])
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("shape", [(300, 400, 1024), (5, 300, 512)])
+def test_scales_at_odd_addresses_take_the_same_kernel(shape, codes, by):
+    """Many rows by a weight whose scales are not 16-byte aligned: the path and the bits of aligned ones."""
+    g = torch.Generator().manual_seed(41)
+    N, K = shape[-2:]
+    gather = shape[0] == 5
+    w = torch.randn(shape if gather else (N, K), generator=g)
+    qw = qm.quantize(w.to(DEV), mode="mxfp4")
+    odd = qm.QuantizedWeight(qw.value, at_odd_address(qw.scales, by), None, 32, 4, True, "mxfp4")
+    x = torch.randn((300, K), generator=g).bfloat16().to(DEV)
+    ids = torch.randint(-1, 5, (300, 2), generator=g, dtype=torch.int32).to(DEV)
+    xo = x
+    if codes:
+        x = qm.quantize(x, mode="mxfp4")
+        xo = qm.QuantizedWeight(x.value, at_odd_address(x.scales, by), None, 32, 4, True, "mxfp4")
+    run = (lambda a, b: qm.gather_mxfp4_matmul(a, b, ids)) if gather else qm.mxfp4_matmul
+    y = run(x, qw)
+    path = qm.last_path()
+    assert path == ("mxfp4_gather_tiled" if gather else "mxfp4_tiled")
+    for a, b in ((x, odd), (xo, odd), (xo, qw)):
+        assert torch.equal(run(a, b), y)
+        assert qm.last_path() == path

@@ -120,3 +120,19 @@ def test_combine_rejects(lib):
                 dict(gw=None), dict(gy=ODD), dict(gw=ODD), dict(gh=ODD)):
         assert call(**bad) == INVALID, bad
     assert call(T=0, gy=None, h=None, w=None, gh=None, gw=None) == 0
+
+
+def test_scales_at_odd_addresses_are_no_limit(lib):
+    """A weight whose scales are not 16-byte aligned is refused no sooner and asks for no more than another."""
+    base = dict(x=P, xdt=BF16, xs=None, act=None, B=2048, K=16384, wq=P, ws=P, E=8, N=4096, e=P, R=16384, work=None,
+                nb=0, y=P, ydt=BF16, st=None)
+    need = lib.qlin_gather_mxfp4_matmul_workspace_bytes(2048, 16384, 16384, 8, 4096, BF16)
+    for scales in (P, ODD, ctypes.c_void_p(0x1008)):
+        assert caller(lib.qlin_gather_mxfp4_matmul, base)(ws=scales) == INVALID
+        assert f"workspace of {need} bytes" in err(lib)
+    base = dict(x=P, xdt=BF16, xs=None, act=None, M=1 << 20, K=16384, wq=P, ws=P, N=16384, work=None, nb=0, y=P,
+                ydt=BF16, st=None)
+    need = lib.qlin_mxfp4_matmul_workspace_bytes(1 << 20, 16384, 16384, BF16)
+    for scales in (P, ODD, ctypes.c_void_p(0x1008)):
+        assert caller(lib.qlin_mxfp4_matmul, base)(ws=scales) == INVALID
+        assert f"workspace of {need} bytes" in err(lib)
