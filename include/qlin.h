@@ -350,7 +350,8 @@ qlin_status qlin_moe_route_grad(const void* logits, qlin_dtype dtype, int64_t T,
  *   y         out, [M, N] of y_dtype (QLIN_F32, QLIN_F16 or QLIN_BF16).
  * K must be a multiple of 32 (at most 2^22); x words and wq 16-byte aligned.
  * M == 0 is a no-op. Products of more output tiles than one launch holds
- * (none below 2^26 columns and 2^35 outputs) are QLIN_ERR_UNSUPPORTED.
+ * (none up to 2^29 rows, 2^25 columns and 2^34 outputs) are
+ * QLIN_ERR_UNSUPPORTED.
  */
 size_t qlin_mxfp4_matmul_workspace_bytes(int64_t M, int64_t K, int64_t N, qlin_dtype x_dtype);
 qlin_status qlin_mxfp4_matmul(const void* x, qlin_dtype x_dtype, const void* x_scales,
@@ -365,10 +366,12 @@ qlin_status qlin_mxfp4_matmul(const void* x, qlin_dtype x_dtype, const void* x_s
  * [T, k, N] is token t through its j-th expert. Each expert's weight is read
  * in place, once per tile of its rows.
  *   x         B rows, as for qlin_mxfp4_matmul; R must be a multiple of B.
- *   wq, scales  [E, N, K/8], [E, N, K/32]; E <= 8000, R <= 2^31 - 2^14.
+ *   wq, scales  [E, N, K/8], [E, N, K/32].
  *   experts   int32 [R]; a row whose entry is outside [0, E) becomes zeros.
  *   workspace  at least qlin_gather_mxfp4_matmul_workspace_bytes bytes.
- * R == 0 is a no-op.
+ * R == 0 is a no-op. QLIN_ERR_UNSUPPORTED: E > 8000, R > 2^31 - 2^14, B * K >=
+ * 2^32 where R > E, more output tiles than one launch holds (as above, with
+ * R + 256 E for the rows).
  */
 size_t qlin_gather_mxfp4_matmul_workspace_bytes(int64_t B, int64_t R, int64_t K, int64_t E,
                                                 int64_t N, qlin_dtype x_dtype);

@@ -136,3 +136,26 @@ def test_scales_at_odd_addresses_are_no_limit(lib):
     for scales in (P, ODD, ctypes.c_void_p(0x1008)):
         assert caller(lib.qlin_mxfp4_matmul, base)(ws=scales) == INVALID
         assert f"workspace of {need} bytes" in err(lib)
+
+
+def test_limits_that_the_header_states(lib):
+    """No product within them is refused; x of 2^32 values by experts is, unless index rows are no more than experts."""
+    dense = caller(lib.qlin_mxfp4_matmul, dict(x=P, xdt=BF16, xs=None, act=None, M=0, K=0, wq=P, ws=P, N=0, work=None,
+                                               nb=0, y=P, ydt=BF16, st=None))
+    gather = caller(lib.qlin_gather_mxfp4_matmul, dict(x=P, xdt=BF16, xs=None, act=None, B=0, K=0, wq=P, ws=P, E=0,
+                                                       N=0, e=P, R=0, work=None, nb=0, y=P, ydt=BF16, st=None))
+    for K in (32, 512, 4096, 1 << 22):
+        for m in range(5, 30):
+            for n in range(0, 26):
+                for M, N in ((1 << m, 1 << n), ((1 << m) - 15, max((1 << n) - 1, 1)), ((1 << m) - 1, 1 << n)):
+                    if M * N > 1 << 34 or M * N * K <= 96e6:      # (small ones need no workspace and would run)
+                        continue
+                    assert dense(M=M, K=K, N=N) == INVALID and "workspace" in err(lib), (M, N, K)
+                    for E in (1, 8000):
+                        if M > E and M + 256 * E <= 1 << 29 and (M + 256 * E) * N <= 1 << 34:
+                            assert gather(B=1, R=M, K=K, E=E, N=N) == INVALID and "workspace" in err(lib), (M, N, K, E)
+    assert gather(B=1 << 20, R=1 << 20, K=4096, E=8, N=64) == UNSUPPORTED and "2^32 values" in err(lib)
+    assert gather(B=1 << 27, R=1 << 27, K=32, E=8, N=64) == UNSUPPORTED and "2^32 values" in err(lib)
+    assert gather(B=(1 << 20) - 1, R=(1 << 20) - 1, K=4096, E=8, N=64) == INVALID and "workspace" in err(lib)
+    # what they said before: 2^26 columns and 2^35 outputs
+    assert dense(M=(1 << 31) - 1, K=32, N=16) == UNSUPPORTED and "launch" in err(lib)
