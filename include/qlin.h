@@ -303,7 +303,8 @@ size_t qlin_gather_qmm_noalloc_max_experts(void);
  *   experts  out, int32 [T, k]: the k largest s + bias in descending order,
  *            equal ones by ascending index (without a bias the logits
  *            themselves are compared). An expert whose logit is not finite, or
- *            whose s + bias is NaN, cannot be chosen; places left over get -1.
+ *            whose s + bias is NaN or -infinity, cannot be chosen; places left
+ *            over get -1.
  *   weights  out, fp32 [T, k]: scale * s of the expert (without its bias),
  *            divided by the sum of the token's chosen s + 1e-20 if renormalize;
  *            0 at places left over.

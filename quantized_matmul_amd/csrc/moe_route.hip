@@ -9,8 +9,8 @@
 //          s (+ b); the `kept` best groups stay in the choice;
 //   choice the k largest keys, descending, equal keys by ascending index;
 //   weight w_i = c s_i, or c s_i / (sum_chosen s + 1e-20).
-// An expert whose logit is not finite (or whose key is NaN) cannot be chosen;
-// places that stay empty get expert -1 and weight 0.
+// An expert whose logit is not finite (or whose key is NaN or -inf) cannot be
+// chosen; places that stay empty get expert -1 and weight 0.
 //
 // Gradient for g = dL/dw, S = the renormalizing sum:
 //   ds_i = c g_i, or (c g_i - sum_j g_j w_j) / S, taken as
