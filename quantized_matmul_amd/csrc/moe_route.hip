@@ -55,8 +55,9 @@ struct RouteArgs {
 };
 
 // exp(x) for x <= 0 within 2 ulp: 2^(x log2 e), with what the product's
-// rounding lost put back to first order. Below -104 (under half of the least
-// subnormal; -inf and NaN too) the argument is held there, so the result is 0.
+// rounding lost put back to first order. Results below 2^-126 (x < -87.34) are
+// 0, as the hardware's 2^x gives no subnormal numbers; the argument is held at
+// -104 (-inf and NaN too).
 __device__ __forceinline__ float exp_of(float x) {
     const float hi = 0x1.715476p+0f, lo = 0x1.4ae0cp-26f;   // log2 e = hi + lo
     x = fmaxf(x, -104.0f);

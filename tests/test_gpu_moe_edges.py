@@ -103,3 +103,38 @@ def test_scales_at_odd_addresses_take_the_same_kernel(shape, codes, by):
     for a, b in ((x, odd), (xo, odd), (xo, qw)):
         assert torch.equal(run(a, b), y)
         assert qm.last_path() == path
+
+
+def near_ties(dtype, M, K, seed):
+    """x [M, 2 K] whose silu(gate) * up lies near ties of its block's 4-bit codes; gates from -80 to 20."""
+    rng = np.random.default_rng(seed)
+    gate = torch.from_numpy(rng.uniform(-80, 20, (M, K // 32, 1)) + rng.uniform(-3, 3, (M, K // 32, 32))).to(DTYPES[dtype])
+    g = f64(gate)
+    tie = rng.choice([.25, .75, 1.25, 1.75, 2.5, 3.5, 5.0], g.shape)
+    tie[:, :, 0] = 4.7                                        # the block's largest magnitude or next to it
+    want = tie * (1 + rng.uniform(-2.0 ** -17, 2.0 ** -17, g.shape)) * rng.choice([-1.0, 1.0], g.shape)
+    up = want / (g / (1 + np.exp(-g)))
+    up = up / np.exp2(np.rint(np.log2(np.abs(up[:, :, :1]))))  # the first value's up near 1
+    if dtype == "f16":
+        up = np.clip(up, -60000, 60000)
+    x = torch.cat([gate.reshape(M, K), torch.from_numpy(up).reshape(M, K).to(DTYPES[dtype])], 1)
+    return x
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_swiglu_rounds_to_codes_within_its_stated_error(dtype):
+    """silu(gate) * up carries a relative error of at most d = (1.25 |gate| + 7) 2^-24: the argument of 2^x is rounded
+    (2^-24 of itself, and log2 e is within 2^-26), then come 2^x and 1 / x (2^-23 each) and three roundings. So each
+    code lies between those of v (1 - d) and v (1 + d), which are equal but next to a tie."""
+    M, K = 64, 160
+    x = near_ties(dtype, M, K, 61)
+    g, v = f64(x)[:, :K], ref.swiglu(f64(x))
+    d = (1.25 * np.abs(g) + 7) * 2.0 ** -24
+    a, b = ref.mxfp4_round(v * (1 - d)), ref.mxfp4_round(v * (1 + d))
+    top = [np.floor(np.log2(np.abs(v * f).reshape(M, -1, 32).max(2))) for f in (1 - d, 1 + d)]
+    assert (top[0] == top[1]).all()                           # no block's exponent hangs on the error
+    eye = qm.quantize(torch.eye(K, device=DEV), mode="mxfp4")
+    y = f64(qm.mxfp4_matmul(x.to(DEV), eye, activation="swiglu", out_dtype=torch.float32))
+    assert ((np.minimum(a, b) <= y) & (y <= np.maximum(a, b))).all()
+    if dtype == "f32":
+        assert (a != b).any()
