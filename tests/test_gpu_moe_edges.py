@@ -138,3 +138,19 @@ def test_swiglu_rounds_to_codes_within_its_stated_error(dtype):
     assert ((np.minimum(a, b) <= y) & (y <= np.maximum(a, b))).all()
     if dtype == "f32":
         assert (a != b).any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_activation_rounding_of_the_smallest_blocks(dtype):
+    """Blocks whose largest value is about the type's least normal number and below, ties and their neighbours among
+    the values: exact, as against an identity of 2^40 whose products are normal numbers."""
+    M, K = 48, 160
+    rng = np.random.default_rng(51)
+    ties = np.array([0, .25, .5, .75, 1, 1.25, 1.5, 1.75, 2, 2.5, 3, 3.5, 4, 5, 6, 7])
+    v = rng.choice(ties, (M, K // 32, 32)) * (1 + rng.integers(-1, 2, (M, K // 32, 32)) * UNIT[dtype] * 2)
+    low, high = (-24, -10) if dtype == "f16" else (-135, -118)
+    v *= rng.choice([-1.0, 1.0], v.shape) * np.exp2(rng.integers(low, high, (M, K // 32, 1)))
+    x = torch.from_numpy(v.reshape(M, K)).to(DTYPES[dtype])
+    eye = qm.quantize(torch.eye(K, device=DEV) * 2.0 ** 40, mode="mxfp4")
+    y = qm.mxfp4_matmul(x.to(DEV), eye, out_dtype=torch.float32)
+    np.testing.assert_array_equal(f64(y), ref.mxfp4_round(f64(x)) * 2.0 ** 40)
