@@ -147,6 +147,9 @@ __global__ void __launch_bounds__(COMBINE_THREADS) combine_grad_kernel(CombineAr
     if (lane == 0) a.gw[r] = sum;
 }
 
+// Whether a call of `rows` rows of D values in all goes past the caches.
+bool past_caches(int dt, double rows, int64_t D) { return rows * (double)D * (dt == QLIN_F32 ? 4 : 2) >= (double)kStreamBytes; }
+
 bool wide(int dt, int64_t D, const void* a, const void* b, const void* c) {
     const int64_t per = dt == QLIN_F32 ? 4 : 8;
     return D % per == 0 && (((uintptr_t)a | (uintptr_t)b | (uintptr_t)c) & 15) == 0;
@@ -198,7 +201,7 @@ hipError_t launch_moe_combine(const void* h, int dt, int64_t T, int k, int64_t D
     CombineArgs a{};
     a.h = h; a.w = weights; a.experts = experts; a.T = T; a.D = D; a.k = k; a.y = y;
     const bool vec = wide(dt, D, h, y, nullptr);
-    if (T * (k + 1) * D * (dt == QLIN_F32 ? 4 : 2) >= kStreamBytes) by_type<true>(dt, a, vec, st, false);
+    if (past_caches(dt, (double)T * (k + 1.0), D)) by_type<true>(dt, a, vec, st, false);
     else by_type<false>(dt, a, vec, st, false);
     return hipGetLastError();
 }
@@ -209,7 +212,7 @@ hipError_t launch_moe_combine_grad(const void* gy, const void* h, int dt, int64_
     CombineArgs a{};
     a.h = h; a.w = weights; a.experts = experts; a.T = T; a.D = D; a.k = k; a.gy = gy; a.gh = gh; a.gw = gw;
     const bool vec = wide(dt, D, h, gy, gh);
-    if (T * (2 * k + 1) * D * (dt == QLIN_F32 ? 4 : 2) >= kStreamBytes) by_type<true>(dt, a, vec, st, true);
+    if (past_caches(dt, (double)T * (2.0 * k + 1.0), D)) by_type<true>(dt, a, vec, st, true);
     else by_type<false>(dt, a, vec, st, true);
     return hipGetLastError();
 }
