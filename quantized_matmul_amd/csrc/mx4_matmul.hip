@@ -671,9 +671,16 @@ int forced_tile() {
 // saves: up to 12 MB of such reads dense and 24 MB by experts (measured around
 // them, us streamed and not: 13 rows, N 653, K 3712 6.5 and 8.8; 36 rows, N
 // 5578, K 800, 20 MB 13.7 and 9.0; 51 by 10 experts, N 462, K 1952 7.3 and 9.6;
-// 210 by 32, N 393, K 768, 32 MB 11.4 and 9.5), and by experts also while index
-// rows are no more than experts, hardly two of which share one. Dense, up to 16
-// rows stream from codes.
+// 210 by 32, N 393, K 768, 32 MB 11.4 and 9.5). Dense, up to 16 rows stream from
+// codes. By experts index rows stream also while they are no more than experts:
+// each reads its expert's W, so this wins while few share one and loses where
+// many do. Top 8 of E, K 2048, us streamed and with the best tile, experts in
+// even demand and (in brackets) in a log-normal one of deviation 2:
+//   64, N 1536:   16 rows 7.8, 11.0 (7.5, 10.7)  32 11.2, 14.4 (10.9, 11.7)  64 19.2, 19.6 (18.3, 14.7)
+//   64, N 4096:   16 rows 14.0, 16.6 (13.7, 15.3)  32 25.9, 28.5 (23.3, 20.0)  64 46.3, 44.1 (42.6, 28.0)
+//   256, N 4096:  64 rows 50.5, 55.0 (43.1, 35.8)  128 93.8, 89.9 (82.4, 53.1)  256 181, 132 (161, 78.5)
+// The sizes alone do not tell the demand, and a bound by bytes would have to
+// weigh the repeats; this one does not.
 // Beyond, the tile whose rounds over the CUs take least. An expert's last row
 // tile is half empty on average, so R rows make R / m + E / 2 tiles, or one an
 // expert if that is more. Over 223 drawn sizes the choice costs 1.3% more than
