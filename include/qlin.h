@@ -407,6 +407,138 @@ qlin_status qlin_moe_combine_grad(const void* grad_y, const void* h, qlin_dtype 
                                   const int32_t* experts, void* grad_h, float* grad_weights,
                                   void* stream);
 
+/*
+ * qlin_rotary -- rotary positions of each head of x: its first R values are
+ * taken as R/2 pairs, pair i being values (i, i + R/2), or (2i, 2i + 1) where
+ * interleaved, and is turned by positions[t] * freqs[i]:
+ *   (a, b) -> scale * (a cos - b sin, a sin + b cos);
+ * values from R on are copied. Angles are taken in fp64 (to 2^-52 of the
+ * number of turns), the rest in fp32, rounded once.
+ *   x, y       [T, heads, D] of dtype (QLIN_F32, QLIN_F16 or QLIN_BF16), heads
+ *              and values dense, tokens x_stride and y_stride elements apart
+ *              (x_stride may be any number >= 0, y_stride at least heads * D).
+ *              y may be x with the same stride (in place); otherwise the two
+ *              must not overlap.
+ *   positions  int32 [T], any sign.
+ *   freqs      fp32 [R/2], the angle of a step; scaling for long contexts goes
+ *              into them (and into scale).
+ * D a multiple of 8, at most 256; R even, 2 <= R <= D. T == 0 is a no-op.
+ */
+qlin_status qlin_rotary(const void* x, qlin_dtype dtype, int64_t T, int64_t x_stride, int64_t heads,
+                        int64_t D, int64_t R, const int32_t* positions, const float* freqs,
+                        int interleaved, double scale, void* y, int64_t y_stride, void* stream);
+
+/*
+ * qlin_rotary_grad -- gradient of qlin_rotary with respect to x, for grad_y in
+ * x's place: the angles' sign changed. Arguments as there.
+ */
+qlin_status qlin_rotary_grad(const void* grad_y, qlin_dtype dtype, int64_t T, int64_t grad_y_stride,
+                             int64_t heads, int64_t D, int64_t R, const int32_t* positions,
+                             const float* freqs, int interleaved, double scale, void* grad_x,
+                             int64_t grad_x_stride, void* stream);
+
+/*
+ * qlin_kv_cache -- a cache of attention keys and values held in 4 bits: for
+ * each of the two a pool [pages, heads, page_size, head_dim], quantized along
+ * head_dim by qlin_quantize's rule and in its layout (codes [..., head_dim/8],
+ * scales and biases [..., head_dim/group_size]), so that qlin_dequantize and
+ * qlin_quantize of pages * heads * page_size rows take it too. Filled in by
+ * the caller and read during the call only; it describes thirteen things that
+ * every call on a cache needs alike, which is why it is a struct.
+ *   mode, group_size, bits  "affine" (32, 64 or 128), "mxfp4" (32) or "nvfp4"
+ *             (16); bits is 4.
+ *   dtype     "affine": the type of scales and biases (QLIN_F32, QLIN_F16 or
+ *             QLIN_BF16), which keys, values and queries then have too.
+ *             Otherwise unused (scales are bytes, biases NULL).
+ *   page_size  a multiple of 16. Slot p * page_size + o is place o of page p;
+ *             pages * page_size < 2^31, pages * heads * page_size < 2^35.
+ *   head_dim  a multiple of 32 and of group_size, at most 256; heads <= 4096.
+ *   codes 16-byte aligned, scales and biases to their type.
+ */
+typedef struct qlin_kv_cache {
+    uint32_t* k_codes;
+    void* k_scales;
+    void* k_biases;
+    uint32_t* v_codes;
+    void* v_scales;
+    void* v_biases;
+    const char* mode;
+    int64_t pages, heads, page_size, head_dim;
+    int group_size, bits;
+    qlin_dtype dtype;
+} qlin_kv_cache;
+
+/*
+ * qlin_kv_cache_write -- rows of keys and values quantized into the cache:
+ * token t's heads to slot slots[t].
+ *   k, v      [T, heads, head_dim] of dtype ("affine": the cache's), heads and
+ *             values dense, tokens k_stride and v_stride elements apart (any
+ *             number >= 0), so that they may lie in a projection's rows.
+ *   slots     int32 [T]. A slot outside [0, pages * page_size) is left out (-1
+ *             for the padding of a batch). No slot may come twice in a call:
+ *             its bytes would be a mix of the rows that race for it.
+ * T == 0 is a no-op; T * heads * head_dim <= 2^36.
+ */
+qlin_status qlin_kv_cache_write(const qlin_kv_cache* cache, const void* k, const void* v,
+                                qlin_dtype dtype, int64_t T, int64_t k_stride, int64_t v_stride,
+                                const int32_t* slots, void* stream);
+
+/*
+ * qlin_kv_cache_read -- rows of the cache as numbers (qlin_dequantize's):
+ *   k, v      out, [T, heads, head_dim] of dtype (QLIN_F32, QLIN_F16 or
+ *             QLIN_BF16), dense, 16-byte aligned.
+ *   slots     int32 [T], in any order, any number of times; a slot outside the
+ *             pool gives zeros.
+ */
+qlin_status qlin_kv_cache_read(const qlin_kv_cache* cache, const int32_t* slots, int64_t T, void* k,
+                               void* v, qlin_dtype dtype, void* stream);
+
+/*
+ * qlin_kv_cache_attention -- attention of rows of q to the keys of their
+ * sequences in the cache: out = sum over keys j of p_j v_j, p the softmax of
+ * scale * <q, k_j> over the keys that the row sees. For decode, for several
+ * drafted tokens at once, and for (parts of) prompts.
+ *   q         [T, q_heads, head_dim] of dtype QLIN_F32, QLIN_F16 or QLIN_BF16
+ *             ("affine": the cache's), tokens q_stride elements apart; q_heads a
+ *             multiple of heads, query head i reads key head i / (q_heads / heads).
+ *   offsets   int32 [B + 1], never falling: rows [offsets[b], offsets[b + 1])
+ *             are sequence b's, in the order of their places; rows before
+ *             offsets[0] and from offsets[B] on are left as they are in out.
+ *             NULL: T == B, one row each.
+ *   lengths   int32 [B]: keys of each sequence, its rows of this call among
+ *             them (write them first): row i of n stands at key lengths - n + i.
+ *             Taken as at most width * page_size.
+ *   table     int32 [B, width]: key j lies at place j % page_size of page
+ *             table[b, j / page_size]. Pages may be shared; a page number
+ *             outside the pool takes its keys out; entries past a sequence's
+ *             keys are not read.
+ *   causal    nonzero: a row sees no key behind its own place.
+ *   window    > 0: nor any window or more places before it; 0: all.
+ *   out       [T, q_heads, head_dim] of dtype, dense. A row that sees no key
+ *             gives zeros.
+ *   workspace  device memory of at least qlin_kv_cache_attention_workspace_bytes
+ *             bytes for the same sizes, 16-byte aligned (may be NULL where that
+ *             is 0); overwritten, nothing in it counts before or after a call.
+ *             Calls that share one must not overlap.
+ * Sizes alone choose how it runs, so a captured call may be replayed with other
+ * lengths, tables and offsets in the same buffers. Scores, their softmax and
+ * the sums are fp32. f16 and bf16 with head_dim 64, 96, 128, 192 or 256 run on
+ * the matrix cores: there the p_j and the values are rounded to dtype (keys are
+ * not where few rows share them), so values outside f16's range do not go with an f16 q.
+ * Keys and values that a row of a tile sees must be finite; what lies behind a
+ * sequence's end may be anything. Results do not depend on scheduling.
+ * T, B < 2^31, T * q_heads < 2^31. T == 0 is a no-op.
+ */
+size_t qlin_kv_cache_attention_workspace_bytes(const qlin_kv_cache* cache, qlin_dtype dtype, int64_t T,
+                                               int64_t q_heads, int64_t B, int64_t width,
+                                               int has_offsets, int64_t window);
+qlin_status qlin_kv_cache_attention(const qlin_kv_cache* cache, const void* q, qlin_dtype dtype,
+                                    int64_t T, int64_t q_stride, int64_t q_heads,
+                                    const int32_t* table, int64_t B, int64_t width,
+                                    const int32_t* lengths, const int32_t* offsets, double scale,
+                                    int causal, int64_t window, void* workspace,
+                                    size_t workspace_bytes, void* out, void* stream);
+
 /* Message describing the calling thread's last failed call ("" if none). */
 const char* qlin_last_error(void);
 

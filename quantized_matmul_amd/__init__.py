@@ -9,12 +9,15 @@ library is not built, every call raises.
 Raw ABI calls (same names as the C functions, minus the ``qlin_`` prefix):
 ``quantize``, ``dequantize``, ``quantized_matmul``, ``quantized_dense``,
 ``qqmm``, ``gather_qmm``, ``moe_route``, ``moe_route_grad``, ``mxfp4_matmul``,
-``gather_mxfp4_matmul``, ``moe_combine``, ``moe_combine_grad`` operate on
-explicit tensors. ``QuantizedWeight`` bundles the packed weight with its
+``gather_mxfp4_matmul``, ``moe_combine``, ``moe_combine_grad``, ``rotary``,
+``rotary_grad``, ``kv_cache_write``, ``kv_cache_read``, ``kv_cache_attention``
+operate on explicit tensors. ``QuantizedWeight`` bundles the packed weight with its
 metadata, mirroring the field set of the "Emily.QuantizedWeight" page
-(value, scales, biases, group_size, bits, transpose, mode).
+(value, scales, biases, group_size, bits, transpose, mode); ``KVCache``
+bundles the two pools of a cache of attention keys and values.
 """
 from ._binding import (  # noqa: F401
+    KVCache,
     QlinError,
     QuantizedWeight,
     dequantize,
@@ -23,6 +26,11 @@ from ._binding import (  # noqa: F401
     gather_qmm,
     gather_qmm_noalloc,
     gather_qmm_workspace_bytes,
+    kv_cache,
+    kv_cache_attention,
+    kv_cache_attention_workspace_bytes,
+    kv_cache_read,
+    kv_cache_write,
     last_path,
     library_path,
     load_library,
@@ -38,5 +46,8 @@ from ._binding import (  # noqa: F401
     quantized_dense,
     quantized_matmul,
     quantized_matmul_workspace_bytes,
+    rotary,
+    rotary_frequencies,
+    rotary_grad,
     MODE_DEFAULTS,
 )

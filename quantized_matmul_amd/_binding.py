@@ -9,6 +9,7 @@ Pages followed for the user-facing defaults:
 """
 import ctypes
 import dataclasses
+import math
 import os
 from typing import Optional
 
@@ -21,9 +22,18 @@ _LIB_PATH = os.path.join(_HERE, "libqlin.so")
 MODE_DEFAULTS = {"affine": (64, 4), "mxfp4": (32, 4), "mxfp8": (32, 8), "nvfp4": (16, 4)}
 
 _DTYPE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.uint8: 3}
+_FLOATS = (torch.float32, torch.float16, torch.bfloat16)
 _STATUS = {1: "invalid argument", 2: "unsupported", 3: "device error"}
 
 _lib = None
+
+
+class _CacheStruct(ctypes.Structure):
+    """qlin_kv_cache."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "k_biases", "v_codes", "v_scales", "v_biases")]
+                + [("mode", ctypes.c_char_p)]
+                + [(n, ctypes.c_int64) for n in ("pages", "heads", "page_size", "head_dim")]
+                + [(n, ctypes.c_int) for n in ("group_size", "bits", "dtype")])
 
 
 class QlinError(RuntimeError):
@@ -82,11 +92,21 @@ def load_library():
     lib.qlin_gather_mxfp4_matmul_workspace_bytes.restype = sz
     lib.qlin_moe_combine.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp]
     lib.qlin_moe_combine_grad.argtypes = [vp, vp, i32, i64, i64, i64, vp, vp, vp, vp, vp]
+    cache = ctypes.POINTER(_CacheStruct)
+    lib.qlin_rotary.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, vp, i32, f64, vp, i64, vp]
+    lib.qlin_rotary_grad.argtypes = lib.qlin_rotary.argtypes
+    lib.qlin_kv_cache_write.argtypes = [cache, vp, vp, i32, i64, i64, i64, vp, vp]
+    lib.qlin_kv_cache_read.argtypes = [cache, vp, i64, vp, vp, i32, vp]
+    lib.qlin_kv_cache_attention.argtypes = [cache, vp, i32, i64, i64, i64, vp, i64, i64, vp, vp, f64, i32, i64,
+                                            vp, sz, vp, vp]
+    lib.qlin_kv_cache_attention_workspace_bytes.argtypes = [cache, i32, i64, i64, i64, i64, i32, i64]
+    lib.qlin_kv_cache_attention_workspace_bytes.restype = sz
     lib.qlin_last_error.restype = ctypes.c_char_p
     lib.qlin_last_path.restype = ctypes.c_char_p
     for f in ("qlin_quantize", "qlin_dequantize", "qlin_quantized_matmul", "qlin_quantized_dense",
               "qlin_gather_qmm", "qlin_moe_route", "qlin_moe_route_grad", "qlin_mxfp4_matmul",
-              "qlin_gather_mxfp4_matmul", "qlin_moe_combine", "qlin_moe_combine_grad"):
+              "qlin_gather_mxfp4_matmul", "qlin_moe_combine", "qlin_moe_combine_grad", "qlin_rotary",
+              "qlin_rotary_grad", "qlin_kv_cache_write", "qlin_kv_cache_read", "qlin_kv_cache_attention"):
         getattr(lib, f).restype = i32
     _lib = lib
     return lib
@@ -633,3 +653,250 @@ def moe_combine_grad(grad_y: torch.Tensor, h: torch.Tensor, weights: torch.Tenso
     _check(lib.qlin_moe_combine_grad(grad_y.data_ptr(), h.data_ptr(), code, T, k, D, weights.data_ptr(), ids,
                                      grad_h.data_ptr(), grad_w.data_ptr(), _stream(dev)))
     return grad_h, grad_w
+
+
+def _run(dev, f, *args):
+    """f(*args, stream) on dev's current stream, with dev as the current device."""
+    if dev.index == torch.cuda.current_device():
+        _check(f(*args, _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            _check(f(*args, _stream(dev)))
+
+
+def _token_rows(name, t, dev, dtype, shape):
+    """Elements between the tokens of t [T, heads, D], whose heads and values are dense."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev} (got {t.device})")
+    if t.dim() != 3 or t.shape[1:] != shape[1:] or (shape[0] is not None and t.shape[0] != shape[0]):
+        raise ValueError(f"{name} must be [T, heads, head_dim] = {tuple(shape)} (got {tuple(t.shape)})")
+    stride, heads, values = t.stride()
+    if (values != 1 and t.shape[2] > 1) or (heads != t.shape[2] and t.shape[1] > 1):
+        raise ValueError(f"the heads and values of {name} must be dense (only its tokens may lie apart)")
+    return stride if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _index_rows(name, t, dev, n):
+    _check_tensor(name, t, dev, torch.int32)
+    if t.dim() != 1 or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be one-dimensional" + ("" if n is None else f" with {n} entries"))
+
+
+def rotary_frequencies(dim: int, base: float = 10000.0, factor: float = 1.0, method: str = "linear",
+                       trained: int = 4096, slow: float = 1.0, fast: float = 32.0, device="cuda") -> torch.Tensor:
+    """Angles of a step for rotary, float32 [dim / 2]: base ** (-2 i / dim), scaled for contexts `factor` times the
+    trained one.
+
+    method "linear" divides all of them by factor; "base" raises the base to base * factor ** (dim / (dim - 2)), which
+    leaves the first and divides the last by factor; "parts" divides those that turn at most `slow` times in `trained`
+    tokens, leaves those that turn `fast` times or more, and mixes the two in between, evenly in the turns.
+    """
+    if dim < 2 or dim % 2:
+        raise ValueError("dim must be even and positive")
+    if not factor > 0 or not base > 0:
+        raise ValueError("base and factor must be positive")
+    i = torch.arange(0, dim, 2, dtype=torch.float64)
+    if method == "base":
+        if dim < 4:
+            raise ValueError('method "base" needs dim of 4 or more')
+        base = base * factor ** (dim / (dim - 2))
+    freqs = base ** (-i / dim)
+    if method == "linear":
+        freqs = freqs / factor
+    elif method == "parts":
+        if not fast > slow:
+            raise ValueError("fast must be above slow")
+        keep = ((trained * freqs / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        freqs = freqs * keep + freqs / factor * (1 - keep)
+    elif method != "base":
+        raise ValueError(f'unknown method "{method}" (linear, base, parts)')
+    return freqs.float().to(device)
+
+
+def _rotary(call, name, x, positions, freqs, interleaved, scale, out):
+    if not x.is_cuda:
+        raise ValueError("qlin tensors live in GPU memory (got a CPU tensor)")
+    dev = x.device
+    code = _float_code(name, x)
+    stride = _token_rows(name, x, dev, x.dtype, x.shape)
+    T, heads, D = x.shape
+    _index_rows("positions", positions, dev, T)
+    _check_tensor("freqs", freqs, dev, torch.float32)
+    if freqs.dim() != 1:
+        raise ValueError("freqs must be one-dimensional")
+    if out is None:
+        out = torch.empty((T, heads, D), dtype=x.dtype, device=dev)
+        out_stride = heads * D
+    else:
+        out_stride = _token_rows("out", out, dev, x.dtype, x.shape)
+    _run(dev, call, x.data_ptr(), code, T, stride, heads, D, 2 * freqs.shape[0], positions.data_ptr(), freqs.data_ptr(),
+         bool(interleaved), scale, out.data_ptr(), out_stride)
+    return out
+
+
+def rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, interleaved: bool = False,
+           scale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """qlin_rotary: the first 2 * len(freqs) values of each head of x [T, heads, D] turned in pairs by
+    positions[t] * freqs[i] (pairs (i, i + len(freqs)), or neighbours where interleaved) and multiplied by scale, the
+    rest copied.
+
+    positions int32 [T], freqs float32 (rotary_frequencies). x's tokens may lie apart, as the heads of a projection's
+    rows do; so may out's, and out may be x.
+    """
+    return _rotary((_lib or load_library()).qlin_rotary, "x", x, positions, freqs, interleaved, scale, out)
+
+
+def rotary_grad(grad_y: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, interleaved: bool = False,
+                scale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """qlin_rotary_grad: gradient of rotary with respect to x."""
+    return _rotary((_lib or load_library()).qlin_rotary_grad, "grad_y", grad_y, positions, freqs, interleaved, scale, out)
+
+
+class KVCache:
+    """Attention keys and values held in 4 bits (qlin_kv_cache): two pools [pages, heads, page_size, head_dim],
+    quantized along head_dim as `quantize` does it ("affine" with 4 bits, "mxfp4" or "nvfp4").
+
+    key and value are their QuantizedWeights (`dequantize` takes them). Slot p * page_size + o is place o of page p.
+    """
+
+    def __init__(self, key: QuantizedWeight, value: QuantizedWeight):
+        if (key.mode, key.group_size, key.bits) != (value.mode, value.group_size, value.bits):
+            raise ValueError("keys and values must be quantized alike")
+        dev = _dev(key.value)
+        dtype = key.scales.dtype
+        lead = tuple(key.value.shape)
+        if len(lead) != 4:
+            raise ValueError("a cache's words are [pages, heads, page_size, head_dim / 8]")
+        if key.group_size < 1 or lead[3] * 8 % key.group_size:
+            raise ValueError("head_dim must be a multiple of group_size")
+        groups = lead[:3] + (lead[3] * 8 // key.group_size,)
+        affine = key.mode == "affine"
+        if affine and dtype not in _FLOATS:
+            raise ValueError("an affine cache's scales must be float32, float16 or bfloat16")
+        for side, w in (("key", key), ("value", value)):
+            _check_tensor(f"the {side} words", w.value, dev, torch.int32)
+            _check_tensor(f"the {side} scales", w.scales, dev, dtype if affine else torch.uint8)
+            if tuple(w.value.shape) != lead or tuple(w.scales.shape) != groups:
+                raise ValueError(f"the {side} words and scales must be {lead} and {groups}")
+            if (w.biases is not None) != affine:
+                raise ValueError("affine caches have biases, others have none")
+            if affine:
+                _check_tensor(f"the {side} biases", w.biases, dev, dtype)
+                if tuple(w.biases.shape) != groups:
+                    raise ValueError(f"the {side} biases must be {groups}")
+        self.pages, self.heads, self.page_size = lead[:3]
+        self.head_dim = lead[3] * 8
+        self.group_size, self.bits, self.mode, self.device = key.group_size, key.bits, key.mode, dev
+        self.dtype = dtype if affine else None      # of an affine cache's scales, and so of its rows
+        # the tensors themselves are kept, so that the addresses below stay theirs
+        self._parts = tuple(t for w in (key, value) for t in (w.value, w.scales, w.biases))
+        self._struct = _CacheStruct(*[None if t is None else t.data_ptr() for t in self._parts], self.mode.encode(),
+                                    self.pages, self.heads, self.page_size, self.head_dim, self.group_size, self.bits,
+                                    _DTYPE[dtype])
+
+    @property
+    def key(self) -> QuantizedWeight:
+        return QuantizedWeight(*self._parts[:3], self.group_size, self.bits, True, self.mode)
+
+    @property
+    def value(self) -> QuantizedWeight:
+        return QuantizedWeight(*self._parts[3:], self.group_size, self.bits, True, self.mode)
+
+
+def kv_cache(pages: int, heads: int, page_size: int, head_dim: int, group_size: Optional[int] = None,
+             mode: str = "affine", dtype: torch.dtype = torch.bfloat16, device="cuda") -> KVCache:
+    """An empty KVCache; dtype is that of an affine cache's scales and rows."""
+    group_size = MODE_DEFAULTS.get(mode, (64, 4))[0] if group_size is None else group_size
+    if group_size < 1 or head_dim < 1 or head_dim % group_size:
+        raise ValueError("head_dim must be a multiple of group_size")
+    lead = (pages, heads, page_size)
+    groups = lead + (head_dim // group_size,)
+
+    def pool():
+        scales = torch.zeros(groups, dtype=dtype if mode == "affine" else torch.uint8, device=device)
+        return QuantizedWeight(torch.zeros(lead + (head_dim // 8,), dtype=torch.int32, device=device), scales,
+                               torch.zeros_like(scales) if mode == "affine" else None, group_size, 4, True, mode)
+
+    return KVCache(pool(), pool())
+
+
+def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
+    """qlin_kv_cache_write: k and v [T, heads, head_dim] quantized into the cache, token t into slot slots[t].
+
+    slots int32 [T]; one outside the pool (-1) is left out, and none may come twice. The tokens of k and v may lie
+    apart, as in a projection's rows.
+    """
+    lib = _lib or load_library()
+    dev = cache.device
+    code = _float_code("k", k)
+    shape = (k.shape[0] if k.dim() else None, cache.heads, cache.head_dim)
+    k_stride = _token_rows("k", k, dev, cache.dtype or k.dtype, shape)
+    v_stride = _token_rows("v", v, dev, k.dtype, shape)
+    _index_rows("slots", slots, dev, shape[0])
+    _run(dev, lib.qlin_kv_cache_write, cache._struct, k.data_ptr(), v.data_ptr(), code, shape[0], k_stride, v_stride,
+         slots.data_ptr())
+
+
+def kv_cache_read(cache: KVCache, slots: torch.Tensor, dtype: Optional[torch.dtype] = None):
+    """qlin_kv_cache_read: (k, v) [T, heads, head_dim] of the rows at slots (int32 [T]), zeros for slots outside the
+    pool; dtype by default the scales' for affine, float32 otherwise, as for dequantize."""
+    lib = _lib or load_library()
+    dev = cache.device
+    _index_rows("slots", slots, dev, None)
+    dtype = dtype or cache.dtype or torch.float32
+    if dtype not in _FLOATS:
+        raise ValueError("dtype must be float32, float16 or bfloat16")
+    shape = (slots.shape[0], cache.heads, cache.head_dim)
+    k = torch.empty(shape, dtype=dtype, device=dev)
+    v = torch.empty(shape, dtype=dtype, device=dev)
+    _run(dev, lib.qlin_kv_cache_read, cache._struct, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
+         _DTYPE[dtype])
+    return k, v
+
+
+def kv_cache_attention_workspace_bytes(cache: KVCache, T: int, q_heads: int, B: int, width: int, has_offsets: bool,
+                                       window: int = 0, dtype: torch.dtype = torch.bfloat16) -> int:
+    """qlin_kv_cache_attention_workspace_bytes for q [T, q_heads, head_dim] of dtype."""
+    return int(load_library().qlin_kv_cache_attention_workspace_bytes(
+        cache._struct, _DTYPE[dtype], T, q_heads, B, width, int(has_offsets), window))
+
+
+def kv_cache_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lengths: torch.Tensor,
+                       offsets: Optional[torch.Tensor] = None, scale: Optional[float] = None, causal: bool = True,
+                       window: int = 0, workspace: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """qlin_kv_cache_attention: attention of q [T, q_heads, head_dim] to the keys of its sequences in the cache.
+
+    Sequence b has lengths[b] keys (int32 [B]), in the pages table[b] (int32 [B, width]) names; its rows of q are
+    offsets[b] to offsets[b + 1] (int32 [B + 1]), the last of them at its last key, or row b alone without offsets.
+    causal hides the keys behind a row's place, window > 0 those that many or more before it. scale is
+    head_dim ** -0.5 by default. Rows of no sequence are left as they are in out (zeros without out); rows that see no
+    key become zeros.
+    """
+    lib = _lib or load_library()
+    dev = cache.device
+    code = _float_code("q", q)
+    if q.dim() != 3:
+        raise ValueError("q must be [T, q_heads, head_dim]")
+    T, heads, D = q.shape
+    q_stride = _token_rows("q", q, dev, cache.dtype or q.dtype, (T, heads, cache.head_dim))
+    _check_tensor("table", table, dev, torch.int32)
+    if table.dim() != 2:
+        raise ValueError("table must be [B, width]")
+    B, width = table.shape
+    _index_rows("lengths", lengths, dev, B)
+    if offsets is not None:
+        _index_rows("offsets", offsets, dev, B + 1)
+    if out is None:
+        # with offsets there may be rows of no sequence
+        out = (torch.empty if offsets is None else torch.zeros)((T, heads, D), dtype=q.dtype, device=dev)
+    else:
+        out = _out(out, (T, heads, D), q.dtype, dev)
+    keep, ws, ws_bytes = _workspace(workspace, lib.qlin_kv_cache_attention_workspace_bytes(
+        cache._struct, code, T, heads, B, width, offsets is not None, window), dev)
+    _run(dev, lib.qlin_kv_cache_attention, cache._struct, q.data_ptr(), code, T, q_stride, heads, table.data_ptr(), B,
+         width, lengths.data_ptr(), None if offsets is None else offsets.data_ptr(),
+         D ** -0.5 if scale is None else scale, bool(causal), window, ws, ws_bytes, out.data_ptr())
+    return out

@@ -1,0 +1,189 @@
+// rotary.hip -- rotary positions: the first R values of each head are taken as
+// R/2 pairs (i, i + R/2), or (2i, 2i + 1) interleaved, and pair i of token t is
+// turned by the angle positions[t] * freqs[i]:
+//     (a, b) -> scale * (a cos - b sin, a sin + b cos)
+// The gradient is the same with the angle's sign changed (the transpose).
+//
+// Bound by the memory: x is read and y written once. A thread owns 16 bytes of
+// a head's row and walks the heads, so that its angles (fp64 product and
+// reduction, polynomials of degree 9 and 10 for sine and cosine) are taken once
+// a token. The partners come from the same row, which the wave's neighbouring
+// lanes read in the same instruction. All of a row's lanes belong to one wave
+// and load before any of them stores, so y may be x.
+
+#include <type_traits>
+
+#include "kv_common.h"
+
+namespace qlin {
+namespace {
+
+// Sine and cosine of 2 pi r for an fp64 number of turns: the turn's fraction
+// is exact in fp64 up to the rounding of r itself, the eighth of a turn around
+// the nearest quarter is left to Taylor polynomials (below 2 * 10^-9 off).
+__device__ __forceinline__ void sincos_turns(double r, float* s, float* c) {
+    const double q = rint(r * 4.0);
+    const float x = (float)((r - q * 0.25) * 6.283185307179586476925);
+    const float x2 = x * x;
+    float p = __builtin_fmaf(x2, 1.0f / 362880.0f, -1.0f / 5040.0f);
+    p = __builtin_fmaf(x2, p, 1.0f / 120.0f);
+    p = __builtin_fmaf(x2, p, -1.0f / 6.0f);
+    const float sn = __builtin_fmaf(x * x2, p, x);
+    p = __builtin_fmaf(x2, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+    p = __builtin_fmaf(x2, p, -1.0f / 720.0f);
+    p = __builtin_fmaf(x2, p, 1.0f / 24.0f);
+    p = __builtin_fmaf(x2, p, -0.5f);
+    const float cs = __builtin_fmaf(x2, p, 1.0f);
+    const int k = (int)(int64_t)(q - 4.0 * floor(q * 0.25));
+    const float a = (k & 1) ? cs : sn, b = (k & 1) ? sn : cs;
+    *s = (k & 2) ? -a : a;
+    *c = (k == 1 || k == 2) ? -b : b;
+}
+
+template <int DT>
+__device__ __forceinline__ float load_one(const void* p, int64_t i) {
+    return load_f<DT>(p, i);
+}
+
+// NV elements (16 bytes) at element i; VEC: one 16-byte load.
+template <int DT, int NV, bool VEC>
+__device__ __forceinline__ void load_run(const void* p, int64_t i, float (&v)[NV]) {
+    if constexpr (!VEC) {
+#pragma unroll
+        for (int e = 0; e < NV; ++e) v[e] = load_f<DT>(p, i + e);
+    } else if constexpr (DT == QLIN_F32) {
+        const float4 t = *(const float4*)((const float*)p + i);
+        v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+    } else {
+        const uint4 t = *(const uint4*)((const uint16_t*)p + i);
+        const uint32_t d[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = DT == QLIN_BF16 ? __uint_as_float(d[e] << 16) : f16_bits_to_f32(d[e] & 0xFFFFu);
+            v[2 * e + 1] = DT == QLIN_BF16 ? __uint_as_float(d[e] & 0xFFFF0000u) : f16_bits_to_f32(d[e] >> 16);
+        }
+    }
+}
+
+template <int DT, int NV, bool VEC>
+__device__ __forceinline__ void store_run(void* p, int64_t i, const float (&v)[NV]) {
+    if constexpr (!VEC) {
+#pragma unroll
+        for (int e = 0; e < NV; ++e) store_f<DT>(p, i + e, v[e]);
+    } else if constexpr (DT == QLIN_F32) {
+        *(float4*)((float*)p + i) = float4{v[0], v[1], v[2], v[3]};
+    } else {
+        uint32_t d[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (DT == QLIN_BF16) {
+                typedef __attribute__((ext_vector_type(2))) __bf16 T2;
+                d[e] = __builtin_bit_cast(uint32_t, T2{(__bf16)v[2 * e], (__bf16)v[2 * e + 1]});
+            } else {
+                d[e] = f32_to_f16_rne(v[2 * e]) | (f32_to_f16_rne(v[2 * e + 1]) << 16);
+            }
+        }
+        *(uint4*)((uint16_t*)p + i) = uint4{d[0], d[1], d[2], d[3]};
+    }
+}
+
+// PAIR 0: interleaved, the partner is a neighbour; 1: half a rotated row away,
+// a whole number of runs; 2: half a row away, anywhere.
+// LANES lanes (a power of two) take a head's row; a block of 256 threads takes
+// 256 / LANES (token, head part) items, part = heads / parts of them.
+template <int DT, int PAIR, bool VEC, int LANES>
+__global__ void __launch_bounds__(256) rotary_kernel(RotaryArgs a, int parts, int part_heads) {
+    constexpr int NV = DT == QLIN_F32 ? 4 : 8;
+    const int64_t item = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
+    const int64_t t = item / parts;
+    const int h0 = (int)(item - t * parts) * part_heads;
+    const int e = (threadIdx.x % LANES) * NV;
+    const bool live = t < a.T && e < a.D;
+    if (!live) return;
+    const int half = a.R / 2;
+    const double turns = (double)a.positions[t] * 0.15915494309189533577;
+    float c[NV], s[NV];
+    int partner[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int d = e + i;
+        const bool turned = d < a.R;
+        const bool second = PAIR == 0 ? d & 1 : d >= half;
+        const int f = PAIR == 0 ? d >> 1 : (second ? d - half : d);
+        partner[i] = !turned ? d : (PAIR == 0 ? d ^ 1 : (second ? d - half : d + half));
+        float sn = 0.0f, cs = 1.0f;
+        if (turned) {
+            sincos_turns(turns * (double)a.freqs[f], &sn, &cs);
+            sn *= a.scale;
+            cs *= a.scale;
+        }
+        s[i] = second != (a.backward != 0) ? sn : -sn;
+        c[i] = cs;
+    }
+    const int run = PAIR == 1 ? partner[0] : 0;
+    const int h1 = min(h0 + part_heads, a.heads);
+    for (int h = h0; h < h1; ++h) {
+        const int64_t row = t * a.x_stride + (int64_t)h * a.D;
+        float v[NV], w[NV], y[NV];
+        load_run<DT, NV, VEC>(a.x, row + e, v);
+        if constexpr (PAIR == 1) {
+            load_run<DT, NV, VEC>(a.x, row + run, w);
+        } else if constexpr (PAIR == 2) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) w[i] = load_f<DT>(a.x, row + partner[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) w[i] = v[i ^ 1];
+        }
+        // the product with the sine rounds first, then the sum: 2^-23 of the pair's size at most
+#pragma unroll
+        for (int i = 0; i < NV; ++i) y[i] = e + i < a.R ? __builtin_fmaf(v[i], c[i], w[i] * s[i]) : v[i];
+        store_run<DT, NV, VEC>(a.y, t * a.y_stride + (int64_t)h * a.D + e, y);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_rotary(const RotaryArgs& a, int dt, hipStream_t st) {
+    const int elem = dt == QLIN_F32 ? 4 : 2, nv = 16 / elem;
+    const bool vec = (((uintptr_t)a.x | (uintptr_t)a.y | (uintptr_t)(a.x_stride * elem) | (uintptr_t)(a.y_stride * elem)) & 15) == 0;
+    const int pair = a.interleaved ? 0 : ((a.R / 2) % nv == 0 ? 1 : 2);
+    int lanes = 1;
+    while (lanes * nv < a.D) lanes *= 2;
+    // heads of a thread: all of them where the tokens alone fill the chip
+    const int64_t want = 4096 * (256 / lanes) / 4;
+    int parts = a.T >= want ? 1 : (int)((want + a.T - 1) / a.T);
+    if (parts > a.heads) parts = a.heads;
+    const int part_heads = (a.heads + parts - 1) / parts;
+    parts = (a.heads + part_heads - 1) / part_heads;
+    const int64_t items = a.T * parts, per = 256 / lanes;
+    const unsigned nb = (unsigned)((items + per - 1) / per);
+    auto go = [&](auto dtc, auto pc, auto vc) -> hipError_t {
+        constexpr int DT = decltype(dtc)::value, P = decltype(pc)::value;
+        constexpr bool V = decltype(vc)::value;
+        switch (lanes) {
+        case 1: rotary_kernel<DT, P, V, 1><<<nb, 256, 0, st>>>(a, parts, part_heads); break;
+        case 2: rotary_kernel<DT, P, V, 2><<<nb, 256, 0, st>>>(a, parts, part_heads); break;
+        case 4: rotary_kernel<DT, P, V, 4><<<nb, 256, 0, st>>>(a, parts, part_heads); break;
+        case 8: rotary_kernel<DT, P, V, 8><<<nb, 256, 0, st>>>(a, parts, part_heads); break;
+        case 16: rotary_kernel<DT, P, V, 16><<<nb, 256, 0, st>>>(a, parts, part_heads); break;
+        case 32: rotary_kernel<DT, P, V, 32><<<nb, 256, 0, st>>>(a, parts, part_heads); break;
+        case 64: rotary_kernel<DT, P, V, 64><<<nb, 256, 0, st>>>(a, parts, part_heads); break;
+        default: return hipErrorInvalidValue;
+        }
+        return hipGetLastError();
+    };
+    auto paired = [&](auto dtc, auto vc) -> hipError_t {
+        if (pair == 0) return go(dtc, std::integral_constant<int, 0>{}, vc);
+        if (pair == 1) return go(dtc, std::integral_constant<int, 1>{}, vc);
+        return go(dtc, std::integral_constant<int, 2>{}, vc);
+    };
+    auto typed = [&](auto dtc) -> hipError_t {
+        return vec ? paired(dtc, std::true_type{}) : paired(dtc, std::false_type{});
+    };
+    if (dt == QLIN_F32) return typed(std::integral_constant<int, QLIN_F32>{});
+    if (dt == QLIN_F16) return typed(std::integral_constant<int, QLIN_F16>{});
+    return typed(std::integral_constant<int, QLIN_BF16>{});
+}
+
+}  // namespace qlin
