@@ -20,9 +20,8 @@ LIB = os.path.join(HERE, "libqlin.so")
 SOURCES = ["qlin_api.cpp", "quant.hip", "qmm_generic.hip", "qmm_decode.hip", "qmm_tiled.hip", "qmm_nt.hip",
            "qmm_prefill.hip", "qmm_prefill2.hip", "gather_index.hip", "qqmm_mx8.hip",
            "moe_api.cpp", "moe_route.hip", "moe_combine.hip", "mx4_prepare.hip", "mx4_matmul.hip",
-           "kv_api.cpp", "kv_store.hip", "rotary.hip", "attend_plan.cpp", "attend_simple.hip",
-           "attend_tile_64.hip", "attend_tile_96.hip", "attend_tile_128.hip", "attend_tile_192.hip",
-           "attend_tile_256.hip"]
+           "kv_api.cpp", "kv_store.hip", "rotary.hip", "attend.cpp", "attend_simple.hip",
+           "attend_64.hip", "attend_96.hip", "attend_128.hip", "attend_192.hip", "attend_256.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 COMMON = ["--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17", "-Wall",
           "-Wno-unused-function", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

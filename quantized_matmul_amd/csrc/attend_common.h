@@ -8,6 +8,11 @@ namespace qlin {
 namespace {
 
 typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
+typedef __attribute__((ext_vector_type(2))) float f32x2;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -31,6 +36,80 @@ __device__ __forceinline__ float scale_at(const void* p, int64_t i) {
     if constexpr (MODE == AFFINE) return load_f<SDT>(p, i);
     else if constexpr (MODE == NVFP4) return e4m3_to_f32(((const uint8_t*)p)[i]);
     else return e8m0_to_f32(((const uint8_t*)p)[i]);
+}
+
+// Two numbers rounded to nearest even.
+template <int DT>
+__device__ __forceinline__ uint32_t round2(float a, float b) {
+    if constexpr (DT == QLIN_BF16) return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+    else return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), f16x2));
+}
+
+struct TileArgs {
+    AttendArgs a;
+    KvPool c;
+    int chunk, splits;           // keys of a workgroup; splits of the grid
+    float* part_o;               // [tile, head, split, row, D]
+    float* part_ml;              // [tile, head, split, row, 2]: maximum (of scores times log2 e), sum
+    const uint8_t* images;       // prompt tiles: dense keys and values of kImageKeys keys, [sequence, key block, head]
+    uint64_t* present;           // [sequence, key block]: which of its keys are there
+    float* key_scale;            // [sequence, key block, head]: what its keys are to be multiplied by
+    int key_blocks;              // of a sequence
+};
+
+template <int DT>
+__device__ __forceinline__ void store4(void* p, int64_t i, f32x4 v) {
+    *(uint2*)((uint16_t*)p + i) = uint2{round2<DT>(v[0], v[1]), round2<DT>(v[2], v[3])};
+}
+
+// Joins the chunks of each row, out = sum f o / sum f l with f = exp2(m - largest
+// m), in the order of the chunks: a wave a row, D / 4 lanes a chunk, the others
+// the next chunks. unit: as the chunks were cut.
+template <int DT, int D>
+__global__ void __launch_bounds__(256) attend_join_kernel(TileArgs t, int tile_rows, int unit) {
+    constexpr int L4 = D / 4, AT_ONCE = 64 / L4;
+    const AttendArgs& a = t.a;
+    const KvPool& c = t.c;
+    const int groups = tile_rows / 4;
+    const int row = (int)(blockIdx.x % groups) * 4 + threadIdx.x / 64, h = blockIdx.x / groups % c.heads;
+    const int64_t tile = blockIdx.x / groups / c.heads;
+    const TileWork w = tile_work(a, c, tile, tile_rows, t.chunk, unit);
+    if (row >= w.rows || w.splits <= 1) return;
+    const int lane = threadIdx.x % 64;
+    const int64_t part = ((tile * c.heads + h) * t.splits) * tile_rows + row;
+    const float* ml = t.part_ml + part * 2;
+    const int64_t step = (int64_t)tile_rows * 2;
+    float top = kNone;
+    for (int i = lane; i < w.splits; i += 64) top = fmaxf(top, ml[i * step]);
+#pragma unroll
+    for (int off = 32; off; off /= 2) top = fmaxf(top, __shfl_xor(top, off, 64));
+    const int mine = lane / L4, d = lane % L4 * 4;
+    f32x4 x{0, 0, 0, 0};
+    float l = 0.0f;
+    if (mine < AT_ONCE) {
+#pragma unroll 4
+        for (int i = mine; i < w.splits; i += AT_ONCE) {
+            const float m = ml[i * step], f = m == kNone ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+            l = __builtin_fmaf(f, ml[i * step + 1], l);
+            x += f * *(const f32x4*)(t.part_o + (part + (int64_t)i * tile_rows) * D + d);
+        }
+    }
+#pragma unroll
+    for (int i = 1; i < AT_ONCE; ++i) {
+        l += __shfl(l, lane + i * L4, 64);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] += __shfl(x[e], lane + i * L4, 64);
+    }
+    if (lane >= L4) return;
+    x *= l == 0.0f ? 0.0f : 1.0f / l;
+    const int share = a.q_heads / c.heads, rr = w.row0 + row;
+    store4<DT>(a.out, ((w.s.first + rr / share) * a.q_heads + h * share + rr % share) * D + d, x);
+}
+
+template <int DT, int D>
+hipError_t launch_join(const TileArgs& t, int64_t tiles, int tile_rows, int unit, hipStream_t st) {
+    attend_join_kernel<DT, D><<<(unsigned)(tiles * t.c.heads * (tile_rows / 4)), 256, 0, st>>>(t, tile_rows, unit);
+    return hipGetLastError();
 }
 
 }  // namespace

@@ -33,12 +33,6 @@
 namespace qlin {
 namespace {
 
-typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
-typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
-typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
-typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
-typedef __attribute__((ext_vector_type(2))) float f32x2;
-
 constexpr int kWaves = 4;
 constexpr int kStep = 32;                       // keys of a wave's step
 constexpr int kMaxChunk = 4096;                 // keys of a workgroup, a multiple of kWaves * kStep
@@ -50,13 +44,6 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
     else
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
-
-// Two numbers rounded to nearest even.
-template <int DT>
-__device__ __forceinline__ uint32_t round2(float a, float b) {
-    if constexpr (DT == QLIN_BF16) return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
-    else return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), f16x2));
 }
 
 // A word's eight codes as an MFMA operand: AFFINE 16 + c, pairs (i, i + 4);
@@ -109,19 +96,6 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-struct TileArgs {
-    AttendArgs a;
-    KvPool c;
-    int chunk, splits;           // keys of a workgroup; splits of the grid
-    float* part_o;               // [tile, head, split, row, D]
-    float* part_ml;              // [tile, head, split, row, 2]
-};
-
-template <int DT>
-__device__ __forceinline__ void store4(void* p, int64_t i, f32x4 v) {
-    *(uint2*)((uint16_t*)p + i) = uint2{round2<DT>(v[0], v[1]), round2<DT>(v[2], v[3])};
-}
-
 // GQ: a quant group's words over 4 (AFFINE 32/64/128: 1/2/4; MXFP4: 1; NVFP4: unused)
 template <int DT, int MODE, int D, int GQ, int NT>
 __global__ void __launch_bounds__(256, D * NT <= 256 ? 2 : 1) attend_tile_kernel(TileArgs t) {
@@ -142,9 +116,9 @@ __global__ void __launch_bounds__(256, D * NT <= 256 ? 2 : 1) attend_tile_kernel
     const KvPool& c = t.c;
     const int split = blockIdx.x % t.splits, h = blockIdx.x / t.splits % c.heads;
     const int64_t tile = blockIdx.x / t.splits / c.heads;
-    const TileWork w = tile_work(a, c, tile, R, t.chunk);
+    const TileWork w = tile_work(a, c, tile, R, t.chunk, kKvUnit);
     if (!w.rows || (split && split >= w.splits)) return;
-    const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64, r = lane % 16, j = lane / 16;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, r = lane % 16, j = lane / 16;
     const int share = a.q_heads / c.heads;
     const int k0 = w.k0 + split * t.chunk, k1 = w.splits ? min(w.hi, k0 + t.chunk) : k0;
     const int steps = (k1 - k0 + kStep - 1) / kStep;
@@ -455,56 +429,11 @@ __global__ void __launch_bounds__(256, D * NT <= 256 ? 2 : 1) attend_tile_kernel
     }
 }
 
-// Joins the chunks of each row: weights exp2(m - largest m), in the order of the
-// chunks within D/4 lanes' groups, then over the groups.
-template <int DT, int D>
-__global__ void __launch_bounds__(256) attend_join_kernel(TileArgs t, int tile_rows) {
-    constexpr int L4 = D / 4, GROUPS = 256 / L4;
-    __shared__ f32x4 sums[GROUPS][L4];
-    __shared__ float parts[GROUPS];
-    const AttendArgs& a = t.a;
-    const KvPool& c = t.c;
-    const int row = blockIdx.x % tile_rows, h = blockIdx.x / tile_rows % c.heads;
-    const int64_t tile = blockIdx.x / tile_rows / c.heads;
-    const TileWork w = tile_work(a, c, tile, tile_rows, t.chunk);
-    if (row >= w.rows || w.splits <= 1) return;
-    const int64_t part = (tile * c.heads + h) * t.splits;
-    const float* ml = t.part_ml + (part * tile_rows + row) * 2;
-    float top = kNone;
-    for (int i = threadIdx.x % 64; i < w.splits; i += 64) top = fmaxf(top, ml[(int64_t)i * tile_rows * 2]);
-#pragma unroll
-    for (int off = 32; off; off /= 2) top = fmaxf(top, __shfl_xor(top, off, 64));
-    const int g = threadIdx.x / L4, d = threadIdx.x % L4;
-    f32x4 x{0, 0, 0, 0};
-    float l = 0.0f;
-    if (g < GROUPS) {
-        for (int i = g; i < w.splits; i += GROUPS) {
-            const float mi = ml[(int64_t)i * tile_rows * 2];
-            const float f = mi == kNone ? 0.0f : __builtin_amdgcn_exp2f(mi - top);
-            l = __builtin_fmaf(f, ml[(int64_t)i * tile_rows * 2 + 1], l);
-            x += f * *(const f32x4*)(t.part_o + ((part + i) * tile_rows + row) * D + d * 4);
-        }
-        sums[g][d] = x;
-        if (d == 0) parts[g] = l;
-    }
-    __syncthreads();
-    if (threadIdx.x >= L4) return;
-    l = parts[0];
-#pragma unroll
-    for (int i = 1; i < GROUPS; ++i) {
-        x += sums[i][d];
-        l += parts[i];
-    }
-    x *= l == 0.0f ? 0.0f : 1.0f / l;
-    const int share = a.q_heads / c.heads, rr = w.row0 + row;
-    store4<DT>(a.out, ((w.s.first + rr / share) * a.q_heads + h * share + rr % share) * D + d * 4, x);
-}
-
 template <int D>
 hipError_t launch_tile_of(const AttendArgs& a, const KvPool& c, int dt, const AttendPlan& p, void* workspace,
                           hipStream_t st) {
     const int R = 16 * p.nt;
-    TileArgs t{a, c, p.chunk, p.splits, (float*)workspace, nullptr};
+    TileArgs t{a, c, p.chunk, p.splits, (float*)workspace, nullptr, nullptr, nullptr, nullptr, 0};
     t.part_ml = t.part_o + p.tiles * c.heads * p.splits * R * D;
     const unsigned grid = (unsigned)(p.tiles * c.heads * p.splits);
     auto run = [&](auto dtc, auto mode, auto gq) -> hipError_t {
@@ -517,8 +446,7 @@ hipError_t launch_tile_of(const AttendArgs& a, const KvPool& c, int dt, const At
             else return hipErrorInvalidValue;
             hipError_t e = hipGetLastError();
             if (e != hipSuccess || p.splits == 1) return e;
-            attend_join_kernel<DT, D><<<(unsigned)(p.tiles * c.heads * R), 256, 0, st>>>(t, R);
-            return hipGetLastError();
+            return launch_join<DT, D>(t, p.tiles, R, kKvUnit, st);
         }
     };
     auto moded = [&](auto dtc) -> hipError_t {

@@ -222,7 +222,7 @@ qlin_status qlin_kv_cache_attention(const qlin_kv_cache* cache, const void* q, q
     qlin_status s;
     if ((s = check_cache(cache, &p)) || (s = check_attention(p, dtype, T, q_heads, B, width, offsets != nullptr, window)))
         return s;
-    if (!std::isfinite((float)scale)) return fail(QLIN_ERR_INVALID_ARGUMENT, "scale must be finite in fp32");
+    if (!std::isfinite((float)(scale * 2))) return fail(QLIN_ERR_INVALID_ARGUMENT, "twice the scale must be finite in fp32");
     if (q_stride < 0 || q_stride > (1LL << 31)) return fail(QLIN_ERR_INVALID_ARGUMENT, "q_stride must be in [0, 2^31]");
     if (T == 0 || B == 0) return ok();
     if (!q || !lengths || !out || (width && !table)) return fail(QLIN_ERR_INVALID_ARGUMENT, "NULL tensor pointer");

@@ -3,6 +3,7 @@
 // reading back, attention).
 #pragma once
 
+#include "attend_plan.h"
 #include "kv_index.h"
 #include "qlin_common.h"
 
@@ -31,20 +32,8 @@ struct RotaryArgs {
 };
 hipError_t launch_rotary(const RotaryArgs& a, int dt, hipStream_t st);
 
-// How a call runs, from its sizes alone.
-struct AttendPlan {
-    int path;                        // 0 simple, 1 row tiles of the matrix cores, 2 prompt tiles
-    int nt;                          // path 1: tiles of 16 rows a workgroup takes
-    int64_t tiles;                   // row tiles of all sequences, at most
-    int chunk, splits;               // keys a workgroup takes, workgroups along the keys
-    size_t bytes;                    // workspace
-};
-AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t width, const KvPool& c, int64_t window,
-                       bool one_row);
 hipError_t launch_attend(const AttendArgs& a, const KvPool& c, int dt, const AttendPlan& p, void* workspace,
                          hipStream_t st);
 hipError_t launch_attend_simple(const AttendArgs& a, const KvPool& c, int dt, hipStream_t st);
-hipError_t launch_attend_tile(const AttendArgs& a, const KvPool& c, int dt, const AttendPlan& p, void* workspace,
-                              hipStream_t st);
 
 }  // namespace qlin

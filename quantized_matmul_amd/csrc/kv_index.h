@@ -105,12 +105,13 @@ QLIN_HD Seen seen_by(const AttendArgs& a, const Sequence& s, int i) {
     return {(int)lo, (int)hi};
 }
 
-// What a tile of rows has to read: keys [k0, hi) in `splits` chunks.
+// What a tile of rows has to read: keys [k0, hi) in `splits` chunks, k0 a multiple of `unit`.
 struct TileWork {
     Sequence s;
     int b, row0, rows, lo, hi, k0, splits;       // row0: of the sequence's n * share rows; rows: of this tile
 };
-QLIN_HD TileWork tile_work(const AttendArgs& a, const KvPool& c, int64_t tile, int tile_rows, int chunk) {
+QLIN_HD TileWork tile_work(const AttendArgs& a, const KvPool& c, int64_t tile, int tile_rows, int chunk,
+                           int unit) {
     const int share = a.q_heads / c.heads;
     TileWork w;
     int64_t rt;
@@ -133,7 +134,7 @@ QLIN_HD TileWork tile_work(const AttendArgs& a, const KvPool& c, int64_t tile, i
     w.rows = rows < tile_rows ? (int)rows : tile_rows;
     w.lo = seen_by(a, w.s, w.row0 / share).lo;
     w.hi = seen_by(a, w.s, (w.row0 + w.rows - 1) / share).hi;
-    w.k0 = w.lo & ~(kKvUnit - 1);
+    w.k0 = w.lo & ~(unit - 1);
     w.splits = w.hi > w.lo ? (w.hi - w.k0 + chunk - 1) / chunk : 0;
     return w;
 }

@@ -39,10 +39,11 @@ def rotary(x, positions, freqs, interleaved=False, scale=1.0, backward=False):
 
 def attention(q, k, v, n_rows, scale, causal=True, window=0, dead=None):
     """One sequence: q [n, HQ, D], k and v [L, H, D]; dead [L] marks keys that are not there. Returns the output and, for
-    each value of it, the sum of p |v| that error bounds are taken of."""
+    each value of it, the sum of p |v| that error bounds are taken of, and the root of the sum of (p (v - o) e)^2, where e is
+    the root of scale^2 sum (q k)^2: what independent errors of the values of k, of one relative size, come to."""
     n, HQ, D = q.shape
     L, H = k.shape[:2]
-    out, size = np.zeros((n, HQ, D)), np.zeros((n, HQ, D))
+    out, size, spread = np.zeros((n, HQ, D)), np.zeros((n, HQ, D)), np.zeros((n, HQ, D))
     for i in range(n):
         at = L - n_rows + i
         keys = np.arange(L)
@@ -60,4 +61,6 @@ def attention(q, k, v, n_rows, scale, causal=True, window=0, dead=None):
             p = np.exp(score - score.max())
             p /= p.sum()
             out[i, h], size[i, h] = p @ vv, p @ np.abs(vv)
-    return out, size
+            e = np.sqrt((kk * kk) @ (q[i, h] * q[i, h])) * abs(scale)
+            spread[i, h] = np.sqrt((p * e) ** 2 @ (vv - out[i, h]) ** 2)
+    return out, size, spread
