@@ -453,7 +453,7 @@ qlin_status qlin_rotary_grad(const void* grad_y, qlin_dtype dtype, int64_t T, in
  *   page_size  a multiple of 16. Slot p * page_size + o is place o of page p;
  *             pages * page_size < 2^31, pages * heads * page_size < 2^35.
  *   head_dim  a multiple of 32 and of group_size, at most 256; heads <= 4096.
- *   codes 16-byte aligned, scales and biases to their type.
+ *   All six pointers 16-byte aligned.
  */
 typedef struct qlin_kv_cache {
     uint32_t* k_codes;

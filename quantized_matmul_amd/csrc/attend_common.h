@@ -18,13 +18,15 @@ typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -__builtin_inff();
 
-// Eight numbers of a word of E2M1 codes, times s.
+// Eight numbers of a word of E2M1 codes, times s (POWER: a power of two, or
+// zero, which the conversion takes for a very small one).
+template <bool POWER = false>
 __device__ __forceinline__ void e2m1_values(uint32_t w, float s, float (&v)[8]) {
-#define QLIN_PAIR(i)                                                           \
-    {                                                                          \
-        const auto f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, i);   \
-        v[2 * i] = f[0] * s;                                                   \
-        v[2 * i + 1] = f[1] * s;                                               \
+#define QLIN_PAIR(i)                                                                        \
+    {                                                                                       \
+        const auto f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, POWER ? s : 1.0f, i);    \
+        v[2 * i] = POWER ? f[0] : f[0] * s;                                                 \
+        v[2 * i + 1] = POWER ? f[1] : f[1] * s;                                             \
     }
     QLIN_PAIR(0) QLIN_PAIR(1) QLIN_PAIR(2) QLIN_PAIR(3)
 #undef QLIN_PAIR
@@ -71,8 +73,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(TileArgs t, int tile_r
     const AttendArgs& a = t.a;
     const KvPool& c = t.c;
     const int groups = tile_rows / 4;
-    const int row = (int)(blockIdx.x % groups) * 4 + threadIdx.x / 64, h = blockIdx.x / groups % c.heads;
-    const int64_t tile = blockIdx.x / groups / c.heads;
+    const int row = (int)(blockIdx.x % groups) * 4 + threadIdx.x / 64, h = blockIdx.y;
+    const int64_t tile = blockIdx.x / groups;
     const TileWork w = tile_work(a, c, tile, tile_rows, t.chunk, unit);
     if (row >= w.rows || w.splits <= 1) return;
     const int lane = threadIdx.x % 64;
@@ -108,7 +110,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(TileArgs t, int tile_r
 
 template <int DT, int D>
 hipError_t launch_join(const TileArgs& t, int64_t tiles, int tile_rows, int unit, hipStream_t st) {
-    attend_join_kernel<DT, D><<<(unsigned)(tiles * t.c.heads * (tile_rows / 4)), 256, 0, st>>>(t, tile_rows, unit);
+    attend_join_kernel<DT, D><<<dim3((unsigned)(tiles * (tile_rows / 4)), (unsigned)t.c.heads), 256, 0, st>>>(t, tile_rows, unit);
     return hipGetLastError();
 }
 

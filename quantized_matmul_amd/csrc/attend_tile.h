@@ -13,8 +13,8 @@
 //   scores^T = K q^T: lane (r = lane % 16, j = lane / 16) of an A operand holds
 //     key r's codes, eight of them a word as they lie in memory; q's operand has
 //     its values in the same order. Keys stay codes: affine ones become 16 + c
-//     (bf16) by a shift and one and-or for two of them, the accumulator starts
-//     at -16 sum(q), and scale and bias join in fp32: score = s acc + z sum(q).
+//     (bf16) by a shift and one and-or for two of them, and scale and bias join
+//     in fp32: score = s acc + (z - 16 s) sum(q).
 //   o^T = V^T p^T: the scores leave the matrix cores as p's operand wants them
 //     (lane (q row, j) has keys 4j..4j+3 of both sub-tiles), so lane (r, j) of V's
 //     operand takes word r of those eight keys: its eight codes are eight rows of
@@ -33,9 +33,8 @@
 namespace qlin {
 namespace {
 
-constexpr int kWaves = 4;
 constexpr int kStep = 32;                       // keys of a wave's step
-constexpr int kMaxChunk = 4096;                 // keys of a workgroup, a multiple of kWaves * kStep
+constexpr int kWindow = 4096;                   // keys whose pages are looked up at once
 constexpr int kScaleRow = kStep + 4;            // floats of a group's scales of a step in LDS: rows on other banks
 
 template <int DT>
@@ -46,33 +45,19 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// A word's eight codes as an MFMA operand: AFFINE 16 + c, pairs (i, i + 4);
-// else the code's number, pairs (2i, 2i + 1).
-template <int DT, int MODE>
+// A word's eight E2M1 codes as numbers, in their order.
+template <int DT>
 __device__ __forceinline__ u32x4 code_operand(uint32_t w) {
-    if constexpr (MODE == AFFINE) {
-        if constexpr (DT == QLIN_BF16)
-            return u32x4{((w << 3) & 0x00780078u) | 0x41804180u, ((w >> 1) & 0x00780078u) | 0x41804180u,
-                         ((w >> 5) & 0x00780078u) | 0x41804180u, ((w >> 9) & 0x00780078u) | 0x41804180u};
-        else
-            return u32x4{((w << 6) & 0x03C003C0u) | 0x4C004C00u, ((w << 2) & 0x03C003C0u) | 0x4C004C00u,
-                         ((w >> 2) & 0x03C003C0u) | 0x4C004C00u, ((w >> 6) & 0x03C003C0u) | 0x4C004C00u};
-    } else if constexpr (DT == QLIN_BF16) {
+    if constexpr (DT == QLIN_BF16)
         return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0)),
                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1)),
                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2)),
                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3))};
-    } else {
+    else
         return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0)),
                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1)),
                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2)),
                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3))};
-    }
-}
-// Value of q in the half-word e (0..7) of that operand.
-template <int MODE>
-__device__ __forceinline__ constexpr int operand_place(int e) {
-    return MODE == AFFINE ? (e / 2) + 4 * (e % 2) : e;
 }
 
 // Largest (sum) over the four lanes l, l ^ 16, l ^ 32, l ^ 48.
@@ -89,6 +74,38 @@ __device__ __forceinline__ float across_sum(float v) {
     return v + __shfl_xor(v, 32, 64);
 }
 
+// 16 (4) bytes a lane from memory into LDS, 64 lanes one after the other from
+// byte `to` on. As statements the compiler would take any later read of LDS for
+// a read of what they bring and wait for all of them there; written out, the
+// waits are wait_loads'. They have no register to write but M0, which nothing
+// else here uses, and the wait state before its use is theirs.
+__device__ __forceinline__ uint32_t lds_byte(const void* p) {
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
+}
+__device__ __forceinline__ void to_lds16(uint32_t to, const uint8_t* base, uint32_t offset) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(offset), "s"(base) : "memory");
+}
+__device__ __forceinline__ void to_lds16(uint32_t to, const uint8_t* from) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+}
+__device__ __forceinline__ void to_lds4(uint32_t to, const uint8_t* from) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory");
+}
+
+// s_waitcnt vmcnt(N). Field layout: vmcnt [3:0] and [15:14], expcnt [6:4], lgkmcnt [11:8].
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+    asm volatile("" ::: "memory");
+}
+
+// s_waitcnt lgkmcnt(0).
+__device__ __forceinline__ void wait_reads() {
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    asm volatile("" ::: "memory");
+}
+
 // LDS writes of a wave before its own reads, without a barrier for the others.
 __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -96,58 +113,110 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// Bits that hide a constant's or a number's value from the compiler, which
+// else takes masks apart again into more instructions.
+__device__ __forceinline__ uint32_t scalar_bits(uint32_t x) {
+    asm("" : "+s"(x));
+    return x;
+}
+__device__ __forceinline__ uint32_t vector_bits(uint32_t x) {
+    asm("" : "+v"(x));
+    return x;
+}
+
+// Nibble I of both halves of w as a pair of 16 + c.
+template <int DT, int I>
+__device__ __forceinline__ uint32_t sixteen_plus(uint32_t w, uint32_t mask, uint32_t sixteen) {
+    constexpr int UP = (DT == QLIN_BF16 ? 3 : 6) - 4 * I;      // from the nibble's place to the highest bits of a mantissa
+    if constexpr (UP >= 0) return ((w << UP) & mask) | sixteen;
+    else return ((w >> -UP) & mask) | sixteen;
+}
+
+// How a kernel's rows are laid out: see the top.
+template <int DT, int MODE, int D, int GQ, int NT, bool PS>
+struct TileShape {
+    static constexpr int G = MODE == NVFP4 ? 16 : 32 * GQ;   // values of a quant group
+    static constexpr int NG = D / G;                         // quant groups of a row
+    static constexpr int DUP = PS ? NG : 1;                  // columns of a row of q
+    static constexpr int PER = 16 / DUP;                     // rows of q in 16 columns
+    static constexpr int R = PER * NT;
+};
+
 // GQ: a quant group's words over 4 (AFFINE 32/64/128: 1/2/4; MXFP4: 1; NVFP4: unused)
-template <int DT, int MODE, int D, int GQ, int NT>
-__global__ void __launch_bounds__(256, D * NT <= 256 ? 2 : 1) attend_tile_kernel(TileArgs t) {
+// PS: values stay codes, see the top (AFFINE, at most two groups).
+template <int DT, int MODE, int D, int GQ, int NT, bool PS, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, D * NT > 256 ? 1 : 2) attend_tile_kernel(TileArgs t) {
+    using S = TileShape<DT, MODE, D, GQ, NT, PS>;
     constexpr int HW = D / 8;                              // words of a head's row
     constexpr int NM = D / 32;                             // MFMAs along D for 16 keys
-    constexpr int G = MODE == NVFP4 ? 16 : 32 * GQ;
-    constexpr int NG = D / G;                              // quant groups of a row
+    constexpr int G = S::G, NG = S::NG, R = S::R, PER = S::PER;
     constexpr int VC = (HW + 15) / 16;                     // words of a value a lane takes
-    constexpr int R = 16 * NT;
     constexpr bool AFF = MODE == AFFINE;
-    constexpr int ARR = AFF ? 4 : 2;                       // scale arrays of a step
-    constexpr int SCALES = kWaves * ARR * NG * kScaleRow, OBUF = R * (D + 4);
-    __shared__ int32_t blocks[kMaxChunk / kKvUnit];
-    __shared__ float buf[SCALES > OBUF ? SCALES : OBUF];
-    __shared__ float wave_ml[kWaves][R][2];
+    static_assert(!PS || (AFF && NG <= 2 && DT == QLIN_BF16), "values as codes");
+    constexpr int ARR = AFF ? 4 : 2;                       // scale arrays of a step: keys', values', biases in the same order
+    constexpr int WSCALES = ARR * NG * kScaleRow;          // a wave's scales as numbers
+    constexpr int CH = D / 32;                             // 16-byte chunks of a head's row
+    constexpr int ES = AFF ? 2 : 1;                        // bytes of a scale
+    constexpr int U = 16 * NG * ES / 4;                    // dwords of 16 keys' scales
+    constexpr int NC = D / 32, NI = (ARR * 2 * U + 63) / 64;     // loads of a step: codes, scales
+    constexpr int STAGE = 32 * D + NI * 256;
+    // two workgroups, or eight waves in one, fill a CU's LDS
+    constexpr int ROOM = (WAVES == 4 ? 78 : 156) * 1024 - WAVES * WSCALES * 4;
+    constexpr int ST = WAVES * 4 * STAGE <= ROOM ? 4 : (WAVES * 3 * STAGE <= ROOM ? 3 : 2);
+    constexpr int ROW = D + 4;                             // floats of a row of o in LDS, rows on other banks
+    constexpr int REGIONS = WAVES * R * ROW * 4 <= 72 * 1024 ? WAVES : (4 * R * ROW * 4 <= 72 * 1024 ? 4 : 1);
+    constexpr int RING = WAVES * ST * STAGE, BUF = RING > REGIONS * R * ROW * 4 ? RING : REGIONS * R * ROW * 4;
+    __shared__ int32_t blocks[kWindow / kKvUnit];
+    __shared__ __attribute__((aligned(16))) uint8_t ring[BUF];
+    __shared__ __attribute__((aligned(16))) float numbers[WAVES * WSCALES];
+    __shared__ float wave_ml[WAVES][R][2];
 
     const AttendArgs& a = t.a;
     const KvPool& c = t.c;
-    const int split = blockIdx.x % t.splits, h = blockIdx.x / t.splits % c.heads;
-    const int64_t tile = blockIdx.x / t.splits / c.heads;
+    const int h = blockIdx.y, split = t.splits == 1 ? 0 : blockIdx.x % t.splits;
+    const int64_t tile = t.splits == 1 ? blockIdx.x : blockIdx.x / t.splits;
     const TileWork w = tile_work(a, c, tile, R, t.chunk, kKvUnit);
     if (!w.rows || (split && split >= w.splits)) return;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, r = lane % 16, j = lane / 16;
     const int share = a.q_heads / c.heads;
     const int k0 = w.k0 + split * t.chunk, k1 = w.splits ? min(w.hi, k0 + t.chunk) : k0;
     const int steps = (k1 - k0 + kStep - 1) / kStep;
-    {
-        const int32_t* table = a.table + (int64_t)w.b * a.width;
-        for (int i = tid; i < steps * (kStep / kKvUnit); i += 256) {
-            const int key = k0 + i * kKvUnit;
+    const int32_t* const table = a.table + (int64_t)w.b * a.width;
+    auto look_up = [&](int first) {                        // row blocks of the keys of a window
+        const int n = min(steps * (kStep / kKvUnit) - first, kWindow / kKvUnit);
+        for (int i = tid; i < n; i += 64 * WAVES) {
+            const int key = k0 + (first + i) * kKvUnit;
             blocks[i] = key < k1 ? kv_row_block(table, c.pages, c.heads, c.page, h, key / kKvUnit) : -1;
         }
-    }
+    };
+    look_up(0);
 
     // rows of q: their place, the keys they see, their operand
     Seen seen[NT];
     u32x4 q[NT][NM];
-    f32x4 start[NT][AFF ? NG : 1];
     float qsum[NT][AFF ? NG : 1];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int rr = min(w.row0 + n * 16 + r, w.row0 + w.rows - 1);     // rows past the end repeat the last
+        const int rr = min(w.row0 + n * PER + r % PER, w.row0 + w.rows - 1);     // rows past the end repeat the last
         seen[n] = seen_by(a, w.s, rr / share);
         const uint16_t* qp = (const uint16_t*)a.q + (w.s.first + rr / share) * a.q_stride + (int64_t)(h * share + rr % share) * D;
+        const bool aligned = ((uintptr_t)qp & 15) == 0;
 #pragma unroll
         for (int m = 0; m < NM; ++m) {
             const int word = MODE == NVFP4 ? m * 4 + j : m / GQ * (4 * GQ) + j * GQ + m % GQ;
-            uint32_t e[8];
+            u32x4 v;
+            if (aligned) {
+                v = *(const u32x4*)(qp + word * 8);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = qp[word * 8 + operand_place<MODE>(i)];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) q[n][m][i] = e[2 * i] | (e[2 * i + 1] << 16);
+                for (int i = 0; i < 4; ++i) v[i] = qp[word * 8 + 2 * i] | ((uint32_t)qp[word * 8 + 2 * i + 1] << 16);
+            }
+            if constexpr (AFF) {                           // values 0..7 to the order of the codes: 0 4 1 5 2 6 3 7
+                q[n][m] = u32x4{(v[0] & 0xFFFFu) | (v[2] << 16), (v[0] >> 16) | (v[2] & 0xFFFF0000u),
+                                (v[1] & 0xFFFFu) | (v[3] << 16), (v[1] >> 16) | (v[3] & 0xFFFF0000u)};
+            } else {
+                q[n][m] = v;
+            }
         }
         if constexpr (AFF) {
 #pragma unroll
@@ -163,211 +232,304 @@ __global__ void __launch_bounds__(256, D * NT <= 256 ? 2 : 1) attend_tile_kernel
                     }
                 sum = across_sum(sum);
                 qsum[n][g] = sum;
-                start[n][g] = f32x4{-16.0f * sum, -16.0f * sum, -16.0f * sum, -16.0f * sum};
             }
         }
     }
+    // keys that every row of the tile sees
+    const int all_lo = seen_by(a, w.s, (w.row0 + w.rows - 1) / share).lo, all_hi = seen_by(a, w.s, w.row0 / share).hi;
     __syncthreads();
 
-    f32x4 o[NT][VC * 8];
-    float m[NT], l[NT];
+    f32x4 o[NT][VC * 8], ones[NT];
+    float m[NT], l[NT], zsum[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         m[n] = kNone;
-        l[n] = 0.0f;
+        l[n] = zsum[n] = 0.0f;
+        ones[n] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < VC * 8; ++i) o[n][i] = f32x4{0, 0, 0, 0};
     }
     const float scale = a.scale * kLog2e;
-    float* const sl = buf + wave * (ARR * NG * kScaleRow);               // this wave's scales: [array, group, key]
+    float* const sl = numbers + wave * WSCALES;                          // this wave's scales: [array, group, key]
     constexpr int SE = (kStep * NG + 63) / 64;                           // a lane's numbers of an array
     constexpr int VROW = HW < 16 ? HW : 16;
+    const uint32_t mask = scalar_bits(DT == QLIN_BF16 ? 0x00780078u : 0x03C003C0u);
+    const uint32_t sixteen = vector_bits(DT == QLIN_BF16 ? 0x41804180u : 0x4C004C00u);
 
-    uint32_t kw[2][NM], vw[8][VC];
-    float sraw[ARR][SE];
-    int32_t rb[2];
-
-    auto load = [&](int step) {
+    // A stage of the ring: the codes of the step's keys and values, [16 keys of them, K or V][row][chunk], then the bytes
+    // of their scales. Key 4 y + x lies in row 4 x + y, its chunks by x further round, so that neither K's reads (16
+    // keys, one chunk) nor V's (keys 4 j + i, 16 words) meet in a bank.
+    uint8_t* const mine = ring + wave * (ST * STAGE);
+    auto turn_of = [](int x) { return (CH & (CH - 1)) ? 0 : x & (CH - 1); };
+    auto word_at = [&](int st, int side, int key, int word) -> int {
+        const int x = key % 4, row = x * 4 + key / 4;
+        return (st * 2 + side) * (8 * D) + row * (D / 2) + (((word / 4) ^ turn_of(x)) * 16) + word % 4 * 4;
+    };
+    // what the lane fetches of each load, past the 16 keys' place in its pool
+    uint32_t code_from[NC];
+    const uint8_t* scale_from[NI];
+    bool scale_second[NI];
 #pragma unroll
-        for (int st = 0; st < 2; ++st) rb[st] = __builtin_amdgcn_readfirstlane(blocks[step * 2 + st]);
+    for (int i = 0; i < NC; ++i) {
+        const int at = (i * 64 + lane) % (D / 2), row = at / CH, x = row / 4, key = row % 4 * 4 + x;
+        code_from[i] = key * (D / 2) + ((at % CH) ^ turn_of(x)) * 16;
+    }
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-            const int64_t row = (int64_t)max(rb[st], 0) * kKvUnit;
-            const uint32_t* kp = c.codes[0] + row * HW;
-            const uint32_t* vp = c.codes[1] + row * HW;
-            if constexpr (MODE == NVFP4) {
+    for (int i = 0; i < NI; ++i) {
+        const int at = min(i * 64 + lane, ARR * 2 * U - 1), s = at / U % ARR;
+        const void* p = c.scales[0];
 #pragma unroll
-                for (int i = 0; i < NM; ++i) kw[st][i] = kp[r * HW + i * 4 + j];
+        for (int e = 1; e < ARR; ++e)
+            if (s == e) p = e < 2 ? c.scales[e] : c.biases[e - 2];
+        scale_from[i] = (const uint8_t*)p + at % U * 4;
+        scale_second[i] = at / U >= ARR;
+    }
+    auto fetch = [&](int at, int stage) {                    // step `at` of the window
+        int32_t b[2];
+#pragma unroll
+        for (int st = 0; st < 2; ++st) b[st] = max(__builtin_amdgcn_readfirstlane(blocks[at * 2 + st]), 0);
+        const uint32_t to = lds_byte(mine) + stage * STAGE;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            if constexpr (D == 128) {                        // a load is 16 keys' rows of one side
+                to_lds16(to + i * 1024, (const uint8_t*)c.codes[i % 2] + (int64_t)b[i / 2] * (8 * D), code_from[i]);
             } else {
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const uint32_t* p = kp + r * HW + g * (4 * GQ) + j * GQ;
-                    if constexpr (GQ == 4) {
-                        const uint4 v = *(const uint4*)p;
-                        kw[st][4 * g] = v.x; kw[st][4 * g + 1] = v.y; kw[st][4 * g + 2] = v.z; kw[st][4 * g + 3] = v.w;
-                    } else if constexpr (GQ == 2) {
-                        const uint2 v = *(const uint2*)p;
-                        kw[st][2 * g] = v.x; kw[st][2 * g + 1] = v.y;
-                    } else {
-                        kw[st][g] = *p;
-                    }
-                }
+                const int part = (i * 64 + lane) / (D / 2);
+                const uint8_t* const k = (const uint8_t*)c.codes[part % 2];
+                to_lds16(to + i * 1024, k + (int64_t)(part / 2 ? b[1] : b[0]) * (8 * D) + code_from[i]);
             }
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < NI; ++i)
+            to_lds4(to + 32 * D + i * 256, scale_from[i] + (int64_t)(scale_second[i] ? b[1] : b[0]) * (U * 4));
+    };
+
+    for (int first = 0; first < steps; first += kWindow / kStep) {
+        if (first) {                                         // another window: its row blocks take the place of the last ones
+            __syncthreads();
+            look_up(first * (kStep / kKvUnit));
+            __syncthreads();
+        }
+        const int n_steps = min(steps - first, kWindow / kStep);
+        // ST - 1 steps on their way; past the end the last one again, so that the counts of loads stay the same
+        if (wave < n_steps) {
+#pragma unroll
+            for (int i = 0; i < ST - 1; ++i) fetch(min(wave + i * WAVES, n_steps - 1), i);
+        }
+        int stage = 0;
+        for (int step = wave; step < n_steps; step += WAVES, stage = stage + 1 == ST ? 0 : stage + 1) {
+            const int key0 = k0 + (first + step) * kStep;
+            const int32_t rb[2] = {__builtin_amdgcn_readfirstlane(blocks[step * 2]), __builtin_amdgcn_readfirstlane(blocks[step * 2 + 1])};
+            fetch(min(step + (ST - 1) * WAVES, n_steps - 1), stage == 0 ? ST - 1 : stage - 1);
+            wait_loads<(ST - 1) * (NC + NI)>();              // this step's have landed
+            const uint8_t* const in = mine + stage * STAGE;
+            // the scales as numbers where the lanes find those of their keys; the keys' take the softmax's scale along,
+            // and their biases what 16 + c has too much
+#pragma unroll
+            for (int e = 0; e < SE; ++e) {
+                const int at = lane + 64 * e, key = min(at / NG, kStep - 1), g = at % NG, st = key / kKvUnit;
+                const bool live = (st ? rb[1] : rb[0]) >= 0 && key0 + key < k1;
+                const uint8_t* const raw = in + 32 * D + st * (ARR * U * 4) + (key % kKvUnit * NG + g) * ES;
+                float x[ARR];
+#pragma unroll
+                for (int s = 0; s < ARR; ++s) x[s] = scale_at<MODE, DT>(raw + s * (U * 4), 0);
+                if (MODE != NVFP4) x[0] *= scale;
+                if (AFF) x[ARR - 2] = __builtin_fmaf(x[0], -16.0f, x[ARR - 2] * scale);
+                if (PS) x[ARR - 1] = __builtin_fmaf(x[1], 8.0f, x[ARR - 1]);
+                if (kStep * NG % 64 == 0 || at < kStep * NG)
+#pragma unroll
+                    for (int s = 0; s < ARR; ++s) sl[(s * NG + g) * kScaleRow + key] = live ? x[s] : 0.0f;
+            }
+            wave_fence();
+            uint32_t vw[8][VC];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
 #pragma unroll
                 for (int v = 0; v < VC; ++v) {
                     const int word = v * 16 + r;
-                    vw[st * 4 + i][v] = vp[(4 * j + i) * HW + (word < HW ? word : word - VROW)];
+                    vw[e][v] = *(const uint32_t*)(in + word_at(e / 4, 1, 4 * j + e % 4, word < HW ? word : word - VROW));
                 }
-        }
+            f32x4 sc[NT][2];
 #pragma unroll
-        for (int e = 0; e < SE; ++e) {
-            const int at = lane + 64 * e, key = at / NG, g = at % NG;
-            const bool second = key >= kKvUnit;
-            const int32_t b = second ? rb[1] : rb[0];
-            const bool live = b >= 0 && k0 + step * kStep + key < k1 && at < kStep * NG;
-            const int64_t i = ((int64_t)max(b, 0) * kKvUnit + key % kKvUnit) * NG + g;
+            for (int st = 0; st < 2; ++st) {
+                if constexpr (MODE == NVFP4) {
 #pragma unroll
-            for (int s = 0; s < ARR; ++s) {
-                const void* p = s < 2 ? c.scales[s] : c.biases[s - 2];
-                const float x = AFF ? load_f<DT>(p, i) : scale_at<MODE, DT>(p, i);
-                sraw[s][e] = live ? x : 0.0f;
-            }
-        }
-    };
-
-    if (wave < steps) load(wave);
-    for (int step = wave; step < steps; step += kWaves) {
-        const int key0 = k0 + step * kStep;
-        // the step's scales where the lanes find those of their keys
+                    for (int n = 0; n < NT; ++n) sc[n][st] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < SE; ++e) {
-            const int at = lane + 64 * e;
-            if (kStep * NG % 64 == 0 || at < kStep * NG)
+                    for (int i = 0; i < NM; ++i) {
+                        // the word's group is not its MFMA's only one: its codes take their scale here, exact in both types
+                        const float s = sl[(2 * i + j / 2) * kScaleRow + st * 16 + r];
+                        float v[8];
+                        e2m1_values(*(const uint32_t*)(in + word_at(st, 0, r, i * 4 + j)), s, v);
+                        const u32x4 k{round2<DT>(v[0], v[1]), round2<DT>(v[2], v[3]), round2<DT>(v[4], v[5]), round2<DT>(v[6], v[7])};
 #pragma unroll
-                for (int s = 0; s < ARR; ++s) sl[(s * NG + at % NG) * kScaleRow + at / NG] = sraw[s][e];
-        }
-        wave_fence();
-        f32x4 sc[NT][2];
+                        for (int n = 0; n < NT; ++n) sc[n][st] = mfma16<DT>(k, q[n][i], sc[n][st]);
+                    }
+                } else {
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-            if constexpr (MODE == NVFP4) {
+                    for (int g = 0; g < NG; ++g) {
+                        const f32x4 s = *(const f32x4*)(sl + g * kScaleRow + st * 16 + 4 * j);
+                        f32x4 z{0, 0, 0, 0};
+                        if constexpr (AFF) z = *(const f32x4*)(sl + (2 * NG + g) * kScaleRow + st * 16 + 4 * j);
+                        uint32_t kw[GQ];
+                        const uint8_t* const kp = in + word_at(st, 0, r, g * (4 * GQ) + j * GQ);
+                        if constexpr (GQ == 4) {
+                            const uint4 x = *(const uint4*)kp;
+                            kw[0] = x.x; kw[1] = x.y; kw[2] = x.z; kw[3] = x.w;
+                        } else if constexpr (GQ == 2) {
+                            const uint2 x = *(const uint2*)kp;
+                            kw[0] = x.x; kw[1] = x.y;
+                        } else {
+                            kw[0] = *(const uint32_t*)kp;
+                        }
+                        u32x4 k[GQ];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) sc[n][st] = f32x4{0, 0, 0, 0};
+                        for (int i = 0; i < GQ; ++i) {
+                            const uint32_t x = kw[i];
+                            if constexpr (AFF)
+                                k[i] = u32x4{sixteen_plus<DT, 0>(x, mask, sixteen), sixteen_plus<DT, 1>(x, mask, sixteen),
+                                             sixteen_plus<DT, 2>(x, mask, sixteen), sixteen_plus<DT, 3>(x, mask, sixteen)};
+                            else k[i] = code_operand<DT>(x);
+                        }
 #pragma unroll
-                for (int i = 0; i < NM; ++i) {
-                    // the word's group is not its MFMA's only one: its codes take their scale here, exact in both types
-                    const float s = sl[(2 * i + j / 2) * kScaleRow + st * 16 + r];
-                    float v[8];
-                    e2m1_values(kw[st][i], s, v);
-                    const u32x4 k{round2<DT>(v[0], v[1]), round2<DT>(v[2], v[3]), round2<DT>(v[4], v[5]), round2<DT>(v[6], v[7])};
+                        for (int n = 0; n < NT; ++n) {
+                            f32x4 acc{0, 0, 0, 0};
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) sc[n][st] = mfma16<DT>(k, q[n][i], sc[n][st]);
-                }
-            } else {
+                            for (int i = 0; i < GQ; ++i) acc = mfma16<DT>(k[i], q[n][g * GQ + i], acc);
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const f32x4 s = *(const f32x4*)(sl + g * kScaleRow + st * 16 + 4 * j);
-                    f32x4 z{0, 0, 0, 0};
-                    if constexpr (AFF) z = *(const f32x4*)(sl + (2 * NG + g) * kScaleRow + st * 16 + 4 * j);
-                    u32x4 k[GQ];
-#pragma unroll
-                    for (int i = 0; i < GQ; ++i) k[i] = code_operand<DT, MODE>(kw[st][g * GQ + i]);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        f32x4 acc = AFF ? start[n][g] : f32x4{0, 0, 0, 0};
-#pragma unroll
-                        for (int i = 0; i < GQ; ++i) acc = mfma16<DT>(k[i], q[n][g * GQ + i], acc);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float x = g ? sc[n][st][i] : 0.0f;
-                            if constexpr (AFF) x = g ? __builtin_fmaf(z[i], qsum[n][g], x) : z[i] * qsum[n][g];
-                            sc[n][st][i] = (AFF || g) ? __builtin_fmaf(s[i], acc[i], x) : s[i] * acc[i];
+                            for (int i = 0; i < 4; ++i) {
+                                float x = g ? sc[n][st][i] : 0.0f;
+                                if constexpr (AFF) x = g ? __builtin_fmaf(z[i], qsum[n][g], x) : z[i] * qsum[n][g];
+                                sc[n][st][i] = (AFF || g) ? __builtin_fmaf(s[i], acc[i], x) : s[i] * acc[i];
+                            }
                         }
                     }
                 }
             }
-        }
-        const bool whole[2] = {rb[0] >= 0, rb[1] >= 0};
-        u32x4 p[NT];
+            const bool whole = key0 >= all_lo && key0 + kStep <= all_hi && (rb[0] | rb[1]) >= 0;
+            u32x4 p[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float x[8];
+            for (int n = 0; n < NT; ++n) {
+                float x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = sc[n][e / 4][e % 4] * scale;
-            const bool inside = key0 >= seen[n].lo && key0 + kStep <= seen[n].hi && whole[0] && whole[1];
-            if (__any(!inside)) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int key = key0 + e / 4 * 16 + 4 * j + e % 4;
-                    if (key < seen[n].lo || key >= seen[n].hi || !whole[e / 4]) x[e] = kNone;
-                }
-            }
-            float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-            top = fmaxf(across_max(top), m[n]);
-            if (__any(top > m[n])) {
-                const float f = m[n] == kNone ? 0.0f : __builtin_amdgcn_exp2f(m[n] - top);
-                m[n] = top;
-                l[n] *= f;
-#pragma unroll
-                for (int i = 0; i < VC * 8; ++i) o[n][i] *= f;
-            }
-            const float base = m[n] == kNone ? 0.0f : m[n];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[e] = __builtin_amdgcn_exp2f(x[e] - base);
-                l[n] += x[e];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p[n][i] = round2<DT>(x[2 * i], x[2 * i + 1]);
-        }
-        // values: word v*16 + r of the lane's eight keys
-#pragma unroll
-        for (int v = 0; v < VC; ++v) {
-            const int word = v * 16 + r, g = (word < HW ? word : word - VROW) / (G / 8);
-            const f32x4 s0 = *(const f32x4*)(sl + (NG + g) * kScaleRow + 4 * j);
-            const f32x4 s1 = *(const f32x4*)(sl + (NG + g) * kScaleRow + 16 + 4 * j);
-            if constexpr (AFF) {
-                const f32x4 z0 = *(const f32x4*)(sl + (3 * NG + g) * kScaleRow + 4 * j);
-                const f32x4 z1 = *(const f32x4*)(sl + (3 * NG + g) * kScaleRow + 16 + 4 * j);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float x[8];
+                for (int e = 0; e < 8; ++e) x[e] = MODE == NVFP4 ? sc[n][e / 4][e % 4] * scale : sc[n][e / 4][e % 4];
+                if (!whole) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const uint32_t even = vw[e][v] & 0x0F0F0F0Fu, odd = (vw[e][v] >> 4) & 0x0F0F0F0Fu;
-                        const float code = (float)(((i & 1 ? odd : even) >> (i / 2 * 8)) & 0xFFu);
-                        x[e] = __builtin_fmaf(e < 4 ? s0[e & 3] : s1[e & 3], code, e < 4 ? z0[e & 3] : z1[e & 3]);
+                        const int key = key0 + e / 4 * 16 + 4 * j + e % 4;
+                        if (key < seen[n].lo || key >= seen[n].hi || rb[e / 4] < 0) x[e] = kNone;
                     }
-                    const u32x4 vt{round2<DT>(x[0], x[1]), round2<DT>(x[2], x[3]), round2<DT>(x[4], x[5]), round2<DT>(x[6], x[7])};
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) o[n][v * 8 + i] = mfma16<DT>(vt, p[n], o[n][v * 8 + i]);
                 }
-            } else {
-                float x[8][8];
+                float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+                top = across_max(top);
+                if (__any(top > m[n])) {
+                    const float to = fmaxf(top, m[n]), f = m[n] == kNone ? 0.0f : __builtin_amdgcn_exp2f(m[n] - to);
+                    m[n] = to;
+                    l[n] *= f;
+                    if constexpr (PS) {
+                        zsum[n] *= f;
+                        ones[n] *= f;
+                    }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) e2m1_values(vw[e][v], e < 4 ? s0[e & 3] : s1[e & 3], x[e]);
+                    for (int i = 0; i < VC * 8; ++i) o[n][i] *= f;
+                }
+                const float base = m[n] == kNone ? 0.0f : m[n];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const u32x4 vt{round2<DT>(x[0][i], x[1][i]), round2<DT>(x[2][i], x[3][i]),
-                                   round2<DT>(x[4][i], x[5][i]), round2<DT>(x[6][i], x[7][i])};
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = __builtin_amdgcn_exp2f(x[e] - base);
+                    l[n] += x[e];
+                }
+                if constexpr (PS) {                          // p times the scales of the column's group; the biases' part
+                    const float* const vs = sl + (NG + r / PER) * kScaleRow + 4 * j;
+                    const float* const vz = sl + (3 * NG + r / PER) * kScaleRow + 4 * j;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) o[n][v * 8 + i] = mfma16<DT>(vt, p[n], o[n][v * 8 + i]);
+                    for (int st = 0; st < 2; ++st) {
+                        const f32x4 s = *(const f32x4*)(vs + 16 * st), z = *(const f32x4*)(vz + 16 * st);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            zsum[n] = __builtin_fmaf(x[4 * st + i], z[i], zsum[n]);
+                            x[4 * st + i] *= s[i];
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[n][i] = round2<DT>(x[2 * i], x[2 * i + 1]);
+                if constexpr (PS) ones[n] = mfma16<DT>(u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}, p[n], ones[n]);
+            }
+            // values: word v*16 + r of the lane's eight keys
+#pragma unroll
+            for (int v = 0; v < VC; ++v) {
+                if constexpr (PS) {
+                    auto four = [&](uint32_t halves, int to) {       // the low or high halves: four codes of each key
+                        u32x4 x;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[e] = __builtin_amdgcn_perm(vw[2 * e + 1][v], vw[2 * e][v], halves);
+                        auto one = [&](auto ic) {
+                            constexpr int I = decltype(ic)::value;
+                            const u32x4 vt{sixteen_plus<DT, I>(x[0], mask, sixteen), sixteen_plus<DT, I>(x[1], mask, sixteen),
+                                           sixteen_plus<DT, I>(x[2], mask, sixteen), sixteen_plus<DT, I>(x[3], mask, sixteen)};
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) o[n][v * 8 + to + I] = mfma16<DT>(vt, p[n], o[n][v * 8 + to + I]);
+                        };
+                        one(std::integral_constant<int, 0>{});
+                        one(std::integral_constant<int, 1>{});
+                        one(std::integral_constant<int, 2>{});
+                        one(std::integral_constant<int, 3>{});
+                    };
+                    four(0x05040100u, 0);
+                    four(0x07060302u, 4);
+                } else {
+                    const int word = v * 16 + r, g = (word < HW ? word : word - VROW) / (G / 8);
+                    const f32x4 s0 = *(const f32x4*)(sl + (NG + g) * kScaleRow + 4 * j);
+                    const f32x4 s1 = *(const f32x4*)(sl + (NG + g) * kScaleRow + 16 + 4 * j);
+                    if constexpr (AFF) {
+                        const f32x4 z0 = *(const f32x4*)(sl + (3 * NG + g) * kScaleRow + 4 * j);
+                        const f32x4 z1 = *(const f32x4*)(sl + (3 * NG + g) * kScaleRow + 16 + 4 * j);
+                        uint32_t code[8][2];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            code[e][0] = vector_bits(vw[e][v] & 0x0F0F0F0Fu);
+                            code[e][1] = vector_bits((vw[e][v] >> 4) & 0x0F0F0F0Fu);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float x[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                x[e] = __builtin_fmaf(e < 4 ? s0[e & 3] : s1[e & 3], (float)((code[e][i & 1] >> (i / 2 * 8)) & 0xFFu),
+                                                      e < 4 ? z0[e & 3] : z1[e & 3]);
+                            const u32x4 vt{round2<DT>(x[0], x[1]), round2<DT>(x[2], x[3]), round2<DT>(x[4], x[5]), round2<DT>(x[6], x[7])};
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) o[n][v * 8 + i] = mfma16<DT>(vt, p[n], o[n][v * 8 + i]);
+                        }
+                    } else {
+                        float x[8][8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) e2m1_values<MODE == MXFP4>(vw[e][v], e < 4 ? s0[e & 3] : s1[e & 3], x[e]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const u32x4 vt{round2<DT>(x[0][i], x[1][i]), round2<DT>(x[2][i], x[3][i]),
+                                           round2<DT>(x[4][i], x[5][i]), round2<DT>(x[6][i], x[7][i])};
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) o[n][v * 8 + i] = mfma16<DT>(vt, p[n], o[n][v * 8 + i]);
+                        }
+                    }
                 }
             }
+            wait_reads();                                    // this stage is read before another takes its place
         }
-        wave_fence();                                        // scales are read before the next step's come
-        if (step + kWaves < steps) load(step + kWaves);
+        wait_loads<0>();                                     // the loads past the end have landed, too
     }
 
-    // the waves' sums: a common maximum, then o added up in LDS in the order of the waves
+    // the waves' sums: a common maximum, then o added up in the order of the waves
+    float* const buf = (float*)ring;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         l[n] = across_sum(l[n]);
-        if (j == 0) {
-            wave_ml[wave][n * 16 + r][0] = m[n];
-            wave_ml[wave][n * 16 + r][1] = l[n];
+        if constexpr (PS) zsum[n] = across_sum(zsum[n]);
+        if (j == 0 && r < PER) {
+            wave_ml[wave][n * PER + r][0] = m[n];
+            wave_ml[wave][n * PER + r][1] = l[n];
         }
     }
     __syncthreads();
@@ -375,23 +537,24 @@ __global__ void __launch_bounds__(256, D * NT <= 256 ? 2 : 1) attend_tile_kernel
     for (int n = 0; n < NT; ++n) {
         float top = kNone;
 #pragma unroll
-        for (int i = 0; i < kWaves; ++i) top = fmaxf(top, wave_ml[i][n * 16 + r][0]);
+        for (int i = 0; i < WAVES; ++i) top = fmaxf(top, wave_ml[i][n * PER + r % PER][0]);
         const float f = m[n] == kNone ? 0.0f : __builtin_amdgcn_exp2f(m[n] - top);
+        const float plus = PS ? zsum[n] - 24.0f * ones[n][0] : 0.0f;      // all rows of `ones` are the column's sum
 #pragma unroll
-        for (int i = 0; i < VC * 8; ++i) o[n][i] *= f;
+        for (int i = 0; i < VC * 8; ++i) o[n][i] = PS ? (o[n][i] + plus) * f : o[n][i] * f;
     }
-    for (int turn = 0; turn < kWaves; ++turn) {
-        if (turn == wave) {
+    for (int turn = 0; turn < WAVES / REGIONS; ++turn) {
+        if (turn == wave / REGIONS) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                if (n * 16 + r >= w.rows) continue;
+                if (n * PER + r % PER >= w.rows) continue;
 #pragma unroll
                 for (int v = 0; v < VC; ++v)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int word = v * 16 + 4 * j + i;
-                        if (word >= HW) continue;
-                        f32x4* at = (f32x4*)(buf + (n * 16 + r) * (D + 4) + word * 8);
+                        if (word >= HW || (PS && word / (G / 8) != r / PER)) continue;
+                        f32x4* at = (f32x4*)(buf + (wave % REGIONS * R + n * PER + r % PER) * ROW + word * 8);
                         f32x4 x0{o[n][v * 8][i], o[n][v * 8 + 1][i], o[n][v * 8 + 2][i], o[n][v * 8 + 3][i]};
                         f32x4 x1{o[n][v * 8 + 4][i], o[n][v * 8 + 5][i], o[n][v * 8 + 6][i], o[n][v * 8 + 7][i]};
                         if (turn) {
@@ -406,15 +569,17 @@ __global__ void __launch_bounds__(256, D * NT <= 256 ? 2 : 1) attend_tile_kernel
         __syncthreads();
     }
     const int64_t part = (tile * c.heads + h) * t.splits + split;
-    for (int e = tid; e < w.rows * (D / 4); e += 256) {
+    for (int e = tid; e < w.rows * (D / 4); e += 64 * WAVES) {
         const int row = e / (D / 4), d = e % (D / 4) * 4;
         float top = kNone, sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kWaves; ++i) top = fmaxf(top, wave_ml[i][row][0]);
+        for (int i = 0; i < WAVES; ++i) top = fmaxf(top, wave_ml[i][row][0]);
 #pragma unroll
-        for (int i = 0; i < kWaves; ++i)
+        for (int i = 0; i < WAVES; ++i)
             sum += wave_ml[i][row][0] == kNone ? 0.0f : wave_ml[i][row][1] * __builtin_amdgcn_exp2f(wave_ml[i][row][0] - top);
-        f32x4 x = *(const f32x4*)(buf + row * (D + 4) + d);
+        f32x4 x = *(const f32x4*)(buf + row * ROW + d);
+#pragma unroll
+        for (int i = 1; i < REGIONS; ++i) x += *(const f32x4*)(buf + (i * R + row) * ROW + d);
         if (w.splits <= 1) {
             x *= sum == 0.0f ? 0.0f : 1.0f / sum;                        // a row that sees no key: zeros
             const int rr = w.row0 + row;
@@ -432,21 +597,40 @@ __global__ void __launch_bounds__(256, D * NT <= 256 ? 2 : 1) attend_tile_kernel
 template <int D>
 hipError_t launch_tile_of(const AttendArgs& a, const KvPool& c, int dt, const AttendPlan& p, void* workspace,
                           hipStream_t st) {
-    const int R = 16 * p.nt;
     TileArgs t{a, c, p.chunk, p.splits, (float*)workspace, nullptr, nullptr, nullptr, nullptr, 0};
-    t.part_ml = t.part_o + p.tiles * c.heads * p.splits * R * D;
-    const unsigned grid = (unsigned)(p.tiles * c.heads * p.splits);
+    t.part_ml = t.part_o + p.tiles * c.heads * p.splits * p.rows * D;
+    const dim3 grid((unsigned)(p.tiles * p.splits), (unsigned)c.heads);
     auto run = [&](auto dtc, auto mode, auto gq) -> hipError_t {
         constexpr int DT = decltype(dtc)::value, M = decltype(mode)::value, GQ = decltype(gq)::value;
         if constexpr (M == AFFINE && D % (32 * GQ) != 0) {
             return hipErrorInvalidValue;
         } else {
-            if (p.nt == 1) attend_tile_kernel<DT, M, D, GQ, 1><<<grid, 256, 0, st>>>(t);
-            else if (p.nt == 2) attend_tile_kernel<DT, M, D, GQ, 2><<<grid, 256, 0, st>>>(t);
-            else return hipErrorInvalidValue;
+            constexpr bool CAN = M == AFFINE && DT == QLIN_BF16 && D / (32 * GQ) <= 2;     // as the plan has it
+            
+            auto go = [&](auto ntc, auto psc) {
+                constexpr int NT = decltype(ntc)::value;
+                constexpr bool PS = decltype(psc)::value;
+                constexpr int MANY = 8;
+                if constexpr (NT == 1 && D <= 128)
+                    if (p.waves == MANY) {
+                        attend_tile_kernel<DT, M, D, GQ, NT, PS, MANY><<<grid, 64 * MANY, 0, st>>>(t);
+                        return;
+                    }
+                attend_tile_kernel<DT, M, D, GQ, NT, PS, 4><<<grid, 256, 0, st>>>(t);
+            };
+            using N1 = std::integral_constant<int, 1>;
+            using N2 = std::integral_constant<int, 2>;
+            if (p.codes != (CAN && p.codes)) return hipErrorInvalidValue;
+            if (p.nt == 1) {
+                if (CAN && p.codes) go(N1{}, std::integral_constant<bool, CAN>{});
+                else go(N1{}, std::false_type{});
+            } else {
+                if (CAN && p.codes && D == 32 * GQ) go(N2{}, std::integral_constant<bool, CAN && D == 32 * GQ>{});
+                else go(N2{}, std::false_type{});
+            }
             hipError_t e = hipGetLastError();
             if (e != hipSuccess || p.splits == 1) return e;
-            return launch_join<DT, D>(t, p.tiles, R, kKvUnit, st);
+            return launch_join<DT, D>(t, p.tiles, p.rows, kKvUnit, st);
         }
     };
     auto moded = [&](auto dtc) -> hipError_t {

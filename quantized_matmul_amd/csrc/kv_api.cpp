@@ -85,9 +85,7 @@ qlin_status check_pool(const qlin::KvPool& p) {
         if (!affine && p.biases[side]) return fail(QLIN_ERR_INVALID_ARGUMENT, "only affine caches have biases");
         qlin_status s;
         if ((s = check_aligned(p.codes[side], 16, "codes"))) return s;
-        if (affine && ((s = check_aligned(p.scales[side], elem(p.sdt), "scales")) ||
-                       (s = check_aligned(p.biases[side], elem(p.sdt), "biases"))))
-            return s;
+        if ((s = check_aligned(p.scales[side], 16, "scales")) || (s = check_aligned(p.biases[side], 16, "biases"))) return s;
     }
     return QLIN_OK;
 }
@@ -231,6 +229,7 @@ qlin_status qlin_kv_cache_attention(const qlin_kv_cache* cache, const void* q, q
         (s = check_aligned(offsets, 4, "offsets")))
         return s;
     const qlin::AttendPlan plan = qlin::attend_plan(dtype, T, (int)q_heads, B, width, p, window, offsets == nullptr);
+    if (!plan.fits) return fail(QLIN_ERR_UNSUPPORTED, "more rows than one launch holds: split them over several calls");
     if (plan.bytes) {
         if (!workspace || workspace_bytes < plan.bytes)
             return fail(QLIN_ERR_INVALID_ARGUMENT, "workspace of %zu bytes needed (got %zu)", plan.bytes,

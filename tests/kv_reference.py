@@ -37,10 +37,10 @@ def rotary(x, positions, freqs, interleaved=False, scale=1.0, backward=False):
     return y
 
 
-def attention(q, k, v, n_rows, scale, causal=True, window=0, dead=None):
+def attention(q, k, v, n_rows, scale, causal=True, window=0, dead=None, steps=None):
     """One sequence: q [n, HQ, D], k and v [L, H, D]; dead [L] marks keys that are not there. Returns the output and, for
     each value of it, the sum of p |v| that error bounds are taken of, and the root of the sum of (p (v - o) e)^2, where e is
-    the root of scale^2 sum (q k)^2: what independent errors of the values of k, of one relative size, come to."""
+    the root of scale^2 sum (q k)^2: what independent errors of the values of k, of one relative size, come to. steps [L, H, D]: instead of |v| in that sum."""
     n, HQ, D = q.shape
     L, H = k.shape[:2]
     out, size, spread = np.zeros((n, HQ, D)), np.zeros((n, HQ, D)), np.zeros((n, HQ, D))
@@ -60,7 +60,8 @@ def attention(q, k, v, n_rows, scale, causal=True, window=0, dead=None):
             score = kk @ q[i, h] * scale
             p = np.exp(score - score.max())
             p /= p.sum()
-            out[i, h], size[i, h] = p @ vv, p @ np.abs(vv)
+            out[i, h] = p @ vv
+            size[i, h] = p @ (np.abs(vv) if steps is None else steps[keys, h // (HQ // H)])
             e = np.sqrt((kk * kk) @ (q[i, h] * q[i, h])) * abs(scale)
             spread[i, h] = np.sqrt((p * e) ** 2 @ (vv - out[i, h]) ** 2)
     return out, size, spread

@@ -9,7 +9,9 @@ Tolerance, for each output o = sum p v with size = sum p |v|:
             their standard deviation (2^-25 of the largest where f16 has no more bits, inside the scores' bound); through scores and softmax they reach o as `spread` of kv_reference, times 6 for the many outputs
             (and twice that, as p and the sum of p move together).
   exp2      1 ulp each: 2 * 2^-23.
-  p, v      on the matrix cores each rounded to the type once: 2 u of the size, u = eps / 2 of the type.
+  p, v      on the matrix cores each rounded to the type once: 2 u of the size, u = eps / 2 of the type. Where the values
+            stay codes (bf16, affine) p times the group's scale is rounded instead, and multiplies c - 8, the rest being
+            fp32: u p s |c - 8|, which is at most 8 s u p for each key.
   sums      fp32 over L keys: sqrt(L) + 8 roundings of 2^-24.
   output    one rounding: u of itself; and f16's smallest step.
 """
@@ -89,6 +91,10 @@ class Problem:
             k, v = [np.where(dead[:, None, None], 0.0, x[np.where(dead, 0, p), :, i % self.page]) for x in pools] if L else \
                 (np.zeros((0, self.H, self.D)),) * 2
             o, size, spread = ref.attention(q[first : first + n], k, v, n, scale, causal, window, dead)
+            if self.mode == "affine" and self.dtype == "bf16" and not self.prompt and L:
+                s = np.repeat(np.nan_to_num(f64(self.cache.value.scales)), self.g, -1)
+                steps = 8 * np.where(dead[:, None, None], 0.0, s[np.where(dead, 0, p), :, i % self.page])
+                size = size + ref.attention(q[first : first + n], k, v, n, scale, causal, window, dead, steps)[1]
             kmax = np.abs(k).max() if L else 0.0
             d = 4 * np.sqrt(self.D) * 2.0 ** -24 * abs(scale) * np.abs(q[first : first + n]).sum(-1, keepdims=True) * 6 * kmax
             out[first : first + n] = o
