@@ -17,6 +17,7 @@ typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -__builtin_inff();
+constexpr float kSlack = 8.0f;                  // log2 of how far scores may pass the running maximum
 
 // Eight numbers of a word of E2M1 codes, times s (POWER: a power of two, or
 // zero, which the conversion takes for a very small one).

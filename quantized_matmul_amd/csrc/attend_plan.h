@@ -26,7 +26,7 @@ struct AttendPlan {
 inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t width, const KvPool& c, int64_t window,
                               bool one_row) {
     constexpr int64_t kStepKeys = 32;        // keys of a wave's step
-    constexpr int64_t kChunkMost = 2048;     // keys a workgroup takes, where that makes no more than kMany of them
+    constexpr int64_t kChunkMost = 4096;     // keys a workgroup takes, where that makes no more than kMany of them
     constexpr int64_t kWorkgroups = 2048;    // enough of them to fill the chip evenly
     constexpr int64_t kMany = 32768;
     constexpr int64_t kPromptRows = 64;      // rows of a sequence and key head, on average, from which a prompt is one

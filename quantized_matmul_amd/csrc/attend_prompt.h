@@ -37,7 +37,6 @@ namespace {
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 
 constexpr int kImageKeys = 64;
-constexpr float kSlack = 8.0f;                  // log2 of how far scores may pass the maximum
 
 template <int DT>
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {

@@ -124,6 +124,9 @@ __device__ __forceinline__ uint32_t vector_bits(uint32_t x) {
     return x;
 }
 
+// Keeps a rare branch a branch: what follows is not done beforehand.
+__device__ __forceinline__ void out_of_line() { asm volatile(""); }
+
 // Nibble I of both halves of w as a pair of 16 + c.
 template <int DT, int I>
 __device__ __forceinline__ uint32_t sixteen_plus(uint32_t w, uint32_t mask, uint32_t sixteen) {
@@ -142,10 +145,14 @@ struct TileShape {
     static constexpr int R = PER * NT;
 };
 
+// Waves of a SIMD: what o and q leave of the registers. Measured (64 x 8192 to
+// 32768 keys, D 128): 2 waves 310 us, 3 waves 284 us.
+constexpr int tile_residents(int D, int NT, int waves) { return D * NT > 256 ? 1 : (NT == 1 && D <= 128 && waves == 4 ? 3 : 2); }
+
 // GQ: a quant group's words over 4 (AFFINE 32/64/128: 1/2/4; MXFP4: 1; NVFP4: unused)
 // PS: values stay codes, see the top (AFFINE, at most two groups).
 template <int DT, int MODE, int D, int GQ, int NT, bool PS, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES, D * NT > 256 ? 1 : 2) attend_tile_kernel(TileArgs t) {
+__global__ void __launch_bounds__(64 * WAVES, tile_residents(D, NT, WAVES)) attend_tile_kernel(TileArgs t) {
     using S = TileShape<DT, MODE, D, GQ, NT, PS>;
     constexpr int HW = D / 8;                              // words of a head's row
     constexpr int NM = D / 32;                             // MFMAs along D for 16 keys
@@ -160,8 +167,8 @@ __global__ void __launch_bounds__(64 * WAVES, D * NT > 256 ? 1 : 2) attend_tile_
     constexpr int U = 16 * NG * ES / 4;                    // dwords of 16 keys' scales
     constexpr int NC = D / 32, NI = (ARR * 2 * U + 63) / 64;     // loads of a step: codes, scales
     constexpr int STAGE = 32 * D + NI * 256;
-    // two workgroups, or eight waves in one, fill a CU's LDS
-    constexpr int ROOM = (WAVES == 4 ? 78 : 156) * 1024 - WAVES * WSCALES * 4;
+    // LDS of a workgroup, so that as many fit a CU
+    constexpr int ROOM = (WAVES == 8 ? 156 : (tile_residents(D, NT, WAVES) == 3 ? 52 : 78)) * 1024 - WAVES * WSCALES * 4;
     constexpr int ST = WAVES * 4 * STAGE <= ROOM ? 4 : (WAVES * 3 * STAGE <= ROOM ? 3 : 2);
     constexpr int ROW = D + 4;                             // floats of a row of o in LDS, rows on other banks
     constexpr int REGIONS = WAVES * R * ROW * 4 <= 72 * 1024 ? WAVES : (4 * R * ROW * 4 <= 72 * 1024 ? 4 : 1);
@@ -240,10 +247,11 @@ __global__ void __launch_bounds__(64 * WAVES, D * NT > 256 ? 1 : 2) attend_tile_
     __syncthreads();
 
     f32x4 o[NT][VC * 8], ones[NT];
-    float m[NT], l[NT], zsum[NT];
+    float m[NT], l[NT], zsum[NT], base[NT];                // base: m, or 0 while there is none
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         m[n] = kNone;
+        base[n] = 0.0f;
         l[n] = zsum[n] = 0.0f;
         ones[n] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -316,11 +324,13 @@ __global__ void __launch_bounds__(64 * WAVES, D * NT > 256 ? 1 : 2) attend_tile_
 #pragma unroll
             for (int i = 0; i < ST - 1; ++i) fetch(min(wave + i * WAVES, n_steps - 1), i);
         }
-        int stage = 0;
-        for (int step = wave; step < n_steps; step += WAVES, stage = stage + 1 == ST ? 0 : stage + 1) {
+        auto run = [&](int step, auto stage_c) {
+            constexpr int stage = decltype(stage_c)::value;
             const int key0 = k0 + (first + step) * kStep;
             const int32_t rb[2] = {__builtin_amdgcn_readfirstlane(blocks[step * 2]), __builtin_amdgcn_readfirstlane(blocks[step * 2 + 1])};
-            fetch(min(step + (ST - 1) * WAVES, n_steps - 1), stage == 0 ? ST - 1 : stage - 1);
+            fetch(min(step + (ST - 1) * WAVES, n_steps - 1), (stage + ST - 1) % ST);
+            // every row sees all the step's keys, and they are there
+            const bool whole = key0 >= all_lo && key0 + kStep <= all_hi && (rb[0] | rb[1]) >= 0;
             wait_loads<(ST - 1) * (NC + NI)>();              // this step's have landed
             const uint8_t* const in = mine + stage * STAGE;
             // the scales as numbers where the lanes find those of their keys; the keys' take the softmax's scale along,
@@ -328,7 +338,6 @@ __global__ void __launch_bounds__(64 * WAVES, D * NT > 256 ? 1 : 2) attend_tile_
 #pragma unroll
             for (int e = 0; e < SE; ++e) {
                 const int at = lane + 64 * e, key = min(at / NG, kStep - 1), g = at % NG, st = key / kKvUnit;
-                const bool live = (st ? rb[1] : rb[0]) >= 0 && key0 + key < k1;
                 const uint8_t* const raw = in + 32 * D + st * (ARR * U * 4) + (key % kKvUnit * NG + g) * ES;
                 float x[ARR];
 #pragma unroll
@@ -336,9 +345,15 @@ __global__ void __launch_bounds__(64 * WAVES, D * NT > 256 ? 1 : 2) attend_tile_
                 if (MODE != NVFP4) x[0] *= scale;
                 if (AFF) x[ARR - 2] = __builtin_fmaf(x[0], -16.0f, x[ARR - 2] * scale);
                 if (PS) x[ARR - 1] = __builtin_fmaf(x[1], 8.0f, x[ARR - 1]);
+                if (!whole) {                                // what is not there is no number
+                    out_of_line();
+                    const bool live = (st ? rb[1] : rb[0]) >= 0 && key0 + key < k1;
+#pragma unroll
+                    for (int s = 0; s < ARR; ++s) x[s] = live ? x[s] : 0.0f;
+                }
                 if (kStep * NG % 64 == 0 || at < kStep * NG)
 #pragma unroll
-                    for (int s = 0; s < ARR; ++s) sl[(s * NG + g) * kScaleRow + key] = live ? x[s] : 0.0f;
+                    for (int s = 0; s < ARR; ++s) sl[(s * NG + g) * kScaleRow + key] = x[s];
             }
             wave_fence();
             uint32_t vw[8][VC];
@@ -398,22 +413,23 @@ __global__ void __launch_bounds__(64 * WAVES, D * NT > 256 ? 1 : 2) attend_tile_
                             for (int i = 0; i < GQ; ++i) acc = mfma16<DT>(k[i], q[n][g * GQ + i], acc);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                float x = g ? sc[n][st][i] : 0.0f;
-                                if constexpr (AFF) x = g ? __builtin_fmaf(z[i], qsum[n][g], x) : z[i] * qsum[n][g];
-                                sc[n][st][i] = (AFF || g) ? __builtin_fmaf(s[i], acc[i], x) : s[i] * acc[i];
+                                float x = g ? sc[n][st][i] : -base[n];
+                                if constexpr (AFF) x = __builtin_fmaf(z[i], qsum[n][g], x);
+                                sc[n][st][i] = __builtin_fmaf(s[i], acc[i], x);
                             }
                         }
                     }
                 }
             }
-            const bool whole = key0 >= all_lo && key0 + kStep <= all_hi && (rb[0] | rb[1]) >= 0;
             u32x4 p[NT];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float x[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = MODE == NVFP4 ? sc[n][e / 4][e % 4] * scale : sc[n][e / 4][e % 4];
+                for (int e = 0; e < 8; ++e)
+                    x[e] = MODE == NVFP4 ? __builtin_fmaf(sc[n][e / 4][e % 4], scale, -base[n]) : sc[n][e / 4][e % 4];
                 if (!whole) {
+                    out_of_line();
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int key = key0 + e / 4 * 16 + 4 * j + e % 4;
@@ -422,9 +438,15 @@ __global__ void __launch_bounds__(64 * WAVES, D * NT > 256 ? 1 : 2) attend_tile_
                 }
                 float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
                 top = across_max(top);
-                if (__any(top > m[n])) {
-                    const float to = fmaxf(top, m[n]), f = m[n] == kNone ? 0.0f : __builtin_amdgcn_exp2f(m[n] - to);
+                // the maximum follows where a score passes it by 2^8, or the first number comes
+                if (__any(top > (m[n] == kNone ? kNone : kSlack))) {
+                    out_of_line();
+                    const float to = fmaxf(top + base[n], m[n]), f = m[n] == kNone ? 0.0f : __builtin_amdgcn_exp2f(m[n] - to);
+                    const float more = to == kNone ? 0.0f : to - base[n];
                     m[n] = to;
+                    base[n] += more;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] -= more;
                     l[n] *= f;
                     if constexpr (PS) {
                         zsum[n] *= f;
@@ -433,10 +455,9 @@ __global__ void __launch_bounds__(64 * WAVES, D * NT > 256 ? 1 : 2) attend_tile_
 #pragma unroll
                     for (int i = 0; i < VC * 8; ++i) o[n][i] *= f;
                 }
-                const float base = m[n] == kNone ? 0.0f : m[n];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    x[e] = __builtin_amdgcn_exp2f(x[e] - base);
+                    x[e] = __builtin_amdgcn_exp2f(x[e]);
                     l[n] += x[e];
                 }
                 if constexpr (PS) {                          // p times the scales of the column's group; the biases' part
@@ -517,6 +538,19 @@ __global__ void __launch_bounds__(64 * WAVES, D * NT > 256 ? 1 : 2) attend_tile_
                 }
             }
             wait_reads();                                    // this stage is read before another takes its place
+        };
+        for (int step = wave; step < n_steps; step += ST * WAVES) {
+            run(step, std::integral_constant<int, 0>{});
+            if (step + WAVES >= n_steps) break;
+            run(step + WAVES, std::integral_constant<int, 1>{});
+            if constexpr (ST > 2) {
+                if (step + 2 * WAVES >= n_steps) break;
+                run(step + 2 * WAVES, std::integral_constant<int, 2>{});
+            }
+            if constexpr (ST > 3) {
+                if (step + 3 * WAVES >= n_steps) break;
+                run(step + 3 * WAVES, std::integral_constant<int, 3>{});
+            }
         }
         wait_loads<0>();                                     // the loads past the end have landed, too
     }
