@@ -1,4 +1,4 @@
 #include "csrc/attend_tile.h"
 namespace qlin { namespace {
-template __global__ void attend_tile_kernel<QLIN_BF16,AFFINE,128,2,1,true,4>(TileArgs);
+template __global__ void attend_tile_kernel<QLIN_F16,NVFP4,64,1,3,false>(TileArgs);
 } }

@@ -66,35 +66,41 @@ __device__ __forceinline__ void store4(void* p, int64_t i, f32x4 v) {
 }
 
 // Joins the chunks of each row, out = sum f o / sum f l with f = exp2(m - largest
-// m), in the order of the chunks: a wave a row, D / 4 lanes a chunk, the others
-// the next chunks. unit: as the chunks were cut.
-template <int DT, int D>
+// m): WAVES waves a row, D / 4 lanes a chunk, the others the next chunks; sums
+// in one fixed order. unit: as the chunks were cut.
+template <int DT, int D, int WAVES>
 __global__ void __launch_bounds__(256) attend_join_kernel(TileArgs t, int tile_rows, int unit) {
-    constexpr int L4 = D / 4, AT_ONCE = 64 / L4;
+    constexpr int L4 = D / 4, AT_ONCE = 64 / L4, ROWS = 4 / WAVES, STRIDE = AT_ONCE * WAVES;
+    __shared__ f32x4 part_x[WAVES][WAVES > 1 ? L4 : 1];
+    __shared__ float part_l[WAVES];
     const AttendArgs& a = t.a;
     const KvPool& c = t.c;
-    const int groups = tile_rows / 4;
-    const int row = (int)(blockIdx.x % groups) * 4 + threadIdx.x / 64, h = blockIdx.y;
+    const int groups = tile_rows / ROWS, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    const int row = (int)(blockIdx.x % groups) * ROWS + wave / WAVES, h = blockIdx.y;
     const int64_t tile = blockIdx.x / groups;
-    const TileWork w = tile_work(a, c, tile, tile_rows, t.chunk, unit);
-    if (row >= w.rows || w.splits <= 1) return;
-    const int lane = threadIdx.x % 64;
     const int64_t part = ((tile * c.heads + h) * t.splits) * tile_rows + row;
-    const float* ml = t.part_ml + part * 2;
-    const int64_t step = (int64_t)tile_rows * 2;
-    float top = kNone;
-    for (int i = lane; i < w.splits; i += 64) top = fmaxf(top, ml[i * step]);
+    const float2* const ml = (const float2*)t.part_ml + part;
+    // the first chunks' numbers, before the lengths say how many there are
+    const float2 early = ml[(int64_t)min(lane, t.splits - 1) * tile_rows];
+    TileWork w = tile_of(a, c, tile, tile_rows);
+    if (row >= w.rows) return;
+    tile_keys(a, c, w, t.chunk, unit);
+    if (w.splits <= 1) return;
+    float top = lane < w.splits ? early.x : kNone;
+    for (int i = lane + 64; i < w.splits; i += 64) top = fmaxf(top, ml[(int64_t)i * tile_rows].x);
 #pragma unroll
     for (int off = 32; off; off /= 2) top = fmaxf(top, __shfl_xor(top, off, 64));
-    const int mine = lane / L4, d = lane % L4 * 4;
+    const int mine = wave % WAVES * AT_ONCE + lane / L4, d = lane % L4 * 4;
     f32x4 x{0, 0, 0, 0};
     float l = 0.0f;
-    if (mine < AT_ONCE) {
+    if (lane / L4 < AT_ONCE) {
+        const float* const o = t.part_o + part * D + d;
 #pragma unroll 4
-        for (int i = mine; i < w.splits; i += AT_ONCE) {
-            const float m = ml[i * step], f = m == kNone ? 0.0f : __builtin_amdgcn_exp2f(m - top);
-            l = __builtin_fmaf(f, ml[i * step + 1], l);
-            x += f * *(const f32x4*)(t.part_o + (part + (int64_t)i * tile_rows) * D + d);
+        for (int i = mine; i < w.splits; i += STRIDE) {
+            const float2 e = ml[(int64_t)i * tile_rows];
+            const float f = e.x == kNone ? 0.0f : __builtin_amdgcn_exp2f(e.x - top);
+            l = __builtin_fmaf(f, e.y, l);
+            x += f * *(const f32x4*)(o + (int64_t)i * tile_rows * D);
         }
     }
 #pragma unroll
@@ -103,15 +109,31 @@ __global__ void __launch_bounds__(256) attend_join_kernel(TileArgs t, int tile_r
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] += __shfl(x[e], lane + i * L4, 64);
     }
+    if constexpr (WAVES > 1) {
+        if (lane < L4) part_x[wave][lane] = x;
+        if (lane == 0) part_l[wave] = l;
+        __syncthreads();
+        if (wave) return;
+#pragma unroll
+        for (int i = 1; i < WAVES; ++i) {
+            if (lane < L4) x += part_x[i][lane];
+            l += part_l[i];
+        }
+    }
     if (lane >= L4) return;
     x *= l == 0.0f ? 0.0f : 1.0f / l;
     const int share = a.q_heads / c.heads, rr = w.row0 + row;
     store4<DT>(a.out, ((w.s.first + rr / share) * a.q_heads + h * share + rr % share) * D + d, x);
 }
 
+// A wave a row, or four where few rows have many chunks (65 chunks of 32 rows, D
+// 128: 6.7 and 3.8 us; 10 chunks of 2048 rows: 7.8 and 11.1 us).
 template <int DT, int D>
 hipError_t launch_join(const TileArgs& t, int64_t tiles, int tile_rows, int unit, hipStream_t st) {
-    attend_join_kernel<DT, D><<<dim3((unsigned)(tiles * (tile_rows / 4)), (unsigned)t.c.heads), 256, 0, st>>>(t, tile_rows, unit);
+    if (t.splits > 8 && tiles * tile_rows * t.c.heads <= 2048)
+        attend_join_kernel<DT, D, 4><<<dim3((unsigned)(tiles * tile_rows), (unsigned)t.c.heads), 256, 0, st>>>(t, tile_rows, unit);
+    else
+        attend_join_kernel<DT, D, 1><<<dim3((unsigned)(tiles * (tile_rows / 4)), (unsigned)t.c.heads), 256, 0, st>>>(t, tile_rows, unit);
     return hipGetLastError();
 }
 

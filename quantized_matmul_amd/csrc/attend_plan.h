@@ -14,7 +14,6 @@ struct AttendPlan {
     int rows;                        // of a tile
     int nt;                          // path 1: runs of 16 columns of a tile
     int codes;                       // path 1: values multiplied as codes (a column for each quant group of a row)
-    int waves;                       // path 1: of a workgroup
     int64_t tiles;                   // row tiles of all sequences, at most
     int chunk, splits;               // keys a workgroup takes, workgroups along the keys
     int key_blocks;                  // path 2: blocks of 64 keys of a sequence, at most
@@ -25,7 +24,7 @@ struct AttendPlan {
 
 inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t width, const KvPool& c, int64_t window,
                               bool one_row) {
-    constexpr int64_t kStepKeys = 32;        // keys of a wave's step
+    constexpr int64_t kStepKeys = 128;       // keys that the four waves of a workgroup take at a time
     constexpr int64_t kChunkMost = 4096;     // keys a workgroup takes, where that makes no more than kMany of them
     constexpr int64_t kWorkgroups = 2048;    // enough of them to fill the chip evenly
     constexpr int64_t kMany = 32768;
@@ -68,22 +67,19 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
     p.codes = groups == 1 || (groups == 2 && mean <= 8);
     const int dup = p.codes ? groups : 1;
     p.nt = mean > 16 ? 2 : 1;
+    if (c.D == 64 && mean > 32) p.nt = 3;                    // (larger heads' rows do not fit the registers)
     p.rows = 16 * p.nt / dup;
     p.tiles = one_row ? B * ((share + p.rows - 1) / p.rows) : T * share / p.rows + B;
     const int64_t base = p.tiles * c.heads;
-    p.waves = 4;
-    if (base <= 256 && p.nt == 1 && c.D <= 128) p.waves = 8;
-    const int64_t unit = p.waves * kStepKeys;
-    int64_t splits = (kWorkgroups * 4 / p.waves + base - 1) / base;
-    if (p.waves > 4 && keys <= 2048) splits = 1;             // no second launch
-    int64_t chunk = ((keys + splits - 1) / splits + unit - 1) / unit * unit;
-    if (chunk > kChunkMost && !(splits == 1 && keys <= 2048)) chunk = kChunkMost;
+    int64_t splits = (kWorkgroups + base - 1) / base;
+    int64_t chunk = ((keys + splits - 1) / splits + kStepKeys - 1) / kStepKeys * kStepKeys;
+    if (chunk > kChunkMost) chunk = kChunkMost;
     while (chunk < keys && base * (keys / chunk) > kMany) chunk *= 2;
     if (chunk >= keys) chunk = 1 << 30;
     p.chunk = (int)(chunk < (1 << 30) ? chunk : 1 << 30);
     p.splits = (int)((keys + kKvUnit + p.chunk - 1) / p.chunk);
     if (p.splits > 1) p.bytes = (size_t)(base * p.splits * p.rows) * (c.D + 2) * sizeof(float);
-    p.fits = base * p.splits <= kItems / (64 * p.waves);
+    p.fits = base * p.splits <= kItems / 256;
     return p;
 }
 

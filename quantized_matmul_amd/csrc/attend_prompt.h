@@ -77,7 +77,8 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
     const int tid = threadIdx.x;
     if (tid < kImageKeys / kKvUnit)
         blocks[tid] = key0 + tid * kKvUnit < s.keys
-                          ? kv_row_block(a.table + (int64_t)b * a.width, c.pages, c.heads, c.page, h, key0 / kKvUnit + tid)
+                          ? kv_row_block(a.table[(int64_t)b * a.width + (key0 + tid * kKvUnit) / c.page], c.pages, c.heads,
+                                         c.page, h, key0 / kKvUnit + tid)
                           : -1;
     __syncthreads();
     const int per = c.g / 8, groups = D / c.g;
@@ -155,8 +156,10 @@ __global__ void __launch_bounds__(256, 2) attend_prompt_kernel(TileArgs t, int64
     // heads over the XCDs, so that each L2 keeps its head's keys; the last tiles, which see most, first
     const int h = blockIdx.x % c.heads, split = blockIdx.x / c.heads % t.splits;
     const int64_t tile = tiles - 1 - blockIdx.x / c.heads / t.splits;
-    const TileWork w = tile_work(a, c, tile, R, t.chunk, kImageKeys);
-    if (!w.rows || (split && split >= w.splits)) return;
+    TileWork w = tile_of(a, c, tile, R);
+    if (!w.rows) return;
+    tile_keys(a, c, w, t.chunk, kImageKeys);
+    if (split && split >= w.splits) return;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, r = lane % 32, hb = lane / 32;
     const int share = a.q_heads / c.heads;
     const int k0 = w.k0 + split * t.chunk, k1 = w.splits ? min(w.hi, k0 + t.chunk) : k0;

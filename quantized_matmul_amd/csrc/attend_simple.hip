@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(256) attend_simple_kernel(AttendArgs a, KvPool
     for (int k0 = seen.lo; k0 < seen.hi; k0 += 64 / LANES) {
         const int key = k0 + lane / LANES;
         int32_t rb = -1;
-        if (key < seen.hi) rb = kv_row_block(table, c.pages, c.heads, c.page, h, key / kKvUnit);
+        if (key < seen.hi) rb = kv_row_block(table[key / c.page], c.pages, c.heads, c.page, h, key / kKvUnit);
         float v[2][8];
 #pragma unroll
         for (int side = 0; side < 2; ++side) {

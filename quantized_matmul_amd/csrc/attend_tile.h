@@ -33,6 +33,7 @@
 namespace qlin {
 namespace {
 
+constexpr int WAVES = 4;                        // of a workgroup
 constexpr int kStep = 32;                       // keys of a wave's step
 constexpr int kWindow = 4096;                   // keys whose pages are looked up at once
 constexpr int kScaleRow = kStep + 4;            // floats of a group's scales of a step in LDS: rows on other banks
@@ -147,17 +148,21 @@ struct TileShape {
 
 // Waves of a SIMD: what o and q leave of the registers. Measured (64 x 8192 to
 // 32768 keys, D 128): 2 waves 310 us, 3 waves 284 us.
-constexpr int tile_residents(int D, int NT, int waves) { return D * NT > 256 ? 1 : (NT == 1 && D <= 128 && waves == 4 ? 3 : 2); }
+constexpr int tile_residents(int D, int NT) {
+    return NT == 1 && D <= 128 ? 3 : (D * NT <= 256 ? 2 : 1);
+}
 
 // GQ: a quant group's words over 4 (AFFINE 32/64/128: 1/2/4; MXFP4: 1; NVFP4: unused)
 // PS: values stay codes, see the top (AFFINE, at most two groups).
-template <int DT, int MODE, int D, int GQ, int NT, bool PS, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES, tile_residents(D, NT, WAVES)) attend_tile_kernel(TileArgs t) {
+template <int DT, int MODE, int D, int GQ, int NT, bool PS>
+__global__ void __launch_bounds__(256, tile_residents(D, NT)) attend_tile_kernel(TileArgs t) {
     using S = TileShape<DT, MODE, D, GQ, NT, PS>;
     constexpr int HW = D / 8;                              // words of a head's row
     constexpr int NM = D / 32;                             // MFMAs along D for 16 keys
     constexpr int G = S::G, NG = S::NG, R = S::R, PER = S::PER;
+    constexpr bool HALF = HW == 8;                         // 8 words for 16 lanes: each takes half of one
     constexpr int VC = (HW + 15) / 16;                     // words of a value a lane takes
+    constexpr int CL = HALF ? 4 : 8, OT = VC * CL;         // codes of a word it takes; tiles of o
     constexpr bool AFF = MODE == AFFINE;
     static_assert(!PS || (AFF && NG <= 2 && DT == QLIN_BF16), "values as codes");
     constexpr int ARR = AFF ? 4 : 2;                       // scale arrays of a step: keys', values', biases in the same order
@@ -168,7 +173,7 @@ __global__ void __launch_bounds__(64 * WAVES, tile_residents(D, NT, WAVES)) atte
     constexpr int NC = D / 32, NI = (ARR * 2 * U + 63) / 64;     // loads of a step: codes, scales
     constexpr int STAGE = 32 * D + NI * 256;
     // LDS of a workgroup, so that as many fit a CU
-    constexpr int ROOM = (WAVES == 8 ? 156 : (tile_residents(D, NT, WAVES) == 3 ? 52 : 78)) * 1024 - WAVES * WSCALES * 4;
+    constexpr int ROOM = (tile_residents(D, NT) == 3 ? 52 : 78) * 1024 - WAVES * WSCALES * 4;
     constexpr int ST = WAVES * 4 * STAGE <= ROOM ? 4 : (WAVES * 3 * STAGE <= ROOM ? 3 : 2);
     constexpr int ROW = D + 4;                             // floats of a row of o in LDS, rows on other banks
     constexpr int REGIONS = WAVES * R * ROW * 4 <= 72 * 1024 ? WAVES : (4 * R * ROW * 4 <= 72 * 1024 ? 4 : 1);
@@ -182,10 +187,38 @@ __global__ void __launch_bounds__(64 * WAVES, tile_residents(D, NT, WAVES)) atte
     const KvPool& c = t.c;
     const int h = blockIdx.y, split = t.splits == 1 ? 0 : blockIdx.x % t.splits;
     const int64_t tile = t.splits == 1 ? blockIdx.x : blockIdx.x / t.splits;
-    const TileWork w = tile_work(a, c, tile, R, t.chunk, kKvUnit);
-    if (!w.rows || (split && split >= w.splits)) return;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, r = lane % 16, j = lane / 16;
     const int share = a.q_heads / c.heads;
+    TileWork w = tile_of(a, c, tile, R);
+    if (!w.rows) return;
+    // Ahead of the lengths, which say whether they count: the page of the thread's first row block, known without a
+    // window; and the rows of q.
+    int32_t guess = -1;
+    if (!a.window && a.width) {
+        const uint32_t page = ((uint32_t)split * (uint32_t)t.chunk + tid * kKvUnit) / (uint32_t)c.page;
+        guess = a.table[(int64_t)w.b * a.width + min(page, (uint32_t)a.width - 1)];
+    }
+    u32x4 q[NT][NM];
+    int at_row[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int rr = min(w.row0 + n * PER + r % PER, w.row0 + w.rows - 1);     // rows past the end repeat the last
+        at_row[n] = rr / share;
+        const uint16_t* qp = (const uint16_t*)a.q + (w.s.first + at_row[n]) * a.q_stride + (int64_t)(h * share + rr % share) * D;
+        const bool aligned = (((uintptr_t)a.q | (uintptr_t)(a.q_stride * 2)) & 15) == 0;
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+            const int word = MODE == NVFP4 ? m * 4 + j : m / GQ * (4 * GQ) + j * GQ + m % GQ;
+            if (aligned) {
+                q[n][m] = *(const u32x4*)(qp + word * 8);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[n][m][i] = qp[word * 8 + 2 * i] | ((uint32_t)qp[word * 8 + 2 * i + 1] << 16);
+            }
+        }
+    }
+    tile_keys(a, c, w, t.chunk, kKvUnit);
+    if (split && split >= w.splits) return;
     const int k0 = w.k0 + split * t.chunk, k1 = w.splits ? min(w.hi, k0 + t.chunk) : k0;
     const int steps = (k1 - k0 + kStep - 1) / kStep;
     const int32_t* const table = a.table + (int64_t)w.b * a.width;
@@ -193,60 +226,19 @@ __global__ void __launch_bounds__(64 * WAVES, tile_residents(D, NT, WAVES)) atte
         const int n = min(steps * (kStep / kKvUnit) - first, kWindow / kKvUnit);
         for (int i = tid; i < n; i += 64 * WAVES) {
             const int key = k0 + (first + i) * kKvUnit;
-            blocks[i] = key < k1 ? kv_row_block(table, c.pages, c.heads, c.page, h, key / kKvUnit) : -1;
+            int32_t p = guess;
+            if (a.window || first || i != tid) p = key < k1 ? table[key / c.page] : -1;
+            blocks[i] = key < k1 ? kv_row_block(p, c.pages, c.heads, c.page, h, key / kKvUnit) : -1;
         }
     };
     look_up(0);
-
-    // rows of q: their place, the keys they see, their operand
-    Seen seen[NT];
-    u32x4 q[NT][NM];
-    float qsum[NT][AFF ? NG : 1];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int rr = min(w.row0 + n * PER + r % PER, w.row0 + w.rows - 1);     // rows past the end repeat the last
-        seen[n] = seen_by(a, w.s, rr / share);
-        const uint16_t* qp = (const uint16_t*)a.q + (w.s.first + rr / share) * a.q_stride + (int64_t)(h * share + rr % share) * D;
-        const bool aligned = ((uintptr_t)qp & 15) == 0;
-#pragma unroll
-        for (int m = 0; m < NM; ++m) {
-            const int word = MODE == NVFP4 ? m * 4 + j : m / GQ * (4 * GQ) + j * GQ + m % GQ;
-            u32x4 v;
-            if (aligned) {
-                v = *(const u32x4*)(qp + word * 8);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = qp[word * 8 + 2 * i] | ((uint32_t)qp[word * 8 + 2 * i + 1] << 16);
-            }
-            if constexpr (AFF) {                           // values 0..7 to the order of the codes: 0 4 1 5 2 6 3 7
-                q[n][m] = u32x4{(v[0] & 0xFFFFu) | (v[2] << 16), (v[0] >> 16) | (v[2] & 0xFFFF0000u),
-                                (v[1] & 0xFFFFu) | (v[3] << 16), (v[1] >> 16) | (v[3] & 0xFFFF0000u)};
-            } else {
-                q[n][m] = v;
-            }
-        }
-        if constexpr (AFF) {
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                float sum = 0.0f;
-#pragma unroll
-                for (int m = 0; m < GQ; ++m)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t d = q[n][g * GQ + m][i];
-                        sum += DT == QLIN_BF16 ? __uint_as_float(d << 16) : f16_bits_to_f32(d & 0xFFFFu);
-                        sum += DT == QLIN_BF16 ? __uint_as_float(d & 0xFFFF0000u) : f16_bits_to_f32(d >> 16);
-                    }
-                sum = across_sum(sum);
-                qsum[n][g] = sum;
-            }
-        }
-    }
     // keys that every row of the tile sees
     const int all_lo = seen_by(a, w.s, (w.row0 + w.rows - 1) / share).lo, all_hi = seen_by(a, w.s, w.row0 / share).hi;
-    __syncthreads();
+    Seen seen[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) seen[n] = seen_by(a, w.s, at_row[n]);
 
-    f32x4 o[NT][VC * 8], ones[NT];
+    f32x4 o[NT][OT], ones[NT];
     float m[NT], l[NT], zsum[NT], base[NT];                // base: m, or 0 while there is none
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -255,7 +247,7 @@ __global__ void __launch_bounds__(64 * WAVES, tile_residents(D, NT, WAVES)) atte
         l[n] = zsum[n] = 0.0f;
         ones[n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < VC * 8; ++i) o[n][i] = f32x4{0, 0, 0, 0};
+        for (int i = 0; i < OT; ++i) o[n][i] = f32x4{0, 0, 0, 0};
     }
     const float scale = a.scale * kLog2e;
     float* const sl = numbers + wave * WSCALES;                          // this wave's scales: [array, group, key]
@@ -312,17 +304,49 @@ __global__ void __launch_bounds__(64 * WAVES, tile_residents(D, NT, WAVES)) atte
             to_lds4(to + 32 * D + i * 256, scale_from[i] + (int64_t)(scale_second[i] ? b[1] : b[0]) * (U * 4));
     };
 
+    // ST - 1 steps of a window on their way; past its end the last one again, so that the counts of loads stay the same
+    auto begin = [&](int n_steps) {
+        if (wave < n_steps) {
+#pragma unroll
+            for (int i = 0; i < ST - 1; ++i) fetch(min(wave + i * WAVES, n_steps - 1), i);
+        }
+    };
+#pragma unroll
+    for (int n = 0; n < NT; ++n)                             // q has come: no later wait for it is one for those loads
+#pragma unroll
+        for (int m = 0; m < NM; ++m) asm volatile("" : "+v"(q[n][m]));
+    __syncthreads();
+    begin(min(steps, kWindow / kStep));
+
+    float qsum[NT][AFF ? NG : 1];
+    if constexpr (AFF) {                                     // q's values 0..7 to the order of the codes: 0 4 1 5 2 6 3 7; sums
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int m = 0; m < GQ; ++m) {
+                    const u32x4 v = q[n][g * GQ + m];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        sum += DT == QLIN_BF16 ? __uint_as_float(v[i] << 16) : f16_bits_to_f32(v[i] & 0xFFFFu);
+                        sum += DT == QLIN_BF16 ? __uint_as_float(v[i] & 0xFFFF0000u) : f16_bits_to_f32(v[i] >> 16);
+                    }
+                    q[n][g * GQ + m] = u32x4{(v[0] & 0xFFFFu) | (v[2] << 16), (v[0] >> 16) | (v[2] & 0xFFFF0000u),
+                                             (v[1] & 0xFFFFu) | (v[3] << 16), (v[1] >> 16) | (v[3] & 0xFFFF0000u)};
+                }
+                qsum[n][g] = across_sum(sum);
+            }
+    }
+
     for (int first = 0; first < steps; first += kWindow / kStep) {
+        const int n_steps = min(steps - first, kWindow / kStep);
         if (first) {                                         // another window: its row blocks take the place of the last ones
             __syncthreads();
             look_up(first * (kStep / kKvUnit));
             __syncthreads();
-        }
-        const int n_steps = min(steps - first, kWindow / kStep);
-        // ST - 1 steps on their way; past the end the last one again, so that the counts of loads stay the same
-        if (wave < n_steps) {
-#pragma unroll
-            for (int i = 0; i < ST - 1; ++i) fetch(min(wave + i * WAVES, n_steps - 1), i);
+            begin(n_steps);
         }
         auto run = [&](int step, auto stage_c) {
             constexpr int stage = decltype(stage_c)::value;
@@ -361,7 +385,7 @@ __global__ void __launch_bounds__(64 * WAVES, tile_residents(D, NT, WAVES)) atte
             for (int e = 0; e < 8; ++e)
 #pragma unroll
                 for (int v = 0; v < VC; ++v) {
-                    const int word = v * 16 + r;
+                    const int word = HALF ? r / 2 : v * 16 + r;
                     vw[e][v] = *(const uint32_t*)(in + word_at(e / 4, 1, 4 * j + e % 4, word < HW ? word : word - VROW));
                 }
             f32x4 sc[NT][2];
@@ -453,7 +477,7 @@ __global__ void __launch_bounds__(64 * WAVES, tile_residents(D, NT, WAVES)) atte
                         ones[n] *= f;
                     }
 #pragma unroll
-                    for (int i = 0; i < VC * 8; ++i) o[n][i] *= f;
+                    for (int i = 0; i < OT; ++i) o[n][i] *= f;
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -490,17 +514,21 @@ __global__ void __launch_bounds__(64 * WAVES, tile_residents(D, NT, WAVES)) atte
                             const u32x4 vt{sixteen_plus<DT, I>(x[0], mask, sixteen), sixteen_plus<DT, I>(x[1], mask, sixteen),
                                            sixteen_plus<DT, I>(x[2], mask, sixteen), sixteen_plus<DT, I>(x[3], mask, sixteen)};
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) o[n][v * 8 + to + I] = mfma16<DT>(vt, p[n], o[n][v * 8 + to + I]);
+                            for (int n = 0; n < NT; ++n) o[n][v * CL + to + I] = mfma16<DT>(vt, p[n], o[n][v * CL + to + I]);
                         };
                         one(std::integral_constant<int, 0>{});
                         one(std::integral_constant<int, 1>{});
                         one(std::integral_constant<int, 2>{});
                         one(std::integral_constant<int, 3>{});
                     };
-                    four(0x05040100u, 0);
-                    four(0x07060302u, 4);
+                    if constexpr (HALF) {
+                        four(r & 1 ? 0x07060302u : 0x05040100u, 0);
+                    } else {
+                        four(0x05040100u, 0);
+                        four(0x07060302u, 4);
+                    }
                 } else {
-                    const int word = v * 16 + r, g = (word < HW ? word : word - VROW) / (G / 8);
+                    const int word = HALF ? r / 2 : v * 16 + r, g = (word < HW ? word : word - VROW) / (G / 8);
                     const f32x4 s0 = *(const f32x4*)(sl + (NG + g) * kScaleRow + 4 * j);
                     const f32x4 s1 = *(const f32x4*)(sl + (NG + g) * kScaleRow + 16 + 4 * j);
                     if constexpr (AFF) {
@@ -509,11 +537,12 @@ __global__ void __launch_bounds__(64 * WAVES, tile_residents(D, NT, WAVES)) atte
                         uint32_t code[8][2];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            code[e][0] = vector_bits(vw[e][v] & 0x0F0F0F0Fu);
-                            code[e][1] = vector_bits((vw[e][v] >> 4) & 0x0F0F0F0Fu);
+                            const uint32_t w4 = HALF ? vw[e][v] >> (16 * (r & 1)) : vw[e][v];
+                            code[e][0] = vector_bits(w4 & 0x0F0F0F0Fu);
+                            code[e][1] = vector_bits((w4 >> 4) & 0x0F0F0F0Fu);
                         }
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < CL; ++i) {
                             float x[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
@@ -521,18 +550,20 @@ __global__ void __launch_bounds__(64 * WAVES, tile_residents(D, NT, WAVES)) atte
                                                       e < 4 ? z0[e & 3] : z1[e & 3]);
                             const u32x4 vt{round2<DT>(x[0], x[1]), round2<DT>(x[2], x[3]), round2<DT>(x[4], x[5]), round2<DT>(x[6], x[7])};
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) o[n][v * 8 + i] = mfma16<DT>(vt, p[n], o[n][v * 8 + i]);
+                            for (int n = 0; n < NT; ++n) o[n][v * CL + i] = mfma16<DT>(vt, p[n], o[n][v * CL + i]);
                         }
                     } else {
                         float x[8][8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) e2m1_values<MODE == MXFP4>(vw[e][v], e < 4 ? s0[e & 3] : s1[e & 3], x[e]);
+                        for (int e = 0; e < 8; ++e)
+                            e2m1_values<MODE == MXFP4>(HALF ? vw[e][v] >> (16 * (r & 1)) : vw[e][v], e < 4 ? s0[e & 3] : s1[e & 3],
+                                                       x[e]);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < CL; ++i) {
                             const u32x4 vt{round2<DT>(x[0][i], x[1][i]), round2<DT>(x[2][i], x[3][i]),
                                            round2<DT>(x[4][i], x[5][i]), round2<DT>(x[6][i], x[7][i])};
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) o[n][v * 8 + i] = mfma16<DT>(vt, p[n], o[n][v * 8 + i]);
+                            for (int n = 0; n < NT; ++n) o[n][v * CL + i] = mfma16<DT>(vt, p[n], o[n][v * CL + i]);
                         }
                     }
                 }
@@ -566,16 +597,19 @@ __global__ void __launch_bounds__(64 * WAVES, tile_residents(D, NT, WAVES)) atte
             wave_ml[wave][n * PER + r][1] = l[n];
         }
     }
-    __syncthreads();
+    __syncthreads();                                         // (the ring is read)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        float top = kNone;
+        float f = 1.0f;                                      // waves with a region of their own are weighted below
+        if constexpr (REGIONS < WAVES) {
+            float top = kNone;
 #pragma unroll
-        for (int i = 0; i < WAVES; ++i) top = fmaxf(top, wave_ml[i][n * PER + r % PER][0]);
-        const float f = m[n] == kNone ? 0.0f : __builtin_amdgcn_exp2f(m[n] - top);
+            for (int i = 0; i < WAVES; ++i) top = fmaxf(top, wave_ml[i][n * PER + r % PER][0]);
+            f = m[n] == kNone ? 0.0f : __builtin_amdgcn_exp2f(m[n] - top);
+        }
         const float plus = PS ? zsum[n] - 24.0f * ones[n][0] : 0.0f;      // all rows of `ones` are the column's sum
 #pragma unroll
-        for (int i = 0; i < VC * 8; ++i) o[n][i] = PS ? (o[n][i] + plus) * f : o[n][i] * f;
+        for (int i = 0; i < OT; ++i) o[n][i] = PS ? (o[n][i] + plus) * f : o[n][i] * f;
     }
     for (int turn = 0; turn < WAVES / REGIONS; ++turn) {
         if (turn == wave / REGIONS) {
@@ -586,17 +620,16 @@ __global__ void __launch_bounds__(64 * WAVES, tile_residents(D, NT, WAVES)) atte
                 for (int v = 0; v < VC; ++v)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int word = v * 16 + 4 * j + i;
-                        if (word >= HW || (PS && word / (G / 8) != r / PER)) continue;
-                        f32x4* at = (f32x4*)(buf + (wave % REGIONS * R + n * PER + r % PER) * ROW + word * 8);
-                        f32x4 x0{o[n][v * 8][i], o[n][v * 8 + 1][i], o[n][v * 8 + 2][i], o[n][v * 8 + 3][i]};
-                        f32x4 x1{o[n][v * 8 + 4][i], o[n][v * 8 + 5][i], o[n][v * 8 + 6][i], o[n][v * 8 + 7][i]};
-                        if (turn) {
-                            x0 += at[0];
-                            x1 += at[1];
+                        const int word = v * 16 + 4 * j + i;           // HALF: half-word
+                        if (word >= D / CL || (PS && word * CL / G != r / PER)) continue;
+                        f32x4* at = (f32x4*)(buf + (wave % REGIONS * R + n * PER + r % PER) * ROW + word * CL);
+#pragma unroll
+                        for (int u = 0; u < CL / 4; ++u) {
+                            f32x4 x{o[n][v * CL + 4 * u][i], o[n][v * CL + 4 * u + 1][i], o[n][v * CL + 4 * u + 2][i],
+                                    o[n][v * CL + 4 * u + 3][i]};
+                            if (turn) x += at[u];
+                            at[u] = x;
                         }
-                        at[0] = x0;
-                        at[1] = x1;
                     }
             }
         }
@@ -605,15 +638,18 @@ __global__ void __launch_bounds__(64 * WAVES, tile_residents(D, NT, WAVES)) atte
     const int64_t part = (tile * c.heads + h) * t.splits + split;
     for (int e = tid; e < w.rows * (D / 4); e += 64 * WAVES) {
         const int row = e / (D / 4), d = e % (D / 4) * 4;
-        float top = kNone, sum = 0.0f;
+        float top = kNone, sum = 0.0f, f[WAVES];
 #pragma unroll
         for (int i = 0; i < WAVES; ++i) top = fmaxf(top, wave_ml[i][row][0]);
+        f32x4 x{0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < WAVES; ++i)
-            sum += wave_ml[i][row][0] == kNone ? 0.0f : wave_ml[i][row][1] * __builtin_amdgcn_exp2f(wave_ml[i][row][0] - top);
-        f32x4 x = *(const f32x4*)(buf + row * ROW + d);
+        for (int i = 0; i < WAVES; ++i) {
+            f[i] = wave_ml[i][row][0] == kNone ? 0.0f : __builtin_amdgcn_exp2f(wave_ml[i][row][0] - top);
+            sum = __builtin_fmaf(f[i], wave_ml[i][row][1], sum);
+        }
 #pragma unroll
-        for (int i = 1; i < REGIONS; ++i) x += *(const f32x4*)(buf + (i * R + row) * ROW + d);
+        for (int i = 0; i < REGIONS; ++i)
+            x += *(const f32x4*)(buf + (i * R + row) * ROW + d) * (REGIONS == WAVES ? f[i] : 1.0f);
         if (w.splits <= 1) {
             x *= sum == 0.0f ? 0.0f : 1.0f / sum;                        // a row that sees no key: zeros
             const int rr = w.row0 + row;
@@ -642,27 +678,22 @@ hipError_t launch_tile_of(const AttendArgs& a, const KvPool& c, int dt, const At
             constexpr bool CAN = M == AFFINE && DT == QLIN_BF16 && D / (32 * GQ) <= 2;     // as the plan has it
             
             auto go = [&](auto ntc, auto psc) {
-                constexpr int NT = decltype(ntc)::value;
-                constexpr bool PS = decltype(psc)::value;
-                constexpr int MANY = 8;
-                if constexpr (NT == 1 && D <= 128)
-                    if (p.waves == MANY) {
-                        attend_tile_kernel<DT, M, D, GQ, NT, PS, MANY><<<grid, 64 * MANY, 0, st>>>(t);
-                        return;
-                    }
-                attend_tile_kernel<DT, M, D, GQ, NT, PS, 4><<<grid, 256, 0, st>>>(t);
+                attend_tile_kernel<DT, M, D, GQ, decltype(ntc)::value, decltype(psc)::value><<<grid, 256, 0, st>>>(t);
             };
-            using N1 = std::integral_constant<int, 1>;
-            using N2 = std::integral_constant<int, 2>;
-            if (p.codes != (CAN && p.codes)) return hipErrorInvalidValue;
-            if (p.nt == 1) {
-                if (CAN && p.codes) go(N1{}, std::integral_constant<bool, CAN>{});
-                else go(N1{}, std::false_type{});
-            } else {
-                if (CAN && p.codes && D == 32 * GQ) go(N2{}, std::integral_constant<bool, CAN && D == 32 * GQ>{});
-                else go(N2{}, std::false_type{});
-            }
-            hipError_t e = hipGetLastError();
+            constexpr bool ALL = CAN && D == 32 * GQ;               // a single group: codes for any number of rows
+            auto sized = [&](auto ntc) -> hipError_t {
+                constexpr int NT = decltype(ntc)::value;
+                constexpr bool PS = NT == 1 ? CAN : ALL;
+                if (p.codes && !PS) return hipErrorInvalidValue;
+                if (PS && p.codes) go(ntc, std::integral_constant<bool, PS>{});
+                else if constexpr (!ALL) go(ntc, std::false_type{});
+                return hipGetLastError();
+            };
+            hipError_t e;
+            if (p.nt == 1) e = sized(std::integral_constant<int, 1>{});
+            else if (p.nt == 2) e = sized(std::integral_constant<int, 2>{});
+            else if constexpr (D == 64) e = sized(std::integral_constant<int, 3>{});
+            else e = hipErrorInvalidValue;
             if (e != hipSuccess || p.splits == 1) return e;
             return launch_join<DT, D>(t, p.tiles, p.rows, kKvUnit, st);
         }

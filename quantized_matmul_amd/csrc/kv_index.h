@@ -30,11 +30,10 @@ constexpr int kKvUnit = 16;      // rows of a page come in runs of this many
 
 // Pages [0, pages) exist: the row block (row number over 16) of head h where
 // key block `block` (its keys over 16) of a sequence lies, or -1 where its page
-// number is none. The caller has checked that block * 16 < width * page.
-QLIN_HD int32_t kv_row_block(const int32_t* table_row, int64_t pages, int heads, int page, int h, int block) {
-    const int per = page / kKvUnit;
-    const int32_t p = table_row[block / per];
+// number p is none.
+QLIN_HD int32_t kv_row_block(int32_t p, int64_t pages, int heads, int page, int h, int block) {
     if (p < 0 || p >= pages) return -1;
+    const int per = page / kKvUnit;
     return (int32_t)(((int64_t)p * heads + h) * per + block % per);
 }
 
@@ -71,8 +70,7 @@ struct Sequence {
     int64_t first;
     int n, keys;
 };
-QLIN_HD Sequence sequence_of(const AttendArgs& a, const KvPool& c, int b) {
-    Sequence s;
+QLIN_HD void rows_of(const AttendArgs& a, int b, Sequence& s) {
     int64_t end;
     if (a.offsets) {
         s.first = a.offsets[b];
@@ -84,9 +82,16 @@ QLIN_HD Sequence sequence_of(const AttendArgs& a, const KvPool& c, int b) {
         end = b + 1;
     }
     s.n = (int)(end - s.first);
+}
+QLIN_HD int keys_of(const AttendArgs& a, const KvPool& c, int b) {
     const int64_t held = (int64_t)a.width * c.page, most = held < 0x7FFFFFF0LL ? held : 0x7FFFFFF0LL;
     const int64_t k = a.lengths[b];
-    s.keys = (int)(k < 0 ? 0 : (k > most ? most : k));
+    return (int)(k < 0 ? 0 : (k > most ? most : k));
+}
+QLIN_HD Sequence sequence_of(const AttendArgs& a, const KvPool& c, int b) {
+    Sequence s;
+    rows_of(a, b, s);
+    s.keys = keys_of(a, c, b);
     return s;
 }
 
@@ -105,38 +110,42 @@ QLIN_HD Seen seen_by(const AttendArgs& a, const Sequence& s, int i) {
     return {(int)lo, (int)hi};
 }
 
-// What a tile of rows has to read: keys [k0, hi) in `splits` chunks, k0 a multiple of `unit`.
+// A tile of rows, and what it has to read: keys [lo, hi), taken from k0 (a
+// multiple of `unit`) on in `splits` chunks.
 struct TileWork {
     Sequence s;
     int b, row0, rows, lo, hi, k0, splits;       // row0: of the sequence's n * share rows; rows: of this tile
 };
-QLIN_HD TileWork tile_work(const AttendArgs& a, const KvPool& c, int64_t tile, int tile_rows, int chunk,
-                           int unit) {
+QLIN_HD TileWork tile_of(const AttendArgs& a, const KvPool& c, int64_t tile, int tile_rows) {
     const int share = a.q_heads / c.heads;
     TileWork w;
     int64_t rt;
+    w.rows = 0;
     if (a.offsets) {
         // sequence b starts at tile floor(offsets[b] * share / tile_rows) + b: a tile more than it needs at most
         auto start = [&](int b) { return (int64_t)a.offsets[b] * share / tile_rows + b; };
         w.b = last_at_most(a.B, tile, start);
         rt = tile - start(w.b);
     } else {
-        const int per = (share + tile_rows - 1) / tile_rows;
-        w.b = (int)(tile / per);
+        const uint32_t per = (share + tile_rows - 1) / tile_rows;      // (tiles of a launch number below 2^32)
+        w.b = (int)(per == 1 ? (uint32_t)tile : (uint32_t)tile / per);
         rt = tile - (int64_t)w.b * per;
     }
-    w.rows = 0;
     if (w.b >= a.B || rt < 0) return w;
-    w.s = sequence_of(a, c, w.b);
+    rows_of(a, w.b, w.s);
     const int64_t rows = (int64_t)w.s.n * share - rt * tile_rows;
     if (rows <= 0) return w;
     w.row0 = (int)(rt * tile_rows);
     w.rows = rows < tile_rows ? (int)rows : tile_rows;
+    return w;
+}
+QLIN_HD void tile_keys(const AttendArgs& a, const KvPool& c, TileWork& w, int chunk, int unit) {
+    const int share = a.q_heads / c.heads;
+    w.s.keys = keys_of(a, c, w.b);
     w.lo = seen_by(a, w.s, w.row0 / share).lo;
     w.hi = seen_by(a, w.s, (w.row0 + w.rows - 1) / share).hi;
     w.k0 = w.lo & ~(unit - 1);
     w.splits = w.hi > w.lo ? (w.hi - w.k0 + chunk - 1) / chunk : 0;
-    return w;
 }
 
 }  // namespace qlin
