@@ -92,7 +92,7 @@ def load_library():
     lib.qlin_gather_mxfp4_matmul_workspace_bytes.restype = sz
     lib.qlin_moe_combine.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp]
     lib.qlin_moe_combine_grad.argtypes = [vp, vp, i32, i64, i64, i64, vp, vp, vp, vp, vp]
-    cache = ctypes.POINTER(_CacheStruct)
+    cache = vp
     lib.qlin_rotary.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, vp, i32, f64, vp, i64, vp]
     lib.qlin_rotary_grad.argtypes = lib.qlin_rotary.argtypes
     lib.qlin_kv_cache_write.argtypes = [cache, vp, vp, i32, i64, i64, i64, vp, vp]
@@ -655,33 +655,41 @@ def moe_combine_grad(grad_y: torch.Tensor, h: torch.Tensor, weights: torch.Tenso
     return grad_h, grad_w
 
 
-def _run(dev, f, *args):
-    """f(*args, stream) on dev's current stream, with dev as the current device."""
-    if dev.index == torch.cuda.current_device():
-        _check(f(*args, _stream(dev)))
-    else:
-        with torch.cuda.device(dev):
-            _check(f(*args, _stream(dev)))
+_current_device = torch._C._cuda_getDevice
 
 
-def _token_rows(name, t, dev, dtype, shape):
-    """Elements between the tokens of t [T, heads, D], whose heads and values are dense."""
+def _elsewhere(dev, f, args):
+    """f(*args, stream) with dev, which is not the current device, made it for the call."""
+    with torch.cuda.device(dev):
+        return f(*args, _stream(dev))
+
+
+def _token_rows(name, t, dev, dtype, heads, dim, tokens):
+    """Elements between the tokens of t [tokens, heads, dim], whose heads and values are dense (None: any size)."""
+    shape, strides = t.shape, t.stride()
+    if (t.dtype is dtype and len(shape) == 3 and t.device == dev and strides[2] == 1 and strides[1] == shape[2]
+            and (heads is None or shape[1] == heads) and (dim is None or shape[2] == dim)
+            and (tokens is None or shape[0] == tokens)):
+        return strides[0] if shape[0] > 1 else shape[1] * shape[2]
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype} (got {t.dtype})")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev} (got {t.device})")
-    if t.dim() != 3 or t.shape[1:] != shape[1:] or (shape[0] is not None and t.shape[0] != shape[0]):
-        raise ValueError(f"{name} must be [T, heads, head_dim] = {tuple(shape)} (got {tuple(t.shape)})")
-    stride, heads, values = t.stride()
-    if (values != 1 and t.shape[2] > 1) or (heads != t.shape[2] and t.shape[1] > 1):
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or (dim is not None and shape[2] != dim) \
+            or (tokens is not None and shape[0] != tokens):
+        raise ValueError(f"{name} must be [{'T' if tokens is None else tokens}, {'heads' if heads is None else heads}, "
+                         f"{'head_dim' if dim is None else dim}] (got {tuple(shape)})")
+    if (strides[2] != 1 and shape[2] > 1) or (strides[1] != shape[2] and shape[1] > 1):
         raise ValueError(f"the heads and values of {name} must be dense (only its tokens may lie apart)")
-    return stride if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return strides[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _index_rows(name, t, dev, n):
+    if t.dtype is torch.int32 and t.device == dev and t.is_contiguous() and len(t.shape) == 1 \
+            and (n is None or t.shape[0] == n):
+        return
     _check_tensor(name, t, dev, torch.int32)
-    if t.dim() != 1 or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must be one-dimensional" + ("" if n is None else f" with {n} entries"))
+    raise ValueError(f"{name} must be one-dimensional" + ("" if n is None else f" with {n} entries"))
 
 
 def rotary_frequencies(dim: int, base: float = 10000.0, factor: float = 1.0, method: str = "linear",
@@ -716,23 +724,26 @@ def rotary_frequencies(dim: int, base: float = 10000.0, factor: float = 1.0, met
 
 
 def _rotary(call, name, x, positions, freqs, interleaved, scale, out):
-    if not x.is_cuda:
-        raise ValueError("qlin tensors live in GPU memory (got a CPU tensor)")
     dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("qlin tensors live in GPU memory (got a CPU tensor)")
     code = _float_code(name, x)
-    stride = _token_rows(name, x, dev, x.dtype, x.shape)
+    stride = _token_rows(name, x, dev, x.dtype, None, None, None)
     T, heads, D = x.shape
     _index_rows("positions", positions, dev, T)
     _check_tensor("freqs", freqs, dev, torch.float32)
-    if freqs.dim() != 1:
+    if len(freqs.shape) != 1:
         raise ValueError("freqs must be one-dimensional")
     if out is None:
         out = torch.empty((T, heads, D), dtype=x.dtype, device=dev)
         out_stride = heads * D
     else:
-        out_stride = _token_rows("out", out, dev, x.dtype, x.shape)
-    _run(dev, call, x.data_ptr(), code, T, stride, heads, D, 2 * freqs.shape[0], positions.data_ptr(), freqs.data_ptr(),
-         bool(interleaved), scale, out.data_ptr(), out_stride)
+        out_stride = _token_rows("out", out, dev, x.dtype, heads, D, T)
+    args = (x.data_ptr(), code, T, stride, heads, D, 2 * freqs.shape[0], positions.data_ptr(), freqs.data_ptr(),
+            interleaved, scale, out.data_ptr(), out_stride)
+    rc = call(*args, _stream(dev)) if dev.index == _current_device() else _elsewhere(dev, call, args)
+    if rc:
+        _check(rc)
     return out
 
 
@@ -795,6 +806,7 @@ class KVCache:
         self._struct = _CacheStruct(*[None if t is None else t.data_ptr() for t in self._parts], self.mode.encode(),
                                     self.pages, self.heads, self.page_size, self.head_dim, self.group_size, self.bits,
                                     _DTYPE[dtype])
+        self._address = ctypes.addressof(self._struct)
 
     @property
     def key(self) -> QuantizedWeight:
@@ -831,12 +843,15 @@ def kv_cache_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torc
     lib = _lib or load_library()
     dev = cache.device
     code = _float_code("k", k)
-    shape = (k.shape[0] if k.dim() else None, cache.heads, cache.head_dim)
-    k_stride = _token_rows("k", k, dev, cache.dtype or k.dtype, shape)
-    v_stride = _token_rows("v", v, dev, k.dtype, shape)
-    _index_rows("slots", slots, dev, shape[0])
-    _run(dev, lib.qlin_kv_cache_write, cache._struct, k.data_ptr(), v.data_ptr(), code, shape[0], k_stride, v_stride,
-         slots.data_ptr())
+    k_stride = _token_rows("k", k, dev, cache.dtype or k.dtype, cache.heads, cache.head_dim, None)
+    T = k.shape[0]
+    v_stride = _token_rows("v", v, dev, k.dtype, cache.heads, cache.head_dim, T)
+    _index_rows("slots", slots, dev, T)
+    args = (cache._address, k.data_ptr(), v.data_ptr(), code, T, k_stride, v_stride, slots.data_ptr())
+    call = lib.qlin_kv_cache_write
+    rc = call(*args, _stream(dev)) if dev.index == _current_device() else _elsewhere(dev, call, args)
+    if rc:
+        _check(rc)
 
 
 def kv_cache_read(cache: KVCache, slots: torch.Tensor, dtype: Optional[torch.dtype] = None):
@@ -851,8 +866,11 @@ def kv_cache_read(cache: KVCache, slots: torch.Tensor, dtype: Optional[torch.dty
     shape = (slots.shape[0], cache.heads, cache.head_dim)
     k = torch.empty(shape, dtype=dtype, device=dev)
     v = torch.empty(shape, dtype=dtype, device=dev)
-    _run(dev, lib.qlin_kv_cache_read, cache._struct, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(),
-         _DTYPE[dtype])
+    args = (cache._address, slots.data_ptr(), shape[0], k.data_ptr(), v.data_ptr(), _DTYPE[dtype])
+    call = lib.qlin_kv_cache_read
+    rc = call(*args, _stream(dev)) if dev.index == _current_device() else _elsewhere(dev, call, args)
+    if rc:
+        _check(rc)
     return k, v
 
 
@@ -860,7 +878,7 @@ def kv_cache_attention_workspace_bytes(cache: KVCache, T: int, q_heads: int, B: 
                                        window: int = 0, dtype: torch.dtype = torch.bfloat16) -> int:
     """qlin_kv_cache_attention_workspace_bytes for q [T, q_heads, head_dim] of dtype."""
     return int(load_library().qlin_kv_cache_attention_workspace_bytes(
-        cache._struct, _DTYPE[dtype], T, q_heads, B, width, int(has_offsets), window))
+        cache._address, _DTYPE[dtype], T, q_heads, B, width, int(has_offsets), window))
 
 
 def kv_cache_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lengths: torch.Tensor,
@@ -878,12 +896,10 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, len
     lib = _lib or load_library()
     dev = cache.device
     code = _float_code("q", q)
-    if q.dim() != 3:
-        raise ValueError("q must be [T, q_heads, head_dim]")
+    q_stride = _token_rows("q", q, dev, cache.dtype or q.dtype, None, cache.head_dim, None)
     T, heads, D = q.shape
-    q_stride = _token_rows("q", q, dev, cache.dtype or q.dtype, (T, heads, cache.head_dim))
     _check_tensor("table", table, dev, torch.int32)
-    if table.dim() != 2:
+    if len(table.shape) != 2:
         raise ValueError("table must be [B, width]")
     B, width = table.shape
     _index_rows("lengths", lengths, dev, B)
@@ -895,8 +911,12 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, len
     else:
         out = _out(out, (T, heads, D), q.dtype, dev)
     keep, ws, ws_bytes = _workspace(workspace, lib.qlin_kv_cache_attention_workspace_bytes(
-        cache._struct, code, T, heads, B, width, offsets is not None, window), dev)
-    _run(dev, lib.qlin_kv_cache_attention, cache._struct, q.data_ptr(), code, T, q_stride, heads, table.data_ptr(), B,
-         width, lengths.data_ptr(), None if offsets is None else offsets.data_ptr(),
-         D ** -0.5 if scale is None else scale, bool(causal), window, ws, ws_bytes, out.data_ptr())
+        cache._address, code, T, heads, B, width, offsets is not None, window), dev)
+    args = (cache._address, q.data_ptr(), code, T, q_stride, heads, table.data_ptr(), B, width, lengths.data_ptr(),
+            None if offsets is None else offsets.data_ptr(), D ** -0.5 if scale is None else scale, causal, window, ws,
+            ws_bytes, out.data_ptr())
+    call = lib.qlin_kv_cache_attention
+    rc = call(*args, _stream(dev)) if dev.index == _current_device() else _elsewhere(dev, call, args)
+    if rc:
+        _check(rc)
     return out

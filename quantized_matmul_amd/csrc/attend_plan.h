@@ -26,7 +26,6 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
                               bool one_row) {
     constexpr int64_t kStepKeys = 128;       // keys that the four waves of a workgroup take at a time
     constexpr int64_t kChunkMost = 4096;     // keys a workgroup takes, where that makes no more than kMany of them
-    constexpr int64_t kWorkgroups = 2048;    // enough of them to fill the chip evenly
     constexpr int64_t kMany = 32768;
     constexpr int64_t kPromptRows = 64;      // rows of a sequence and key head, on average, from which a prompt is one
     constexpr int64_t kImages = 1LL << 33;   // bytes of decoded keys and values at most
@@ -71,7 +70,10 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
     p.rows = 16 * p.nt / dup;
     p.tiles = one_row ? B * ((share + p.rows - 1) / p.rows) : T * share / p.rows + B;
     const int64_t base = p.tiles * c.heads;
-    int64_t splits = (kWorkgroups + base - 1) / base;
+    // as many workgroups as fit the chip at once (twice as many where two fit a CU). Measured with 768, 1024 and 2048,
+    // D 128, us: 16 x 6000 keys 26.7, 31.1, 33.8; 16000 keys 15.2, 19.6, 19.4; drafts of two a CU 30.8, 28.7, 32.1
+    const int64_t fit = p.nt == 1 && c.D <= 128 ? 768 : 1024;
+    int64_t splits = (fit + base - 1) / base;
     int64_t chunk = ((keys + splits - 1) / splits + kStepKeys - 1) / kStepKeys * kStepKeys;
     if (chunk > kChunkMost) chunk = kChunkMost;
     while (chunk < keys && base * (keys / chunk) > kMany) chunk *= 2;
