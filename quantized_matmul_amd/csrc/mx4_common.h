@@ -142,23 +142,6 @@ constexpr int64_t kMx4MaxExperts = 8000;
 // Index rows of one call: their numbers, rounded up to a chunk of the plan, are 32-bit integers.
 constexpr int64_t kMx4MaxRows = (1LL << 31) - (1LL << 14);
 
-// n / d for n < 2^32 by a multiplication and shifts (Granlund and Montgomery's
-// division by an invariant); the host makes it.
-struct FastDiv {
-    uint32_t mul, shift;   // mul 0: d is 1
-    static FastDiv by(uint32_t d) {
-        if (d <= 1) return {0, 0};
-        uint32_t l = 0;    // ceil(log2 d)
-        while ((1ull << l) < d) ++l;
-        return {(uint32_t)((((1ull << l) - d) << 32) / d + 1), l - 1};
-    }
-    __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
-        if (!mul) return n;
-        const uint32_t h = __umulhi(n, mul);
-        return (h + ((n - h) >> 1)) >> shift;
-    }
-};
-
 // A row tile: everything a workgroup needs to know of it in one 32-byte load.
 struct Mx4Tile {
     uint32_t group;         // expert; E: rows without one, whose outputs are zeros

@@ -128,6 +128,31 @@ def test_constant_and_zero_rows():
         assert torch.equal(a.bfloat16(), want) and torch.equal(b.bfloat16(), -want)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("mode,g", [("affine", 32), ("affine", 64), ("affine", 128), ("mxfp4", 32), ("nvfp4", 16)])
+def test_ties_zeros_and_small_rows(mode, g, dtype):
+    """Quotients half way between codes, signed zeros in either order, the smallest and the largest groups: the oracle's bytes."""
+    D, rows = 128, []
+    step = torch.arange(D).float()
+    for size in (1.0, 0.25, 2.0 ** -12, 3.0):
+        rows += [step % 31 / 2 * size, (step % 31 / 2 - 7.5) * size, (step % 13 / 4 - 1.5) * size, (step * 7 % 25 / 8 - 1.5) * size]
+    zeros = torch.zeros(D)
+    rows += [zeros, -zeros, torch.where(step % 3 == 0, -zeros, zeros), torch.where(step % 5 == 1, -zeros, zeros),
+             torch.where(step % 4 == 0, -zeros, step % 4), torch.where(step % 4 == 0, zeros, -(step % 4)),
+             torch.where(step % 32 < 16, zeros, -zeros), torch.where(step % 32 < 16, -zeros, zeros)]
+    tiny, most = torch.finfo(DTYPES[dtype]).smallest_normal, torch.finfo(DTYPES[dtype]).max
+    rows += [(step % 9 - 4) * tiny, (step % 9 - 4) * tiny / 8, step * tiny, (step % 17 - 8) / 8 * most / 8, torch.full((D,), -tiny)]
+    x = torch.stack(rows).to(DTYPES[dtype])[:, None].to(DEV)
+    cache = qm.kv_cache(2, 1, 32, D, g, mode, DTYPES[dtype], DEV)
+    slots = torch.arange(len(rows), dtype=torch.int32, device=DEV)
+    qm.kv_cache_write(cache, x, x.flip(0), slots)
+    for w, y in ((cache.key, x), (cache.value, x.flip(0))):
+        want = oracle.quantize(to_oracle(y).reshape(-1, D), ORACLE_DT[DTYPES[dtype]], g, 4, mode)
+        for t, ref_t in zip((w.value, w.scales, w.biases), want):
+            if t is not None:
+                np.testing.assert_array_equal(to_oracle(at(t.cpu(), slots.cpu(), 32)).reshape(ref_t.shape), ref_t)
+
+
 def test_a_pool_past_32_bits():
     """A pool of more than 2^32 bytes of codes: its last rows are written and read where they lie."""
     H, D, page = 8, 256, 4096
