@@ -34,7 +34,7 @@ __device__ __forceinline__ void sincos_turns(double r, float* s, float* c) {
     p = __builtin_fmaf(x2, p, 1.0f / 24.0f);
     p = __builtin_fmaf(x2, p, -0.5f);
     const float cs = __builtin_fmaf(x2, p, 1.0f);
-    const int k = (int)(int64_t)(q - 4.0 * floor(q * 0.25));
+    const int k = (int)(q - 4.0 * floor(q * 0.25));
     const float a = (k & 1) ? cs : sn, b = (k & 1) ? sn : cs;
     *s = (k & 2) ? -a : a;
     *c = (k == 1 || k == 2) ? -b : b;
@@ -46,6 +46,8 @@ __device__ __forceinline__ float load_one(const void* p, int64_t i) {
 }
 
 // NV elements (16 bytes) at element i; VEC: one 16-byte load.
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+
 template <int DT, int NV, bool VEC>
 __device__ __forceinline__ void load_run(const void* p, int64_t i, float (&v)[NV]) {
     if constexpr (!VEC) {
@@ -65,13 +67,18 @@ __device__ __forceinline__ void load_run(const void* p, int64_t i, float (&v)[NV
     }
 }
 
-template <int DT, int NV, bool VEC>
+// PAST: past the caches.
+template <int DT, int NV, bool VEC, bool PAST>
 __device__ __forceinline__ void store_run(void* p, int64_t i, const float (&v)[NV]) {
+    auto put = [](u32x4 x, void* to) {
+        if constexpr (PAST) __builtin_nontemporal_store(x, (u32x4*)to);
+        else *(u32x4*)to = x;
+    };
     if constexpr (!VEC) {
 #pragma unroll
         for (int e = 0; e < NV; ++e) store_f<DT>(p, i + e, v[e]);
     } else if constexpr (DT == QLIN_F32) {
-        *(float4*)((float*)p + i) = float4{v[0], v[1], v[2], v[3]};
+        put(u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])}, (float*)p + i);
     } else {
         uint32_t d[4];
 #pragma unroll
@@ -83,7 +90,7 @@ __device__ __forceinline__ void store_run(void* p, int64_t i, const float (&v)[N
                 d[e] = f32_to_f16_rne(v[2 * e]) | (f32_to_f16_rne(v[2 * e + 1]) << 16);
             }
         }
-        *(uint4*)((uint16_t*)p + i) = uint4{d[0], d[1], d[2], d[3]};
+        put(u32x4{d[0], d[1], d[2], d[3]}, (uint16_t*)p + i);
     }
 }
 
@@ -91,7 +98,7 @@ __device__ __forceinline__ void store_run(void* p, int64_t i, const float (&v)[N
 // a whole number of runs; 2: half a row away, anywhere.
 // LANES lanes (a power of two) take a head's row; a block of 256 threads takes
 // 256 / LANES (token, head part) items, part = heads / parts of them.
-template <int DT, int PAIR, bool VEC, int LANES>
+template <int DT, int PAIR, bool VEC, int LANES, bool PAST>
 __global__ void __launch_bounds__(256) rotary_kernel(RotaryArgs a, int parts, int part_heads) {
     constexpr int NV = DT == QLIN_F32 ? 4 : 8;
     const int64_t item = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
@@ -122,23 +129,33 @@ __global__ void __launch_bounds__(256) rotary_kernel(RotaryArgs a, int parts, in
     }
     const int run = PAIR == 1 ? partner[0] : 0;
     const int h1 = min(h0 + part_heads, a.heads);
-    for (int h = h0; h < h1; ++h) {
-        const int64_t row = t * a.x_stride + (int64_t)h * a.D;
-        float v[NV], w[NV], y[NV];
-        load_run<DT, NV, VEC>(a.x, row + e, v);
-        if constexpr (PAIR == 1) {
-            load_run<DT, NV, VEC>(a.x, row + run, w);
-        } else if constexpr (PAIR == 2) {
+    // HB heads' loads at once: a store may not be passed by a later load, as y may be x
+    constexpr int HB = 4;
+    for (int h = h0; h < h1; h += HB) {
+        float v[HB][NV], w[HB][NV];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) w[i] = load_f<DT>(a.x, row + partner[i]);
-        } else {
+        for (int u = 0; u < HB; ++u) {
+            const int64_t row = t * a.x_stride + (int64_t)min(h + u, h1 - 1) * a.D;
+            load_run<DT, NV, VEC>(a.x, row + e, v[u]);
+            if constexpr (PAIR == 1) {
+                load_run<DT, NV, VEC>(a.x, row + run, w[u]);
+            } else if constexpr (PAIR == 2) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) w[i] = v[i ^ 1];
+                for (int i = 0; i < NV; ++i) w[u][i] = load_f<DT>(a.x, row + partner[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) w[u][i] = v[u][i ^ 1];
+            }
         }
-        // the product with the sine rounds first, then the sum: 2^-23 of the pair's size at most
 #pragma unroll
-        for (int i = 0; i < NV; ++i) y[i] = e + i < a.R ? __builtin_fmaf(v[i], c[i], w[i] * s[i]) : v[i];
-        store_run<DT, NV, VEC>(a.y, t * a.y_stride + (int64_t)h * a.D + e, y);
+        for (int u = 0; u < HB; ++u) {
+            if (h + u >= h1) break;
+            float y[NV];
+            // the product with the sine rounds first, then the sum: 2^-23 of the pair's size at most
+#pragma unroll
+            for (int i = 0; i < NV; ++i) y[i] = e + i < a.R ? __builtin_fmaf(v[u][i], c[i], w[u][i] * s[i]) : v[u][i];
+            store_run<DT, NV, VEC, PAST>(a.y, t * a.y_stride + (int64_t)(h + u) * a.D + e, y);
+        }
     }
 }
 
@@ -156,22 +173,40 @@ hipError_t launch_rotary(const RotaryArgs& a, int dt, hipStream_t st) {
     if (parts > a.heads) parts = a.heads;
     const int part_heads = (a.heads + parts - 1) / parts;
     parts = (a.heads + part_heads - 1) / part_heads;
-    const int64_t items = a.T * parts, per = 256 / lanes;
-    const unsigned nb = (unsigned)((items + per - 1) / per);
+    const int64_t per = 256 / lanes;
+    // tokens of a launch, whose work-items stay below 2^32
+    const int64_t most = ((1LL << 31) / 256) * per / parts;
+    const bool past = a.x != a.y && 2 * a.T * a.heads * a.D * elem >= kStreamBytes;
+    RotaryArgs part = a;
+    unsigned nb = 0;
     auto go = [&](auto dtc, auto pc, auto vc) -> hipError_t {
         constexpr int DT = decltype(dtc)::value, P = decltype(pc)::value;
         constexpr bool V = decltype(vc)::value;
-        switch (lanes) {
-        case 1: rotary_kernel<DT, P, V, 1><<<nb, 256, 0, st>>>(a, parts, part_heads); break;
-        case 2: rotary_kernel<DT, P, V, 2><<<nb, 256, 0, st>>>(a, parts, part_heads); break;
-        case 4: rotary_kernel<DT, P, V, 4><<<nb, 256, 0, st>>>(a, parts, part_heads); break;
-        case 8: rotary_kernel<DT, P, V, 8><<<nb, 256, 0, st>>>(a, parts, part_heads); break;
-        case 16: rotary_kernel<DT, P, V, 16><<<nb, 256, 0, st>>>(a, parts, part_heads); break;
-        case 32: rotary_kernel<DT, P, V, 32><<<nb, 256, 0, st>>>(a, parts, part_heads); break;
-        case 64: rotary_kernel<DT, P, V, 64><<<nb, 256, 0, st>>>(a, parts, part_heads); break;
-        default: return hipErrorInvalidValue;
+        auto run = [&](auto lc) {
+            constexpr int L = decltype(lc)::value;
+            if (V && past) rotary_kernel<DT, P, V, L, V><<<nb, 256, 0, st>>>(part, parts, part_heads);
+            else rotary_kernel<DT, P, V, L, false><<<nb, 256, 0, st>>>(part, parts, part_heads);
+        };
+        for (int64_t t = 0; t < a.T; t += most) {
+            part.T = a.T - t < most ? a.T - t : most;
+            part.x = (const char*)a.x + t * a.x_stride * elem;
+            part.y = (char*)a.y + t * a.y_stride * elem;
+            part.positions = a.positions + t;
+            nb = (unsigned)((part.T * parts + per - 1) / per);
+            switch (lanes) {
+            case 1: run(std::integral_constant<int, 1>{}); break;
+            case 2: run(std::integral_constant<int, 2>{}); break;
+            case 4: run(std::integral_constant<int, 4>{}); break;
+            case 8: run(std::integral_constant<int, 8>{}); break;
+            case 16: run(std::integral_constant<int, 16>{}); break;
+            case 32: run(std::integral_constant<int, 32>{}); break;
+            case 64: run(std::integral_constant<int, 64>{}); break;
+            default: return hipErrorInvalidValue;
+            }
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
         }
-        return hipGetLastError();
+        return hipSuccess;
     };
     auto paired = [&](auto dtc, auto vc) -> hipError_t {
         if (pair == 0) return go(dtc, std::integral_constant<int, 0>{}, vc);
