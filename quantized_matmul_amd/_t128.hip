@@ -1,4 +1,4 @@
-#include "csrc/attend_tile.h"
+#include "csrc/attend_prompt.h"
 namespace qlin { namespace {
-template __global__ void attend_tile_kernel<QLIN_F16,NVFP4,64,1,3,false>(TileArgs);
+template __global__ void attend_prompt_kernel<QLIN_BF16,128,2>(TileArgs, int64_t);
 } }

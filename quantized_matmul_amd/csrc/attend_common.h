@@ -57,6 +57,7 @@ struct TileArgs {
     const uint8_t* images;       // prompt tiles: dense keys and values of kImageKeys keys, [sequence, key block, head]
     uint64_t* present;           // [sequence, key block]: which of its keys are there
     float* key_scale;            // [sequence, key block, head]: what its keys are to be multiplied by
+    int32_t* value_power;        // [sequence, key block, head]: the power of two that its values are to be multiplied by
     int key_blocks;              // of a sequence
 };
 

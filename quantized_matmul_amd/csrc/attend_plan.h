@@ -56,7 +56,7 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
         p.splits = (int)((keys + 64 + p.chunk - 1) / p.chunk);
         p.key_blocks = (int)(blocks ? blocks : 1);
         p.present_at = (size_t)B * p.key_blocks * c.heads * c.D * 256;
-        p.part_at = (p.present_at + (size_t)B * p.key_blocks * (8 + 4 * c.heads) + 255) / 256 * 256;
+        p.part_at = (p.present_at + (size_t)B * p.key_blocks * (8 + 8 * c.heads) + 255) / 256 * 256;
         p.bytes = p.part_at + (p.splits > 1 ? (size_t)(base * p.splits * p.rows) * (c.D + 2) * sizeof(float) : 0);
         p.fits = base * p.splits <= kItems / 256;
         return p;

@@ -7,11 +7,14 @@
 // operands are contiguous (no bank is met twice) and blocks go from memory to
 // LDS as they are. The eight keys of a piece are those that a lane's scores come
 // out as: 4 hb .. 4 hb + 3 and 8 + 4 hb .. (hb = lane / 32).
-// Keys and q are multiplied as f16 for either type, a block's keys divided by a
-// power of two that takes their largest into [1, 2), a row of q likewise: bf16
-// keys put 2^-9 of |q| |k| on a score, which a sharp softmax passes on (error
-// 0.0051 of the output where 0.0017 is its own rounding); f16 keys 2^-12, and
-// no value leaves f16's range.
+// Keys, values, q and p are multiplied as f16 for either type, a block's keys
+// divided by a power of two that takes their largest into [1, 2), its values and
+// a row of q likewise: bf16 keys put 2^-9 of |q| |k| on a score, which a sharp
+// softmax passes on, and bf16 values and p as much on the output (errors of a
+// bf16 output, whose own rounding is 0.0017: 0.0051; with f16 keys 0.0025, with
+// all in f16 0.0018). No value leaves f16's range; what is 2^-14 of the largest
+// of its block and less is held to 2^-25 of that. o is kept in units of the
+// largest block's power of two so far, p of other blocks divided accordingly.
 // Decoding inside the attention kernel would cost every workgroup again what
 // this does once: 190 of about 560 vector instructions of 64 keys (D 128), where
 // the matrix cores need the time of 512.
@@ -37,13 +40,10 @@ namespace {
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 
 constexpr int kImageKeys = 64;
+constexpr int kNoPower = -1000;                  // below any number's
 
-template <int DT>
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
-    if constexpr (DT == QLIN_BF16)
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
 // floor(log2 |x|) of a finite number other than zero.
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
     const int lo = seen_by(a, s, 0).lo, hi = seen_by(a, s, s.n - 1).hi, key0 = kb * kImageKeys;
     if (key0 >= hi || key0 + kImageKeys <= lo) return;
     __shared__ int32_t blocks[kImageKeys / kKvUnit];
-    __shared__ float largest[4];
+    __shared__ float largest[2][4];
     const int tid = threadIdx.x;
     if (tid < kImageKeys / kKvUnit)
         blocks[tid] = key0 + tid * kKvUnit < s.keys
@@ -87,6 +87,23 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
         const int32_t rb = blocks[key / kKvUnit];
         return rb >= 0 && key0 + key < s.keys ? (int64_t)rb * kKvUnit + key % kKvUnit : -1;
     };
+    // power of two of the largest value of a side's keys
+    auto power = [&](int side) {
+        const int64_t row = row_of(tid % 64);
+        float most = 0.0f;
+        for (int g = tid / 64; g < groups; g += 4)
+            if (row >= 0) {
+                const float sc = scale_at<MODE, DT>(c.scales[side], row * groups + g);
+                const float z = MODE == AFFINE ? load_f<DT>(c.biases[side], row * groups + g) : 0.0f;
+                most = fmaxf(most, MODE == AFFINE ? fmaxf(fabsf(z), fabsf(__builtin_fmaf(sc, 15.0f, z))) : 6.0f * fabsf(sc));
+            }
+#pragma unroll
+        for (int off = 32; off; off /= 2) most = fmaxf(most, __shfl_xor(most, off, 64));
+        if (tid % 64 == 0) largest[side][tid / 64] = most;
+        __syncthreads();
+        most = fmaxf(fmaxf(largest[side][0], largest[side][1]), fmaxf(largest[side][2], largest[side][3]));
+        return most > 0.0f ? ilogb_of(most) : 0;
+    };
     {
         const int key = tid % 64;
         const int64_t row = row_of(key);
@@ -94,19 +111,7 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
             const uint64_t there = __ballot(row >= 0);
             if (tid == 0) t.present[(int64_t)b * t.key_blocks + kb] = there;
         }
-        float most = 0.0f;
-        for (int g = tid / 64; g < groups; g += 4)
-            if (row >= 0) {
-                const float sc = scale_at<MODE, DT>(c.scales[0], row * groups + g);
-                const float z = MODE == AFFINE ? load_f<DT>(c.biases[0], row * groups + g) : 0.0f;
-                most = fmaxf(most, MODE == AFFINE ? fmaxf(fabsf(z), fabsf(__builtin_fmaf(sc, 15.0f, z))) : 6.0f * fabsf(sc));
-            }
-#pragma unroll
-        for (int off = 32; off; off /= 2) most = fmaxf(most, __shfl_xor(most, off, 64));
-        if (key == 0) largest[tid / 64] = most;
-        __syncthreads();
-        most = fmaxf(fmaxf(largest[0], largest[1]), fmaxf(largest[2], largest[3]));
-        const int e = most > 0.0f ? ilogb_of(most) : 0;
+        const int e = power(0);
         if (tid == 0) t.key_scale[((int64_t)b * t.key_blocks + kb) * c.heads + h] = __builtin_ldexpf(1.0f, e);
         for (int w = tid / 64; w < HW; w += 4) {
             u32x4 out{0, 0, 0, 0};
@@ -123,6 +128,8 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
             *(u32x4*)(image + w * (kImageKeys * 16) + key * 16) = out;
         }
     }
+    const int ve = power(1);
+    if (tid == 0) t.value_power[((int64_t)b * t.key_blocks + kb) * c.heads + h] = ve;
     for (int e = tid; e < 8 * HW; e += 256) {
         const int w = e % HW, piece = e / HW;    // keys 16 (piece / 2) + 4 (piece % 2) + {0..3, 8..11}
         float v[8][8];
@@ -133,6 +140,8 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
                 const int64_t g = row * groups + w / per;
                 word_values<MODE>(c.codes[1][row * HW + w], scale_at<MODE, DT>(c.scales[1], g),
                                   MODE == AFFINE ? load_f<DT>(c.biases[1], g) : 0.0f, v[i]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[i][k] = __builtin_ldexpf(v[i][k], -ve);
             } else {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[i][k] = 0.0f;
@@ -141,8 +150,8 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
         uint8_t* const to = image + kImageKeys * D * 2 + (piece * D + w * 8) * 16;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            *(u32x4*)(to + k * 16) = u32x4{round2<DT>(v[0][k], v[1][k]), round2<DT>(v[2][k], v[3][k]),
-                                           round2<DT>(v[4][k], v[5][k]), round2<DT>(v[6][k], v[7][k])};
+            *(u32x4*)(to + k * 16) = u32x4{round2<QLIN_F16>(v[0][k], v[1][k]), round2<QLIN_F16>(v[2][k], v[3][k]),
+                                           round2<QLIN_F16>(v[4][k], v[5][k]), round2<QLIN_F16>(v[6][k], v[7][k])};
     }
 }
 
@@ -215,6 +224,7 @@ __global__ void __launch_bounds__(256, 2) attend_prompt_kernel(TileArgs t, int64
 
     f32x16 o[RT][DTILES];
     float m[RT], l[RT];
+    int unit = kNoPower;                         // o's power of two
 #pragma unroll
     for (int n = 0; n < RT; ++n) {
         m[n] = kNone;
@@ -240,10 +250,23 @@ __global__ void __launch_bounds__(256, 2) attend_prompt_kernel(TileArgs t, int64
         const int buf = (kb - kb0) & 1;
         const uint64_t there = t.present[(int64_t)w.b * t.key_blocks + kb];   // waited for with the block
         const float key_scale = t.key_scale[((int64_t)w.b * t.key_blocks + kb) * c.heads + h];
+        const int value_power = t.value_power[((int64_t)w.b * t.key_blocks + kb) * c.heads + h];
         __syncthreads();                         // this block has landed, the other buffer is read
         if (kb + 1 < kb1) fetch(kb + 1, buf ^ 1);
         const int key0 = kb * kImageKeys;
         if (idle || key0 >= see_last.hi || key0 + kImageKeys <= see_first.lo) continue;
+        const int up = __builtin_amdgcn_readfirstlane(value_power);
+        if (up > unit) {
+            const float f = __builtin_ldexpf(1.0f, unit == kNoPower ? 0 : unit - up);
+            unit = up;
+#pragma unroll
+            for (int n = 0; n < RT; ++n)
+#pragma unroll
+                for (int d = 0; d < DTILES; ++d) o[n][d] *= f;
+        }
+        // p is multiplied by 2^down, its sum back; where that is nothing beside the largest block, by no less than 2^-64
+        const int fall = max(up - unit, -64);
+        const float down = (float)fall, back = __builtin_ldexpf(1.0f, -fall);
         const bool whole = there == ~0ull && key0 >= see_last.lo && key0 + kImageKeys <= see_first.hi;
         const uint8_t* const kl = lds[buf] + hb * (kImageKeys * 16) + r * 16;
         const uint8_t* const vl = lds[buf] + kImageKeys * D * 2 + hb * (D * 16) + r * 16;
@@ -258,7 +281,7 @@ __global__ void __launch_bounds__(256, 2) attend_prompt_kernel(TileArgs t, int64
             for (int k = 0; k < KS; ++k) {
                 const u32x4 ka = *(const u32x4*)(kl + k * (2 * kImageKeys * 16) + kt * 512);
 #pragma unroll
-                for (int n = 0; n < RT; ++n) s[n] = mfma32<QLIN_F16>(ka, q[n][k], s[n]);
+                for (int n = 0; n < RT; ++n) s[n] = mfma32(ka, q[n][k], s[n]);
             }
             u32x4 p[RT][2];
 #pragma unroll
@@ -289,16 +312,16 @@ __global__ void __launch_bounds__(256, 2) attend_prompt_kernel(TileArgs t, int64
 #pragma unroll
                     for (int d = 0; d < DTILES; ++d) o[n][d] *= f;
                 }
-                const float base = m[n] == kNone ? 0.0f : m[n];
+                const float base = (m[n] == kNone ? 0.0f : m[n]) - down;
                 float sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     s[n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], to_log2, -base));
                     sum += s[n][i];
                 }
-                l[n] += sum;
+                l[n] = __builtin_fmaf(sum, back, l[n]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) p[n][i / 4][i % 4] = round2<DT>(s[n][2 * i], s[n][2 * i + 1]);
+                for (int i = 0; i < 8; ++i) p[n][i / 4][i % 4] = round2<QLIN_F16>(s[n][2 * i], s[n][2 * i + 1]);
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k)
@@ -306,7 +329,7 @@ __global__ void __launch_bounds__(256, 2) attend_prompt_kernel(TileArgs t, int64
                 for (int d = 0; d < DTILES; ++d) {
                     const u32x4 va = *(const u32x4*)(vl + (kt * 4 + k * 2) * (D * 16) + d * 512);
 #pragma unroll
-                    for (int n = 0; n < RT; ++n) o[n][d] = mfma32<DT>(va, p[n][k], o[n][d]);
+                    for (int n = 0; n < RT; ++n) o[n][d] = mfma32(va, p[n][k], o[n][d]);
                 }
         }
     }
@@ -315,10 +338,11 @@ __global__ void __launch_bounds__(256, 2) attend_prompt_kernel(TileArgs t, int64
 #pragma unroll
     for (int n = 0; n < RT; ++n) {
         l[n] += __shfl_xor(l[n], 32, 64);
+        const float of = unit == kNoPower ? 1.0f : __builtin_ldexpf(1.0f, unit);
         const int row = first + n * 32 + r;
         if (row >= w.rows) continue;
         if (w.splits <= 1) {
-            const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];          // a row that sees no key: zeros
+            const float inv = l[n] == 0.0f ? 0.0f : of / l[n];            // a row that sees no key: zeros
             const int rr = w.row0 + row;
             const int64_t to = ((w.s.first + rr / share) * a.q_heads + h * share + rr % share) * D + 4 * hb;
 #pragma unroll
@@ -337,7 +361,7 @@ __global__ void __launch_bounds__(256, 2) attend_prompt_kernel(TileArgs t, int64
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     *(f32x4*)(t.part_o + (part + row) * D + 4 * hb + d * 32 + i * 8) =
-                        f32x4{o[n][d][4 * i], o[n][d][4 * i + 1], o[n][d][4 * i + 2], o[n][d][4 * i + 3]};
+                        f32x4{o[n][d][4 * i], o[n][d][4 * i + 1], o[n][d][4 * i + 2], o[n][d][4 * i + 3]} * of;
         }
     }
 }
@@ -348,7 +372,8 @@ hipError_t launch_prompt_of(const AttendArgs& a, const KvPool& c, int dt, const 
     constexpr int RT = D <= 128 ? 2 : 1, R = 128 * RT;
     char* const ws = (char*)workspace;
     TileArgs t{a, c, p.chunk, p.splits, (float*)(ws + p.part_at), nullptr, (uint8_t*)ws, (uint64_t*)(ws + p.present_at),
-               (float*)(ws + p.present_at) + (int64_t)a.B * p.key_blocks * 2, p.key_blocks};
+               (float*)(ws + p.present_at) + (int64_t)a.B * p.key_blocks * 2, nullptr, p.key_blocks};
+    t.value_power = (int32_t*)t.key_scale + (int64_t)a.B * p.key_blocks * c.heads;
     t.part_ml = t.part_o + p.tiles * c.heads * p.splits * R * D;
     auto run = [&](auto dtc, auto mode) -> hipError_t {
         constexpr int DT = decltype(dtc)::value, M = decltype(mode)::value;

@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(256, tile_residents(D, NT)) attend_tile_kernel
 template <int D>
 hipError_t launch_tile_of(const AttendArgs& a, const KvPool& c, int dt, const AttendPlan& p, void* workspace,
                           hipStream_t st) {
-    TileArgs t{a, c, p.chunk, p.splits, (float*)workspace, nullptr, nullptr, nullptr, nullptr, 0};
+    TileArgs t{a, c, p.chunk, p.splits, (float*)workspace, nullptr, nullptr, nullptr, nullptr, nullptr, 0};
     t.part_ml = t.part_o + p.tiles * c.heads * p.splits * p.rows * D;
     const dim3 grid((unsigned)(p.tiles * p.splits), (unsigned)c.heads);
     auto run = [&](auto dtc, auto mode, auto gq) -> hipError_t {

@@ -5,6 +5,7 @@ Tolerance, for each output o = sum p v with size = sum p |v|:
             sqrt(D) roundings of 2^-24 (their signs are random, 4 standard deviations) of scale * sum |q| (31 s + |z|),
             which is below 40 * scale * sum |q| * max |k| for affine codes (s is 1/15 of a group's range, at most 2/15 of
             max |k|: 31 s <= 4.2 max |k|; taken as 6); p then is off by e^d, output and sum alike: 2 d of the size.
+            In prompts u is f16's for either type, and what is small beside the largest value is held to 2^-24 of that.
   keys      in prompts rounded to f16 for either type: independent errors of at most 2^-11 |k|, 2^-11 / sqrt(3) |k| in
             their standard deviation (2^-25 of the largest where f16 has no more bits, inside the scores' bound); through scores and softmax they reach o as `spread` of kv_reference, times 6 for the many outputs
             (and twice that, as p and the sum of p move together).
@@ -98,10 +99,13 @@ class Problem:
             kmax = np.abs(k).max() if L else 0.0
             d = 4 * np.sqrt(self.D) * 2.0 ** -24 * abs(scale) * np.abs(q[first : first + n]).sum(-1, keepdims=True) * 6 * kmax
             out[first : first + n] = o
-            tol[first : first + n] = size * (2 * u + 2 * d + 2.0 ** -22 + (np.sqrt(L) + 8) * 2.0 ** -24) + u * np.abs(o) \
+            pv = 2.0 ** -11 if self.prompt else u
+            tol[first : first + n] = size * (2 * pv + 2 * d + 2.0 ** -22 + (np.sqrt(L) + 8) * 2.0 ** -24) + u * np.abs(o) \
                 + (2.0 ** -24 if self.dtype == "f16" else 0)
             if self.prompt and self.mode == "affine":
                 tol[first : first + n] += 12 * 2.0 ** -11 / np.sqrt(3) * spread
+            if self.prompt and L:
+                tol[first : first + n] += 2.0 ** -24 * np.abs(v).max()
             first += n
         return out, tol
 
@@ -249,6 +253,22 @@ def test_queries_and_keys_of_any_size(rows, mode, g):
         k = torch.nan_to_num(live[0].float(), 0.0, 0.0, 0.0) * k_size
         p.cache = qm.KVCache(qm.quantize(k.bfloat16().contiguous(), g, 4, mode), p.cache.value)
         p.q = (p.q.float() * q_size).bfloat16()
+        p.check(p.call())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows", [1, 90])
+def test_values_of_any_size(rows, dtype):
+    """Values whose size changes from page to page by powers of two, up and down."""
+    p = Problem([rows, rows], [500, 300], 2, 2, 64, "affine", 64, dtype, 64, seed=31, garbage=False)
+    v = qm.dequantize(p.cache.value, torch.float32)
+    sizes = 2.0 ** torch.tensor([0, 9, -9, 3, -14, 10, -3, 0, 6, -8, 2, -1, 4, 8, -12, 1, 0, 0, 0, 0])[: v.shape[0]]
+    p.cache = qm.KVCache(p.cache.key, qm.quantize((v * sizes.to(DEV)[:, None, None, None]).to(DTYPES[dtype]).contiguous(), 64, 4))
+    p.check(p.call())
+    if dtype == "bf16":
+        p.cache = qm.KVCache(p.cache.key, qm.quantize((v * 1e30 * sizes.to(DEV)[:, None, None, None] ** 2).bfloat16().contiguous(), 64, 4))
+        p.check(p.call())
+        p.cache = qm.KVCache(p.cache.key, qm.quantize((v * 1e-30 * sizes.to(DEV)[:, None, None, None] ** 2).bfloat16().contiguous(), 64, 4))
         p.check(p.call())
 
 
