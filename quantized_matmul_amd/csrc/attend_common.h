@@ -76,9 +76,10 @@ __global__ void __launch_bounds__(256) attend_join_kernel(TileArgs t, int tile_r
     __shared__ float part_l[WAVES];
     const AttendArgs& a = t.a;
     const KvPool& c = t.c;
-    const int groups = tile_rows / ROWS, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+    const int groups = (tile_rows + ROWS - 1) / ROWS, wave = threadIdx.x / 64, lane = threadIdx.x % 64;
     const int row = (int)(blockIdx.x % groups) * ROWS + wave / WAVES, h = blockIdx.y;
     const int64_t tile = blockIdx.x / groups;
+    if (row >= tile_rows) return;
     const int64_t part = ((tile * c.heads + h) * t.splits) * tile_rows + row;
     const float2* const ml = (const float2*)t.part_ml + part;
     // the first chunks' numbers, before the lengths say how many there are
@@ -134,7 +135,7 @@ hipError_t launch_join(const TileArgs& t, int64_t tiles, int tile_rows, int unit
     if (t.splits > 8 && tiles * tile_rows * t.c.heads <= 2048)
         attend_join_kernel<DT, D, 4><<<dim3((unsigned)(tiles * tile_rows), (unsigned)t.c.heads), 256, 0, st>>>(t, tile_rows, unit);
     else
-        attend_join_kernel<DT, D, 1><<<dim3((unsigned)(tiles * (tile_rows / 4)), (unsigned)t.c.heads), 256, 0, st>>>(t, tile_rows, unit);
+        attend_join_kernel<DT, D, 1><<<dim3((unsigned)(tiles * ((tile_rows + 3) / 4)), (unsigned)t.c.heads), 256, 0, st>>>(t, tile_rows, unit);
     return hipGetLastError();
 }
 

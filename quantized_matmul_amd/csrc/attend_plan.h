@@ -46,10 +46,11 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
     const int64_t blocks = (held + 63) / 64;
     if (mean > kPromptRows && blocks * B <= kImages / ((int64_t)c.heads * c.D * 256)) {
         p.path = 2;
-        p.rows = c.D <= 128 ? 256 : 128;
+        // tiles of 256 rows where they fill the chip (two workgroups a CU), or of 128 (three)
+        p.rows = c.D <= 128 && (T * share / 256 + B) * c.heads >= 512 ? 256 : 128;
         p.tiles = T * share / p.rows + B;
-        const int64_t base = p.tiles * c.heads;
-        int64_t splits = (512 + base - 1) / base;
+        const int64_t base = p.tiles * c.heads, fit = p.rows == 128 && c.D <= 128 ? 768 : 512;
+        int64_t splits = (fit + base - 1) / base;
         int64_t chunk = ((keys + splits - 1) / splits + 255) / 256 * 256;
         if (splits == 1) chunk = 1 << 30;
         p.chunk = (int)(chunk < (1 << 30) ? chunk : 1 << 30);
@@ -63,11 +64,11 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
     }
     p.path = 1;
     const int groups = c.mode == 0 && dt == QLIN_BF16 ? c.D / c.g : 0;
-    p.codes = groups == 1 || (groups == 2 && mean <= 8);
+    p.codes = groups == 1 || (groups >= 2 && groups <= 4 && mean <= 16 / groups);
     const int dup = p.codes ? groups : 1;
-    p.nt = mean > 16 ? 2 : 1;
-    if (c.D == 64 && mean > 32) p.nt = 3;                    // (larger heads' rows do not fit the registers)
-    p.rows = 16 * p.nt / dup;
+    p.nt = mean > 16 && c.D <= 128 ? 2 : 1;
+    if (c.D == 64 && mean > 32) p.nt = 3;                    // (what the registers hold)
+    p.rows = 16 / dup * p.nt;
     p.tiles = one_row ? B * ((share + p.rows - 1) / p.rows) : T * share / p.rows + B;
     const int64_t base = p.tiles * c.heads;
     // as many workgroups as fit the chip at once (twice as many where two fit a CU). Measured with 768, 1024 and 2048,

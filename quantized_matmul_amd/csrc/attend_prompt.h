@@ -61,10 +61,10 @@ __device__ __forceinline__ void word_values(uint32_t w, float s, float z, float 
     }
 }
 
-// A block of 256 threads: the 64 keys of one image.
-template <int DT, int MODE, int D>
+// A block of 256 threads: the 64 keys of one image, in parts of BK keys.
+template <int DT, int MODE, int D, int BK>
 __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* images) {
-    constexpr int HW = D / 8;
+    constexpr int HW = D / 8, PART = BK * D * 4;
     const AttendArgs& a = t.a;
     const KvPool& c = t.c;
     const int h = blockIdx.x % c.heads, kb = blockIdx.x / c.heads % t.key_blocks, b = blockIdx.x / c.heads / t.key_blocks;
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
                 out = u32x4{round2<QLIN_F16>(v[0], v[1]), round2<QLIN_F16>(v[2], v[3]), round2<QLIN_F16>(v[4], v[5]),
                             round2<QLIN_F16>(v[6], v[7])};
             }
-            *(u32x4*)(image + w * (kImageKeys * 16) + key * 16) = out;
+            *(u32x4*)(image + key / BK * PART + w * (BK * 16) + key % BK * 16) = out;
         }
     }
     const int ve = power(1);
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
                 for (int k = 0; k < 8; ++k) v[i][k] = 0.0f;
             }
         }
-        uint8_t* const to = image + kImageKeys * D * 2 + (piece * D + w * 8) * 16;
+        uint8_t* const to = image + piece / (BK / 8) * PART + BK * D * 2 + (piece % (BK / 8) * D + w * 8) * 16;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             *(u32x4*)(to + k * 16) = u32x4{round2<QLIN_F16>(v[0][k], v[1][k]), round2<QLIN_F16>(v[2][k], v[3][k]),
@@ -155,11 +155,16 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
     }
 }
 
+// Waves of a SIMD that the registers hold.
+constexpr int prompt_residents(int D, int RT) { return D <= 128 && RT == 1 ? 3 : 2; }
+// Keys of a buffer: two (three) workgroups' pairs of them fit a CU's LDS.
+constexpr int prompt_keys(int D, int RT) { return D <= 128 && RT == 2 ? 64 : 32; }
+
 template <int DT, int D, int RT>
-__global__ void __launch_bounds__(256, 2) attend_prompt_kernel(TileArgs t, int64_t tiles) {
-    constexpr int R = 128 * RT, KS = D / 16, DTILES = D / 32;
-    constexpr int IMAGE = kImageKeys * D * 4, ROUNDS = IMAGE / 4096;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2][IMAGE];
+__global__ void __launch_bounds__(256, prompt_residents(D, RT)) attend_prompt_kernel(TileArgs t, int64_t tiles) {
+    constexpr int R = 128 * RT, KS = D / 16, DTILES = D / 32, BK = prompt_keys(D, RT);
+    constexpr int IMAGE = kImageKeys * D * 4, PART = BK * D * 4, ROUNDS = PART / 4096, PARTS = kImageKeys / BK;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2][PART];
     const AttendArgs& a = t.a;
     const KvPool& c = t.c;
     // heads over the XCDs, so that each L2 keeps its head's keys; the last tiles, which see most, first
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(256, 2) attend_prompt_kernel(TileArgs t, int64
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, r = lane % 32, hb = lane / 32;
     const int share = a.q_heads / c.heads;
     const int k0 = w.k0 + split * t.chunk, k1 = w.splits ? min(w.hi, k0 + t.chunk) : k0;
-    const int kb0 = k0 / kImageKeys, kb1 = (k1 + kImageKeys - 1) / kImageKeys;
+    const int kb0 = k0 / BK, kb1 = (k1 + BK - 1) / BK;
 
     auto row_at = [&](int i) { return min(w.row0 + i, w.row0 + w.rows - 1); };   // rows past the end repeat the last
     const int first = wave * 32 * RT;
@@ -237,7 +242,7 @@ __global__ void __launch_bounds__(256, 2) attend_prompt_kernel(TileArgs t, int64
 
     const uint8_t* const images = t.images + ((int64_t)w.b * t.key_blocks * c.heads + h) * IMAGE;
     auto fetch = [&](int kb, int buf) {
-        const uint8_t* from = images + (int64_t)kb * c.heads * IMAGE + tid * 16;
+        const uint8_t* from = images + (int64_t)(kb / PARTS) * c.heads * IMAGE + kb % PARTS * PART + tid * 16;
 #pragma unroll
         for (int i = 0; i < ROUNDS; ++i)
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + i * 4096),
@@ -248,13 +253,14 @@ __global__ void __launch_bounds__(256, 2) attend_prompt_kernel(TileArgs t, int64
     if (kb0 < kb1) fetch(kb0, 0);
     for (int kb = kb0; kb < kb1; ++kb) {
         const int buf = (kb - kb0) & 1;
-        const uint64_t there = t.present[(int64_t)w.b * t.key_blocks + kb];   // waited for with the block
-        const float key_scale = t.key_scale[((int64_t)w.b * t.key_blocks + kb) * c.heads + h];
-        const int value_power = t.value_power[((int64_t)w.b * t.key_blocks + kb) * c.heads + h];
+        const int64_t ib = (int64_t)w.b * t.key_blocks + kb / PARTS;          // waited for with the block:
+        const uint64_t there = PARTS == 1 ? t.present[ib] : ((const uint32_t*)t.present)[ib * 2 + kb % 2] | 0xFFFFFFFF00000000ull;
+        const float key_scale = t.key_scale[ib * c.heads + h];
+        const int value_power = t.value_power[ib * c.heads + h];
         __syncthreads();                         // this block has landed, the other buffer is read
         if (kb + 1 < kb1) fetch(kb + 1, buf ^ 1);
-        const int key0 = kb * kImageKeys;
-        if (idle || key0 >= see_last.hi || key0 + kImageKeys <= see_first.lo) continue;
+        const int key0 = kb * BK;
+        if (idle || key0 >= see_last.hi || key0 + BK <= see_first.lo) continue;
         const int up = __builtin_amdgcn_readfirstlane(value_power);
         if (up > unit) {
             const float f = __builtin_ldexpf(1.0f, unit == kNoPower ? 0 : unit - up);
@@ -267,11 +273,11 @@ __global__ void __launch_bounds__(256, 2) attend_prompt_kernel(TileArgs t, int64
         // p is multiplied by 2^down, its sum back; where that is nothing beside the largest block, by no less than 2^-64
         const int fall = max(up - unit, -64);
         const float down = (float)fall, back = __builtin_ldexpf(1.0f, -fall);
-        const bool whole = there == ~0ull && key0 >= see_last.lo && key0 + kImageKeys <= see_first.hi;
-        const uint8_t* const kl = lds[buf] + hb * (kImageKeys * 16) + r * 16;
-        const uint8_t* const vl = lds[buf] + kImageKeys * D * 2 + hb * (D * 16) + r * 16;
+        const bool whole = there == ~0ull && key0 >= see_last.lo && key0 + BK <= see_first.hi;
+        const uint8_t* const kl = lds[buf] + hb * (BK * 16) + r * 16;
+        const uint8_t* const vl = lds[buf] + BK * D * 2 + hb * (D * 16) + r * 16;
 #pragma unroll 1
-        for (int kt = 0; kt < 2; ++kt) {
+        for (int kt = 0; kt < BK / 32; ++kt) {
             f32x16 s[RT];
 #pragma unroll
             for (int n = 0; n < RT; ++n)
@@ -279,7 +285,7 @@ __global__ void __launch_bounds__(256, 2) attend_prompt_kernel(TileArgs t, int64
                 for (int i = 0; i < 16; ++i) s[n][i] = 0.0f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                const u32x4 ka = *(const u32x4*)(kl + k * (2 * kImageKeys * 16) + kt * 512);
+                const u32x4 ka = *(const u32x4*)(kl + k * (2 * BK * 16) + kt * 512);
 #pragma unroll
                 for (int n = 0; n < RT; ++n) s[n] = mfma32(ka, q[n][k], s[n]);
             }
@@ -366,10 +372,10 @@ __global__ void __launch_bounds__(256, 2) attend_prompt_kernel(TileArgs t, int64
     }
 }
 
-template <int D>
-hipError_t launch_prompt_of(const AttendArgs& a, const KvPool& c, int dt, const AttendPlan& p, void* workspace,
-                            hipStream_t st) {
-    constexpr int RT = D <= 128 ? 2 : 1, R = 128 * RT;
+template <int D, int RT>
+hipError_t launch_prompt_rows(const AttendArgs& a, const KvPool& c, int dt, const AttendPlan& p, void* workspace,
+                              hipStream_t st) {
+    constexpr int R = 128 * RT, BK = prompt_keys(D, RT);
     char* const ws = (char*)workspace;
     TileArgs t{a, c, p.chunk, p.splits, (float*)(ws + p.part_at), nullptr, (uint8_t*)ws, (uint64_t*)(ws + p.present_at),
                (float*)(ws + p.present_at) + (int64_t)a.B * p.key_blocks * 2, nullptr, p.key_blocks};
@@ -377,7 +383,7 @@ hipError_t launch_prompt_of(const AttendArgs& a, const KvPool& c, int dt, const 
     t.part_ml = t.part_o + p.tiles * c.heads * p.splits * R * D;
     auto run = [&](auto dtc, auto mode) -> hipError_t {
         constexpr int DT = decltype(dtc)::value, M = decltype(mode)::value;
-        attend_lay_kernel<DT, M, D><<<(unsigned)((int64_t)a.B * p.key_blocks * c.heads), 256, 0, st>>>(t, (uint8_t*)ws);
+        attend_lay_kernel<DT, M, D, BK><<<(unsigned)((int64_t)a.B * p.key_blocks * c.heads), 256, 0, st>>>(t, (uint8_t*)ws);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         attend_prompt_kernel<DT, D, RT><<<(unsigned)(p.tiles * c.heads * p.splits), 256, 0, st>>>(t, p.tiles);
@@ -391,6 +397,14 @@ hipError_t launch_prompt_of(const AttendArgs& a, const KvPool& c, int dt, const 
         return run(dtc, std::integral_constant<int, AFFINE>{});
     };
     return dt == QLIN_BF16 ? moded(std::integral_constant<int, QLIN_BF16>{}) : moded(std::integral_constant<int, QLIN_F16>{});
+}
+
+template <int D>
+hipError_t launch_prompt_of(const AttendArgs& a, const KvPool& c, int dt, const AttendPlan& p, void* workspace,
+                            hipStream_t st) {
+    if constexpr (D <= 128)
+        if (p.rows == 256) return launch_prompt_rows<D, 2>(a, c, dt, p, workspace, st);
+    return p.rows == 128 ? launch_prompt_rows<D, 1>(a, c, dt, p, workspace, st) : hipErrorInvalidValue;
 }
 
 }  // namespace

@@ -33,7 +33,6 @@
 namespace qlin {
 namespace {
 
-constexpr int WAVES = 4;                        // of a workgroup
 constexpr int kStep = 32;                       // keys of a wave's step
 constexpr int kWindow = 4096;                   // keys whose pages are looked up at once
 constexpr int kScaleRow = kStep + 4;            // floats of a group's scales of a step in LDS: rows on other banks
@@ -146,6 +145,9 @@ struct TileShape {
     static constexpr int R = PER * NT;
 };
 
+// Waves of a workgroup: two workgroups' rings of loads fit a CU's LDS.
+constexpr int tile_waves(int D) { return D == 256 ? 3 : 4; }
+
 // Waves of a SIMD: what o and q leave of the registers. Measured (64 x 8192 to
 // 32768 keys, D 128): 2 waves 310 us, 3 waves 284 us.
 constexpr int tile_residents(int D, int NT) {
@@ -153,9 +155,10 @@ constexpr int tile_residents(int D, int NT) {
 }
 
 // GQ: a quant group's words over 4 (AFFINE 32/64/128: 1/2/4; MXFP4: 1; NVFP4: unused)
-// PS: values stay codes, see the top (AFFINE, at most two groups).
+// PS: values stay codes, see the top (AFFINE, at most four groups).
 template <int DT, int MODE, int D, int GQ, int NT, bool PS>
-__global__ void __launch_bounds__(256, tile_residents(D, NT)) attend_tile_kernel(TileArgs t) {
+__global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) attend_tile_kernel(TileArgs t) {
+    constexpr int WAVES = tile_waves(D);
     using S = TileShape<DT, MODE, D, GQ, NT, PS>;
     constexpr int HW = D / 8;                              // words of a head's row
     constexpr int NM = D / 32;                             // MFMAs along D for 16 keys
@@ -164,7 +167,7 @@ __global__ void __launch_bounds__(256, tile_residents(D, NT)) attend_tile_kernel
     constexpr int VC = (HW + 15) / 16;                     // words of a value a lane takes
     constexpr int CL = HALF ? 4 : 8, OT = VC * CL;         // codes of a word it takes; tiles of o
     constexpr bool AFF = MODE == AFFINE;
-    static_assert(!PS || (AFF && NG <= 2 && DT == QLIN_BF16), "values as codes");
+    static_assert(!PS || (AFF && NG <= 4 && DT == QLIN_BF16), "values as codes");
     constexpr int ARR = AFF ? 4 : 2;                       // scale arrays of a step: keys', values', biases in the same order
     constexpr int WSCALES = ARR * NG * kScaleRow;          // a wave's scales as numbers
     constexpr int CH = D / 32;                             // 16-byte chunks of a head's row
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(256, tile_residents(D, NT)) attend_tile_kernel
     constexpr int ROOM = (tile_residents(D, NT) == 3 ? 52 : 78) * 1024 - WAVES * WSCALES * 4;
     constexpr int ST = WAVES * 4 * STAGE <= ROOM ? 4 : (WAVES * 3 * STAGE <= ROOM ? 3 : 2);
     constexpr int ROW = D + 4;                             // floats of a row of o in LDS, rows on other banks
-    constexpr int REGIONS = WAVES * R * ROW * 4 <= 72 * 1024 ? WAVES : (4 * R * ROW * 4 <= 72 * 1024 ? 4 : 1);
+    constexpr int REGIONS = WAVES * R * ROW * 4 <= 72 * 1024 ? WAVES : 1;
     constexpr int RING = WAVES * ST * STAGE, BUF = RING > REGIONS * R * ROW * 4 ? RING : REGIONS * R * ROW * 4;
     __shared__ int32_t blocks[kWindow / kKvUnit];
     __shared__ __attribute__((aligned(16))) uint8_t ring[BUF];
@@ -485,8 +488,9 @@ __global__ void __launch_bounds__(256, tile_residents(D, NT)) attend_tile_kernel
                     l[n] += x[e];
                 }
                 if constexpr (PS) {                          // p times the scales of the column's group; the biases' part
-                    const float* const vs = sl + (NG + r / PER) * kScaleRow + 4 * j;
-                    const float* const vz = sl + (3 * NG + r / PER) * kScaleRow + 4 * j;
+                    const int group = min(r / PER, NG - 1);
+                    const float* const vs = sl + (NG + group) * kScaleRow + 4 * j;
+                    const float* const vz = sl + (3 * NG + group) * kScaleRow + 4 * j;
 #pragma unroll
                     for (int st = 0; st < 2; ++st) {
                         const f32x4 s = *(const f32x4*)(vs + 16 * st), z = *(const f32x4*)(vz + 16 * st);
@@ -675,10 +679,10 @@ hipError_t launch_tile_of(const AttendArgs& a, const KvPool& c, int dt, const At
         if constexpr (M == AFFINE && D % (32 * GQ) != 0) {
             return hipErrorInvalidValue;
         } else {
-            constexpr bool CAN = M == AFFINE && DT == QLIN_BF16 && D / (32 * GQ) <= 2;     // as the plan has it
+            constexpr bool CAN = M == AFFINE && DT == QLIN_BF16 && D / (32 * GQ) <= 4;     // as the plan has it
             
             auto go = [&](auto ntc, auto psc) {
-                attend_tile_kernel<DT, M, D, GQ, decltype(ntc)::value, decltype(psc)::value><<<grid, 256, 0, st>>>(t);
+                attend_tile_kernel<DT, M, D, GQ, decltype(ntc)::value, decltype(psc)::value><<<grid, 64 * tile_waves(D), 0, st>>>(t);
             };
             constexpr bool ALL = CAN && D == 32 * GQ;               // a single group: codes for any number of rows
             auto sized = [&](auto ntc) -> hipError_t {
@@ -691,9 +695,11 @@ hipError_t launch_tile_of(const AttendArgs& a, const KvPool& c, int dt, const At
             };
             hipError_t e;
             if (p.nt == 1) e = sized(std::integral_constant<int, 1>{});
-            else if (p.nt == 2) e = sized(std::integral_constant<int, 2>{});
-            else if constexpr (D == 64) e = sized(std::integral_constant<int, 3>{});
-            else e = hipErrorInvalidValue;
+            else if constexpr (D <= 128) {
+                if (p.nt == 2) e = sized(std::integral_constant<int, 2>{});
+                else if constexpr (D == 64) e = sized(std::integral_constant<int, 3>{});
+                else e = hipErrorInvalidValue;
+            } else e = hipErrorInvalidValue;
             if (e != hipSuccess || p.splits == 1) return e;
             return launch_join<DT, D>(t, p.tiles, p.rows, kKvUnit, st);
         }
