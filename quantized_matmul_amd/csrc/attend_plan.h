@@ -31,7 +31,8 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
     constexpr int64_t kImages = 1LL << 33;   // bytes of decoded keys and values at most
     constexpr int64_t kItems = (1LL << 32) - 1024;     // work-items of a launch
     AttendPlan p{};
-    const int64_t share = q_heads / c.heads, held = width * c.page;
+    const int64_t share = q_heads / c.heads;
+    const int64_t held = width > kKvMaxKeys / c.page ? kKvMaxKeys : width * c.page;
     const bool sized = c.D == 64 || c.D == 96 || c.D == 128 || c.D == 192 || c.D == 256;
     if (dt == QLIN_F32 || !sized) {
         p.fits = T * q_heads <= kItems / 64;
@@ -50,7 +51,8 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
         p.rows = c.D <= 128 && (T * share / 256 + B) * c.heads >= 512 ? 256 : 128;
         p.tiles = T * share / p.rows + B;
         const int64_t base = p.tiles * c.heads, fit = p.rows == 128 && c.D <= 128 ? 768 : 512;
-        int64_t splits = (fit + base - 1) / base;
+        // keys are split only to fill the chip: each chunk's o goes through the memory twice
+        const int64_t splits = base < fit ? fit / base : 1;
         int64_t chunk = ((keys + splits - 1) / splits + 255) / 256 * 256;
         if (splits == 1) chunk = 1 << 30;
         p.chunk = (int)(chunk < (1 << 30) ? chunk : 1 << 30);
@@ -64,7 +66,8 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
     }
     p.path = 1;
     const int groups = c.mode == 0 && dt == QLIN_BF16 ? c.D / c.g : 0;
-    p.codes = groups == 1 || (groups >= 2 && groups <= 4 && mean <= 16 / groups);
+    // (four groups of D 128 take more columns than they save: 124 us decoded, 137 as codes; of D 256 142 and 116)
+    p.codes = groups == 1 || (groups >= 2 && (groups <= 3 || (groups == 4 && c.D == 256)) && mean <= 16 / groups);
     const int dup = p.codes ? groups : 1;
     p.nt = mean > 16 && c.D <= 128 ? 2 : 1;
     if (c.D == 64 && mean > 32) p.nt = 3;                    // (what the registers hold)

@@ -679,7 +679,8 @@ hipError_t launch_tile_of(const AttendArgs& a, const KvPool& c, int dt, const At
         if constexpr (M == AFFINE && D % (32 * GQ) != 0) {
             return hipErrorInvalidValue;
         } else {
-            constexpr bool CAN = M == AFFINE && DT == QLIN_BF16 && D / (32 * GQ) <= 4;     // as the plan has it
+            constexpr int GROUPS = D / (32 * GQ);
+            constexpr bool CAN = M == AFFINE && DT == QLIN_BF16 && (GROUPS <= 3 || (GROUPS == 4 && D == 256));   // as the plan has it
             
             auto go = [&](auto ntc, auto psc) {
                 attend_tile_kernel<DT, M, D, GQ, decltype(ntc)::value, decltype(psc)::value><<<grid, 64 * tile_waves(D), 0, st>>>(t);

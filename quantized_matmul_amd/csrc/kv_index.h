@@ -27,6 +27,7 @@ struct KvPool {
 };
 
 constexpr int kKvUnit = 16;      // rows of a page come in runs of this many
+constexpr int64_t kKvMaxKeys = 0x7FFFFF00;   // of a sequence: key numbers and those of a block past them fit an int
 
 // Pages [0, pages) exist: the row block (row number over 16) of head h where
 // key block `block` (its keys over 16) of a sequence lies, or -1 where its page
@@ -84,7 +85,7 @@ QLIN_HD void rows_of(const AttendArgs& a, int b, Sequence& s) {
     s.n = (int)(end - s.first);
 }
 QLIN_HD int keys_of(const AttendArgs& a, const KvPool& c, int b) {
-    const int64_t held = (int64_t)a.width * c.page, most = held < 0x7FFFFFF0LL ? held : 0x7FFFFFF0LL;
+    const int64_t held = (int64_t)a.width * c.page, most = held < kKvMaxKeys ? held : kKvMaxKeys;
     const int64_t k = a.lengths[b];
     return (int)(k < 0 ? 0 : (k > most ? most : k));
 }
