@@ -27,6 +27,8 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
     constexpr int64_t kStepKeys = 128;       // keys that the four waves of a workgroup take at a time
     constexpr int64_t kChunkMost = 4096;     // keys a workgroup takes, where that makes no more than kMany of them
     constexpr int64_t kMany = 32768;
+    // keys that one workgroup takes sooner than a second launch joins several (500 keys 8.6 us, joined 9.2; 800 11.1 and 9.7)
+    constexpr int64_t kOneChunk = 640;
     constexpr int64_t kPromptRows = 64;      // rows of a sequence and key head, on average, from which a prompt is one
     constexpr int64_t kImages = 1LL << 33;   // bytes of decoded keys and values at most
     constexpr int64_t kItems = (1LL << 32) - 1024;     // work-items of a launch
@@ -77,7 +79,7 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
     // as many workgroups as fit the chip at once (twice as many where two fit a CU). Measured with 768, 1024 and 2048,
     // D 128, us: 16 x 6000 keys 26.7, 31.1, 33.8; 16000 keys 15.2, 19.6, 19.4; drafts of two a CU 30.8, 28.7, 32.1
     const int64_t fit = p.nt == 1 && c.D <= 128 ? 768 : 1024;
-    int64_t splits = (fit + base - 1) / base;
+    int64_t splits = keys <= kOneChunk ? 1 : (fit + base - 1) / base;
     int64_t chunk = ((keys + splits - 1) / splits + kStepKeys - 1) / kStepKeys * kStepKeys;
     if (chunk > kChunkMost) chunk = kChunkMost;
     while (chunk < keys && base * (keys / chunk) > kMany) chunk *= 2;
