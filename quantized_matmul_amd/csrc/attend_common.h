@@ -41,6 +41,9 @@ __device__ __forceinline__ float scale_at(const void* p, int64_t i) {
     else return e8m0_to_f32(((const uint8_t*)p)[i]);
 }
 
+// floor(log2 |x|) of a finite number other than zero.
+__device__ __forceinline__ int ilogb_of(float x) { return __builtin_amdgcn_frexp_expf(x) - 1; }
+
 // Two numbers rounded to nearest even.
 template <int DT>
 __device__ __forceinline__ uint32_t round2(float a, float b) {

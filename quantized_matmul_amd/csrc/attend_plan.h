@@ -22,6 +22,10 @@ struct AttendPlan {
     bool fits;                       // one launch holds it
 };
 
+// Workgroups of the row tiles that a CU holds (waves of a SIMD, what o and q leave
+// of the registers; rings of loads, what fits LDS).
+constexpr int tile_residents(int D, int NT) { return D * NT <= 128 ? 3 : (D * NT <= 256 ? 2 : 1); }
+
 inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t width, const KvPool& c, int64_t window,
                               bool one_row) {
     constexpr int64_t kStepKeys = 128;       // keys that the four waves of a workgroup take at a time
@@ -29,7 +33,11 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
     constexpr int64_t kMany = 32768;
     // keys that one workgroup takes sooner than a second launch joins several (500 keys 8.6 us, joined 9.2; 800 11.1 and 9.7)
     constexpr int64_t kOneChunk = 640;
-    constexpr int64_t kPromptRows = 64;      // rows of a sequence and key head, on average, from which a prompt is one
+    constexpr int64_t kStart = 768;          // keys that a workgroup could take in the time of its start and end
+    // Rows of a sequence and key head, on average, above which a prompt is one: below, the launch that lays the keys out
+    // costs more than it saves. us, row tiles and prompts, D 128: 256 rows over 16000 keys 62 and 75, 64 sequences of
+    // them 1720 and 2390; 768 rows 141 and 117. D 256: 96 rows 79 and 95, 256 rows 148 and 122.
+    const int64_t kPromptRows = c.D <= 128 ? 512 : 192;
     constexpr int64_t kImages = 1LL << 33;   // bytes of decoded keys and values at most
     constexpr int64_t kItems = (1LL << 32) - 1024;     // work-items of a launch
     AttendPlan p{};
@@ -71,16 +79,28 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
     // (four groups of D 128 take more columns than they save: 124 us decoded, 137 as codes; of D 256 142 and 116)
     p.codes = groups == 1 || (groups >= 2 && (groups <= 3 || (groups == 4 && c.D == 256)) && mean <= 16 / groups);
     const int dup = p.codes ? groups : 1;
+    // 32 columns where the rows fill more than 16, as the codes are decoded once for them: 64 sequences of 64 rows over
+    // 16000 keys, D 128, 583 us, in tiles of 16 rows 666 (48 columns, of D 64, took 424 for 384)
     p.nt = mean > 16 && c.D <= 128 ? 2 : 1;
-    if (c.D == 64 && mean > 32) p.nt = 3;                    // (what the registers hold)
     p.rows = 16 / dup * p.nt;
     p.tiles = one_row ? B * ((share + p.rows - 1) / p.rows) : T * share / p.rows + B;
     const int64_t base = p.tiles * c.heads;
-    // as many workgroups as fit the chip at once (twice as many where two fit a CU). Measured with 768, 1024 and 2048,
-    // D 128, us: 16 x 6000 keys 26.7, 31.1, 33.8; 16000 keys 15.2, 19.6, 19.4; drafts of two a CU 30.8, 28.7, 32.1
-    const int64_t fit = p.nt == 1 && c.D <= 128 ? 768 : 1024;
-    int64_t splits = keys <= kOneChunk ? 1 : (fit + base - 1) / base;
-    int64_t chunk = ((keys + splits - 1) / splits + kStepKeys - 1) / kStepKeys * kStepKeys;
+    // Chunks for one to four rounds of the workgroups that the chip holds at once, never a little more than a round,
+    // whichever should end first: rounds by the length of a chunk, and a last chunk that starts when all the others are
+    // done, as lengths differ. bf16, D 128, us: 32 sequences of 4000 to 16000 keys, always 768 workgroups 111, so 89;
+    // 16 sequences of 1 to 5 rows of 32 heads over those keys 124, so 95; 5 sequences of 1 to 3 rows over 2000 to 8000
+    // keys 26 and 26.
+    const int64_t slots = 256 * tile_residents(c.D, p.nt);
+    const int64_t even = B * ((mean + p.rows - 1) / p.rows), ragged = T * share / p.rows + B / 2;
+    const int64_t busy = (one_row ? p.tiles : (even > ragged ? even : ragged)) * c.heads;
+    int64_t chunk = keys;
+    double best = 0;
+    for (int64_t r = 1; keys > kOneChunk && r <= 4; ++r) {
+        const int64_t s = r * slots / busy > 1 ? r * slots / busy : 1;
+        const int64_t size = ((keys + s - 1) / s + kStepKeys - 1) / kStepKeys * kStepKeys;
+        const double time = ((double)busy * (double)s + (double)slots) * (double)(size + kStart);
+        if (r == 1 || time < best) best = time, chunk = size;
+    }
     if (chunk > kChunkMost) chunk = kChunkMost;
     while (chunk < keys && base * (keys / chunk) > kMany) chunk *= 2;
     if (chunk >= keys) chunk = 1 << 30;

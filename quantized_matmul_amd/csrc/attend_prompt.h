@@ -46,9 +46,6 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// floor(log2 |x|) of a finite number other than zero.
-__device__ __forceinline__ int ilogb_of(float x) { return __builtin_amdgcn_frexp_expf(x) - 1; }
-
 template <int MODE>
 __device__ __forceinline__ void word_values(uint32_t w, float s, float z, float (&v)[8]) {
     if constexpr (MODE == AFFINE) {

@@ -1,29 +1,54 @@
 // attend_tile.h -- attention over the 4-bit cache on the matrix cores, for the
 // rows of q that share few keys' reads: decode and drafted tokens. One head
-// size a translation unit (attend_tile_*.hip).
+// size a translation unit (attend_64.hip and its neighbours).
 //
 // A sequence's rows of one key head (n tokens by q_heads / heads query heads)
-// form tiles of 16 NT rows; a workgroup takes a tile and `chunk` keys, its four
-// waves every fourth step of 32 keys, each with its own running maximum m, sum l
-// and o (o = sum of p v, p = exp2(score - m)), joined through LDS at the end.
-// Workgroups of other chunks of the same rows leave o, m and l in the workspace
-// and attend_join adds them up.
+// form tiles; a workgroup takes a tile and `chunk` keys, its four waves (three
+// where D is 256) every fourth step of 32 keys, each with its own running maximum
+// m, sum l and o (o = sum of p v, p = exp2(score - m)), joined through LDS at the
+// end. Workgroups of other chunks of the same rows leave o, m and l in the
+// workspace and attend_join adds them up.
 //
-// Everything of a step stays in registers, no key or value passes through LDS:
-//   scores^T = K q^T: lane (r = lane % 16, j = lane / 16) of an A operand holds
-//     key r's codes, eight of them a word as they lie in memory; q's operand has
-//     its values in the same order. Keys stay codes: affine ones become 16 + c
-//     (bf16) by a shift and one and-or for two of them, and scale and bias join
-//     in fp32: score = s acc + (z - 16 s) sum(q).
-//   o^T = V^T p^T: the scores leave the matrix cores as p's operand wants them
-//     (lane (q row, j) has keys 4j..4j+3 of both sub-tiles), so lane (r, j) of V's
-//     operand takes word r of those eight keys: its eight codes are eight rows of
-//     V^T, decoded in fp32 and rounded in pairs of keys.
-// Scales and biases go through LDS once, as numbers (a lane there needs those of
-// eight keys); keys outside the sequence get zeros there, whatever their page holds.
+// Loads. Codes and scales go from memory straight into a ring of a wave's own in
+// LDS, one to three steps ahead, without a barrier: a wave waits for the count of
+// its own loads alone. What is ahead costs no registers that way, so that three
+// workgroups fit a CU: 64 x 8192 to 32768 keys, D 128, loads into registers 363
+// us, through the ring 344, three workgroups 294 (two 310).
+//
+// Products, 16 x 16 x 32:
+//   scores^T = K q^T. Lane (r = lane % 16, j = lane / 16) of K's operand holds
+//     eight codes of key r, a word as it lies in memory; q's operand has its values
+//     in the same order. Keys stay codes, and scales join in fp32. Affine codes
+//     become 16 + c by a shift and one and-or for two of them (a nibble put at the
+//     top of the mantissa of 16), which the bias makes up for: score = s acc +
+//     (z - 16 s) sum(q). E2M1 codes are the hardware's conversion; nvfp4's groups
+//     of 16 are shorter than the product's 32, so its codes take their scale
+//     before, in f16, which holds every product of the two exactly.
+//   o^T = V^T p^T. The scores leave the matrix cores as p's operand wants them
+//     (lane (q row, j) has keys 4j..4j+3 of both halves of the step), so lane
+//     (r, j) of V's operand takes word r of those eight keys: its eight codes are
+//     eight rows of V^T. Two ways to make them numbers:
+//     - decoded: fl(s c + z), rounded to the type (f16 by packed instructions, two
+//       keys each; bf16 in fp32 and rounded in pairs).
+//     - as codes (PS; bf16 affine): p takes the scale and the codes stay 16 + c,
+//       2.5 instructions a pair instead of 4 and more. A column of p belongs to a
+//       single group then, so a row of q has as many columns as a row has groups
+//       (DUP), and 16 columns hold 16 / groups rows. What is left of each value is
+//       z + 8 s (summed in fp32) and 8 s too many of 16 + c - 8, taken off at the
+//       end as 24 times the sum of the rounded p s, which a product with ones
+//       gives: what p s lost by rounding multiplies c - 8, not 16 + c.
+//       64 x 8192 to 32768 keys, D 128, groups of 64: 335 us decoded, 293 as codes.
+//   Rounded on the way: p (or p s) and decoded values to the type, half a step
+//   each; nvfp4's p to f16. Sums, m and l are fp32.
+//
+// Scales go through LDS a second time, as numbers (a lane there needs those of
+// eight keys); keys outside the sequence get zeros there, whatever their page
+// holds, and the lowest score.
 //
 // Bound by the memory: D/2 bytes and the scales of a key and of a value, read
-// once for the tile's rows.
+// once for the tile's rows. 64 sequences of 8192 to 32768 keys (D 128, 8 heads,
+// groups of 64) are 1.48 GB, 293 us with the join: 5.1 TB/s of the 6.2 that a
+// plain read reaches; the vector units are busy for three quarters of that time.
 #pragma once
 
 #include <type_traits>
@@ -58,6 +83,17 @@ __device__ __forceinline__ u32x4 code_operand(uint32_t w) {
                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1)),
                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2)),
                      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3))};
+}
+
+// A number twice, and the four pairs of an operand times it.
+__device__ __forceinline__ f16x2 both(float s) { return f16x2{(_Float16)s, (_Float16)s}; }
+__device__ __forceinline__ u32x4 times(u32x4 a, f16x2 s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t pair = a[i];                          // (a bit cast of the element itself reads the first)
+        a[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, pair) * s);
+    }
+    return a;
 }
 
 // Largest (sum) over the four lanes l, l ^ 16, l ^ 32, l ^ 48.
@@ -148,12 +184,6 @@ struct TileShape {
 // Waves of a workgroup: two workgroups' rings of loads fit a CU's LDS.
 constexpr int tile_waves(int D) { return D == 256 ? 3 : 4; }
 
-// Waves of a SIMD: what o and q leave of the registers. Measured (64 x 8192 to
-// 32768 keys, D 128): 2 waves 310 us, 3 waves 284 us.
-constexpr int tile_residents(int D, int NT) {
-    return NT == 1 && D <= 128 ? 3 : (D * NT <= 256 ? 2 : 1);
-}
-
 // GQ: a quant group's words over 4 (AFFINE 32/64/128: 1/2/4; MXFP4: 1; NVFP4: unused)
 // PS: values stay codes, see the top (AFFINE, at most four groups).
 template <int DT, int MODE, int D, int GQ, int NT, bool PS>
@@ -167,6 +197,7 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
     constexpr int VC = (HW + 15) / 16;                     // words of a value a lane takes
     constexpr int CL = HALF ? 4 : 8, OT = VC * CL;         // codes of a word it takes; tiles of o
     constexpr bool AFF = MODE == AFFINE;
+    constexpr int MT = MODE == NVFP4 ? (int)QLIN_F16 : DT; // type of the matrix cores' operands: all of nvfp4 fits f16
     static_assert(!PS || (AFF && NG <= 4 && DT == QLIN_BF16), "values as codes");
     constexpr int ARR = AFF ? 4 : 2;                       // scale arrays of a step: keys', values', biases in the same order
     constexpr int WSCALES = ARR * NG * kScaleRow;          // a wave's scales as numbers
@@ -242,7 +273,10 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
     for (int n = 0; n < NT; ++n) seen[n] = seen_by(a, w.s, at_row[n]);
 
     f32x4 o[NT][OT], ones[NT];
-    float m[NT], l[NT], zsum[NT], base[NT];                // base: m, or 0 while there is none
+    // p = exp2(score - base), base being m + kUnder, or 0 while there is no m. kUnder keeps sums of bf16's largest values
+    // inside fp32; f16, whose values cannot leave it, has no bits to give for that.
+    constexpr float kUnder = MT == QLIN_BF16 ? kSlack : 0.0f;
+    float m[NT], l[NT], zsum[NT], base[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         m[n] = kNone;
@@ -343,6 +377,30 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
             }
     }
 
+    float scale_of[NT];                                      // of scores of these operands
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        scale_of[n] = scale;
+        if constexpr (MODE == NVFP4 && DT == QLIN_BF16) {    // a row as f16 in a power of two of its largest value,
+            // which holds all but what is below 2^-17 of that, and that to 2^-25 of it
+            uint32_t most = 0;
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) most = max(most, max(q[n][m][i] & 0x7FFFu, q[n][m][i] >> 16 & 0x7FFFu));
+            most = max(most, (uint32_t)__shfl_xor((int)most, 16, 64));
+            most = max(most, (uint32_t)__shfl_xor((int)most, 32, 64));
+            const int e = most ? ilogb_of(bf16_bits_to_f32(most)) : 0;
+            scale_of[n] = __builtin_ldexpf(scale, e);
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    q[n][m][i] = round2<QLIN_F16>(__builtin_ldexpf(bf16_bits_to_f32(q[n][m][i] & 0xFFFFu), -e),
+                                                  __builtin_ldexpf(bf16_bits_to_f32(q[n][m][i] >> 16), -e));
+        }
+    }
+
     for (int first = 0; first < steps; first += kWindow / kStep) {
         const int n_steps = min(steps - first, kWindow / kStep);
         if (first) {                                         // another window: its row blocks take the place of the last ones
@@ -399,13 +457,11 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
                     for (int n = 0; n < NT; ++n) sc[n][st] = f32x4{0, 0, 0, 0};
 #pragma unroll
                     for (int i = 0; i < NM; ++i) {
-                        // the word's group is not its MFMA's only one: its codes take their scale here, exact in both types
-                        const float s = sl[(2 * i + j / 2) * kScaleRow + st * 16 + r];
-                        float v[8];
-                        e2m1_values(*(const uint32_t*)(in + word_at(st, 0, r, i * 4 + j)), s, v);
-                        const u32x4 k{round2<DT>(v[0], v[1]), round2<DT>(v[2], v[3]), round2<DT>(v[4], v[5]), round2<DT>(v[6], v[7])};
+                        // the word's group is not its MFMA's only one: its codes take their scale here, exact in f16
+                        const f16x2 s = both(sl[(2 * i + j / 2) * kScaleRow + st * 16 + r]);
+                        const u32x4 k = times(code_operand<QLIN_F16>(*(const uint32_t*)(in + word_at(st, 0, r, i * 4 + j))), s);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) sc[n][st] = mfma16<DT>(k, q[n][i], sc[n][st]);
+                        for (int n = 0; n < NT; ++n) sc[n][st] = mfma16<MT>(k, q[n][i], sc[n][st]);
                     }
                 } else {
 #pragma unroll
@@ -454,7 +510,7 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
                 float x[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    x[e] = MODE == NVFP4 ? __builtin_fmaf(sc[n][e / 4][e % 4], scale, -base[n]) : sc[n][e / 4][e % 4];
+                    x[e] = MODE == NVFP4 ? __builtin_fmaf(sc[n][e / 4][e % 4], scale_of[n], -base[n]) : sc[n][e / 4][e % 4];
                 if (!whole) {
                     out_of_line();
 #pragma unroll
@@ -466,10 +522,10 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
                 float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
                 top = across_max(top);
                 // the maximum follows where a score passes it by 2^8, or the first number comes
-                if (__any(top > (m[n] == kNone ? kNone : kSlack))) {
+                if (__any(top > (m[n] == kNone ? kNone : kSlack - kUnder))) {
                     out_of_line();
                     const float to = fmaxf(top + base[n], m[n]), f = m[n] == kNone ? 0.0f : __builtin_amdgcn_exp2f(m[n] - to);
-                    const float more = to == kNone ? 0.0f : to - base[n];
+                    const float more = to == kNone ? 0.0f : to + kUnder - base[n];
                     m[n] = to;
                     base[n] += more;
 #pragma unroll
@@ -502,7 +558,7 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[n][i] = round2<DT>(x[2 * i], x[2 * i + 1]);
+                for (int i = 0; i < 4; ++i) p[n][i] = round2<MT>(x[2 * i], x[2 * i + 1]);
                 if constexpr (PS) ones[n] = mfma16<DT>(u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}, p[n], ones[n]);
             }
             // values: word v*16 + r of the lane's eight keys
@@ -538,30 +594,89 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
                     if constexpr (AFF) {
                         const f32x4 z0 = *(const f32x4*)(sl + (3 * NG + g) * kScaleRow + 4 * j);
                         const f32x4 z1 = *(const f32x4*)(sl + (3 * NG + g) * kScaleRow + 16 + 4 * j);
-                        uint32_t code[8][2];
+                        if constexpr (DT == QLIN_F16) {        // fl(s c + z) by packed instructions, two keys each
+                            f16x2 s2[4], z2[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const uint32_t w4 = HALF ? vw[e][v] >> (16 * (r & 1)) : vw[e][v];
-                            code[e][0] = vector_bits(w4 & 0x0F0F0F0Fu);
-                            code[e][1] = vector_bits((w4 >> 4) & 0x0F0F0F0Fu);
+                            for (int e = 0; e < 4; ++e) {
+                                s2[e] = __builtin_convertvector((e < 2 ? f32x2{s0[2 * e], s0[2 * e + 1]} : f32x2{s1[2 * e - 4], s1[2 * e - 3]}), f16x2);
+                                z2[e] = __builtin_convertvector((e < 2 ? f32x2{z0[2 * e], z0[2 * e + 1]} : f32x2{z1[2 * e - 4], z1[2 * e - 3]}), f16x2);
+                            }
+                            auto four = [&](uint32_t halves, int to) {
+                                uint32_t x[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) x[e] = __builtin_amdgcn_perm(vw[2 * e + 1][v], vw[2 * e][v], halves);
+                                auto one = [&](auto ic) {
+                                    constexpr int I = decltype(ic)::value;
+                                    u32x4 vt;
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const f16x2 c2 = __builtin_bit_cast(f16x2, sixteen_plus<DT, I>(x[e], mask, sixteen)) - (f16x2){16, 16};
+                                        vt[e] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c2, s2[e], z2[e]));
+                                    }
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n) o[n][v * CL + to + I] = mfma16<MT>(vt, p[n], o[n][v * CL + to + I]);
+                                };
+                                one(std::integral_constant<int, 0>{});
+                                one(std::integral_constant<int, 1>{});
+                                one(std::integral_constant<int, 2>{});
+                                one(std::integral_constant<int, 3>{});
+                            };
+                            if constexpr (HALF) {
+                                four(r & 1 ? 0x07060302u : 0x05040100u, 0);
+                            } else {
+                                four(0x05040100u, 0);
+                                four(0x07060302u, 4);
+                            }
+                        } else {
+                            uint32_t code[8][2];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const uint32_t w4 = HALF ? vw[e][v] >> (16 * (r & 1)) : vw[e][v];
+                                code[e][0] = vector_bits(w4 & 0x0F0F0F0Fu);
+                                code[e][1] = vector_bits((w4 >> 4) & 0x0F0F0F0Fu);
+                            }
+#pragma unroll
+                            for (int i = 0; i < CL; ++i) {
+                                float x[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    x[e] = __builtin_fmaf(e < 4 ? s0[e & 3] : s1[e & 3], (float)((code[e][i & 1] >> (i / 2 * 8)) & 0xFFu),
+                                                          e < 4 ? z0[e & 3] : z1[e & 3]);
+                                const u32x4 vt{round2<DT>(x[0], x[1]), round2<DT>(x[2], x[3]), round2<DT>(x[4], x[5]), round2<DT>(x[6], x[7])};
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) o[n][v * CL + i] = mfma16<DT>(vt, p[n], o[n][v * CL + i]);
+                            }
                         }
+                    } else if constexpr (MODE == NVFP4) {     // exact in f16; pairs of values to pairs of keys
 #pragma unroll
-                        for (int i = 0; i < CL; ++i) {
-                            float x[8];
+                        for (int half = 0; half < CL / 4; ++half) {
+                            u32x4 vt[4];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                x[e] = __builtin_fmaf(e < 4 ? s0[e & 3] : s1[e & 3], (float)((code[e][i & 1] >> (i / 2 * 8)) & 0xFFu),
-                                                      e < 4 ? z0[e & 3] : z1[e & 3]);
-                            const u32x4 vt{round2<DT>(x[0], x[1]), round2<DT>(x[2], x[3]), round2<DT>(x[4], x[5]), round2<DT>(x[6], x[7])};
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t pair[2][2];
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) o[n][v * CL + i] = mfma16<DT>(vt, p[n], o[n][v * CL + i]);
+                                for (int k = 0; k < 2; ++k) {
+                                    const int key = 2 * e + k;
+                                    const uint32_t w4 = HALF ? vw[key][v] >> (16 * (r & 1)) : vw[key][v] >> (16 * half);
+                                    const f16x2 s = both(key < 4 ? s0[key & 3] : s1[key & 3]);
+                                    pair[k][0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w4, 1.0f, 0) * s);
+                                    pair[k][1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w4, 1.0f, 1) * s);
+                                }
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    vt[i][e] = __builtin_amdgcn_perm(pair[1][i / 2], pair[0][i / 2], i & 1 ? 0x07060302u : 0x05040100u);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+                                    o[n][v * CL + half * 4 + i] = mfma16<MT>(vt[i], p[n], o[n][v * CL + half * 4 + i]);
                         }
                     } else {
                         float x[8][8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            e2m1_values<MODE == MXFP4>(HALF ? vw[e][v] >> (16 * (r & 1)) : vw[e][v], e < 4 ? s0[e & 3] : s1[e & 3],
-                                                       x[e]);
+                            e2m1_values<true>(HALF ? vw[e][v] >> (16 * (r & 1)) : vw[e][v], e < 4 ? s0[e & 3] : s1[e & 3], x[e]);
 #pragma unroll
                         for (int i = 0; i < CL; ++i) {
                             const u32x4 vt{round2<DT>(x[0][i], x[1][i]), round2<DT>(x[2][i], x[3][i]),
@@ -681,7 +796,6 @@ hipError_t launch_tile_of(const AttendArgs& a, const KvPool& c, int dt, const At
         } else {
             constexpr int GROUPS = D / (32 * GQ);
             constexpr bool CAN = M == AFFINE && DT == QLIN_BF16 && (GROUPS <= 3 || (GROUPS == 4 && D == 256));   // as the plan has it
-            
             auto go = [&](auto ntc, auto psc) {
                 attend_tile_kernel<DT, M, D, GQ, decltype(ntc)::value, decltype(psc)::value><<<grid, 64 * tile_waves(D), 0, st>>>(t);
             };
@@ -692,14 +806,13 @@ hipError_t launch_tile_of(const AttendArgs& a, const KvPool& c, int dt, const At
                 if (p.codes && !PS) return hipErrorInvalidValue;
                 if (PS && p.codes) go(ntc, std::integral_constant<bool, PS>{});
                 else if constexpr (!ALL) go(ntc, std::false_type{});
+                else return hipErrorInvalidValue;
                 return hipGetLastError();
             };
             hipError_t e;
             if (p.nt == 1) e = sized(std::integral_constant<int, 1>{});
             else if constexpr (D <= 128) {
-                if (p.nt == 2) e = sized(std::integral_constant<int, 2>{});
-                else if constexpr (D == 64) e = sized(std::integral_constant<int, 3>{});
-                else e = hipErrorInvalidValue;
+                e = p.nt == 2 ? sized(std::integral_constant<int, 2>{}) : hipErrorInvalidValue;
             } else e = hipErrorInvalidValue;
             if (e != hipSuccess || p.splits == 1) return e;
             return launch_join<DT, D>(t, p.tiles, p.rows, kKvUnit, st);

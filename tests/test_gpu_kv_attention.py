@@ -177,13 +177,14 @@ def test_prompts(D, mode, g, dtype):
 @pytest.mark.parametrize("causal,window", [(True, 0), (True, 100), (False, 0), (False, 70)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_prompt_masks(dtype, causal, window):
-    for rows, lengths, page in (([200, 1, 300], [260, 500, 120], 16), ([513], [513], 80), ([260, 0, 270], [0, 10, 100], 16)):
+    for rows, lengths, page in (([200, 1, 300], [260, 500, 120], 16), ([513], [513], 80), ([260, 0, 270], [0, 10, 100], 16),
+                                ([600, 1, 700], [660, 500, 720], 16), ([760, 0, 870], [0, 10, 300], 32)):
         p = Problem(rows, lengths, 2, 2, 128, "affine", 64, dtype, page, seed=len(rows))
         p.check(p.call(causal=causal, window=window), causal=causal, window=window)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("rows", [1, 3, 90])
+@pytest.mark.parametrize("rows", [1, 3, 90, 300])
 def test_bad_pages_take_their_keys_out(dtype, rows):
     p = Problem([rows, rows], [400, 170], 2, 2, 64, "affine", 64, dtype, 16, seed=5)
     for b, i, v in ((0, 0, -1), (0, 3, 1 << 30), (0, 9, -(1 << 31)), (1, 2, p.cache.pages), (1, 10, -5)):
@@ -206,7 +207,7 @@ def test_pages_may_be_shared_and_long_tables_end_early():
     p.check(p.call())
 
 
-@pytest.mark.parametrize("rows", [1, 60])
+@pytest.mark.parametrize("rows", [1, 60, 600])
 def test_rows_behind_the_last_sequence_stay(rows):
     """A padded batch: rows before the first sequence and behind the last are left as they are."""
     p = Problem([rows, 2], [100, 50], 2, 2, 128, "mxfp4", 32, "bf16", 16, seed=7)
@@ -220,7 +221,7 @@ def test_rows_behind_the_last_sequence_stay(rows):
     assert (fresh[:3] == 0).all() and (fresh[T + 3 :] == 0).all()
 
 
-@pytest.mark.parametrize("rows", [1, 90])
+@pytest.mark.parametrize("rows", [1, 90, 300])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_strided_queries_scale_and_large_scores(rows, dtype):
     p = Problem([rows, rows], [150, 90], 2, 2, 64, "affine", 32, dtype, 16, seed=8)
@@ -243,7 +244,7 @@ def test_strided_queries_scale_and_large_scores(rows, dtype):
     assert (np.abs(f64(got) - want) <= tol * 4 + 1e-3 * np.abs(want).max()).all()
 
 
-@pytest.mark.parametrize("rows", [1, 90])
+@pytest.mark.parametrize("rows", [1, 90, 300])
 @pytest.mark.parametrize("mode,g", [("affine", 64), ("mxfp4", 32)])
 def test_queries_and_keys_of_any_size(rows, mode, g):
     """bf16 reaches far past f16 on both sides: keys of 1e8 under queries of 1e-8, keys of 1e-25, queries of zero."""
@@ -257,7 +258,7 @@ def test_queries_and_keys_of_any_size(rows, mode, g):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("rows", [1, 90])
+@pytest.mark.parametrize("rows", [1, 90, 300])
 def test_values_of_any_size(rows, dtype):
     """Values whose size changes from page to page by powers of two, up and down."""
     p = Problem([rows, rows], [500, 300], 2, 2, 64, "affine", 64, dtype, 64, seed=31, garbage=False)
