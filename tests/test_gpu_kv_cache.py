@@ -169,6 +169,43 @@ def test_a_pool_past_32_bits():
     assert int((cache.key.value != 0).any(-1).sum()) <= 4 * H
 
 
+@pytest.mark.parametrize("mode", ["affine", "mxfp4"])
+def test_captured_on_another_stream_and_replayed(mode):
+    """Rows turned, written and read back, and a gradient turned back, in one graph: every replay gives the eager bits
+    for what its buffers hold then."""
+    D, T = 64, 300
+    freqs = qm.rotary_frequencies(D, device=DEV)
+    x, v = [rand((T, 2, D), "bf16", i) for i in range(2)]
+    positions = torch.arange(T, dtype=torch.int32, device=DEV)
+    slots = torch.randperm(20 * 16, generator=torch.Generator().manual_seed(5))[:T].to(torch.int32).to(DEV)
+
+    def run(cache, turned):
+        qm.rotary(x, positions, freqs, out=turned)
+        qm.kv_cache_write(cache, turned, v, slots)
+        return (*qm.kv_cache_read(cache, slots), qm.rotary_grad(v, positions, freqs))
+
+    cache, turned, stream = qm.kv_cache(20, 2, 16, D, mode=mode, device=DEV), torch.empty_like(x), torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        run(cache, turned)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            outs = run(cache, turned)
+    torch.cuda.current_stream().wait_stream(stream)
+    for i in range(4):
+        x.copy_(rand((T, 2, D), "bf16", 10 + i))
+        positions.add_(i)
+        slots.copy_(slots.roll(1))
+        other = qm.kv_cache(20, 2, 16, D, mode=mode, device=DEV)
+        want = run(other, torch.empty_like(x))
+        (torch.randn(1 << 16, device=DEV) * 2.0).sum()      # unrelated work
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b), i
+
+
 def test_refusals():
     cache = qm.kv_cache(2, 2, 16, 64, 64, "affine", torch.bfloat16, DEV)
     k, slots = rand((3, 2, 64), "bf16", 1), torch.zeros(3, dtype=torch.int32, device=DEV)
