@@ -511,11 +511,12 @@ qlin_status qlin_kv_cache_read(const qlin_kv_cache* cache, const int32_t* slots,
  *   table     int32 [B, width]: key j lies at place j % page_size of page
  *             table[b, j / page_size]. Pages may be shared; a page number
  *             outside the pool takes its keys out; entries past a sequence's
- *             keys are not read.
+ *             keys may be anything.
  *   causal    nonzero: a row sees no key behind its own place.
  *   window    > 0: nor any window or more places before it; 0: all.
- *   out       [T, q_heads, head_dim] of dtype, dense. A row that sees no key
- *             gives zeros.
+ *   scale     any sign, or zero; twice of it finite in fp32.
+ *   out       [T, q_heads, head_dim] of dtype, dense, 16-byte aligned; it must
+ *             not overlap q. A row that sees no key gives zeros.
  *   workspace  device memory of at least qlin_kv_cache_attention_workspace_bytes
  *             bytes for the same sizes, 16-byte aligned (may be NULL where that
  *             is 0); overwritten, nothing in it counts before or after a call.
@@ -523,8 +524,18 @@ qlin_status qlin_kv_cache_read(const qlin_kv_cache* cache, const int32_t* slots,
  * Sizes alone choose how it runs, so a captured call may be replayed with other
  * lengths, tables and offsets in the same buffers. Scores, their softmax and
  * the sums are fp32. f16 and bf16 with head_dim 64, 96, 128, 192 or 256 run on
- * the matrix cores: there the p_j and the values are rounded to dtype (keys are
- * not where few rows share them), so values outside f16's range do not go with an f16 q.
+ * the matrix cores, with operands of 16 bits:
+ *   - few rows to a sequence and key head: keys exactly; each p_j and each value
+ *     is rounded to dtype once (bf16 "affine" of few groups: p_j times the
+ *     value's scale, with its code; "nvfp4": p_j to f16, values exactly, a bf16
+ *     row of q as f16 in a power of two of its largest value). "mxfp4" values
+ *     outside f16's range do not go with an f16 q there.
+ *   - many: keys, values, p_j and a bf16 row of q are rounded to f16, in powers
+ *     of two of the largest of a block of 64 keys, or of a row of q; what is
+ *     small beside that keeps 2^-25 of it.
+ * bf16 values may be of any size between 2^-110 and 2^110.
+ * QLIN_ERR_UNSUPPORTED where one launch does not hold a call's rows (2^24
+ * workgroups of 8 to 256 rows of a key head, with their chunks of keys).
  * Keys and values that a row of a tile sees must be finite; what lies behind a
  * sequence's end may be anything. Results do not depend on scheduling.
  * T, B < 2^31, T * q_heads < 2^31. T == 0 is a no-op.
@@ -547,7 +558,8 @@ const char* qlin_last_error(void);
  * launch (a static string: "decode", "in_out", "in_out_split",
  * "in_out_row_blocks", "prefill", "tiled", "generic", "gather_decode",
  * "gather_prefill", "qqmm_scaled_mfma", "mxfp4_stream", "mxfp4_tiled",
- * "mxfp4_gather_stream", "mxfp4_gather_tiled"; "" before any). "generic" is the fp32 VALU fallback for
+ * "mxfp4_gather_stream", "mxfp4_gather_tiled", "kv_attention_simple",
+ * "kv_attention_rows", "kv_attention_prompt"; "" before any). "generic" is the fp32 VALU fallback for
  * shapes the fast kernels do not take, typically an order of magnitude
  * slower; QLIN_WARN_FALLBACK=1 also prints a line to stderr when it runs.
  */

@@ -228,6 +228,9 @@ qlin_status qlin_kv_cache_attention(const qlin_kv_cache* cache, const void* q, q
         (s = check_aligned(table, 4, "table")) || (s = check_aligned(lengths, 4, "lengths")) ||
         (s = check_aligned(offsets, 4, "offsets")))
         return s;
+    const uintptr_t qb = (uintptr_t)q, qe = qb + ((T - 1) * q_stride + q_heads * p.D) * elem(dtype);
+    const uintptr_t ob = (uintptr_t)out, oe = ob + T * q_heads * p.D * elem(dtype);
+    if (qb < oe && ob < qe) return fail(QLIN_ERR_INVALID_ARGUMENT, "out overlaps q");
     const qlin::AttendPlan plan = qlin::attend_plan(dtype, T, (int)q_heads, B, width, p, window, offsets == nullptr);
     if (!plan.fits) return fail(QLIN_ERR_UNSUPPORTED, "more rows than one launch holds: split them over several calls");
     if (plan.bytes) {

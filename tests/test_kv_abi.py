@@ -97,7 +97,7 @@ def test_attention_rejects(lib):
     need = size(cache(), BF16, 4, 16, 4, 300, 0, 0)
     assert need > 0
     base = dict(c=cache(), q=P, dt=BF16, T=4, qs=2048, qh=16, table=P, B=4, width=300, lengths=P, offsets=None, scale=0.1,
-                causal=1, window=0, ws=P, nb=need, out=P, st=None)
+                causal=1, window=0, ws=P, nb=need, out=2 * P, st=None)
     call = caller(lib.qlin_kv_cache_attention, base)
     for kw in BAD_CACHES + BAD_POINTERS:
         assert call(c=cache(**kw)) == INVALID, kw
@@ -107,9 +107,10 @@ def test_attention_rejects(lib):
                 dict(B=-1), dict(width=-1), dict(window=-1), dict(scale=float("inf")), dict(qs=-1), dict(qs=(1 << 31) + 1),
                 dict(q=None), dict(table=None), dict(lengths=None), dict(out=None), dict(q=ODD), dict(out=P + 8),
                 dict(table=P + 2), dict(lengths=P + 2), dict(offsets=P + 2), dict(ws=None), dict(nb=need - 1),
-                dict(ws=P + 8)):
+                dict(ws=P + 8), dict(out=P), dict(out=P + 3 * 4096 + 4080), dict(out=P - 4 * 4096 + 16)):
         assert call(**bad) == INVALID, bad
         assert err(lib)
+    assert call(out=P) == INVALID and "overlaps" in err(lib)
     assert call(T=1 << 30, B=1 << 30) == UNSUPPORTED
     assert call(width=1 << 31) == UNSUPPORTED
     assert call(T=0, B=0, q=None, table=None, lengths=None, out=None, ws=None, nb=0) == 0
