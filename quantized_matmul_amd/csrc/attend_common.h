@@ -33,6 +33,18 @@ __device__ __forceinline__ void e2m1_values(uint32_t w, float s, float (&v)[8]) 
 #undef QLIN_PAIR
 }
 
+template <int MODE>
+__device__ __forceinline__ void word_values(uint32_t w, float s, float z, float (&v)[8]) {
+    if constexpr (MODE == AFFINE) {
+        const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = __builtin_fmaf(s, (float)(((i & 1 ? odd : even) >> (i / 2 * 8)) & 0xFFu), z);
+    } else {
+        e2m1_values(w, s, v);
+    }
+}
+
 // Scale (and bias) of a group as numbers.
 template <int MODE, int SDT>
 __device__ __forceinline__ float scale_at(const void* p, int64_t i) {

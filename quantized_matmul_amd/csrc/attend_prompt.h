@@ -46,18 +46,6 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-template <int MODE>
-__device__ __forceinline__ void word_values(uint32_t w, float s, float z, float (&v)[8]) {
-    if constexpr (MODE == AFFINE) {
-        const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = __builtin_fmaf(s, (float)(((i & 1 ? odd : even) >> (i / 2 * 8)) & 0xFFu), z);
-    } else {
-        e2m1_values(w, s, v);
-    }
-}
-
 // A block of 256 threads: the 64 keys of one image, in parts of BK keys.
 template <int DT, int MODE, int D, int BK>
 __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* images) {

@@ -279,6 +279,9 @@ def test_long_sequences_in_many_chunks():
     p.check(p.call(window=5000), window=5000)
     p = Problem([1], [70000], 1, 2, 64, "nvfp4", 16, "f16", 256, seed=10)
     p.check(p.call())
+    for rows, lengths, D in (([1, 2], [9000, 20000], 128), ([300, 1], [1500, 1200], 160)):
+        p = Problem(rows, lengths, 1, 4, D, "affine", 32, "f32", 64, seed=17)
+        p.check(p.call())
 
 
 def test_a_pool_past_32_bits():
