@@ -525,11 +525,13 @@ qlin_status qlin_kv_cache_read(const qlin_kv_cache* cache, const int32_t* slots,
  * lengths, tables and offsets in the same buffers. Scores, their softmax and
  * the sums are fp32. f16 and bf16 with head_dim 64, 96, 128, 192 or 256 run on
  * the matrix cores, with operands of 16 bits:
- *   - few rows to a sequence and key head: keys exactly; each p_j and each value
- *     is rounded to dtype once (bf16 "affine" of few groups: p_j times the
- *     value's scale, with its code; "nvfp4": p_j to f16, values exactly, a bf16
- *     row of q as f16 in a power of two of its largest value). "mxfp4" values
- *     outside f16's range do not go with an f16 q there.
+ *   - few rows to a sequence and key head: keys exactly; each p_j and each
+ *     "affine" value is rounded to f16 once, bf16 values in units of a power of
+ *     two that follows the largest (small ones keep 2^-25 of that), or, in few
+ *     groups, p_j times the value's scale to bf16, with its code; "mxfp4": p_j to
+ *     dtype, "nvfp4": to f16, values exactly (a bf16 row of q as f16 in a power of
+ *     two of its largest value there). "mxfp4" values outside f16's range do not
+ *     go with an f16 q there.
  *   - many: keys, values, p_j and a bf16 row of q are rounded to f16, in powers
  *     of two of the largest of a block of 64 keys, or of a row of q; what is
  *     small beside that keeps 2^-25 of it.

@@ -76,8 +76,12 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
     }
     p.path = 1;
     const int groups = c.mode == 0 && dt == QLIN_BF16 ? c.D / c.g : 0;
-    // (four groups of D 128 take more columns than they save: 124 us decoded, 137 as codes; of D 256 142 and 116)
-    p.codes = groups == 1 || (groups >= 2 && (groups <= 3 || (groups == 4 && c.D == 256)) && mean <= 16 / groups);
+    // Values as codes where a sequence's rows fit a tile of 16 / groups: one token of each, or twice the average (D up to
+    // 128: there a second tile costs more than decoding). us, decoded and as codes: D 128, groups of 64, 64 sequences of
+    // 5000 to 20000 keys 252 and 225, 16 of 1 to 3 rows of four heads over 2000 to 8000 keys 41 and 48; those of D 256,
+    // groups of 128, 90 and 73. Four groups of D 128 take more columns than they save (107 and 137), not of D 256.
+    p.codes = groups == 1 || (groups >= 2 && (groups <= 3 || (groups == 4 && c.D == 256)) &&
+                              (T <= B || c.D > 128 ? mean : 2 * mean) <= 16 / groups);
     const int dup = p.codes ? groups : 1;
     // 32 columns where the rows fill more than 16, as the codes are decoded once for them: 64 sequences of 64 rows over
     // 16000 keys, D 128, 583 us, in tiles of 16 rows 666 (48 columns, of D 64, took 424 for 384)

@@ -28,8 +28,12 @@
 //     (lane (q row, j) has keys 4j..4j+3 of both halves of the step), so lane
 //     (r, j) of V's operand takes word r of those eight keys: its eight codes are
 //     eight rows of V^T. Two ways to make them numbers:
-//     - decoded: fl(s c + z), rounded to the type (f16 by packed instructions, two
-//       keys each; bf16 in fp32 and rounded in pairs).
+//     - decoded: fl(s c + z) as f16 by packed instructions, two keys each. bf16
+//       values are in units of a power of two that follows the largest one so far
+//       (a wave's; o is scaled where it moves): no value leaves f16's range, and
+//       what is small beside the largest keeps 2^-25 of it. In bf16, p and the
+//       values put 0.0015 on outputs that round by 0.0017 themselves; in f16 nothing
+//       that shows, in the same time (64 rows, groups of 32: 82 us for 75).
 //     - as codes (PS; bf16 affine): p takes the scale and the codes stay 16 + c,
 //       2.5 instructions a pair instead of 4 and more. A column of p belongs to a
 //       single group then, so a row of q has as many columns as a row has groups
@@ -37,9 +41,10 @@
 //       z + 8 s (summed in fp32) and 8 s too many of 16 + c - 8, taken off at the
 //       end as 24 times the sum of the rounded p s, which a product with ones
 //       gives: what p s lost by rounding multiplies c - 8, not 16 + c.
-//       64 x 8192 to 32768 keys, D 128, groups of 64: 335 us decoded, 293 as codes.
-//   Rounded on the way: p (or p s) and decoded values to the type, half a step
-//   each; nvfp4's p to f16. Sums, m and l are fp32.
+//       64 x 5000 to 20000 keys, D 128, groups of 64: 252 us decoded, 228 as codes
+//       (outputs off by 0.0021 where rounding alone is 0.0017).
+//   Rounded on the way: p s to bf16 (as codes); p and decoded values to f16; mxfp4's
+//   p to the type, its values not at all, nor nvfp4's. Sums, m and l are fp32.
 //
 // Scales go through LDS a second time, as numbers (a lane there needs those of
 // eight keys); keys outside the sequence get zeros there, whatever their page
@@ -197,7 +202,10 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
     constexpr int VC = (HW + 15) / 16;                     // words of a value a lane takes
     constexpr int CL = HALF ? 4 : 8, OT = VC * CL;         // codes of a word it takes; tiles of o
     constexpr bool AFF = MODE == AFFINE;
-    constexpr int MT = MODE == NVFP4 ? (int)QLIN_F16 : DT; // type of the matrix cores' operands: all of nvfp4 fits f16
+    // types of the products' operands: all of nvfp4 fits f16; decoded bf16 values are f16 in a power of two
+    constexpr int KT = MODE == NVFP4 ? (int)QLIN_F16 : DT;
+    constexpr bool UNIT = AFF && DT == QLIN_BF16 && !PS;
+    constexpr int VT = UNIT ? (int)QLIN_F16 : KT;
     static_assert(!PS || (AFF && NG <= 4 && DT == QLIN_BF16), "values as codes");
     constexpr int ARR = AFF ? 4 : 2;                       // scale arrays of a step: keys', values', biases in the same order
     constexpr int WSCALES = ARR * NG * kScaleRow;          // a wave's scales as numbers
@@ -275,7 +283,7 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
     f32x4 o[NT][OT], ones[NT];
     // p = exp2(score - base), base being m + kUnder, or 0 while there is no m. kUnder keeps sums of bf16's largest values
     // inside fp32; f16, whose values cannot leave it, has no bits to give for that.
-    constexpr float kUnder = MT == QLIN_BF16 ? kSlack : 0.0f;
+    constexpr float kUnder = VT == QLIN_BF16 ? kSlack : 0.0f;
     float m[NT], l[NT], zsum[NT], base[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -286,12 +294,16 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
 #pragma unroll
         for (int i = 0; i < OT; ++i) o[n][i] = f32x4{0, 0, 0, 0};
     }
+    // UNIT: o and the values are in units of 2^unit, which follows the largest value so far where one passes it by 2^15
+    float largest = 0.0f, to_unit = 1.0f;
+    int unit = 0;
     const float scale = a.scale * kLog2e;
     float* const sl = numbers + wave * WSCALES;                          // this wave's scales: [array, group, key]
     constexpr int SE = (kStep * NG + 63) / 64;                           // a lane's numbers of an array
     constexpr int VROW = HW < 16 ? HW : 16;
     const uint32_t mask = scalar_bits(DT == QLIN_BF16 ? 0x00780078u : 0x03C003C0u);
     const uint32_t sixteen = vector_bits(DT == QLIN_BF16 ? 0x41804180u : 0x4C004C00u);
+    const uint32_t value_mask = UNIT ? scalar_bits(0x03C003C0u) : mask, value_sixteen = UNIT ? vector_bits(0x4C004C00u) : sixteen;
 
     // A stage of the ring: the codes of the step's keys and values, [16 keys of them, K or V][row][chunk], then the bytes
     // of their scales. Key 4 y + x lies in row 4 x + y, its chunks by x further round, so that neither K's reads (16
@@ -420,25 +432,53 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
             const uint8_t* const in = mine + stage * STAGE;
             // the scales as numbers where the lanes find those of their keys; the keys' take the softmax's scale along,
             // and their biases what 16 + c has too much
+            float x[SE][ARR];
 #pragma unroll
             for (int e = 0; e < SE; ++e) {
                 const int at = lane + 64 * e, key = min(at / NG, kStep - 1), g = at % NG, st = key / kKvUnit;
                 const uint8_t* const raw = in + 32 * D + st * (ARR * U * 4) + (key % kKvUnit * NG + g) * ES;
-                float x[ARR];
 #pragma unroll
-                for (int s = 0; s < ARR; ++s) x[s] = scale_at<MODE, DT>(raw + s * (U * 4), 0);
-                if (MODE != NVFP4) x[0] *= scale;
-                if (AFF) x[ARR - 2] = __builtin_fmaf(x[0], -16.0f, x[ARR - 2] * scale);
-                if (PS) x[ARR - 1] = __builtin_fmaf(x[1], 8.0f, x[ARR - 1]);
+                for (int s = 0; s < ARR; ++s) x[e][s] = scale_at<MODE, DT>(raw + s * (U * 4), 0);
+                if (MODE != NVFP4) x[e][0] *= scale;
+                if (AFF) x[e][ARR - 2] = __builtin_fmaf(x[e][0], -16.0f, x[e][ARR - 2] * scale);
+                if (PS) x[e][ARR - 1] = __builtin_fmaf(x[e][1], 8.0f, x[e][ARR - 1]);
                 if (!whole) {                                // what is not there is no number
                     out_of_line();
                     const bool live = (st ? rb[1] : rb[0]) >= 0 && key0 + key < k1;
 #pragma unroll
-                    for (int s = 0; s < ARR; ++s) x[s] = live ? x[s] : 0.0f;
+                    for (int s = 0; s < ARR; ++s) x[e][s] = live ? x[e][s] : 0.0f;
                 }
+            }
+            if constexpr (UNIT) {
+                float most = 0.0f;
+#pragma unroll
+                for (int e = 0; e < SE; ++e) most = fmaxf(most, __builtin_fmaf(fabsf(x[e][1]), 15.0f, fabsf(x[e][3])));
+                if (__any(most > largest)) {
+                    out_of_line();
+#pragma unroll
+                    for (int off = 32; off; off /= 2) most = fmaxf(most, __shfl_xor(most, off, 64));
+                    const int to = max(ilogb_of(most), -120);      // (2^-to is a number)
+                    const float f = largest == 0.0f ? 1.0f : __builtin_ldexpf(1.0f, unit - to);
+                    unit = to;
+                    to_unit = __builtin_ldexpf(1.0f, -to);
+                    largest = __builtin_ldexpf(1.0f, to + 15);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < OT; ++i) o[n][i] *= f;
+                }
+#pragma unroll
+                for (int e = 0; e < SE; ++e) {
+                    x[e][1] *= to_unit;
+                    x[e][3] *= to_unit;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < SE; ++e) {
+                const int at = lane + 64 * e, key = min(at / NG, kStep - 1), g = at % NG;
                 if (kStep * NG % 64 == 0 || at < kStep * NG)
 #pragma unroll
-                    for (int s = 0; s < ARR; ++s) sl[(s * NG + g) * kScaleRow + key] = x[s];
+                    for (int s = 0; s < ARR; ++s) sl[(s * NG + g) * kScaleRow + key] = x[e][s];
             }
             wave_fence();
             uint32_t vw[8][VC];
@@ -461,7 +501,7 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
                         const f16x2 s = both(sl[(2 * i + j / 2) * kScaleRow + st * 16 + r]);
                         const u32x4 k = times(code_operand<QLIN_F16>(*(const uint32_t*)(in + word_at(st, 0, r, i * 4 + j))), s);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) sc[n][st] = mfma16<MT>(k, q[n][i], sc[n][st]);
+                        for (int n = 0; n < NT; ++n) sc[n][st] = mfma16<KT>(k, q[n][i], sc[n][st]);
                     }
                 } else {
 #pragma unroll
@@ -558,7 +598,7 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[n][i] = round2<MT>(x[2 * i], x[2 * i + 1]);
+                for (int i = 0; i < 4; ++i) p[n][i] = round2<VT>(x[2 * i], x[2 * i + 1]);
                 if constexpr (PS) ones[n] = mfma16<DT>(u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}, p[n], ones[n]);
             }
             // values: word v*16 + r of the lane's eight keys
@@ -594,58 +634,38 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
                     if constexpr (AFF) {
                         const f32x4 z0 = *(const f32x4*)(sl + (3 * NG + g) * kScaleRow + 4 * j);
                         const f32x4 z1 = *(const f32x4*)(sl + (3 * NG + g) * kScaleRow + 16 + 4 * j);
-                        if constexpr (DT == QLIN_F16) {        // fl(s c + z) by packed instructions, two keys each
-                            f16x2 s2[4], z2[4];
+                        // fl(s c + z) by packed instructions, two keys each
+                        f16x2 s2[4], z2[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                s2[e] = __builtin_convertvector((e < 2 ? f32x2{s0[2 * e], s0[2 * e + 1]} : f32x2{s1[2 * e - 4], s1[2 * e - 3]}), f16x2);
-                                z2[e] = __builtin_convertvector((e < 2 ? f32x2{z0[2 * e], z0[2 * e + 1]} : f32x2{z1[2 * e - 4], z1[2 * e - 3]}), f16x2);
-                            }
-                            auto four = [&](uint32_t halves, int to) {
-                                uint32_t x[4];
+                        for (int e = 0; e < 4; ++e) {
+                            s2[e] = __builtin_convertvector((e < 2 ? f32x2{s0[2 * e], s0[2 * e + 1]} : f32x2{s1[2 * e - 4], s1[2 * e - 3]}), f16x2);
+                            z2[e] = __builtin_convertvector((e < 2 ? f32x2{z0[2 * e], z0[2 * e + 1]} : f32x2{z1[2 * e - 4], z1[2 * e - 3]}), f16x2);
+                        }
+                        auto four = [&](uint32_t halves, int to) {
+                            uint32_t x[4];
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) x[e] = __builtin_amdgcn_perm(vw[2 * e + 1][v], vw[2 * e][v], halves);
-                                auto one = [&](auto ic) {
-                                    constexpr int I = decltype(ic)::value;
-                                    u32x4 vt;
+                            for (int e = 0; e < 4; ++e) x[e] = __builtin_amdgcn_perm(vw[2 * e + 1][v], vw[2 * e][v], halves);
+                            auto one = [&](auto ic) {
+                                constexpr int I = decltype(ic)::value;
+                                u32x4 vt;
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        const f16x2 c2 = __builtin_bit_cast(f16x2, sixteen_plus<DT, I>(x[e], mask, sixteen)) - (f16x2){16, 16};
-                                        vt[e] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c2, s2[e], z2[e]));
-                                    }
+                                for (int e = 0; e < 4; ++e) {
+                                    const f16x2 c2 = __builtin_bit_cast(f16x2, sixteen_plus<QLIN_F16, I>(x[e], value_mask, value_sixteen)) - (f16x2){16, 16};
+                                    vt[e] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c2, s2[e], z2[e]));
+                                }
 #pragma unroll
-                                    for (int n = 0; n < NT; ++n) o[n][v * CL + to + I] = mfma16<MT>(vt, p[n], o[n][v * CL + to + I]);
-                                };
-                                one(std::integral_constant<int, 0>{});
-                                one(std::integral_constant<int, 1>{});
-                                one(std::integral_constant<int, 2>{});
-                                one(std::integral_constant<int, 3>{});
+                                for (int n = 0; n < NT; ++n) o[n][v * CL + to + I] = mfma16<VT>(vt, p[n], o[n][v * CL + to + I]);
                             };
-                            if constexpr (HALF) {
-                                four(r & 1 ? 0x07060302u : 0x05040100u, 0);
-                            } else {
-                                four(0x05040100u, 0);
-                                four(0x07060302u, 4);
-                            }
+                            one(std::integral_constant<int, 0>{});
+                            one(std::integral_constant<int, 1>{});
+                            one(std::integral_constant<int, 2>{});
+                            one(std::integral_constant<int, 3>{});
+                        };
+                        if constexpr (HALF) {
+                            four(r & 1 ? 0x07060302u : 0x05040100u, 0);
                         } else {
-                            uint32_t code[8][2];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const uint32_t w4 = HALF ? vw[e][v] >> (16 * (r & 1)) : vw[e][v];
-                                code[e][0] = vector_bits(w4 & 0x0F0F0F0Fu);
-                                code[e][1] = vector_bits((w4 >> 4) & 0x0F0F0F0Fu);
-                            }
-#pragma unroll
-                            for (int i = 0; i < CL; ++i) {
-                                float x[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    x[e] = __builtin_fmaf(e < 4 ? s0[e & 3] : s1[e & 3], (float)((code[e][i & 1] >> (i / 2 * 8)) & 0xFFu),
-                                                          e < 4 ? z0[e & 3] : z1[e & 3]);
-                                const u32x4 vt{round2<DT>(x[0], x[1]), round2<DT>(x[2], x[3]), round2<DT>(x[4], x[5]), round2<DT>(x[6], x[7])};
-#pragma unroll
-                                for (int n = 0; n < NT; ++n) o[n][v * CL + i] = mfma16<DT>(vt, p[n], o[n][v * CL + i]);
-                            }
+                            four(0x05040100u, 0);
+                            four(0x07060302u, 4);
                         }
                     } else if constexpr (MODE == NVFP4) {     // exact in f16; pairs of values to pairs of keys
 #pragma unroll
@@ -670,7 +690,7 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
                             for (int i = 0; i < 4; ++i)
 #pragma unroll
                                 for (int n = 0; n < NT; ++n)
-                                    o[n][v * CL + half * 4 + i] = mfma16<MT>(vt[i], p[n], o[n][v * CL + half * 4 + i]);
+                                    o[n][v * CL + half * 4 + i] = mfma16<VT>(vt[i], p[n], o[n][v * CL + half * 4 + i]);
                         }
                     } else {
                         float x[8][8];
@@ -728,7 +748,7 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
         }
         const float plus = PS ? zsum[n] - 24.0f * ones[n][0] : 0.0f;      // all rows of `ones` are the column's sum
 #pragma unroll
-        for (int i = 0; i < OT; ++i) o[n][i] = PS ? (o[n][i] + plus) * f : o[n][i] * f;
+        for (int i = 0; i < OT; ++i) o[n][i] = PS ? (o[n][i] + plus) * f : o[n][i] * (UNIT ? f * __builtin_ldexpf(1.0f, unit) : f);
     }
     for (int turn = 0; turn < WAVES / REGIONS; ++turn) {
         if (turn == wave / REGIONS) {

@@ -12,7 +12,8 @@ Tolerance, for each output o = sum p v with size = sum p |v|:
   exp2      1 ulp each: 2 * 2^-23.
   p, v      on the matrix cores each rounded to the type once: 2 u of the size, u = eps / 2 of the type. Where the values
             stay codes (bf16, affine) p times the group's scale is rounded instead, and multiplies c - 8, the rest being
-            fp32: u p s |c - 8|, which is at most 8 s u p for each key.
+            fp32: u p s |c - 8|, which is at most 8 s u p for each key. (Other bf16 affine values and their p are
+            rounded to f16, inside this.)
   sums      fp32 over L keys: sqrt(L) + 8 roundings of 2^-24.
   output    one rounding: u of itself; and f16's smallest step.
 """
@@ -271,6 +272,28 @@ def test_values_of_any_size(rows, dtype):
         p.check(p.call())
         p.cache = qm.KVCache(p.cache.key, qm.quantize((v * 1e-30 * sizes.to(DEV)[:, None, None, None] ** 2).bfloat16().contiguous(), 64, 4))
         p.check(p.call())
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("g", [32, 64])
+def test_decoded_values_of_any_size(rows, g):
+    """bf16 values that are decoded, of sizes that grow and fall by up to 2^40 from page to page, tiny ones, and zeros.
+
+    They are f16 in units of a power of two of the largest |z| + 15 |s| so far, at most 3 max |v|: what is below 2^-14 of
+    it is off by 2^-25 of it, 2^-23 max |v| and less for a weighted mean of values."""
+    print(f"decoded sizes rows {rows} g{g}", flush=True)
+    p = Problem([rows, rows], [500, 300], 2, 5, 128, "affine", g, "bf16", 64, seed=33, garbage=False)
+    v = qm.dequantize(p.cache.value, torch.float32)
+    steps = 2.0 ** torch.tensor([0, 18, -20, 3, -14, 20, -3, 0, 16, -8, 2, -1, 4, 8, -12, 1, 0, 0, 0, 0])[: v.shape[0]]
+    for size in (1.0, 1e30, 1e-30, 1e-38, 0.0):
+        w = (v * size * steps.to(DEV)[:, None, None, None]).bfloat16().contiguous()
+        p.cache = qm.KVCache(p.cache.key, qm.quantize(w, g, 4))
+        got = p.call()
+        assert qm.last_path() == "kv_attention_rows"
+        p.prompt = False
+        want, tol = p.want()
+        tol = tol + 2.0 ** -23 * np.abs(p.dense()[1]).max() + 2.0 ** -126      # (and what bf16 outputs flush or step by)
+        assert np.isfinite(f64(got)).all() and (np.abs(f64(got) - want) <= tol).all(), size
 
 
 def test_long_sequences_in_many_chunks():
