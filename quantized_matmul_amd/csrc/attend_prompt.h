@@ -14,7 +14,8 @@
 // bf16 output, whose own rounding is 0.0017: 0.0051; with f16 keys 0.0025, with
 // all in f16 0.0018). No value leaves f16's range; what is 2^-14 of the largest
 // of its block and less is held to 2^-25 of that. o is kept in units of the
-// largest block's power of two so far, p of other blocks divided accordingly.
+// largest block's power of two so far, p of other blocks divided accordingly; a
+// block without values has none.
 // Decoding inside the attention kernel would cost every workgroup again what
 // this does once: 190 of about 560 vector instructions of 64 keys (D 128), where
 // the matrix cores need the time of 512.
@@ -49,7 +50,7 @@ namespace {
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 
 constexpr int kImageKeys = 64;
-constexpr int kNoPower = -1000;                  // below any number's
+constexpr int kNoPower = -1000;                  // of zeros: below any number's
 
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
         const int32_t rb = blocks[key / kKvUnit];
         return rb >= 0 && key0 + key < s.keys ? (int64_t)rb * kKvUnit + key % kKvUnit : -1;
     };
-    // power of two of the largest value of a side's keys
+    // power of two of the largest value of a side's keys, kNoPower where they are all zero or not there
     auto power = [&](int side) {
         const int64_t row = row_of(tid % 64);
         float most = 0.0f;
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
         if (tid % 64 == 0) largest[side][tid / 64] = most;
         __syncthreads();
         most = fmaxf(fmaxf(largest[side][0], largest[side][1]), fmaxf(largest[side][2], largest[side][3]));
-        return most > 0.0f ? ilogb_of(most) : 0;
+        return most > 0.0f ? ilogb_of(most) : kNoPower;
     };
     {
         const int key = tid % 64;
@@ -105,7 +106,8 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
             const uint64_t there = __ballot(row >= 0);
             if (tid == 0) t.present[(int64_t)b * t.key_blocks + kb] = there;
         }
-        const int e = power(0);
+        int e = power(0);
+        if (e == kNoPower) e = 0;
         if (tid == 0) t.key_scale[((int64_t)b * t.key_blocks + kb) * c.heads + h] = __builtin_ldexpf(1.0f, e);
         for (int w = tid / 64; w < HW; w += 4) {
             u32x4 out{0, 0, 0, 0};
@@ -264,8 +266,9 @@ __global__ void __launch_bounds__(256, prompt_residents(D, RT)) attend_prompt_ke
 #pragma unroll
                 for (int d = 0; d < DTILES; ++d) o[n][d] *= f;
         }
-        // p is multiplied by 2^down, its sum back; where that is nothing beside the largest block, by no less than 2^-64
-        const int fall = max(up - unit, -64);
+        // p is multiplied by 2^down, its sum back; where that is nothing beside the largest block, by no less than 2^-64.
+        // A block without values (zeros, pages that are not there) moves nothing and keeps its p.
+        const int fall = up == kNoPower ? 0 : max(up - unit, -64);
         const float down = (float)fall, back = __builtin_ldexpf(1.0f, -fall);
         const bool whole = there == ~0ull && key0 >= see_last.lo && key0 + BK <= see_first.hi;
         const uint8_t* const kl = lds[buf] + hb * (BK * 16) + r * 16;
