@@ -20,7 +20,9 @@
 //   affine   q = rint(fl(d / s)), d = fl(v - z). The quotient is an fp64 product
 //            with 1 / s rounded once more, as there, and so is fl((max - z) / 15):
 //            a quotient of two 24-bit numbers lies 2^-48 from any rounding boundary
-//            or on it. s is rounded up, so q is in [0, 15] without a clamp;
+//            or on it. s is rounded up, so q is in [0, 15] without a clamp, but
+//            where an fp32 s is a few of the smallest steps: to nearest it may be
+//            half a step short, of 15 steps and less enough for a q of 15.5.
 //            v_cvt_pk_u8_f32 rounds it to the nearest even byte.
 //            Minimum and maximum by the hardware's min and max; only where the
 //            minimum is zero does the order of +0 and -0 count, and plain
@@ -113,6 +115,11 @@ __device__ __forceinline__ uint32_t affine_word(const float (&v)[8], float* scal
     float q[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) q[e] = (float)((double)(v[e] - z) * r);
+    if constexpr (DT == QLIN_F32)
+        if (__any(s < 0x1p-145f)) {              // 16 steps
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q[e] = q[e] > 15.0f ? 15.0f : q[e];
+        }
     uint32_t even = 0, odd = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
