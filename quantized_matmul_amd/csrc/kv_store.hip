@@ -23,12 +23,14 @@
 //            or on it. s is rounded up, so q is in [0, 15] without a clamp, but
 //            where an fp32 s is a few of the smallest steps: to nearest it may be
 //            half a step short, of 15 steps and less enough for a q of 15.5.
-//            v_cvt_pk_u8_f32 rounds it to the nearest even byte.
+//            v_cvt_pk_u8_f32 rounds it to the nearest even byte, a NaN to zero.
 //            Minimum and maximum by the hardware's min and max; only where the
-//            minimum is zero does the order of +0 and -0 count, and plain
-//            comparisons decide.
+//            minimum is zero does the order of +0 and -0 count, and only where a
+//            word's first value is a NaN is it not passed over: plain comparisons
+//            decide there, which may leave values of that word outside [z, z + 15 s].
 //   mxfp4, nvfp4  the hardware's E2M1 conversion (nearest even, saturating) of
-//            v at the block's power of two, or of fl(v / s) at scale one.
+//            v at the block's power of two, or of fl(v / s) at scale one; but not
+//            of a NaN, which is no zero there.
 
 #include "kv_common.h"
 #include "quant_common.h"
@@ -97,7 +99,8 @@ __device__ __forceinline__ uint32_t affine_word(const float (&v)[8], float* scal
     }
     lo = -group_most<LPG>(-lo);
     hi = group_most<LPG>(hi);
-    if (__any(lo == 0.0f)) {
+    bool clamp = __any(v[0] != v[0]);
+    if (clamp || __any(lo == 0.0f)) {
         float l = v[0], h = v[0];
 #pragma unroll
         for (int e = 1; e < 8; ++e) {
@@ -115,11 +118,11 @@ __device__ __forceinline__ uint32_t affine_word(const float (&v)[8], float* scal
     float q[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) q[e] = (float)((double)(v[e] - z) * r);
-    if constexpr (DT == QLIN_F32)
-        if (__any(s < 0x1p-145f)) {              // 16 steps
+    if constexpr (DT == QLIN_F32) clamp |= __any(s < 0x1p-145f) != 0;      // 16 steps
+    if (clamp) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) q[e] = q[e] > 15.0f ? 15.0f : q[e];
-        }
+        for (int e = 0; e < 8; ++e) q[e] = q[e] > 0.0f ? fminf(q[e], 15.0f) : 0.0f;
+    }
     uint32_t even = 0, odd = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -144,18 +147,21 @@ __device__ __forceinline__ uint32_t micro_word(const float (&v)[8], uint32_t* by
     for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[e]));
     const MicroScale<MODE> m = micro_scale<MODE>(group_most<LPG>(most));
     *byte = m.sbyte;
+    bool each = MODE == MXFP4 && __any(m.e == -127);         // the conversion's scale has to be a normal number
+    each |= __any(__builtin_isunordered(v[0], v[1]) | __builtin_isunordered(v[2], v[3]) | __builtin_isunordered(v[4], v[5]) |
+                  __builtin_isunordered(v[6], v[7])) != 0;
+    if (each) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w |= micro_encode<MODE>(v[k], m) << (4 * k);
+        return w;
+    }
     if constexpr (MODE == NVFP4) {
         float q[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) q[e] = m.sc == 0.0f ? __uint_as_float(__float_as_uint(v[e]) & 0x80000000u) : div_by_recip(v[e], m.rsc);
         return e2m1_word(q, 1.0f);
     } else {
-        if (__any(m.e == -127)) {                // the conversion's scale has to be a normal number
-            uint32_t w = 0;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) w |= micro_encode<MODE>(v[k], m) << (4 * k);
-            return w;
-        }
         return e2m1_word(v, __uint_as_float(m.sbyte << 23));
     }
 }

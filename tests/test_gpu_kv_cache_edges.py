@@ -1,5 +1,5 @@
 """Rows that a cache's write has to hold as qlin_quantize holds them, byte for byte, where its own arithmetic could
-differ: groups of a few of the smallest steps."""
+differ: groups of a few of the smallest fp32 steps, values that are no number."""
 import numpy as np
 import pytest
 import torch
@@ -27,6 +27,13 @@ def written(x, g, mode):
             for w in (cache.key, cache.value)]
 
 
+def same(a, b):
+    """Equal bits; a NaN equals any NaN."""
+    if a is None or not a.is_floating_point():
+        return (a is None and b is None) or torch.equal(a, b)
+    return torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(7.0, 8.0, 9.0), b.nan_to_num(7.0, 8.0, 9.0))
+
+
 @pytest.mark.parametrize("mode,g", FORMATS)
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 def test_groups_of_the_smallest_numbers(dtype, mode, g):
@@ -46,3 +53,25 @@ def test_groups_of_the_smallest_numbers(dtype, mode, g):
         for t, w in zip(side, want):
             if t is not None:
                 np.testing.assert_array_equal(to_oracle(t).reshape(w.shape), w)
+
+
+@pytest.mark.parametrize("mode,g", FORMATS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_values_that_are_no_number(dtype, mode, g):
+    """NaN and infinities at every place of a group, alone and together: the bytes of `quantize`."""
+    D = 128
+    gen = torch.Generator().manual_seed(3)
+    nan, inf = float("nan"), float("inf")
+    rows = []
+    for bad in ((nan,), (-nan,), (inf,), (-inf,), (nan, inf), (inf, nan), (-inf, inf), (nan, nan, -inf)):
+        for at in list(range(0, 40)) + [63, 64, 72, 96, 120, 127]:
+            x = torch.randn(D, generator=gen)
+            for k, b in enumerate(bad):
+                x[(at + 5 * k) % D] = b
+            rows.append(x)
+    rows += [torch.full((D,), nan), torch.full((D,), inf), torch.full((D,), -inf)]
+    x = torch.stack(rows).to(DTYPES[dtype]).to(DEV)
+    want = qm.quantize(x, g, 4, mode)
+    for side in written(x, g, mode):
+        for t, w in zip(side, (want.value, want.scales, want.biases)):
+            assert same(t, w)
