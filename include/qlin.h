@@ -538,8 +538,10 @@ qlin_status qlin_kv_cache_read(const qlin_kv_cache* cache, const int32_t* slots,
  * bf16 values may be of any size between 2^-110 and 2^110.
  * QLIN_ERR_UNSUPPORTED where one launch does not hold a call's rows (2^24
  * workgroups of 4 to 256 rows of a key head, with their chunks of keys).
- * Keys and values that a row of a tile sees must be finite; what lies behind a
- * sequence's end may be anything. Results do not depend on scheduling.
+ * Keys and values that any row of a sequence sees must be finite, as its rows
+ * share their products; what none of them sees, behind the sequence's end and
+ * before the first row's window, may be anything. Results do not depend on
+ * scheduling.
  * T, B < 2^31, T * q_heads < 2^31. T == 0 is a no-op.
  */
 size_t qlin_kv_cache_attention_workspace_bytes(const qlin_kv_cache* cache, qlin_dtype dtype, int64_t T,

@@ -78,9 +78,9 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
     __syncthreads();
     const int per = c.g / 8, groups = D / c.g;
     uint8_t* const image = images + (((int64_t)b * t.key_blocks + kb) * c.heads + h) * (kImageKeys * D * 4);
-    auto row_of = [&](int key) -> int64_t {      // -1: not there
+    auto row_of = [&](int key) -> int64_t {      // -1: not there, or no row sees it
         const int32_t rb = blocks[key / kKvUnit];
-        return rb >= 0 && key0 + key < s.keys ? (int64_t)rb * kKvUnit + key % kKvUnit : -1;
+        return rb >= 0 && key0 + key >= lo && key0 + key < hi ? (int64_t)rb * kKvUnit + key % kKvUnit : -1;
     };
     // power of two of the largest value of a side's keys, kNoPower where they are all zero or not there
     auto power = [&](int side) {

@@ -47,8 +47,8 @@
 //   p to the type, its values not at all, nor nvfp4's. Sums, m and l are fp32.
 //
 // Scales go through LDS a second time, as numbers (a lane there needs those of
-// eight keys); keys outside the sequence get zeros there, whatever their page
-// holds, and the lowest score.
+// eight keys); keys that no row of the tile sees (behind its end, before its
+// window) get zeros there, whatever their page holds, and the lowest score.
 //
 // Bound by the memory: D/2 bytes and the scales of a key and of a value, read
 // once for the tile's rows. 64 sequences of 8192 to 32768 keys (D 128, 8 heads,
@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
                 if (PS) x[e][ARR - 1] = __builtin_fmaf(x[e][1], 8.0f, x[e][ARR - 1]);
                 if (!whole) {                                // what is not there is no number
                     out_of_line();
-                    const bool live = (st ? rb[1] : rb[0]) >= 0 && key0 + key < k1;
+                    const bool live = (st ? rb[1] : rb[0]) >= 0 && key0 + key >= w.lo && key0 + key < k1;
 #pragma unroll
                     for (int s = 0; s < ARR; ++s) x[e][s] = live ? x[e][s] : 0.0f;
                 }

@@ -1,4 +1,6 @@
-"""Attention over a 4-bit cache on the GPU where blocks of keys hold no values. Problems, formulas and tolerances are those of test_gpu_kv_attention."""
+"""Attention over a 4-bit cache on the GPU where blocks of keys hold no values and where keys that no row sees are no
+numbers. Problems, formulas and tolerances are those of test_gpu_kv_attention."""
+import numpy as np
 import pytest
 import torch
 
@@ -27,3 +29,32 @@ def test_blocks_without_values_beside_small_ones(rows, mode, g, size):
     assert qm.last_path() == ("kv_attention_prompt" if rows == 300 else "kv_attention_rows")
     p.check(got)
     assert (got[2 * rows :] == 0).all()
+
+
+@pytest.mark.parametrize("what", ["nan", "large"])
+@pytest.mark.parametrize("mode,g", [("affine", 32), ("affine", 64), ("affine", 128), ("mxfp4", 32), ("nvfp4", 16)])
+@pytest.mark.parametrize("rows,D,dtype", [(1, 128, "bf16"), (1, 128, "f16"), (5, 64, "bf16"), (40, 128, "bf16"), (300, 128, "bf16"),
+                                          (300, 64, "f16"), (1, 256, "bf16"), (3, 160, "f16"), (1, 128, "f32")])
+def test_keys_before_the_window_may_be_anything(rows, D, dtype, mode, g, what):
+    """What no row sees does not change a bit of the output, be it no number or far larger than what is seen."""
+    if D % g:
+        pytest.skip("head_dim is no multiple of the group")
+    print(f"before the window rows {rows} D{D} {dtype} {mode} g{g} {what}", flush=True)
+    window = 45
+    p = Problem([rows, rows, rows], [rows + 171, rows + 54, rows + 20], 2, 2 if rows > 1 else 3, D, mode, g, dtype, 16, seed=41,
+                garbage=False)
+    clean = p.call(window=window)
+    p.check(clean, window=window)
+    hidden = np.zeros((p.cache.pages, 16), dtype=bool)
+    for b, n in enumerate(p.lengths_host):
+        for key in range(max(0, n - rows + 1 - window)):
+            hidden[p.table_host[b, key // 16], key % 16] = True
+    assert hidden.any()
+    hole = torch.from_numpy(hidden).to(DEV)[:, None, :, None]
+    for w in (p.cache.key, p.cache.value):
+        if mode != "affine":
+            w.scales.masked_fill_(hole, 255 if what == "nan" else (120 if mode == "nvfp4" else 140))
+        else:
+            w.scales.masked_fill_(hole, float("nan") if what == "nan" else 4000.0)
+            w.biases.masked_fill_(hole, float("inf") if what == "nan" else -3000.0)
+    assert torch.equal(p.call(window=window), clean)
