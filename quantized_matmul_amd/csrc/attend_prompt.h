@@ -172,7 +172,8 @@ __global__ void __launch_bounds__(256, prompt_residents(D, RT)) attend_prompt_ke
     if (split && split >= w.splits) return;
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid / 64), lane = tid % 64, r = lane % 32, hb = lane / 32;
     const int share = a.q_heads / c.heads;
-    const int k0 = w.k0 + split * t.chunk, k1 = w.splits ? min(w.hi, k0 + t.chunk) : k0;
+    const KeyRange keys = chunk_of(w, split, t.chunk);
+    const int k0 = keys.first, k1 = keys.end;
     const int kb0 = k0 / BK, kb1 = (k1 + BK - 1) / BK;
 
     auto row_at = [&](int i) { return min(w.row0 + i, w.row0 + w.rows - 1); };   // rows past the end repeat the last

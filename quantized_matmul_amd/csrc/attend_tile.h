@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
     }
     tile_keys(a, c, w, t.chunk, kKvUnit);
     if (split && split >= w.splits) return;
-    const int k0 = w.k0 + split * t.chunk, k1 = w.splits ? min(w.hi, k0 + t.chunk) : k0;
+    const KeyRange keys = chunk_of(w, split, t.chunk);
+    const int k0 = keys.first, k1 = keys.end;
     const int steps = (k1 - k0 + kStep - 1) / kStep;
     const int32_t* const table = a.table + (int64_t)w.b * a.width;
     auto look_up = [&](int first) {                        // row blocks of the keys of a window

@@ -146,7 +146,18 @@ QLIN_HD void tile_keys(const AttendArgs& a, const KvPool& c, TileWork& w, int ch
     w.lo = seen_by(a, w.s, w.row0 / share).lo;
     w.hi = seen_by(a, w.s, (w.row0 + w.rows - 1) / share).hi;
     w.k0 = w.lo & ~(unit - 1);
-    w.splits = w.hi > w.lo ? (w.hi - w.k0 + chunk - 1) / chunk : 0;
+    w.splits = w.hi > w.lo ? (w.hi - w.k0 - 1) / chunk + 1 : 0;
+}
+
+// Keys of chunk `split` of a tile (of its splits, or the first of none): no sum
+// here passes the tile's last key, which a chunk of any length may.
+struct KeyRange {
+    int first, end;
+};
+QLIN_HD KeyRange chunk_of(const TileWork& w, int split, int chunk) {
+    const int first = w.k0 + split * chunk;
+    if (!w.splits) return {first, first};
+    return {first, w.hi - first < chunk ? w.hi : first + chunk};
 }
 
 }  // namespace qlin

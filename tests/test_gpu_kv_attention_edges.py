@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_kv_attention import DEV, Problem
+from test_gpu_kv_attention import DEV, Problem, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +58,24 @@ def test_keys_before_the_window_may_be_anything(rows, D, dtype, mode, g, what):
             w.scales.masked_fill_(hole, float("nan") if what == "nan" else 4000.0)
             w.biases.masked_fill_(hole, float("inf") if what == "nan" else -3000.0)
     assert torch.equal(p.call(window=window), clean)
+
+
+@pytest.mark.parametrize("window", [300, 0])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sequences_of_2_to_the_30_keys_and_more(dtype, window):
+    """One page named again and again: its last places are what a window sees, and every place has the same share of a
+    softmax over all of it, however often it comes."""
+    page, pages = 1 << 18, 8191 if dtype == "bf16" else 4100
+    if dtype == "f32" and not window:
+        pytest.skip("the vector units take seconds for these")
+    print(f"long {dtype} window {window}", flush=True)
+    p = Problem([1], [page], 1, 2, 64, "affine", 64, dtype, page, seed=43, spare=0)
+    p.prompt = False
+    want, tol = p.want(window=window)
+    table = torch.zeros((1, pages), dtype=torch.int32, device=DEV)
+    lengths = torch.tensor([pages * page], dtype=torch.int32, device=DEV)
+    got = qm.kv_cache_attention(p.q, p.cache, table, lengths, window=window)
+    # as many fp32 additions as keys: each sum is off by up to sqrt(keys) of its roundings
+    tol = tol + (0 if window else 2 * np.sqrt(pages * page) * 2.0 ** -24 * np.abs(p.dense()[1]).max())
+    err = np.abs(f64(got) - want)
+    assert (err <= tol).all(), (err.max(), tol.min())
