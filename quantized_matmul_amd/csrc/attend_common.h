@@ -120,11 +120,13 @@ __global__ void __launch_bounds__(256) attend_join_kernel(TileArgs t, int tile_r
             x += f * *(const f32x4*)(o + (int64_t)i * tile_rows * D);
         }
     }
+    const f32x4 own = x;                         // what the lane itself has: sums in between would count twice
+    const float own_l = l;
 #pragma unroll
     for (int i = 1; i < AT_ONCE; ++i) {
-        l += __shfl(l, lane + i * L4, 64);
+        l += __shfl(own_l, lane + i * L4, 64);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] += __shfl(x[e], lane + i * L4, 64);
+        for (int e = 0; e < 4; ++e) x[e] += __shfl(own[e], lane + i * L4, 64);
     }
     if constexpr (WAVES > 1) {
         if (lane < L4) part_x[wave][lane] = x;
