@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
     constexpr int ROOM = (tile_residents(D, NT) == 3 ? 52 : 78) * 1024 - WAVES * WSCALES * 4;
     constexpr int ST = WAVES * 4 * STAGE <= ROOM ? 4 : (WAVES * 3 * STAGE <= ROOM ? 3 : 2);
     constexpr int ROW = D + 4;                             // floats of a row of o in LDS, rows on other banks
-    constexpr int REGIONS = WAVES * R * ROW * 4 <= 72 * 1024 ? WAVES : 1;
-    constexpr int RING = WAVES * ST * STAGE, BUF = RING > REGIONS * R * ROW * 4 ? RING : REGIONS * R * ROW * 4;
+    constexpr int RING = WAVES * ST * STAGE, SUMS = WAVES * R * ROW * 4, BUF = RING > SUMS ? RING : SUMS;
+    static_assert(SUMS <= 72 * 1024, "two workgroups a CU");
     __shared__ int32_t blocks[kWindow / kKvUnit];
     __shared__ __attribute__((aligned(16))) uint8_t ring[BUF];
     __shared__ __attribute__((aligned(16))) float numbers[WAVES * WSCALES];
@@ -740,41 +740,24 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
     __syncthreads();                                         // (the ring is read)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        float f = 1.0f;                                      // waves with a region of their own are weighted below
-        if constexpr (REGIONS < WAVES) {
-            float top = kNone;
-#pragma unroll
-            for (int i = 0; i < WAVES; ++i) top = fmaxf(top, wave_ml[i][n * PER + r % PER][0]);
-            f = m[n] == kNone ? 0.0f : __builtin_amdgcn_exp2f(m[n] - top);
-        }
         const float plus = PS ? zsum[n] - 24.0f * ones[n][0] : 0.0f;      // all rows of `ones` are the column's sum
 #pragma unroll
-        for (int i = 0; i < OT; ++i) o[n][i] = PS ? (o[n][i] + plus) * f : o[n][i] * (UNIT ? f * __builtin_ldexpf(1.0f, unit) : f);
-    }
-    for (int turn = 0; turn < WAVES / REGIONS; ++turn) {
-        if (turn == wave / REGIONS) {
+        for (int i = 0; i < OT; ++i) o[n][i] = PS ? o[n][i] + plus : (UNIT ? o[n][i] * __builtin_ldexpf(1.0f, unit) : o[n][i]);
+        if (n * PER + r % PER >= w.rows) continue;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (n * PER + r % PER >= w.rows) continue;
+        for (int v = 0; v < VC; ++v)
 #pragma unroll
-                for (int v = 0; v < VC; ++v)
+            for (int i = 0; i < 4; ++i) {
+                const int word = v * 16 + 4 * j + i;           // HALF: half-word
+                if (word >= D / CL || (PS && word * CL / G != r / PER)) continue;
+                f32x4* const at = (f32x4*)(buf + (wave * R + n * PER + r % PER) * ROW + word * CL);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int word = v * 16 + 4 * j + i;           // HALF: half-word
-                        if (word >= D / CL || (PS && word * CL / G != r / PER)) continue;
-                        f32x4* at = (f32x4*)(buf + (wave % REGIONS * R + n * PER + r % PER) * ROW + word * CL);
-#pragma unroll
-                        for (int u = 0; u < CL / 4; ++u) {
-                            f32x4 x{o[n][v * CL + 4 * u][i], o[n][v * CL + 4 * u + 1][i], o[n][v * CL + 4 * u + 2][i],
-                                    o[n][v * CL + 4 * u + 3][i]};
-                            if (turn) x += at[u];
-                            at[u] = x;
-                        }
-                    }
+                for (int u = 0; u < CL / 4; ++u)
+                    at[u] = f32x4{o[n][v * CL + 4 * u][i], o[n][v * CL + 4 * u + 1][i], o[n][v * CL + 4 * u + 2][i],
+                                  o[n][v * CL + 4 * u + 3][i]};
             }
-        }
-        __syncthreads();
     }
+    __syncthreads();
     const int64_t part = (tile * c.heads + h) * t.splits + split;
     for (int e = tid; e < w.rows * (D / 4); e += 64 * WAVES) {
         const int row = e / (D / 4), d = e % (D / 4) * 4;
@@ -788,8 +771,7 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
             sum = __builtin_fmaf(f[i], wave_ml[i][row][1], sum);
         }
 #pragma unroll
-        for (int i = 0; i < REGIONS; ++i)
-            x += *(const f32x4*)(buf + (i * R + row) * ROW + d) * (REGIONS == WAVES ? f[i] : 1.0f);
+        for (int i = 0; i < WAVES; ++i) x += *(const f32x4*)(buf + (i * R + row) * ROW + d) * f[i];
         if (w.splits <= 1) {
             x *= sum == 0.0f ? 0.0f : 1.0f / sum;                        // a row that sees no key: zeros
             const int rr = w.row0 + row;

@@ -43,11 +43,6 @@ __device__ __forceinline__ void sincos_turns(double r, float* s, float* c) {
     *c = (k == 1 || k == 2) ? -b : b;
 }
 
-template <int DT>
-__device__ __forceinline__ float load_one(const void* p, int64_t i) {
-    return load_f<DT>(p, i);
-}
-
 // NV elements (16 bytes) at element i; VEC: one 16-byte load.
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 
