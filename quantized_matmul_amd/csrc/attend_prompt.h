@@ -267,9 +267,9 @@ __global__ void __launch_bounds__(256, prompt_residents(D, RT)) attend_prompt_ke
 #pragma unroll
                 for (int d = 0; d < DTILES; ++d) o[n][d] *= f;
         }
-        // p is multiplied by 2^down, its sum back; where that is nothing beside the largest block, by no less than 2^-64.
-        // A block without values (zeros, pages that are not there) moves nothing and keeps its p.
-        const int fall = up == kNoPower ? 0 : max(up - unit, -64);
+        // p is multiplied by 2^down, its sum back; where that is nothing beside the largest block (or there are no values),
+        // by no less than 2^-64
+        const int fall = max(up - unit, -64);
         const float down = (float)fall, back = __builtin_ldexpf(1.0f, -fall);
         const bool whole = there == ~0ull && key0 >= see_last.lo && key0 + BK <= see_first.hi;
         const uint8_t* const kl = lds[buf] + hb * (BK * 16) + r * 16;
