@@ -155,9 +155,8 @@ struct KeyRange {
     int first, end;
 };
 QLIN_HD KeyRange chunk_of(const TileWork& w, int split, int chunk) {
-    const int first = w.k0 + split * chunk;
-    if (!w.splits) return {first, first};
-    return {first, w.hi - first < chunk ? w.hi : first + chunk};
+    const int first = w.k0 + split * chunk, left = w.splits ? w.hi - first : 0;
+    return {first, first + (left < chunk ? left : chunk)};
 }
 
 }  // namespace qlin
