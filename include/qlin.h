@@ -534,7 +534,8 @@ qlin_status qlin_kv_cache_read(const qlin_kv_cache* cache, const int32_t* slots,
  *     go with an f16 q there.
  *   - many: keys, values, p_j and a bf16 row of q are rounded to f16, in powers
  *     of two of the largest of a block of 64 keys, or of a row of q; what is
- *     small beside that keeps 2^-25 of it.
+ *     small beside that keeps 2^-25 of it; p_j keeps 2^-21 of the row's largest
+ *     where the values of its block are within 2^64 of the call's largest.
  * bf16 values may be of any size between 2^-110 and 2^110.
  * QLIN_ERR_UNSUPPORTED where one launch does not hold a call's rows (2^24
  * workgroups of 4 to 256 rows of a key head, with their chunks of keys).

@@ -13,9 +13,11 @@
 // softmax passes on, and bf16 values and p as much on the output (errors of a
 // bf16 output, whose own rounding is 0.0017: 0.0051; with f16 keys 0.0025, with
 // all in f16 0.0018). No value leaves f16's range; what is 2^-14 of the largest
-// of its block and less is held to 2^-25 of that. o is kept in units of the
-// largest block's power of two so far, p of other blocks divided accordingly; a
-// block without values has none.
+// of its block and less is held to 2^-25 of that. o is kept in units of a power
+// of two that follows the blocks': up to any larger one, and down where a block's
+// lies 2^4 and more below, so that p, divided by what is left between the two, is
+// held to 2^-21 at least (blocks within 2^64 of the largest; rows may see none but
+// small ones). A block without values has no power.
 // Decoding inside the attention kernel would cost every workgroup again what
 // this does once: 190 of about 560 vector instructions of 64 keys (D 128), where
 // the matrix cores need the time of 512.
@@ -51,6 +53,8 @@ typedef __attribute__((ext_vector_type(16))) float f32x16;
 
 constexpr int kImageKeys = 64;
 constexpr int kNoPower = -1000;                  // of zeros: below any number's
+constexpr int kFall = 4;                         // how far a block's power may lie below o's
+constexpr int kReach = 64;                       // how far o's may lie below the largest so far: o stays inside fp32
 
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -226,7 +230,7 @@ __global__ void __launch_bounds__(256, prompt_residents(D, RT)) attend_prompt_ke
 
     f32x16 o[RT][DTILES];
     float m[RT], l[RT];
-    int unit = kNoPower;                         // o's power of two
+    int unit = kNoPower, least = kNoPower;       // o's power of two; kReach below the largest so far
 #pragma unroll
     for (int n = 0; n < RT; ++n) {
         m[n] = kNone;
@@ -259,9 +263,11 @@ __global__ void __launch_bounds__(256, prompt_residents(D, RT)) attend_prompt_ke
         const int key0 = kb * BK;
         if (idle || key0 >= see_last.hi || key0 + BK <= see_first.lo) continue;
         const int up = __builtin_amdgcn_readfirstlane(value_power);
-        if (up > unit) {
-            const float f = __builtin_ldexpf(1.0f, unit == kNoPower ? 0 : unit - up);
-            unit = up;
+        least = max(least, up - kReach);
+        const int to = max(up, least);
+        if (__builtin_expect((unsigned)(unit - to) > (unsigned)kFall, 0) && up != kNoPower) {     // (1580 us, 1571 so)
+            const float f = __builtin_ldexpf(1.0f, unit == kNoPower ? 0 : unit - to);
+            unit = to;
 #pragma unroll
             for (int n = 0; n < RT; ++n)
 #pragma unroll
@@ -269,7 +275,7 @@ __global__ void __launch_bounds__(256, prompt_residents(D, RT)) attend_prompt_ke
         }
         // p is multiplied by 2^down, its sum back; where that is nothing beside the largest block (or there are no values),
         // by no less than 2^-64
-        const int fall = max(up - unit, -64);
+        const int fall = max(up - unit, -kReach);
         const float down = (float)fall, back = __builtin_ldexpf(1.0f, -fall);
         const bool whole = there == ~0ull && key0 >= see_last.lo && key0 + BK <= see_first.hi;
         const uint8_t* const kl = lds[buf] + hb * (BK * 16) + r * 16;

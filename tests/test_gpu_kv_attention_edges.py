@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_kv_attention import DEV, Problem, f64
+from test_gpu_kv_attention import DEV, DTYPES, Problem, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +79,37 @@ def test_sequences_of_2_to_the_30_keys_and_more(dtype, window):
     tol = tol + (0 if window else 2 * np.sqrt(pages * page) * 2.0 ** -24 * np.abs(p.dense()[1]).max())
     err = np.abs(f64(got) - want)
     assert (err <= tol).all(), (err.max(), tol.min())
+
+
+@pytest.mark.parametrize("power", [8, 20, 40, 60])
+@pytest.mark.parametrize("order", ["down", "up"])
+@pytest.mark.parametrize("D,dtype,mode,g", [(64, "bf16", "affine", 64), (128, "bf16", "mxfp4", 32), (192, "bf16", "affine", 32),
+                                            (128, "f16", "affine", 64)])
+def test_small_values_seen_beside_a_prompts_large_ones(D, dtype, mode, g, order, power):
+    """Rows whose window holds small values only, in a prompt whose other values are 2^power times as large, before them or
+    behind: what they lose is relative to the blocks of 64 keys that they see (p of 50 keys, each to 2^-21 of the row's largest)."""
+    if dtype == "f16" and power > 8:
+        pytest.skip("outside f16")
+    print(f"sizes {order} 2^{power} D{D} {dtype} {mode}", flush=True)
+    rows, window, page = 700, 50, 64
+    p = Problem([rows], [rows], 1, 2, D, mode, g, dtype, page, seed=44, garbage=False)
+    v = qm.dequantize(p.cache.value, torch.float32) * (1.0 if dtype == "bf16" else 2.0 ** -4)
+    # the sequence's middle pages are 2^-power of the others, or the others 2^-power of them
+    middle = torch.from_numpy(p.table_host[0, 3:8].astype(np.int64)).to(DEV)
+    is_middle = torch.zeros(v.shape[0], dtype=torch.bool, device=DEV)
+    is_middle[middle] = True
+    small = is_middle if order == "down" else ~is_middle
+    v = torch.where(small[:, None, None, None], v * 2.0 ** -power, v)
+    p.cache = qm.KVCache(p.cache.key, qm.quantize(v.to(DTYPES[dtype]).contiguous(), g, 4, mode))
+    got = p.call(window=window)
+    assert qm.last_path() == "kv_attention_prompt"
+    p.prompt = True
+    want, tol = p.want(window=window)
+    values = p.dense()[1]
+    tol = tol - 2.0 ** -24 * np.abs(values[p.table_host[0]]).max()       # that of the whole sequence's largest value
+    for i in range(rows):
+        blocks = np.unique(np.arange(max(0, i - window + 1), i + 1) // page)
+        tol[i] += (window * 2.0 ** -21 + 2.0 ** -24) * np.abs(values[p.table_host[0, blocks]]).max()
+    err = np.abs(f64(got) - want)
+    assert np.isfinite(f64(got)).all()
+    assert (err <= tol).all(), (err / tol).max()
