@@ -1,5 +1,5 @@
 """Attention over a 4-bit cache on the GPU where blocks of keys hold no values and where keys that no row sees are no
-numbers. Problems, formulas and tolerances are those of test_gpu_kv_attention."""
+numbers, sequences of 2^30 keys, sizes of values that change. Problems, formulas and tolerances are those of test_gpu_kv_attention."""
 import numpy as np
 import pytest
 import torch
@@ -113,3 +113,16 @@ def test_small_values_seen_beside_a_prompts_large_ones(D, dtype, mode, g, order,
     err = np.abs(f64(got) - want)
     assert np.isfinite(f64(got)).all()
     assert (err <= tol).all(), (err / tol).max()
+
+
+@pytest.mark.parametrize("rows", [1, 5, 300])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_the_same_call_gives_the_same_bits(rows, dtype):
+    """Between other work, on a workspace that held something else."""
+    p = Problem([rows, rows, 1], [5000, 3001, 700], 2, 4, 128, "affine", 64, dtype, 64, seed=42)
+    first = p.call()
+    need = qm.kv_cache_attention_workspace_bytes(p.cache, p.q.shape[0], 8, 3, p.table.shape[1], True, dtype=DTYPES[dtype])
+    for i in range(20):
+        ws = torch.full((max(need, 16),), 37 * i % 256, dtype=torch.uint8, device=DEV)
+        (torch.randn(1 << 18, device=DEV) * 2.0).sum()
+        assert torch.equal(p.call(workspace=ws), first)
