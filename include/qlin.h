@@ -520,7 +520,10 @@ qlin_status qlin_kv_cache_read(const qlin_kv_cache* cache, const int32_t* slots,
  *   workspace  device memory of at least qlin_kv_cache_attention_workspace_bytes
  *             bytes for the same sizes, 16-byte aligned (may be NULL where that
  *             is 0); overwritten, nothing in it counts before or after a call.
- *             Calls that share one must not overlap.
+ *             Calls that share one must not overlap. Many rows to a sequence
+ *             and key head take B * width * page_size * heads * head_dim * 4
+ *             bytes and more there, by the table's width, whatever the lengths;
+ *             above 8 GiB they run as few do.
  * Sizes alone choose how it runs, so a captured call may be replayed with other
  * lengths, tables and offsets in the same buffers. Scores, their softmax and
  * the sums are fp32. f16 and bf16 with head_dim 64, 96, 128, 192 or 256 run on

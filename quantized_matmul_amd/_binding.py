@@ -891,7 +891,8 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, len
     offsets[b] to offsets[b + 1] (int32 [B + 1]), the last of them at its last key, or row b alone without offsets.
     causal hides the keys behind a row's place, window > 0 those that many or more before it. scale is
     head_dim ** -0.5 by default. Rows of no sequence are left as they are in out (zeros without out); rows that see no
-    key become zeros.
+    key become zeros. Prompts take a workspace by the table's width, not the lengths (up to 8 GiB; qlin.h): a table no
+    wider than the longest sequence keeps it small.
     """
     lib = _lib or load_library()
     dev = cache.device

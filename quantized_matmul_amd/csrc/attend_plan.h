@@ -84,7 +84,8 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
                               (T <= B || c.D > 128 ? mean : 2 * mean) <= 16 / groups);
     const int dup = p.codes ? groups : 1;
     // 32 columns where the rows fill more than 16, as the codes are decoded once for them: 64 sequences of 64 rows over
-    // 16000 keys, D 128, 583 us, in tiles of 16 rows 666 (48 columns, of D 64, took 424 for 384)
+    // 16000 keys, D 128, 583 us, in tiles of 16 rows 666 (48 columns, of D 64, took 424 for 384: 48 + 16 rows instead of
+    // 32 + 32; 33 to 48 rows, which take a second tile that reads and decodes their keys again, were not measured)
     p.nt = mean > 16 && c.D <= 128 ? 2 : 1;
     p.rows = 16 / dup * p.nt;
     p.tiles = one_row ? B * ((share + p.rows - 1) / p.rows) : T * share / p.rows + B;
@@ -94,7 +95,7 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
     // done, as lengths differ. bf16, D 128, us: 32 sequences of 4000 to 16000 keys, always 768 workgroups 111, so 89;
     // 16 sequences of 1 to 5 rows of 32 heads over those keys 124, so 95; 5 sequences of 1 to 3 rows over 2000 to 8000
     // keys 26 and 26.
-    const int64_t slots = 256 * tile_residents(c.D, p.nt);
+    const int64_t slots = 256 * tile_residents(c.D, p.nt);     // (an MI355X has 256 CUs)
     const int64_t even = B * ((mean + p.rows - 1) / p.rows), ragged = T * share / p.rows + B / 2;
     const int64_t busy = (one_row ? p.tiles : (even > ragged ? even : ragged)) * c.heads;
     int64_t chunk = keys;

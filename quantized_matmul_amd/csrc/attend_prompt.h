@@ -34,7 +34,7 @@
 // otherwise RT = 1, in buffers of 32 keys, which three workgroups (two above 128)
 // hold at once.
 //
-// 8192 rows of 32 heads over 16384 keys of 8 (D 128, bf16): 1.53 to 1.6 ms, 1.03
+// 8192 rows of 32 heads over 16384 keys of 8 (D 128, bf16): 1.53 to 1.66 ms, 1.0
 // to 1.08 PFLOP/s; laying the keys out is 29 us of that. The matrix cores are
 // busy for half the cycles and the vector units (softmax) for as many, two waves
 // of a SIMD in turn, at 2.0 of 2.4 GHz. Priorities for either part, and barriers

@@ -13,7 +13,9 @@
 // LDS, one to three steps ahead, without a barrier: a wave waits for the count of
 // its own loads alone. What is ahead costs no registers that way, so that three
 // workgroups fit a CU: 64 x 8192 to 32768 keys, D 128, loads into registers 363
-// us, through the ring 344, three workgroups 294 (two 310).
+// us, through the ring 344, three workgroups 294 (two 310). Not so for affine
+// groups of 32 in 32 columns: 10 to 25 registers of o, q and the scales do not fit
+// (bf16 D 64, 96 and 128, f16 D 64 and 128), and their reloads wait for the ring.
 //
 // Products, 16 x 16 x 32:
 //   scores^T = K q^T. Lane (r = lane % 16, j = lane / 16) of K's operand holds
