@@ -112,7 +112,8 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
     p.chunk = (int)(chunk < (1 << 30) ? chunk : 1 << 30);
     p.splits = (int)((keys + kKvUnit + p.chunk - 1) / p.chunk);
     if (p.splits > 1) p.bytes = (size_t)(base * p.splits * p.rows) * (c.D + 2) * sizeof(float);
-    p.fits = base * p.splits <= kItems / 256;
+    // (the join takes a wave a row, four a workgroup)
+    p.fits = base * p.splits <= kItems / 256 && (p.splits == 1 || p.tiles * ((p.rows + 3) / 4) <= kItems / 256);
     return p;
 }
 

@@ -71,6 +71,25 @@ int main() {
                                         }
                                     }
     CHECK(calls > 10000);
+    // what fits the attention's launch fits the join's, too: a wave a row
+    int fit = 0;
+    for (int share : {1, 20, 64})
+        for (int64_t T : {(int64_t)1 << 12, (int64_t)1 << 20, (int64_t)1 << 22, ((int64_t)1 << 23) - 16, (int64_t)1 << 24})
+            for (int64_t width : {3, 65, 127})
+                for (int64_t B : {T, T / 4}) {
+                    KvPool c{};
+                    c.D = 64;
+                    c.g = 64;
+                    c.heads = 1;
+                    c.page = 1 << 24;
+                    c.pages = 1;
+                    const AttendPlan p = attend_plan(QLIN_BF16, T, share, B, width, c, 0, B == T);
+                    CHECK(p.path == 1);
+                    if (!p.fits || p.splits == 1) continue;
+                    CHECK(p.tiles * ((p.rows + 3) / 4) * 256 < (int64_t)1 << 32);
+                    ++fit;
+                }
+    CHECK(fit > 3);
     printf("ok\n");
     return 0;
 }
