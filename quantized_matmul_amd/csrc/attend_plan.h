@@ -54,7 +54,7 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
     int64_t keys = held;
     if (window && window < keys - T - 64) keys = window + T + 64;
     if (keys < 1) keys = 1;
-    const int64_t blocks = (held + 63) / 64;
+    const int64_t blocks = held ? (held + 63) / 64 : 1;
     if (mean > kPromptRows && blocks * B <= kImages / ((int64_t)c.heads * c.D * 256)) {
         p.path = 2;
         // tiles of 256 rows where they fill the chip (two workgroups a CU), or of 128 (three)
@@ -67,7 +67,7 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
         if (splits == 1) chunk = 1 << 30;
         p.chunk = (int)(chunk < (1 << 30) ? chunk : 1 << 30);
         p.splits = (int)((keys + 64 + p.chunk - 1) / p.chunk);
-        p.key_blocks = (int)(blocks ? blocks : 1);
+        p.key_blocks = (int)blocks;
         p.present_at = (size_t)B * p.key_blocks * c.heads * c.D * 256;
         p.part_at = (p.present_at + (size_t)B * p.key_blocks * (8 + 8 * c.heads) + 255) / 256 * 256;
         p.bytes = p.part_at + (p.splits > 1 ? (size_t)(base * p.splits * p.rows) * (c.D + 2) * sizeof(float) : 0);

@@ -90,6 +90,18 @@ int main() {
                     ++fit;
                 }
     CHECK(fit > 3);
+    // decoded keys and values take 8 GiB at most, also for tables without a page
+    for (int64_t width : {0, 1, 9, 5000})
+        for (int64_t B : {1, 7, 1000, 50000}) {
+            KvPool c{};
+            c.D = 128;
+            c.g = 64;
+            c.heads = 8;
+            c.page = 64;
+            c.pages = 10;
+            const AttendPlan p = attend_plan(QLIN_BF16, B * 600, 8, B, width, c, 0, false);
+            CHECK(p.present_at <= (size_t)1 << 33);
+        }
     printf("ok\n");
     return 0;
 }
