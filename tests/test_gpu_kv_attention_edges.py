@@ -126,3 +126,31 @@ def test_the_same_call_gives_the_same_bits(rows, dtype):
         ws = torch.full((max(need, 16),), 37 * i % 256, dtype=torch.uint8, device=DEV)
         (torch.randn(1 << 18, device=DEV) * 2.0).sum()
         assert torch.equal(p.call(workspace=ws), first)
+
+
+@pytest.mark.parametrize("rows", [3, 300])
+def test_a_padded_batch_captured_without_an_output(rows):
+    """The output and its zeros for rows of no sequence are the graph's own: every replay writes both anew."""
+    p = Problem([rows, rows], [400, 350], 2, 2, 128, "affine", 64, "bf16", 32, seed=45)
+    q = torch.cat([p.q, torch.full((7, 4, 128), float("nan"), device=DEV, dtype=p.q.dtype)])
+
+    def call():
+        return qm.kv_cache_attention(q, p.cache, p.table, p.lengths, offsets=p.offsets)
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            out = call()
+    torch.cuda.current_stream().wait_stream(stream)
+    for lengths in ([400, 350], [rows, 0], [399, 1], [400, 350]):
+        p.lengths.copy_(torch.tensor(lengths, dtype=torch.int32))
+        want = call()
+        (torch.randn(1 << 16, device=DEV) * 2.0).sum()
+        out.fill_(5.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and (out[2 * rows :] == 0).all()
