@@ -63,6 +63,16 @@ __device__ __forceinline__ uint32_t round2(float a, float b) {
     else return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), f16x2));
 }
 
+// sum plus the two numbers of a pair that round2 made, exact but for the sums' own
+// rounding (subnormal f16 numbers among them).
+template <int DT>
+__device__ __forceinline__ float add2(uint32_t pair, float sum) {
+    if constexpr (DT == QLIN_BF16)
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), bf16x2{(__bf16)1.0f, (__bf16)1.0f}, sum, false);
+    else
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, pair), f16x2{(_Float16)1.0f, (_Float16)1.0f}, sum, false);
+}
+
 struct TileArgs {
     AttendArgs a;
     KvPool c;

@@ -17,7 +17,9 @@
 // of two that follows the blocks': up to any larger one, and down where a block's
 // lies 2^4 and more below, so that p, divided by what is left between the two, is
 // held to 2^-21 at least (blocks within 2^64 of the largest; rows may see none but
-// small ones). A block without values has no power.
+// small ones). A block without values has no power. f16 rows add up p as it
+// multiplies the values, rounded, so that their weights make one (equal values come
+// out as they are; in bf16 that does not show, and cost 2 %).
 // Decoding inside the attention kernel would cost every workgroup again what
 // this does once: 190 of about 560 vector instructions of 64 keys (D 128), where
 // the matrix cores need the time of 512.
@@ -327,11 +329,21 @@ __global__ void __launch_bounds__(256, prompt_residents(D, RT)) attend_prompt_ke
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     s[n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], to_log2, -base));
-                    sum += s[n][i];
+                    if constexpr (DT == QLIN_BF16) sum += s[n][i];
                 }
-                l[n] = __builtin_fmaf(sum, back, l[n]);
+                if constexpr (DT == QLIN_BF16) l[n] = __builtin_fmaf(sum, back, l[n]);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) p[n][i / 4][i % 4] = round2<QLIN_F16>(s[n][2 * i], s[n][2 * i + 1]);
+                if constexpr (DT == QLIN_F16) {      // of p as it multiplies the values, unless that is nothing
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sum = add2<QLIN_F16>(p[n][i / 4][i % 4], sum);
+                    if (__builtin_expect(fall < -kFall, 0)) {
+                        sum = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) sum += s[n][i];
+                    }
+                    l[n] = __builtin_fmaf(sum, back, l[n]);
+                }
             }
 #pragma unroll
             for (int k = 0; k < 2; ++k)

@@ -46,7 +46,9 @@
 //       64 x 5000 to 20000 keys, D 128, groups of 64: 252 us decoded, 228 as codes
 //       (outputs off by 0.0021 where rounding alone is 0.0017).
 //   Rounded on the way: p s to bf16 (as codes); p and decoded values to f16; mxfp4's
-//   p to the type, its values not at all, nor nvfp4's. Sums, m and l are fp32.
+//   p to the type, its values not at all, nor nvfp4's. Sums, m and l are fp32; l adds
+//   up p as it multiplies the values, rounded, so that a row's weights make one (bf16
+//   mxfp4: outputs off by 1.15 times their own rounding where exact p had 1.27).
 //
 // Scales go through LDS a second time, as numbers (a lane there needs those of
 // eight keys); keys that no row of the tile sees (behind its end, before its
@@ -584,7 +586,7 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     x[e] = __builtin_amdgcn_exp2f(x[e]);
-                    l[n] += x[e];
+                    if constexpr (PS) l[n] += x[e];
                 }
                 if constexpr (PS) {                          // p times the scales of the column's group; the biases' part
                     const int group = min(r / PER, NG - 1);
@@ -601,7 +603,10 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p[n][i] = round2<VT>(x[2 * i], x[2 * i + 1]);
+                for (int i = 0; i < 4; ++i) {
+                    p[n][i] = round2<VT>(x[2 * i], x[2 * i + 1]);
+                    if constexpr (!PS) l[n] = add2<VT>(p[n][i], l[n]);     // as it multiplies the values: see the top
+                }
                 if constexpr (PS) ones[n] = mfma16<DT>(u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}, p[n], ones[n]);
             }
             // values: word v*16 + r of the lane's eight keys
