@@ -31,9 +31,10 @@
 //     (r, j) of V's operand takes word r of those eight keys: its eight codes are
 //     eight rows of V^T. Two ways to make them numbers:
 //     - decoded: fl(s c + z) as f16 by packed instructions, two keys each. bf16
-//       values are in units of a power of two that follows the largest one so far
-//       (a wave's; o is scaled where it moves): no value leaves f16's range, and
-//       what is small beside the largest keeps 2^-25 of it. In bf16, p and the
+//       values are in units of a power of two that follows the largest of a step
+//       (a wave's; o is scaled where it moves), up by 2^15, down by 2^6: no value
+//       leaves f16's range, and what is small beside the step's largest keeps 2^-19
+//       of it (steps within 2^64 of the largest so far). In bf16, p and the
 //       values put 0.0015 on outputs that round by 0.0017 themselves; in f16 nothing
 //       that shows, in the same time (64 rows, groups of 32: 82 us for 75).
 //     - as codes (PS; bf16 affine): p takes the scale and the codes stay 16 + c,
@@ -299,9 +300,11 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
 #pragma unroll
         for (int i = 0; i < OT; ++i) o[n][i] = f32x4{0, 0, 0, 0};
     }
-    // UNIT: o and the values are in units of 2^unit, which follows the largest value so far where one passes it by 2^15
-    float largest = 0.0f, to_unit = 1.0f;
-    int unit = 0;
+    // UNIT: o and the values are in units of 2^unit, which follows the largest of a step: up where values would leave f16,
+    // down where little of them would be left
+    constexpr int kUp = 15, kDown = 6, kReach = 64;
+    float largest = 0.0f, least = -1.0f, to_unit = 1.0f;
+    int unit = 0, unit_least = -120;                         // (2^-unit is a number; o stays inside fp32)
     const float scale = a.scale * kLog2e;
     float* const sl = numbers + wave * WSCALES;                          // this wave's scales: [array, group, key]
     constexpr int SE = (kStep * NG + 63) / 64;                           // a lane's numbers of an array
@@ -458,19 +461,23 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
                 float most = 0.0f;
 #pragma unroll
                 for (int e = 0; e < SE; ++e) most = fmaxf(most, __builtin_fmaf(fabsf(x[e][1]), 15.0f, fabsf(x[e][3])));
-                if (__any(most > largest)) {
+                if (__any(most > largest) || !__any(most > least)) {
                     out_of_line();
 #pragma unroll
                     for (int off = 32; off; off /= 2) most = fmaxf(most, __shfl_xor(most, off, 64));
-                    const int to = max(ilogb_of(most), -120);      // (2^-to is a number)
-                    const float f = largest == 0.0f ? 1.0f : __builtin_ldexpf(1.0f, unit - to);
-                    unit = to;
-                    to_unit = __builtin_ldexpf(1.0f, -to);
-                    largest = __builtin_ldexpf(1.0f, to + 15);
+                    const int of = __builtin_amdgcn_readfirstlane(ilogb_of(most)), to = max(of, unit_least);
+                    if (__any(most > 0.0f) && (largest == 0.0f || to != unit)) {
+                        const float f = largest == 0.0f ? 1.0f : __builtin_ldexpf(1.0f, unit - to);
+                        unit = to;
+                        unit_least = max(unit_least, to - kReach);
+                        to_unit = __builtin_ldexpf(1.0f, -to);
+                        largest = __builtin_ldexpf(1.0f, to + kUp);
+                        least = to == unit_least ? -1.0f : __builtin_ldexpf(1.0f, to - kDown);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int i = 0; i < OT; ++i) o[n][i] *= f;
+                            for (int i = 0; i < OT; ++i) o[n][i] *= f;
+                    }
                 }
 #pragma unroll
                 for (int e = 0; e < SE; ++e) {

@@ -1,13 +1,38 @@
 """Attention over a 4-bit cache on the GPU: what the matrix cores' 16-bit operands may cost. Problems and formulas are those
 of test_gpu_kv_attention, tolerances narrower where a rounding is left out."""
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_kv_attention import DEV, DTYPES, Problem, rand
+import kv_reference as ref
+from test_gpu_kv_attention import DEV, DTYPES, UNIT, Problem, f64, rand
 
 pytestmark = pytest.mark.gpu
 
 qm = pytest.importorskip("quantized_matmul_amd")
+
+
+def bound(p, window, pv, codes, causal=True):
+    """What attention has to give, and how far off it may be: test_gpu_kv_attention's terms, with p and values rounded to pv
+    each (codes: p times the scale, which multiplies c - 8) and keys that are exact."""
+    pools, q, first = p.dense(), f64(p.q), 0
+    out, tol, u = np.zeros(q.shape), np.zeros(q.shape), UNIT[p.dtype]
+    for b, (n, L) in enumerate(zip(p.rows, p.lengths_host)):
+        i = np.arange(L)
+        k, v = [x[p.table_host[b, i // p.page], :, i % p.page] for x in pools]
+        rows = slice(first, first + n)
+        o, size, _ = ref.attention(q[rows], k, v, n, p.D ** -0.5, causal, window)
+        if codes:
+            s = np.repeat(f64(p.cache.value.scales), p.g, -1)[p.table_host[b, i // p.page], :, i % p.page]
+            rounded = ref.attention(q[rows], k, v, n, p.D ** -0.5, causal, window, None, 8 * s)[1] * pv
+        else:
+            rounded = 2 * size * pv
+        d = 4 * np.sqrt(p.D) * 2.0 ** -24 * p.D ** -0.5 * np.abs(q[rows]).sum(-1, keepdims=True) * 6 * np.abs(k).max()
+        out[rows] = o
+        tol[rows] = rounded + size * (2 * d + 2.0 ** -22 + (np.sqrt(L) + 8) * 2.0 ** -24) + u * np.abs(o) \
+            + 2.0 ** -24 * np.abs(v).max() + (2.0 ** -24 if p.dtype == "f16" else 0)
+        first += n
+    return out, tol
 
 
 @pytest.mark.parametrize("rows", [1, 5, 40, 300])
@@ -28,3 +53,39 @@ def test_equal_values_come_out_as_they_are(D, dtype, mode, g, rows):
     got = p.call(window=window)
     want = torch.from_numpy(p.dense()[1][0, :, 0]).to(DTYPES[dtype]).to(DEV).repeat_interleave(3, 0)
     assert torch.equal(got, want.expand_as(got))
+
+
+@pytest.mark.parametrize("power", [10, 20, 40, 60])
+@pytest.mark.parametrize("order", ["down", "up"])
+@pytest.mark.parametrize("D,g,G", [(128, 32, 1), (128, 64, 1), (64, 32, 20), (256, 64, 3), (128, 128, 2)])
+def test_small_values_that_take_all_the_weight_beside_large_ones(D, g, G, order, power):
+    """Tokens whose weight lies on values that are 2^-power of others, whose keys they turn away from."""
+    print(f"weights {order} 2^{power} D{D} g{g} G{G}", flush=True)
+    p = Problem([1, 1], [630, 400], 1, G, D, "affine", g, "bf16", 64, seed=48, garbage=False)    # one workgroup each
+    p.q = (p.q[:, :1] + 0.1 * p.q).bfloat16()                # the heads of a token look the same way
+    k, v = [qm.dequantize(w, torch.float32) for w in (p.cache.key, p.cache.value)]
+    for b in range(2):
+        n = -(-p.lengths_host[b] // 64)
+        large = [i for i in range(n) if ((i * 5 // n) % 2 == 0) == (order == "down")]
+        at = torch.from_numpy(p.table_host[b, large].astype(np.int64)).to(DEV)
+        away = p.q[b].float().mean(0)
+        k[at] = -away * (150 * D ** 0.5 / (away * away).sum()) + 0.02 * k[at]
+        small = torch.ones(v.shape[0], dtype=torch.bool, device=DEV)
+        small[at] = False
+        mine = torch.zeros_like(small)
+        mine[torch.from_numpy(p.table_host[b, :n].astype(np.int64)).to(DEV)] = True
+        v[small & mine] *= 2.0 ** -power
+    p.cache = qm.KVCache(*[qm.quantize(x.bfloat16().contiguous(), g, 4) for x in (k, v)])
+    got = p.call()
+    assert qm.last_path() == "kv_attention_rows"
+    want, tol = bound(p, 0, 2.0 ** -11, False)
+    values = np.abs(p.dense()[1])
+    for b in range(2):
+        mine = p.table_host[b, : -(-p.lengths_host[b] // 64)]
+        largest = values[mine].max()
+        low = np.min([values[i].max() for i in mine])        # the small pages' largest
+        # of the large keys e^-120 is left; what is small in a page keeps 2^-19 of its largest, |z| + 15 s up to 3 of those
+        tol[b] += -2.0 ** -24 * largest + 3 * 2.0 ** -18 * low + 2.0 ** -160 * largest
+    err = np.abs(f64(got) - want)
+    assert np.isfinite(f64(got)).all() and (np.abs(want).max() < 100 * low)
+    assert (err <= tol).all(), (err / tol).max()
