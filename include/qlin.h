@@ -529,10 +529,10 @@ qlin_status qlin_kv_cache_read(const qlin_kv_cache* cache, const int32_t* slots,
  * the sums are fp32. f16 and bf16 with head_dim 64, 96, 128, 192 or 256 run on
  * the matrix cores, with operands of 16 bits:
  *   - few rows to a sequence and key head: keys exactly; each p_j and each
- *     "affine" value is rounded to f16 once, bf16 values in units of a power of
- *     two that follows the largest of 32 keys (small ones keep 2^-19 of that, where
- *     it is within 2^64 of the largest of all), or, in few groups, p_j times the
- *     value's scale to bf16, with its code; "mxfp4": p_j to
+ *     "affine" value (or, for bf16 in few groups, p_j times the value's scale, with
+ *     its code) is rounded to f16 once, for bf16 in units of a power of two that
+ *     follows the largest value (scale) of 32 keys: small ones keep 2^-19 of that,
+ *     where it is within 2^64 of the largest of all; "mxfp4": p_j to
  *     dtype, "nvfp4": to f16, values exactly (a bf16 row of q as f16 in a power of
  *     two of its largest value there). "mxfp4" values outside f16's range do not
  *     go with an f16 q there.

@@ -43,13 +43,15 @@
 //       (DUP), and 16 columns hold 16 / groups rows. What is left of each value is
 //       z + 8 s (summed in fp32) and 8 s too many of 16 + c - 8, taken off at the
 //       end as 24 times the sum of the rounded p s, which a product with ones
-//       gives: what p s lost by rounding multiplies c - 8, not 16 + c.
-//       64 x 5000 to 20000 keys, D 128, groups of 64: 252 us decoded, 228 as codes
-//       (outputs off by 0.0021 where rounding alone is 0.0017).
-//   Rounded on the way: p s to bf16 (as codes); p and decoded values to f16; mxfp4's
-//   p to the type, its values not at all, nor nvfp4's. Sums, m and l are fp32; l adds
-//   up p as it multiplies the values, rounded, so that a row's weights make one (bf16
-//   mxfp4: outputs off by 1.15 times their own rounding where exact p had 1.27).
+//       gives: what p s lost by rounding multiplies c - 8, not 16 + c. p s is f16 in
+//       units that follow the largest scale of a step, as those of decoded values
+//       do: outputs are off by their own rounding, 0.0017, where p s in bf16 made it
+//       0.0021 (64 x 8192 to 32768 keys 296 us, in bf16 294).
+//       64 x 5000 to 20000 keys, D 128, groups of 64: 252 us decoded, 228 as codes.
+//   Rounded on the way: p s (as codes), p and decoded values to f16; mxfp4's p to the
+//   type, its values not at all, nor nvfp4's. Sums, m and l are fp32; l adds up p as
+//   it multiplies the values, rounded, so that a row's weights make one (bf16 mxfp4:
+//   outputs off by 1.15 times their own rounding where exact p had 1.27).
 //
 // Scales go through LDS a second time, as numbers (a lane there needs those of
 // eight keys); keys that no row of the tile sees (behind its end, before its
@@ -57,7 +59,7 @@
 //
 // Bound by the memory: D/2 bytes and the scales of a key and of a value, read
 // once for the tile's rows. 64 sequences of 8192 to 32768 keys (D 128, 8 heads,
-// groups of 64) are 1.48 GB, 293 us with the join: 5.1 TB/s of the 6.2 that a
+// groups of 64) are 1.48 GB, 296 us with the join: 5.0 TB/s of the 6.2 that a
 // plain read reaches; the vector units are busy for three quarters of that time.
 #pragma once
 
@@ -207,9 +209,9 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
     constexpr int VC = (HW + 15) / 16;                     // words of a value a lane takes
     constexpr int CL = HALF ? 4 : 8, OT = VC * CL;         // codes of a word it takes; tiles of o
     constexpr bool AFF = MODE == AFFINE;
-    // types of the products' operands: all of nvfp4 fits f16; decoded bf16 values are f16 in a power of two
+    // types of the products' operands: all of nvfp4 fits f16; bf16 values (or p times their scales) are f16 in a power of two
     constexpr int KT = MODE == NVFP4 ? (int)QLIN_F16 : DT;
-    constexpr bool UNIT = AFF && DT == QLIN_BF16 && !PS;
+    constexpr bool UNIT = AFF && DT == QLIN_BF16;
     constexpr int VT = UNIT ? (int)QLIN_F16 : KT;
     static_assert(!PS || (AFF && NG <= 4 && DT == QLIN_BF16), "values as codes");
     constexpr int ARR = AFF ? 4 : 2;                       // scale arrays of a step: keys', values', biases in the same order
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
     f32x4 o[NT][OT], ones[NT];
     // p = exp2(score - base), base being m + kUnder, or 0 while there is no m. kUnder keeps sums of bf16's largest values
     // inside fp32; f16, whose values cannot leave it, has no bits to give for that.
-    constexpr float kUnder = VT == QLIN_BF16 ? kSlack : 0.0f;
+    constexpr float kUnder = VT == QLIN_BF16 || PS ? kSlack : 0.0f;
     float m[NT], l[NT], zsum[NT], base[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -300,9 +302,9 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
 #pragma unroll
         for (int i = 0; i < OT; ++i) o[n][i] = f32x4{0, 0, 0, 0};
     }
-    // UNIT: o and the values are in units of 2^unit, which follows the largest of a step: up where values would leave f16,
-    // down where little of them would be left
-    constexpr int kUp = 15, kDown = 6, kReach = 64;
+    // UNIT: o and the values (PS: the scales) are in units of 2^unit, which follows the largest of a step: up where that
+    // would leave f16 (of the value, of p times the scale), down where little of it would be left
+    constexpr int kHead = PS ? 6 : 0, kUp = PS ? 8 : 15, kDown = 6, kReach = 64;     // (p is 2^-kUnder at first)
     float largest = 0.0f, least = -1.0f, to_unit = 1.0f;
     int unit = 0, unit_least = -120;                         // (2^-unit is a number; o stays inside fp32)
     const float scale = a.scale * kLog2e;
@@ -460,29 +462,32 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
             if constexpr (UNIT) {
                 float most = 0.0f;
 #pragma unroll
-                for (int e = 0; e < SE; ++e) most = fmaxf(most, __builtin_fmaf(fabsf(x[e][1]), 15.0f, fabsf(x[e][3])));
+                for (int e = 0; e < SE; ++e)
+                    most = fmaxf(most, PS ? fabsf(x[e][1]) : __builtin_fmaf(fabsf(x[e][1]), 15.0f, fabsf(x[e][3])));
                 if (__any(most > largest) || !__any(most > least)) {
                     out_of_line();
 #pragma unroll
                     for (int off = 32; off; off /= 2) most = fmaxf(most, __shfl_xor(most, off, 64));
-                    const int of = __builtin_amdgcn_readfirstlane(ilogb_of(most)), to = max(of, unit_least);
+                    const int of = __builtin_amdgcn_readfirstlane(ilogb_of(most)), to = max(of - kHead, unit_least);
                     if (__any(most > 0.0f) && (largest == 0.0f || to != unit)) {
                         const float f = largest == 0.0f ? 1.0f : __builtin_ldexpf(1.0f, unit - to);
                         unit = to;
                         unit_least = max(unit_least, to - kReach);
                         to_unit = __builtin_ldexpf(1.0f, -to);
-                        largest = __builtin_ldexpf(1.0f, to + kUp);
-                        least = to == unit_least ? -1.0f : __builtin_ldexpf(1.0f, to - kDown);
+                        largest = __builtin_ldexpf(1.0f, to + kHead + kUp);
+                        least = to == unit_least ? -1.0f : __builtin_ldexpf(1.0f, to + kHead - kDown);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
+                        for (int n = 0; n < NT; ++n) {
+                            if constexpr (PS) ones[n] *= f;
 #pragma unroll
                             for (int i = 0; i < OT; ++i) o[n][i] *= f;
+                        }
                     }
                 }
 #pragma unroll
                 for (int e = 0; e < SE; ++e) {
                     x[e][1] *= to_unit;
-                    x[e][3] *= to_unit;
+                    if constexpr (!PS) x[e][3] *= to_unit;
                 }
             }
 #pragma unroll
@@ -614,7 +619,7 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
                     p[n][i] = round2<VT>(x[2 * i], x[2 * i + 1]);
                     if constexpr (!PS) l[n] = add2<VT>(p[n][i], l[n]);     // as it multiplies the values: see the top
                 }
-                if constexpr (PS) ones[n] = mfma16<DT>(u32x4{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}, p[n], ones[n]);
+                if constexpr (PS) ones[n] = mfma16<VT>(u32x4{0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u}, p[n], ones[n]);
             }
             // values: word v*16 + r of the lane's eight keys
 #pragma unroll
@@ -626,10 +631,10 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
                         for (int e = 0; e < 4; ++e) x[e] = __builtin_amdgcn_perm(vw[2 * e + 1][v], vw[2 * e][v], halves);
                         auto one = [&](auto ic) {
                             constexpr int I = decltype(ic)::value;
-                            const u32x4 vt{sixteen_plus<DT, I>(x[0], mask, sixteen), sixteen_plus<DT, I>(x[1], mask, sixteen),
-                                           sixteen_plus<DT, I>(x[2], mask, sixteen), sixteen_plus<DT, I>(x[3], mask, sixteen)};
+                            const u32x4 vt{sixteen_plus<VT, I>(x[0], value_mask, value_sixteen), sixteen_plus<VT, I>(x[1], value_mask, value_sixteen),
+                                           sixteen_plus<VT, I>(x[2], value_mask, value_sixteen), sixteen_plus<VT, I>(x[3], value_mask, value_sixteen)};
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) o[n][v * CL + to + I] = mfma16<DT>(vt, p[n], o[n][v * CL + to + I]);
+                            for (int n = 0; n < NT; ++n) o[n][v * CL + to + I] = mfma16<VT>(vt, p[n], o[n][v * CL + to + I]);
                         };
                         one(std::integral_constant<int, 0>{});
                         one(std::integral_constant<int, 1>{});
@@ -754,9 +759,10 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
     __syncthreads();                                         // (the ring is read)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const float plus = PS ? zsum[n] - 24.0f * ones[n][0] : 0.0f;      // all rows of `ones` are the column's sum
+        const float too_much = PS ? 24.0f * ones[n][0] : 0.0f;            // all rows of `ones` are the column's sum
+        const float one = UNIT ? __builtin_ldexpf(1.0f, unit) : 1.0f;
 #pragma unroll
-        for (int i = 0; i < OT; ++i) o[n][i] = PS ? o[n][i] + plus : (UNIT ? o[n][i] * __builtin_ldexpf(1.0f, unit) : o[n][i]);
+        for (int i = 0; i < OT; ++i) o[n][i] = PS ? (o[n][i] - too_much) * one + zsum[n] : (UNIT ? o[n][i] * one : o[n][i]);
         if (n * PER + r % PER >= w.rows) continue;
 #pragma unroll
         for (int v = 0; v < VC; ++v)

@@ -89,3 +89,23 @@ def test_small_values_that_take_all_the_weight_beside_large_ones(D, g, G, order,
     err = np.abs(f64(got) - want)
     assert np.isfinite(f64(got)).all() and (np.abs(want).max() < 100 * low)
     assert (err <= tol).all(), (err / tol).max()
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("D,g,G", [(64, 32, 2), (64, 64, 4), (96, 32, 1), (128, 64, 2), (128, 128, 4), (192, 64, 1), (256, 64, 1)])
+def test_weights_of_values_as_codes(D, g, G, rows):
+    """bf16 tokens: what p times a group's scale, which multiplies its codes, loses does not show beside the output's rounding.
+
+    Rounded to f16 it is off by 2^-11 / sqrt(3) of p s |c - 8| in the mean square, independent for each key; p s |c - 8| is
+    about p |v| here (values around zero), whose squares' sum is at most max |v| |o| where few keys hold the weight. The
+    output's rounding to bf16 is off by 2^-9 / sqrt(3) of it and more: a quarter at most, and sqrt(1 + 1 / 16) = 1.03 of
+    it in all; 1.1 leaves room for |v| above |o|."""
+    print(f"codes D{D} g{g} G{G} rows {rows}", flush=True)
+    p = Problem([rows] * 12, [40 + 37 * i for i in range(12)], 4, G, D, "affine", g, "bf16", 16, seed=49, std=2.5, garbage=False)
+    got = p.call()
+    assert qm.last_path() == "kv_attention_rows"
+    want, _ = bound(p, 0, 0.0, False)
+    rounding = f64(torch.from_numpy(want).bfloat16()) - want
+    off = np.sqrt(((f64(got) - want) ** 2).mean() / (rounding ** 2).mean())
+    print(f"error over that of rounding: {off:.3f}")
+    assert off <= 1.1
