@@ -522,7 +522,7 @@ qlin_status qlin_kv_cache_read(const qlin_kv_cache* cache, const int32_t* slots,
  *             is 0); overwritten, nothing in it counts before or after a call.
  *             Calls that share one must not overlap. Many rows to a sequence
  *             and key head take B * width * page_size * heads * head_dim * 4
- *             bytes and more there, by the table's width, whatever the lengths;
+ *             bytes (* 6: f16, "affine") and more there, by the table's width, whatever the lengths;
  *             above 8 GiB they run as few do.
  * Sizes alone choose how it runs, so a captured call may be replayed with other
  * lengths, tables and offsets in the same buffers. Scores, their softmax and
@@ -539,7 +539,9 @@ qlin_status qlin_kv_cache_read(const qlin_kv_cache* cache, const int32_t* slots,
  *   - many: keys, values, p_j and a bf16 row of q are rounded to f16, in powers
  *     of two of the largest of a block of 64 keys, or of a row of q; what is
  *     small beside that keeps 2^-25 of it; p_j keeps 2^-21 of the row's largest
- *     where the values of its block are within 2^64 of the call's largest.
+ *     where the values of its block are within 2^64 of the call's largest. An f16
+ *     q takes "affine" keys as two f16 numbers each, the second the first one's
+ *     rest.
  * bf16 values may be of any size between 2^-110 and 2^110.
  * QLIN_ERR_UNSUPPORTED where one launch does not hold a call's rows (2^24
  * workgroups of 4 to 256 rows of a key head, with their chunks of keys).

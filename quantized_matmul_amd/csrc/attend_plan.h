@@ -26,6 +26,9 @@ struct AttendPlan {
 // of the registers; rings of loads, what fits LDS).
 constexpr int tile_residents(int D, int NT) { return D * NT <= 128 ? 3 : (D * NT <= 256 ? 2 : 1); }
 
+// f16 prompts take affine keys as two f16 numbers each, whose sum has their bits.
+constexpr bool prompt_halves(int dt, int mode) { return dt == QLIN_F16 && mode == 0; }
+
 inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t width, const KvPool& c, int64_t window,
                               bool one_row) {
     constexpr int64_t kStepKeys = 128;       // keys that the four waves of a workgroup take at a time
@@ -40,6 +43,7 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
     const int64_t kPromptRows = c.D <= 128 ? 512 : 192;
     constexpr int64_t kImages = 1LL << 33;   // bytes of decoded keys and values at most
     constexpr int64_t kItems = (1LL << 32) - 1024;     // work-items of a launch
+    const int64_t key_bytes = c.D * (prompt_halves(dt, c.mode) ? 6 : 4);     // of a decoded key and its value
     AttendPlan p{};
     const int64_t share = q_heads / c.heads;
     const int64_t held = width > kKvMaxKeys / c.page ? kKvMaxKeys : width * c.page;
@@ -55,7 +59,7 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
     if (window && window < keys - T - 64) keys = window + T + 64;
     if (keys < 1) keys = 1;
     const int64_t blocks = held ? (held + 63) / 64 : 1;
-    if (mean > kPromptRows && blocks * B <= kImages / ((int64_t)c.heads * c.D * 256)) {
+    if (mean > kPromptRows && blocks * B <= kImages / (c.heads * key_bytes * 64)) {
         p.path = 2;
         // tiles of 256 rows where they fill the chip (two workgroups a CU), or of 128 (three)
         p.rows = c.D <= 128 && (T * share / 256 + B) * c.heads >= 512 ? 256 : 128;
@@ -68,7 +72,7 @@ inline AttendPlan attend_plan(int dt, int64_t T, int q_heads, int64_t B, int64_t
         p.chunk = (int)(chunk < (1 << 30) ? chunk : 1 << 30);
         p.splits = (int)((keys + 64 + p.chunk - 1) / p.chunk);
         p.key_blocks = (int)blocks;
-        p.present_at = (size_t)B * p.key_blocks * c.heads * c.D * 256;
+        p.present_at = (size_t)(B * p.key_blocks * c.heads * key_bytes * 64);
         p.part_at = (p.present_at + (size_t)B * p.key_blocks * (8 + 8 * c.heads) + 255) / 256 * 256;
         p.bytes = p.part_at + (p.splits > 1 ? (size_t)(base * p.splits * p.rows) * (c.D + 2) * sizeof(float) : 0);
         p.fits = base * p.splits <= kItems / 256;

@@ -20,6 +20,11 @@
 // small ones). A block without values has no power. f16 rows add up p as it
 // multiplies the values, rounded, so that their weights make one (equal values come
 // out as they are; in bf16 that does not show, and cost 2 %).
+// f16 prompts take affine keys as two f16 numbers, the second the first one's rest,
+// and two products: with one, scores made outputs 2.5 times as far off as their own
+// rounding, with both 1.43 (p's and the values' rounding). 8192 rows over 16384
+// keys (D 128) 1.75 and 2.28 ms, 4096 over 8192 of D 256, which then has the CU's
+// LDS to itself, 0.91 and 1.64.
 // Decoding inside the attention kernel would cost every workgroup again what
 // this does once: 190 of about 560 vector instructions of 64 keys (D 128), where
 // the matrix cores need the time of 512.
@@ -65,7 +70,8 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
 // A block of 256 threads: the 64 keys of one image, in parts of BK keys.
 template <int DT, int MODE, int D, int BK>
 __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* images) {
-    constexpr int HW = D / 8, PART = BK * D * 4;
+    constexpr bool LO = prompt_halves(DT, MODE);
+    constexpr int HW = D / 8, KEYS = BK * D * (LO ? 4 : 2), PART = KEYS + BK * D * 2;      // (LO: their rests behind the keys)
     const AttendArgs& a = t.a;
     const KvPool& c = t.c;
     const int h = blockIdx.x % c.heads, kb = blockIdx.x / c.heads % t.key_blocks, b = blockIdx.x / c.heads / t.key_blocks;
@@ -83,7 +89,7 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
                           : -1;
     __syncthreads();
     const int per = c.g / 8, groups = D / c.g;
-    uint8_t* const image = images + (((int64_t)b * t.key_blocks + kb) * c.heads + h) * (kImageKeys * D * 4);
+    uint8_t* const image = images + (((int64_t)b * t.key_blocks + kb) * c.heads + h) * (kImageKeys / BK * PART);
     auto row_of = [&](int key) -> int64_t {      // -1: not there, or no row sees it
         const int32_t rb = blocks[key / kKvUnit];
         return rb >= 0 && key0 + key >= lo && key0 + key < hi ? (int64_t)rb * kKvUnit + key % kKvUnit : -1;
@@ -116,7 +122,7 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
         if (e == kNoPower) e = 0;
         if (tid == 0) t.key_scale[((int64_t)b * t.key_blocks + kb) * c.heads + h] = __builtin_ldexpf(1.0f, e);
         for (int w = tid / 64; w < HW; w += 4) {
-            u32x4 out{0, 0, 0, 0};
+            u32x4 out{0, 0, 0, 0}, rest{0, 0, 0, 0};
             if (row >= 0) {
                 const int64_t g = row * groups + w / per;
                 float v[8];
@@ -126,8 +132,15 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
                 for (int i = 0; i < 8; ++i) v[i] = __builtin_ldexpf(v[i], -e);
                 out = u32x4{round2<QLIN_F16>(v[0], v[1]), round2<QLIN_F16>(v[2], v[3]), round2<QLIN_F16>(v[4], v[5]),
                             round2<QLIN_F16>(v[6], v[7])};
+                if constexpr (LO) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        rest[i] = round2<QLIN_F16>(v[2 * i] - f16_bits_to_f32(out[i] & 0xFFFFu), v[2 * i + 1] - f16_bits_to_f32(out[i] >> 16));
+                }
             }
-            *(u32x4*)(image + key / BK * PART + w * (BK * 16) + key % BK * 16) = out;
+            uint8_t* const to = image + key / BK * PART + w * (BK * 16) + key % BK * 16;
+            *(u32x4*)to = out;
+            if constexpr (LO) *(u32x4*)(to + BK * D * 2) = rest;
         }
     }
     const int ve = power(1);
@@ -149,7 +162,7 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
                 for (int k = 0; k < 8; ++k) v[i][k] = 0.0f;
             }
         }
-        uint8_t* const to = image + piece / (BK / 8) * PART + BK * D * 2 + (piece % (BK / 8) * D + w * 8) * 16;
+        uint8_t* const to = image + piece / (BK / 8) * PART + KEYS + (piece % (BK / 8) * D + w * 8) * 16;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             *(u32x4*)(to + k * 16) = u32x4{round2<QLIN_F16>(v[0][k], v[1][k]), round2<QLIN_F16>(v[2][k], v[3][k]),
@@ -157,15 +170,16 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
     }
 }
 
-// Waves of a SIMD that the registers hold.
-constexpr int prompt_residents(int D, int RT) { return D <= 128 && RT == 1 ? 3 : 2; }
+// Waves of a SIMD that the registers (and LDS, see below) hold.
+constexpr int prompt_residents(int D, int RT, bool LO) { return D <= 128 && RT == 1 ? 3 : (D == 256 && LO ? 1 : 2); }
 // Keys of a buffer: two (three) workgroups' pairs of them fit a CU's LDS.
-constexpr int prompt_keys(int D, int RT) { return D <= 128 && RT == 2 ? 64 : 32; }
+constexpr int prompt_keys(int D, int RT, bool LO) { return D <= 128 && RT == 2 && !LO ? 64 : 32; }
 
-template <int DT, int D, int RT>
-__global__ void __launch_bounds__(256, prompt_residents(D, RT)) attend_prompt_kernel(TileArgs t, int64_t tiles) {
-    constexpr int R = 128 * RT, KS = D / 16, DTILES = D / 32, BK = prompt_keys(D, RT);
-    constexpr int IMAGE = kImageKeys * D * 4, PART = BK * D * 4, ROUNDS = PART / 4096, PARTS = kImageKeys / BK;
+// LO: keys come with their rests.
+template <int DT, int D, int RT, bool LO>
+__global__ void __launch_bounds__(256, prompt_residents(D, RT, LO)) attend_prompt_kernel(TileArgs t, int64_t tiles) {
+    constexpr int R = 128 * RT, KS = D / 16, DTILES = D / 32, BK = prompt_keys(D, RT, LO), KEYS = BK * D * (LO ? 4 : 2);
+    constexpr int PART = KEYS + BK * D * 2, ROUNDS = (PART + 4095) / 4096, PARTS = kImageKeys / BK, IMAGE = PARTS * PART;
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][PART];
     const AttendArgs& a = t.a;
     const KvPool& c = t.c;
@@ -247,10 +261,12 @@ __global__ void __launch_bounds__(256, prompt_residents(D, RT)) attend_prompt_ke
     auto fetch = [&](int kb, int buf) {
         const uint8_t* from = images + (int64_t)(kb / PARTS) * c.heads * IMAGE + kb % PARTS * PART + tid * 16;
 #pragma unroll
-        for (int i = 0; i < ROUNDS; ++i)
+        for (int i = 0; i < ROUNDS; ++i) {
+            if (PART % 4096 && i == ROUNDS - 1 && wave >= PART % 4096 / 1024) break;
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + i * 4096),
                                              (__attribute__((address_space(3))) void*)(lds[buf] + i * 4096 + wave * 1024),
                                              16, 0, 0);
+        }
     };
 
     if (kb0 < kb1) fetch(kb0, 0);
@@ -281,7 +297,7 @@ __global__ void __launch_bounds__(256, prompt_residents(D, RT)) attend_prompt_ke
         const float down = (float)fall, back = __builtin_ldexpf(1.0f, -fall);
         const bool whole = there == ~0ull && key0 >= see_last.lo && key0 + BK <= see_first.hi;
         const uint8_t* const kl = lds[buf] + hb * (BK * 16) + r * 16;
-        const uint8_t* const vl = lds[buf] + BK * D * 2 + hb * (D * 16) + r * 16;
+        const uint8_t* const vl = lds[buf] + KEYS + hb * (D * 16) + r * 16;
 #pragma unroll 1
         for (int kt = 0; kt < BK / 32; ++kt) {
             f32x16 s[RT];
@@ -294,6 +310,11 @@ __global__ void __launch_bounds__(256, prompt_residents(D, RT)) attend_prompt_ke
                 const u32x4 ka = *(const u32x4*)(kl + k * (2 * BK * 16) + kt * 512);
 #pragma unroll
                 for (int n = 0; n < RT; ++n) s[n] = mfma32(ka, q[n][k], s[n]);
+                if constexpr (LO) {
+                    const u32x4 kr = *(const u32x4*)(kl + BK * D * 2 + k * (2 * BK * 16) + kt * 512);
+#pragma unroll
+                    for (int n = 0; n < RT; ++n) s[n] = mfma32(kr, q[n][k], s[n]);
+                }
             }
             u32x4 p[RT][2];
 #pragma unroll
@@ -391,7 +412,7 @@ __global__ void __launch_bounds__(256, prompt_residents(D, RT)) attend_prompt_ke
 template <int D, int RT>
 hipError_t launch_prompt_rows(const AttendArgs& a, const KvPool& c, int dt, const AttendPlan& p, void* workspace,
                               hipStream_t st) {
-    constexpr int R = 128 * RT, BK = prompt_keys(D, RT);
+    constexpr int R = 128 * RT;
     char* const ws = (char*)workspace;
     TileArgs t{a, c, p.chunk, p.splits, (float*)(ws + p.part_at), nullptr, (uint8_t*)ws, (uint64_t*)(ws + p.present_at),
                (float*)(ws + p.present_at) + (int64_t)a.B * p.key_blocks * 2, nullptr, p.key_blocks};
@@ -399,10 +420,12 @@ hipError_t launch_prompt_rows(const AttendArgs& a, const KvPool& c, int dt, cons
     t.part_ml = t.part_o + p.tiles * c.heads * p.splits * R * D;
     auto run = [&](auto dtc, auto mode) -> hipError_t {
         constexpr int DT = decltype(dtc)::value, M = decltype(mode)::value;
+        constexpr bool LO = prompt_halves(DT, M);
+        constexpr int BK = prompt_keys(D, RT, LO);
         attend_lay_kernel<DT, M, D, BK><<<(unsigned)((int64_t)a.B * p.key_blocks * c.heads), 256, 0, st>>>(t, (uint8_t*)ws);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        attend_prompt_kernel<DT, D, RT><<<(unsigned)(p.tiles * c.heads * p.splits), 256, 0, st>>>(t, p.tiles);
+        attend_prompt_kernel<DT, D, RT, LO><<<(unsigned)(p.tiles * c.heads * p.splits), 256, 0, st>>>(t, p.tiles);
         e = hipGetLastError();
         if (e != hipSuccess || p.splits == 1) return e;
         return launch_join<DT, D>(t, p.tiles, R, kImageKeys, st);

@@ -109,3 +109,22 @@ def test_weights_of_values_as_codes(D, g, G, rows):
     off = np.sqrt(((f64(got) - want) ** 2).mean() / (rounding ** 2).mean())
     print(f"error over that of rounding: {off:.3f}")
     assert off <= 1.1
+
+
+@pytest.mark.parametrize("D,g", [(64, 32), (96, 32), (128, 64), (128, 128), (192, 64), (256, 32)])
+def test_prompts_of_f16_keep_their_keys(D, g):
+    """f16 prompts over affine keys: scores as exact as fp32 sums, though a key has more bits than f16.
+
+    What is rounded to f16 then is p, a value and the output, each as much as the other: sqrt(3) of the output's rounding in
+    the mean square, where one key holds the weight, and less elsewhere."""
+    print(f"f16 prompt D{D} g{g}", flush=True)
+    p = Problem([290, 600], [700, 600], 1, 2, D, "affine", g, "f16", 64, seed=50, std=2.0, garbage=False)
+    got = p.call()
+    assert qm.last_path() == "kv_attention_prompt"
+    want, tol = bound(p, 0, 2.0 ** -11, False)
+    err = np.abs(f64(got) - want)
+    assert (err <= tol).all(), (err / tol).max()
+    rounding = f64(torch.from_numpy(want).half()) - want
+    off = np.sqrt((err ** 2).mean() / (rounding ** 2).mean())
+    print(f"error over that of rounding: {off:.3f}")
+    assert off <= 3 ** 0.5
