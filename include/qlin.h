@@ -531,7 +531,7 @@ qlin_status qlin_kv_cache_read(const qlin_kv_cache* cache, const int32_t* slots,
  *   - few rows to a sequence and key head: keys exactly; each p_j and each
  *     "affine" value (or, for bf16 in few groups, p_j times the value's scale, with
  *     its code) is rounded to f16 once, for bf16 in units of a power of two that
- *     follows the largest value (scale) of 32 keys: small ones keep 2^-19 of that,
+ *     follows the largest value (scale) of 32 keys: small ones keep 2^-17 of that,
  *     where it is within 2^64 of the largest of all; "mxfp4": p_j to
  *     dtype, "nvfp4": to f16, values exactly (a bf16 row of q as f16 in a power of
  *     two of its largest value there). "mxfp4" values outside f16's range do not

@@ -14,8 +14,9 @@
 // its own loads alone. What is ahead costs no registers that way, so that three
 // workgroups fit a CU: 64 x 8192 to 32768 keys, D 128, loads into registers 363
 // us, through the ring 344, three workgroups 294 (two 310). Not so for affine
-// groups of 32 in 32 columns: 10 to 25 registers of o, q and the scales do not fit
-// (bf16 D 64, 96 and 128, f16 D 64 and 128), and their reloads wait for the ring.
+// groups of 32 in 32 columns of D 64 and 128: 5 to 28 registers of o, q and the
+// scales do not fit (1 to 3 in 16 columns of D 96 and 192), and their reloads wait
+// for the ring.
 //
 // Products, 16 x 16 x 32:
 //   scores^T = K q^T. Lane (r = lane % 16, j = lane / 16) of K's operand holds
@@ -46,7 +47,7 @@
 //       gives: what p s lost by rounding multiplies c - 8, not 16 + c. p s is f16 in
 //       units that follow the largest scale of a step, as those of decoded values
 //       do: outputs are off by their own rounding, 0.0017, where p s in bf16 made it
-//       0.0021 (64 x 8192 to 32768 keys 296 us, in bf16 294).
+//       0.0021 (64 x 8192 to 32768 keys 295 us, in bf16 294; 500 keys 9.7 and 9.4).
 //       64 x 5000 to 20000 keys, D 128, groups of 64: 252 us decoded, 228 as codes.
 //   Rounded on the way: p s (as codes), p and decoded values to f16; mxfp4's p to the
 //   type, its values not at all, nor nvfp4's. Sums, m and l are fp32; l adds up p as
@@ -116,6 +117,17 @@ __device__ __forceinline__ float across_max(float v) {
     u = __float_as_uint(v);
     a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
     return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+// Largest of a wave's numbers, in every lane (steps within rows of 16 lanes first).
+__device__ __forceinline__ float wave_max(float v) {
+    auto with = [&](auto ctrl) {
+        v = fmaxf(v, __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), decltype(ctrl)::value, 0xf, 0xf, true)));
+    };
+    with(std::integral_constant<int, 0xB1>{});               // neighbours, pairs, halves of 8, of 16
+    with(std::integral_constant<int, 0x4E>{});
+    with(std::integral_constant<int, 0x141>{});
+    with(std::integral_constant<int, 0x140>{});
+    return across_max(v);
 }
 __device__ __forceinline__ float across_sum(float v) {
     v += __shfl_xor(v, 16, 64);
@@ -466,8 +478,7 @@ __global__ void __launch_bounds__(64 * tile_waves(D), tile_residents(D, NT)) att
                     most = fmaxf(most, PS ? fabsf(x[e][1]) : __builtin_fmaf(fabsf(x[e][1]), 15.0f, fabsf(x[e][3])));
                 if (__any(most > largest) || !__any(most > least)) {
                     out_of_line();
-#pragma unroll
-                    for (int off = 32; off; off /= 2) most = fmaxf(most, __shfl_xor(most, off, 64));
+                    most = wave_max(most);
                     const int of = __builtin_amdgcn_readfirstlane(ilogb_of(most)), to = max(of - kHead, unit_least);
                     if (__any(most > 0.0f) && (largest == 0.0f || to != unit)) {
                         const float f = largest == 0.0f ? 1.0f : __builtin_ldexpf(1.0f, unit - to);
