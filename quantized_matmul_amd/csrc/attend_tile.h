@@ -60,7 +60,7 @@
 //
 // Bound by the memory: D/2 bytes and the scales of a key and of a value, read
 // once for the tile's rows. 64 sequences of 8192 to 32768 keys (D 128, 8 heads,
-// groups of 64) are 1.48 GB, 296 us with the join: 5.0 TB/s of the 6.2 that a
+// groups of 64) are 1.48 GB, 295 us with the join: 5.0 TB/s of the 6.2 that a
 // plain read reaches; the vector units are busy for three quarters of that time.
 #pragma once
 
