@@ -143,11 +143,15 @@ qlin_status rotary(const void* x, int dtype, int64_t T, int64_t x_stride, int64_
     if ((s = check_aligned(x, elem(dtype), "x")) || (s = check_aligned(y, elem(dtype), "y")) ||
         (s = check_aligned(positions, 4, "positions")) || (s = check_aligned(freqs, 4, "freqs")))
         return s;
-    const uintptr_t xb = (uintptr_t)x, yb = (uintptr_t)y;
-    const uintptr_t xe = xb + ((T - 1) * x_stride + heads * D) * elem(dtype);
-    const uintptr_t ye = yb + ((T - 1) * y_stride + heads * D) * elem(dtype);
-    if (!(xb == yb && (x_stride == y_stride || T == 1)) && xb < ye && yb < xe)
-        return fail(QLIN_ERR_INVALID_ARGUMENT, "x and y overlap and are not one and the same");
+    const uintptr_t xb = (uintptr_t)x, yb = (uintptr_t)y, row = heads * D * elem(dtype);
+    const uintptr_t xe = xb + (T - 1) * x_stride * elem(dtype) + row, ye = yb + (T - 1) * y_stride * elem(dtype) + row;
+    if (!(xb == yb && (x_stride == y_stride || T == 1)) && xb < ye && yb < xe) {
+        // parts of the same rows: y's place in the row of x that it starts behind, apart from that row's and the next one's values
+        const uintptr_t step = x_stride * elem(dtype), back = (xb > yb ? xb - yb : 0), skip = step ? (back + step - 1) / step * step : 0;
+        const uintptr_t place = step ? (yb + skip - xb) % step : 0;
+        if (T == 1 || x_stride != y_stride || place < row || place + row > step)
+            return fail(QLIN_ERR_INVALID_ARGUMENT, "x and y overlap and are not one and the same");
+    }
     const qlin::RotaryArgs a{x, y, T, x_stride, y_stride, (int)heads, (int)D, (int)R, positions, freqs, (float)scale,
                              interleaved != 0, backward};
     return device_status(qlin::launch_rotary(a, dtype, st), "rotary");
