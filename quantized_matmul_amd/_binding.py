@@ -875,10 +875,11 @@ def kv_cache_read(cache: KVCache, slots: torch.Tensor, dtype: Optional[torch.dty
 
 
 def kv_cache_attention_workspace_bytes(cache: KVCache, T: int, q_heads: int, B: int, width: int, has_offsets: bool,
-                                       window: int = 0, dtype: torch.dtype = torch.bfloat16) -> int:
-    """qlin_kv_cache_attention_workspace_bytes for q [T, q_heads, head_dim] of dtype."""
+                                       window: int = 0, dtype: Optional[torch.dtype] = None) -> int:
+    """qlin_kv_cache_attention_workspace_bytes for q [T, q_heads, head_dim] of dtype (an affine cache's own, else bfloat16,
+    by default)."""
     return int(load_library().qlin_kv_cache_attention_workspace_bytes(
-        cache._address, _DTYPE[dtype], T, q_heads, B, width, int(has_offsets), window))
+        cache._address, _DTYPE[dtype or cache.dtype or torch.bfloat16], T, q_heads, B, width, int(has_offsets), window))
 
 
 def kv_cache_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lengths: torch.Tensor,

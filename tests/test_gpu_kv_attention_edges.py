@@ -154,3 +154,14 @@ def test_a_padded_batch_captured_without_an_output(rows):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and (out[2 * rows :] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,mode,g", [("f16", "affine", 64), ("bf16", "affine", 64), ("f32", "affine", 64), ("bf16", "mxfp4", 32)])
+def test_the_workspace_that_is_asked_for_is_enough(dtype, mode, g):
+    """By default for rows of an affine cache's own type."""
+    for rows in (1, 300):
+        p = Problem([rows], [5000], 2, 2, 64, mode, g, dtype, 64, seed=51)
+        need = qm.kv_cache_attention_workspace_bytes(p.cache, rows, 4, 1, p.table.shape[1], True)
+        assert (need == 0) == (dtype == "f32")
+        got = p.call(workspace=torch.empty(max(need, 16), dtype=torch.uint8, device=DEV))
+        assert torch.equal(got, p.call())
