@@ -23,8 +23,7 @@
 // f16 prompts take affine keys as two f16 numbers, the second the first one's rest,
 // and two products: with one, scores made outputs 2.5 times as far off as their own
 // rounding, with both 1.43 (p's and the values' rounding). 8192 rows over 16384
-// keys (D 128) 1.75 and 2.28 ms, 4096 over 8192 of D 256, which then has the CU's
-// LDS to itself, 0.91 and 1.64.
+// keys (D 128) 1.75 and 2.28 ms, 4096 over 8192 of D 256 0.91 and 1.18.
 // Decoding inside the attention kernel would cost every workgroup again what
 // this does once: 190 of about 560 vector instructions of 64 keys (D 128), where
 // the matrix cores need the time of 512.
@@ -170,17 +169,21 @@ __global__ void __launch_bounds__(256) attend_lay_kernel(TileArgs t, uint8_t* im
     }
 }
 
-// Waves of a SIMD that the registers (and LDS, see below) hold.
-constexpr int prompt_residents(int D, int RT, bool LO) { return D <= 128 && RT == 1 ? 3 : (D == 256 && LO ? 1 : 2); }
+// Waves of a SIMD that the registers hold.
+constexpr int prompt_residents(int D, int RT) { return D <= 128 && RT == 1 ? 3 : 2; }
 // Keys of a buffer: two (three) workgroups' pairs of them fit a CU's LDS.
 constexpr int prompt_keys(int D, int RT, bool LO) { return D <= 128 && RT == 2 && !LO ? 64 : 32; }
+// Buffers of a workgroup: of two with one each, the other computes while one's keys come (D 256, 4096 rows over 8192 keys:
+// 1.64 ms by one workgroup with two buffers, 1.18 so).
+constexpr int prompt_buffers(int D, bool LO) { return D == 256 && LO ? 1 : 2; }
 
 // LO: keys come with their rests.
 template <int DT, int D, int RT, bool LO>
-__global__ void __launch_bounds__(256, prompt_residents(D, RT, LO)) attend_prompt_kernel(TileArgs t, int64_t tiles) {
+__global__ void __launch_bounds__(256, prompt_residents(D, RT)) attend_prompt_kernel(TileArgs t, int64_t tiles) {
     constexpr int R = 128 * RT, KS = D / 16, DTILES = D / 32, BK = prompt_keys(D, RT, LO), KEYS = BK * D * (LO ? 4 : 2);
     constexpr int PART = KEYS + BK * D * 2, ROUNDS = (PART + 4095) / 4096, PARTS = kImageKeys / BK, IMAGE = PARTS * PART;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[2][PART];
+    constexpr int BUFS = prompt_buffers(D, LO);
+    __shared__ __attribute__((aligned(16))) uint8_t lds[BUFS][PART];
     const AttendArgs& a = t.a;
     const KvPool& c = t.c;
     // heads over the XCDs, so that each L2 keeps its head's keys; the last tiles, which see most, first
@@ -269,15 +272,19 @@ __global__ void __launch_bounds__(256, prompt_residents(D, RT, LO)) attend_promp
         }
     };
 
-    if (kb0 < kb1) fetch(kb0, 0);
+    if (BUFS == 2 && kb0 < kb1) fetch(kb0, 0);
     for (int kb = kb0; kb < kb1; ++kb) {
-        const int buf = (kb - kb0) & 1;
+        const int buf = (kb - kb0) & (BUFS - 1);
+        if constexpr (BUFS == 1) {
+            __syncthreads();                     // the last block is read
+            fetch(kb, 0);
+        }
         const int64_t ib = (int64_t)w.b * t.key_blocks + kb / PARTS;          // waited for with the block:
         const uint64_t there = PARTS == 1 ? t.present[ib] : ((const uint32_t*)t.present)[ib * 2 + kb % 2] | 0xFFFFFFFF00000000ull;
         const float key_scale = t.key_scale[ib * c.heads + h];
         const int value_power = t.value_power[ib * c.heads + h];
         __syncthreads();                         // this block has landed, the other buffer is read
-        if (kb + 1 < kb1) fetch(kb + 1, buf ^ 1);
+        if (BUFS == 2 && kb + 1 < kb1) fetch(kb + 1, buf ^ 1);
         const int key0 = kb * BK;
         if (idle || key0 >= see_last.hi || key0 + BK <= see_first.lo) continue;
         const int up = __builtin_amdgcn_readfirstlane(value_power);
